@@ -75,11 +75,30 @@ enum {
                                   stride and was clamped */
   MLA_STATUS_BAD_SLOT = 4,     /* a page's slot run lay outside the pool; its
                                   rows were read as zeros */
-  MLA_STATUS_BAD_WORK = 8      /* a work-list entry named no work unit; that
+  MLA_STATUS_BAD_WORK = 8,     /* a work-list entry named no work unit; that
                                   cluster did nothing (see mla_plan_sched) */
+  MLA_STATUS_BAD_POSITION = 16 /* a token's position lay outside the rotation
+                                  table (mla_kv_append); nothing of that token
+                                  was written */
 };
 
-typedef enum { MLA_KV_BF16 = 0, MLA_KV_FP8_E4M3 = 1 } mla_kv_dtype;
+/* Storage of a pool's rows.  MLA_KV_FP4_E2M1 (4-bit, microscaled; the library's
+ * own format, the pages have no 4-bit cache) is a row of MLA_FP4_ROW_BYTES
+ * bytes:
+ *   [0, 256)    E2M1 codes of c_kv, element 2i in the low half of byte i
+ *   [256, 288)  E4M3 scales, scale j for elements 16j .. 16j + 15
+ *   [288, 352)  E4M3 codes of the RoPE key (positions keep 8 bits)
+ * with ONE fp32 factor g per pool (kv_scale, device fp32 [1], finite, > 0):
+ *   c_kv = E2M1 * E4M3 scale * g,   rope = E4M3 * g.
+ * The block scales adapt to each token; g only centres their range (E4M3
+ * scales hold 2^-9 .. 448), so a g near the latents' typical block maximum / 6
+ * suits; values beyond 2688 g (c_kv) and 448 g (rope) saturate. */
+typedef enum {
+  MLA_KV_BF16 = 0,
+  MLA_KV_FP8_E4M3 = 1,
+  MLA_KV_FP4_E2M1 = 2
+} mla_kv_dtype;
+#define MLA_FP4_ROW_BYTES 352
 
 /* Latent row geometry ([VRAM-KV], [K3-MEM]). */
 #define MLA_ROW_DIM 576   /* kv_lora_rank + qk_rope_head_dim */
@@ -154,7 +173,8 @@ int mla_plan_ex(int V, int q_len, int H, int rows_per_unit,
  * measured times on GB300, B = 1..24 requests x 100k / 400k tokens: a work
  * unit costs about that many pages beyond its own).
  *   B, num_shards  requests and context shards (V = B * num_shards);
- *   kv_dtype       MLA_KV_BF16 or MLA_KV_FP8_E4M3 (else MLA_ERR_INVALID_ARG)
+ *   kv_dtype       MLA_KV_BF16, MLA_KV_FP8_E4M3 or MLA_KV_FP4_E2M1 (planned
+ *                  as BF16) (else MLA_ERR_INVALID_ARG)
  *   seq_lens_host  host int32 [num_shards * B] (shard-local lengths).
  */
 int mla_plan(int B, int q_len, int H, int num_shards, mla_kv_dtype kv_dtype,
@@ -277,8 +297,10 @@ int mla_check_page_table(const int32_t* req_to_token_host, int64_t stride,
  *   q_nope_absorbed  bf16 [B, q_len, H, 512], contiguous, 16-B aligned
  *   q_rope           bf16 [B, q_len, H, 64], contiguous, 16-B aligned
  *   kv_pages         [num_slots, 576]: bf16 (1152-B rows) or E4M3 bytes
- *                    (576-B rows); 16-B aligned; num_slots >= page_size
- *   kv_scale         fp32 [num_slots] (FP8), 16-B aligned; NULL for BF16
+ *                    (576-B rows), or [num_slots, 352] bytes (FP4, see
+ *                    mla_kv_dtype); 16-B aligned; num_slots >= page_size
+ *   kv_scale         fp32 [num_slots] (FP8), fp32 [1] (FP4), 16-B aligned;
+ *                    NULL for BF16
  *   req_to_token     int32 [num_shards*B, r2t_stride]; only the entry of the
  *                    first token of each page is read (see
  *                    mla_check_page_table for the contract)
@@ -304,7 +326,7 @@ int mla_check_page_table(const int32_t* req_to_token_host, int64_t stride,
  *                    (see mla_plan_sched) in launch order.  It must hold
  *                    every id 0 .. num_work - 1 once, num_work = num_splits *
  *                    num_shards * B * ceil(q_len * H / R), R = 256 rows for
- *                    BF16 KV and 128 for FP8 (else MLA_ERR_INVALID_ARG); an
+ *                    BF16 and FP4 KV and 128 for FP8 (else MLA_ERR_INVALID_ARG); an
  *                    entry outside that range sets MLA_STATUS_BAD_WORK and
  *                    its cluster does nothing.  The results do not depend on
  *                    the order.
@@ -451,6 +473,81 @@ int64_t mla_scratch_bytes(int B, int q_len, int H, int num_shards,
 int mla_kv_write(const void* rows, int64_t n, const int32_t* slots,
                  void* kv_pages, mla_kv_dtype kv_dtype, float* kv_scale,
                  int64_t num_slots, int* status, mla_stream_t stream);
+
+/*
+ * Appending new tokens to the pool, from the projection's raw output: the
+ * latent's RMS norm, the rotation of the RoPE key and of the queries' RoPE
+ * parts by each token's position, and the write in the pool's format, in one
+ * launch (the pages' mla_prepare does this before the decode; they give its
+ * time only).  For token r of n, in fp32 with one rounding into the stored type:
+ *   c    = rows[r, :512] * rsqrt(mean(rows[r, :512]^2) + eps) * norm_weight
+ *          (norm_weight NULL: c = rows[r, :512])
+ *   rope = R(rows[r, 512:576]),  q_out[r, h] = R(q[r, h]) for every head h
+ *   R:     (a, b) -> (a cos_k - b sin_k, a sin_k + b cos_k) for the 32 pairs
+ *          k: elements (2k, 2k + 1) if interleaved, else (k, k + 32); cos_k =
+ *          cos_sin[positions[r], k], sin_k = cos_sin[positions[r], 32 + k]
+ *   stored at slots[r]: BF16: bf16(c), bf16(rope).  FP8: mla_kv_write's rule on
+ *          the fp32 values (scale = max|v| / 448, code = E4M3(v / scale)).
+ *          FP4: scale j = E4M3(max|c of block j| / (6 g)), code = E2M1(c /
+ *          (scale j * g)) (codes 0 where that is 0), rope code = E4M3(rope /
+ *          g); all to nearest even, saturated.
+ *   rows         bf16, row r at rows + r * row_stride elements (>= 576, a
+ *                multiple of 8), 16-B aligned; finite
+ *   norm_weight  bf16 [512] or NULL, 16-B aligned;  eps finite, >= 0
+ *   slots        int32 [n]: a slot outside [0, num_slots) is skipped
+ *                (MLA_STATUS_BAD_SLOT; its queries are still rotated)
+ *   positions    int32 [n]: one outside [0, max_pos) skips the token's row and
+ *                queries (MLA_STATUS_BAD_POSITION)
+ *   cos_sin      fp32 [max_pos, 64], 32 cosines then 32 sines, 16-B aligned
+ *   kv_scale     FP8: fp32 [num_slots], written; FP4: fp32 [1], read; BF16: NULL
+ *   q, q_out     bf16 [n, H, 64] with the given strides in elements (multiples
+ *                of 8), 16-B aligned; q_out may be q; H = 0: no queries
+ * n = 0 is a no-op.  Slots written by two rows of one call get either row.
+ */
+int mla_kv_append(const void* rows, int64_t row_stride, int64_t n,
+                  const void* norm_weight, float eps, const int32_t* slots,
+                  const int32_t* positions, const float* cos_sin,
+                  int64_t max_pos, int interleaved, void* kv_pages,
+                  mla_kv_dtype kv_dtype, float* kv_scale, int64_t num_slots,
+                  const void* q, int64_t q_token_stride, int64_t q_head_stride,
+                  void* q_out, int64_t qo_token_stride, int64_t qo_head_stride,
+                  int H, int* status, mla_stream_t stream);
+
+/*
+ * The rows at `slots` back as bf16 [n, 576] (each stored value in fp32, rounded
+ * once): what a prefill step up-projects from a cached context.  A slot
+ * outside [0, num_slots) reads as zeros (MLA_STATUS_BAD_SLOT).
+ *   out   bf16, row r at out + r * out_stride elements (>= 576, a multiple of
+ *         8), 16-B aligned
+ */
+int mla_kv_read(const void* kv_pages, mla_kv_dtype kv_dtype,
+                const float* kv_scale, int64_t num_slots, const int32_t* slots,
+                int64_t n, void* out, int64_t out_stride, int* status,
+                mla_stream_t stream);
+
+/*
+ * Residual addition and RMS norm, the step before a layer's projections (no
+ * counterpart on the pages), per row of d values, in fp32 with each output
+ * rounded once:
+ *   h = x + residual,  residual_out = bf16(h)       (residual NULL: h = x)
+ *   y = h * rsqrt(mean(h^2) + eps) * weight
+ *   out = bf16(y);  out8 = E4M3(y / s) (nearest even, saturated), s = max|y| /
+ *   448 over the row (group 0) or over each `group` values (32, 64 or 128; d a
+ *   multiple of it); a group of zeros gets scale 0 and codes 0.
+ *   x, residual, residual_out, out   bf16 rows at their strides (elements);
+ *                 residual_out may be residual, out may be x
+ *   weight        bf16 [d];  out or out8 may be NULL, not both
+ *   out8, scales  E4M3 bytes [n, d] and fp32 [n, d / group or 1] at their strides
+ * d <= 32768 (else MLA_ERR_UNSUPPORTED).  Rows that start on 16-byte boundaries
+ * (out8: 8) with d a multiple of 8 take whole vectors; any other alignment
+ * takes single elements.  n = 0 is a no-op.
+ */
+int mla_add_rms_norm(const void* x, int64_t x_stride, const void* residual,
+                     int64_t residual_stride, void* residual_out,
+                     int64_t residual_out_stride, const void* weight, float eps,
+                     int64_t n, int d, void* out, int64_t out_stride, void* out8,
+                     int64_t out8_stride, float* scales, int64_t scales_stride,
+                     int group, mla_stream_t stream);
 
 /*
  * The per-head projections around the absorbed decode ([K3-MEM]: w_kc is

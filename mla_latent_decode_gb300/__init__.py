@@ -21,10 +21,12 @@ import torch
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libmla_decode.so")
 ROW_DIM, NOPE_DIM, ROPE_DIM, VALUE_DIM, PAGE_SIZE = 576, 512, 64, 512, 64
-KV_BF16, KV_FP8_E4M3 = 0, 1
-_KV_DTYPE = {"bf16": KV_BF16, "fp8_e4m3": KV_FP8_E4M3}
+KV_BF16, KV_FP8_E4M3, KV_FP4_E2M1 = 0, 1, 2
+_KV_DTYPE = {"bf16": KV_BF16, "fp8_e4m3": KV_FP8_E4M3, "fp4_e2m1": KV_FP4_E2M1}
+FP4_ROW_BYTES = 352  # 512 E2M1 codes, 32 E4M3 block scales, 64 E4M3 RoPE codes
 ROWS_PER_UNIT = 256  # query rows per work unit of the BF16 tensor-core kernel
 STATUS_WAIT_TIMEOUT, STATUS_BAD_LENGTH, STATUS_BAD_SLOT, STATUS_BAD_WORK = 1, 2, 4, 8
+STATUS_BAD_POSITION = 16
 
 _lib = None
 _lock = threading.Lock()
@@ -84,6 +86,11 @@ def library() -> ctypes.CDLL:
                                          p, p, p, p]),
             "mla_scratch_bytes": (i64, [i32, i32, i32, i32, i32]),
             "mla_kv_write": (i32, [p, i64, p, p, i32, p, i64, p, p]),
+            "mla_kv_append": (i32, [p, i64, i64, p, f32, p, p, p, i64, i32, p, i32, p,
+                                    i64, p, i64, i64, p, i64, i64, i32, p, p]),
+            "mla_kv_read": (i32, [p, i32, p, i64, p, i64, p, i64, p, p]),
+            "mla_add_rms_norm": (i32, [p, i64, p, i64, p, i64, p, f32, i64, i32, p, i64,
+                                       p, i64, p, i64, i32, p]),
             "mla_absorb_q": (i32, [p, p, p, i32, i32, p, p]),
             "mla_project_out": (i32, [p, p, p, i32, i32, p, p]),
             "mla_lse_combine": (i32, [p, p, i32, i64, p, p, p]),
@@ -265,8 +272,9 @@ def _kv_dtype(kv: torch.Tensor) -> int:
     if kv.dtype == torch.bfloat16:
         return KV_BF16
     if kv.dtype in (torch.uint8, torch.float8_e4m3fn):
-        return KV_FP8_E4M3
-    raise TypeError(f"kv dtype {kv.dtype}: expected bfloat16 or uint8 (E4M3)")
+        # the two byte pools differ in their row: 576 E4M3 codes, or 352 bytes
+        return KV_FP4_E2M1 if kv.shape[-1] == FP4_ROW_BYTES else KV_FP8_E4M3
+    raise TypeError(f"kv dtype {kv.dtype}: expected bfloat16 or uint8 (E4M3, FP4)")
 
 
 def decode_partial(q_nope, q_rope, kv, kv_scale, req_to_token, seq_lens,
@@ -390,6 +398,142 @@ def kv_write(rows, slots, kv, kv_scale=None, status=None, stream=None):
     _check(library().mla_kv_write(_ptr(rows), n, _ptr(slots), _ptr(kv),
                                   _kv_dtype(kv), _ptr(kv_scale), kv.shape[0],
                                   _ptr(status), _stream(stream)))
+
+
+def _rows_arg(t: torch.Tensor, name: str, width: int, dtype=torch.bfloat16):
+    """A 2-D argument whose rows are contiguous (any row stride)."""
+    if t.dtype != dtype or t.dim() != 2 or t.shape[1] != width or t.stride(1) != 1:
+        raise ValueError(f"{name}: expected {dtype} rows of {width} contiguous values, "
+                         f"got {t.dtype} {tuple(t.shape)} with strides {t.stride()}")
+    return _ptr(t), t.stride(0) if t.shape[0] > 1 else max(t.stride(0), width)
+
+
+def _int32_arg(t: torch.Tensor, name: str, n: int):
+    if t.dtype != torch.int32 or t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{name}: expected {n} contiguous int32 values, got {t.dtype} "
+                         f"{tuple(t.shape)}")
+    return _ptr(t)
+
+
+def _pool_args(kv: torch.Tensor, kv_scale: Optional[torch.Tensor]):
+    kind = _kv_dtype(kv)
+    width = FP4_ROW_BYTES if kind == KV_FP4_E2M1 else ROW_DIM
+    if kv.dim() != 2 or kv.shape[1] != width or not kv.is_contiguous():
+        raise ValueError(f"kv: expected a contiguous [num_slots, {width}] pool, got "
+                         f"{tuple(kv.shape)} with strides {kv.stride()}")
+    if kv_scale is not None:
+        need = kv.shape[0] if kind == KV_FP8_E4M3 else 1
+        if kv_scale.dtype != torch.float32 or kv_scale.numel() < need or not kv_scale.is_contiguous():
+            raise ValueError(f"kv_scale: expected {need} contiguous float32 values")
+    return _ptr(kv), kind, _ptr(kv_scale), kv.shape[0]
+
+
+def kv_append(rows, slots, positions, cos_sin, kv, kv_scale=None, norm_weight=None,
+              eps: float = 1e-6, q_rope=None, q_out=None, interleaved: bool = True,
+              status=None, stream=None):
+    """Append new tokens to the pool: RMS norm of the latent (norm_weight bf16
+    [512] or None), rotation of the RoPE key and of the queries by position,
+    and the write in the pool's format, in one launch; see mla_kv_append.
+
+    rows bf16 [n, 576] (rows may be strided), slots / positions int32 [n],
+    cos_sin fp32 [max_pos, 64]; kv: bf16 [slots, 576], uint8 [slots, 576]
+    (E4M3, kv_scale fp32 [slots]) or uint8 [slots, 352] (FP4, kv_scale fp32
+    [1]); q_rope bf16 [n, H, 64] (strided) or None.  Returns q_out (allocated
+    unless given; q_out=q_rope rotates in place), None without queries."""
+    n = rows.shape[0]
+    row_ptr, row_stride = _rows_arg(rows, "rows", ROW_DIM)
+    kv_ptr, kind, scale_ptr, num_slots = _pool_args(kv, kv_scale)
+    if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2 or cos_sin.shape[1] != ROPE_DIM \
+            or not cos_sin.is_contiguous():
+        raise ValueError("cos_sin: expected contiguous float32 [max_pos, 64]")
+    if norm_weight is not None and (norm_weight.dtype != torch.bfloat16 or norm_weight.numel() != NOPE_DIM
+                                    or not norm_weight.is_contiguous()):
+        raise ValueError("norm_weight: expected 512 contiguous bfloat16 values")
+    H, q_args = 0, [None, 0, 0, None, 0, 0]
+    if q_rope is not None:
+        if q_out is None:
+            q_out = torch.empty(q_rope.shape, dtype=torch.bfloat16, device=q_rope.device)
+        for t, name in ((q_rope, "q_rope"), (q_out, "q_out")):
+            if t.dtype != torch.bfloat16 or t.dim() != 3 or t.shape[0] != n or \
+                    t.shape[2] != ROPE_DIM or t.shape != q_rope.shape or t.stride(2) != 1:
+                raise ValueError(f"{name}: expected bfloat16 [{n}, H, 64] with contiguous "
+                                 f"head rows, got {t.dtype} {tuple(t.shape)} {t.stride()}")
+        H = q_rope.shape[1]
+        q_args = [_ptr(q_rope), q_rope.stride(0), q_rope.stride(1),
+                  _ptr(q_out), q_out.stride(0), q_out.stride(1)]
+    with _on(rows):
+        _check(library().mla_kv_append(
+            row_ptr, row_stride, n, _ptr(norm_weight), float(eps),
+            _int32_arg(slots, "slots", n), _int32_arg(positions, "positions", n),
+            _ptr(cos_sin), cos_sin.shape[0], int(interleaved), kv_ptr, kind, scale_ptr,
+            num_slots, *q_args, H, _ptr(status), _stream(stream)))
+    return q_out if q_rope is not None else None
+
+
+def kv_read(kv, slots, kv_scale=None, out=None, status=None, stream=None):
+    """The rows at `slots` (int32 [n]) of any pool as bf16 [n, 576]; see
+    mla_kv_read."""
+    n = slots.numel()
+    kv_ptr, kind, scale_ptr, num_slots = _pool_args(kv, kv_scale)
+    if out is None:
+        out = torch.empty((n, ROW_DIM), dtype=torch.bfloat16, device=kv.device)
+    out_ptr, out_stride = _rows_arg(out, "out", ROW_DIM)
+    if out.shape[0] != n:
+        raise ValueError(f"out: expected {n} rows, got {out.shape[0]}")
+    with _on(kv):
+        _check(library().mla_kv_read(kv_ptr, kind, scale_ptr, num_slots,
+                                     _int32_arg(slots, "slots", n), n, out_ptr,
+                                     out_stride, _ptr(status), _stream(stream)))
+    return out
+
+
+def add_rms_norm(x, weight, residual=None, eps: float = 1e-6, out=None, out8=None,
+                 scales=None, group: int = 0, residual_out=None, e4m3: bool = False,
+                 stream=None):
+    """Residual addition and RMS norm over the rows of x bf16 [n, d]; see
+    mla_add_rms_norm.  Writes `out` (bf16) and / or `out8` (E4M3) with `scales`
+    (fp32 [n, 1], or [n, d // group] with group 32, 64 or 128), whichever are
+    given; with neither, `out` is allocated, or with e4m3=True out8 and scales.
+    The residual is updated in place unless residual_out is given.
+
+    Returns (out, out8, scales, residual_out), None for what was not asked."""
+    if x.dim() != 2:
+        raise ValueError(f"x: expected [n, d], got {tuple(x.shape)}")
+    n, d = x.shape
+    if out is None and out8 is None and not e4m3:
+        out = torch.empty((n, d), dtype=torch.bfloat16, device=x.device)
+    if out8 is None and e4m3:
+        out8 = torch.empty((n, d), dtype=torch.float8_e4m3fn, device=x.device)
+    if out8 is not None and scales is None:
+        scales = torch.empty((n, d // group if group else 1), dtype=torch.float32, device=x.device)
+    if residual is not None and residual_out is None:
+        residual_out = residual
+    if residual is None and residual_out is not None:
+        raise ValueError("residual_out without a residual")
+    if weight.dtype != torch.bfloat16 or weight.numel() != d or not weight.is_contiguous():
+        raise ValueError(f"weight: expected {d} contiguous bfloat16 values")
+    args = []
+    for t, name in ((x, "x"), (residual, "residual"), (residual_out, "residual_out")):
+        args += [None, 0] if t is None else list(_rows_arg(t, name, d))
+        if t is not None and t.shape[0] != n:
+            raise ValueError(f"{name}: expected {n} rows, got {t.shape[0]}")
+    outs = []
+    if out is not None and out.shape[0] != n:
+        raise ValueError(f"out: expected {n} rows, got {out.shape[0]}")
+    outs += [None, 0] if out is None else list(_rows_arg(out, "out", d))
+    if out8 is None:
+        outs += [None, 0, None, 0]
+    else:
+        if out8.dtype not in (torch.uint8, torch.float8_e4m3fn):
+            raise ValueError(f"out8: expected float8_e4m3fn or uint8, got {out8.dtype}")
+        if out8.shape[0] != n or scales.shape[0] != n:
+            raise ValueError(f"out8, scales: expected {n} rows")
+        outs += list(_rows_arg(out8, "out8", d, out8.dtype))
+        outs += list(_rows_arg(scales, "scales", d // group if group else 1, torch.float32))
+    with _on(x):
+        _check(library().mla_add_rms_norm(*args, _ptr(weight), float(eps), n, d, *outs,
+                                          group, _stream(stream)))
+    return out, out8, scales, residual_out
 
 
 def absorb_q(q_nope, w_kc, out=None, status=None, stream=None):

@@ -27,6 +27,10 @@ int fail(int code, const char* fmt, ...) {
   return code;
 }
 
+static bool known_kv_dtype(mla_kv_dtype t) {
+  return t == MLA_KV_BF16 || t == MLA_KV_FP8_E4M3 || t == MLA_KV_FP4_E2M1;
+}
+
 int check_decode_args(const DecodeArgs& a) {
   if (!a.q_nope || !a.q_rope || !a.kv || !a.req_to_token || !a.seq_lens ||
       !a.O_part || !a.LSE_part)
@@ -45,10 +49,10 @@ int check_decode_args(const DecodeArgs& a) {
   if (a.page_size != MLA_PAGE_SIZE)
     return fail(MLA_ERR_UNSUPPORTED, "page_size %d: only %d is built",
                 a.page_size, MLA_PAGE_SIZE);
-  if (a.kv_dtype != MLA_KV_BF16 && a.kv_dtype != MLA_KV_FP8_E4M3)
+  if (!known_kv_dtype(a.kv_dtype))
     return fail(MLA_ERR_INVALID_ARG, "unknown kv_dtype %d", (int)a.kv_dtype);
-  if (a.kv_dtype == MLA_KV_FP8_E4M3 && !a.kv_scale)
-    return fail(MLA_ERR_INVALID_ARG, "FP8 KV needs kv_scale");
+  if (a.kv_dtype != MLA_KV_BF16 && !a.kv_scale)
+    return fail(MLA_ERR_INVALID_ARG, "FP8 and FP4 KV need kv_scale");
   if (a.num_slots < a.page_size || a.num_slots > ((int64_t)1 << 31) - 1)
     return fail(MLA_ERR_INVALID_ARG, "num_slots %lld out of range",
                 (long long)a.num_slots);
@@ -227,7 +231,7 @@ int mla_plan(int B, int q_len, int H, int num_shards, mla_kv_dtype kv_dtype,
              float* wave_eff_out) {
   if (B < 1 || num_shards < 1)
     return fail(MLA_ERR_INVALID_ARG, "B and num_shards must be >= 1");
-  if (kv_dtype != MLA_KV_BF16 && kv_dtype != MLA_KV_FP8_E4M3)
+  if (!known_kv_dtype(kv_dtype))
     return fail(MLA_ERR_INVALID_ARG, "unknown kv_dtype %d", (int)kv_dtype);
   // BF16: 256 query rows per 4-CTA cluster; E4M3: 128 rows per 2-CTA cluster.
   const bool fp8 = kv_dtype == MLA_KV_FP8_E4M3;
@@ -500,7 +504,7 @@ int mla_plan_parts(int B, int q_len, int H, int num_shards,
                    int* num_parts_out, float* wave_eff_out) {
   if (B < 1 || num_shards < 1)
     return fail(MLA_ERR_INVALID_ARG, "B and num_shards must be >= 1");
-  if (kv_dtype != MLA_KV_BF16 && kv_dtype != MLA_KV_FP8_E4M3)
+  if (!known_kv_dtype(kv_dtype))
     return fail(MLA_ERR_INVALID_ARG, "unknown kv_dtype %d", (int)kv_dtype);
   const int slots = decode_slots(kv_dtype, num_sms);
   if (slots < 0) return slots;
@@ -520,7 +524,7 @@ int mla_plan_sched(int B, int q_len, int H, int num_shards,
                    float* wave_eff_out) {
   if (B < 1 || num_shards < 1)
     return fail(MLA_ERR_INVALID_ARG, "B and num_shards must be >= 1");
-  if (kv_dtype != MLA_KV_BF16 && kv_dtype != MLA_KV_FP8_E4M3)
+  if (!known_kv_dtype(kv_dtype))
     return fail(MLA_ERR_INVALID_ARG, "unknown kv_dtype %d", (int)kv_dtype);
   const int slots = decode_slots(kv_dtype, num_sms);
   if (slots < 0) return slots;

@@ -13,6 +13,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
+#include "mla_fp4.cuh"
 #include "mla_internal.h"
 
 namespace {
@@ -27,7 +28,7 @@ struct SimtParams {
   const __nv_bfloat16* q_rope;
   const void* kv;
   const float* kv_scale;
-  int kv_fp8;
+  mla_kv_dtype kv_dtype;
   int64_t num_slots;
   const int32_t* r2t;
   int64_t r2t_stride;
@@ -54,7 +55,20 @@ __device__ __forceinline__ float warp_sum(float x) {
 
 __device__ __forceinline__ float kv_value(const SimtParams& p, int64_t slot,
                                           int d) {
-  if (p.kv_fp8) {
+  if (p.kv_dtype == MLA_KV_FP4_E2M1) {
+    const uint8_t* row = static_cast<const uint8_t*>(p.kv) + slot * mla::kFp4RowBytes;
+    const float g = p.kv_scale[0];
+    __nv_fp8_e4m3 f;
+    if (d >= MLA_NOPE_DIM) {
+      f.__x = row[mla::kFp4RopeOff + d - MLA_NOPE_DIM];
+      return float(f) * g;
+    }
+    f.__x = row[mla::kFp4ScaleOff + d / 16];
+    uint32_t h[4];
+    mla::e2m1x8_to_f16((uint32_t)row[d / 2] >> (4 * (d & 1)) & 0xFu, h);
+    return mla::h2_to_f32(h[0]).x * float(f) * g;
+  }
+  if (p.kv_dtype == MLA_KV_FP8_E4M3) {
     __nv_fp8_e4m3 f;
     f.__x = static_cast<const uint8_t*>(p.kv)[slot * MLA_ROW_DIM + d];
     return float(f) * p.kv_scale[slot];
@@ -191,7 +205,7 @@ int launch_simt(const DecodeArgs& a) {
   p.q_rope = static_cast<const __nv_bfloat16*>(a.q_rope);
   p.kv = a.kv;
   p.kv_scale = a.kv_scale;
-  p.kv_fp8 = a.kv_dtype == MLA_KV_FP8_E4M3;
+  p.kv_dtype = a.kv_dtype;
   p.num_slots = a.num_slots;
   p.r2t = a.req_to_token;
   p.r2t_stride = a.r2t_stride;
@@ -219,6 +233,13 @@ int launch_simt(const DecodeArgs& a) {
   e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_fail(e, "launch mla_partial_simt_kernel");
   return MLA_OK;
+}
+
+// FP4 KV: the CUDA-core kernel serves the fp32 partial outputs.
+int launch_fp4(const DecodeArgs& a) {
+  if (a.o_bf16 || a.counters)
+    return fail(MLA_ERR_UNSUPPORTED, "FP4 KV: fp32 partial outputs only");
+  return launch_simt(a);
 }
 
 }  // namespace mla

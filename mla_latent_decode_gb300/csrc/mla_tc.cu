@@ -1302,6 +1302,7 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1)
 
 int launch_tc(const DecodeArgs& a) {
   if (a.kv_dtype == MLA_KV_FP8_E4M3) return launch_tc_fp8(a);
+  if (a.kv_dtype == MLA_KV_FP4_E2M1) return launch_fp4(a);
   TcParams p;
   p.q_nope = static_cast<const uint4*>(a.q_nope);
   p.q_rope = static_cast<const uint4*>(a.q_rope);
