@@ -235,11 +235,4 @@ int launch_simt(const DecodeArgs& a) {
   return MLA_OK;
 }
 
-// FP4 KV: the CUDA-core kernel serves the fp32 partial outputs.
-int launch_fp4(const DecodeArgs& a) {
-  if (a.o_bf16 || a.counters)
-    return fail(MLA_ERR_UNSUPPORTED, "FP4 KV: fp32 partial outputs only");
-  return launch_simt(a);
-}
-
 }  // namespace mla
