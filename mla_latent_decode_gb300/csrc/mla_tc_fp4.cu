@@ -575,9 +575,12 @@ __device__ __forceinline__ void convert_o(Smem& s, const Fp4Params& p, const Wor
 }
 
 // The pair's odd CTA, one thread: passes "stage written" on to the leader.
-// The release arrive orders the converters' writes (made visible to the async
-// proxy by their fences and to this thread by the wait) before the leader's
-// MMA; this thread has no memory traffic of its own for the release to wait on.
+// The arrive is relaxed: it reports finished work.  The boxes lie in this SM's
+// own shared memory, each converter warp has fenced its writes to the async
+// proxy and arrived on made, and this thread has seen that phase complete, so
+// nothing is left to publish to the leader, whose MMA makes this SM's tensor
+// core read them here.  A release arrive held every stage up by its round
+// trip: 1519 us instead of 1298 at 16 x 5 x 96 x 100k tokens.
 __device__ __forceinline__ void relay_made(Smem& s, const Fp4Params& p, int n, int stages,
                                            uint32_t rank, uint32_t lead) {
   const uint32_t full0 = mapa(smem_u32(&s.full[0]), lead);
@@ -587,12 +590,27 @@ __device__ __forceinline__ void relay_made(Smem& s, const Fp4Params& p, int n, i
       signal_abort(s, p, rank);
       return;
     }
-    mbar_arrive_cluster(full0 + 8u * stage);
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(
+                     full0 + 8u * stage)
+                 : "memory");
     if (++stage == (uint32_t)stages) {
       stage = 0;
       phase ^= 1u;
     }
   }
+}
+
+// One lane of a converged warp.  With the warp index and the TMEM base
+// shuffled from lane 0 the compiler keeps MMA descriptors in uniform
+// registers; behind a test of threadIdx they pass through vector registers, an
+// issue cost of about 45 cycles per MMA on an idle SM and more on a busy one
+// (a probe; N = 128 executes in 64).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t e;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(e));
+  return e != 0;
 }
 
 // --------------------------------------------------- S pair: MMA (rank 0) ----
@@ -1188,7 +1206,9 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   Smem& s = *reinterpret_cast<Smem*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  // Warp-uniform by construction, so that the MMA issue works on uniform
+  // registers (see elect_one).
+  const int warp = __shfl_sync(kFull, (int)threadIdx.x / 32, 0), lane = threadIdx.x % 32;
   const uint32_t rank = cluster_ctarank();
   const int unit = cluster_unit(p);
   if (unit < 0) {  // every CTA of the cluster read the same entry
@@ -1252,7 +1272,7 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = s.tmem_base;
+  const uint32_t tmem = __shfl_sync(kFull, s.tmem_base, 0);
   cluster_sync();  // every CTA's barriers exist before any remote operation
 
   // Fused combine ([K3-MLA], dcp_lse_combine, in the same launch): rank 0
@@ -1306,7 +1326,7 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1)
       else
         copy_pages(s, p, w, 0, 1, lane);
     } else if (warp == 1) {
-      if (lane == 0) {
+      if (elect_one()) {
         if (rank == 0)
           mma_s(s, p, w, tmem, rank);
         else if (rank == 2)
