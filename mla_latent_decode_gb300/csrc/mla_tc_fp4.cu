@@ -106,6 +106,7 @@ struct __align__(1024) Smem {
   uint64_t empty[kStages];   // every CTA: its boxes of a stage were consumed
   uint64_t sfull[2];        // S-CTAs: S buffer b holds a tile
   uint64_t sempty[2];       // rank 0: both S-CTAs read buffer b (16 warps)
+  uint64_t pmade[kNP];      // S-CTAs: slot k's message is written (4 warps)
   uint64_t pfull[kNP];      // O-CTAs: the P message of slot k landed here
   uint64_t pready[kNP];     // rank 2: rank 3's message of slot k landed
   uint64_t pempty[kNP];     // S-CTAs: slot k consumed by the O pair
@@ -665,6 +666,32 @@ __device__ __forceinline__ void mma_s(Smem& s, const Fp4Params& p, const Work& w
   }
 }
 
+// -------------------------------------------- S-CTA: P messages (warp 3) ----
+// One thread sends each page's message (P, rescale factors, flags) to the row
+// group's O-CTA once the four warps of its warpgroup have written it, so no
+// softmax warp spends its time on the copies or on a barrier per page.
+__device__ __forceinline__ void ship_pages(Smem& s, const Fp4Params& p, const Work& w,
+                                           uint32_t rank) {
+  const uint32_t orank = rank + 2;
+  const uint32_t peer_pfull0 = mapa(smem_u32(&s.pfull[0]), orank);
+  for (int m = 0; m < w.npages; ++m) {
+    const int k = m % kNP;
+    if (!mbar_wait(smem_u32(&s.pmade[k]), (m / kNP) & 1, &s.abort_flag)) {
+      signal_abort(s, p, rank);
+      return;
+    }
+    uint8_t* stg = s.pslot[k];
+    // The receiver armed pfull[k] with the byte count itself.
+    bulk_copy_to_peer(mapa(smem_u32(stg), orank), smem_u32(stg), kPMsgBytes,
+                      peer_pfull0 + 8u * k);
+    // Rank 2 issues the pair's P x V MMAs and decides on rescales: it gets
+    // rank 1's rescale flags too, counted on its own pfull[k].
+    if (rank == 1)
+      bulk_copy_to_peer(mapa(smem_u32(stg + kPeerFlagOff), 2), smem_u32(stg + kFlagOff), 16,
+                        mapa(smem_u32(&s.pfull[k]), 2));
+  }
+}
+
 // ------------------------------------------------------ S-CTA: the queries ----
 // Thread (g, r) of the softmax warpgroups takes dims 256 g .. 256 g + 255 of
 // row r (g = 0 also the RoPE part): the row's largest |q| gives the exponent
@@ -760,9 +787,7 @@ __device__ __forceinline__ void softmax(Smem& s, const Fp4Params& p, const Work&
 
   float m_ref = -INFINITY, l = 0.f;
   const uint32_t orank = rank + 2;  // the O-CTA of this row group
-  const uint32_t peer_pfull0 = mapa(smem_u32(&s.pfull[0]), orank);
   const int ntiles = (w.npages + kTilePages - 1) / kTilePages;
-  const uint32_t bar_wg = 2 + g;  // named barrier of this warpgroup
   for (int j = 0; j < ntiles; ++j) {
     const int msg = j * kTilePages + g;  // this warpgroup's page in the range
     const bool have = msg < w.npages;
@@ -805,8 +830,9 @@ __device__ __forceinline__ void softmax(Smem& s, const Fp4Params& p, const Work&
         max3(max3(mx[0], mx[1], mx[2]), max3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7])) * sc;
     // Row maximum over the whole tile: exchange with the other warpgroup.
     // The arrays alternate, so a tile's writes never meet the last one's reads.
+    // Warp `quad` of both warpgroups holds the same 32 rows: 64 threads meet.
     s.xch[buf][g][r] = mt_own;
-    named_bar_sync(1, 256);
+    named_bar_sync(4 + quad, 64);
     const float mt = fmaxf(mt_own, s.xch[buf][g ^ 1][r]);
     float alpha = 1.f;
     if (mt > -INFINITY) {
@@ -843,7 +869,7 @@ __device__ __forceinline__ void softmax(Smem& s, const Fp4Params& p, const Work&
     f2unpack(acc1, b0, b1);
     l += (a0 + a1) + (b0 + b1);
 
-    // Ship the page: wait for its slot, store, hand it to the peer.
+    // Write the page's message once its slot is free; warp 3 sends it.
     const int k = msg % kNP;
     const int u = msg / kNP;  // use index of slot k
     if (u > 0 && ok &&
@@ -861,17 +887,8 @@ __device__ __forceinline__ void softmax(Smem& s, const Fp4Params& p, const Work&
     const bool any = __any_sync(kFull, g == 0 && alpha != 1.f);
     if (lane == 0) reinterpret_cast<uint32_t*>(stg + kFlagOff)[quad] = any ? 1u : 0u;
     fence_proxy_async_smem();
-    named_bar_sync(bar_wg, 128);
-    if (quad == 0 && lane == 0 && ok && !s.abort_flag) {
-      // The receiver armed pfull[k] with the byte count itself.
-      bulk_copy_to_peer(mapa(smem_u32(stg), orank), smem_u32(stg), kPMsgBytes,
-                        peer_pfull0 + 8u * k);
-      // Rank 2 issues the pair's P x V MMAs and decides on rescales: it
-      // gets rank 1's rescale flags too, counted on its own pfull[k].
-      if (rank == 1)
-        bulk_copy_to_peer(mapa(smem_u32(stg + kPeerFlagOff), 2),
-                          smem_u32(stg + kFlagOff), 16, mapa(smem_u32(&s.pfull[k]), 2));
-    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&s.pmade[k]));
   }
 
   // Final statistics: l = sum of both warpgroups' partial sums.
@@ -1243,6 +1260,7 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(&s.sempty[i]), 16);  // 8 softmax warps x 2 S-CTAs
     }
     for (int i = 0; i < kNP; ++i) {
+      mbar_init(smem_u32(&s.pmade[i]), 4);
       mbar_init(smem_u32(&s.pfull[i]), 1);
       mbar_init(smem_u32(&s.pready[i]), 1);
       mbar_init(smem_u32(&s.pempty[i]), 1);
@@ -1342,6 +1360,9 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1)
         else
           relay_made(s, p, w.npages, kStagesO, rank, 2);
       }
+      __syncwarp();
+    } else if (warp == 3) {
+      if (s_side && lane == 0) ship_pages(s, p, w, rank);
       __syncwarp();
     } else if (warp >= kDequantWarp0) {
       const int tid = (warp - kDequantWarp0) * 32 + lane;
