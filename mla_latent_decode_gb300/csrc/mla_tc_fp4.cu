@@ -29,9 +29,9 @@
 //     warp 1       rank 0: issues S[256 rows, 128 tokens] = Q K^T into one of
 //                  two TMEM buffers (A = Q_nope from TMEM / Q_rope from shared
 //                  memory); rank 1: tells rank 0 which boxes are ready;
-//     warps 4-11   softmax: warpgroup g takes page g of a tile, thread = row;
+//     warps 4-11   softmax: warpgroup g takes every second tile, thread = row;
 //                  base-2 running statistics with lazy rescaling; P (f16) and
-//                  rescale factors travel to the O-CTA by bulk copy.
+//                  rescale factors travel to the O-CTA by bulk copy (warp 3).
 //   O-CTA rank 2 + r, O (128 x 512 fp32) of row group 2u + r in all of TMEM:
 //     warps 0, 12-15 as above, over dims [256 n + 128 r, +128), n = 0, 1;
 //     warp 1       rank 2: issues O += P V (B = V, MN-major from the same
@@ -83,6 +83,17 @@ constexpr float kTau = 8.f;          // lazy-rescale threshold (log2 units)
 constexpr uint32_t kFull = 0xffffffffu;
 constexpr uint16_t kMaskS = 0x3;     // cluster ranks of the S pair
 constexpr uint16_t kMaskO = 0xC;     // cluster ranks of the O pair
+// Register split of the S-CTAs (setmaxnreg): 512 threads launch with 128 each;
+// the control and converter warpgroups give some away so that the softmax can
+// hold 128 scores and their p.  One-way: nobody asks for registers back.  Of
+// five splits measured (16 x 5 x 96 x 100k tokens) 72/72/184 spills least and
+// runs 1140 us; 40/72/200 1175, 56/72/192 1176, 80/80/176 1243, 64/96/176 1260.
+constexpr int kRegsLaunch = 128;
+constexpr int kRegsControl = 72;
+constexpr int kRegsConvert = 72;
+constexpr int kRegsSoftmax = 184;
+static_assert(128 * (kRegsControl + kRegsConvert + 2 * kRegsSoftmax) <= kThreads * kRegsLaunch,
+              "register split exceeds the launch allocation");
 
 // Instruction descriptor for kind::f16 with F16 A/B and an FP32 accumulator.
 constexpr uint32_t idesc_f16_f32(int M, int N, bool b_mn_major) {
@@ -98,14 +109,15 @@ struct __align__(1024) Smem {
   uint8_t qrope[kRows * 128];               // S-CTA: Q_rope rows (f16)
   uint8_t pslot[kNP][kPSlotStride];
   float fin[kRows];
-  float xch[2][2][kRows];   // S-CTA: per-tile-parity, per-warpgroup row maxima
+  float mref[kRows];        // S-CTA: every row's running reference
+  float xch[2][2][kRows];   // S-CTA: per-warpgroup row values at either end
   uint64_t raw_full[kRaw];  // a raw page landed
   uint64_t raw_empty[kRaw]; // the converters are done with it
   uint64_t full[kStages];    // pair leader: both CTAs' boxes of a stage are written
   uint64_t made[kStages];    // pair's other CTA: its boxes of a stage are written
   uint64_t empty[kStages];   // every CTA: its boxes of a stage were consumed
   uint64_t sfull[2];        // S-CTAs: S buffer b holds a tile
-  uint64_t sempty[2];       // rank 0: both S-CTAs read buffer b (16 warps)
+  uint64_t sempty[2];       // rank 0: both S-CTAs read buffer b (8 warps)
   uint64_t pmade[kNP];      // S-CTAs: slot k's message is written (4 warps)
   uint64_t pfull[kNP];      // O-CTAs: the P message of slot k landed here
   uint64_t pready[kNP];     // rank 2: rank 3's message of slot k landed
@@ -757,9 +769,13 @@ __device__ __forceinline__ float place_query(Smem& s, uint32_t tmem, uint32_t la
 }
 
 // ------------------------------------------------------ S-CTA: softmax ----
-// Warps 4..11 of each S-CTA: warpgroup g = 0 (warps 4-7) takes page 0 of each
-// S tile, g = 1 (warps 8-11) page 1 (S columns [64 g, +64) of the buffer).
-// Thread = query row r (TMEM lane) of this CTA's row group.
+// Warps 4..11 of each S-CTA: warpgroup g (warps 4-7, 8-11) takes the tiles j
+// with j % 2 = g, which are those of S buffer g, so a tile's chain of loads,
+// maximum, exponentials and stores has two tile periods.  Thread = query row r
+// (TMEM lane) of this CTA's row group, with the tile's 128 scores in registers:
+// the buffer is free for the tile after next as soon as they are loaded (read
+// twice instead, the buffer is held through the first page's exponentials:
+// 1347 us at 16 x 5 x 96 x 100k tokens).
 __device__ __forceinline__ void softmax(Smem& s, const Fp4Params& p, const Work& w,
                                         uint32_t tmem, uint32_t rank, int warp, int lane) {
   const int g = (warp - 4) >> 2;
@@ -785,118 +801,131 @@ __device__ __forceinline__ void softmax(Smem& s, const Fp4Params& p, const Work&
     arrive_leader(smem_u32(&s.qready), rank, 0);
   }
 
-  float m_ref = -INFINITY, l = 0.f;
-  const uint32_t orank = rank + 2;  // the O-CTA of this row group
+  // The running reference m of each row passes from tile to tile through
+  // mref, from one warpgroup to the other; a warp of each holds the same 32
+  // rows, so 64 threads meet per hand-over.
+  float m_own = -INFINITY, l = 0.f;  // l: this warpgroup's sum, in units of 2^m_own
   const int ntiles = (w.npages + kTilePages - 1) / kTilePages;
-  for (int j = 0; j < ntiles; ++j) {
-    const int msg = j * kTilePages + g;  // this warpgroup's page in the range
-    const bool have = msg < w.npages;
-    const uint32_t buf = j & 1;
-    uint32_t s0[32], s1[32];
-    if (ok && !mbar_wait(smem_u32(&s.sfull[buf]), (j >> 1) & 1, &s.abort_flag)) ok = false;
+  for (int j = g; j < ntiles; j += 2) {
+    const int m0 = j * kTilePages;  // the tile's first page
+    const bool two = m0 + 1 < w.npages;
+    uint32_t sv[128];
+    if (ok && !mbar_wait(smem_u32(&s.sfull[g]), (j >> 1) & 1, &s.abort_flag)) ok = false;
     tc_fence_after();
-    if (__all_sync(kFull, ok) && have) {
-      const uint32_t col = tmem + lane_base + kSCol0 + 128u * buf + 64u * g;
-      tmem_ld32(col, s0);
-      tmem_ld32(col + 32, s1);
+    if (__all_sync(kFull, ok)) {
+      const uint32_t col = tmem + lane_base + kSCol0 + 128u * g;
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        tmem_ld32(col + 32u * q, *reinterpret_cast<uint32_t(*)[32]>(&sv[32 * q]));
       tmem_wait_ld();
     }
     tc_fence_before();
     __syncwarp();
-    if (lane == 0) signal_leader(smem_u32(&s.sempty[buf]), rank, 0);
-
+    if (lane == 0) signal_leader(smem_u32(&s.sempty[g]), rank, 0);
     // Columns this row may not see become -inf (a select: garbage or NaN in a
     // masked column never propagates); only the range's last tiles need it.
-    const int64_t nv = have ? n - (w.p0 + msg) * kPage : 0;
-    const int nvis = nv <= 0 ? 0 : (nv >= kPage ? kPage : (int)nv);
-    if (!__all_sync(kFull, nvis == kPage)) {
+    const int64_t nv = n - (w.p0 + m0) * kPage;
+    const int most = two ? 2 * kPage : kPage;
+    const int nvis = nv <= 0 ? 0 : (nv >= most ? most : (int)nv);
+    if (!__all_sync(kFull, nvis == 2 * kPage)) {
 #pragma unroll
-      for (int c = 0; c < 32; ++c) {
-        s0[c] = c < nvis ? s0[c] : __float_as_uint(-INFINITY);
-        s1[c] = 32 + c < nvis ? s1[c] : __float_as_uint(-INFINITY);
-      }
+      for (int c = 0; c < 128; ++c)
+        sv[c] = c < nvis ? sv[c] : __float_as_uint(-INFINITY);
     }
-    auto xs = [&](int c) -> float {
-      return __uint_as_float(c < 32 ? s0[c] : s1[c - 32]);
-    };
     // Row maximum of the raw scores; the scale is positive, so the maximum
     // of the scaled scores is the scaled maximum (rounding is monotone).
-    float mx[8];
+    float mx[16];
 #pragma unroll
-    for (int c = 0; c < 8; ++c)
-      mx[c] = fmaxf(max3(xs(c), xs(c + 8), xs(c + 16)),
-                    max3(max3(xs(c + 24), xs(c + 32), xs(c + 40)), xs(c + 48), xs(c + 56)));
-    const float mt_own =
-        max3(max3(mx[0], mx[1], mx[2]), max3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7])) * sc;
-    // Row maximum over the whole tile: exchange with the other warpgroup.
-    // The arrays alternate, so a tile's writes never meet the last one's reads.
-    // Warp `quad` of both warpgroups holds the same 32 rows: 64 threads meet.
-    s.xch[buf][g][r] = mt_own;
-    named_bar_sync(4 + quad, 64);
-    const float mt = fmaxf(mt_own, s.xch[buf][g ^ 1][r]);
-    float alpha = 1.f;
+    for (int c = 0; c < 16; ++c) {
+      const auto x = [&](int k) { return __uint_as_float(sv[c + 16 * k]); };
+      mx[c] = fmaxf(max3(x(0), x(1), x(2)), max3(max3(x(3), x(4), x(5)), x(6), x(7)));
+    }
+    const float mt =
+        max3(max3(max3(mx[0], mx[1], mx[2]), max3(mx[3], mx[4], mx[5]), max3(mx[6], mx[7], mx[8])),
+             max3(mx[9], mx[10], mx[11]), max3(max3(mx[12], mx[13], mx[14]), mx[15], -INFINITY)) *
+        sc;
+    if (j > 0) named_bar_sync(4 + 2 * quad + g, 64);  // the last tile's reference is in
+    const float m_old = j > 0 ? s.mref[r] : -INFINITY;
+    float m_ref = m_old, alpha = 1.f;
     if (mt > -INFINITY) {
-      if (m_ref == -INFINITY) {
+      if (m_old == -INFINITY) {
         m_ref = mt;  // first visible token of this row: O is still zero
-      } else if (mt > m_ref + kTau) {
-        alpha = ex2(m_ref - mt);
-        l *= alpha;
+      } else if (mt > m_old + kTau) {
+        alpha = ex2(m_old - mt);
         m_ref = mt;
       }
     }
-    if (!have) continue;
+    s.mref[r] = m_ref;
+    if (j + 1 < ntiles) named_bar_arrive(4 + 2 * quad + (g ^ 1), 64);
+    if (m_own != m_ref) {
+      l = m_own == -INFINITY ? 0.f : l * ex2(m_own - m_ref);
+      m_own = m_ref;
+    }
     // A row with nothing visible yet keeps m_ref = -inf: shift by 0 instead
     // so every p is ex2(-inf) = 0, not NaN.
     const float shift = m_ref == -INFINITY ? 0.f : m_ref;
-
-    // p = 2^(x * scale - m_ref): one packed FMA per pair of columns, the row
-    // sum of the unrounded p in two packed accumulators.  P is shipped as f16:
-    // at most 2^8 by the lazy rescaling, 2^-12 relative rounding.
-    uint32_t pk[32];
     const uint64_t sc2 = f2pack(sc, sc), nshift2 = f2pack(-shift, -shift);
-    uint64_t acc0 = f2pack(0.f, 0.f), acc1 = acc0;
+    const bool any = __any_sync(kFull, alpha != 1.f);
 #pragma unroll
-    for (int c = 0; c < 32; ++c) {
-      float ya, yb;
-      f2unpack(ffma2(f2pack(xs(2 * c), xs(2 * c + 1)), sc2, nshift2), ya, yb);
-      const float pa = ex2(ya), pb = ex2(yb);
-      if (c & 1) acc1 = fadd2(acc1, f2pack(pa, pb));
-      else acc0 = fadd2(acc0, f2pack(pa, pb));
-      pk[c] = pack_f16(pa, pb);
-    }
-    float a0, a1, b0, b1;
-    f2unpack(acc0, a0, a1);
-    f2unpack(acc1, b0, b1);
-    l += (a0 + a1) + (b0 + b1);
+    for (int q = 0; q < 2; ++q) {
+      if (q == 1 && !two) break;
+      // p = 2^(x * scale - m_ref): one packed FMA per pair of columns, the
+      // row sum of the unrounded p in two packed accumulators.  P is shipped
+      // as f16: at most 2^8 by the lazy rescaling, 2^-11 relative rounding.
+      uint32_t pk[32];
+      uint64_t acc0 = f2pack(0.f, 0.f), acc1 = acc0;
+#pragma unroll
+      for (int c = 0; c < 32; ++c) {
+        float ya, yb;
+        f2unpack(ffma2(f2pack(__uint_as_float(sv[64 * q + 2 * c]),
+                              __uint_as_float(sv[64 * q + 2 * c + 1])),
+                       sc2, nshift2),
+                 ya, yb);
+        const float pa = ex2(ya), pb = ex2(yb);
+        if (c & 1) acc1 = fadd2(acc1, f2pack(pa, pb));
+        else acc0 = fadd2(acc0, f2pack(pa, pb));
+        pk[c] = pack_f16(pa, pb);
+      }
+      float a0, a1, b0, b1;
+      f2unpack(acc0, a0, a1);
+      f2unpack(acc1, b0, b1);
+      l += (a0 + a1) + (b0 + b1);
 
-    // Write the page's message once its slot is free; warp 3 sends it.
-    const int k = msg % kNP;
-    const int u = msg / kNP;  // use index of slot k
-    if (u > 0 && ok &&
-        !mbar_wait(smem_u32(&s.pempty[k]), (u - 1) & 1, &s.abort_flag))
-      ok = false;
-    uint8_t* stg = s.pslot[k];
+      // Write the page's message once its slot is free; warp 3 sends it.
+      const int msg = m0 + q;
+      const int k = msg % kNP;
+      const int u = msg / kNP;  // use index of slot k
+      if (u > 0 && ok &&
+          !mbar_wait(smem_u32(&s.pempty[k]), (u - 1) & 1, &s.abort_flag))
+        ok = false;
+      uint8_t* stg = s.pslot[k];
 #pragma unroll
-    for (int cc = 0; cc < 8; ++cc)
-      // K-major, 128-B swizzle: 8-row groups 1024 B apart, 16-B chunk cc
-      // of row r at position cc ^ (r % 8) within its 128-B row.
-      *reinterpret_cast<uint4*>(stg + (r >> 3) * 1024 + box_chunk_offset(r & 7, cc)) =
-          make_uint4(pk[4 * cc], pk[4 * cc + 1], pk[4 * cc + 2], pk[4 * cc + 3]);
-    // The tile's rescale travels with its first page only.
-    reinterpret_cast<float*>(stg + kAlphaOff)[r] = g == 0 ? alpha : 1.f;
-    const bool any = __any_sync(kFull, g == 0 && alpha != 1.f);
-    if (lane == 0) reinterpret_cast<uint32_t*>(stg + kFlagOff)[quad] = any ? 1u : 0u;
-    fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(smem_u32(&s.pmade[k]));
+      for (int cc = 0; cc < 8; ++cc)
+        // K-major, 128-B swizzle: 8-row groups 1024 B apart, 16-B chunk cc
+        // of row r at position cc ^ (r % 8) within its 128-B row.
+        *reinterpret_cast<uint4*>(stg + (r >> 3) * 1024 + box_chunk_offset(r & 7, cc)) =
+            make_uint4(pk[4 * cc], pk[4 * cc + 1], pk[4 * cc + 2], pk[4 * cc + 3]);
+      // The tile's rescale travels with its first page only.
+      reinterpret_cast<float*>(stg + kAlphaOff)[r] = q == 0 ? alpha : 1.f;
+      if (lane == 0)
+        reinterpret_cast<uint32_t*>(stg + kFlagOff)[quad] = q == 0 && any ? 1u : 0u;
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&s.pmade[k]));
+    }
   }
 
-  // Final statistics: l = sum of both warpgroups' partial sums.
-  named_bar_sync(1, 256);  // the last tile's maxima have been read
-  s.xch[0][g][r] = l;
+  // Final statistics: both warpgroups' sums in units of the last reference.
+  s.xch[0][g][r] = m_own;
+  s.xch[1][g][r] = l;
   named_bar_sync(1, 256);
   if (g == 0) {
-    const float lt = l + s.xch[0][1][r];
+    const float m_ref = s.mref[r];
+    const auto part_sum = [&](int k) {
+      const float m = s.xch[0][k][r];
+      return m == -INFINITY ? 0.f : s.xch[1][k][r] * ex2(m - m_ref);
+    };
+    const float lt = part_sum(0) + part_sum(1);
     if (row_ok) {
       const int64_t rows = (int64_t)p.B * p.q_len * p.H;
       const int64_t part = (int64_t)w.split * (p.V / p.B) + w.shard;
@@ -908,8 +937,8 @@ __device__ __forceinline__ void softmax(Smem& s, const Fp4Params& p, const Work&
     fence_proxy_async_smem();
     named_bar_sync(2, 128);
     if (warp == 4 && lane == 0 && !s.abort_flag)
-      bulk_copy_to_peer(mapa(smem_u32(s.fin), orank), smem_u32(s.fin),
-                        kRows * 4, mapa(smem_u32(&s.fin_full), orank));
+      bulk_copy_to_peer(mapa(smem_u32(s.fin), rank + 2), smem_u32(s.fin), kRows * 4,
+                        mapa(smem_u32(&s.fin_full), rank + 2));
     // Before teardown: every P slot released by the O pair, so no remote
     // arrive can land after this CTA exits.
     for (int m = max(0, w.npages - kNP); m < w.npages && ok; ++m)
@@ -1257,7 +1286,7 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&s.sfull[i]), 1);
-      mbar_init(smem_u32(&s.sempty[i]), 16);  // 8 softmax warps x 2 S-CTAs
+      mbar_init(smem_u32(&s.sempty[i]), 8);  // a warpgroup of either S-CTA
     }
     for (int i = 0; i < kNP; ++i) {
       mbar_init(smem_u32(&s.pmade[i]), 4);
@@ -1323,7 +1352,9 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1)
                         (int64_t)w.b * R + r0 + r, p.out, p.lse_out, lane);
   };
 
-  // The pair's TMEM is released only after all four CTAs are done with it.
+  // Teardown, repeated at the end of every S-CTA role: they never rejoin, so no
+  // warp ever asks setmaxnreg for registers back.  The pair's TMEM is released
+  // only after all four CTAs are done with it.
   auto teardown = [&]() {
     if (p.counters) __threadfence();  // this CTA's part before the arrival
     tc_fence_before();
@@ -1336,42 +1367,51 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1)
     if (p.counters) fused_combine();
   };
 
-  if (w.npages > 0) {
-    const bool s_side = rank < 2, leads = (rank & 1) == 0;
-    if (warp == 0) {
-      if (s_side)
+  const bool leads = (rank & 1) == 0;
+  if (w.npages > 0 && rank < 2) {
+    if (warp < 4) {
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsControl));
+      if (warp == 0) {
         copy_pages(s, p, w, (int)rank, kTilePages, lane);
-      else
-        copy_pages(s, p, w, 0, 1, lane);
+      } else if (warp == 1) {
+        if (leads && elect_one()) mma_s(s, p, w, tmem, rank);
+      } else if (warp == 2) {
+        if (!leads && lane == 0)
+          relay_made(s, p, (w.npages + 1) / kTilePages * kStagesS, kStagesS, rank, 0);
+      } else if (lane == 0) {
+        ship_pages(s, p, w, rank);
+      }
+      __syncwarp();
+      teardown();
+      return;
+    }
+    if (warp >= kDequantWarp0) {
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsConvert));
+      convert_s(s, p, w, rank, (warp - kDequantWarp0) * 32 + lane, lane);
+      teardown();
+      return;
+    }
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+    softmax(s, p, w, tmem, rank, warp, lane);
+    teardown();
+    return;
+  }
+  if (w.npages > 0) {
+    if (warp == 0) {
+      copy_pages(s, p, w, 0, 1, lane);
     } else if (warp == 1) {
       if (elect_one()) {
-        if (rank == 0)
-          mma_s(s, p, w, tmem, rank);
-        else if (rank == 2)
+        if (leads)
           mma_o(s, p, w, tmem, rank);
-        else if (rank == 3)
+        else
           relay_o(s, p, w, rank);
       }
       __syncwarp();
     } else if (warp == 2) {
-      if (lane == 0 && !leads) {
-        if (s_side)
-          relay_made(s, p, (w.npages + 1) / kTilePages * kStagesS, kStagesS, rank, 0);
-        else
-          relay_made(s, p, w.npages, kStagesO, rank, 2);
-      }
-      __syncwarp();
-    } else if (warp == 3) {
-      if (s_side && lane == 0) ship_pages(s, p, w, rank);
+      if (lane == 0 && !leads) relay_made(s, p, w.npages, kStagesO, rank, 2);
       __syncwarp();
     } else if (warp >= kDequantWarp0) {
-      const int tid = (warp - kDequantWarp0) * 32 + lane;
-      if (s_side)
-        convert_s(s, p, w, rank, tid, lane);
-      else
-        convert_o(s, p, w, rank, tid, lane);
-    } else if (s_side && warp >= 4) {
-      softmax(s, p, w, tmem, rank, warp, lane);
+      convert_o(s, p, w, rank, (warp - kDequantWarp0) * 32 + lane, lane);
     } else if (warp >= 4 && warp < 8) {
       correct_and_store(s, p, &o_map, w, tmem, rank, warp, lane);
     } else if (warp >= 8) {
