@@ -457,33 +457,33 @@ __device__ __forceinline__ void convert_s(Smem& s, const Fp4Params& p, const Wor
     const bool have = kTilePages * j + (int)rank < w.npages;
     const uint8_t* row = s.raw[slot] + t * kFp4RowBytes;
     uint4 sa = make_uint4(0, 0, 0, 0), sb = sa;
+    uint4 code[kBoxesS + 1];
     bool bad = false;
+    // The codes of stage st: loaded before the previous stage's fence, so the
+    // loads pass under it (the tile's first stage: under the page's wait).
+    const auto load_codes = [&](int st) {
+#pragma unroll
+      for (int k = 0; k < kBoxesS; ++k) {
+        const int c = kBoxesS * st + k;
+        if (c < 8) {
+          code[k] = *reinterpret_cast<const uint4*>(row + 32 * c + 16 * h);
+        } else {
+          code[k] = *reinterpret_cast<const uint4*>(row + kFp4RopeOff + 32 * h);
+          code[k + 1] = *reinterpret_cast<const uint4*>(row + kFp4RopeOff + 32 * h + 16);
+        }
+      }
+    };
     if (have) {
       ok = ok && mbar_wait(smem_u32(&s.raw_full[slot]), rphase, &s.abort_flag);
-      if (!__all_sync(kFull, ok)) break;
       bad = s.raw_bad[slot] != 0;
-      if (!bad) {
-        sa = *reinterpret_cast<const uint4*>(row + kFp4ScaleOff);
-        sb = *reinterpret_cast<const uint4*>(row + kFp4ScaleOff + 16);
-      }
+      load_codes(0);
+      sa = *reinterpret_cast<const uint4*>(row + kFp4ScaleOff);
+      sb = *reinterpret_cast<const uint4*>(row + kFp4ScaleOff + 16);
+      if (bad) sa = sb = make_uint4(0, 0, 0, 0);
     }
     const uint32_t sw[8] = {sa.x, sa.y, sa.z, sa.w, sb.x, sb.y, sb.z, sb.w};
 #pragma unroll
     for (int st = 0; st < kStagesS; ++st) {
-      // This stage's codes are on their way while the stage is waited for.
-      uint4 code[kBoxesS + 1];
-      if (have) {
-#pragma unroll
-        for (int k = 0; k < kBoxesS; ++k) {
-          const int c = kBoxesS * st + k;
-          if (c < 8) {
-            code[k] = *reinterpret_cast<const uint4*>(row + 32 * c + 16 * h);
-          } else {
-            code[k] = *reinterpret_cast<const uint4*>(row + kFp4RopeOff + 32 * h);
-            code[k + 1] = *reinterpret_cast<const uint4*>(row + kFp4RopeOff + 32 * h + 16);
-          }
-        }
-      }
       ok = ok && mbar_wait(smem_u32(&s.empty[st]), phase, &s.abort_flag);
       if (!__all_sync(kFull, ok)) break;
       if (have) {
@@ -502,6 +502,7 @@ __device__ __forceinline__ void convert_s(Smem& s, const Fp4Params& p, const Wor
             *reinterpret_cast<uint4*>(box + box_chunk_offset(t, 4 * h + 3)) = plain8(b.z, b.w);
           }
         }
+        if (st + 1 < kStagesS) load_codes(st + 1);
         fence_proxy_async_smem();
       }
       __syncwarp();
