@@ -106,8 +106,17 @@ constexpr double kPlanUnitCostBf16 = 16.0;
 constexpr double kPlanUnitCostFp8 = 32.0;
 constexpr double kPlanSplitCost = 1.0;
 
-static double plan_unit_cost(mla_kv_dtype kv_dtype) {
-  return kv_dtype == MLA_KV_FP8_E4M3 ? kPlanUnitCostFp8 : kPlanUnitCostBf16;
+// The few-row FP4 kernel's unit (one CTA; a page costs it about 0.9 us too).
+constexpr double kPlanUnitCostFew = 8.0;
+
+// Whether mla_fp4_few.cu serves the launch: one CTA per (request, part).
+static bool few_rows(mla_kv_dtype kv_dtype, int q_len, int H) {
+  return kv_dtype == MLA_KV_FP4_E2M1 && (int64_t)q_len * H <= kFp4FewRows;
+}
+
+static double plan_unit_cost(mla_kv_dtype kv_dtype, bool few) {
+  return few ? kPlanUnitCostFew
+             : kv_dtype == MLA_KV_FP8_E4M3 ? kPlanUnitCostFp8 : kPlanUnitCostBf16;
 }
 
 // The planners score each candidate plan by its list-scheduling makespan
@@ -226,6 +235,27 @@ int mla_plan_ex(int V, int q_len, int H, int rows_per_unit,
   return MLA_OK;
 }
 
+// Slots (resident work units) of the kernel that serves the launch (num_sms >
+// 0: those of a device with that many SMs).  BF16 and FP4: 256 query rows per
+// 4-CTA cluster; E4M3: 128 rows per 2-CTA cluster; FP4 with few rows: a CTA.
+static int decode_slots(mla_kv_dtype kv_dtype, int q_len, int H, int num_sms) {
+  const bool fp8 = kv_dtype == MLA_KV_FP8_E4M3;
+  const bool few = few_rows(kv_dtype, q_len, H);
+  const int ctas = few ? 1 : fp8 ? 2 : 4;
+  if (num_sms > 0) return std::max(1, num_sms / ctas);
+  int slots;
+  if (few) {
+    int dev = 0;
+    const cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+    slots = mla_num_sms(dev);
+  } else {
+    slots = fp8 ? pair_slots_fp8() : mla_cluster_slots();
+  }
+  if (slots == 0) return fail(MLA_ERR_CUDA, "no decode cluster fits on this device");
+  return slots;
+}
+
 int mla_plan(int B, int q_len, int H, int num_shards, mla_kv_dtype kv_dtype,
              const int32_t* seq_lens_host, int num_sms, int* num_splits_out,
              float* wave_eff_out) {
@@ -233,20 +263,13 @@ int mla_plan(int B, int q_len, int H, int num_shards, mla_kv_dtype kv_dtype,
     return fail(MLA_ERR_INVALID_ARG, "B and num_shards must be >= 1");
   if (!known_kv_dtype(kv_dtype))
     return fail(MLA_ERR_INVALID_ARG, "unknown kv_dtype %d", (int)kv_dtype);
-  // BF16: 256 query rows per 4-CTA cluster; E4M3: 128 rows per 2-CTA cluster.
   const bool fp8 = kv_dtype == MLA_KV_FP8_E4M3;
-  const int ctas = fp8 ? 2 : 4;
-  int slots;
-  if (num_sms > 0) {
-    slots = std::max(1, num_sms / ctas);
-  } else {
-    slots = fp8 ? pair_slots_fp8() : mla_cluster_slots();
-    if (slots < 0) return slots;
-    if (slots == 0) return fail(MLA_ERR_CUDA, "no decode cluster fits on this device");
-  }
+  const int slots = decode_slots(kv_dtype, q_len, H, num_sms);
+  if (slots < 0) return slots;
   return mla_plan_ex(B * num_shards, q_len, H,
                      fp8 ? MLA_ROWS_PER_UNIT / 2 : MLA_ROWS_PER_UNIT,
-                     seq_lens_host, slots, 64, plan_unit_cost(kv_dtype), kPlanSplitCost,
+                     seq_lens_host, slots, 64,
+                     plan_unit_cost(kv_dtype, few_rows(kv_dtype, q_len, H)), kPlanSplitCost,
                      num_splits_out, wave_eff_out, nullptr);
 }
 
@@ -427,17 +450,6 @@ static int plan_parts_impl(int V, int q_len, int H, int rows_per_unit,
   return MLA_OK;
 }
 
-// Cluster slots of the kernel that serves kv_dtype (num_sms > 0: that many
-// SMs divided by the cluster size instead of asking the device).
-static int decode_slots(mla_kv_dtype kv_dtype, int num_sms) {
-  const bool fp8 = kv_dtype == MLA_KV_FP8_E4M3;
-  const int ctas = fp8 ? 2 : 4;
-  if (num_sms > 0) return std::max(1, num_sms / ctas);
-  const int slots = fp8 ? pair_slots_fp8() : mla_cluster_slots();
-  if (slots == 0) return fail(MLA_ERR_CUDA, "no decode cluster fits on this device");
-  return slots;
-}
-
 int mla_plan_parts_ex(int V, int q_len, int H, int rows_per_unit,
                       const int32_t* seq_lens_host, int slots, int s_max,
                       int max_parts, double c0, double lam,
@@ -506,12 +518,13 @@ int mla_plan_parts(int B, int q_len, int H, int num_shards,
     return fail(MLA_ERR_INVALID_ARG, "B and num_shards must be >= 1");
   if (!known_kv_dtype(kv_dtype))
     return fail(MLA_ERR_INVALID_ARG, "unknown kv_dtype %d", (int)kv_dtype);
-  const int slots = decode_slots(kv_dtype, num_sms);
+  const int slots = decode_slots(kv_dtype, q_len, H, num_sms);
   if (slots < 0) return slots;
   return mla_plan_parts_ex(B * num_shards, q_len, H,
                            kv_dtype == MLA_KV_FP8_E4M3 ? MLA_ROWS_PER_UNIT / 2
                                                        : MLA_ROWS_PER_UNIT,
-                           seq_lens_host, slots, 64, max_parts, plan_unit_cost(kv_dtype),
+                           seq_lens_host, slots, 64, max_parts,
+                           plan_unit_cost(kv_dtype, few_rows(kv_dtype, q_len, H)),
                            kPlanSplitCost, split_pages_out, num_parts_out,
                            wave_eff_out, nullptr);
 }
@@ -526,12 +539,13 @@ int mla_plan_sched(int B, int q_len, int H, int num_shards,
     return fail(MLA_ERR_INVALID_ARG, "B and num_shards must be >= 1");
   if (!known_kv_dtype(kv_dtype))
     return fail(MLA_ERR_INVALID_ARG, "unknown kv_dtype %d", (int)kv_dtype);
-  const int slots = decode_slots(kv_dtype, num_sms);
+  const int slots = decode_slots(kv_dtype, q_len, H, num_sms);
   if (slots < 0) return slots;
   return mla_plan_sched_ex(B * num_shards, q_len, H,
                            kv_dtype == MLA_KV_FP8_E4M3 ? MLA_ROWS_PER_UNIT / 2
                                                        : MLA_ROWS_PER_UNIT,
-                           seq_lens_host, slots, 64, max_parts, plan_unit_cost(kv_dtype),
+                           seq_lens_host, slots, 64, max_parts,
+                           plan_unit_cost(kv_dtype, few_rows(kv_dtype, q_len, H)),
                            kPlanSplitCost, split_pages_out, num_parts_out,
                            work_out, work_capacity, num_work_out, wave_eff_out,
                            nullptr);

@@ -46,9 +46,8 @@
 #include <cstring>
 
 #include "mla_combine.cuh"
-#include "mla_fp4.cuh"
+#include "mla_fp4_decode.cuh"
 #include "mla_tma.cuh"
-#include "ptx_sm103.cuh"
 
 namespace mla {
 namespace {
@@ -64,13 +63,11 @@ constexpr int kBoxesO = 4;           // O-CTA: a stage is a page's four boxes
 constexpr int kStagesO = 2;
 constexpr int kStages = 3;           // barriers of the larger ring
 constexpr int kRaw = 3;              // raw page ring
-constexpr int kRawBytes = MLA_PAGE_SIZE * kFp4RowBytes;  // 22528
 constexpr int kTilePages = 2;        // pages per S tile, one per S-CTA
 constexpr int kChunks = MLA_ROW_DIM / 64;                // 9 boxes per page
 static_assert(kBoxesS * kStagesS == kBoxes && kBoxesO * kStagesO <= kBoxes, "ring");
 constexpr int kNP = 4;               // P message slots (page index mod 4)
 constexpr int kRows = MLA_ROWS_PER_UNIT / 2;  // 128 query rows per CTA
-constexpr int kPage = MLA_PAGE_SIZE;           // 64 tokens
 constexpr int kPBytes = kRows * kPage * 2;          // 16384
 constexpr int kAlphaOff = kPBytes;                  // float alpha[128]
 constexpr int kFlagOff = kPBytes + kRows * 4;       // uint32 flags[4]
@@ -79,8 +76,6 @@ constexpr int kPeerFlagOff = kPMsgBytes;            // rank 2: rank 1's flags
 constexpr int kPSlotStride = 17408;                 // 17 KB, 1024-aligned
 constexpr uint32_t kSCol0 = 256;                    // two S buffers of 128 columns
 constexpr int kDequantWarp0 = 12;
-constexpr float kTau = 8.f;          // lazy-rescale threshold (log2 units)
-constexpr uint32_t kFull = 0xffffffffu;
 constexpr uint16_t kMaskS = 0x3;     // cluster ranks of the S pair
 constexpr uint16_t kMaskO = 0xC;     // cluster ranks of the O pair
 // Register split of the S-CTAs (setmaxnreg): 512 threads launch with 128 each;
@@ -95,13 +90,8 @@ constexpr int kRegsSoftmax = 184;
 static_assert(128 * (kRegsControl + kRegsConvert + 2 * kRegsSoftmax) <= kThreads * kRegsLaunch,
               "register split exceeds the launch allocation");
 
-// Instruction descriptor for kind::f16 with F16 A/B and an FP32 accumulator.
-constexpr uint32_t idesc_f16_f32(int M, int N, bool b_mn_major) {
-  return (1u << 4) | ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) |
-         ((uint32_t)(M >> 4) << 24);
-}
-constexpr uint32_t kIdescS = idesc_f16_f32(256, 128, false);
-constexpr uint32_t kIdescO = idesc_f16_f32(256, 256, true);
+constexpr uint32_t kIdescS = idesc_f16_f32(256, 128, false, false);
+constexpr uint32_t kIdescO = idesc_f16_f32(256, 256, false, true);
 
 struct __align__(1024) Smem {
   uint8_t ring[kBoxes][kBoxBytes];          // 72 KB of operand boxes
@@ -140,40 +130,6 @@ constexpr int kSmemBytes = (int)sizeof(Smem) + 1024;
 static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
 static_assert(kPMsgBytes % 16 == 0 && kRawBytes % 1024 == 0, "copy sizes, alignment");
 static_assert(kPeerFlagOff + 16 <= kPSlotStride, "P slot layout");
-
-struct Fp4Params {
-  const uint8_t* kv;
-  const float* g;          // the pool's factor
-  int64_t num_slots;
-  const int32_t* r2t;
-  int64_t r2t_stride;
-  const int32_t* seq_lens;
-  const int32_t* kv_limit;
-  const int32_t* split_pages;  // [V, num_splits + 1] page boundaries or NULL
-  const int32_t* work;         // unit ids in launch order or NULL
-  int B, q_len, H, V, num_splits, U;  // U = row pairs (256 rows) per request
-  float scale_log2;        // sm_scale * log2(e)
-  float* O_part;
-  float* LSE_part;
-  int* status;
-  int q_box_rows;          // rows of a query TMA box: min(128, B * q_len * H)
-  int o_tma;               // O_part rows leave by TMA store (o_map is valid)
-  int o_bf16;              // O_part holds bf16 values (else fp32)
-  __nv_bfloat16* out;      // fused combine (NULL counters: partials only)
-  float* lse_out;
-  int* counters;
-};
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<uint32_t*>(&h);
-}
 
 // Three-operand maximum (one ALU instruction on sm_100 and later).
 __device__ __forceinline__ float max3(float a, float b, float c) {
@@ -243,90 +199,17 @@ __device__ __forceinline__ void signal_abort(Smem& s, const Fp4Params& p,
 // (split * V + v) * U + u, the cluster's index or, with a work list, the
 // list's entry at that index (an entry that names no unit: skip); this
 // CTA's row group is 2u + (rank & 1).
-struct Work {
-  int v, b, shard, split, r_base, nrows, npages;
-  int64_t L, p0;
-  int64_t nmin;  // fewest tokens any query of the request sees
+struct Work : UnitRange {
+  int r_base, nrows;
 };
-
-// The cluster's unit id, or -1 for a work-list entry outside [0, units).
-__device__ __forceinline__ int cluster_unit(const Fp4Params& p) {
-  const int k = blockIdx.x / kCtas;
-  if (!p.work) return k;
-  const int unit = p.work[k];
-  return unit < 0 || (int64_t)unit >= (int64_t)p.V * p.num_splits * p.U ? -1
-                                                                         : unit;
-}
 
 __device__ __forceinline__ Work unit_work(const Fp4Params& p, int unit,
                                           uint32_t rank) {
   Work w;
-  const int u = unit % p.U;
-  unit /= p.U;
-  w.v = unit % p.V;
-  w.split = unit / p.V;
-  w.b = w.v % p.B;
-  w.shard = w.v / p.B;
-  const int R = p.q_len * p.H;
-  w.r_base = (2 * u + (int)(rank & 1)) * kRows;
-  w.nrows = max(0, min(kRows, R - w.r_base));
-  int64_t L = p.seq_lens[w.v];
-  if (L > p.r2t_stride) L = p.r2t_stride;
-  if (L < 0) L = 0;
-  w.L = L;
-  const int64_t P = (L + kPage - 1) / kPage;
-  int64_t p1;
-  split_page_range(
-      p.split_pages ? p.split_pages + (int64_t)w.v * (p.num_splits + 1) : nullptr,
-      p.num_splits, w.split, P, w.p0, p1);
-  w.npages = (int)(p1 - w.p0);
-  // Tokens in [nmin, L) are visible to some query rows of the request and
-  // masked for others; tokens at or past L to none (see convert_o).
-  int64_t nmin = L - p.q_len + 1;
-  if (p.kv_limit) {
-    nmin = L;
-    for (int i = 0; i < p.q_len; ++i) {
-      const int64_t n = p.kv_limit[(int64_t)w.v * p.q_len + i];
-      nmin = n < nmin ? n : nmin;
-    }
-  }
-  w.nmin = nmin < 0 ? 0 : (nmin > L ? L : nmin);
+  unit_range(p, unit / p.U, w);
+  w.r_base = (2 * (unit % p.U) + (int)(rank & 1)) * kRows;
+  w.nrows = max(0, min(kRows, p.q_len * p.H - w.r_base));
   return w;
-}
-
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
-// The page-table entry of page m of the unit's range as stored (0 past the
-// range), and its check: the base slot, or -1 if it lies outside the pool.
-// Split so that a load can be put in flight before its value is needed.
-__device__ __forceinline__ int32_t page_entry(const Fp4Params& p, const Work& w,
-                                              int m) {
-  if (m >= w.npages) return 0;
-  return p.r2t[(int64_t)w.v * p.r2t_stride + (w.p0 + m) * kPage];
-}
-__device__ __forceinline__ int32_t checked_base(const Fp4Params& p, int32_t base) {
-  if (base < 0 || (base & (kPage - 1)) || (int64_t)base + kPage > p.num_slots)
-    return -1;
-  return base;
-}
-__device__ __forceinline__ int32_t page_base(const Fp4Params& p, const Work& w,
-                                             int m) {
-  return checked_base(p, page_entry(p, w, m));
-}
-
-// Bulk copy of `bytes` (a multiple of 16) from global memory into this CTA's
-// shared memory, completing on `bar`.
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
-                                          uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, "
-      "[%3];" ::"r"(dst),
-      "l"(src), "r"(bytes), "r"(bar)
-      : "memory");
 }
 
 // S-CTA, warp 0, at kernel entry: initialise the query barriers and put the
@@ -414,18 +297,6 @@ __device__ __forceinline__ void copy_pages(Smem& s, const Fp4Params& p, const Wo
 }
 
 // ------------------------------------------------------------- conversion ---
-// 16 codes (two words) and the f16 pair of their scale (both halves equal) ->
-// two 16-byte chunks of operand.
-__device__ __forceinline__ uint4 scaled8(uint32_t codes, uint32_t s2) {
-  uint32_t h[4];
-  e2m1x8_to_f16(codes, h);
-  return make_uint4(h2mul(h[0], s2), h2mul(h[1], s2), h2mul(h[2], s2), h2mul(h[3], s2));
-}
-__device__ __forceinline__ uint4 plain8(uint32_t a, uint32_t b) {
-  return make_uint4(e4m3x2_to_f16(a), e4m3x2_to_f16(a >> 16), e4m3x2_to_f16(b),
-                    e4m3x2_to_f16(b >> 16));
-}
-
 // Half a token's 64-dim chunk of c_kv (32 codes, scales `two` = 2 bytes) into
 // row `t` of a box: chunks 4 h .. 4 h + 3.
 __device__ __forceinline__ void convert_half(uint8_t* box, const uint4& c,
@@ -521,15 +392,6 @@ __device__ __forceinline__ void convert_s(Smem& s, const Fp4Params& p, const Wor
   if (!__all_sync(kFull, ok) && lane == 0) signal_abort(s, p, rank);
 }
 
-// Block scales with every NaN (0x7F, 0xFF) replaced by 0.
-__device__ __forceinline__ uint32_t finite_scales(uint32_t w) {
-  uint32_t keep = 0;
-#pragma unroll
-  for (int k = 0; k < 4; ++k)
-    if (((w >> (8 * k)) & 0x7Fu) != 0x7Fu) keep |= 0xFFu << (8 * k);
-  return w & keep;
-}
-
 // O-CTA rank 2 + hh, warps 12..15: dims [256 n + 128 hh, +128) of every page
 // (n = 0, 1; box 2n + i of the page's stage = dims 256 n + 128 hh + 64 i).  A
 // masked token gets p = 0 exactly, but 0 * NaN would still poison O = P V: the
@@ -612,19 +474,6 @@ __device__ __forceinline__ void relay_made(Smem& s, const Fp4Params& p, int n, i
       phase ^= 1u;
     }
   }
-}
-
-// One lane of a converged warp.  With the warp index and the TMEM base
-// shuffled from lane 0 the compiler keeps MMA descriptors in uniform
-// registers; behind a test of threadIdx they pass through vector registers, an
-// issue cost of about 45 cycles per MMA on an idle SM and more on a busy one
-// (a probe; N = 128 executes in 64).
-__device__ __forceinline__ bool elect_one() {
-  uint32_t e;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(e));
-  return e != 0;
 }
 
 // --------------------------------------------------- S pair: MMA (rank 0) ----
@@ -1257,7 +1106,7 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1)
   // registers (see elect_one).
   const int warp = __shfl_sync(kFull, (int)threadIdx.x / 32, 0), lane = threadIdx.x % 32;
   const uint32_t rank = cluster_ctarank();
-  const int unit = cluster_unit(p);
+  const int unit = launch_unit(p, blockIdx.x / kCtas);
   if (unit < 0) {  // every CTA of the cluster read the same entry
     if (rank == 0 && threadIdx.x == 0 && p.status)
       atomicOr(p.status, MLA_STATUS_BAD_WORK);
@@ -1451,6 +1300,8 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1)
 
 int launch_fp4(const DecodeArgs& a) {
   Fp4Params p;
+  p.q_nope = static_cast<const uint4*>(a.q_nope);
+  p.q_rope = static_cast<const uint4*>(a.q_rope);
   p.kv = static_cast<const uint8_t*>(a.kv);
   p.g = a.kv_scale;
   p.num_slots = a.num_slots;
@@ -1476,6 +1327,8 @@ int launch_fp4(const DecodeArgs& a) {
   const int64_t units = (int64_t)p.V * p.num_splits * p.U;
   if (units * kCtas > 0x7fffffff)
     return fail(MLA_ERR_INVALID_ARG, "grid too large");
+  p.o_bf16 = a.o_bf16;
+  if (a.q_len * a.H <= kFp4FewRows) return launch_fp4_few(p, a.stream);
   CUtensorMap qn_map, qr_map;
   int rc = make_query_maps(&qn_map, &qr_map, a, &p.q_box_rows);
   if (rc != MLA_OK) return rc;
@@ -1487,7 +1340,6 @@ int launch_fp4(const DecodeArgs& a) {
   std::memset(&o_map, 0, sizeof(o_map));
   const int64_t o_rows =
       (int64_t)p.num_splits * a.num_shards * a.B * a.q_len * a.H;
-  p.o_bf16 = a.o_bf16;
   if (p.o_bf16) {
     const uint64_t dims[3] = {(uint64_t)MLA_VALUE_DIM, (uint64_t)o_rows, 1};
     const uint64_t strides[2] = {(uint64_t)MLA_VALUE_DIM * 2,

@@ -133,6 +133,9 @@ CASES = {
     "rows_129": dict(B=1, q=3, H=43, lens=[1281]),
     "long": dict(B=1, q=2, H=8, lens=[20011]),
     "heads16_q1": dict(B=9, q=1, H=16, lens=[4097, 2000, 31, 640, 3, 1, 999, 64, 2500]),
+    "rows_17": dict(B=2, q=1, H=17, lens=[777, 128]),
+    "rows_32_q4": dict(B=3, q=4, H=8, lens=[1000, 65, 3]),
+    "rows_30_long": dict(B=1, q=5, H=6, lens=[9001]),
     "heads33_q1": dict(B=3, q=1, H=33, lens=[900, 65, 1025]),
 }
 
@@ -241,6 +244,54 @@ def test_bad_pages_read_as_zeros_and_lengths_are_clamped(simt):
     case.up()
     case.run(1, simt=simt)
     assert case.status & mla.STATUS_BAD_LENGTH
+
+
+ROWS = [dict(B=2, q=1, H=16, lens=[1300, 70]), dict(B=2, q=3, H=9, lens=[640, 2]),
+        dict(B=2, q=2, H=60, lens=[1000, 129]), dict(B=2, q=5, H=96, lens=[700, 64])]
+
+
+@pytest.mark.parametrize("shape", ROWS)
+def test_bf16_parts(shape):
+    case = Case(seed=20, **shape)
+    O, LSE = case.run(2, part_dtype=torch.bfloat16)
+    assert O.dtype == torch.bfloat16 and case.status == 0
+    check(case, O, LSE, 2, heads=[0, case.H - 1], bf16=True)
+    O32, LSE32 = case.run(2)
+    assert torch.equal(O, O32.bfloat16()) and torch.equal(LSE, LSE32)
+
+
+@pytest.mark.parametrize("shape", ROWS)
+def test_one_launch_equals_two(shape):
+    """decode_fused and decode_scratch merge the very parts of decode_partial."""
+    case = Case(seed=21, **shape)
+    S, bnd, work, _ = mla.plan_sched(case.B, case.q, case.H, case.lens, kv_dtype="fp4_e2m1")
+    S, bnd = (S, bnd) if S > 1 else (2, None)
+    bnd = None if bnd is None else torch.as_tensor(bnd, dtype=torch.int32).cuda()
+    O, LSE = case.run(S, bnd=bnd)
+    out, lse = mla.lse_combine(O, LSE)
+    args = (case.qn, case.qr, case.kv, case.gd, case.r2t, case.sl, None, S, SCALE)
+    counters = mla.fused_counters(case.B, case.q, case.H, "cuda")
+    for _ in range(2):  # the counters are left zero
+        out2, lse2 = mla.decode_fused(*args, split_pages=bnd, counters=counters)
+        assert torch.allclose(out2.float(), out.float(), rtol=2.0 ** -7, atol=1e-6)
+        assert torch.allclose(lse2, lse, rtol=1e-6, atol=1e-6, equal_nan=True)
+        assert int(counters.abs().sum()) == 0
+    out3, lse3 = mla.decode_scratch(*args, split_pages=bnd)
+    assert torch.equal(out3, out2) and torch.equal(lse3, lse2)
+
+
+def test_rising_maxima_rescale():
+    """Scores that grow along the context: the references rise tile by tile."""
+    for shape in (dict(B=1, q=1, H=5), dict(B=1, q=2, H=60)):
+        case = Case(lens=[1500], seed=22, q_scale=0.05, **shape)
+        t = np.arange(1500)
+        rows = case.r2t_host[0, :1500]
+        case.kv_host[rows, 256:288] = np.minimum(16 + t // 16, 0x7E)[:, None]
+        case.kv_host[rows, :256] &= 0x77
+        case.q_nope = case.q_nope.abs()
+        case.up()
+        O, LSE = case.run(2)
+        check(case, O, LSE, 2, heads=[0, case.H - 1])
 
 
 def test_side_stream_equals_default_stream():
