@@ -7,23 +7,26 @@
 // bound the work (352 bytes per token against 34 to 70 kFLOP) as long as the
 // conversion and the shared-memory traffic keep up.  The products are turned
 // round: tokens and value dims are the M side, the query rows the N side,
-//   S^T[128 tokens, N rows] = K Q^T,   O^T[512 dims, N rows] += V^T P^T,
+//   S^T[64 tokens, N rows] = K Q^T,   O^T[512 dims, N rows] += V^T P^T,
 // so a row costs N = 16 or 32 of the MMA's width, not a padded 128 of its
-// height, and one CTA holds everything of a (request, part):
-//   warp 0       raw pages by bulk copy;
-//   warps 8-15   convert: thread = token; 128 dims of c_kv at a time go into two
-//                16-KB boxes (128 tokens x 64 dims, 128-byte swizzle), which are
-//                the K-major A of the scores and the MN-major A of the outputs;
-//                the RoPE key goes to TMEM (A of the scores only);
-//   warp 1       issues the MMAs of a two-page tile: 36 of M = 128, N, K = 16 for
-//                S^T, then 8 per 128 value dims for O^T;
-//   warps 4-7    softmax: thread = token, its N scores in registers.  The
-//                running references only change when some score passes its
-//                row's by 2^8: one vote per tile; then the maxima cross the
-//                lanes and warps and O^T (lane = dim) is rescaled in place.
-//                Row sums stay per thread until the end.
+// height, and one CTA holds everything of a (request, part).  Per page:
+//   warp 0       copies the raw page (one bulk copy; a ring of two);
+//   warps 8-15   convert it in two halves of the dims: four threads per token,
+//                a block of 16 of every 64 dims each, into 8-KB boxes (64 tokens
+//                x 64 dims f16, 128-byte swizzle) that are the K-major A of the
+//                scores and, read MN-major, the A of the outputs; two sets of
+//                boxes, passed on and freed by halves;
+//   warp 1       issues 36 MMAs of M = 64, N, K = 16 for the next page's S^T,
+//                then this page's 4 per 128 value dims of O^T (M = 128);
+//   warps 4-7    softmax: two threads per token, N / 2 scores each.  The running
+//                references only change when some score passes its row's by
+//                2^8: one vote per page; then the maxima cross the lanes and
+//                warps and O^T (lane = dim) is rescaled in place.  Row sums
+//                stay per thread until the end.
 // P (f16, row by row over the tokens) and Q (f16, mla_tc_fp4.cu's row scale)
-// are the K-major B operands in shared memory.
+// are the K-major B operands in shared memory.  An MMA of this width costs its
+// operand bytes at 128 per cycle (probe: M = 64, N = 16: 23 cycles, M = 128: 39),
+// so a page's products take about 1400 cycles.
 #include <cstring>
 
 #include "mla_combine.cuh"
@@ -35,24 +38,23 @@ namespace {
 using namespace ptx;
 
 constexpr int kThreads = 512;
-constexpr int kTileTokens = 128;
 constexpr int kChunks = MLA_ROW_DIM / 64;    // 9 chunks of 64 dims
-constexpr int kVBox = kTileTokens * 128;     // 16 KB: 128 tokens x 64 dims f16
-constexpr int kBatches = 5;                  // per tile: 4 x 128 dims, RoPE
-constexpr uint32_t kColS = 32;               // the RoPE key takes TMEM columns [0, 32)
+constexpr int kBox = kPage * 128;            // 8 KB: 64 tokens x 64 dims f16
+constexpr int kRaw = 2;                      // raw pages in flight
 
 template <int N>
 struct Few {
   static constexpr int kQBox = N * 128;               // N rows x 64 values
-  static constexpr int kRaw = N == 16 ? 3 : 2;        // raw pages that fit
-  static constexpr uint32_t kColO = kColS + N;        // four blocks of N columns
-  static constexpr uint32_t kIdescS = idesc_f16_f32(128, N, false, false);
+  static constexpr uint32_t kColO = 2 * N;            // after two S^T buffers
+  static constexpr uint32_t kIdescS = idesc_f16_f32(64, N, false, false);
   static constexpr uint32_t kIdescO = idesc_f16_f32(128, N, true, false);
-  static_assert(kColO + 4 * N <= 512, "TMEM columns");
+  static constexpr uint32_t kCols = 256;              // 6 N, a power of two
+  static_assert(6 * N <= kCols, "TMEM columns");
   struct __align__(1024) Smem {
-    uint8_t v[kChunks - 1][kVBox];
+    uint8_t v[2][kChunks - 1][kBox];
+    uint8_t kr[kBox];           // the RoPE key (one set: N = 32 leaves no room)
     uint8_t q[kChunks][kQBox];
-    uint8_t pt[2][kQBox];       // P: rows x 64 tokens, for either page
+    uint8_t pt[2][kQBox];       // P: rows x 64 tokens
     uint8_t raw[kRaw][kRawBytes];
     float sc[N];                // softmax scale (log2) * g * the row's 2^(e - 14)
     float mref[N];              // running references
@@ -61,13 +63,12 @@ struct Few {
     float wred[4][N];           // per-warp maxima, then sums
     int32_t lim[N];             // tokens of the request the row sees
     uint64_t raw_full[kRaw];    // a raw page landed
-    uint64_t raw_empty[kRaw];   // its four converter warps are done with it
-    uint64_t cfull[kBatches];   // batch i of the tile is converted (4 warps)
-    uint64_t sfull;             // S^T is in TMEM (and K has been read)
-    uint64_t sread;             // the softmax has read S^T (4 warps)
-    uint64_t pready;            // P is written and O^T rescaled (4 warps)
-    uint64_t vfree[4];          // the products with value dims 128 b .. have read
-                                // their boxes (b = 3: all, and P)
+    uint64_t raw_empty[kRaw];   // the eight converter warps have read it
+    uint64_t cfull[2][2];       // half h of box set b is written (8 warps)
+    uint64_t sfull[2];          // S^T buffer b holds a page's scores
+    uint64_t pready[2];         // P buffer b is written, O^T rescaled (4 warps)
+    uint64_t vfree[2][2];       // the outputs' products have read half h of set b
+                                // (h = 1: all of it, and P)
     uint64_t drain;
     uint32_t raw_bad[kRaw];
     uint32_t tmem_base;
@@ -124,7 +125,6 @@ __device__ __forceinline__ bool any_of_128(bool x) {
 template <int N>
 __device__ __forceinline__ void copy_pages(typename Few<N>::Smem& s, const Fp4Params& p,
                                            const UnitRange& w, int lane) {
-  constexpr int kRaw = Few<N>::kRaw;
   bool ok = true;
   int issued = 0;
   int32_t ent = 0;
@@ -210,104 +210,83 @@ __device__ __forceinline__ void place_query(typename Few<N>::Smem& s, const Fp4P
   }
 }
 
-// Warps 8..15: warp % 4 gives the tokens (TMEM lanes) 32 (warp % 4) .. of the
-// tile, so warps 2, 3 mod 4 hold the second page; the two sets of four warps
-// take alternate batches.  The scales of tokens past the length or of a bad
+// Warps 8..15: thread = token tid / 4 and block tid % 4 of each 64 dims (the
+// 8-byte reads of rows 352 bytes apart and the swizzled 16-byte writes are both
+// free of bank conflicts).  The scales of tokens past the length or of a bad
 // page count as 0.  A NaN scale of a token that only some rows see has to show
 // in those rows' scores but must not reach O through a masked p = 0: the boxes,
 // shared by both products, hold 0 there and the token's RoPE key, which only
 // the scores read, is NaN instead.
 template <int N>
 __device__ __forceinline__ void convert(typename Few<N>::Smem& s, const Fp4Params& p,
-                                        const UnitRange& w, uint32_t tmem, int warp,
-                                        int lane) {
-  constexpr int kRaw = Few<N>::kRaw;
-  const int quad = warp & 3, set = (warp >> 2) & 1;
-  const int tok = quad * 32 + lane, pg = tok >> 6, tr = tok & 63;
-  const uint32_t trow = tmem + ((uint32_t)(quad * 32) << 16);
-  const int ntiles = (w.npages + 1) / 2;
+                                        const UnitRange& w, int tid, int lane) {
+  const int t = tid >> 2, part = tid & 3;
+  const uint32_t trow = (t >> 3) * 1024 + (t & 7) * 128;
+  const uint32_t o0 = trow + (((2 * part) ^ (t & 7)) << 4);
+  const uint32_t o1 = trow + (((2 * part + 1) ^ (t & 7)) << 4);
   bool ok = true;
-  for (int t = 0; t < ntiles; ++t) {
-    const int m = 2 * t + pg;
-    const bool have = m < w.npages;
-    const int slot = m % kRaw;
-    const uint8_t* row = s.raw[slot] + tr * kFp4RowBytes;
-    uint32_t sw[8] = {};
-    bool bad = false, san = false;
-    if (have) {
-      ok = ok && mbar_wait(smem_u32(&s.raw_full[slot]), (m / kRaw) & 1, &s.abort_flag);
-      const int64_t at = (w.p0 + m) * kPage + tr;
-      bad = s.raw_bad[slot] != 0;
-      san = at >= w.nmin && at < w.L;
-      if (!bad && at < w.L) {
-        const uint4 a = *reinterpret_cast<const uint4*>(row + kFp4ScaleOff);
-        const uint4 b = *reinterpret_cast<const uint4*>(row + kFp4ScaleOff + 16);
-        sw[0] = a.x, sw[1] = a.y, sw[2] = a.z, sw[3] = a.w;
-        sw[4] = b.x, sw[5] = b.y, sw[6] = b.z, sw[7] = b.w;
-      }
-    }
+  for (int m = 0; m < w.npages; ++m) {
+    const int slot = m % kRaw, set = m & 1;
+    const uint8_t* row = s.raw[slot] + t * kFp4RowBytes;
+    ok = ok && mbar_wait(smem_u32(&s.raw_full[slot]), (m / kRaw) & 1, &s.abort_flag);
+    const int64_t at = (w.p0 + m) * kPage + t;
+    const bool bad = s.raw_bad[slot] != 0;
+    uint2 code[8];
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+      code[c] = *reinterpret_cast<const uint2*>(row + 32 * c + 8 * part);
+    const uint4 sa = *reinterpret_cast<const uint4*>(row + kFp4ScaleOff);
+    const uint4 sb = *reinterpret_cast<const uint4*>(row + kFp4ScaleOff + 16);
+    uint4 rope = *reinterpret_cast<const uint4*>(row + kFp4RopeOff + 16 * part);
+    uint32_t sw[8] = {sa.x, sa.y, sa.z, sa.w, sb.x, sb.y, sb.z, sb.w};
     bool nan = false;
-    if (san) {
+    if (at >= w.nmin || bad) {
+      const bool live = at < w.L && !bad;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const uint32_t f = finite_scales(sw[k]);
-        nan |= f != sw[k];
-        sw[k] = f;
+      for (int c = 0; c < 8; ++c) {
+        const uint32_t f = live ? finite_scales(sw[c]) : 0u;
+        nan |= live && f != sw[c];
+        sw[c] = f;
       }
+      if (bad) rope = make_uint4(0, 0, 0, 0);
     }
+    __syncwarp();  // every lane has read the page
+    if (lane == 0) mbar_arrive(smem_u32(&s.raw_empty[slot]));
 #pragma unroll
-    for (int i = 0; i < kBatches; ++i) {
-      if (((t + i) & 1) != set) continue;
-      uint4 code[4];
-      if (have) {
-        const uint8_t* src = row + (i < 4 ? 64 * i : kFp4RopeOff);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) code[k] = *reinterpret_cast<const uint4*>(src + 16 * k);
-      }
-      // The last tile's products have read this batch's boxes (the outputs come
-      // after the scores) or its RoPE key (the scores).
-      if (t > 0)
-        ok = ok && mbar_wait(i < 4 ? smem_u32(&s.vfree[i]) : smem_u32(&s.sfull), (t - 1) & 1,
-                             &s.abort_flag);
+    for (int h = 0; h < 2; ++h) {
+      // The page two back has left this half.
+      if (m > 1)
+        ok = ok && mbar_wait(smem_u32(&s.vfree[set][h]), ((m >> 1) - 1) & 1, &s.abort_flag);
+      // The last page's scores have read the RoPE key.
+      if (h == 1 && m > 0)
+        ok = ok && mbar_wait(smem_u32(&s.sfull[set ^ 1]), ((m - 1) >> 1) & 1, &s.abort_flag);
       if (!__all_sync(kFull, ok)) break;
-      if (have && i < 4) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {  // 32 dims: half a box row
-          uint8_t* box = s.v[2 * i + (k >> 1)] + (tok >> 3) * 1024 + (tok & 7) * 128;
-          const uint32_t sc =
-              e4m3x2_to_f16((sw[2 * i + (k >> 1)] >> (16 * (k & 1))) & 0xFFFFu);
-          const uint32_t lo = __byte_perm(sc, sc, 0x1010), hi = __byte_perm(sc, sc, 0x3232);
-          const uint32_t cw[4] = {code[k].x, code[k].y, code[k].z, code[k].w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            *reinterpret_cast<uint4*>(box + (((4 * (k & 1) + e) ^ (tok & 7)) << 4)) =
-                scaled8(cw[e], e < 2 ? lo : hi);
-        }
-        fence_proxy_async_smem();
-      } else if (have) {
-        uint32_t h[32];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          if (bad) code[k] = make_uint4(0, 0, 0, 0);
-          const uint4 lo = plain8(code[k].x, code[k].y), hi = plain8(code[k].z, code[k].w);
-          h[8 * k] = lo.x, h[8 * k + 1] = lo.y, h[8 * k + 2] = lo.z, h[8 * k + 3] = lo.w;
-          h[8 * k + 4] = hi.x, h[8 * k + 5] = hi.y, h[8 * k + 6] = hi.z, h[8 * k + 7] = hi.w;
-        }
-        if (nan) h[0] = 0x7E007E00u;
-        tmem_st32(trow, h);
-        tmem_wait_st();
-        tc_fence_before();
+      for (int c = 4 * h; c < 4 * h + 4; ++c) {
+        const uint32_t sc = e4m3x2_to_f16((sw[c] >> (8 * part)) & 0xFFu);
+        const uint32_t s2 = __byte_perm(sc, sc, 0x1010);
+        *reinterpret_cast<uint4*>(s.v[set][c] + o0) = scaled8(code[c].x, s2);
+        *reinterpret_cast<uint4*>(s.v[set][c] + o1) = scaled8(code[c].y, s2);
       }
+      if (h == 1) {
+        uint4 r0 = plain8(rope.x, rope.y);
+        if (nan) r0.x = 0x7E007E00u;
+        *reinterpret_cast<uint4*>(s.kr + o0) = r0;
+        *reinterpret_cast<uint4*>(s.kr + o1) = plain8(rope.z, rope.w);
+      }
+      fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&s.cfull[i]));
+      if (lane == 0) mbar_arrive(smem_u32(&s.cfull[set][h]));
     }
     if (!__all_sync(kFull, ok)) break;
-    if (have && lane == 0) mbar_arrive(smem_u32(&s.raw_empty[slot]));
   }
   if (!__all_sync(kFull, ok) && lane == 0) give_up(s, p);
 }
 
-// Warp 1, one lane: every MMA of the unit.
+// Warp 1, one lane: every MMA of the unit: of this page's outputs and the next
+// page's scores, whichever is ready first (in either fixed order one of them
+// holds up the converters: scores first 120 us, as they come 90 us, for 32
+// requests x 16 heads, 2k to 60k tokens).
 template <int N>
 __device__ __forceinline__ void issue_mmas(typename Few<N>::Smem& s, const Fp4Params& p,
                                            const UnitRange& w, uint32_t tmem) {
@@ -316,46 +295,64 @@ __device__ __forceinline__ void issue_mmas(typename Few<N>::Smem& s, const Fp4Pa
   const uint64_t pd = sdesc_sw128(smem_u32(s.pt[0]), 16, 1024);
   // K: K-major, 128-byte rows.  V^T: MN-major, the next 64 dims one box on, the
   // next 8 tokens 1 KB on.
-  const uint64_t kd = sdesc_sw128(smem_u32(s.v[0]), 16, 1024);
-  const uint64_t vd = sdesc_sw128(smem_u32(s.v[0]), kVBox, 1024);
-  const int ntiles = (w.npages + 1) / 2;
+  const uint64_t kd = sdesc_sw128(smem_u32(s.v[0][0]), 16, 1024);
+  const uint64_t rd = sdesc_sw128(smem_u32(s.kr), 16, 1024);
+  const uint64_t vd = sdesc_sw128(smem_u32(s.v[0][0]), kBox, 1024);
+  constexpr uint64_t kSet = (kChunks - 1) * (kBox >> 4);
   bool ok = true;
-  for (int t = 0; t < ntiles && ok; ++t) {
-    if (t > 0) ok = mbar_wait(smem_u32(&s.sread), (t - 1) & 1, &s.abort_flag);
+  const auto scores = [&](int m) {
+    const uint32_t set = m & 1;
+    const uint32_t d = tmem + set * N;
+    const uint64_t k0 = kd + set * kSet;
 #pragma unroll
-    for (int i = 0; i < kBatches; ++i) {
-      ok = ok && mbar_wait(smem_u32(&s.cfull[i]), t & 1, &s.abort_flag);
-      if (!ok) break;
+    for (int h = 0; h < 2; ++h) {
+      ok = ok && mbar_wait(smem_u32(&s.cfull[set][h]), (m >> 1) & 1, &s.abort_flag);
+      if (!ok) return;
       tc_fence_after();
-      if (i < 4) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const int c = 2 * i + (k >> 2);
-          mma_ss(tmem + kColS, kd + c * (kVBox >> 4) + 2 * (k & 3),
-                 qd + c * (F::kQBox >> 4) + 2 * (k & 3), F::kIdescS, (i | k) ? 1u : 0u);
-        }
-      } else {
+      for (int c = 4 * h; c < 4 * h + 4 + h; ++c)
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          mma_ts(tmem + kColS, tmem + 8u * k, qd + 8 * (F::kQBox >> 4) + 2 * k, F::kIdescS, 1u);
+          mma_ss(d, (c < 8 ? k0 + c * (kBox >> 4) : rd) + 2 * k,
+                 qd + c * (F::kQBox >> 4) + 2 * k, F::kIdescS, (c | k) ? 1u : 0u);
+    }
+    mma_commit(smem_u32(&s.sfull[set]));
+  };
+  if (w.npages > 0) scores(0);
+  for (int m = 0; m < w.npages && ok; ++m) {
+    const uint32_t set = m & 1;
+    // The buffer of S^T(m + 1) was read before P(m - 1) was ready.
+    const uint32_t pbar = smem_u32(&s.pready[set]), pph = (m >> 1) & 1;
+    bool next = m + 1 < w.npages;  // its scores are still to issue
+    if (next) {
+      const uint32_t cbar = smem_u32(&s.cfull[set ^ 1][0]), cph = ((m + 1) >> 1) & 1;
+      const uint64_t t0 = globaltimer();
+      for (uint32_t it = 1; !mbar_try_wait(pbar, pph); ++it) {
+        if (mbar_try_wait(cbar, cph)) {
+          scores(m + 1);
+          next = false;
+          break;
+        }
+        if ((it & 63) == 0 && (*const_cast<volatile int*>(&s.abort_flag) ||
+                               globaltimer() - t0 > kWaitNs)) {
+          ok = false;
+          break;
+        }
       }
     }
-    if (!ok) break;
-    mma_commit(smem_u32(&s.sfull));
-    ok = mbar_wait(smem_u32(&s.pready), t & 1, &s.abort_flag);
+    ok = ok && mbar_wait(pbar, pph, &s.abort_flag);
     if (!ok) break;
     tc_fence_after();
-    const int pages = min(2, w.npages - 2 * t);
+    const uint64_t v0 = vd + set * kSet, p0 = pd + set * (F::kQBox >> 4);
 #pragma unroll
     for (int b = 0; b < 4; ++b) {
-      const uint32_t d = tmem + F::kColO + (uint32_t)(N * b);
-      for (int g = 0; g < pages; ++g)
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          mma_ss(d, vd + 2 * b * (kVBox >> 4) + 512 * g + 128 * k,
-                 pd + g * (F::kQBox >> 4) + 2 * k, F::kIdescO, (t | g | k) ? 1u : 0u);
-      mma_commit(smem_u32(&s.vfree[b]));
+      for (int k = 0; k < 4; ++k)
+        mma_ss(tmem + F::kColO + (uint32_t)(N * b), v0 + 2 * b * (kBox >> 4) + 128 * k,
+               p0 + 2 * k, F::kIdescO, k ? 1u : (m ? 1u : 0u));
+      if (b & 1) mma_commit(smem_u32(&s.vfree[set][b >> 1]));
     }
+    if (next) scores(m + 1);
   }
   if (!ok) give_up(s, p);
   // No MMA may still run when the accumulators are freed.
@@ -364,77 +361,101 @@ __device__ __forceinline__ void issue_mmas(typename Few<N>::Smem& s, const Fp4Pa
   mbar_wait(smem_u32(&s.drain), 0, &never);
 }
 
-// Warps 4..7: thread = token 32 (warp % 4) + lane of every tile; at the end,
-// and when O^T is rescaled, thread = value dim of a block of 128.
+// N columns of the 16 TMEM lanes from `taddr` on, the first half of them in
+// lanes 0..15, the second half in lanes 16..31.
+template <int N>
+__device__ __forceinline__ void tmem_ld_halves(uint32_t taddr, uint32_t (&r)[N / 2]) {
+  if constexpr (N == 32)
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x32bx2.x16.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16], 16;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+          "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]),
+          "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+  else
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x32bx2.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8], 8;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+          "=r"(r[6]), "=r"(r[7])
+        : "r"(taddr));
+}
+
+// Warps 4..7: an accumulator of M = 64 rows lies in the first 16 lanes of every
+// TMEM quadrant, so warp `quad` has tokens 16 quad .. + 15 and a thread token
+// 16 quad + lane % 16 with rows N / 2 (lane / 16) .. .  At the end, and when O^T
+// is rescaled, thread = value dim of a block of 128.
 template <int N>
 __device__ __forceinline__ void softmax(typename Few<N>::Smem& s, const Fp4Params& p,
                                         const UnitRange& w, uint32_t tmem, int warp, int lane) {
   using F = Few<N>;
-  const int quad = warp & 3, tok = quad * 32 + lane;
+  constexpr int H = N / 2;
+  const int quad = warp & 3, dim = quad * 32 + lane;
+  const int tok = quad * 16 + (lane & 15), n0 = H * (lane >> 4);
   const uint32_t trow = tmem + ((uint32_t)(quad * 32) << 16);
   const int R = p.q_len * p.H;
-  const int ntiles = (w.npages + 1) / 2;
   bool ok = true;
-  float l[N];
+  float l[H], sc[H], m_ref[H];
 #pragma unroll
-  for (int n = 0; n < N; ++n) l[n] = 0.f;
-  for (int t = 0; t < ntiles; ++t) {
-    uint32_t x[N];
-    ok = ok && mbar_wait(smem_u32(&s.sfull), t & 1, &s.abort_flag);
+  for (int k = 0; k < H; ++k) {
+    l[k] = 0.f;
+    sc[k] = s.sc[n0 + k];
+    m_ref[k] = -INFINITY;
+  }
+  uint8_t* const dst0 = s.pt[0] + (tok & 7) * 2;
+  for (int m = 0; m < w.npages; ++m) {
+    const uint32_t set = m & 1;
+    uint32_t x[H];
+    ok = ok && mbar_wait(smem_u32(&s.sfull[set]), (m >> 1) & 1, &s.abort_flag);
     tc_fence_after();
     if (__all_sync(kFull, ok)) {
-      tmem_ld_n<N>(trow + kColS, x);
+      tmem_ld_halves<N>(trow + set * N, x);
       tmem_wait_ld();
     }
-    tc_fence_before();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(smem_u32(&s.sread));
-
     // Scores in units of log2; tokens a row may not see become -inf (a select:
     // garbage or NaN in a masked score never propagates).
-    const int64_t t0 = (w.p0 + 2 * t) * kPage;
-    const bool open = t0 + kTileTokens <= w.nmin && 2 * t + 1 < w.npages;
-    const int64_t at = 2 * t + (tok >> 6) < w.npages ? t0 + tok : INT64_MAX;
-    float y[N];
+    const int64_t t0 = (w.p0 + m) * kPage;
+    const bool open = t0 + kPage <= w.nmin;
+    float y[H];
     bool over = false;
 #pragma unroll
-    for (int n = 0; n < N; ++n) {
-      y[n] = __uint_as_float(x[n]) * s.sc[n];
-      if (!open && at >= s.lim[n]) y[n] = -INFINITY;
-      over |= y[n] > s.mref[n] + kTau;
+    for (int k = 0; k < H; ++k) {
+      y[k] = __uint_as_float(x[k]) * sc[k];
+      if (!open && t0 + tok >= s.lim[n0 + k]) y[k] = -INFINITY;
+      over |= y[k] > m_ref[k] + kTau;
     }
     if (any_of_128(over)) {
-      // Some row's maximum rises: the tile's maxima over all 128 tokens, as
-      // integers that order like the floats (a NaN counts as none).
-      float mine = 0.f;
+      // Some row's maximum rises: the page's maxima over its 64 tokens.
 #pragma unroll
-      for (int n = 0; n < N; ++n) {
-        const int b = __float_as_int(y[n] == y[n] ? y[n] : -INFINITY);
-        const int m = __reduce_max_sync(kFull, b ^ ((b >> 31) & 0x7FFFFFFF));
-        if (lane == n) mine = __int_as_float(m ^ ((m >> 31) & 0x7FFFFFFF));
+      for (int k = 0; k < H; ++k) {
+        float z = fmaxf(y[k], -INFINITY);  // a NaN counts as none
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) z = fmaxf(z, __shfl_xor_sync(kFull, z, o));
+        if ((lane & 15) == 0) s.wred[quad][n0 + k] = z;
       }
-      if (lane < N) s.wred[quad][lane] = mine;
       named_bar_sync(2, 128);
-      if (tok < N) {
-        const float mt = fmaxf(fmaxf(s.wred[0][tok], s.wred[1][tok]),
-                               fmaxf(s.wred[2][tok], s.wred[3][tok]));
-        const float old = s.mref[tok];
+      if (dim < N) {
+        const float mt = fmaxf(fmaxf(s.wred[0][dim], s.wred[1][dim]),
+                               fmaxf(s.wred[2][dim], s.wred[3][dim]));
+        const float old = s.mref[dim];
         float a = 1.f;
         if (mt > -INFINITY && (old == -INFINITY || mt > old + kTau)) {
           if (old > -INFINITY) a = ex2(old - mt);  // else O and l are still zero
-          s.mref[tok] = mt;
+          s.mref[dim] = mt;
         }
-        s.alpha[tok] = a;
+        s.alpha[dim] = a;
       }
       named_bar_sync(2, 128);
       bool scale = false;
 #pragma unroll
-      for (int n = 0; n < N; ++n) {
-        l[n] *= s.alpha[n];
-        scale |= s.alpha[n] != 1.f;
+      for (int n = 0; n < N; ++n) scale |= s.alpha[n] != 1.f;
+#pragma unroll
+      for (int k = 0; k < H; ++k) {
+        l[k] *= s.alpha[n0 + k];
+        m_ref[k] = s.mref[n0 + k];
       }
-      if (scale && t > 0) {  // the same in every thread
-        ok = ok && mbar_wait(smem_u32(&s.vfree[3]), (t - 1) & 1, &s.abort_flag);
+      if (scale && m > 0) {  // the same in every thread
+        ok = ok && mbar_wait(smem_u32(&s.vfree[set ^ 1][1]), ((m - 1) >> 1) & 1, &s.abort_flag);
         tc_fence_after();
         if (__all_sync(kFull, ok)) {
 #pragma unroll 1
@@ -452,49 +473,49 @@ __device__ __forceinline__ void softmax(typename Few<N>::Smem& s, const Fp4Param
       }
     }
     // p = 2^(y - m_ref) (0 for a row that has seen nothing yet), f16 at
-    // [row][token] once the last tile's products have read P.
-    if (t > 0) ok = ok && mbar_wait(smem_u32(&s.vfree[3]), (t - 1) & 1, &s.abort_flag);
-    uint8_t* dst = s.pt[tok >> 6] + (tok & 7) * 2;
-    const int cc = (tok & 63) >> 3;
+    // [row][token] once the outputs of two pages back have read this buffer.
+    if (m > 1) ok = ok && mbar_wait(smem_u32(&s.vfree[set][1]), ((m >> 1) - 1) & 1, &s.abort_flag);
+    uint8_t* const dst = dst0 + set * F::kQBox;
 #pragma unroll
-    for (int n = 0; n < N; ++n) {
-      const float m = s.mref[n];
-      const float e = ex2(y[n] - (m == -INFINITY ? 0.f : m));
-      l[n] += e;
-      *reinterpret_cast<__half*>(dst + (n >> 3) * 1024 + (n & 7) * 128 + ((cc ^ (n & 7)) << 4)) =
-          __float2half_rn(e);
+    for (int k = 0; k < H; ++k) {
+      const int n = n0 + k;
+      const float e = ex2(y[k] - (m_ref[k] == -INFINITY ? 0.f : m_ref[k]));
+      l[k] += e;
+      *reinterpret_cast<__half*>(dst + (n >> 3) * 1024 + (n & 7) * 128 +
+                                 (((tok >> 3) ^ (n & 7)) << 4)) = __float2half_rn(e);
     }
     fence_proxy_async_smem();
     tc_fence_before();
     __syncwarp();
-    if (lane == 0) mbar_arrive(smem_u32(&s.pready));
-    if (!__all_sync(kFull, ok) && lane == 0) give_up(s, p);
+    if (lane == 0) mbar_arrive(smem_u32(&s.pready[set]));
   }
+  if (!__all_sync(kFull, ok) && lane == 0) give_up(s, p);
 
   // Row sums over the lanes and warps, LSE, and O_part = g O / l: lane = dim, so
   // every store of a warp is one line of a row.
   named_bar_sync(2, 128);
 #pragma unroll
-  for (int n = 0; n < N; ++n) {
-    float z = l[n];
+  for (int k = 0; k < H; ++k) {
+    float z = l[k];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(kFull, z, o);
-    if (lane == 0) s.wred[quad][n] = z;
+    for (int o = 8; o > 0; o >>= 1) z += __shfl_xor_sync(kFull, z, o);
+    if ((lane & 15) == 0) s.wred[quad][n0 + k] = z;
   }
   named_bar_sync(2, 128);
   const int64_t rows = (int64_t)p.B * R;
   const int64_t part = (int64_t)w.split * (p.V / p.B) + w.shard;
   const int64_t row0 = part * rows + (int64_t)w.b * R;
-  if (tok < N) {
-    const float lt = (s.wred[0][tok] + s.wred[1][tok]) + (s.wred[2][tok] + s.wred[3][tok]);
-    if (tok < R)
+  if (dim < N) {
+    const float lt = (s.wred[0][dim] + s.wred[1][dim]) + (s.wred[2][dim] + s.wred[3][dim]);
+    if (dim < R)
       // no visible token: -inf; a NaN sum (a NaN score seen) stays NaN
-      p.LSE_part[row0 + tok] =
-          lt == 0.f ? -INFINITY : (s.mref[tok] + log2f(lt)) * 0.69314718055994531f;
-    s.fin[tok] = lt == 0.f ? 0.f : p.g[0] / lt;
+      p.LSE_part[row0 + dim] =
+          lt == 0.f ? -INFINITY : (s.mref[dim] + log2f(lt)) * 0.69314718055994531f;
+    s.fin[dim] = lt == 0.f ? 0.f : p.g[0] / lt;
   }
   named_bar_sync(2, 128);
-  ok = ok && mbar_wait(smem_u32(&s.vfree[3]), (ntiles - 1) & 1, &s.abort_flag);
+  const int last = w.npages - 1;
+  ok = ok && mbar_wait(smem_u32(&s.vfree[last & 1][1]), (last >> 1) & 1, &s.abort_flag);
   tc_fence_after();
   if (!__all_sync(kFull, ok)) {
     if (lane == 0) give_up(s, p);
@@ -505,7 +526,7 @@ __device__ __forceinline__ void softmax(typename Few<N>::Smem& s, const Fp4Param
     uint32_t o[N];
     tmem_ld_n<N>(trow + F::kColO + (uint32_t)(N * b), o);
     tmem_wait_ld();
-    const int64_t at = row0 * MLA_VALUE_DIM + 128 * b + tok;
+    const int64_t at = row0 * MLA_VALUE_DIM + 128 * b + dim;
 #pragma unroll
     for (int n = 0; n < N; ++n) {
       if (n >= R) break;
@@ -540,22 +561,25 @@ __global__ void __launch_bounds__(kThreads, 1) mla_partial_fp4_few_kernel(const 
   if (threadIdx.x == 0) {
     s.abort_flag = 0;
     s.last = 0;
-    for (int i = 0; i < F::kRaw; ++i) {
+    for (int i = 0; i < kRaw; ++i) {
       mbar_init(smem_u32(&s.raw_full[i]), 1);
-      mbar_init(smem_u32(&s.raw_empty[i]), 4);
+      mbar_init(smem_u32(&s.raw_empty[i]), 8);
     }
-    for (int i = 0; i < kBatches; ++i) mbar_init(smem_u32(&s.cfull[i]), 4);
-    for (int i = 0; i < 4; ++i) mbar_init(smem_u32(&s.vfree[i]), 1);
-    mbar_init(smem_u32(&s.sfull), 1);
-    mbar_init(smem_u32(&s.sread), 4);
-    mbar_init(smem_u32(&s.pready), 4);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&s.sfull[i]), 1);
+      mbar_init(smem_u32(&s.pready[i]), 4);
+      for (int h = 0; h < 2; ++h) {
+        mbar_init(smem_u32(&s.cfull[i][h]), 8);
+        mbar_init(smem_u32(&s.vfree[i][h]), 1);
+      }
+    }
     mbar_init(smem_u32(&s.drain), 1);
     fence_mbar_init();
     if (p.seq_lens[w.v] > p.r2t_stride && p.status)
       atomicOr(p.status, MLA_STATUS_BAD_LENGTH);
   }
   if (warp == 1) {
-    tmem_alloc(smem_u32(&s.tmem_base), 512);
+    tmem_alloc(smem_u32(&s.tmem_base), F::kCols);
     tmem_relinquish();
   }
   if (w.npages > 0) place_query<N>(s, p, w, warp, lane);
@@ -572,7 +596,7 @@ __global__ void __launch_bounds__(kThreads, 1) mla_partial_fp4_few_kernel(const 
       if (elect_one()) issue_mmas<N>(s, p, w, tmem);
       __syncwarp();
     } else if (warp >= 8) {
-      convert<N>(s, p, w, tmem, warp, lane);
+      convert<N>(s, p, w, (int)threadIdx.x - 256, lane);
     } else if (warp >= 4) {
       softmax<N>(s, p, w, tmem, warp, lane);
     }
@@ -591,7 +615,7 @@ __global__ void __launch_bounds__(kThreads, 1) mla_partial_fp4_few_kernel(const 
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 1) tmem_dealloc(tmem, 512);
+  if (warp == 1) tmem_dealloc(tmem, F::kCols);
   if (!p.counters) return;
   // Fused combine: the part whose arrival completes the request's count merges
   // its rows, every part being in memory by then.
