@@ -274,7 +274,6 @@ __device__ __forceinline__ void convert(typename Few<N>::Smem& s, const Fp4Param
         *reinterpret_cast<uint4*>(s.kr + o0) = r0;
         *reinterpret_cast<uint4*>(s.kr + o1) = plain8(rope.z, rope.w);
       }
-      fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&s.cfull[set][h]));
     }
@@ -308,6 +307,7 @@ __device__ __forceinline__ void issue_mmas(typename Few<N>::Smem& s, const Fp4Pa
     for (int h = 0; h < 2; ++h) {
       ok = ok && mbar_wait(smem_u32(&s.cfull[set][h]), (m >> 1) & 1, &s.abort_flag);
       if (!ok) return;
+      fence_proxy_async_smem();
       tc_fence_after();
 #pragma unroll
       for (int c = 4 * h; c < 4 * h + 4 + h; ++c)
@@ -342,6 +342,7 @@ __device__ __forceinline__ void issue_mmas(typename Few<N>::Smem& s, const Fp4Pa
     }
     ok = ok && mbar_wait(pbar, pph, &s.abort_flag);
     if (!ok) break;
+    fence_proxy_async_smem();
     tc_fence_after();
     const uint64_t v0 = vd + set * kSet, p0 = pd + set * (F::kQBox >> 4);
 #pragma unroll
@@ -484,7 +485,6 @@ __device__ __forceinline__ void softmax(typename Few<N>::Smem& s, const Fp4Param
       *reinterpret_cast<__half*>(dst + (n >> 3) * 1024 + (n & 7) * 128 +
                                  (((tok >> 3) ^ (n & 7)) << 4)) = __float2half_rn(e);
     }
-    fence_proxy_async_smem();
     tc_fence_before();
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(&s.pready[set]));

@@ -54,7 +54,8 @@ namespace {
 
 using namespace ptx;
 
-constexpr int kThreads = 512;        // 16 warps
+// Warps 0-3 control, 4-11 softmax (S) or rescale and epilogue (O), 12-15 convert.
+constexpr int kThreads = 512;
 constexpr int kCtas = 4;             // S pair (ranks 0,1) + O pair (ranks 2,3)
 constexpr int kBoxes = 9;            // operand ring: 8-KB boxes
 constexpr int kBoxesS = 3;           // S-CTA: a stage is three 64-dim chunks
@@ -63,7 +64,7 @@ constexpr int kBoxesO = 4;           // O-CTA: a stage is a page's four boxes
 constexpr int kStagesO = 2;
 constexpr int kStages = 3;           // barriers of the larger ring
 constexpr int kRaw = 3;              // raw page ring
-constexpr int kTilePages = 2;        // pages per S tile, one per S-CTA
+constexpr int kTilePages = 2;        // pages per S tile of the pair, one per S-CTA
 constexpr int kChunks = MLA_ROW_DIM / 64;                // 9 boxes per page
 static_assert(kBoxesS * kStagesS == kBoxes && kBoxesO * kStagesO <= kBoxes, "ring");
 constexpr int kNP = 4;               // P message slots (page index mod 4)
@@ -82,7 +83,7 @@ constexpr uint16_t kMaskO = 0xC;     // cluster ranks of the O pair
 // the control and converter warpgroups give some away so that the softmax can
 // hold 128 scores and their p.  One-way: nobody asks for registers back.  Of
 // five splits measured (16 x 5 x 96 x 100k tokens) 72/72/184 spills least and
-// runs 1140 us; 40/72/200 1175, 56/72/192 1176, 80/80/176 1243, 64/96/176 1260.
+// ran 1140 us; 40/72/200 1175, 56/72/192 1176, 80/80/176 1243, 64/96/176 1260.
 constexpr int kRegsLaunch = 128;
 constexpr int kRegsControl = 72;
 constexpr int kRegsConvert = 72;
@@ -309,6 +310,15 @@ __device__ __forceinline__ void convert_half(uint8_t* box, const uint4& c,
   *reinterpret_cast<uint4*>(box + box_chunk_offset(t, 4 * h + 3)) = scaled8(c.w, hi);
 }
 
+// Half a token's RoPE key (32 codes) into row t of its box.
+__device__ __forceinline__ void convert_rope_half(uint8_t* box, const uint4& a, const uint4& b,
+                                                  int t, int h) {
+  *reinterpret_cast<uint4*>(box + box_chunk_offset(t, 4 * h + 0)) = plain8(a.x, a.y);
+  *reinterpret_cast<uint4*>(box + box_chunk_offset(t, 4 * h + 1)) = plain8(a.z, a.w);
+  *reinterpret_cast<uint4*>(box + box_chunk_offset(t, 4 * h + 2)) = plain8(b.x, b.y);
+  *reinterpret_cast<uint4*>(box + box_chunk_offset(t, 4 * h + 3)) = plain8(b.z, b.w);
+}
+
 // S-CTA, warps 12..15: page 2j + rank of every tile j, chunk by chunk: two
 // threads per token, 32 dims each (their 16-byte reads of rows 352 bytes apart
 // and their swizzled 16-byte writes are both free of bank conflicts).  The
@@ -367,14 +377,10 @@ __device__ __forceinline__ void convert_s(Smem& s, const Fp4Params& p, const Wor
           } else {
             uint4 a = code[k], b = code[k + 1];
             if (bad) a = b = make_uint4(0, 0, 0, 0);
-            *reinterpret_cast<uint4*>(box + box_chunk_offset(t, 4 * h + 0)) = plain8(a.x, a.y);
-            *reinterpret_cast<uint4*>(box + box_chunk_offset(t, 4 * h + 1)) = plain8(a.z, a.w);
-            *reinterpret_cast<uint4*>(box + box_chunk_offset(t, 4 * h + 2)) = plain8(b.x, b.y);
-            *reinterpret_cast<uint4*>(box + box_chunk_offset(t, 4 * h + 3)) = plain8(b.z, b.w);
+            convert_rope_half(box, a, b, t, h);
           }
         }
         if (st + 1 < kStagesS) load_codes(st + 1);
-        fence_proxy_async_smem();
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&done[st]));
@@ -432,7 +438,6 @@ __device__ __forceinline__ void convert_o(Smem& s, const Fp4Params& p, const Wor
     for (int k = 0; k < kBoxesO; ++k)
       convert_half(s.ring[kBoxesO * stage + k], code[k],
                    ((k & 1 ? sn[k >> 1].y : sn[k >> 1].x) >> (16 * h)) & 0xFFFFu, t, h);
-    fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) {
       mbar_arrive(smem_u32(&done[stage]));
@@ -466,6 +471,7 @@ __device__ __forceinline__ void relay_made(Smem& s, const Fp4Params& p, int n, i
       signal_abort(s, p, rank);
       return;
     }
+    fence_proxy_async_smem();
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(
                      full0 + 8u * stage)
                  : "memory");
@@ -499,28 +505,27 @@ __device__ __forceinline__ void mma_s(Smem& s, const Fp4Params& p, const Work& w
     }
     tc_fence_after();
     const uint32_t d = tmem + kSCol0 + 128u * buf;
-#pragma unroll
+#pragma unroll 1
     for (int st = 0; st < kStagesS; ++st) {
       if (!mbar_wait(smem_u32(&s.full[st]), j & 1, &s.abort_flag)) {
         signal_abort(s, p, rank);
         return;
       }
+      fence_proxy_async_smem();
       tc_fence_after();
+      const uint64_t b = b0 + (uint64_t)(kBoxesS * st) * (kBoxBytes >> 4);
+      const uint32_t a = tmem + 32u * kBoxesS * st;
 #pragma unroll
-      for (int k = 0; k < kBoxesS; ++k) {
-        const int c = kBoxesS * st + k;
-        const uint64_t b = b0 + c * (kBoxBytes >> 4);
-        if (c < 8) {
-          mma_ts_pair(d, tmem + 32u * c + 0, b + 0, kIdescS, c > 0 ? 1u : 0u);
-          mma_ts_pair(d, tmem + 32u * c + 8, b + 2, kIdescS, 1u);
-          mma_ts_pair(d, tmem + 32u * c + 16, b + 4, kIdescS, 1u);
-          mma_ts_pair(d, tmem + 32u * c + 24, b + 6, kIdescS, 1u);
-        } else {
-          mma_ss_pair(d, qr + 0, b + 0, kIdescS, 1u);
-          mma_ss_pair(d, qr + 2, b + 2, kIdescS, 1u);
-          mma_ss_pair(d, qr + 4, b + 4, kIdescS, 1u);
-          mma_ss_pair(d, qr + 6, b + 6, kIdescS, 1u);
-        }
+      for (int k = 0; k < 4 * (kBoxesS - 1); ++k)
+        mma_ts_pair(d, a + 8u * k, b + (k >> 2) * (kBoxBytes >> 4) + 2 * (k & 3), kIdescS,
+                    (st | k) ? 1u : 0u);
+      const uint64_t b2 = b + (kBoxesS - 1) * (kBoxBytes >> 4);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (st < kStagesS - 1)
+          mma_ts_pair(d, a + 32u * (kBoxesS - 1) + 8u * k, b2 + 2 * k, kIdescS, 1u);
+        else
+          mma_ss_pair(d, qr + 2 * k, b2 + 2 * k, kIdescS, 1u);
       }
       mma_commit_pair(smem_u32(&s.empty[st]), kMaskS);
     }
@@ -542,6 +547,7 @@ __device__ __forceinline__ void ship_pages(Smem& s, const Fp4Params& p, const Wo
       signal_abort(s, p, rank);
       return;
     }
+    fence_proxy_async_smem();
     uint8_t* stg = s.pslot[k];
     // The receiver armed pfull[k] with the byte count itself.
     bulk_copy_to_peer(mapa(smem_u32(stg), orank), smem_u32(stg), kPMsgBytes,
@@ -575,9 +581,9 @@ __device__ __forceinline__ float place_query(Smem& s, uint32_t tmem, uint32_t la
       big = max(big, max(x[k] & 0x7FFFu, (x[k] >> 16) & 0x7FFFu));
   };
 #pragma unroll 1
-  for (int k = 0; k < 4; ++k)
+  for (int k = 4 * g; k < 4 * g + 4; ++k)
 #pragma unroll
-    for (int cc = 0; cc < 8; ++cc) take(chunk(query_box(s, 4 * g + k), cc));
+    for (int cc = 0; cc < 8; ++cc) take(chunk(query_box(s, k), cc));
   if (g == 0)
 #pragma unroll
     for (int cc = 0; cc < 8; ++cc) take(chunk(s.qrope, cc));
@@ -591,17 +597,17 @@ __device__ __forceinline__ float place_query(Smem& s, uint32_t tmem, uint32_t la
     return pack_f16(__uint_as_float(w << 16) * up, __uint_as_float(w & 0xFFFF0000u) * up);
   };
 #pragma unroll 1
-  for (int k = 0; k < 4; ++k) {
+  for (int k = 4 * g; k < 4 * g + 4; ++k) {
     uint32_t o[32];
 #pragma unroll
     for (int cc = 0; cc < 8; ++cc) {
-      const uint4 v = chunk(query_box(s, 4 * g + k), cc);
+      const uint4 v = chunk(query_box(s, k), cc);
       o[4 * cc] = conv(v.x);
       o[4 * cc + 1] = conv(v.y);
       o[4 * cc + 2] = conv(v.z);
       o[4 * cc + 3] = conv(v.w);
     }
-    tmem_st32(tmem + lane_base + 32u * (4 * g + k), o);
+    tmem_st32(tmem + lane_base + 32u * k, o);
   }
   if (g == 0) {
 #pragma unroll
@@ -619,6 +625,92 @@ __device__ __forceinline__ float place_query(Smem& s, uint32_t tmem, uint32_t la
 }
 
 // ------------------------------------------------------ S-CTA: softmax ----
+// What a softmax thread knows of its row, and the query's placement.
+struct SoftmaxRow {
+  int r;            // row of the group (TMEM lane)
+  bool in_range;
+  int64_t n, qrow;  // tokens the row sees; its row among the outputs
+  float pool, sc;   // g; the score scale in log2 units
+  bool ok;          // no wait has given up
+};
+__device__ __forceinline__ SoftmaxRow softmax_begin(Smem& s, const Fp4Params& p, const Work& w,
+                                                    uint32_t tmem, uint32_t rank, int warp,
+                                                    int lane) {
+  SoftmaxRow t;
+  const int quad = warp & 3;
+  t.r = quad * 32 + lane;
+  t.in_range = t.r < w.nrows;
+  const int rr = w.r_base + t.r;
+  const int i = t.in_range ? rr / p.H : 0;
+  t.n = 0;
+  if (t.in_range) {
+    t.n = p.kv_limit ? (int64_t)p.kv_limit[(int64_t)w.v * p.q_len + i]
+                     : w.L - p.q_len + 1 + i;
+    t.n = t.n > w.L ? w.L : (t.n < 0 ? 0 : t.n);
+  }
+  t.qrow = (int64_t)w.b * p.q_len * p.H + rr;
+  t.pool = p.g[0];
+  t.ok = mbar_wait(smem_u32(&s.qbar), 0, &s.abort_flag);
+  t.sc = p.scale_log2 * t.pool *
+         place_query(s, tmem, (uint32_t)(quad * 32) << 16, (warp - 4) >> 2, t.r, t.in_range);
+  if (warp == 4 && lane == 0) {
+    mbar_arrive(smem_u32(&s.qmoved));
+    arrive_leader(smem_u32(&s.qready), rank, 0);
+  }
+  return t;
+}
+
+// Final statistics: both warpgroups' sums, l in units of 2^m_own, in units of
+// the last reference; LSE_part, and g / l to the O-CTA.
+__device__ __forceinline__ void softmax_end(Smem& s, const Fp4Params& p, const Work& w,
+                                            const SoftmaxRow& t, float m_own, float l, bool ok,
+                                            uint32_t rank, int warp, int lane) {
+  const int g = (warp - 4) >> 2, r = t.r;
+  const uint32_t orank = rank + 2;  // the O-CTA of this row group
+  s.xch[0][g][r] = m_own;
+  s.xch[1][g][r] = l;
+  named_bar_sync(1, 256);
+  if (g == 0) {
+    const float m_ref = s.mref[r];
+    const auto part_sum = [&](int k) {  // a sum without a reference is 0 or NaN
+      const float m = s.xch[0][k][r], z = s.xch[1][k][r];
+      return m == -INFINITY ? z : z * ex2(m - m_ref);
+    };
+    const float lt = part_sum(0) + part_sum(1);
+    if (t.in_range) {
+      const int64_t rows = (int64_t)p.B * p.q_len * p.H;
+      const int64_t part = (int64_t)w.split * (p.V / p.B) + w.shard;
+      // no visible token: -inf; a NaN sum (a NaN score seen) stays NaN
+      p.LSE_part[part * rows + t.qrow] =
+          lt == 0.f ? -INFINITY : (m_ref + log2f(lt)) * 0.69314718055994531f;
+    }
+    s.fin[r] = lt == 0.f ? 0.f : t.pool / lt;
+    fence_proxy_async_smem();
+    named_bar_sync(2, 128);
+    if (warp == 4 && lane == 0 && !s.abort_flag)
+      bulk_copy_to_peer(mapa(smem_u32(s.fin), orank), smem_u32(s.fin), kRows * 4,
+                        mapa(smem_u32(&s.fin_full), orank));
+    // Before teardown: every P slot released by the O pair, so no remote
+    // arrive can land after this CTA exits.
+    for (int m = max(0, w.npages - kNP); m < w.npages && ok; ++m)
+      if (!mbar_wait(smem_u32(&s.pempty[m % kNP]), (m / kNP) & 1,
+                     &s.abort_flag))
+        ok = false;
+  }
+  if (!__all_sync(kFull, ok) && lane == 0) signal_abort(s, p, rank);
+}
+
+// The tile's reference from the last one's and its own maximum; alpha: the
+// factor of what O and l hold so far.
+__device__ __forceinline__ float next_reference(float m_old, float mt, float& alpha) {
+  alpha = 1.f;
+  if (!(mt > -INFINITY)) return m_old;
+  if (m_old == -INFINITY) return mt;  // first visible token of this row: O is zero
+  if (!(mt > m_old + kTau)) return m_old;
+  alpha = ex2(m_old - mt);
+  return mt;
+}
+
 // Warps 4..11 of each S-CTA: warpgroup g (warps 4-7, 8-11) takes the tiles j
 // with j % 2 = g, which are those of S buffer g, so a tile's chain of loads,
 // maximum, exponentials and stores has two tile periods.  Thread = query row r
@@ -628,44 +720,30 @@ __device__ __forceinline__ float place_query(Smem& s, uint32_t tmem, uint32_t la
 // 1347 us at 16 x 5 x 96 x 100k tokens).
 __device__ __forceinline__ void softmax(Smem& s, const Fp4Params& p, const Work& w,
                                         uint32_t tmem, uint32_t rank, int warp, int lane) {
-  const int g = (warp - 4) >> 2;
-  const int quad = warp & 3;
-  const int r = quad * 32 + lane;
+  const int g = (warp - 4) >> 2, quad = warp & 3;
   const uint32_t lane_base = (uint32_t)(quad * 32) << 16;
-  const bool row_ok = r < w.nrows;
-  const int rr = w.r_base + r;
-  const int i = row_ok ? rr / p.H : 0;
-  int64_t n = 0;
-  if (row_ok) {
-    n = p.kv_limit ? (int64_t)p.kv_limit[(int64_t)w.v * p.q_len + i]
-                   : w.L - p.q_len + 1 + i;
-    n = n > w.L ? w.L : (n < 0 ? 0 : n);
-  }
-  const int64_t qrow = (int64_t)w.b * p.q_len * p.H + rr;
-  const float pool = p.g[0];
-
-  bool ok = mbar_wait(smem_u32(&s.qbar), 0, &s.abort_flag);
-  const float sc = p.scale_log2 * pool * place_query(s, tmem, lane_base, g, r, row_ok);
-  if (warp == 4 && lane == 0) {
-    mbar_arrive(smem_u32(&s.qmoved));
-    arrive_leader(smem_u32(&s.qready), rank, 0);
-  }
+  const SoftmaxRow t = softmax_begin(s, p, w, tmem, rank, warp, lane);
+  const int r = t.r;
+  const int64_t n = t.n;
+  const float sc = t.sc;
+  bool ok = t.ok;
 
   // The running reference m of each row passes from tile to tile through
   // mref, from one warpgroup to the other; a warp of each holds the same 32
   // rows, so 64 threads meet per hand-over.
   float m_own = -INFINITY, l = 0.f;  // l: this warpgroup's sum, in units of 2^m_own
+  constexpr int kCols = kPage * kTilePages;
   const int ntiles = (w.npages + kTilePages - 1) / kTilePages;
   for (int j = g; j < ntiles; j += 2) {
     const int m0 = j * kTilePages;  // the tile's first page
     const bool two = m0 + 1 < w.npages;
-    uint32_t sv[128];
+    uint32_t sv[kCols];
     if (ok && !mbar_wait(smem_u32(&s.sfull[g]), (j >> 1) & 1, &s.abort_flag)) ok = false;
     tc_fence_after();
     if (__all_sync(kFull, ok)) {
       const uint32_t col = tmem + lane_base + kSCol0 + 128u * g;
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
+      for (int q = 0; q < kCols / 32; ++q)
         tmem_ld32(col + 32u * q, *reinterpret_cast<uint32_t(*)[32]>(&sv[32 * q]));
       tmem_wait_ld();
     }
@@ -677,38 +755,33 @@ __device__ __forceinline__ void softmax(Smem& s, const Fp4Params& p, const Work&
     const int64_t nv = n - (w.p0 + m0) * kPage;
     const int most = two ? 2 * kPage : kPage;
     const int nvis = nv <= 0 ? 0 : (nv >= most ? most : (int)nv);
-    if (!__all_sync(kFull, nvis == 2 * kPage)) {
+    if (!__all_sync(kFull, nvis == kCols)) {
 #pragma unroll
-      for (int c = 0; c < 128; ++c)
+      for (int c = 0; c < kCols; ++c)
         sv[c] = c < nvis ? sv[c] : __float_as_uint(-INFINITY);
     }
     // Row maximum of the raw scores; the scale is positive, so the maximum
     // of the scaled scores is the scaled maximum (rounding is monotone).
-    float mx[16];
+    constexpr int kM = kCols / 8;
+    float mx[kM];
 #pragma unroll
-    for (int c = 0; c < 16; ++c) {
-      const auto x = [&](int k) { return __uint_as_float(sv[c + 16 * k]); };
+    for (int c = 0; c < kM; ++c) {
+      const auto x = [&](int k) { return __uint_as_float(sv[c + kM * k]); };
       mx[c] = fmaxf(max3(x(0), x(1), x(2)), max3(max3(x(3), x(4), x(5)), x(6), x(7)));
     }
-    const float mt =
-        max3(max3(max3(mx[0], mx[1], mx[2]), max3(mx[3], mx[4], mx[5]), max3(mx[6], mx[7], mx[8])),
-             max3(mx[9], mx[10], mx[11]), max3(max3(mx[12], mx[13], mx[14]), mx[15], -INFINITY)) *
-        sc;
+#pragma unroll
+    for (int c = kM / 2; c > 0; c >>= 1)
+#pragma unroll
+      for (int k = 0; k < c; ++k) mx[k] = fmaxf(mx[k], mx[k + c]);
+    const float mt = mx[0] * sc;
     if (j > 0) named_bar_sync(4 + 2 * quad + g, 64);  // the last tile's reference is in
     const float m_old = j > 0 ? s.mref[r] : -INFINITY;
-    float m_ref = m_old, alpha = 1.f;
-    if (mt > -INFINITY) {
-      if (m_old == -INFINITY) {
-        m_ref = mt;  // first visible token of this row: O is still zero
-      } else if (mt > m_old + kTau) {
-        alpha = ex2(m_old - mt);
-        m_ref = mt;
-      }
-    }
+    float alpha;
+    const float m_ref = next_reference(m_old, mt, alpha);
     s.mref[r] = m_ref;
     if (j + 1 < ntiles) named_bar_arrive(4 + 2 * quad + (g ^ 1), 64);
     if (m_own != m_ref) {
-      l = m_own == -INFINITY ? 0.f : l * ex2(m_own - m_ref);
+      if (m_own != -INFINITY) l *= ex2(m_own - m_ref);
       m_own = m_ref;
     }
     // A row with nothing visible yet keeps m_ref = -inf: shift by 0 instead
@@ -717,7 +790,7 @@ __device__ __forceinline__ void softmax(Smem& s, const Fp4Params& p, const Work&
     const uint64_t sc2 = f2pack(sc, sc), nshift2 = f2pack(-shift, -shift);
     const bool any = __any_sync(kFull, alpha != 1.f);
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
+    for (int q = 0; q < kTilePages; ++q) {
       if (q == 1 && !two) break;
       // p = 2^(x * scale - m_ref): one packed FMA per pair of columns, the
       // row sum of the unrounded p in two packed accumulators.  P is shipped
@@ -759,44 +832,12 @@ __device__ __forceinline__ void softmax(Smem& s, const Fp4Params& p, const Work&
       reinterpret_cast<float*>(stg + kAlphaOff)[r] = q == 0 ? alpha : 1.f;
       if (lane == 0)
         reinterpret_cast<uint32_t*>(stg + kFlagOff)[quad] = q == 0 && any ? 1u : 0u;
-      fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&s.pmade[k]));
     }
   }
 
-  // Final statistics: both warpgroups' sums in units of the last reference.
-  s.xch[0][g][r] = m_own;
-  s.xch[1][g][r] = l;
-  named_bar_sync(1, 256);
-  if (g == 0) {
-    const float m_ref = s.mref[r];
-    const auto part_sum = [&](int k) {
-      const float m = s.xch[0][k][r];
-      return m == -INFINITY ? 0.f : s.xch[1][k][r] * ex2(m - m_ref);
-    };
-    const float lt = part_sum(0) + part_sum(1);
-    if (row_ok) {
-      const int64_t rows = (int64_t)p.B * p.q_len * p.H;
-      const int64_t part = (int64_t)w.split * (p.V / p.B) + w.shard;
-      // no visible token: -inf; a NaN sum (a NaN score seen) stays NaN
-      p.LSE_part[part * rows + qrow] =
-          lt == 0.f ? -INFINITY : (m_ref + log2f(lt)) * 0.69314718055994531f;
-    }
-    s.fin[r] = lt == 0.f ? 0.f : pool / lt;
-    fence_proxy_async_smem();
-    named_bar_sync(2, 128);
-    if (warp == 4 && lane == 0 && !s.abort_flag)
-      bulk_copy_to_peer(mapa(smem_u32(s.fin), rank + 2), smem_u32(s.fin), kRows * 4,
-                        mapa(smem_u32(&s.fin_full), rank + 2));
-    // Before teardown: every P slot released by the O pair, so no remote
-    // arrive can land after this CTA exits.
-    for (int m = max(0, w.npages - kNP); m < w.npages && ok; ++m)
-      if (!mbar_wait(smem_u32(&s.pempty[m % kNP]), (m / kNP) & 1,
-                     &s.abort_flag))
-        ok = false;
-  }
-  if (!__all_sync(kFull, ok) && lane == 0) signal_abort(s, p, rank);
+  softmax_end(s, p, w, t, m_own, l, ok, rank, warp, lane);
 }
 
 // --------------------------------------------------- O pair: MMA (rank 2) ----
@@ -850,6 +891,7 @@ __device__ __forceinline__ void mma_o(Smem& s, const Fp4Params& p,
       ok = false;
       break;
     }
+    fence_proxy_async_smem();
     tc_fence_after();
 #pragma unroll
     for (int n = 0; n < 2; ++n) {
@@ -1260,10 +1302,10 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1)
     } else if (warp == 2) {
       if (lane == 0 && !leads) relay_made(s, p, w.npages, kStagesO, rank, 2);
       __syncwarp();
-    } else if (warp >= kDequantWarp0) {
-      convert_o(s, p, w, rank, (warp - kDequantWarp0) * 32 + lane, lane);
     } else if (warp >= 4 && warp < 8) {
       correct_and_store(s, p, &o_map, w, tmem, rank, warp, lane);
+    } else if (warp >= kDequantWarp0) {
+      convert_o(s, p, w, rank, (warp - kDequantWarp0) * 32 + lane, lane);
     } else if (warp >= 8) {
       store_o_upper(s, p, &o_map, w, tmem, warp, lane);
     }
@@ -1353,11 +1395,10 @@ int launch_fp4(const DecodeArgs& a) {
               make_o_part_map(&o_map, p.O_part, o_rows) == MLA_OK;
   }
   cudaError_t e = cudaFuncSetAttribute(
-      mla_partial_fp4_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-      kSmemBytes);
+      mla_partial_fp4_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
   if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(fp4)");
-  mla_partial_fp4_kernel<<<(unsigned)(units * kCtas), kThreads, kSmemBytes,
-                          a.stream>>>(qn_map, qr_map, o_map, p);
+  mla_partial_fp4_kernel<<<(unsigned)(units * kCtas), kThreads, kSmemBytes, a.stream>>>(
+      qn_map, qr_map, o_map, p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_fail(e, "launch mla_partial_fp4_kernel");
   return MLA_OK;

@@ -226,6 +226,16 @@ def test_masked_tokens_hold_anything(simt):
         assert LSE2[1, 0, 0, 3:].isnan().all() and O2[1, 0, 0, 3:].isnan().all()
 
 
+@pytest.mark.parametrize("shape", [dict(B=1, q=1, H=9), dict(B=1, q=1, H=70), dict(B=1, q=2, H=96)])
+def test_rows_that_saw_nan_stay_nan(shape):
+    """A context that opens with NaN tokens and goes on finite: NaN throughout."""
+    case = Case(lens=[900], seed=15, **shape)
+    case.kv_host[case.r2t_host[0, :200], 256:288] = 0x7F
+    case.up()
+    O, LSE = case.run(1)
+    assert O.isnan().all() and LSE.isnan().all()
+
+
 @pytest.mark.parametrize("simt", [False, True])
 def test_bad_pages_read_as_zeros_and_lengths_are_clamped(simt):
     case = Case(2, 1, 20, [300, 200], seed=11)
