@@ -11,6 +11,7 @@ There is no CPU fallback: if the library is missing, loading it raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -43,6 +44,8 @@ class MlaError(RuntimeError):
 def library() -> ctypes.CDLL:
     """Load libmla_decode.so (built by ``build.build()``); raise if absent."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -114,18 +117,29 @@ def _check(rc: int) -> int:
 
 
 def _ptr(t: Optional[torch.Tensor]):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
+
+
+_HERE_ALREADY = contextlib.nullcontext()
+# torch.cuda.current_stream(), without the Stream object around the handle
+# (2.9 us of a call's host time on a Grace core, against 0.1 us)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _on(t: torch.Tensor):
     """Make the tensor's device current for a call: the library launches
     on (and looks up per-device state for) the current device."""
+    if t.is_cuda and t.device.index == torch.cuda.current_device():
+        return _HERE_ALREADY
     return torch.cuda.device(t.device)
 
 
 def _stream(stream: Optional[torch.cuda.Stream]):
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is not None:
+        return _raw_stream(torch.cuda.current_device())
+    return torch.cuda.current_stream().cuda_stream
 
 
 def _host_i32(x) -> "ctypes.Array":
@@ -400,32 +414,35 @@ def kv_write(rows, slots, kv, kv_scale=None, status=None, stream=None):
                                   _ptr(status), _stream(stream)))
 
 
-def _rows_arg(t: torch.Tensor, name: str, width: int, dtype=torch.bfloat16):
-    """A 2-D argument whose rows are contiguous (any row stride)."""
-    if t.dtype != dtype or t.dim() != 2 or t.shape[1] != width or t.stride(1) != 1:
-        raise ValueError(f"{name}: expected {dtype} rows of {width} contiguous values, "
-                         f"got {t.dtype} {tuple(t.shape)} with strides {t.stride()}")
-    return _ptr(t), t.stride(0) if t.shape[0] > 1 else max(t.stride(0), width)
+def _rows_arg(t: torch.Tensor, name: str, n: int, width: int, dtype=torch.bfloat16):
+    """A 2-D argument of n rows of `width` contiguous values (any row stride):
+    its address and row stride."""
+    shape, stride = t.shape, t.stride()
+    if t.dtype != dtype or shape != (n, width) or (stride[1] != 1 and width > 1):
+        raise ValueError(f"{name}: expected {dtype} [{n}, {width}] with contiguous rows, "
+                         f"got {t.dtype} {tuple(shape)} with strides {stride}")
+    return t.data_ptr(), stride[0] if n > 1 else max(stride[0], width)
 
 
 def _int32_arg(t: torch.Tensor, name: str, n: int):
     if t.dtype != torch.int32 or t.numel() != n or not t.is_contiguous():
         raise ValueError(f"{name}: expected {n} contiguous int32 values, got {t.dtype} "
                          f"{tuple(t.shape)}")
-    return _ptr(t)
+    return t.data_ptr()
 
 
 def _pool_args(kv: torch.Tensor, kv_scale: Optional[torch.Tensor]):
     kind = _kv_dtype(kv)
-    width = FP4_ROW_BYTES if kind == KV_FP4_E2M1 else ROW_DIM
-    if kv.dim() != 2 or kv.shape[1] != width or not kv.is_contiguous():
-        raise ValueError(f"kv: expected a contiguous [num_slots, {width}] pool, got "
-                         f"{tuple(kv.shape)} with strides {kv.stride()}")
-    if kv_scale is not None:
-        need = kv.shape[0] if kind == KV_FP8_E4M3 else 1
-        if kv_scale.dtype != torch.float32 or kv_scale.numel() < need or not kv_scale.is_contiguous():
-            raise ValueError(f"kv_scale: expected {need} contiguous float32 values")
-    return _ptr(kv), kind, _ptr(kv_scale), kv.shape[0]
+    slots, width = kv.shape if kv.dim() == 2 else (0, 0)
+    if width != (FP4_ROW_BYTES if kind == KV_FP4_E2M1 else ROW_DIM) or not kv.is_contiguous():
+        raise ValueError(f"kv: expected a contiguous [num_slots, {ROW_DIM}] (FP4: "
+                         f"{FP4_ROW_BYTES}) pool, got {tuple(kv.shape)} with strides {kv.stride()}")
+    if kv_scale is None:
+        return kv.data_ptr(), kind, None, slots
+    need = slots if kind == KV_FP8_E4M3 else 1
+    if kv_scale.dtype != torch.float32 or kv_scale.numel() < need or not kv_scale.is_contiguous():
+        raise ValueError(f"kv_scale: expected {need} contiguous float32 values")
+    return kv.data_ptr(), kind, kv_scale.data_ptr(), slots
 
 
 def kv_append(rows, slots, positions, cos_sin, kv, kv_scale=None, norm_weight=None,
@@ -441,32 +458,36 @@ def kv_append(rows, slots, positions, cos_sin, kv, kv_scale=None, norm_weight=No
     [1]); q_rope bf16 [n, H, 64] (strided) or None.  Returns q_out (allocated
     unless given; q_out=q_rope rotates in place), None without queries."""
     n = rows.shape[0]
-    row_ptr, row_stride = _rows_arg(rows, "rows", ROW_DIM)
+    row_ptr, row_stride = _rows_arg(rows, "rows", n, ROW_DIM)
     kv_ptr, kind, scale_ptr, num_slots = _pool_args(kv, kv_scale)
-    if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2 or cos_sin.shape[1] != ROPE_DIM \
-            or not cos_sin.is_contiguous():
+    max_pos, pairs = cos_sin.shape if cos_sin.dim() == 2 else (0, 0)
+    if cos_sin.dtype != torch.float32 or pairs != ROPE_DIM or not cos_sin.is_contiguous():
         raise ValueError("cos_sin: expected contiguous float32 [max_pos, 64]")
-    if norm_weight is not None and (norm_weight.dtype != torch.bfloat16 or norm_weight.numel() != NOPE_DIM
-                                    or not norm_weight.is_contiguous()):
-        raise ValueError("norm_weight: expected 512 contiguous bfloat16 values")
-    H, q_args = 0, [None, 0, 0, None, 0, 0]
+    weight_ptr = None
+    if norm_weight is not None:
+        if norm_weight.dtype != torch.bfloat16 or norm_weight.numel() != NOPE_DIM \
+                or not norm_weight.is_contiguous():
+            raise ValueError("norm_weight: expected 512 contiguous bfloat16 values")
+        weight_ptr = norm_weight.data_ptr()
+    H, q_args = 0, (None, 0, 0, None, 0, 0)
     if q_rope is not None:
         if q_out is None:
             q_out = torch.empty(q_rope.shape, dtype=torch.bfloat16, device=q_rope.device)
-        for t, name in ((q_rope, "q_rope"), (q_out, "q_out")):
-            if t.dtype != torch.bfloat16 or t.dim() != 3 or t.shape[0] != n or \
-                    t.shape[2] != ROPE_DIM or t.shape != q_rope.shape or t.stride(2) != 1:
-                raise ValueError(f"{name}: expected bfloat16 [{n}, H, 64] with contiguous "
-                                 f"head rows, got {t.dtype} {tuple(t.shape)} {t.stride()}")
-        H = q_rope.shape[1]
-        q_args = [_ptr(q_rope), q_rope.stride(0), q_rope.stride(1),
-                  _ptr(q_out), q_out.stride(0), q_out.stride(1)]
+        shape, qs, os_ = q_rope.shape, q_rope.stride(), q_out.stride()
+        if len(shape) != 3 or shape[0] != n or shape[2] != ROPE_DIM or q_out.shape != shape or \
+                q_rope.dtype != torch.bfloat16 or q_out.dtype != torch.bfloat16 or \
+                qs[2] != 1 or os_[2] != 1:
+            raise ValueError(f"q_rope, q_out: expected bfloat16 [{n}, H, 64] with contiguous head "
+                             f"rows, got {q_rope.dtype} {tuple(shape)} {qs} and {q_out.dtype} "
+                             f"{tuple(q_out.shape)} {os_}")
+        H = shape[1]
+        q_args = (q_rope.data_ptr(), qs[0], qs[1], q_out.data_ptr(), os_[0], os_[1])
+    slots_ptr, pos_ptr = _int32_arg(slots, "slots", n), _int32_arg(positions, "positions", n)
     with _on(rows):
         _check(library().mla_kv_append(
-            row_ptr, row_stride, n, _ptr(norm_weight), float(eps),
-            _int32_arg(slots, "slots", n), _int32_arg(positions, "positions", n),
-            _ptr(cos_sin), cos_sin.shape[0], int(interleaved), kv_ptr, kind, scale_ptr,
-            num_slots, *q_args, H, _ptr(status), _stream(stream)))
+            row_ptr, row_stride, n, weight_ptr, eps, slots_ptr, pos_ptr, cos_sin.data_ptr(),
+            max_pos, 1 if interleaved else 0, kv_ptr, kind, scale_ptr, num_slots, *q_args, H,
+            _ptr(status), _stream(stream)))
     return q_out if q_rope is not None else None
 
 
@@ -477,9 +498,7 @@ def kv_read(kv, slots, kv_scale=None, out=None, status=None, stream=None):
     kv_ptr, kind, scale_ptr, num_slots = _pool_args(kv, kv_scale)
     if out is None:
         out = torch.empty((n, ROW_DIM), dtype=torch.bfloat16, device=kv.device)
-    out_ptr, out_stride = _rows_arg(out, "out", ROW_DIM)
-    if out.shape[0] != n:
-        raise ValueError(f"out: expected {n} rows, got {out.shape[0]}")
+    out_ptr, out_stride = _rows_arg(out, "out", n, ROW_DIM)
     with _on(kv):
         _check(library().mla_kv_read(kv_ptr, kind, scale_ptr, num_slots,
                                      _int32_arg(slots, "slots", n), n, out_ptr,
@@ -512,27 +531,21 @@ def add_rms_norm(x, weight, residual=None, eps: float = 1e-6, out=None, out8=Non
         raise ValueError("residual_out without a residual")
     if weight.dtype != torch.bfloat16 or weight.numel() != d or not weight.is_contiguous():
         raise ValueError(f"weight: expected {d} contiguous bfloat16 values")
-    args = []
-    for t, name in ((x, "x"), (residual, "residual"), (residual_out, "residual_out")):
-        args += [None, 0] if t is None else list(_rows_arg(t, name, d))
-        if t is not None and t.shape[0] != n:
-            raise ValueError(f"{name}: expected {n} rows, got {t.shape[0]}")
-    outs = []
-    if out is not None and out.shape[0] != n:
-        raise ValueError(f"out: expected {n} rows, got {out.shape[0]}")
-    outs += [None, 0] if out is None else list(_rows_arg(out, "out", d))
-    if out8 is None:
-        outs += [None, 0, None, 0]
-    else:
+    none = (None, 0)
+    x_args = _rows_arg(x, "x", n, d)
+    res_args = none if residual is None else _rows_arg(residual, "residual", n, d)
+    ro_args = none if residual is None else _rows_arg(residual_out, "residual_out", n, d)
+    out_args = none if out is None else _rows_arg(out, "out", n, d)
+    out8_args = sc_args = none
+    if out8 is not None:
         if out8.dtype not in (torch.uint8, torch.float8_e4m3fn):
             raise ValueError(f"out8: expected float8_e4m3fn or uint8, got {out8.dtype}")
-        if out8.shape[0] != n or scales.shape[0] != n:
-            raise ValueError(f"out8, scales: expected {n} rows")
-        outs += list(_rows_arg(out8, "out8", d, out8.dtype))
-        outs += list(_rows_arg(scales, "scales", d // group if group else 1, torch.float32))
+        out8_args = _rows_arg(out8, "out8", n, d, out8.dtype)
+        sc_args = _rows_arg(scales, "scales", n, d // group if group else 1, torch.float32)
     with _on(x):
-        _check(library().mla_add_rms_norm(*args, _ptr(weight), float(eps), n, d, *outs,
-                                          group, _stream(stream)))
+        _check(library().mla_add_rms_norm(
+            *x_args, *res_args, *ro_args, weight.data_ptr(), eps, n, d, *out_args, *out8_args,
+            *sc_args, group, _stream(stream)))
     return out, out8, scales, residual_out
 
 
@@ -608,8 +621,7 @@ def debug_quotients(counters, stream=None):
     device, zeroed: bit mismatches, code mismatches are added."""
     with _on(counters):
         _check(library().mla_debug_quotients(
-            ctypes.c_void_p(counters.data_ptr()),
-            ctypes.c_void_p(counters.data_ptr() + 8), _stream(stream)))
+            counters.data_ptr(), counters.data_ptr() + 8, _stream(stream)))
 
 
 def decode(batch, num_splits: Optional[int] = None, simt: bool = False,
