@@ -77,4 +77,25 @@ __device__ __forceinline__ float2 h2_to_f32(uint32_t h) {
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
+// Quotients by one divisor b > 0: a / b from y = RN(1 / b) and one Markstein
+// correction (P. Markstein, "Computation of elementary functions on the IBM
+// RISC System/6000 processor", IBM J. Res. Dev. 34(1), 1990): three
+// instructions instead of a full division, off by at most one unit in the last
+// place and exact for quotients of few bits, so a code's tie stays a tie.
+// Divisors whose reciprocal leaves the normal range divide directly; b = 0
+// gives 0.
+struct Divisor {
+  float b, y;
+  bool direct;
+  __device__ __forceinline__ explicit Divisor(float d)
+      : b(d), y(0.f), direct(!(d >= 0x1p-90f && d <= 0x1p+120f)) {
+    if (!direct) y = __frcp_rn(d);
+  }
+  __device__ __forceinline__ float operator()(float a) const {
+    if (direct) return b == 0.f ? 0.f : __fdiv_rn(a, b);
+    const float q = __fmul_rn(a, y);
+    return __fmaf_rn(__fmaf_rn(-q, b, a), y, q);
+  }
+};
+
 }  // namespace mla

@@ -4,7 +4,8 @@
 //   y = h * rsqrt(mean(h^2) + eps) * w
 //   out = bf16(y);   out8 = E4M3(y / s), s = max|y| / 448 over the row or over
 //   each group of `group` values
-// in fp32 throughout, each output rounded once.
+// in fp32 throughout, each output rounded once.  y / s is y times the rounded
+// reciprocal of s.
 //
 // A stream bound by HBM (2 + 2 bytes read and 2 + 1 written per value): a
 // block per row, the row's h in registers between its one read and the
@@ -12,7 +13,13 @@
 // 8 * (k * threads + thread), so every warp access is contiguous and a group
 // of 32, 64 or 128 values lies in 4, 8 or 16 neighbouring lanes: its maximum
 // takes 2 to 4 shuffles.  The row's sum (and, with one scale per row, its
-// maximum) crosses the warps through shared memory once.
+// maximum) crosses the warps through shared memory once.  Few rows take a
+// thread per vector, the shortest chain; many rows of 513 to 1024 vectors four
+// vectors a thread and four blocks per SM, whose phases overlap.  Measured on a
+// GB300 at 16383 x 7168, groups of 128 (822 MB): 150 us, 5.5 TB/s, 82% of the
+// copy rate (three blocks 173, five 172, two vectors a thread 185, one 178; a
+// resident grid that loads the next row ahead, two blocks of 125 registers,
+// 249); 80 x 7168: 3.0 us.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -51,157 +58,204 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return *reinterpret_cast<uint32_t*>(&h);
 }
 
-// Eight values from column c0 on; columns past d read as 0.
+// Pairs of fp32 values, two lanes per instruction: at 16 instructions a value
+// the arithmetic, not HBM, bounded this kernel (70% of the issue slots at 16383
+// x 7168).
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t x;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(a), "f"(b));
+  return x;
+}
+__device__ __forceinline__ float2 both(uint64_t x) {
+  float2 v;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(v.x), "=f"(v.y) : "l"(x));
+  return v;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t widen(uint32_t w) {  // two bf16
+  return pair(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+__device__ __forceinline__ uint32_t word(const uint4& u, int k) {
+  return k == 0 ? u.x : k == 1 ? u.y : k == 2 ? u.z : u.w;
+}
+
+// Eight bf16 values from column c0 on as packed pairs; columns past d read as 0.
 template <bool VEC>
-__device__ __forceinline__ void load8(const __nv_bfloat16* row, int c0, int d,
-                                      float (&v)[8]) {
-  if (VEC) {
-    const uint4 u = *reinterpret_cast<const uint4*>(row + c0);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+__device__ __forceinline__ uint4 load8(const __nv_bfloat16* row, int c0, int d) {
+  if (VEC) return *reinterpret_cast<const uint4*>(row + c0);
+  const uint16_t* r = reinterpret_cast<const uint16_t*>(row);
+  uint32_t w[4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      v[2 * k] = __uint_as_float(w[k] << 16);
-      v[2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
-    }
-  } else {
-#pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = c0 + k < d ? __bfloat162float(row[c0 + k]) : 0.f;
-  }
+  for (int k = 0; k < 4; ++k)
+    w[k] = (c0 + 2 * k < d ? r[c0 + 2 * k] : 0u) |
+           ((c0 + 2 * k + 1 < d ? r[c0 + 2 * k + 1] : 0u) << 16);
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 template <bool VEC>
 __device__ __forceinline__ void store8(__nv_bfloat16* row, int c0, int d,
-                                       const float (&v)[8]) {
+                                       const uint64_t (&v)[4]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) w[k] = pack_bf16(both(v[k]).x, both(v[k]).y);
   if (VEC) {
-    *reinterpret_cast<uint4*>(row + c0) =
-        make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]),
-                   pack_bf16(v[6], v[7]));
+    *reinterpret_cast<uint4*>(row + c0) = make_uint4(w[0], w[1], w[2], w[3]);
   } else {
+    uint16_t* r = reinterpret_cast<uint16_t*>(row);
 #pragma unroll
     for (int k = 0; k < 8; ++k)
-      if (c0 + k < d) row[c0 + k] = __float2bfloat16_rn(v[k]);
+      if (c0 + k < d) r[c0 + k] = (uint16_t)(w[k / 2] >> (16 * (k & 1)));
   }
+}
+
+// Sum (MAX: maximum) of one value per thread over the block, in every thread.
+template <bool MAX>
+__device__ __forceinline__ float block_reduce(float v, float* part) {
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, warps = blockDim.x / 32;
+  const auto reduce = [&](float a) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      const float b = __shfl_xor_sync(kAll, a, o);
+      a = MAX ? fmaxf(a, b) : a + b;
+    }
+    return a;
+  };
+  v = reduce(v);
+  if (lane == 0) part[warp] = v;
+  __syncthreads();
+  return reduce(lane < warps ? part[lane] : 0.f);
 }
 
 // VEC: d and every stride are multiples of 8 and every pointer is aligned to
 // its vector, so whole vectors are in range or out of it.
-template <int V, bool VEC>
-__global__ void __launch_bounds__(kMaxThreads) mla_norm_kernel(const NormParams p) {
-  __shared__ float part[2][32];
+template <int V, bool VEC, int T>
+__global__ void __launch_bounds__(T, T == 256 && V == 4 ? 4 : 1) mla_norm_kernel(const NormParams p) {
+  __shared__ float part[3][32];
   const int64_t r = blockIdx.x;
-  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, warps = blockDim.x / 32;
-  float h[V][8];
-  // The mean is summed, not the sum divided: a row overflows only where its
-  // mean square does.
-  const float inv_d = 1.0f / (float)p.d;
-  float ss = 0.f;
+  const auto col = [&](int k) { return 8 * (k * (int)blockDim.x + (int)threadIdx.x); };
+  uint4 x[V], q[V], w[V];  // all loads of the row in flight together
 #pragma unroll
   for (int k = 0; k < V; ++k) {
-    const int c0 = 8 * (k * (int)blockDim.x + (int)threadIdx.x);
-    if (c0 < p.d) {
-      load8<VEC>(p.x + r * p.x_stride, c0, p.d, h[k]);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) h[k][e] = 0.f;
+    x[k] = q[k] = w[k] = make_uint4(0, 0, 0, 0);
+    if (col(k) < p.d) {
+      x[k] = load8<VEC>(p.x + r * p.x_stride, col(k), p.d);
+      if (p.res) q[k] = load8<VEC>(p.res + r * p.res_stride, col(k), p.d);
+      w[k] = load8<VEC>(p.w, col(k), p.d);
     }
   }
-  if (p.res) {
-#pragma unroll
-    for (int k = 0; k < V; ++k) {
-      const int c0 = 8 * (k * (int)blockDim.x + (int)threadIdx.x);
-      if (c0 < p.d) {
-        float q[8];
-        load8<VEC>(p.res + r * p.res_stride, c0, p.d, q);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) h[k][e] += q[e];
-      }
-    }
-  }
+  uint64_t h[V][4], acc = pair(0.f, 0.f);
 #pragma unroll
   for (int k = 0; k < V; ++k)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) ss = fmaf(h[k][e], h[k][e] * inv_d, ss);
+    for (int e = 0; e < 4; ++e) {
+      h[k][e] = add2(widen(word(x[k], e)), widen(word(q[k], e)));
+      acc = fma2(h[k][e], h[k][e], acc);
+    }
+  const float inv_d = 1.0f / (float)p.d;
+  float mean = block_reduce<false>(both(acc).x + both(acc).y, part[0]) * inv_d;
+  if (!(mean < INFINITY)) {
+    // The squares' sum overflowed (or holds a NaN): sum the mean, which only
+    // overflows where the mean square itself does.
+    float ss = 0.f;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(kAll, ss, o);
-  if (lane == 0) part[0][warp] = ss;
-  __syncthreads();
+    for (int k = 0; k < V; ++k)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float2 v = both(h[k][e]);
+        ss = fmaf(v.y, v.y * inv_d, fmaf(v.x, v.x * inv_d, ss));
+      }
+    mean = block_reduce<false>(ss, part[1]);
+  }
   // every row element has been read: the residual may be updated in place
   if (p.res_out) {
 #pragma unroll
-    for (int k = 0; k < V; ++k) {
-      const int c0 = 8 * (k * (int)blockDim.x + (int)threadIdx.x);
-      if (c0 < p.d) store8<VEC>(p.res_out + r * p.res_out_stride, c0, p.d, h[k]);
-    }
+    for (int k = 0; k < V; ++k)
+      if (col(k) < p.d) store8<VEC>(p.res_out + r * p.res_out_stride, col(k), p.d, h[k]);
   }
-  ss = lane < warps ? part[0][lane] : 0.f;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(kAll, ss, o);
-  const float rs = 1.0f / sqrtf(ss + p.eps);
-  float rowmax = 0.f;
+  const float rs = 1.0f / sqrtf(mean + p.eps);
+  const uint64_t rs2 = pair(rs, rs);
+  float amax[V], rowmax = 0.f;
 #pragma unroll
   for (int k = 0; k < V; ++k) {
-    const int c0 = 8 * (k * (int)blockDim.x + (int)threadIdx.x);
-    if (c0 < p.d) {
-      float w[8];
-      load8<VEC>(p.w, c0, p.d, w);
+    amax[k] = 0.f;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        h[k][e] = h[k][e] * rs * w[e];
-        rowmax = fmaxf(rowmax, fabsf(h[k][e]));
-      }
-      if (p.out) store8<VEC>(p.out + r * p.out_stride, c0, p.d, h[k]);
+    for (int e = 0; e < 4; ++e) {
+      h[k][e] = mul2(h[k][e], mul2(rs2, widen(word(w[k], e))));
+      amax[k] = fmaxf(amax[k], fmaxf(fabsf(both(h[k][e]).x), fabsf(both(h[k][e]).y)));
     }
+    if (p.out && col(k) < p.d) store8<VEC>(p.out + r * p.out_stride, col(k), p.d, h[k]);
+    rowmax = fmaxf(rowmax, amax[k]);
   }
   if (!p.out8) return;
-  if (p.group == 0) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-      rowmax = fmaxf(rowmax, __shfl_xor_sync(kAll, rowmax, o));
-    if (lane == 0) part[1][warp] = rowmax;
-    __syncthreads();
-    rowmax = lane < warps ? part[1][lane] : 0.f;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-      rowmax = fmaxf(rowmax, __shfl_xor_sync(kAll, rowmax, o));
-  }
+  if (p.group == 0) rowmax = block_reduce<true>(rowmax, part[2]);
 #pragma unroll
   for (int k = 0; k < V; ++k) {
-    const int c0 = 8 * (k * (int)blockDim.x + (int)threadIdx.x);
-    float amax = rowmax;
-    if (p.group) {
-      amax = 0.f;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(h[k][e]));
+    if (p.group == 0) {
+      amax[k] = rowmax;
+    } else {
       for (int o = p.group / 16; o > 0; o >>= 1)
-        amax = fmaxf(amax, __shfl_xor_sync(kAll, amax, o));
+        amax[k] = fmaxf(amax[k], __shfl_xor_sync(kAll, amax[k], o));
     }
+    const int c0 = col(k);
     if (c0 >= p.d) continue;
-    const float s = __fdiv_rn(amax, 448.0f);
+    const float s = __fdiv_rn(amax[k], 448.0f);
     if (p.group ? c0 % p.group == 0 : c0 == 0)
       p.scales[r * p.scales_stride + (p.group ? c0 / p.group : 0)] = s;
-    uint32_t q[4];
+    uint32_t c8[4];
+    if (s > 0x1p-90f) {
+      const float inv = __frcp_rn(s);
+      const uint64_t inv2 = pair(inv, inv);
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      q[e] = s == 0.f ? 0u : e4m3_pair(__fdiv_rn(h[k][2 * e], s), __fdiv_rn(h[k][2 * e + 1], s));
+      for (int e = 0; e < 4; ++e) {
+        const float2 v = both(mul2(h[k][e], inv2));
+        c8[e] = e4m3_pair(v.x, v.y);
+      }
+    } else {  // the reciprocal leaves the range (or the group is zero)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float2 v = both(h[k][e]);
+        c8[e] = s == 0.f ? 0u : e4m3_pair(__fdiv_rn(v.x, s), __fdiv_rn(v.y, s));
+      }
+    }
     uint8_t* dst = p.out8 + r * p.out8_stride + c0;
     if (VEC) {
-      *reinterpret_cast<uint2*>(dst) = make_uint2(q[0] | (q[1] << 16), q[2] | (q[3] << 16));
+      *reinterpret_cast<uint2*>(dst) = make_uint2(c8[0] | (c8[1] << 16), c8[2] | (c8[3] << 16));
     } else {
 #pragma unroll
       for (int e = 0; e < 8; ++e)
-        if (c0 + e < p.d) dst[e] = (uint8_t)(q[e / 2] >> (8 * (e & 1)));
+        if (c0 + e < p.d) dst[e] = (uint8_t)(c8[e / 2] >> (8 * (e & 1)));
     }
   }
 }
 
 template <bool VEC>
-void launch(const NormParams& p, int64_t n, int vec, int threads, cudaStream_t st) {
+void launch(const NormParams& p, int64_t n, int sms, cudaStream_t st) {
   const unsigned grid = (unsigned)n;
-  if (vec == 1)
-    mla_norm_kernel<1, VEC><<<grid, threads, 0, st>>>(p);
-  else if (vec == 2)
-    mla_norm_kernel<2, VEC><<<grid, threads, 0, st>>>(p);
+  const int vectors = (p.d + 7) / 8;
+  const auto threads = [&](int v) { return ((vectors + v - 1) / v + 31) / 32 * 32; };
+  if (n > 2 * sms && vectors > 512 && vectors <= 1024)
+    mla_norm_kernel<4, VEC, 256><<<grid, threads(4), 0, st>>>(p);
+  else if (n > 2 * sms && vectors > 256 && vectors <= 512)
+    mla_norm_kernel<2, VEC, 256><<<grid, threads(2), 0, st>>>(p);
+  else if (vectors <= 1024)
+    mla_norm_kernel<1, VEC, 1024><<<grid, threads(1), 0, st>>>(p);
+  else if (vectors <= 2048)
+    mla_norm_kernel<2, VEC, 1024><<<grid, threads(2), 0, st>>>(p);
   else
-    mla_norm_kernel<4, VEC><<<grid, threads, 0, st>>>(p);
+    mla_norm_kernel<4, VEC, 1024><<<grid, threads(4), 0, st>>>(p);
 }
 
 }  // namespace
@@ -271,15 +325,16 @@ extern "C" int mla_add_rms_norm(const void* x, int64_t x_stride, const void* res
                      aligned(residual, 16) && aligned(residual_out, 16))) &&
       (!out || (out_stride % 8 == 0 && aligned(out, 16))) &&
       (!out8 || (out8_stride % 8 == 0 && aligned(out8, 8)));
-  const int vectors = (d + 7) / 8;
-  const int vec = vectors <= kMaxThreads ? 1 : vectors <= 2 * kMaxThreads ? 2 : 4;
-  const int threads =
-      std::min(kMaxThreads, ((vectors + vec - 1) / vec + 31) / 32 * 32);
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess)
+    e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return cuda_fail(e, "mla_add_rms_norm: device query");
   if (vec8)
-    launch<true>(p, n, vec, threads, (cudaStream_t)stream);
+    launch<true>(p, n, sms, (cudaStream_t)stream);
   else
-    launch<false>(p, n, vec, threads, (cudaStream_t)stream);
-  const cudaError_t e = cudaGetLastError();
+    launch<false>(p, n, sms, (cudaStream_t)stream);
+  e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_fail(e, "launch mla_norm_kernel");
   return MLA_OK;
 }
