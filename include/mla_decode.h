@@ -173,8 +173,10 @@ int mla_plan_ex(int V, int q_len, int H, int rows_per_unit,
  * measured times on GB300, B = 1..24 requests x 100k / 400k tokens: a work
  * unit costs about that many pages beyond its own).
  *   B, num_shards  requests and context shards (V = B * num_shards);
- *   kv_dtype       MLA_KV_BF16, MLA_KV_FP8_E4M3 or MLA_KV_FP4_E2M1 (planned
- *                  as BF16) (else MLA_ERR_INVALID_ARG)
+ *   kv_dtype       MLA_KV_BF16, MLA_KV_FP8_E4M3 or MLA_KV_FP4_E2M1 (else
+ *                  MLA_ERR_INVALID_ARG); FP4: 256 rows per 4-CTA cluster and
+ *                  c0 = 28, or with q_len * H <= 32 one CTA per (request, part):
+ *                  slots = the SM count (or num_sms), c0 = 4
  *   seq_lens_host  host int32 [num_shards * B] (shard-local lengths).
  */
 int mla_plan(int B, int q_len, int H, int num_shards, mla_kv_dtype kv_dtype,

@@ -106,8 +106,15 @@ constexpr double kPlanUnitCostBf16 = 16.0;
 constexpr double kPlanUnitCostFp8 = 32.0;
 constexpr double kPlanSplitCost = 1.0;
 
-// The few-row FP4 kernel's unit (one CTA; a page costs it about 0.9 us too).
-constexpr double kPlanUnitCostFew = 8.0;
+// FP4: a page costs a cluster 0.76 us and a unit about 10 us beyond its pages,
+// with the idle slots of a last wave on top: of 8, 16, 24 and 32, the last two
+// are fastest everywhere (32 requests x 96 heads x 20k tokens 271, 268, 246,
+// 247 us; 40 x 5 x 96, 100 to 20k tokens 199, 199, 158, 158; 24 ragged x 5 x 96
+// 644, 610, 610, 610).  The few-row kernel's unit, one CTA, is short: of 2, 4, 8
+// and 14, 32 requests x 16 heads, 2k to 60k tokens take 94, 96, 99, 107 us, x 32
+// heads 122, 119, 119, 127.
+constexpr double kPlanUnitCostFp4 = 28.0;
+constexpr double kPlanUnitCostFew = 4.0;
 
 // Whether mla_fp4_few.cu serves the launch: one CTA per (request, part).
 static bool few_rows(mla_kv_dtype kv_dtype, int q_len, int H) {
@@ -115,8 +122,10 @@ static bool few_rows(mla_kv_dtype kv_dtype, int q_len, int H) {
 }
 
 static double plan_unit_cost(mla_kv_dtype kv_dtype, bool few) {
-  return few ? kPlanUnitCostFew
-             : kv_dtype == MLA_KV_FP8_E4M3 ? kPlanUnitCostFp8 : kPlanUnitCostBf16;
+  if (few) return kPlanUnitCostFew;
+  return kv_dtype == MLA_KV_FP4_E2M1   ? kPlanUnitCostFp4
+         : kv_dtype == MLA_KV_FP8_E4M3 ? kPlanUnitCostFp8
+                                       : kPlanUnitCostBf16;
 }
 
 // The planners score each candidate plan by its list-scheduling makespan
