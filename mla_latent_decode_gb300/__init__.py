@@ -291,12 +291,31 @@ def _kv_dtype(kv: torch.Tensor) -> int:
     raise TypeError(f"kv dtype {kv.dtype}: expected bfloat16 or uint8 (E4M3, FP4)")
 
 
+def _check_fp4(q_nope, q_rope, kv, kv_scale, req_to_token, seq_lens) -> None:
+    """The layouts the FP4 decode reads (its pool and its queries are told from
+    the other formats' by shape, so a wrong one is refused here)."""
+    B, q_len, H, _ = q_nope.shape
+    for t, name, width in ((q_nope, "q_nope", NOPE_DIM), (q_rope, "q_rope", ROPE_DIM)):
+        if t.dtype != torch.bfloat16 or t.shape != (B, q_len, H, width) or not t.is_contiguous():
+            raise ValueError(f"{name}: expected contiguous bfloat16 {[B, q_len, H, width]}, got "
+                             f"{t.dtype} {tuple(t.shape)} with strides {t.stride()}")
+    if kv.dim() != 2 or not kv.is_contiguous():
+        raise ValueError(f"kv: expected a contiguous [num_slots, {FP4_ROW_BYTES}] pool")
+    if kv_scale is None or kv_scale.dtype != torch.float32 or kv_scale.numel() < 1:
+        raise ValueError("kv_scale: expected one float32 value, the pool's factor")
+    if req_to_token.dtype != torch.int32 or req_to_token.stride(1) != 1 or \
+            seq_lens.dtype != torch.int32 or not seq_lens.is_contiguous():
+        raise ValueError("req_to_token, seq_lens: expected int32 with contiguous rows")
+
+
 def decode_partial(q_nope, q_rope, kv, kv_scale, req_to_token, seq_lens,
                    kv_limit, num_splits: int, sm_scale: float,
                    num_shards: int = 1, O_part=None, LSE_part=None,
                    status=None, simt: bool = False, stream=None,
                    split_pages=None, work=None, part_dtype=None):
     """Partial (O, LSE) per split and shard; see mla_decode_partial.
+    `kv`: bf16 [slots, 576], uint8 [slots, 576] (E4M3, kv_scale fp32 [slots]) or
+    uint8 [slots, 352] (FP4, kv_scale fp32 [1]);
     `split_pages`: device int32 [num_shards*B, num_splits+1] or None;
     `work`: device int32 unit ids in launch order (plan_sched) or None
     (tensor-core path only).  A bf16 O_part (given, or part_dtype=
@@ -308,6 +327,9 @@ def decode_partial(q_nope, q_rope, kv, kv_scale, req_to_token, seq_lens,
     """
     B, q_len, H, _ = q_nope.shape
     dev = q_nope.device
+    kind = _kv_dtype(kv)
+    if kind == KV_FP4_E2M1:
+        _check_fp4(q_nope, q_rope, kv, kv_scale, req_to_token, seq_lens)
     if O_part is None:
         O_part = torch.empty((num_splits, num_shards, B, q_len, H, VALUE_DIM),
                              dtype=part_dtype or torch.float32, device=dev)
@@ -316,7 +338,7 @@ def decode_partial(q_nope, q_rope, kv, kv_scale, req_to_token, seq_lens,
         LSE_part = torch.empty((num_splits, num_shards, B, q_len, H),
                                dtype=torch.float32, device=dev)
     args = (_ptr(q_nope), _ptr(q_rope), _ptr(kv), _ptr(kv_scale),
-            _kv_dtype(kv), kv.shape[0], _ptr(req_to_token),
+            kind, kv.shape[0], _ptr(req_to_token),
             req_to_token.stride(0), _ptr(seq_lens), _ptr(kv_limit), B, q_len,
             H, num_shards, PAGE_SIZE, float(sm_scale), num_splits,
             _ptr(split_pages))
@@ -352,6 +374,9 @@ def decode_fused(q_nope, q_rope, kv, kv_scale, req_to_token, seq_lens,
     outputs are allocated with torch unless given."""
     B, q_len, H, _ = q_nope.shape
     dev = q_nope.device
+    kind = _kv_dtype(kv)
+    if kind == KV_FP4_E2M1:
+        _check_fp4(q_nope, q_rope, kv, kv_scale, req_to_token, seq_lens)
     if O_part is None:
         O_part = torch.empty((num_splits, num_shards, B, q_len, H, VALUE_DIM),
                              dtype=torch.float32, device=dev)
@@ -366,7 +391,7 @@ def decode_fused(q_nope, q_rope, kv, kv_scale, req_to_token, seq_lens,
         lse_out = torch.empty((B, q_len, H), dtype=torch.float32, device=dev)
     with _on(q_nope):
         _check(library().mla_decode(
-            _ptr(q_nope), _ptr(q_rope), _ptr(kv), _ptr(kv_scale), _kv_dtype(kv),
+            _ptr(q_nope), _ptr(q_rope), _ptr(kv), _ptr(kv_scale), kind,
             kv.shape[0], _ptr(req_to_token), req_to_token.stride(0),
             _ptr(seq_lens), _ptr(kv_limit), B, q_len, H, num_shards, PAGE_SIZE,
             float(sm_scale), num_splits, _ptr(split_pages), _ptr(work),
@@ -390,13 +415,16 @@ def decode_scratch(q_nope, q_rope, kv, kv_scale, req_to_token, seq_lens,
     mla_decode_scratch (calls that may overlap on a device race on it)."""
     B, q_len, H, _ = q_nope.shape
     dev = q_nope.device
+    kind = _kv_dtype(kv)
+    if kind == KV_FP4_E2M1:
+        _check_fp4(q_nope, q_rope, kv, kv_scale, req_to_token, seq_lens)
     if out is None:
         out = torch.empty((B, q_len, H, VALUE_DIM), dtype=torch.bfloat16, device=dev)
     if lse_out is None:
         lse_out = torch.empty((B, q_len, H), dtype=torch.float32, device=dev)
     with _on(q_nope):  # the scratch array used is the current device's
         _check(library().mla_decode_scratch(
-            _ptr(q_nope), _ptr(q_rope), _ptr(kv), _ptr(kv_scale), _kv_dtype(kv),
+            _ptr(q_nope), _ptr(q_rope), _ptr(kv), _ptr(kv_scale), kind,
             kv.shape[0], _ptr(req_to_token), req_to_token.stride(0),
             _ptr(seq_lens), _ptr(kv_limit), B, q_len, H, num_shards, PAGE_SIZE,
             float(sm_scale), num_splits, _ptr(split_pages), _ptr(work),

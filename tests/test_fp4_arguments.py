@@ -121,6 +121,22 @@ def test_binding_refuses_shapes_types_and_strides():
             mla.add_rms_norm(**{**dict(x=x, weight=w), **bad})
 
 
+def test_binding_refuses_fp4_decode_layouts():
+    bf = torch.bfloat16
+    ok = dict(q_nope=torch.zeros((2, 1, 4, 512), dtype=bf), q_rope=torch.zeros((2, 1, 4, 64), dtype=bf),
+              kv=torch.zeros((64, 352), dtype=torch.uint8), kv_scale=torch.ones(1),
+              req_to_token=torch.zeros((2, 64), dtype=torch.int32), seq_lens=torch.ones(2, dtype=torch.int32),
+              kv_limit=None, num_splits=1, sm_scale=0.07)
+    for bad in (dict(q_nope=ok["q_nope"].float()), dict(q_rope=torch.zeros((2, 1, 4, 128), dtype=bf)[..., ::2]),
+                dict(q_rope=torch.zeros((2, 1, 3, 64), dtype=bf)), dict(kv_scale=None),
+                dict(kv_scale=torch.ones(1, dtype=torch.float64)), dict(seq_lens=torch.ones(2, dtype=torch.int64)),
+                dict(kv=torch.zeros((64, 704), dtype=torch.uint8)[:, ::2]),
+                dict(req_to_token=torch.zeros((2, 64), dtype=torch.int64))):
+        for call in (mla.decode_partial, mla.decode_fused, mla.decode_scratch):
+            with pytest.raises(ValueError):
+                call(**{**ok, **bad})
+
+
 def test_reference_formats():
     """The tests' own codecs against torch's E4M3 and the E2M1 value set."""
     codes = torch.arange(256, dtype=torch.int32).to(torch.uint8)
