@@ -37,46 +37,71 @@ namespace {
 
 using namespace ptx;
 
-constexpr int kThreads = 512;
-constexpr int kChunks = MLA_ROW_DIM / 64;    // 9 chunks of 64 dims
-constexpr int kBox = kPage * 128;            // 8 KB: 64 tokens x 64 dims f16
-constexpr int kRaw = 2;                      // raw pages in flight
+constexpr int kChunks = MLA_ROW_DIM / 64;  // 9 chunks of 64 dims
+constexpr int kBox = kPage * 128;          // 8 KB: 64 tokens x 64 dims f16
+constexpr int kHalf = 4 * kBox;            // half of a page's value dims
+constexpr int kConvWarps = 8;
+// Two softmax groups: 640 threads launch with 96 registers each (61440); the MMA
+// warpgroup gives some away.  One-way, 128 x 64 + 256 x 96 + 256 x 112 = 61440.
+constexpr int kRegsMma = 64;
+constexpr int kRegsSoftmax = 112;
 
 template <int N>
 struct Few {
+  static constexpr int kGroups = N > 32 ? 2 : 1;      // softmax warpgroups
+  static constexpr int kConv0 = 4 * kGroups;          // first converter warp
+  static constexpr int kMmaWarp = kConv0 + kConvWarps;
+  // Two softmax groups: whole warpgroups, for the split of the registers.
+  static constexpr int kThreads = kGroups == 2 ? 640 : 32 * (kMmaWarp + 1);
+  static constexpr int kCols1 = N / kGroups;          // rows of a group
+  static constexpr int kH = kCols1 / 2;               // rows of a softmax thread
+  static constexpr int kLd = N > 16 ? 32 : 16;        // O^T columns read at a time
+  // What 227 KB of shared memory and 512 TMEM columns leave room for.
+  static constexpr int kHalves = N > 32 ? 3 : 4;      // ring of half pages
+  static constexpr int kSBufs = N > 64 ? 1 : 2;       // S^T buffers
+  static constexpr int kPBufs = N > 32 ? 1 : 2;       // P buffers
+  // How the raw pages arrive: straight to the converters' registers (needs room
+  // in L1, so little shared memory), through one raw buffer, or (0) through the
+  // slot that the page's first half is converted into.
+  static constexpr bool kDirect = N <= 32;
+  static constexpr int kRaw = N > 64 ? 0 : 1;
+  // In-slot copies are at most kHalves / 2 pages ahead of the converters.
+  static constexpr int kRawFull = kRaw > 0 ? kRaw : 2;
+  static_assert(kRaw > 0 || kHalves <= 4, "a raw_full phase per page in the ring");
   static constexpr int kQBox = N * 128;               // N rows x 64 values
-  static constexpr uint32_t kColO = 2 * N;            // after two S^T buffers
+  static constexpr uint32_t kColO = kSBufs * N;
   static constexpr uint32_t kIdescS = idesc_f16_f32(64, N, false, false);
   static constexpr uint32_t kIdescO = idesc_f16_f32(128, N, true, false);
-  static constexpr uint32_t kCols = 256;              // 6 N, a power of two
-  static_assert(6 * N <= kCols, "TMEM columns");
+  static constexpr uint32_t kCols = N > 32 ? 512 : 256;
+  static_assert(kColO + 4 * N <= kCols, "TMEM columns");
   struct __align__(1024) Smem {
-    uint8_t v[2][kChunks - 1][kBox];
-    uint8_t kr[kBox];           // the RoPE key (one set: N = 32 leaves no room)
+    uint8_t v[kHalves][kHalf];
+    uint8_t kr[kBox];           // the RoPE key (one: a second has no room)
     uint8_t q[kChunks][kQBox];
-    uint8_t pt[2][kQBox];       // P: rows x 64 tokens
-    uint8_t raw[kRaw][kRawBytes];
+    uint8_t pt[kPBufs][kQBox];  // P: rows x 64 tokens
+    uint8_t raw[kRaw > 0 && !kDirect ? kRawBytes : 16];
     float sc[N];                // softmax scale (log2) * g * the row's 2^(e - 14)
     float mref[N];              // running references
-    float alpha[N];
-    float fin[N];               // g / l
-    float wred[4][N];           // per-warp maxima, then sums
     int32_t lim[N];             // tokens of the request the row sees
-    uint64_t raw_full[kRaw];    // a raw page landed
-    uint64_t raw_empty[kRaw];   // the eight converter warps have read it
-    uint64_t cfull[2][2];       // half h of box set b is written (8 warps)
-    uint64_t sfull[2];          // S^T buffer b holds a page's scores
-    uint64_t pready[2];         // P buffer b is written, O^T rescaled (4 warps)
-    uint64_t vfree[2][2];       // the outputs' products have read half h of set b
-                                // (h = 1: all of it, and P)
+    float wred[4][N];           // per-quadrant maxima, then sums; row 0 passes on
+                                // the factors of a rescale and, last, g / l
+    uint64_t raw_full[kRawFull];   // a raw page has landed
+    uint64_t raw_empty;            // the converter warps have read it
+    uint64_t qfull;             // the query rows are written (softmax warps)
+    uint64_t cfull[kHalves];    // a half page is written (8 warps)
+    uint64_t rfull;             // a page's RoPE key is written (8 warps)
+    uint64_t vfree[kHalves];    // the outputs' products have read it
+    uint64_t sfull[kSBufs];     // the buffer holds a page's scores
+    uint64_t sread[kSBufs];     // the softmax warps have them in registers
+    uint64_t pready[kPBufs];    // P is written, O^T rescaled
+    uint64_t odone[kPBufs];     // a page's outputs are added
     uint64_t drain;
-    uint32_t raw_bad[kRaw];
+    uint32_t raw_bad[kRawFull];
     uint32_t tmem_base;
     int abort_flag;
     int last;                   // fused combine: the unit's last part
   };
-  static constexpr int kSmemBytes = (int)sizeof(Smem) + 1024;
-  static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
+  static_assert(sizeof(Smem) <= 227 * 1024, "shared memory budget");
 };
 
 template <typename S>
@@ -108,184 +133,314 @@ __device__ __forceinline__ void tmem_st_n(uint32_t taddr, const uint32_t (&r)[N]
     tmem_st16(taddr, r);
 }
 
-// Whether any of the 128 threads of warps 4..7 says so (named barrier 1).
-__device__ __forceinline__ bool any_of_128(bool x) {
+// Whether any of the kThreadsIn softmax threads says so (named barrier 1).
+template <int kThreadsIn>
+__device__ __forceinline__ bool any_of(bool x) {
   uint32_t r;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
-      "barrier.cta.red.or.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      "barrier.cta.red.or.pred q, 1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(r)
-      : "r"((uint32_t)x)
+      : "r"((uint32_t)x), "n"(kThreadsIn)
       : "memory");
   return r != 0;
 }
 
-// Warp 0: the unit's pages into the raw ring (see copy_pages of
-// mla_tc_fp4.cu).
+// The query rows, by the softmax warps while the first page arrives: warp k rows
+// k, k + kConv0, ..., four rows' loads in flight.  q 2^(14 - e) as f16 into the
+// K-major operand boxes; rows past R become zeros that see nothing.
+template <int N>
+__device__ __forceinline__ void place_query(typename Few<N>::Smem& s, const Fp4Params& p,
+                                            const UnitRange& w, int warp, int lane) {
+  constexpr int kWarps = Few<N>::kConv0, kBatch = N / kWarps < 4 ? N / kWarps : 4;
+  static_assert(N % (kWarps * kBatch) == 0, "rows of a warp");
+  const int R = p.q_len * p.H;
+#pragma unroll 1
+  for (int n0 = warp; n0 < N; n0 += kWarps * kBatch) {
+    uint4 x[kBatch][3];
+#pragma unroll
+    for (int r = 0; r < kBatch; ++r) {
+      const int n = n0 + kWarps * r;
+      const int64_t row = (int64_t)w.b * R + n;
+#pragma unroll
+      for (int k = 0; k < 3; ++k) {
+        const int c = lane + 32 * k;  // 16-byte chunk of the row's 72
+        x[r][k] = make_uint4(0, 0, 0, 0);
+        if (n < R && c < 72)
+          x[r][k] = c < 64 ? p.q_nope[row * 64 + c] : p.q_rope[row * 8 + c - 64];
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < kBatch; ++r) {
+      const int n = n0 + kWarps * r;
+      uint32_t big = 0;
+#pragma unroll
+      for (int k = 0; k < 3; ++k) {
+        const uint32_t y[4] = {x[r][k].x, x[r][k].y, x[r][k].z, x[r][k].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          big = max(big, max(y[e] & 0x7FFFu, (y[e] >> 16) & 0x7FFFu));
+      }
+      big = __reduce_max_sync(kFull, big);
+      const int e = max(min((int)(big >> 7), 254) - 127, -100);
+      const float up = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
+      const auto conv = [&](uint32_t v) -> uint32_t {
+        return pack_f16(__uint_as_float(v << 16) * up, __uint_as_float(v & 0xFFFF0000u) * up);
+      };
+#pragma unroll
+      for (int k = 0; k < 3; ++k) {
+        const int c = lane + 32 * k;
+        if (c < 72)
+          *reinterpret_cast<uint4*>(s.q[c >> 3] + (n >> 3) * 1024 + (n & 7) * 128 +
+                                    (((c & 7) ^ (n & 7)) << 4)) =
+              make_uint4(conv(x[r][k].x), conv(x[r][k].y), conv(x[r][k].z), conv(x[r][k].w));
+      }
+      if (lane == 0) {
+        const int i = n / p.H;
+        int64_t lim = 0;
+        if (n < R) {
+          lim = p.kv_limit ? (int64_t)p.kv_limit[(int64_t)w.v * p.q_len + i]
+                           : w.L - p.q_len + 1 + i;
+          lim = lim > w.L ? w.L : (lim < 0 ? 0 : lim);
+        }
+        s.lim[n] = (int32_t)lim;
+        s.sc[n] = p.scale_log2 * p.g[0] * __uint_as_float((uint32_t)(127 + e - 14) << 23);
+        s.mref[n] = -INFINITY;
+      }
+    }
+  }
+  __syncwarp();
+  if (lane == 0) mbar_arrive(smem_u32(&s.qfull));
+  named_bar_sync(2, 32 * kWarps);  // lim, sc and mref are read by every warp
+}
+
+// A position in the ring of half pages and the times it has wrapped round.
+template <int K>
+struct Ring {
+  uint32_t slot = 0, turn = 0;
+  __device__ __forceinline__ void next() {
+    if (++slot == K) {
+      slot = 0;
+      ++turn;
+    }
+  }
+};
+
+// One warp: the unit's pages as they are stored, one bulk copy each, into the raw
+// ring or, where there is no room for one, into the free half-page slot in which
+// the page's first half will be converted.
 template <int N>
 __device__ __forceinline__ void copy_pages(typename Few<N>::Smem& s, const Fp4Params& p,
                                            const UnitRange& w, int lane) {
+  using F = Few<N>;
   bool ok = true;
   int issued = 0;
   int32_t ent = 0;
+  Ring<F::kHalves> ring;
   for (int m = 0; m < w.npages && ok; ++m) {
     if (m % 32 == 0) ent = page_entry(p, w, m + lane);
     const int32_t base = checked_base(p, __shfl_sync(kFull, ent, m & 31));
     if (lane == 0) {
-      const int slot = m % kRaw;
-      if (mbar_wait(smem_u32(&s.raw_empty[slot]), ((m / kRaw) & 1) ^ 1, &s.abort_flag)) {
-        const uint32_t bar = smem_u32(&s.raw_full[slot]);
-        s.raw_bad[slot] = base < 0;
+      const int f = m % F::kRawFull;
+      bool free;
+      uint8_t* dst;
+      if constexpr (F::kRaw > 0) {
+        free = mbar_wait_cta(smem_u32(&s.raw_empty), (m & 1) ^ 1, &s.abort_flag);
+        dst = s.raw;
+      } else {
+        free = ring.turn == 0 || mbar_wait_cta(smem_u32(&s.vfree[ring.slot]), (ring.turn - 1) & 1,
+                                           &s.abort_flag);
+        dst = s.v[ring.slot];
+      }
+      if (free) {
+        const uint32_t bar = smem_u32(&s.raw_full[f]);
+        s.raw_bad[f] = base < 0;
         if (base < 0) {
           if (p.status) atomicOr(p.status, MLA_STATUS_BAD_SLOT);
           mbar_arrive(bar);
         } else {
           mbar_arrive_expect_tx(bar, kRawBytes);
-          bulk_load(smem_u32(s.raw[slot]), p.kv + (int64_t)base * kFp4RowBytes, kRawBytes,
-                    bar);
+          bulk_load(smem_u32(dst), p.kv + (int64_t)base * kFp4RowBytes, kRawBytes, bar);
         }
         ++issued;
       } else {
         ok = false;
       }
     }
+    ring.next();
+    ring.next();
     ok = __shfl_sync(kFull, ok, 0);
   }
   if (!ok && lane == 0) {
     give_up(s, p);
     // No copy may still be in flight when the CTA leaves.
     int never = 0;
-    for (int i = max(0, issued - kRaw); i < issued; ++i)
-      mbar_wait(smem_u32(&s.raw_full[i % kRaw]), (i / kRaw) & 1, &never);
+    for (int i = max(0, issued - F::kRawFull); i < issued; ++i)
+      mbar_wait_cta(smem_u32(&s.raw_full[i % F::kRawFull]), (i / F::kRawFull) & 1, &never);
   }
 }
 
-// The query rows, all warps: warp n, n + 16, ... row n.  q 2^(14 - e) as f16
-// into the K-major operand boxes; rows past R become zeros that see nothing.
-template <int N>
-__device__ __forceinline__ void place_query(typename Few<N>::Smem& s, const Fp4Params& p,
-                                            const UnitRange& w, int warp, int lane) {
-  const int R = p.q_len * p.H;
-  for (int n = warp; n < N; n += kThreads / 32) {
-    const int64_t row = (int64_t)w.b * R + n;
-    uint4 x[3];
-    uint32_t big = 0;
-#pragma unroll
-    for (int k = 0; k < 3; ++k) {
-      const int c = lane + 32 * k;  // 16-byte chunk of the row's 72
-      x[k] = make_uint4(0, 0, 0, 0);
-      if (n < R && c < 72)
-        x[k] = c < 64 ? p.q_nope[row * 64 + c] : p.q_rope[row * 8 + c - 64];
-      const uint32_t y[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        big = max(big, max(y[e] & 0x7FFFu, (y[e] >> 16) & 0x7FFFu));
-    }
-    big = __reduce_max_sync(kFull, big);
-    const int e = max(min((int)(big >> 7), 254) - 127, -100);
-    const float up = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
-    const auto conv = [&](uint32_t v) -> uint32_t {
-      return pack_f16(__uint_as_float(v << 16) * up, __uint_as_float(v & 0xFFFF0000u) * up);
-    };
-#pragma unroll
-    for (int k = 0; k < 3; ++k) {
-      const int c = lane + 32 * k;
-      if (c < 72)
-        *reinterpret_cast<uint4*>(s.q[c >> 3] + (n >> 3) * 1024 + (n & 7) * 128 +
-                                  (((c & 7) ^ (n & 7)) << 4)) =
-            make_uint4(conv(x[k].x), conv(x[k].y), conv(x[k].z), conv(x[k].w));
-    }
-    if (lane == 0) {
-      const int i = n / p.H;
-      int64_t lim = 0;
-      if (n < R) {
-        lim = p.kv_limit ? (int64_t)p.kv_limit[(int64_t)w.v * p.q_len + i]
-                         : w.L - p.q_len + 1 + i;
-        lim = lim > w.L ? w.L : (lim < 0 ? 0 : lim);
-      }
-      s.lim[n] = (int32_t)lim;
-      s.sc[n] = p.scale_log2 * p.g[0] * __uint_as_float((uint32_t)(127 + e - 14) << 23);
-      s.mref[n] = -INFINITY;
-    }
-  }
+// Two E4M3 scales with a NaN (0x7F, 0xFF) replaced by 0.
+__device__ __forceinline__ uint32_t finite_pair(uint32_t w) {
+  if ((w & 0x7Fu) == 0x7Fu) w &= 0xFF00u;
+  if ((w & 0x7F00u) == 0x7F00u) w &= 0x00FFu;
+  return w;
 }
 
-// Warps 8..15: thread = token tid / 4 and block tid % 4 of each 64 dims (the
-// 8-byte reads of rows 352 bytes apart and the swizzled 16-byte writes are both
-// free of bank conflicts).  The scales of tokens past the length or of a bad
-// page count as 0.  A NaN scale of a token that only some rows see has to show
-// in those rows' scores but must not reach O through a masked p = 0: the boxes,
-// shared by both products, hold 0 there and the token's RoPE key, which only
-// the scores read, is NaN instead.
+__device__ __forceinline__ uint4 load_nc(const uint8_t* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint16_t load_nc2(const uint8_t* p) {
+  uint16_t v;
+  asm volatile("ld.global.nc.L1::no_allocate.u16 %0, [%1];" : "=h"(v) : "l"(p));
+  return v;
+}
+
+// A converter thread's share of a raw page, of which `row` is the warp's first
+// token.
+struct RawShare {
+  uint4 code[4], rope;
+  uint32_t scale[4];
+  bool bad;
+
+  template <bool kGlobal>
+  __device__ __forceinline__ void read(const uint8_t* row, int t4, int v, int rt, int lane) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint8_t* r = row + (t4 + 4 * (j & 1)) * kFp4RowBytes;
+      const uint8_t* c = r + (v + 8 * (j >> 1)) * 16;
+      const uint8_t* q = r + kFp4ScaleOff + (v + 8 * (j >> 1)) * 2;
+      code[j] = kGlobal ? load_nc(c) : *reinterpret_cast<const uint4*>(c);
+      scale[j] = kGlobal ? load_nc2(q) : *reinterpret_cast<const uint16_t*>(q);
+    }
+    const uint8_t* k = row + rt * kFp4RowBytes + kFp4RopeOff + 16 * (lane & 3);
+    rope = kGlobal ? load_nc(k) : *reinterpret_cast<const uint4*>(k);
+  }
+};
+
+// The converters: warp k has tokens 8 k .. 8 k + 7, in registers from the
+// raw page on.  Of the row's 16 vectors of 32 codes a lane has
+// vector v = (lane & 1) + 2 (lane / 8) of the four tokens (lane / 2) % 4 + 4 j,
+// and v + 8: the eight lanes of a phase of a 16-byte load or store touch
+// eight different sixteenths of the banks' 128 bytes.  The scales of tokens past the length or of a bad page count as 0.  A
+// NaN scale of a token that only some rows see has to show in those rows' scores
+// but must not reach O through a masked p = 0: the boxes, shared by both
+// products, hold 0 there and the token's RoPE key, which only the scores read,
+// is NaN instead.
 template <int N>
 __device__ __forceinline__ void convert(typename Few<N>::Smem& s, const Fp4Params& p,
-                                        const UnitRange& w, int tid, int lane) {
-  const int t = tid >> 2, part = tid & 3;
-  const uint32_t trow = (t >> 3) * 1024 + (t & 7) * 128;
-  const uint32_t o0 = trow + (((2 * part) ^ (t & 7)) << 4);
-  const uint32_t o1 = trow + (((2 * part + 1) ^ (t & 7)) << 4);
+                                        const UnitRange& w, int warp, int lane) {
+  using F = Few<N>;
+  const int t4 = (lane >> 1) & 3, v = (lane & 1) + 2 * (lane >> 3);
+  const int rt = lane >> 2;  // token of the lane's RoPE codes
+  const uint32_t at_v = (lane >> 3) * kBox + warp * 1024, ch = 4 * (lane & 1);
+  const uint32_t at_r = warp * 1024 + rt * 128;
   bool ok = true;
-  for (int m = 0; m < w.npages; ++m) {
-    const int slot = m % kRaw, set = m & 1;
-    const uint8_t* row = s.raw[slot] + t * kFp4RowBytes;
-    ok = ok && mbar_wait(smem_u32(&s.raw_full[slot]), (m / kRaw) & 1, &s.abort_flag);
-    const int64_t at = (w.p0 + m) * kPage + t;
-    const bool bad = s.raw_bad[slot] != 0;
-    uint2 code[8];
-#pragma unroll
-    for (int c = 0; c < 8; ++c)
-      code[c] = *reinterpret_cast<const uint2*>(row + 32 * c + 8 * part);
-    const uint4 sa = *reinterpret_cast<const uint4*>(row + kFp4ScaleOff);
-    const uint4 sb = *reinterpret_cast<const uint4*>(row + kFp4ScaleOff + 16);
-    uint4 rope = *reinterpret_cast<const uint4*>(row + kFp4RopeOff + 16 * part);
-    uint32_t sw[8] = {sa.x, sa.y, sa.z, sa.w, sb.x, sb.y, sb.z, sb.w};
-    bool nan = false;
-    if (at >= w.nmin || bad) {
-      const bool live = at < w.L && !bad;
-#pragma unroll
-      for (int c = 0; c < 8; ++c) {
-        const uint32_t f = live ? finite_scales(sw[c]) : 0u;
-        nan |= live && f != sw[c];
-        sw[c] = f;
-      }
-      if (bad) rope = make_uint4(0, 0, 0, 0);
+  // Where the warps meet at a barrier a warp that gave up goes on, waiting for
+  // nothing else.
+  const auto stop = [&] { return F::kRaw > 0 && !__all_sync(kFull, ok); };
+  Ring<F::kHalves> ring;
+  RawShare next;
+  int32_t ent = 0, ent_next = 0;
+  if constexpr (F::kDirect) {
+    ent = page_entry(p, w, lane);
+    ent_next = page_entry(p, w, 32 + lane);
+  }
+  const auto load = [&](int m) {
+    if (m > 0 && m % 32 == 0) {
+      ent = ent_next;
+      ent_next = page_entry(p, w, m + 32 + lane);
     }
-    __syncwarp();  // every lane has read the page
-    if (lane == 0) mbar_arrive(smem_u32(&s.raw_empty[slot]));
+    const int32_t base = checked_base(p, __shfl_sync(kFull, ent, m & 31));
+    next.bad = base < 0;
+    if (next.bad) {
+      if (warp == 0 && lane == 0 && p.status) atomicOr(p.status, MLA_STATUS_BAD_SLOT);
+      return;
+    }
+    next.read<true>(p.kv + ((int64_t)base + 8 * warp) * kFp4RowBytes, t4, v, rt, lane);
+  };
+  if constexpr (F::kDirect) load(0);
+  for (int m = 0; m < w.npages; ++m) {
+    RawShare x;
+    if constexpr (F::kDirect) {
+      x = next;
+      if (m + 1 < w.npages) load(m + 1);
+    } else {
+      const int f = m % F::kRawFull;
+      ok = ok && mbar_wait_cta(smem_u32(&s.raw_full[f]), (m / F::kRawFull) & 1, &s.abort_flag);
+      if (stop()) break;
+      x.bad = s.raw_bad[f] != 0;
+      x.read<false>((F::kRaw > 0 ? s.raw : s.v[ring.slot]) + 8 * warp * kFp4RowBytes, t4, v, rt,
+                    lane);
+      __syncwarp();  // every lane has read the page
+      if (F::kRaw > 0 && lane == 0) mbar_arrive(smem_u32(&s.raw_empty));
+      // In its slot: every warp has, before it is written over.
+      if (F::kRaw == 0) named_bar_sync(3, 32 * kConvWarps);
+    }
+    const int64_t at = (w.p0 + m) * kPage + 8 * warp;  // the warp's first token
+    bool nan = false;  // the token of the lane's RoPE codes has a NaN scale
+    if (at + 8 > w.nmin || x.bad) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int t = t4 + 4 * (j & 1);
+        const bool live = at + t < w.L && !x.bad;
+        const uint32_t f = live ? finite_pair(x.scale[j]) : 0u;
+        const uint32_t b = __ballot_sync(kFull, live && f != x.scale[j]);
+        if (b & (0x03030303u << (2 * (rt & 3))) && (rt >> 2) == (j & 1)) nan = true;
+        x.scale[j] = f;
+      }
+      if (x.bad) x.rope = make_uint4(0, 0, 0, 0);
+    }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      // The page two back has left this half.
-      if (m > 1)
-        ok = ok && mbar_wait(smem_u32(&s.vfree[set][h]), ((m >> 1) - 1) & 1, &s.abort_flag);
-      // The last page's scores have read the RoPE key.
-      if (h == 1 && m > 0)
-        ok = ok && mbar_wait(smem_u32(&s.sfull[set ^ 1]), ((m - 1) >> 1) & 1, &s.abort_flag);
-      if (!__all_sync(kFull, ok)) break;
+      // What lay in this slot before has been read.
+      if (ring.turn > 0 && (F::kRaw > 0 || h == 1))
+        ok = ok && mbar_wait_cta(smem_u32(&s.vfree[ring.slot]), (ring.turn - 1) & 1, &s.abort_flag);
+      if (stop()) break;
+      uint8_t* const box = s.v[ring.slot] + at_v;
 #pragma unroll
-      for (int c = 4 * h; c < 4 * h + 4; ++c) {
-        const uint32_t sc = e4m3x2_to_f16((sw[c] >> (8 * part)) & 0xFFu);
-        const uint32_t s2 = __byte_perm(sc, sc, 0x1010);
-        *reinterpret_cast<uint4*>(s.v[set][c] + o0) = scaled8(code[c].x, s2);
-        *reinterpret_cast<uint4*>(s.v[set][c] + o1) = scaled8(code[c].y, s2);
-      }
-      if (h == 1) {
-        uint4 r0 = plain8(rope.x, rope.y);
-        if (nan) r0.x = 0x7E007E00u;
-        *reinterpret_cast<uint4*>(s.kr + o0) = r0;
-        *reinterpret_cast<uint4*>(s.kr + o1) = plain8(rope.z, rope.w);
+      for (int j = 2 * h; j < 2 * h + 2; ++j) {
+        const int t = t4 + 4 * (j & 1);
+        const uint32_t sc = e4m3x2_to_f16(x.scale[j]);
+        const uint32_t lo = __byte_perm(sc, sc, 0x1010), hi = __byte_perm(sc, sc, 0x3232);
+        uint8_t* const b = box + t * 128;
+        *reinterpret_cast<uint4*>(b + (((ch + 0) ^ t) << 4)) = scaled8(x.code[j].x, lo);
+        *reinterpret_cast<uint4*>(b + (((ch + 1) ^ t) << 4)) = scaled8(x.code[j].y, lo);
+        *reinterpret_cast<uint4*>(b + (((ch + 2) ^ t) << 4)) = scaled8(x.code[j].z, hi);
+        *reinterpret_cast<uint4*>(b + (((ch + 3) ^ t) << 4)) = scaled8(x.code[j].w, hi);
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&s.cfull[set][h]));
+      if (lane == 0) mbar_arrive(smem_u32(&s.cfull[ring.slot]));
+      ring.next();
+      if (h == 0) {
+        // The RoPE key, once the last page's scores have read it.
+        if (m > 0)
+          ok = ok && mbar_wait_cta(smem_u32(&s.sfull[(m - 1) % F::kSBufs]),
+                               ((m - 1) / F::kSBufs) & 1, &s.abort_flag);
+        if (stop()) break;
+        uint4 r0 = plain8(x.rope.x, x.rope.y);
+        if (nan) r0.x = 0x7E007E00u;
+        const uint32_t c = 2 * (lane & 3);
+        *reinterpret_cast<uint4*>(s.kr + at_r + ((c ^ rt) << 4)) = r0;
+        *reinterpret_cast<uint4*>(s.kr + at_r + (((c + 1) ^ rt) << 4)) =
+            plain8(x.rope.z, x.rope.w);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&s.rfull));
+      }
     }
-    if (!__all_sync(kFull, ok)) break;
+    if (stop()) break;
   }
   if (!__all_sync(kFull, ok) && lane == 0) give_up(s, p);
 }
 
-// Warp 1, one lane: every MMA of the unit: of this page's outputs and the next
-// page's scores, whichever is ready first (in either fixed order one of them
-// holds up the converters: scores first 120 us, as they come 90 us, for 32
-// requests x 16 heads, 2k to 60k tokens).
+// The MMA warp, one lane: every MMA of the unit: of this page's outputs and the
+// next page's scores, whichever is ready first (in either fixed order one of
+// them holds up the converters).  A ring of three half pages only ever holds
+// the first half of the next page before this page's first half is left.
 template <int N>
 __device__ __forceinline__ void issue_mmas(typename Few<N>::Smem& s, const Fp4Params& p,
                                            const UnitRange& w, uint32_t tmem) {
@@ -294,43 +449,54 @@ __device__ __forceinline__ void issue_mmas(typename Few<N>::Smem& s, const Fp4Pa
   const uint64_t pd = sdesc_sw128(smem_u32(s.pt[0]), 16, 1024);
   // K: K-major, 128-byte rows.  V^T: MN-major, the next 64 dims one box on, the
   // next 8 tokens 1 KB on.
-  const uint64_t kd = sdesc_sw128(smem_u32(s.v[0][0]), 16, 1024);
+  const uint64_t kd = sdesc_sw128(smem_u32(s.v[0]), 16, 1024);
   const uint64_t rd = sdesc_sw128(smem_u32(s.kr), 16, 1024);
-  const uint64_t vd = sdesc_sw128(smem_u32(s.v[0][0]), kBox, 1024);
-  constexpr uint64_t kSet = (kChunks - 1) * (kBox >> 4);
+  const uint64_t vd = sdesc_sw128(smem_u32(s.v[0]), kBox, 1024);
   bool ok = true;
-  const auto scores = [&](int m) {
-    const uint32_t set = m & 1;
-    const uint32_t d = tmem + set * N;
-    const uint64_t k0 = kd + set * kSet;
+  Ring<F::kHalves> in, out;  // of the scores and of the outputs
+  const auto score_half = [&](int m, int h) {
+    const uint32_t sb = m % F::kSBufs, d = tmem + sb * N, slot = in.slot;
+    ok = ok && mbar_wait_cta(smem_u32(&s.cfull[slot]), in.turn & 1, &s.abort_flag);
+    in.next();
+    if (!ok) return;
+    fence_proxy_async_smem();
+    tc_fence_after();
+    const uint64_t k0 = kd + slot * (kHalf >> 4), q0 = qd + h * 4 * (F::kQBox >> 4);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      ok = ok && mbar_wait(smem_u32(&s.cfull[set][h]), (m >> 1) & 1, &s.abort_flag);
+    for (int c = 0; c < 4; ++c)
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        mma_ss(d, k0 + c * (kBox >> 4) + 2 * k, q0 + c * (F::kQBox >> 4) + 2 * k, F::kIdescS,
+               (h | c | k) ? 1u : 0u);
+    if (h == 0) {
+      ok = ok && mbar_wait_cta(smem_u32(&s.rfull), m & 1, &s.abort_flag);
       if (!ok) return;
       fence_proxy_async_smem();
-      tc_fence_after();
 #pragma unroll
-      for (int c = 4 * h; c < 4 * h + 4 + h; ++c)
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          mma_ss(d, (c < 8 ? k0 + c * (kBox >> 4) : rd) + 2 * k,
-                 qd + c * (F::kQBox >> 4) + 2 * k, F::kIdescS, (c | k) ? 1u : 0u);
+      for (int k = 0; k < 4; ++k)
+        mma_ss(d, rd + 2 * k, qd + 8 * (F::kQBox >> 4) + 2 * k, F::kIdescS, 1u);
+    } else {
+      mma_commit(smem_u32(&s.sfull[sb]));
     }
-    mma_commit(smem_u32(&s.sfull[set]));
   };
-  if (w.npages > 0) scores(0);
+  ok = mbar_wait_cta(smem_u32(&s.qfull), 0, &s.abort_flag);
+  if (ok) {
+    score_half(0, 0);
+    score_half(0, 1);
+  }
   for (int m = 0; m < w.npages && ok; ++m) {
-    const uint32_t set = m & 1;
-    // The buffer of S^T(m + 1) was read before P(m - 1) was ready.
-    const uint32_t pbar = smem_u32(&s.pready[set]), pph = (m >> 1) & 1;
-    bool next = m + 1 < w.npages;  // its scores are still to issue
-    if (next) {
-      const uint32_t cbar = smem_u32(&s.cfull[set ^ 1][0]), cph = ((m + 1) >> 1) & 1;
+    const uint32_t pb = m % F::kPBufs;
+    const uint32_t pbar = smem_u32(&s.pready[pb]), pph = (m / F::kPBufs) & 1;
+    int next = m + 1 < w.npages ? 0 : 2;  // first half of its scores still to issue
+    if (next == 0) {
+      // With two S^T buffers, that of m + 1 was read before P(m - 1) was ready.
+      const uint32_t cbar = smem_u32(&s.cfull[in.slot]), cph = in.turn & 1;
+      const uint32_t rbar = smem_u32(&s.sread[0]), rph = m & 1;
       const uint64_t t0 = globaltimer();
-      for (uint32_t it = 1; !mbar_try_wait(pbar, pph); ++it) {
-        if (mbar_try_wait(cbar, cph)) {
-          scores(m + 1);
-          next = false;
+      for (uint32_t it = 1; !mbar_test_wait(pbar, pph); ++it) {
+        if ((F::kSBufs == 2 || mbar_test_wait(rbar, rph)) && mbar_test_wait(cbar, cph)) {
+          score_half(m + 1, next++);
+          if (F::kHalves >= 4) score_half(m + 1, next++);
           break;
         }
         if ((it & 63) == 0 && (*const_cast<volatile int*>(&s.abort_flag) ||
@@ -340,33 +506,39 @@ __device__ __forceinline__ void issue_mmas(typename Few<N>::Smem& s, const Fp4Pa
         }
       }
     }
-    ok = ok && mbar_wait(pbar, pph, &s.abort_flag);
+    ok = ok && mbar_wait_cta(pbar, pph, &s.abort_flag);
     if (!ok) break;
     fence_proxy_async_smem();
     tc_fence_after();
-    const uint64_t v0 = vd + set * kSet, p0 = pd + set * (F::kQBox >> 4);
+    const uint64_t p0 = pd + pb * (F::kQBox >> 4);
 #pragma unroll
-    for (int b = 0; b < 4; ++b) {
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t slot = out.slot;
+      out.next();
+      const uint64_t v0 = vd + slot * (kHalf >> 4);
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        mma_ss(tmem + F::kColO + (uint32_t)(N * b), v0 + 2 * b * (kBox >> 4) + 128 * k,
-               p0 + 2 * k, F::kIdescO, k ? 1u : (m ? 1u : 0u));
-      if (b & 1) mma_commit(smem_u32(&s.vfree[set][b >> 1]));
+      for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          mma_ss(tmem + F::kColO + (uint32_t)(N * (2 * h + b)), v0 + 2 * b * (kBox >> 4) + 128 * k,
+                 p0 + 2 * k, F::kIdescO, k ? 1u : (m ? 1u : 0u));
+      mma_commit(smem_u32(&s.vfree[slot]));
     }
-    if (next) scores(m + 1);
+    mma_commit(smem_u32(&s.odone[pb]));
+    while (next < 2 && ok) score_half(m + 1, next++);
   }
   if (!ok) give_up(s, p);
   // No MMA may still run when the accumulators are freed.
   int never = 0;
   mma_commit(smem_u32(&s.drain));
-  mbar_wait(smem_u32(&s.drain), 0, &never);
+  mbar_wait_cta(smem_u32(&s.drain), 0, &never);
 }
 
-// N columns of the 16 TMEM lanes from `taddr` on, the first half of them in
+// 2 H columns of the 16 TMEM lanes from `taddr` on, the first half of them in
 // lanes 0..15, the second half in lanes 16..31.
-template <int N>
-__device__ __forceinline__ void tmem_ld_halves(uint32_t taddr, uint32_t (&r)[N / 2]) {
-  if constexpr (N == 32)
+template <int H>
+__device__ __forceinline__ void tmem_ld_halves(uint32_t taddr, uint32_t (&r)[H]) {
+  if constexpr (H == 16) {
     asm volatile(
         "tcgen05.ld.sync.aligned.16x32bx2.x16.b32 "
         "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16], 16;"
@@ -374,44 +546,49 @@ __device__ __forceinline__ void tmem_ld_halves(uint32_t taddr, uint32_t (&r)[N /
           "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]),
           "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
         : "r"(taddr));
-  else
-    asm volatile(
-        "tcgen05.ld.sync.aligned.16x32bx2.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8], 8;"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
-          "=r"(r[6]), "=r"(r[7])
-        : "r"(taddr));
+  } else {
+#pragma unroll
+    for (int k = 0; k < H; k += 8)
+      asm volatile(
+          "tcgen05.ld.sync.aligned.16x32bx2.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8], %9;"
+          : "=r"(r[k]), "=r"(r[k + 1]), "=r"(r[k + 2]), "=r"(r[k + 3]), "=r"(r[k + 4]),
+            "=r"(r[k + 5]), "=r"(r[k + 6]), "=r"(r[k + 7])
+          : "r"(taddr + k), "n"(H));
+  }
 }
 
-// Warps 4..7: an accumulator of M = 64 rows lies in the first 16 lanes of every
-// TMEM quadrant, so warp `quad` has tokens 16 quad .. + 15 and a thread token
-// 16 quad + lane % 16 with rows N / 2 (lane / 16) .. .  At the end, and when O^T
-// is rescaled, thread = value dim of a block of 128.
+// Softmax: an accumulator of M = 64 rows lies in the first 16 lanes of every
+// TMEM quadrant, so a warp of quadrant `quad` has tokens 16 quad .. + 15 and a
+// thread token 16 quad + lane % 16 with kH rows.  At the end, and when O^T is
+// rescaled, thread = value dim of a block of 128.
 template <int N>
 __device__ __forceinline__ void softmax(typename Few<N>::Smem& s, const Fp4Params& p,
                                         const UnitRange& w, uint32_t tmem, int warp, int lane) {
   using F = Few<N>;
-  constexpr int H = N / 2;
-  const int quad = warp & 3, dim = quad * 32 + lane;
-  const int tok = quad * 16 + (lane & 15), n0 = H * (lane >> 4);
+  constexpr int H = F::kH, T = 128 * F::kGroups;
+  const int quad = warp & 3, group = warp >> 2, dim = quad * 32 + lane;
+  const int tok = quad * 16 + (lane & 15), n0 = F::kCols1 * group + H * (lane >> 4);
   const uint32_t trow = tmem + ((uint32_t)(quad * 32) << 16);
   const int R = p.q_len * p.H;
+  float* const alpha = s.wred[0];
   bool ok = true;
-  float l[H], sc[H], m_ref[H];
+  float l[H];
 #pragma unroll
-  for (int k = 0; k < H; ++k) {
-    l[k] = 0.f;
-    sc[k] = s.sc[n0 + k];
-    m_ref[k] = -INFINITY;
-  }
-  uint8_t* const dst0 = s.pt[0] + (tok & 7) * 2;
+  for (int k = 0; k < H; ++k) l[k] = 0.f;
+  uint8_t* const dst0 = s.pt[0] + (n0 >> 3) * 1024 + (tok & 7) * 2;
   for (int m = 0; m < w.npages; ++m) {
-    const uint32_t set = m & 1;
+    const uint32_t sb = m % F::kSBufs, pb = m % F::kPBufs;
     uint32_t x[H];
-    ok = ok && mbar_wait(smem_u32(&s.sfull[set]), (m >> 1) & 1, &s.abort_flag);
+    ok = ok && mbar_wait_cta(smem_u32(&s.sfull[sb]), (m / F::kSBufs) & 1, &s.abort_flag);
     tc_fence_after();
     if (__all_sync(kFull, ok)) {
-      tmem_ld_halves<N>(trow + set * N, x);
+      tmem_ld_halves<H>(trow + sb * N + F::kCols1 * group, x);
       tmem_wait_ld();
+    }
+    if (F::kSBufs == 1) {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&s.sread[sb]));
     }
     // Scores in units of log2; tokens a row may not see become -inf (a select:
     // garbage or NaN in a masked score never propagates).
@@ -421,21 +598,23 @@ __device__ __forceinline__ void softmax(typename Few<N>::Smem& s, const Fp4Param
     bool over = false;
 #pragma unroll
     for (int k = 0; k < H; ++k) {
-      y[k] = __uint_as_float(x[k]) * sc[k];
+      if (k % 8 == 0) asm volatile("" ::: "memory");  // no more loads ahead: registers
+      y[k] = __uint_as_float(x[k]) * s.sc[n0 + k];
       if (!open && t0 + tok >= s.lim[n0 + k]) y[k] = -INFINITY;
-      over |= y[k] > m_ref[k] + kTau;
+      over |= y[k] > s.mref[n0 + k] + kTau;
     }
-    if (any_of_128(over)) {
+    if (any_of<T>(over)) {
       // Some row's maximum rises: the page's maxima over its 64 tokens.
 #pragma unroll
       for (int k = 0; k < H; ++k) {
+        if (k % 8 == 0) asm volatile("" ::: "memory");
         float z = fmaxf(y[k], -INFINITY);  // a NaN counts as none
 #pragma unroll
         for (int o = 8; o > 0; o >>= 1) z = fmaxf(z, __shfl_xor_sync(kFull, z, o));
         if ((lane & 15) == 0) s.wred[quad][n0 + k] = z;
       }
-      named_bar_sync(2, 128);
-      if (dim < N) {
+      named_bar_sync(2, T);
+      if (group == 0 && dim < N) {
         const float mt = fmaxf(fmaxf(s.wred[0][dim], s.wred[1][dim]),
                                fmaxf(s.wred[2][dim], s.wred[3][dim]));
         const float old = s.mref[dim];
@@ -444,56 +623,61 @@ __device__ __forceinline__ void softmax(typename Few<N>::Smem& s, const Fp4Param
           if (old > -INFINITY) a = ex2(old - mt);  // else O and l are still zero
           s.mref[dim] = mt;
         }
-        s.alpha[dim] = a;
+        alpha[dim] = a;
       }
-      named_bar_sync(2, 128);
+      named_bar_sync(2, T);
       bool scale = false;
+#pragma unroll 4
+      for (int n = 0; n < N; ++n) scale |= alpha[n] != 1.f;
 #pragma unroll
-      for (int n = 0; n < N; ++n) scale |= s.alpha[n] != 1.f;
-#pragma unroll
-      for (int k = 0; k < H; ++k) {
-        l[k] *= s.alpha[n0 + k];
-        m_ref[k] = s.mref[n0 + k];
-      }
+      for (int k = 0; k < H; ++k) l[k] *= alpha[n0 + k];
       if (scale && m > 0) {  // the same in every thread
-        ok = ok && mbar_wait(smem_u32(&s.vfree[set ^ 1][1]), ((m - 1) >> 1) & 1, &s.abort_flag);
+        ok = ok && mbar_wait_cta(smem_u32(&s.odone[(m - 1) % F::kPBufs]),
+                             ((m - 1) / F::kPBufs) & 1, &s.abort_flag);
         tc_fence_after();
         if (__all_sync(kFull, ok)) {
 #pragma unroll 1
-          for (int b = 0; b < 4; ++b) {
-            uint32_t o[N];
-            tmem_ld_n<N>(trow + F::kColO + (uint32_t)(N * b), o);
-            tmem_wait_ld();
+          for (int b = group; b < 4; b += F::kGroups)
+#pragma unroll 1
+            for (int c = 0; c < N; c += 16) {
+              const uint32_t at = trow + F::kColO + (uint32_t)(N * b + c);
+              uint32_t o[16];
+              tmem_ld_n<16>(at, o);
+              tmem_wait_ld();
 #pragma unroll
-            for (int n = 0; n < N; ++n)
-              o[n] = __float_as_uint(__uint_as_float(o[n]) * s.alpha[n]);
-            tmem_st_n<N>(trow + F::kColO + (uint32_t)(N * b), o);
-          }
+              for (int n = 0; n < 16; ++n)
+                o[n] = __float_as_uint(__uint_as_float(o[n]) * alpha[c + n]);
+              tmem_st_n<16>(at, o);
+            }
           tmem_wait_st();
         }
       }
     }
     // p = 2^(y - m_ref) (0 for a row that has seen nothing yet), f16 at
-    // [row][token] once the outputs of two pages back have read this buffer.
-    if (m > 1) ok = ok && mbar_wait(smem_u32(&s.vfree[set][1]), ((m >> 1) - 1) & 1, &s.abort_flag);
-    uint8_t* const dst = dst0 + set * F::kQBox;
+    // [row][token] once the outputs before have read this buffer.
+    if (m >= F::kPBufs)
+      ok = ok && mbar_wait_cta(smem_u32(&s.odone[pb]), (m / F::kPBufs - 1) & 1, &s.abort_flag);
+    uint8_t* const dst = dst0 + pb * F::kQBox;
 #pragma unroll
     for (int k = 0; k < H; ++k) {
-      const int n = n0 + k;
-      const float e = ex2(y[k] - (m_ref[k] == -INFINITY ? 0.f : m_ref[k]));
-      l[k] += e;
-      *reinterpret_cast<__half*>(dst + (n >> 3) * 1024 + (n & 7) * 128 +
-                                 (((tok >> 3) ^ (n & 7)) << 4)) = __float2half_rn(e);
+      if (k % 8 == 0) asm volatile("" ::: "memory");
+      const float ref = s.mref[n0 + k];
+      y[k] = ex2(y[k] - (ref == -INFINITY ? 0.f : ref));
+      l[k] += y[k];
     }
+#pragma unroll
+    for (int k = 0; k < H; ++k)
+      *reinterpret_cast<__half*>(dst + (k >> 3) * 1024 + (k & 7) * 128 +
+                                 (((tok >> 3) ^ (k & 7)) << 4)) = __float2half_rn(y[k]);
     tc_fence_before();
     __syncwarp();
-    if (lane == 0) mbar_arrive(smem_u32(&s.pready[set]));
+    if (lane == 0) mbar_arrive(smem_u32(&s.pready[pb]));
   }
   if (!__all_sync(kFull, ok) && lane == 0) give_up(s, p);
 
   // Row sums over the lanes and warps, LSE, and O_part = g O / l: lane = dim, so
   // every store of a warp is one line of a row.
-  named_bar_sync(2, 128);
+  named_bar_sync(2, T);
 #pragma unroll
   for (int k = 0; k < H; ++k) {
     float z = l[k];
@@ -501,51 +685,60 @@ __device__ __forceinline__ void softmax(typename Few<N>::Smem& s, const Fp4Param
     for (int o = 8; o > 0; o >>= 1) z += __shfl_xor_sync(kFull, z, o);
     if ((lane & 15) == 0) s.wred[quad][n0 + k] = z;
   }
-  named_bar_sync(2, 128);
+  named_bar_sync(2, T);
   const int64_t rows = (int64_t)p.B * R;
   const int64_t part = (int64_t)w.split * (p.V / p.B) + w.shard;
   const int64_t row0 = part * rows + (int64_t)w.b * R;
-  if (dim < N) {
+  float* const fin = s.wred[0];
+  if (group == 0 && dim < N) {
     const float lt = (s.wred[0][dim] + s.wred[1][dim]) + (s.wred[2][dim] + s.wred[3][dim]);
     if (dim < R)
       // no visible token: -inf; a NaN sum (a NaN score seen) stays NaN
       p.LSE_part[row0 + dim] =
           lt == 0.f ? -INFINITY : (s.mref[dim] + log2f(lt)) * 0.69314718055994531f;
-    s.fin[dim] = lt == 0.f ? 0.f : p.g[0] / lt;
+    fin[dim] = lt == 0.f ? 0.f : p.g[0] / lt;
   }
-  named_bar_sync(2, 128);
+  named_bar_sync(2, T);
   const int last = w.npages - 1;
-  ok = ok && mbar_wait(smem_u32(&s.vfree[last & 1][1]), (last >> 1) & 1, &s.abort_flag);
+  ok = ok && mbar_wait_cta(smem_u32(&s.odone[last % F::kPBufs]), (last / F::kPBufs) & 1,
+                       &s.abort_flag);
   tc_fence_after();
   if (!__all_sync(kFull, ok)) {
     if (lane == 0) give_up(s, p);
     return;
   }
 #pragma unroll 1
-  for (int b = 0; b < 4; ++b) {
-    uint32_t o[N];
-    tmem_ld_n<N>(trow + F::kColO + (uint32_t)(N * b), o);
-    tmem_wait_ld();
-    const int64_t at = row0 * MLA_VALUE_DIM + 128 * b + dim;
+  for (int b = group; b < 4; b += F::kGroups)
+#pragma unroll 1
+    for (int c = 0; c < N; c += F::kLd) {
+      uint32_t o[F::kLd];
+      tmem_ld_n<F::kLd>(trow + F::kColO + (uint32_t)(N * b + c), o);
+      tmem_wait_ld();
+      const int64_t at = (row0 + c) * MLA_VALUE_DIM + 128 * b + dim;
 #pragma unroll
-    for (int n = 0; n < N; ++n) {
-      if (n >= R) break;
-      const float z = __uint_as_float(o[n]) * s.fin[n];
-      if (p.o_bf16)
-        reinterpret_cast<__nv_bfloat16*>(p.O_part)[at + n * MLA_VALUE_DIM] =
-            __float2bfloat16_rn(z);
-      else
-        p.O_part[at + n * MLA_VALUE_DIM] = z;
+      for (int n = 0; n < F::kLd; ++n) {
+        if (c + n >= R) break;
+        const float z = __uint_as_float(o[n]) * fin[c + n];
+        if (p.o_bf16)
+          reinterpret_cast<__nv_bfloat16*>(p.O_part)[at + n * MLA_VALUE_DIM] =
+              __float2bfloat16_rn(z);
+        else
+          p.O_part[at + n * MLA_VALUE_DIM] = z;
+      }
     }
-  }
 }
 
 template <int N>
-__global__ void __launch_bounds__(kThreads, 1) mla_partial_fp4_few_kernel(const Fp4Params p) {
+__global__ void __launch_bounds__(Few<N>::kThreads, 1)
+mla_partial_fp4_few_kernel(const Fp4Params p) {
   using F = Few<N>;
-  extern __shared__ uint8_t smem_raw[];
-  typename F::Smem& s = *reinterpret_cast<typename F::Smem*>(
-      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  constexpr int kThreads = F::kThreads;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  if (smem_u32(smem_raw) & 1023) {  // no room to round it up
+    if (threadIdx.x == 0 && p.status) atomicOr(p.status, MLA_STATUS_WAIT_TIMEOUT);
+    return;
+  }
+  typename F::Smem& s = *reinterpret_cast<typename F::Smem*>(smem_raw);
   const int warp = __shfl_sync(kFull, (int)threadIdx.x / 32, 0), lane = threadIdx.x % 32;
   // The stream's next kernel (the LSE combine) may be scheduled from now on;
   // it waits for this grid's completion before it reads a part.
@@ -561,46 +754,61 @@ __global__ void __launch_bounds__(kThreads, 1) mla_partial_fp4_few_kernel(const 
   if (threadIdx.x == 0) {
     s.abort_flag = 0;
     s.last = 0;
-    for (int i = 0; i < kRaw; ++i) {
-      mbar_init(smem_u32(&s.raw_full[i]), 1);
-      mbar_init(smem_u32(&s.raw_empty[i]), 8);
+    for (int i = 0; i < F::kRawFull; ++i) mbar_init(smem_u32(&s.raw_full[i]), 1);
+    mbar_init(smem_u32(&s.raw_empty), kConvWarps);
+    for (int i = 0; i < F::kHalves; ++i) {
+      mbar_init(smem_u32(&s.cfull[i]), kConvWarps);
+      mbar_init(smem_u32(&s.vfree[i]), 1);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < F::kSBufs; ++i) {
       mbar_init(smem_u32(&s.sfull[i]), 1);
-      mbar_init(smem_u32(&s.pready[i]), 4);
-      for (int h = 0; h < 2; ++h) {
-        mbar_init(smem_u32(&s.cfull[i][h]), 8);
-        mbar_init(smem_u32(&s.vfree[i][h]), 1);
-      }
+      mbar_init(smem_u32(&s.sread[i]), 4 * F::kGroups);
     }
+    for (int i = 0; i < F::kPBufs; ++i) {
+      mbar_init(smem_u32(&s.pready[i]), 4 * F::kGroups);
+      mbar_init(smem_u32(&s.odone[i]), 1);
+    }
+    mbar_init(smem_u32(&s.qfull), F::kConv0);
+    mbar_init(smem_u32(&s.rfull), kConvWarps);
     mbar_init(smem_u32(&s.drain), 1);
     fence_mbar_init();
     if (p.seq_lens[w.v] > p.r2t_stride && p.status)
       atomicOr(p.status, MLA_STATUS_BAD_LENGTH);
   }
-  if (warp == 1) {
+  if (warp == F::kMmaWarp) {
     tmem_alloc(smem_u32(&s.tmem_base), F::kCols);
     tmem_relinquish();
   }
-  if (w.npages > 0) place_query<N>(s, p, w, warp, lane);
   fence_proxy_async_smem();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(kFull, s.tmem_base, 0);
 
-  if (w.npages > 0) {
-    if (warp == 0) {
-      copy_pages<N>(s, p, w, lane);
-    } else if (warp == 1) {
-      if (elect_one()) issue_mmas<N>(s, p, w, tmem);
-      __syncwarp();
-    } else if (warp >= 8) {
-      convert<N>(s, p, w, (int)threadIdx.x - 256, lane);
-    } else if (warp >= 4) {
-      softmax<N>(s, p, w, tmem, warp, lane);
+  // The end of every role.  Roles that have split the registers never rejoin.
+  const auto finish = [&]() {
+    if (p.counters) __threadfence();  // this CTA's part before its arrival
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == F::kMmaWarp) tmem_dealloc(tmem, F::kCols);
+    if (!p.counters) return;
+    // Fused combine: the part whose arrival completes the request's count merges
+    // its rows, every part being in memory by then.
+    if (threadIdx.x == 0) {
+      int* c = p.counters + w.b;
+      s.last = atom_add_acq_rel_gpu(c, 1) == p.num_splits * (p.V / p.B) - 1;
+      if (s.last) *c = 0;
     }
-  } else {
+    __syncthreads();
+    if (!s.last) return;
+    __threadfence();
+    for (int r = warp; r < R; r += kThreads / 32)
+      combine_row<true>(p.O_part, p.LSE_part, p.num_splits * (p.V / p.B), (int64_t)p.B * R,
+                        (int64_t)w.b * R + r, p.out, p.lse_out, lane);
+  };
+
+  if (w.npages == 0) {
     // No tokens for this part: O = 0, LSE = -inf.
     const int64_t rows = (int64_t)p.B * R;
     const int64_t part = (int64_t)w.split * (p.V / p.B) + w.shard;
@@ -610,35 +818,33 @@ __global__ void __launch_bounds__(kThreads, 1) mla_partial_fp4_few_kernel(const 
     uint4* dst = reinterpret_cast<uint4*>(
         reinterpret_cast<uint8_t*>(p.O_part) + row0 * MLA_VALUE_DIM * (p.o_bf16 ? 2 : 4));
     for (int k = threadIdx.x; k < words; k += kThreads) dst[k] = make_uint4(0, 0, 0, 0);
+  } else if (warp >= F::kMmaWarp) {
+    if constexpr (F::kGroups == 2)
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsMma));
+    if (!F::kDirect && warp == F::kMmaWarp + 1) copy_pages<N>(s, p, w, lane);
+    if (warp == F::kMmaWarp && elect_one()) issue_mmas<N>(s, p, w, tmem);
+    __syncwarp();
+    if constexpr (F::kGroups == 2) return finish();
+  } else if (warp >= F::kConv0) {
+    convert<N>(s, p, w, warp - F::kConv0, lane);
+    if constexpr (F::kGroups == 2) return finish();
+  } else {
+    if constexpr (F::kGroups == 2)
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+    place_query<N>(s, p, w, warp, lane);
+    softmax<N>(s, p, w, tmem, warp, lane);
+    if constexpr (F::kGroups == 2) return finish();
   }
-  if (p.counters) __threadfence();  // this CTA's part before its arrival
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  if (warp == 1) tmem_dealloc(tmem, F::kCols);
-  if (!p.counters) return;
-  // Fused combine: the part whose arrival completes the request's count merges
-  // its rows, every part being in memory by then.
-  if (threadIdx.x == 0) {
-    int* c = p.counters + w.b;
-    s.last = atom_add_acq_rel_gpu(c, 1) == p.num_splits * (p.V / p.B) - 1;
-    if (s.last) *c = 0;
-  }
-  __syncthreads();
-  if (!s.last) return;
-  __threadfence();
-  for (int r = warp; r < R; r += kThreads / 32)
-    combine_row<true>(p.O_part, p.LSE_part, p.num_splits * (p.V / p.B), (int64_t)p.B * R,
-                      (int64_t)w.b * R + r, p.out, p.lse_out, lane);
+  finish();
 }
 
 template <int N>
 int launch(const Fp4Params& p, int64_t units, cudaStream_t stream) {
   auto kernel = mla_partial_fp4_few_kernel<N>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       Few<N>::kSmemBytes);
+                                       (int)sizeof(typename Few<N>::Smem));
   if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(fp4 few)");
-  kernel<<<(unsigned)units, kThreads, Few<N>::kSmemBytes, stream>>>(p);
+  kernel<<<(unsigned)units, Few<N>::kThreads, (int)sizeof(typename Few<N>::Smem), stream>>>(p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_fail(e, "launch mla_partial_fp4_few_kernel");
   return MLA_OK;
@@ -648,7 +854,11 @@ int launch(const Fp4Params& p, int64_t units, cudaStream_t stream) {
 
 int launch_fp4_few(const Fp4Params& p, cudaStream_t stream) {
   const int64_t units = (int64_t)p.V * p.num_splits;
-  return p.q_len * p.H <= 16 ? launch<16>(p, units, stream) : launch<32>(p, units, stream);
+  const int R = p.q_len * p.H;
+  return R <= 16   ? launch<16>(p, units, stream)
+         : R <= 32 ? launch<32>(p, units, stream)
+         : R <= 64 ? launch<64>(p, units, stream)
+                   : launch<96>(p, units, stream);
 }
 
 }  // namespace mla
