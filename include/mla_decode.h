@@ -99,6 +99,8 @@ typedef enum {
   MLA_KV_FP4_E2M1 = 2
 } mla_kv_dtype;
 #define MLA_FP4_ROW_BYTES 352
+#define MLA_FP4_FEW_ROWS 96      /* query rows a request up to which one CTA serves a part */
+#define MLA_PLAN_FEW_SPLITS 160  /* s_max of the default planners for such requests */
 
 /* Latent row geometry ([VRAM-KV], [K3-MEM]). */
 #define MLA_ROW_DIM 576   /* kv_lora_rank + qk_rope_head_dim */
@@ -175,8 +177,9 @@ int mla_plan_ex(int V, int q_len, int H, int rows_per_unit,
  *   B, num_shards  requests and context shards (V = B * num_shards);
  *   kv_dtype       MLA_KV_BF16, MLA_KV_FP8_E4M3 or MLA_KV_FP4_E2M1 (else
  *                  MLA_ERR_INVALID_ARG); FP4: 256 rows per 4-CTA cluster and
- *                  c0 = 28, or with q_len * H <= 32 one CTA per (request, part):
- *                  slots = the SM count (or num_sms), c0 = 4
+ *                  c0 = 28, or with q_len * H <= MLA_FP4_FEW_ROWS one CTA per
+ *                  (request, part): slots = the SM count (or num_sms), c0 = 4
+ *                  and s_max = MLA_PLAN_FEW_SPLITS
  *   seq_lens_host  host int32 [num_shards * B] (shard-local lengths).
  */
 int mla_plan(int B, int q_len, int H, int num_shards, mla_kv_dtype kv_dtype,
@@ -214,7 +217,8 @@ int mla_plan_parts_ex(int V, int q_len, int H, int rows_per_unit,
 /*
  * mla_plan_parts_ex with mla_plan's defaults (rows per unit and slots of the
  * kernel that serves kv_dtype, s_max = 64, c0 and lam as mla_plan).
- * split_pages_out: HOST int32 buffer of at least num_shards * B * 65 entries.
+ * split_pages_out: HOST int32 buffer of at least num_shards * B * (s_max + 1)
+ * entries.
  */
 int mla_plan_parts(int B, int q_len, int H, int num_shards,
                    mla_kv_dtype kv_dtype, const int32_t* seq_lens_host,
@@ -255,8 +259,8 @@ int mla_plan_sched_ex(int V, int q_len, int H, int rows_per_unit,
 /*
  * mla_plan_sched_ex with mla_plan's defaults (rows per unit and slots of the
  * kernel that serves kv_dtype, s_max = 64, c0 and lam as mla_plan).
- * split_pages_out: HOST int32 [num_shards * B * 65]; work_out: HOST int32
- * [work_capacity], at most num_shards * B * 64 * ceil(q_len * H / 128)
+ * split_pages_out: HOST int32 [num_shards * B * (s_max + 1)]; work_out: HOST
+ * int32 [work_capacity], at most num_shards * B * s_max * ceil(q_len * H / 128)
  * entries are written.
  */
 int mla_plan_sched(int B, int q_len, int H, int num_shards,

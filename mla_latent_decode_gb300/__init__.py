@@ -25,6 +25,8 @@ ROW_DIM, NOPE_DIM, ROPE_DIM, VALUE_DIM, PAGE_SIZE = 576, 512, 64, 512, 64
 KV_BF16, KV_FP8_E4M3, KV_FP4_E2M1 = 0, 1, 2
 _KV_DTYPE = {"bf16": KV_BF16, "fp8_e4m3": KV_FP8_E4M3, "fp4_e2m1": KV_FP4_E2M1}
 FP4_ROW_BYTES = 352  # 512 E2M1 codes, 32 E4M3 block scales, 64 E4M3 RoPE codes
+FP4_FEW_ROWS = 96  # query rows a request up to which one CTA serves a part
+PLAN_FEW_SPLITS = 160  # the default planners' largest split count for such requests
 ROWS_PER_UNIT = 256  # query rows per work unit of the BF16 tensor-core kernel
 STATUS_WAIT_TIMEOUT, STATUS_BAD_LENGTH, STATUS_BAD_SLOT, STATUS_BAD_WORK = 1, 2, 4, 8
 STATUS_BAD_POSITION = 16
@@ -158,6 +160,11 @@ def cluster_slots() -> int:
     return _check(library().mla_cluster_slots())
 
 
+def _s_max(kv_dtype: str, q_len: int, H: int) -> int:
+    """The default planners' largest split count."""
+    return PLAN_FEW_SPLITS if kv_dtype == "fp4_e2m1" and q_len * H <= FP4_FEW_ROWS else 64
+
+
 def plan_heuristic(B: int, q_len: int) -> int:
     """The pages' split rule max(1, min(148 // B // (2 q_len), 32))."""
     return _check(library().mla_plan_heuristic(B, q_len))
@@ -215,7 +222,7 @@ def plan_parts(B: int, q_len: int, H: int, seq_lens, num_shards: int = 1,
     arr = _host_i32(seq_lens)
     V = len(arr)
     assert V == B * num_shards
-    out = (ctypes.c_int32 * (V * 65))()
+    out = (ctypes.c_int32 * (V * (_s_max(kv_dtype, q_len, H) + 1)))()
     S, eff = ctypes.c_int(), ctypes.c_float()
     _check(library().mla_plan_parts(B, q_len, H, num_shards, _KV_DTYPE[kv_dtype],
                                     arr, num_sms, max_parts, out,
@@ -257,8 +264,9 @@ def plan_sched(B: int, q_len: int, H: int, seq_lens, num_shards: int = 1,
     arr = _host_i32(seq_lens)
     V = len(arr)
     assert V == B * num_shards
-    cap = V * 64 * (-(-q_len * H // 128))
-    bnd_out = (ctypes.c_int32 * (V * 65))()
+    s_max = _s_max(kv_dtype, q_len, H)
+    cap = V * s_max * (-(-q_len * H // 128))
+    bnd_out = (ctypes.c_int32 * (V * (s_max + 1)))()
     work_out = (ctypes.c_int32 * cap)()
     S, n, eff = ctypes.c_int(), ctypes.c_int64(), ctypes.c_float()
     _check(library().mla_plan_sched(B, q_len, H, num_shards, _KV_DTYPE[kv_dtype],
@@ -296,15 +304,15 @@ def _check_fp4(q_nope, q_rope, kv, kv_scale, req_to_token, seq_lens) -> None:
     the other formats' by shape, so a wrong one is refused here)."""
     B, q_len, H, _ = q_nope.shape
     for t, name, width in ((q_nope, "q_nope", NOPE_DIM), (q_rope, "q_rope", ROPE_DIM)):
-        if t.dtype != torch.bfloat16 or t.shape != (B, q_len, H, width) or not t.is_contiguous():
+        if t.dtype is not torch.bfloat16 or t.numel() != B * q_len * H * width or not t.is_contiguous():
             raise ValueError(f"{name}: expected contiguous bfloat16 {[B, q_len, H, width]}, got "
                              f"{t.dtype} {tuple(t.shape)} with strides {t.stride()}")
     if kv.dim() != 2 or not kv.is_contiguous():
         raise ValueError(f"kv: expected a contiguous [num_slots, {FP4_ROW_BYTES}] pool")
-    if kv_scale is None or kv_scale.dtype != torch.float32 or kv_scale.numel() < 1:
+    if kv_scale is None or kv_scale.dtype is not torch.float32 or kv_scale.numel() < 1:
         raise ValueError("kv_scale: expected one float32 value, the pool's factor")
-    if req_to_token.dtype != torch.int32 or req_to_token.stride(1) != 1 or \
-            seq_lens.dtype != torch.int32 or not seq_lens.is_contiguous():
+    if req_to_token.dtype is not torch.int32 or req_to_token.stride(1) != 1 or \
+            seq_lens.dtype is not torch.int32 or not seq_lens.is_contiguous():
         raise ValueError("req_to_token, seq_lens: expected int32 with contiguous rows")
 
 

@@ -121,6 +121,10 @@ static bool few_rows(mla_kv_dtype kv_dtype, int q_len, int H) {
   return kv_dtype == MLA_KV_FP4_E2M1 && (int64_t)q_len * H <= kFp4FewRows;
 }
 
+// Largest split count the default planners consider.  Few rows: enough for one
+// request to reach every SM.
+static int plan_s_max(bool few) { return few ? MLA_PLAN_FEW_SPLITS : 64; }
+
 static double plan_unit_cost(mla_kv_dtype kv_dtype, bool few) {
   if (few) return kPlanUnitCostFew;
   return kv_dtype == MLA_KV_FP4_E2M1   ? kPlanUnitCostFp4
@@ -277,7 +281,7 @@ int mla_plan(int B, int q_len, int H, int num_shards, mla_kv_dtype kv_dtype,
   if (slots < 0) return slots;
   return mla_plan_ex(B * num_shards, q_len, H,
                      fp8 ? MLA_ROWS_PER_UNIT / 2 : MLA_ROWS_PER_UNIT,
-                     seq_lens_host, slots, 64,
+                     seq_lens_host, slots, plan_s_max(few_rows(kv_dtype, q_len, H)),
                      plan_unit_cost(kv_dtype, few_rows(kv_dtype, q_len, H)), kPlanSplitCost,
                      num_splits_out, wave_eff_out, nullptr);
 }
@@ -532,7 +536,8 @@ int mla_plan_parts(int B, int q_len, int H, int num_shards,
   return mla_plan_parts_ex(B * num_shards, q_len, H,
                            kv_dtype == MLA_KV_FP8_E4M3 ? MLA_ROWS_PER_UNIT / 2
                                                        : MLA_ROWS_PER_UNIT,
-                           seq_lens_host, slots, 64, max_parts,
+                           seq_lens_host, slots, plan_s_max(few_rows(kv_dtype, q_len, H)),
+                           max_parts,
                            plan_unit_cost(kv_dtype, few_rows(kv_dtype, q_len, H)),
                            kPlanSplitCost, split_pages_out, num_parts_out,
                            wave_eff_out, nullptr);
@@ -553,7 +558,8 @@ int mla_plan_sched(int B, int q_len, int H, int num_shards,
   return mla_plan_sched_ex(B * num_shards, q_len, H,
                            kv_dtype == MLA_KV_FP8_E4M3 ? MLA_ROWS_PER_UNIT / 2
                                                        : MLA_ROWS_PER_UNIT,
-                           seq_lens_host, slots, 64, max_parts,
+                           seq_lens_host, slots, plan_s_max(few_rows(kv_dtype, q_len, H)),
+                           max_parts,
                            plan_unit_cost(kv_dtype, few_rows(kv_dtype, q_len, H)),
                            kPlanSplitCost, split_pages_out, num_parts_out,
                            work_out, work_capacity, num_work_out, wave_eff_out,

@@ -95,7 +95,7 @@ int launch_simt(const DecodeArgs& a);
 int launch_tc(const DecodeArgs& a);       // BF16 KV: 4-CTA clusters
 int launch_tc_fp8(const DecodeArgs& a);   // E4M3 KV: 2-CTA clusters
 int launch_fp4(const DecodeArgs& a);      // E2M1 KV: 4-CTA clusters, or
-constexpr int kFp4FewRows = 96;           // single CTAs up to this many rows
+constexpr int kFp4FewRows = MLA_FP4_FEW_ROWS;  // single CTAs up to this many rows
 int pair_slots_fp8();                     // resident 2-CTA clusters (FP8)
 
 }  // namespace mla

@@ -151,3 +151,13 @@ def test_reference_formats():
     row = decode4(kv, 2.0)
     assert row[1, 0] == 2.0 * E2M1[kv[1, 0] & 7] * (-1 if kv[1, 0] & 8 else 1) * e4m3_values(kv[1, 256])
     assert row[2, 575] == 2.0 * e4m3_values(kv[2, 351])
+
+
+@pytest.mark.parametrize("H,L,wide", [(16, 100000, True), (96, 100000, True), (97, 100000, False), (16, 64, False)])
+def test_plan_spreads_one_request_over_every_sm(H, L, wide):
+    """One CTA per part up to 96 rows, so up to 160 parts; clusters stay at 64."""
+    S, bnd, work, _ = mla.plan_sched(1, 1, H, [L], num_sms=152, kv_dtype="fp4_e2m1")
+    assert (S > 64) == wide and S <= 160
+    assert bnd.shape == (1, S + 1) and bnd[0, 0] == 0 and bnd[0, -1] == -(-L // 64) and (np.diff(bnd[0]) >= 0).all()
+    assert sorted(work) == list(range(S))
+    assert mla.plan_parts(1, 1, H, [L], num_sms=152, kv_dtype="fp4_e2m1")[0] <= 160
