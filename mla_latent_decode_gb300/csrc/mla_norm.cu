@@ -51,6 +51,7 @@ struct NormParams {
   float* scales;
   int64_t scales_stride;
   int group;  // 0: one scale per row
+  int shift;  // kShift: values from a vector's boundary to row 0
 };
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
@@ -93,31 +94,40 @@ __device__ __forceinline__ uint32_t word(const uint4& u, int k) {
   return k == 0 ? u.x : k == 1 ? u.y : k == 2 ? u.z : u.w;
 }
 
-// Eight bf16 values from column c0 on as packed pairs; columns past d read as 0.
-template <bool VEC>
+// How a row's eight values lie: kAny element by element; kVec on whole vectors;
+// kShift on whole vectors but for the row's two ends.
+enum Lay { kAny, kVec, kShift };
+template <int L>
+__device__ __forceinline__ bool whole(int c0, int d) {
+  return L == kVec || (L == kShift && c0 >= 0 && c0 + 8 <= d);
+}
+
+// Eight bf16 values from column c0 on as packed pairs; columns outside 0 .. d - 1
+// read as 0.
+template <int L>
 __device__ __forceinline__ uint4 load8(const __nv_bfloat16* row, int c0, int d) {
-  if (VEC) return *reinterpret_cast<const uint4*>(row + c0);
+  if (whole<L>(c0, d)) return *reinterpret_cast<const uint4*>(row + c0);
   const uint16_t* r = reinterpret_cast<const uint16_t*>(row);
   uint32_t w[4];
 #pragma unroll
   for (int k = 0; k < 4; ++k)
-    w[k] = (c0 + 2 * k < d ? r[c0 + 2 * k] : 0u) |
-           ((c0 + 2 * k + 1 < d ? r[c0 + 2 * k + 1] : 0u) << 16);
+    w[k] = ((unsigned)(c0 + 2 * k) < (unsigned)d ? r[c0 + 2 * k] : 0u) |
+           (((unsigned)(c0 + 2 * k + 1) < (unsigned)d ? r[c0 + 2 * k + 1] : 0u) << 16);
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
-template <bool VEC>
+template <int L>
 __device__ __forceinline__ void store8(__nv_bfloat16* row, int c0, int d,
                                        const uint64_t (&v)[4]) {
   uint32_t w[4];
 #pragma unroll
   for (int k = 0; k < 4; ++k) w[k] = pack_bf16(both(v[k]).x, both(v[k]).y);
-  if (VEC) {
+  if (whole<L>(c0, d)) {
     *reinterpret_cast<uint4*>(row + c0) = make_uint4(w[0], w[1], w[2], w[3]);
   } else {
     uint16_t* r = reinterpret_cast<uint16_t*>(row);
 #pragma unroll
     for (int k = 0; k < 8; ++k)
-      if (c0 + k < d) r[c0 + k] = (uint16_t)(w[k / 2] >> (16 * (k & 1)));
+      if ((unsigned)(c0 + k) < (unsigned)d) r[c0 + k] = (uint16_t)(w[k / 2] >> (16 * (k & 1)));
   }
 }
 
@@ -139,21 +149,28 @@ __device__ __forceinline__ float block_reduce(float v, float* part) {
   return reduce(lane < warps ? part[lane] : 0.f);
 }
 
-// VEC: d and every stride are multiples of 8 and every pointer is aligned to
-// its vector, so whole vectors are in range or out of it.
-template <int V, bool VEC, int T>
+// kVec: d and every stride are multiples of 8 and every pointer is aligned to
+// its vector, so whole vectors are in range or out of it.  kShift (one scale per
+// row): the arrays' rows are as far from a vector's boundary as each other's, up
+// to seven values and changing from row to row, as with an odd d; the vectors
+// start on the boundary before the row and the weight, which does not shift with
+// it, is read by element (6000 x 7001: 72 us, every array by element 152).
+template <int V, int L, int T>
 __global__ void __launch_bounds__(T, T == 256 && V == 4 ? 4 : 1) mla_norm_kernel(const NormParams p) {
   __shared__ float part[3][32];
   const int64_t r = blockIdx.x;
-  const auto col = [&](int k) { return 8 * (k * (int)blockDim.x + (int)threadIdx.x); };
+  const int shift = L == kShift ? (int)((p.shift + r * p.x_stride) & 7) : 0;
+  const auto col = [&](int k) {
+    return 8 * (k * (int)blockDim.x + (int)threadIdx.x) - shift;
+  };
   uint4 x[V], q[V], w[V];  // all loads of the row in flight together
 #pragma unroll
   for (int k = 0; k < V; ++k) {
     x[k] = q[k] = w[k] = make_uint4(0, 0, 0, 0);
     if (col(k) < p.d) {
-      x[k] = load8<VEC>(p.x + r * p.x_stride, col(k), p.d);
-      if (p.res) q[k] = load8<VEC>(p.res + r * p.res_stride, col(k), p.d);
-      w[k] = load8<VEC>(p.w, col(k), p.d);
+      x[k] = load8<L>(p.x + r * p.x_stride, col(k), p.d);
+      if (p.res) q[k] = load8<L>(p.res + r * p.res_stride, col(k), p.d);
+      w[k] = load8<L == kVec ? kVec : kAny>(p.w, col(k), p.d);
     }
   }
   uint64_t h[V][4], acc = pair(0.f, 0.f);
@@ -183,7 +200,7 @@ __global__ void __launch_bounds__(T, T == 256 && V == 4 ? 4 : 1) mla_norm_kernel
   if (p.res_out) {
 #pragma unroll
     for (int k = 0; k < V; ++k)
-      if (col(k) < p.d) store8<VEC>(p.res_out + r * p.res_out_stride, col(k), p.d, h[k]);
+      if (col(k) < p.d) store8<L>(p.res_out + r * p.res_out_stride, col(k), p.d, h[k]);
   }
   const float rs = 1.0f / sqrtf(mean + p.eps);
   const uint64_t rs2 = pair(rs, rs);
@@ -196,7 +213,7 @@ __global__ void __launch_bounds__(T, T == 256 && V == 4 ? 4 : 1) mla_norm_kernel
       h[k][e] = mul2(h[k][e], mul2(rs2, widen(word(w[k], e))));
       amax[k] = fmaxf(amax[k], fmaxf(fabsf(both(h[k][e]).x), fabsf(both(h[k][e]).y)));
     }
-    if (p.out && col(k) < p.d) store8<VEC>(p.out + r * p.out_stride, col(k), p.d, h[k]);
+    if (p.out && col(k) < p.d) store8<L>(p.out + r * p.out_stride, col(k), p.d, h[k]);
     rowmax = fmaxf(rowmax, amax[k]);
   }
   if (!p.out8) return;
@@ -212,7 +229,7 @@ __global__ void __launch_bounds__(T, T == 256 && V == 4 ? 4 : 1) mla_norm_kernel
     const int c0 = col(k);
     if (c0 >= p.d) continue;
     const float s = __fdiv_rn(amax[k], 448.0f);
-    if (p.group ? c0 % p.group == 0 : c0 == 0)
+    if (p.group ? c0 % p.group == 0 : k == 0 && threadIdx.x == 0)
       p.scales[r * p.scales_stride + (p.group ? c0 / p.group : 0)] = s;
     uint32_t c8[4];
     if (s > 0x1p-90f) {
@@ -231,31 +248,31 @@ __global__ void __launch_bounds__(T, T == 256 && V == 4 ? 4 : 1) mla_norm_kernel
       }
     }
     uint8_t* dst = p.out8 + r * p.out8_stride + c0;
-    if (VEC) {
+    if (whole<L>(c0, p.d)) {
       *reinterpret_cast<uint2*>(dst) = make_uint2(c8[0] | (c8[1] << 16), c8[2] | (c8[3] << 16));
     } else {
 #pragma unroll
       for (int e = 0; e < 8; ++e)
-        if (c0 + e < p.d) dst[e] = (uint8_t)(c8[e / 2] >> (8 * (e & 1)));
+        if ((unsigned)(c0 + e) < (unsigned)p.d) dst[e] = (uint8_t)(c8[e / 2] >> (8 * (e & 1)));
     }
   }
 }
 
-template <bool VEC>
+template <int L>
 void launch(const NormParams& p, int64_t n, int sms, cudaStream_t st) {
   const unsigned grid = (unsigned)n;
-  const int vectors = (p.d + 7) / 8;
+  const int vectors = (p.d + (L == kShift ? 7 : 0) + 7) / 8;
   const auto threads = [&](int v) { return ((vectors + v - 1) / v + 31) / 32 * 32; };
   if (n > 2 * sms && vectors > 512 && vectors <= 1024)
-    mla_norm_kernel<4, VEC, 256><<<grid, threads(4), 0, st>>>(p);
+    mla_norm_kernel<4, L, 256><<<grid, threads(4), 0, st>>>(p);
   else if (n > 2 * sms && vectors > 256 && vectors <= 512)
-    mla_norm_kernel<2, VEC, 256><<<grid, threads(2), 0, st>>>(p);
+    mla_norm_kernel<2, L, 256><<<grid, threads(2), 0, st>>>(p);
   else if (vectors <= 1024)
-    mla_norm_kernel<1, VEC, 1024><<<grid, threads(1), 0, st>>>(p);
+    mla_norm_kernel<1, L, 1024><<<grid, threads(1), 0, st>>>(p);
   else if (vectors <= 2048)
-    mla_norm_kernel<2, VEC, 1024><<<grid, threads(2), 0, st>>>(p);
+    mla_norm_kernel<2, L, 1024><<<grid, threads(2), 0, st>>>(p);
   else
-    mla_norm_kernel<4, VEC, 1024><<<grid, threads(4), 0, st>>>(p);
+    mla_norm_kernel<4, L, 1024><<<grid, threads(4), 0, st>>>(p);
 }
 
 }  // namespace
@@ -297,7 +314,8 @@ extern "C" int mla_add_rms_norm(const void* x, int64_t x_stride, const void* res
   if (x_stride < d || (residual && (residual_stride < d || residual_out_stride < d)) ||
       (out && out_stride < d) || (out8 && (out8_stride < d || scales_stride < nscales)))
     return fail(MLA_ERR_INVALID_ARG, "mla_add_rms_norm: a row stride is shorter than its row");
-  if (!aligned(x, 2) || !aligned(weight, 2) || (residual && (!aligned(residual, 2) || !aligned(residual_out, 2))) ||
+  if (!aligned(x, 2) || !aligned(weight, 2) ||
+      (residual && (!aligned(residual, 2) || !aligned(residual_out, 2))) ||
       (out && !aligned(out, 2)) || (out8 && !aligned(scales, 4)))
     return fail(MLA_ERR_MISALIGNED,
                 "mla_add_rms_norm: bf16 arrays need 2-B alignment, scales 4-B");
@@ -325,15 +343,29 @@ extern "C" int mla_add_rms_norm(const void* x, int64_t x_stride, const void* res
                      aligned(residual, 16) && aligned(residual_out, 16))) &&
       (!out || (out_stride % 8 == 0 && aligned(out, 16))) &&
       (!out8 || (out8_stride % 8 == 0 && aligned(out8, 8)));
+  // Rows that are off that boundary by the same number of values in every array.
+  const auto off = [](const void* a, int bytes) {
+    return (int)((reinterpret_cast<uintptr_t>(a) / bytes) & 7);
+  };
+  const auto like_x = [&](const void* a, int64_t stride, int bytes) {
+    return !a || (stride % 8 == x_stride % 8 && off(a, bytes) == off(x, 2));
+  };
+  const bool shifted = group == 0 && d + 7 <= 8 * kMaxVec * kMaxThreads &&
+                       like_x(residual, residual_stride, 2) &&
+                       like_x(residual_out, residual_out_stride, 2) &&
+                       like_x(out, out_stride, 2) && like_x(out8, out8_stride, 1);
+  p.shift = off(x, 2);
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess)
     e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return cuda_fail(e, "mla_add_rms_norm: device query");
   if (vec8)
-    launch<true>(p, n, sms, (cudaStream_t)stream);
+    launch<kVec>(p, n, sms, (cudaStream_t)stream);
+  else if (shifted)
+    launch<kShift>(p, n, sms, (cudaStream_t)stream);
   else
-    launch<false>(p, n, sms, (cudaStream_t)stream);
+    launch<kAny>(p, n, sms, (cudaStream_t)stream);
   e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_fail(e, "launch mla_norm_kernel");
   return MLA_OK;

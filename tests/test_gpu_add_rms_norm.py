@@ -108,3 +108,27 @@ def test_many_rows():
     x, w = _rows(n, d, 10), _rows(1, d, 11)[0].contiguous()
     got = mla.add_rms_norm(x, w, None, e4m3=True, out=torch.empty_like(x), group=32)
     _check(x, None, w, 1e-6, got)
+
+
+@pytest.mark.parametrize("n,d", [(9, 1), (17, 7), (16, 9), (700, 1531), (700, 5003), (400, 7001), (3, 32761), (2, 32759)])
+@pytest.mark.parametrize("off", [0, 3])
+def test_rows_shifted_alike(n, d, off):
+    """Odd lengths: every row at another distance from a vector's boundary, the
+    same in all arrays, and nothing written outside the rows."""
+    def frame(k, dtype):
+        flat = torch.zeros(off + n * d + 16, dtype=dtype, device="cuda")
+        if k is not None:
+            flat[off:off + n * d] = _rows(1, n * d, k)[0]
+        return flat, flat[off:off + n * d].view(n, d)
+
+    (_, x), (_, res), w = frame(20, torch.bfloat16), frame(21, torch.bfloat16), _rows(1, d, 22)[0].contiguous()
+    keep = res.clone()
+    flat, out = frame(None, torch.bfloat16)
+    flat8, out8 = frame(None, torch.uint8)
+    got = mla.add_rms_norm(x, w, res, out=out, out8=out8)
+    _check(x, keep, w, 1e-6, got)
+    for t in (flat, flat8):
+        assert int((t[:off] != 0).sum()) == 0 and int((t[off + n * d:] != 0).sum()) == 0
+    # arrays that are not shifted alike
+    other = torch.zeros(n * d + 1, dtype=torch.bfloat16, device="cuda")[1:].view(n, d)
+    _check(x, keep, w, 1e-6, mla.add_rms_norm(x, w, keep.clone(), out=other, e4m3=True))
