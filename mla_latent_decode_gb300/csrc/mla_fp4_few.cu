@@ -87,7 +87,7 @@ struct Few {
                                 // the factors of a rescale and, last, g / l
     uint64_t raw_full[kRawFull];   // a raw page has landed
     uint64_t raw_empty;            // the converter warps have read it
-    uint64_t qfull;             // the query rows are written (softmax warps)
+    uint64_t qfull;             // the query rows are written
     uint64_t cfull[kHalves];    // a half page is written (8 warps)
     uint64_t rfull;             // a page's RoPE key is written (8 warps)
     uint64_t vfree[kHalves];    // the outputs' products have read it
@@ -146,72 +146,67 @@ __device__ __forceinline__ bool any_of(bool x) {
   return r != 0;
 }
 
-// The query rows, by the softmax warps while the first page arrives: warp k rows
-// k, k + kConv0, ..., four rows' loads in flight.  q 2^(14 - e) as f16 into the
-// K-major operand boxes; rows past R become zeros that see nothing.
+// The query rows, by the softmax and the converter warps while the first page
+// arrives: warp k rows k, k + kQWarps, ..., their loads in flight together.
+// q 2^(14 - e) as f16 into the K-major operand boxes; rows past R become zeros
+// that see nothing.
 template <int N>
 __device__ __forceinline__ void place_query(typename Few<N>::Smem& s, const Fp4Params& p,
                                             const UnitRange& w, int warp, int lane) {
-  constexpr int kWarps = Few<N>::kConv0, kBatch = N / kWarps < 4 ? N / kWarps : 4;
-  static_assert(N % (kWarps * kBatch) == 0, "rows of a warp");
+  constexpr int kWarps = Few<N>::kMmaWarp, kRows = (N + kWarps - 1) / kWarps;
   const int R = p.q_len * p.H;
-#pragma unroll 1
-  for (int n0 = warp; n0 < N; n0 += kWarps * kBatch) {
-    uint4 x[kBatch][3];
+  const float g = p.g[0];
+  uint4 x[kRows][3];
 #pragma unroll
-    for (int r = 0; r < kBatch; ++r) {
-      const int n = n0 + kWarps * r;
-      const int64_t row = (int64_t)w.b * R + n;
+  for (int r = 0; r < kRows; ++r) {
+    const int n = warp + kWarps * r;
+    const int64_t row = (int64_t)w.b * R + n;
 #pragma unroll
-      for (int k = 0; k < 3; ++k) {
-        const int c = lane + 32 * k;  // 16-byte chunk of the row's 72
-        x[r][k] = make_uint4(0, 0, 0, 0);
-        if (n < R && c < 72)
-          x[r][k] = c < 64 ? p.q_nope[row * 64 + c] : p.q_rope[row * 8 + c - 64];
-      }
+    for (int k = 0; k < 3; ++k) {
+      const int c = lane + 32 * k;  // 16-byte chunk of the row's 72
+      x[r][k] = make_uint4(0, 0, 0, 0);
+      if (n < R && c < 72) x[r][k] = c < 64 ? p.q_nope[row * 64 + c] : p.q_rope[row * 8 + c - 64];
     }
+  }
+  float mine = 0.f;  // lane r: 2^(e - 14) of the warp's row r
 #pragma unroll
-    for (int r = 0; r < kBatch; ++r) {
-      const int n = n0 + kWarps * r;
-      uint32_t big = 0;
+  for (int r = 0; r < kRows; ++r) {
+    const int n = warp + kWarps * r;
+    uint32_t big2 = 0;
 #pragma unroll
-      for (int k = 0; k < 3; ++k) {
-        const uint32_t y[4] = {x[r][k].x, x[r][k].y, x[r][k].z, x[r][k].w};
+    for (int k = 0; k < 3; ++k)
+      big2 = __vmaxu2(big2, __vmaxu2(__vmaxu2(x[r][k].x & 0x7FFF7FFFu, x[r][k].y & 0x7FFF7FFFu),
+                                     __vmaxu2(x[r][k].z & 0x7FFF7FFFu, x[r][k].w & 0x7FFF7FFFu)));
+    const uint32_t big = __reduce_max_sync(kFull, max(big2 & 0xFFFFu, big2 >> 16));
+    const int e = max(min((int)(big >> 7), 254) - 127, -100);
+    const float up = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
+    const auto conv = [&](uint32_t v) -> uint32_t {
+      return pack_f16(__uint_as_float(v << 16) * up, __uint_as_float(v & 0xFFFF0000u) * up);
+    };
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          big = max(big, max(y[e] & 0x7FFFu, (y[e] >> 16) & 0x7FFFu));
-      }
-      big = __reduce_max_sync(kFull, big);
-      const int e = max(min((int)(big >> 7), 254) - 127, -100);
-      const float up = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
-      const auto conv = [&](uint32_t v) -> uint32_t {
-        return pack_f16(__uint_as_float(v << 16) * up, __uint_as_float(v & 0xFFFF0000u) * up);
-      };
-#pragma unroll
-      for (int k = 0; k < 3; ++k) {
-        const int c = lane + 32 * k;
-        if (c < 72)
-          *reinterpret_cast<uint4*>(s.q[c >> 3] + (n >> 3) * 1024 + (n & 7) * 128 +
-                                    (((c & 7) ^ (n & 7)) << 4)) =
-              make_uint4(conv(x[r][k].x), conv(x[r][k].y), conv(x[r][k].z), conv(x[r][k].w));
-      }
-      if (lane == 0) {
-        const int i = n / p.H;
-        int64_t lim = 0;
-        if (n < R) {
-          lim = p.kv_limit ? (int64_t)p.kv_limit[(int64_t)w.v * p.q_len + i]
-                           : w.L - p.q_len + 1 + i;
-          lim = lim > w.L ? w.L : (lim < 0 ? 0 : lim);
-        }
-        s.lim[n] = (int32_t)lim;
-        s.sc[n] = p.scale_log2 * p.g[0] * __uint_as_float((uint32_t)(127 + e - 14) << 23);
-        s.mref[n] = -INFINITY;
-      }
+    for (int k = 0; k < 3; ++k) {
+      const int c = lane + 32 * k;
+      if (n < N && c < 72)
+        *reinterpret_cast<uint4*>(s.q[c >> 3] + (n >> 3) * 1024 + (n & 7) * 128 +
+                                  (((c & 7) ^ (n & 7)) << 4)) =
+            make_uint4(conv(x[r][k].x), conv(x[r][k].y), conv(x[r][k].z), conv(x[r][k].w));
     }
+    if (lane == r) mine = __uint_as_float((uint32_t)(127 + e - 14) << 23);
+  }
+  const int n = warp + kWarps * lane;
+  if (lane < kRows && n < N) {
+    const int i = n / p.H;
+    int64_t lim = 0;
+    if (n < R) {
+      lim = p.kv_limit ? (int64_t)p.kv_limit[(int64_t)w.v * p.q_len + i] : w.L - p.q_len + 1 + i;
+      lim = lim > w.L ? w.L : (lim < 0 ? 0 : lim);
+    }
+    s.lim[n] = (int32_t)lim;
+    s.sc[n] = p.scale_log2 * g * mine;
+    s.mref[n] = -INFINITY;
   }
   __syncwarp();
   if (lane == 0) mbar_arrive(smem_u32(&s.qfull));
-  named_bar_sync(2, 32 * kWarps);  // lim, sc and mref are read by every warp
 }
 
 // A position in the ring of half pages and the times it has wrapped round.
@@ -364,6 +359,7 @@ __device__ __forceinline__ void convert(typename Few<N>::Smem& s, const Fp4Param
     next.read<true>(p.kv + ((int64_t)base + 8 * warp) * kFp4RowBytes, t4, v, rt, lane);
   };
   if constexpr (F::kDirect) load(0);
+  place_query<N>(s, p, w, F::kConv0 + warp, lane);
   for (int m = 0; m < w.npages; ++m) {
     RawShare x;
     if constexpr (F::kDirect) {
@@ -571,7 +567,8 @@ __device__ __forceinline__ void softmax(typename Few<N>::Smem& s, const Fp4Param
   const uint32_t trow = tmem + ((uint32_t)(quad * 32) << 16);
   const int R = p.q_len * p.H;
   float* const alpha = s.wred[0];
-  bool ok = true;
+  place_query<N>(s, p, w, warp, lane);
+  bool ok = mbar_wait_cta(smem_u32(&s.qfull), 0, &s.abort_flag);
   float l[H];
 #pragma unroll
   for (int k = 0; k < H; ++k) l[k] = 0.f;
@@ -768,7 +765,7 @@ mla_partial_fp4_few_kernel(const Fp4Params p) {
       mbar_init(smem_u32(&s.pready[i]), 4 * F::kGroups);
       mbar_init(smem_u32(&s.odone[i]), 1);
     }
-    mbar_init(smem_u32(&s.qfull), F::kConv0);
+    mbar_init(smem_u32(&s.qfull), F::kMmaWarp);
     mbar_init(smem_u32(&s.rfull), kConvWarps);
     mbar_init(smem_u32(&s.drain), 1);
     fence_mbar_init();
@@ -831,7 +828,6 @@ mla_partial_fp4_few_kernel(const Fp4Params p) {
   } else {
     if constexpr (F::kGroups == 2)
       asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
-    place_query<N>(s, p, w, warp, lane);
     softmax<N>(s, p, w, tmem, warp, lane);
     if constexpr (F::kGroups == 2) return finish();
   }
