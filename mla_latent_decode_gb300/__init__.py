@@ -128,6 +128,11 @@ _HERE_ALREADY = contextlib.nullcontext()
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
+# torch.cuda.current_device() without its test for a first use of CUDA, which a
+# CUDA tensor has behind it (0.3 us of host time against 0.1)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
 def _on(t: torch.Tensor):
     """Make the tensor's device current for a call: the library launches
     on (and looks up per-device state for) the current device."""
@@ -142,6 +147,17 @@ def _stream(stream: Optional[torch.cuda.Stream]):
     if _raw_stream is not None:
         return _raw_stream(torch.cuda.current_device())
     return torch.cuda.current_stream().cuda_stream
+
+
+def _launch(t: torch.Tensor, stream: Optional[torch.cuda.Stream], fn, *args) -> None:
+    """fn(*args, stream) on the tensor's device; raises what it returns."""
+    if t.is_cuda and _raw_stream is not None and t.device.index == (dev := _current_device()):
+        rc = fn(*args, _raw_stream(dev) if stream is None else stream.cuda_stream)
+    else:
+        with _on(t):
+            rc = fn(*args, _stream(stream))
+    if rc < 0:
+        _check(rc)
 
 
 def _host_i32(x) -> "ctypes.Array":
@@ -302,12 +318,14 @@ def _kv_dtype(kv: torch.Tensor) -> int:
 def _check_fp4(q_nope, q_rope, kv, kv_scale, req_to_token, seq_lens) -> None:
     """The layouts the FP4 decode reads (its pool and its queries are told from
     the other formats' by shape, so a wrong one is refused here)."""
-    B, q_len, H, _ = q_nope.shape
-    for t, name, width in ((q_nope, "q_nope", NOPE_DIM), (q_rope, "q_rope", ROPE_DIM)):
-        if t.dtype is not torch.bfloat16 or t.numel() != B * q_len * H * width or not t.is_contiguous():
-            raise ValueError(f"{name}: expected contiguous bfloat16 {[B, q_len, H, width]}, got "
-                             f"{t.dtype} {tuple(t.shape)} with strides {t.stride()}")
-    if kv.dim() != 2 or not kv.is_contiguous():
+    rows = q_nope.numel() // NOPE_DIM
+    if q_nope.dtype is not torch.bfloat16 or q_nope.shape[3] != NOPE_DIM or not q_nope.is_contiguous():
+        raise ValueError("q_nope: expected contiguous bfloat16 [B, q_len, H, 512], got "
+                         f"{q_nope.dtype} {tuple(q_nope.shape)} with strides {q_nope.stride()}")
+    if q_rope.dtype is not torch.bfloat16 or q_rope.numel() != rows * ROPE_DIM or not q_rope.is_contiguous():
+        raise ValueError("q_rope: expected contiguous bfloat16 [B, q_len, H, 64], got "
+                         f"{q_rope.dtype} {tuple(q_rope.shape)} with strides {q_rope.stride()}")
+    if not kv.is_contiguous() or kv.dim() != 2:
         raise ValueError(f"kv: expected a contiguous [num_slots, {FP4_ROW_BYTES}] pool")
     if kv_scale is None or kv_scale.dtype is not torch.float32 or kv_scale.numel() < 1:
         raise ValueError("kv_scale: expected one float32 value, the pool's factor")
@@ -345,22 +363,21 @@ def decode_partial(q_nope, q_rope, kv, kv_scale, req_to_token, seq_lens,
     if LSE_part is None:
         LSE_part = torch.empty((num_splits, num_shards, B, q_len, H),
                                dtype=torch.float32, device=dev)
-    args = (_ptr(q_nope), _ptr(q_rope), _ptr(kv), _ptr(kv_scale),
-            kind, kv.shape[0], _ptr(req_to_token),
-            req_to_token.stride(0), _ptr(seq_lens), _ptr(kv_limit), B, q_len,
+    args = (q_nope.data_ptr(), q_rope.data_ptr(), kv.data_ptr(), _ptr(kv_scale),
+            kind, kv.shape[0], req_to_token.data_ptr(),
+            req_to_token.stride(0), seq_lens.data_ptr(), _ptr(kv_limit), B, q_len,
             H, num_shards, PAGE_SIZE, float(sm_scale), num_splits,
             _ptr(split_pages))
-    with _on(q_nope):
-        tail = (_ptr(O_part), _ptr(LSE_part), _ptr(status), _stream(stream))
-        if simt:
-            if work is not None or bf16_parts:
-                raise ValueError("the CUDA-core path takes no work list and "
-                                 "writes fp32 parts")
-            _check(library().mla_decode_partial_simt(*args, *tail))
-        else:
-            fn = (library().mla_decode_partial_bf16_parts if bf16_parts
-                  else library().mla_decode_partial)
-            _check(fn(*args, _ptr(work), 0 if work is None else work.numel(), *tail))
+    tail = (O_part.data_ptr(), LSE_part.data_ptr(), _ptr(status))
+    if simt:
+        if work is not None or bf16_parts:
+            raise ValueError("the CUDA-core path takes no work list and "
+                             "writes fp32 parts")
+        _launch(q_nope, stream, library().mla_decode_partial_simt, *args, *tail)
+    else:
+        fn = (library().mla_decode_partial_bf16_parts if bf16_parts
+              else library().mla_decode_partial)
+        _launch(q_nope, stream, fn, *args, _ptr(work), 0 if work is None else work.numel(), *tail)
     return O_part, LSE_part
 
 
@@ -454,14 +471,14 @@ def _rows_arg(t: torch.Tensor, name: str, n: int, width: int, dtype=torch.bfloat
     """A 2-D argument of n rows of `width` contiguous values (any row stride):
     its address and row stride."""
     shape, stride = t.shape, t.stride()
-    if t.dtype != dtype or shape != (n, width) or (stride[1] != 1 and width > 1):
+    if t.dtype is not dtype or shape != (n, width) or (stride[1] != 1 and width > 1):
         raise ValueError(f"{name}: expected {dtype} [{n}, {width}] with contiguous rows, "
                          f"got {t.dtype} {tuple(shape)} with strides {stride}")
     return t.data_ptr(), stride[0] if n > 1 else max(stride[0], width)
 
 
 def _int32_arg(t: torch.Tensor, name: str, n: int):
-    if t.dtype != torch.int32 or t.numel() != n or not t.is_contiguous():
+    if t.dtype is not torch.int32 or t.numel() != n or not t.is_contiguous():
         raise ValueError(f"{name}: expected {n} contiguous int32 values, got {t.dtype} "
                          f"{tuple(t.shape)}")
     return t.data_ptr()
@@ -519,11 +536,10 @@ def kv_append(rows, slots, positions, cos_sin, kv, kv_scale=None, norm_weight=No
         H = shape[1]
         q_args = (q_rope.data_ptr(), qs[0], qs[1], q_out.data_ptr(), os_[0], os_[1])
     slots_ptr, pos_ptr = _int32_arg(slots, "slots", n), _int32_arg(positions, "positions", n)
-    with _on(rows):
-        _check(library().mla_kv_append(
+    _launch(rows, stream, library().mla_kv_append,
             row_ptr, row_stride, n, weight_ptr, eps, slots_ptr, pos_ptr, cos_sin.data_ptr(),
             max_pos, 1 if interleaved else 0, kv_ptr, kind, scale_ptr, num_slots, *q_args, H,
-            _ptr(status), _stream(stream)))
+            _ptr(status))
     return q_out if q_rope is not None else None
 
 
@@ -535,10 +551,8 @@ def kv_read(kv, slots, kv_scale=None, out=None, status=None, stream=None):
     if out is None:
         out = torch.empty((n, ROW_DIM), dtype=torch.bfloat16, device=kv.device)
     out_ptr, out_stride = _rows_arg(out, "out", n, ROW_DIM)
-    with _on(kv):
-        _check(library().mla_kv_read(kv_ptr, kind, scale_ptr, num_slots,
-                                     _int32_arg(slots, "slots", n), n, out_ptr,
-                                     out_stride, _ptr(status), _stream(stream)))
+    _launch(kv, stream, library().mla_kv_read, kv_ptr, kind, scale_ptr, num_slots,
+            _int32_arg(slots, "slots", n), n, out_ptr, out_stride, _ptr(status))
     return out
 
 
@@ -578,10 +592,9 @@ def add_rms_norm(x, weight, residual=None, eps: float = 1e-6, out=None, out8=Non
             raise ValueError(f"out8: expected float8_e4m3fn or uint8, got {out8.dtype}")
         out8_args = _rows_arg(out8, "out8", n, d, out8.dtype)
         sc_args = _rows_arg(scales, "scales", n, d // group if group else 1, torch.float32)
-    with _on(x):
-        _check(library().mla_add_rms_norm(
+    _launch(x, stream, library().mla_add_rms_norm,
             *x_args, *res_args, *ro_args, weight.data_ptr(), eps, n, d, *out_args, *out8_args,
-            *sc_args, group, _stream(stream)))
+            *sc_args, group)
     return out, out8, scales, residual_out
 
 
@@ -609,24 +622,19 @@ def project_out(o_latent, w_vc, out=None, status=None, stream=None):
 
 def lse_combine(O_part, LSE_part, out=None, lse_out=None, stream=None):
     """LSE merge over the leading part dims -> (bf16 [rows, 512], fp32 [rows])."""
-    value_shape = LSE_part.shape
-    nd = LSE_part.dim()
-    parts = 1
+    shape = LSE_part.shape
     # leading dims (splits, shards) are parts; the rest are rows
-    lead = 2 if nd == 5 else 1
-    for d in value_shape[:lead]:
-        parts *= d
-    rows = LSE_part.numel() // parts
-    row_shape = tuple(value_shape[lead:])
+    lead = 2 if len(shape) == 5 else 1
+    parts = shape[0] * shape[1] if lead == 2 else shape[0]
     if out is None:
-        out = torch.empty(row_shape + (VALUE_DIM,), dtype=torch.bfloat16,
+        out = torch.empty(tuple(shape[lead:]) + (VALUE_DIM,), dtype=torch.bfloat16,
                           device=O_part.device)
     if lse_out is None:
-        lse_out = torch.empty(row_shape, dtype=torch.float32, device=O_part.device)
+        lse_out = torch.empty(tuple(shape[lead:]), dtype=torch.float32, device=O_part.device)
     fn = (library().mla_lse_combine_bf16_parts if O_part.dtype == torch.bfloat16
           else library().mla_lse_combine)
-    _check(fn(_ptr(O_part), _ptr(LSE_part), parts, rows, _ptr(out), _ptr(lse_out),
-              _stream(stream)))
+    _check(fn(O_part.data_ptr(), LSE_part.data_ptr(), parts, LSE_part.numel() // parts,
+              out.data_ptr(), lse_out.data_ptr(), _stream(stream)))
     return out, lse_out
 
 

@@ -27,6 +27,7 @@
 // are the K-major B operands in shared memory.  An MMA of this width costs its
 // operand bytes at 128 per cycle (probe: M = 64, N = 16: 23 cycles, M = 128: 39),
 // so a page's products take about 1400 cycles.
+#include <atomic>
 #include <cstring>
 
 #include "mla_combine.cuh"
@@ -837,9 +838,18 @@ mla_partial_fp4_few_kernel(const Fp4Params p) {
 template <int N>
 int launch(const Fp4Params& p, int64_t units, cudaStream_t stream) {
   auto kernel = mla_partial_fp4_few_kernel<N>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)sizeof(typename Few<N>::Smem));
-  if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(fp4 few)");
+  // The attribute lasts as long as the device's context: set it once.
+  static std::atomic<uint64_t> set_on{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (!(set_on.load() & bit)) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)sizeof(typename Few<N>::Smem));
+    if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(fp4 few)");
+    set_on.fetch_or(bit);
+  }
   kernel<<<(unsigned)units, Few<N>::kThreads, (int)sizeof(typename Few<N>::Smem), stream>>>(p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_fail(e, "launch mla_partial_fp4_few_kernel");

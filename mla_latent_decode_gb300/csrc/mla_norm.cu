@@ -23,6 +23,7 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "mla_fp4.cuh"
 #include "mla_internal.h"
@@ -355,10 +356,14 @@ extern "C" int mla_add_rms_norm(const void* x, int64_t x_stride, const void* res
                        like_x(residual_out, residual_out_stride, 2) &&
                        like_x(out, out_stride, 2) && like_x(out8, out8_stride, 1);
   p.shift = off(x, 2);
+  static std::atomic<int> sms_of[64];  // asked of each device once
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess)
+  if (e == cudaSuccess && dev < 64) sms = sms_of[dev].load();
+  if (e == cudaSuccess && sms == 0) {
     e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e == cudaSuccess && dev < 64) sms_of[dev].store(sms);
+  }
   if (e != cudaSuccess) return cuda_fail(e, "mla_add_rms_norm: device query");
   if (vec8)
     launch<kVec>(p, n, sms, (cudaStream_t)stream);
