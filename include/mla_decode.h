@@ -92,7 +92,10 @@ enum {
  *   c_kv = E2M1 * E4M3 scale * g,   rope = E4M3 * g.
  * The block scales adapt to each token; g only centres their range (E4M3
  * scales hold 2^-9 .. 448), so a g near the latents' typical block maximum / 6
- * suits; values beyond 2688 g (c_kv) and 448 g (rope) saturate. */
+ * suits; values beyond 2688 g (c_kv) and 448 g (rope) saturate.  The decode's
+ * products run in f16 with fp32 sums: codes times block scales and RoPE codes
+ * are exact there, queries are scaled per row by a power of two (exact down to
+ * 2^-31 of the row's largest), probabilities are rounded to f16 (2^-11). */
 typedef enum {
   MLA_KV_BF16 = 0,
   MLA_KV_FP8_E4M3 = 1,
@@ -544,9 +547,11 @@ int mla_kv_read(const void* kv_pages, mla_kv_dtype kv_dtype,
  *                 residual_out may be residual, out may be x
  *   weight        bf16 [d];  out or out8 may be NULL, not both
  *   out8, scales  E4M3 bytes [n, d] and fp32 [n, d / group or 1] at their strides
+ * y / s is y times the rounded reciprocal of s (one more rounding of 2^-24).
  * d <= 32768 (else MLA_ERR_UNSUPPORTED).  Rows that start on 16-byte boundaries
- * (out8: 8) with d a multiple of 8 take whole vectors; any other alignment
- * takes single elements.  n = 0 is a no-op.
+ * (out8: 8) with d a multiple of 8 take whole vectors, and so, with group 0, do
+ * rows that every array starts equally far from such a boundary (contiguous
+ * arrays of any d); anything else takes single elements.  n = 0 is a no-op.
  */
 int mla_add_rms_norm(const void* x, int64_t x_stride, const void* residual,
                      int64_t residual_stride, void* residual_out,

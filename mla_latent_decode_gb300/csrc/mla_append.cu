@@ -9,8 +9,8 @@
 // all in fp32 and rounded once, into the stored type.  Both halves of the
 // work are streams bound by HBM and, at a decode step's few tokens, by the
 // launch; one launch does both, its blocks split by role.  Measured from a CUDA
-// graph on a GB300: 2.3 us for one token x 96 heads, 2.7 for 80, 36.6 for 8191
-// (215 MB, 5.9 TB/s, 88% of the copy rate), 7.2 for 16383 bf16 rows (38 MB).
+// graph on a GB300: 2.9 us for one token x 96 heads and for 80, 36.3 for 8191
+// (215 MB, 5.9 TB/s, 88% of the copy rate), 7.1 for 16383 bf16 rows (38 MB).
 //
 // Row blocks: a warp per token.  Lane l holds c_kv elements 16 l .. 16 l + 15,
 // one scale block of the 4-bit format, so the block's maximum, scale and codes
@@ -257,7 +257,9 @@ __global__ void __launch_bounds__(kThreads) mla_append_kernel(const AppendParams
   }
 }
 
-// A warp per row: the stored values, rounded once to bf16.
+// A warp per row: the stored values, rounded once to bf16.  Bound by HBM, or by
+// the launch: 1.3 us for one row, 4.3 for 8191 of the 4-bit rows (12 MB), 4.8
+// for 16383 bf16 rows (38 MB, most of it in L2 behind the append).
 template <int KIND>
 __global__ void __launch_bounds__(kThreads)
     mla_read_kernel(const uint8_t* __restrict__ kv, const float* __restrict__ kv_scale,

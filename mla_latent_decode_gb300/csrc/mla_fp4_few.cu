@@ -1,32 +1,41 @@
 // mla_fp4_few.cu -- partial MLA decode over the 4-bit cache for requests of at
-// most 32 query rows (H * q_len: a tensor-parallel share of the heads without
-// or with few drafts).  Same results as mla_tc_fp4.cu, whose clusters pad such
-// a request to 256 rows.
+// most 96 query rows (H * q_len: all heads without drafts, or a tensor-parallel
+// share of them with a few).  Same results as mla_tc_fp4.cu, whose clusters pad
+// such a request to 256 rows.
 //
-// With few rows nothing repeats a token's conversion, so the cache's bytes
-// bound the work (352 bytes per token against 34 to 70 kFLOP) as long as the
-// conversion and the shared-memory traffic keep up.  The products are turned
-// round: tokens and value dims are the M side, the query rows the N side,
+// The products are turned round: tokens and value dims are the M side, the query
+// rows the N side,
 //   S^T[64 tokens, N rows] = K Q^T,   O^T[512 dims, N rows] += V^T P^T,
-// so a row costs N = 16 or 32 of the MMA's width, not a padded 128 of its
-// height, and one CTA holds everything of a (request, part).  Per page:
-//   warp 0       copies the raw page (one bulk copy; a ring of two);
-//   warps 8-15   convert it in two halves of the dims: four threads per token,
-//                a block of 16 of every 64 dims each, into 8-KB boxes (64 tokens
-//                x 64 dims f16, 128-byte swizzle) that are the K-major A of the
-//                scores and, read MN-major, the A of the outputs; two sets of
-//                boxes, passed on and freed by halves;
-//   warp 1       issues 36 MMAs of M = 64, N, K = 16 for the next page's S^T,
-//                then this page's 4 per 128 value dims of O^T (M = 128);
-//   warps 4-7    softmax: two threads per token, N / 2 scores each.  The running
-//                references only change when some score passes its row's by
-//                2^8: one vote per page; then the maxima cross the lanes and
-//                warps and O^T (lane = dim) is rescaled in place.  Row sums
-//                stay per thread until the end.
+// so a row costs N = 16, 32, 64 or 96 of the MMA's width, not a padded 128 of
+// its height, one CTA holds everything of a (request, part) and a token is
+// converted once.  Per page:
+//   the raw page   arrives in the converters' registers or by a bulk copy;
+//   8 warps        convert it in two halves of the dims into 8-KB boxes (64
+//                  tokens x 64 dims f16, 128-byte swizzle) that are the K-major
+//                  A of the scores and, read MN-major, the A of the outputs; a
+//                  ring of half pages, passed on and freed by halves;
+//   1 thread       issues 36 MMAs of M = 64, N, K = 16 for the next page's S^T
+//                  and this page's 4 per 128 value dims of O^T (M = 128);
+//   4 or 8 warps   softmax: a thread has one token's scores of 8 to 24 rows.  The
+//                  running references only change when some score passes its
+//                  row's by 2^8: one vote per page; then the maxima cross the
+//                  lanes and warps and O^T (lane = dim) is rescaled in place.
+//                  Row sums stay per thread until the end.
 // P (f16, row by row over the tokens) and Q (f16, mla_tc_fp4.cu's row scale)
-// are the K-major B operands in shared memory.  An MMA of this width costs its
-// operand bytes at 128 per cycle (probe: M = 64, N = 16: 23 cycles, M = 128: 39),
-// so a page's products take about 1400 cycles.
+// are the K-major B operands in shared memory.
+//
+// What bounds it: shared-memory traffic.  A page's boxes are written once (74 KB)
+// and read by both products, and an MMA this narrow runs at its operands' bytes,
+// 128 a cycle (probe: M = 64 and N = 16, 32, 64, 96: 20, 21, 28, 40 cycles, M =
+// 128: 34, 35, 41, 48).  All of it, raw pages included, is 240, 270, 370 and 430
+// KB a page for the four widths, 1870 to 3360 cycles; measured at 152 requests,
+// one per SM, 1.22, 1.27, 1.89 and 2.54 us a page (2300 to 4900 cycles) and 12 to
+// 27 us for the rest of a launch with its merge.  (A profile of N = 96: the tensor
+// cores' operand path busy 48% of the time, other shared-memory accesses 36%.)
+// 32 ragged requests of 2k to 50k tokens x 16 heads take 86 us (165 MB, 1.9 TB/s),
+// x 32 heads 91; 48 ragged x 96 heads 182 (the clusters: 214); 152 x 96 heads x
+// 6400 tokens 286 (471).  From 97 rows on O^T and S^T need more than TMEM's 512
+// columns.
 #include <atomic>
 #include <cstring>
 
@@ -57,13 +66,19 @@ struct Few {
   static constexpr int kCols1 = N / kGroups;          // rows of a group
   static constexpr int kH = kCols1 / 2;               // rows of a softmax thread
   static constexpr int kLd = N > 16 ? 32 : 16;        // O^T columns read at a time
-  // What 227 KB of shared memory and 512 TMEM columns leave room for.
+  // What 227 KB of shared memory and 512 TMEM columns leave room for.  (A ring
+  // of three half pages instead of four costs N = 16 and 32 a quarter: 168 and
+  // 181 us for 135 and 146 at 152 x 6400 tokens; five, which leave less L1 for
+  // the pages on their way, 138 and 142.)
   static constexpr int kHalves = N > 32 ? 3 : 4;      // ring of half pages
   static constexpr int kSBufs = N > 64 ? 1 : 2;       // S^T buffers
   static constexpr int kPBufs = N > 32 ? 1 : 2;       // P buffers
-  // How the raw pages arrive: straight to the converters' registers (needs room
-  // in L1, so little shared memory), through one raw buffer, or (0) through the
-  // slot that the page's first half is converted into.
+  // How the raw pages arrive: straight to the converters' registers, a page
+  // ahead, which saves their way through shared memory but takes as much L1 as
+  // a page has bytes, so it loses where the rings leave little of the 256 KB;
+  // through one raw buffer; or (0) through the slot that the page's first half
+  // is converted into.  At 152 x 6400 tokens, registers against bulk copies: N =
+  // 16 135 and 140 us, 32 146 and 150, 64 223 and 199, 96 298 and 286.
   static constexpr bool kDirect = N <= 32;
   static constexpr int kRaw = N > 64 ? 0 : 1;
   // In-slot copies are at most kHalves / 2 pages ahead of the converters.
