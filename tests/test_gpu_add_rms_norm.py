@@ -132,3 +132,15 @@ def test_rows_shifted_alike(n, d, off):
     # arrays that are not shifted alike
     other = torch.zeros(n * d + 1, dtype=torch.bfloat16, device="cuda")[1:].view(n, d)
     _check(x, keep, w, 1e-6, mla.add_rms_norm(x, w, keep.clone(), out=other, e4m3=True))
+
+
+@pytest.mark.parametrize("d", [7168, 7167])
+def test_more_values_than_32_bits_count(d):
+    n = 300_001
+    assert n * d > 1 << 31
+    x = torch.zeros((n, d), dtype=torch.bfloat16, device="cuda")
+    last, w = _rows(5, d, 30), _rows(1, d, 31)[0].contiguous()
+    x[-5:] = last
+    _, out8, scales, _ = mla.add_rms_norm(x, w, None, e4m3=True)
+    _check(last, None, w, 1e-6, (None, out8[-5:], scales[-5:], None))
+    assert not out8[:5].view(torch.uint8).any()

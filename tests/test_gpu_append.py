@@ -235,3 +235,22 @@ def test_side_stream_and_empty():
     mla.kv_append(rows[:0], slots[:0], pos[:0], tab, kv, scale, norm_weight=weight)
     assert mla.kv_read(kv, slots[:0], scale).shape == (0, 576)
     assert torch.equal(kv, before)
+
+
+@pytest.mark.parametrize("width,dtype", [(352, torch.uint8), (576, torch.uint8), (576, torch.bfloat16)])
+def test_pool_past_32_bit_offsets(width, dtype):
+    """Rows at the end of a pool of more than 2^32 bytes, and back."""
+    slots = ((1 << 32) // (width * dtype.itemsize) // 64 + 2) * 64
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    rows = torch.randn((70, 576), generator=gen, device="cuda").bfloat16()
+    pos = torch.arange(70, dtype=torch.int32, device="cuda")
+    back = []
+    for total in (128, slots):
+        pool = torch.zeros((total, width), dtype=dtype, device="cuda")
+        scale = None if dtype == torch.bfloat16 else torch.full((total if width == 576 else 1,), 0.0625, device="cuda")
+        at = torch.arange(total - 70, total, dtype=torch.int32, device="cuda")
+        mla.kv_append(rows, at, pos, table(128).cuda(), pool, scale)
+        back.append(mla.kv_read(pool, at, scale))
+        assert int((pool[:total - 70] != 0).sum()) == 0 if total == 128 else not pool[:64].any()
+        del pool
+    assert torch.equal(*back) and back[0].float().abs().max() > 1

@@ -115,3 +115,33 @@ def test_plan_and_one_launch(H):
     # the same fp32 parts, merged in another order, rounded to bf16
     assert torch.allclose(out2.float(), out.float(), rtol=2.0 ** -7, atol=1e-6)
     assert torch.allclose(lse2, lse, rtol=1e-6, atol=1e-6)
+
+
+@pytest.mark.parametrize("q,H", [(1, 16), (1, 64), (1, 96), (5, 96)])
+def test_pool_past_32_bit_offsets(q, H):
+    """The same pages at the end of a pool of 4.6 GB: bitwise the same results."""
+    case = Case(2, q, H, [700, 130], seed=40)
+    O, LSE = case.run(2)
+    slots = 13_000_000 // 64 * 64
+    shift = slots - case.kv.shape[0] // 64 * 64
+    big = torch.zeros((slots, mla.FP4_ROW_BYTES), dtype=torch.uint8, device="cuda")
+    big[shift:shift + case.kv.shape[0]] = case.kv[:slots - shift]
+    assert shift * mla.FP4_ROW_BYTES > 1 << 32
+    case.kv, case.r2t = big, case.r2t + shift
+    O2, LSE2 = case.run(2)
+    assert case.status == 0
+    assert torch.equal(O, O2) and torch.equal(LSE, LSE2)
+
+
+@pytest.mark.parametrize("q,H", [(1, 16), (1, 64), (1, 96), (5, 96)])
+def test_a_query_row_that_is_not_finite_stays_alone(q, H):
+    case = Case(1, q, H, [333], seed=41)
+    O, LSE = case.run(2)
+    case.q_nope[0, 0, 3, 7] = float("nan")
+    case.q_rope[0, 0, 5, 1] = float("inf")
+    case.up()
+    O2, LSE2 = case.run(2)
+    assert LSE2[:, 0, 0, 0, 3].isnan().all() and O2[:, 0, 0, 0, 3].isnan().all()
+    rest = [h for h in range(H) if h not in (3, 5)]
+    assert torch.equal(O[:, :, :, :, rest], O2[:, :, :, :, rest])
+    assert torch.equal(LSE[:, :, :, :, rest], LSE2[:, :, :, :, rest])
