@@ -578,12 +578,11 @@ __device__ __forceinline__ float place_query(Smem& s, uint32_t tmem, uint32_t la
                   : make_uint4(0, 0, 0, 0);
   };
   // The exponent fields order like the magnitudes: the largest |q| as bits.
-  uint32_t big = 0;
+  uint32_t big4[4] = {0, 0, 0, 0};  // two values a word
   const auto take = [&](uint4 v) {
     const uint32_t x[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-      big = max(big, max(x[k] & 0x7FFFu, (x[k] >> 16) & 0x7FFFu));
+    for (int k = 0; k < 4; ++k) big4[k] = __vmaxu2(big4[k], x[k] & 0x7FFF7FFFu);
   };
 #pragma unroll 1
   for (int k = 4 * g; k < 4 * g + 4; ++k)
@@ -592,6 +591,8 @@ __device__ __forceinline__ float place_query(Smem& s, uint32_t tmem, uint32_t la
   if (g == 0)
 #pragma unroll
     for (int cc = 0; cc < 8; ++cc) take(chunk(s.qrope, cc));
+  const uint32_t big2 = __vmaxu2(__vmaxu2(big4[0], big4[1]), __vmaxu2(big4[2], big4[3]));
+  uint32_t big = max(big2 & 0xFFFFu, big2 >> 16);
   s.xch[0][g][r] = __uint_as_float(big);
   named_bar_sync(1, 256);
   big = max(big, __float_as_uint(s.xch[0][g ^ 1][r]));
