@@ -141,14 +141,6 @@ __device__ __forceinline__ void tmem_ld_n(uint32_t taddr, uint32_t (&r)[N]) {
         : "r"(taddr));
   }
 }
-template <int N>
-__device__ __forceinline__ void tmem_st_n(uint32_t taddr, const uint32_t (&r)[N]) {
-  if constexpr (N == 32)
-    tmem_st32(taddr, r);
-  else
-    tmem_st16(taddr, r);
-}
-
 // Whether any of the kThreadsIn softmax threads says so (named barrier 1).
 template <int kThreadsIn>
 __device__ __forceinline__ bool any_of(bool x) {
@@ -660,7 +652,7 @@ __device__ __forceinline__ void softmax(typename Few<N>::Smem& s, const Fp4Param
 #pragma unroll
               for (int n = 0; n < 16; ++n)
                 o[n] = __float_as_uint(__uint_as_float(o[n]) * alpha[c + n]);
-              tmem_st_n<16>(at, o);
+              tmem_st16(at, o);
             }
           tmem_wait_st();
         }
