@@ -264,7 +264,10 @@ int mla_plan_sched_ex(int V, int q_len, int H, int rows_per_unit,
  * kernel that serves kv_dtype, s_max = 64, c0 and lam as mla_plan).
  * split_pages_out: HOST int32 [num_shards * B * (s_max + 1)]; work_out: HOST
  * int32 [work_capacity], at most num_shards * B * s_max * ceil(q_len * H / 128)
- * entries are written.
+ * entries are written, FP4 ceil(q_len * H / MLA_FP4_FEW_ROWS).  FP4 with more rows
+ * than that: the plan for clusters or, for short work, one of single CTAs with
+ * units of MLA_FP4_FEW_ROWS rows, whichever should end sooner; num_work_out tells
+ * the decode which (pass the work list on with its boundaries).
  */
 int mla_plan_sched(int B, int q_len, int H, int num_shards,
                    mla_kv_dtype kv_dtype, const int32_t* seq_lens_host,
@@ -335,7 +338,8 @@ int mla_check_page_table(const int32_t* req_to_token_host, int64_t stride,
  *                    (see mla_plan_sched) in launch order.  It must hold
  *                    every id 0 .. num_work - 1 once, num_work = num_splits *
  *                    num_shards * B * ceil(q_len * H / R), R = 256 rows for
- *                    BF16 and FP4 KV and 128 for FP8 (else MLA_ERR_INVALID_ARG); an
+ *                    BF16 and FP4 KV and 128 for FP8 (else MLA_ERR_INVALID_ARG);
+ *                    FP4 also takes R = MLA_FP4_FEW_ROWS, a CTA per unit; an
  *                    entry outside that range sets MLA_STATUS_BAD_WORK and
  *                    its cluster does nothing.  The results do not depend on
  *                    the order.

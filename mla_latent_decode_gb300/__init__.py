@@ -281,7 +281,7 @@ def plan_sched(B: int, q_len: int, H: int, seq_lens, num_shards: int = 1,
     V = len(arr)
     assert V == B * num_shards
     s_max = _s_max(kv_dtype, q_len, H)
-    cap = V * s_max * (-(-q_len * H // 128))
+    cap = V * s_max * (-(-q_len * H // (FP4_FEW_ROWS if kv_dtype == "fp4_e2m1" else 128)))
     bnd_out = (ctypes.c_int32 * (V * (s_max + 1)))()
     work_out = (ctypes.c_int32 * cap)()
     S, n, eff = ctypes.c_int(), ctypes.c_int64(), ctypes.c_float()

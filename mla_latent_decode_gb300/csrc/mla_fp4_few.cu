@@ -1,7 +1,8 @@
 // mla_fp4_few.cu -- partial MLA decode over the 4-bit cache for requests of at
 // most 96 query rows (H * q_len: all heads without drafts, or a tensor-parallel
 // share of them with a few).  Same results as mla_tc_fp4.cu, whose clusters pad
-// such a request to 256 rows.
+// such a request to 256 rows; and, where a work list says so, for larger ones in
+// groups of 96 rows, which end sooner when the work is short (mla_plan_sched).
 //
 // The products are turned round: tokens and value dims are the M side, the query
 // rows the N side,
@@ -120,6 +121,19 @@ struct Few {
   static_assert(sizeof(Smem) <= 227 * 1024, "shared memory budget");
 };
 
+// A unit: a part of a request's pages for one group of at most 96 of its rows.
+struct GroupRange : UnitRange {
+  int r0;  // the group's first row
+};
+__device__ __forceinline__ int g_rows(const Fp4Params& p, const GroupRange& w) {
+  return min(p.q_len * p.H - w.r0, kFp4FewRows);
+}
+// Its first row among the partial outputs.
+__device__ __forceinline__ int64_t first_row(const Fp4Params& p, const GroupRange& w) {
+  const int64_t R = (int64_t)p.q_len * p.H, part = (int64_t)w.split * (p.V / p.B) + w.shard;
+  return (part * p.B + w.b) * R + w.r0;
+}
+
 template <typename S>
 __device__ __forceinline__ void give_up(S& s, const Fp4Params& p) {
   if (p.status) atomicOr(p.status, MLA_STATUS_WAIT_TIMEOUT);
@@ -160,15 +174,15 @@ __device__ __forceinline__ bool any_of(bool x) {
 // that see nothing.
 template <int N>
 __device__ __forceinline__ void place_query(typename Few<N>::Smem& s, const Fp4Params& p,
-                                            const UnitRange& w, int warp, int lane) {
+                                            const GroupRange& w, int warp, int lane) {
   constexpr int kWarps = Few<N>::kMmaWarp, kRows = (N + kWarps - 1) / kWarps;
-  const int R = p.q_len * p.H;
+  const int R = g_rows(p, w);
   const float g = p.g[0];
   uint4 x[kRows][3];
 #pragma unroll
   for (int r = 0; r < kRows; ++r) {
     const int n = warp + kWarps * r;
-    const int64_t row = (int64_t)w.b * R + n;
+    const int64_t row = (int64_t)w.b * p.q_len * p.H + w.r0 + n;
 #pragma unroll
     for (int k = 0; k < 3; ++k) {
       const int c = lane + 32 * k;  // 16-byte chunk of the row's 72
@@ -203,7 +217,7 @@ __device__ __forceinline__ void place_query(typename Few<N>::Smem& s, const Fp4P
   }
   const int n = warp + kWarps * lane;
   if (lane < kRows && n < N) {
-    const int i = n / p.H;
+    const int i = (w.r0 + n) / p.H;
     int64_t lim = 0;
     if (n < R) {
       lim = p.kv_limit ? (int64_t)p.kv_limit[(int64_t)w.v * p.q_len + i] : w.L - p.q_len + 1 + i;
@@ -336,7 +350,7 @@ struct RawShare {
 // is NaN instead.
 template <int N>
 __device__ __forceinline__ void convert(typename Few<N>::Smem& s, const Fp4Params& p,
-                                        const UnitRange& w, int warp, int lane) {
+                                        const GroupRange& w, int warp, int lane) {
   using F = Few<N>;
   const int t4 = (lane >> 1) & 3, v = (lane & 1) + 2 * (lane >> 3);
   const int rt = lane >> 2;  // token of the lane's RoPE codes
@@ -567,13 +581,13 @@ __device__ __forceinline__ void tmem_ld_halves(uint32_t taddr, uint32_t (&r)[H])
 // rescaled, thread = value dim of a block of 128.
 template <int N>
 __device__ __forceinline__ void softmax(typename Few<N>::Smem& s, const Fp4Params& p,
-                                        const UnitRange& w, uint32_t tmem, int warp, int lane) {
+                                        const GroupRange& w, uint32_t tmem, int warp, int lane) {
   using F = Few<N>;
   constexpr int H = F::kH, T = 128 * F::kGroups;
   const int quad = warp & 3, group = warp >> 2, dim = quad * 32 + lane;
   const int tok = quad * 16 + (lane & 15), n0 = F::kCols1 * group + H * (lane >> 4);
   const uint32_t trow = tmem + ((uint32_t)(quad * 32) << 16);
-  const int R = p.q_len * p.H;
+  const int R = g_rows(p, w);
   float* const alpha = s.wred[0];
   place_query<N>(s, p, w, warp, lane);
   bool ok = mbar_wait_cta(smem_u32(&s.qfull), 0, &s.abort_flag);
@@ -691,9 +705,7 @@ __device__ __forceinline__ void softmax(typename Few<N>::Smem& s, const Fp4Param
     if ((lane & 15) == 0) s.wred[quad][n0 + k] = z;
   }
   named_bar_sync(2, T);
-  const int64_t rows = (int64_t)p.B * R;
-  const int64_t part = (int64_t)w.split * (p.V / p.B) + w.shard;
-  const int64_t row0 = part * rows + (int64_t)w.b * R;
+  const int64_t row0 = first_row(p, w);
   float* const fin = s.wred[0];
   if (group == 0 && dim < N) {
     const float lt = (s.wred[0][dim] + s.wred[1][dim]) + (s.wred[2][dim] + s.wred[3][dim]);
@@ -753,8 +765,9 @@ mla_partial_fp4_few_kernel(const Fp4Params p) {
     if (threadIdx.x == 0 && p.status) atomicOr(p.status, MLA_STATUS_BAD_WORK);
     return;
   }
-  UnitRange w;
-  unit_range(p, unit, w);
+  GroupRange w;
+  unit_range(p, unit / p.U, w);
+  w.r0 = unit % p.U * kFp4FewRows;
   const int R = p.q_len * p.H;
   if (threadIdx.x == 0) {
     s.abort_flag = 0;
@@ -802,7 +815,7 @@ mla_partial_fp4_few_kernel(const Fp4Params p) {
     // its rows, every part being in memory by then.
     if (threadIdx.x == 0) {
       int* c = p.counters + w.b;
-      s.last = atom_add_acq_rel_gpu(c, 1) == p.num_splits * (p.V / p.B) - 1;
+      s.last = atom_add_acq_rel_gpu(c, 1) == p.num_splits * (p.V / p.B) * p.U - 1;
       if (s.last) *c = 0;
     }
     __syncthreads();
@@ -815,11 +828,10 @@ mla_partial_fp4_few_kernel(const Fp4Params p) {
 
   if (w.npages == 0) {
     // No tokens for this part: O = 0, LSE = -inf.
-    const int64_t rows = (int64_t)p.B * R;
-    const int64_t part = (int64_t)w.split * (p.V / p.B) + w.shard;
-    const int64_t row0 = part * rows + (int64_t)w.b * R;
-    if ((int)threadIdx.x < R) p.LSE_part[row0 + threadIdx.x] = -INFINITY;
-    const int words = R * MLA_VALUE_DIM / (p.o_bf16 ? 8 : 4);  // 16-byte words
+    const int rows = g_rows(p, w);
+    const int64_t row0 = first_row(p, w);
+    if ((int)threadIdx.x < rows) p.LSE_part[row0 + threadIdx.x] = -INFINITY;
+    const int words = rows * MLA_VALUE_DIM / (p.o_bf16 ? 8 : 4);  // 16-byte words
     uint4* dst = reinterpret_cast<uint4*>(
         reinterpret_cast<uint8_t*>(p.O_part) + row0 * MLA_VALUE_DIM * (p.o_bf16 ? 2 : 4));
     for (int k = threadIdx.x; k < words; k += kThreads) dst[k] = make_uint4(0, 0, 0, 0);
@@ -866,7 +878,7 @@ int launch(const Fp4Params& p, int64_t units, cudaStream_t stream) {
 }  // namespace
 
 int launch_fp4_few(const Fp4Params& p, cudaStream_t stream) {
-  const int64_t units = (int64_t)p.V * p.num_splits;
+  const int64_t units = (int64_t)p.V * p.num_splits * p.U;
   const int R = p.q_len * p.H;
   return R <= 16   ? launch<16>(p, units, stream)
          : R <= 32 ? launch<32>(p, units, stream)

@@ -1376,7 +1376,10 @@ int launch_fp4(const DecodeArgs& a) {
   if (units * kCtas > 0x7fffffff)
     return fail(MLA_ERR_INVALID_ARG, "grid too large");
   p.o_bf16 = a.o_bf16;
-  if (a.q_len * a.H <= kFp4FewRows) return launch_fp4_few(p, a.stream);
+  if (few_row_groups(a)) {
+    p.U = (a.q_len * a.H + kFp4FewRows - 1) / kFp4FewRows;
+    return launch_fp4_few(p, a.stream);
+  }
   CUtensorMap qn_map, qr_map;
   int rc = make_query_maps(&qn_map, &qr_map, a, &p.q_box_rows);
   if (rc != MLA_OK) return rc;

@@ -161,3 +161,12 @@ def test_plan_spreads_one_request_over_every_sm(H, L, wide):
     assert bnd.shape == (1, S + 1) and bnd[0, 0] == 0 and bnd[0, -1] == -(-L // 64) and (np.diff(bnd[0]) >= 0).all()
     assert sorted(work) == list(range(S))
     assert mla.plan_parts(1, 1, H, [L], num_sms=152, kv_dtype="fp4_e2m1")[0] <= 160
+
+
+@pytest.mark.parametrize("B,q,H,L,groups", [
+    (2, 3, 128, 300, True), (1, 5, 96, 64, True), (16, 5, 96, 100000, False), (1, 5, 96, 100000, False)])
+def test_plan_takes_row_groups_for_short_work(B, q, H, L, groups):
+    S, bnd, work, _ = mla.plan_sched(B, q, H, [L] * B, num_sms=152, kv_dtype="fp4_e2m1")
+    U = -(-q * H // (96 if groups else 256))
+    assert sorted(work) == list(range(B * S * U))
+    assert bnd.shape == (B, S + 1) and (bnd[:, 0] == 0).all() and (bnd[:, -1] == -(-L // 64)).all()

@@ -145,3 +145,40 @@ def test_a_query_row_that_is_not_finite_stays_alone(q, H):
     rest = [h for h in range(H) if h not in (3, 5)]
     assert torch.equal(O[:, :, :, :, rest], O2[:, :, :, :, rest])
     assert torch.equal(LSE[:, :, :, :, rest], LSE2[:, :, :, :, rest])
+
+
+@pytest.mark.parametrize("q,H,lens", [
+    (3, 128, [300, 1]), (5, 96, [64]), (1, 97, [900, 0, 65]), (2, 100, [700, 40, 129]), (8, 128, [2000]), (1, 192, [500])])
+def test_row_groups_of_a_work_list(q, H, lens):
+    """A work list of one unit per 96 rows: the one-CTA kernel in groups of rows,
+    against the definition and, merged in the launch, against its own parts."""
+    case = Case(len(lens), q, H, lens, seed=50)
+    S, U = 3, -(-q * H // 96)
+    P = [-(-L // 64) for L in lens]
+    bnd = [[s * p // S for s in range(S)] + [p] for p in P]
+    order = np.random.default_rng(1).permutation(S * len(lens) * U)
+    O, LSE = case.run(S, bnd=bnd, work=order)
+    assert case.status == 0
+    check(case, O, LSE, S, bnd=bnd, heads=sorted({0, 1, H // 2, H - 2, H - 1}))
+    out, lse = mla.lse_combine(O, LSE)
+    dev = dict(split_pages=torch.as_tensor(bnd, dtype=torch.int32).cuda(),
+               work=torch.as_tensor(order, dtype=torch.int32).cuda())
+    args = (case.qn, case.qr, case.kv, case.gd, case.r2t, case.sl, None, S, 192.0 ** -0.5)
+    counters = mla.fused_counters(case.B, q, H, "cuda")
+    for _ in range(2):
+        out2, lse2 = mla.decode_fused(*args, counters=counters, **dev)
+        assert torch.allclose(out2.float(), out.float(), rtol=2.0 ** -7, atol=1e-6)
+        assert torch.allclose(lse2, lse, rtol=1e-6, atol=1e-6, equal_nan=True)
+        assert int(counters.abs().sum()) == 0
+
+
+def test_short_work_is_planned_in_row_groups():
+    lens = [300, 170]
+    case = Case(2, 3, 128, lens, seed=51)
+    S, bnd, work, _ = mla.plan_sched(2, 3, 128, lens, kv_dtype="fp4_e2m1")
+    assert len(work) == 2 * S * 4
+    O, LSE = case.run(S, bnd=bnd, work=work)
+    assert case.status == 0
+    check(case, O, LSE, S, bnd=bnd, heads=[0, 64, 127])
+    case.run(S, bnd=bnd, work=[len(work)] + list(work[1:]))
+    assert case.status == mla.STATUS_BAD_WORK
