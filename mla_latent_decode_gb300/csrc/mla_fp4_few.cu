@@ -766,8 +766,9 @@ mla_partial_fp4_few_kernel(const Fp4Params p) {
     return;
   }
   GroupRange w;
-  unit_range(p, unit / p.U, w);
-  w.r0 = unit % p.U * kFp4FewRows;
+  // Fewer rows than 96 are one group.
+  unit_range(p, N == kFp4FewRows ? unit / p.U : unit, w);
+  w.r0 = N == kFp4FewRows ? unit % p.U * kFp4FewRows : 0;
   const int R = p.q_len * p.H;
   if (threadIdx.x == 0) {
     s.abort_flag = 0;
