@@ -546,7 +546,10 @@ int mla_kv_read(const void* kv_pages, mla_kv_dtype kv_dtype,
  *   y = h * rsqrt(mean(h^2) + eps) * weight
  *   out = bf16(y);  out8 = E4M3(y / s) (nearest even, saturated), s = max|y| /
  *   448 over the row (group 0) or over each `group` values (32, 64 or 128; d a
- *   multiple of it); a group of zeros gets scale 0 and codes 0.
+ *   multiple of it); a group of zeros gets scale 0 and codes 0, one that holds a
+ *   NaN scale NaN and codes NaN (0x7F).
+ * Values need not be finite: an infinite h makes its own y NaN and the row's
+ * others 0, a NaN the whole row, as the formula has it.
  *   x, residual, residual_out, out   bf16 rows at their strides (elements);
  *                 residual_out may be residual, out may be x
  *   weight        bf16 [d];  out or out8 may be NULL, not both

@@ -95,6 +95,14 @@ __device__ __forceinline__ uint32_t word(const uint4& u, int k) {
   return k == 0 ? u.x : k == 1 ? u.y : k == 2 ? u.z : u.w;
 }
 
+// The larger of two values, NaN where either is: a maximum that dropped a NaN
+// would store a broken row as zeros with scale 0.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
+
 // How a row's eight values lie: kAny element by element; kVec on whole vectors;
 // kShift on whole vectors but for the row's two ends.
 enum Lay { kAny, kVec, kShift };
@@ -132,7 +140,8 @@ __device__ __forceinline__ void store8(__nv_bfloat16* row, int c0, int d,
   }
 }
 
-// Sum (MAX: maximum) of one value per thread over the block, in every thread.
+// Sum (MAX: maximum, as max_nan) of one value per thread over the block, in
+// every thread.
 template <bool MAX>
 __device__ __forceinline__ float block_reduce(float v, float* part) {
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, warps = blockDim.x / 32;
@@ -140,7 +149,7 @@ __device__ __forceinline__ float block_reduce(float v, float* part) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
       const float b = __shfl_xor_sync(kAll, a, o);
-      a = MAX ? fmaxf(a, b) : a + b;
+      a = MAX ? max_nan(a, b) : a + b;
     }
     return a;
   };
@@ -212,10 +221,10 @@ __global__ void __launch_bounds__(T, T == 256 && V == 4 ? 4 : 1) mla_norm_kernel
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       h[k][e] = mul2(h[k][e], mul2(rs2, widen(word(w[k], e))));
-      amax[k] = fmaxf(amax[k], fmaxf(fabsf(both(h[k][e]).x), fabsf(both(h[k][e]).y)));
+      amax[k] = max_nan(amax[k], max_nan(fabsf(both(h[k][e]).x), fabsf(both(h[k][e]).y)));
     }
     if (p.out && col(k) < p.d) store8<L>(p.out + r * p.out_stride, col(k), p.d, h[k]);
-    rowmax = fmaxf(rowmax, amax[k]);
+    rowmax = max_nan(rowmax, amax[k]);
   }
   if (!p.out8) return;
   if (p.group == 0) rowmax = block_reduce<true>(rowmax, part[2]);
@@ -225,7 +234,7 @@ __global__ void __launch_bounds__(T, T == 256 && V == 4 ? 4 : 1) mla_norm_kernel
       amax[k] = rowmax;
     } else {
       for (int o = p.group / 16; o > 0; o >>= 1)
-        amax[k] = fmaxf(amax[k], __shfl_xor_sync(kAll, amax[k], o));
+        amax[k] = max_nan(amax[k], __shfl_xor_sync(kAll, amax[k], o));
     }
     const int c0 = col(k);
     if (c0 >= p.d) continue;
@@ -241,7 +250,7 @@ __global__ void __launch_bounds__(T, T == 256 && V == 4 ? 4 : 1) mla_norm_kernel
         const float2 v = both(mul2(h[k][e], inv2));
         c8[e] = e4m3_pair(v.x, v.y);
       }
-    } else {  // the reciprocal leaves the range (or the group is zero)
+    } else {  // the reciprocal leaves the range, the group is zero or s is NaN
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const float2 v = both(h[k][e]);
