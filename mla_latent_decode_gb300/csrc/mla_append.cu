@@ -356,9 +356,10 @@ extern "C" int mla_kv_append(const void* rows, int64_t row_stride, int64_t n,
   if (n < 0) return fail(MLA_ERR_INVALID_ARG, "mla_kv_append: n = %lld < 0", (long long)n);
   const int rc = check_pool(kv_pages, kv_dtype, kv_scale, num_slots, "mla_kv_append");
   if (rc != MLA_OK) return rc;
-  if (H < 0 || (H > 0 && (!q || !q_out)))
+  if (H < 0) return fail(MLA_ERR_INVALID_ARG, "mla_kv_append: H = %d < 0", H);
+  if (n == 0) return MLA_OK;  // whose arrays may all be NULL
+  if (H > 0 && (!q || !q_out))
     return fail(MLA_ERR_INVALID_ARG, "mla_kv_append: H = %d needs q and q_out", H);
-  if (n == 0) return MLA_OK;
   if (!rows || !slots || !positions || !cos_sin)
     return fail(MLA_ERR_INVALID_ARG,
                 "mla_kv_append: rows, slots, positions and cos_sin are required");

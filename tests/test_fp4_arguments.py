@@ -170,3 +170,19 @@ def test_plan_takes_row_groups_for_short_work(B, q, H, L, groups):
     U = -(-q * H // (96 if groups else 256))
     assert sorted(work) == list(range(B * S * U))
     assert bnd.shape == (B, S + 1) and (bnd[:, 0] == 0).all() and (bnd[:, -1] == -(-L // 64)).all()
+
+
+def test_append_of_no_tokens_with_queries(lib):
+    """n = 0 is a no-op: an empty tensor's address is NULL, whatever H is."""
+    assert append(lib, n=0, q=None, qo=None) == 0
+    assert append(lib, n=0, q=None, qo=None, rows=None, slots=None, pos=None) == 0
+    assert append(lib, n=0, H=-1) == ARG and append(lib, n=0, kv=None) == ARG
+
+
+def test_binding_appends_no_tokens_with_queries(lib, monkeypatch):
+    monkeypatch.setattr(mla, "_launch", lambda t, stream, fn, *args: mla._check(fn(*args, None)))
+    bf, i32 = torch.bfloat16, torch.int32
+    kv, g = torch.zeros((64, 352), dtype=torch.uint8), torch.ones(4)
+    rows, ids = torch.zeros((0, 576), dtype=bf), torch.zeros(0, dtype=i32)
+    got = mla.kv_append(rows, ids, ids, torch.zeros((8, 64)), kv, g, q_rope=torch.zeros((5, 3, 64), dtype=bf)[:0])
+    assert got.shape == (0, 3, 64) and got.dtype == bf
