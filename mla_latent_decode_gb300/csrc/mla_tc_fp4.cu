@@ -28,7 +28,8 @@
 //                  tokens x 64 dims f16, K-major, 128-byte swizzle);
 //     warp 1       rank 0: issues S[256 rows, 128 tokens] = Q K^T into one of
 //                  two TMEM buffers (A = Q_nope from TMEM / Q_rope from shared
-//                  memory); rank 1: tells rank 0 which boxes are ready;
+//                  memory);
+//     warp 2       rank 1: tells rank 0 which boxes are ready;
 //     warps 4-11   softmax: warpgroup g takes every second tile, thread = row;
 //                  base-2 running statistics with lazy rescaling; P (f16) and
 //                  rescale factors travel to the O-CTA by bulk copy (warp 3).
@@ -41,9 +42,9 @@
 // M = 128, N = 128, K = 16 f16 MMAs at 64.1 cycles and N = 256 at 128.1, so
 // the narrower tile costs nothing and the next tile's products overlap the
 // softmax of the last.
-// Measured: 16 requests x 5 x 96 rows x 100k tokens 1.06 ms, 1.58 PFLOP/s of
-// useful products, 83% of the measured bf16 rate (94% of the rows are real: 480
-// of 512); 24 ragged requests of 1k to 200k tokens 610 us, 1.41 PFLOP/s.
+// Measured, with the merge: 16 requests x 5 x 96 rows x 100k tokens 1113 us, 1.50
+// PFLOP/s of useful products, 79% of the measured bf16 rate (94% of the rows are
+// real: 480 of 512); 24 ragged requests of 1k to 200k tokens 642 us, 1.34 PFLOP/s.
 #include <cuda_bf16.h>
 
 #include <cstring>
@@ -80,6 +81,7 @@ constexpr int kPeerFlagOff = kPMsgBytes;            // rank 2: rank 1's flags
 constexpr int kPSlotStride = 17408;                 // 17 KB, 1024-aligned
 constexpr uint32_t kSCol0 = 256;                    // two S buffers of 128 columns
 constexpr int kDequantWarp0 = 12;
+constexpr uint32_t kNoteBytes = 16;
 constexpr uint16_t kMaskS = 0x3;     // cluster ranks of the S pair
 constexpr uint16_t kMaskO = 0xC;     // cluster ranks of the O pair
 // Register split of the S-CTAs (setmaxnreg): 512 threads launch with 128 each;
@@ -103,12 +105,14 @@ struct __align__(1024) Smem {
   uint8_t raw[kRaw][kRawBytes];             // 66 KB of pages as stored
   uint8_t qrope[kRows * 128];               // S-CTA: Q_rope rows (f16)
   uint8_t pslot[kNP][kPSlotStride];
+  uint32_t note[4];         // what a note copies, of no meaning (see relay_made)
   float fin[kRows];
   float mref[kRows];        // S-CTA: every row's running reference
   float xch[2][2][kRows];   // S-CTA: per-warpgroup row values at either end
   uint64_t raw_full[kRaw];  // a raw page landed
   uint64_t raw_empty[kRaw]; // the converters are done with it
   uint64_t full[kStages];    // pair leader: both CTAs' boxes of a stage are written
+                             // (its own warps' arrivals, the other CTA's note)
   uint64_t made[kStages];    // pair's other CTA: its boxes of a stage are written
   uint64_t empty[kStages];   // every CTA: its boxes of a stage were consumed
   uint64_t sfull[2];        // S-CTAs: S buffer b holds a tile
@@ -174,10 +178,9 @@ __device__ __forceinline__ void arrive_leader(uint32_t bar, uint32_t rank,
     mbar_arrive_cluster(mapa(bar, lead));
 }
 
-// The same for a signal that only reports completed work: the thread has
-// already waited for its own TMEM loads or stores (tcgen05.wait) or seen the
-// data land on a barrier, so nothing remains to publish and the arrive can be
-// relaxed.  A remote release costs the issuing thread hundreds to thousands
+// The same for a signal that only reports completed reads: the thread has its
+// scores out of TMEM in registers (tcgen05.wait), so nothing remains to publish
+// and the arrive can be relaxed.  A remote release costs the issuing thread hundreds to thousands
 // of cycles under load; a relaxed remote arrive a few.
 __device__ __forceinline__ void signal_leader(uint32_t bar, uint32_t rank,
                                               uint32_t lead) {
@@ -323,6 +326,15 @@ __device__ __forceinline__ void convert_rope_half(uint8_t* box, const uint4& a, 
   *reinterpret_cast<uint4*>(box + box_chunk_offset(t, 4 * h + 3)) = plain8(b.z, b.w);
 }
 
+// A converter warp's arrival for a stage.  One thread of the pair's leader also
+// arms full for the other CTA's note.
+__device__ __forceinline__ void stage_written(uint64_t* bar, bool arms) {
+  if (arms)
+    mbar_arrive_expect_tx(smem_u32(bar), kNoteBytes);
+  else
+    mbar_arrive(smem_u32(bar));
+}
+
 // S-CTA, warps 12..15: page 2j + rank of every tile j, chunk by chunk: two
 // threads per token, 32 dims each (their 16-byte reads of rows 352 bytes apart
 // and their swizzled 16-byte writes are both free of bank conflicts).  The
@@ -387,7 +399,7 @@ __device__ __forceinline__ void convert_s(Smem& s, const Fp4Params& p, const Wor
         if (st + 1 < kStagesS) load_codes(st + 1);
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&done[st]));
+      if (lane == 0) stage_written(&done[st], rank == 0 && tid == 0);
     }
     phase ^= 1u;
     if (!__all_sync(kFull, ok)) break;
@@ -444,7 +456,7 @@ __device__ __forceinline__ void convert_o(Smem& s, const Fp4Params& p, const Wor
                    ((k & 1 ? sn[k >> 1].y : sn[k >> 1].x) >> (16 * h)) & 0xFFFFu, t, h);
     __syncwarp();
     if (lane == 0) {
-      mbar_arrive(smem_u32(&done[stage]));
+      stage_written(&done[stage], rank == 2 && tid == 0);
       mbar_arrive(smem_u32(&s.raw_empty[slot]));
     }
     if (++stage == kStagesO) {
@@ -459,27 +471,32 @@ __device__ __forceinline__ void convert_o(Smem& s, const Fp4Params& p, const Wor
   if (!__all_sync(kFull, ok) && lane == 0) signal_abort(s, p, rank);
 }
 
-// The pair's odd CTA, one thread: passes "stage written" on to the leader.
-// The arrive is relaxed: it reports finished work.  The boxes lie in this SM's
-// own shared memory, each converter warp has arrived on made after its writes, and this thread has
-// seen that phase complete and fences them to the async proxy, so
-// nothing is left to publish to the leader, whose MMA makes this SM's tensor
-// core read them here.  A release arrive held every stage up by its round
-// trip: 1519 us instead of 1298 at 16 x 5 x 96 x 100k tokens, of an earlier
-// state of the kernel.
+// The pair's odd CTA, one thread: passes "stage written" on to the leader, whose
+// MMA reads this CTA's boxes too, by a note: a bulk copy of 16 bytes into the
+// leader that completes on its full barrier.  The converters' stores are ordered
+// before the MMA by made (their release, this thread's acquire), the proxy fence,
+// the copy issued after it, the release of the copy's completion at cluster
+// scope and the leader's acquire.  A relaxed arrive would order nothing; a
+// release arrive does, but holds this thread up for its round trip: at 16 x 5 x
+// 96 x 100k tokens the kernel takes 1595 us with that, 1363 with two threads
+// taking turns at it, and 1113 with notes (1131 where the wait for made may
+// suspend the thread, 1139 where each converter warp sends its own note, 1480
+// with stages of one box; ragged 885, 771, 642, 648, 658 and 827).
 __device__ __forceinline__ void relay_made(Smem& s, const Fp4Params& p, int n, int stages,
                                            uint32_t rank, uint32_t lead) {
   const uint32_t full0 = mapa(smem_u32(&s.full[0]), lead);
+  const uint32_t note = mapa(smem_u32(s.note), lead);
   uint32_t stage = 0, phase = 0;
   for (int i = 0; i < n; ++i) {
-    if (!mbar_wait(smem_u32(&s.made[stage]), phase, &s.abort_flag)) {
-      signal_abort(s, p, rank);
-      return;
-    }
+    const uint64_t t0 = globaltimer();
+    for (uint32_t it = 1; !mbar_test_wait(smem_u32(&s.made[stage]), phase); ++it)
+      if ((it & 63) == 0 &&
+          (*const_cast<volatile int*>(&s.abort_flag) || globaltimer() - t0 > kWaitNs)) {
+        signal_abort(s, p, rank);
+        return;
+      }
     fence_proxy_async_smem();
-    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(
-                     full0 + 8u * stage)
-                 : "memory");
+    bulk_copy_to_peer(note, smem_u32(s.note), kNoteBytes, full0 + 8u * stage);
     if (++stage == (uint32_t)stages) {
       stage = 0;
       phase ^= 1u;
@@ -928,7 +945,9 @@ __device__ __forceinline__ void mma_o(Smem& s, const Fp4Params& p,
 
 // --------------------------------------------------- O pair: relay (rank 3) ----
 // Tells rank 2 when a P message has landed in rank 3 (bulk-copy bytes can
-// only complete on a barrier of the receiving CTA), and re-arms the slot.
+// only complete on a barrier of the receiving CTA), and re-arms the slot.  The
+// arrive is a release: rank 2's MMA reads the message here.  (One thread with
+// nothing else to do, four messages ahead: a note costs the same.)
 __device__ __forceinline__ void relay_o(Smem& s, const Fp4Params& p,
                                         const Work& w, uint32_t rank) {
   const uint32_t pready0 = mapa(smem_u32(&s.pready[0]), 2);
@@ -940,10 +959,7 @@ __device__ __forceinline__ void relay_o(Smem& s, const Fp4Params& p,
     }
     if (m + kNP < w.npages)
       mbar_arrive_expect_tx(smem_u32(&s.pfull[k]), kPMsgBytes);
-    asm volatile(
-        "mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(
-            pready0 + 8u * k)
-        : "memory");
+    mbar_arrive_cluster(pready0 + 8u * k);
   }
 }
 
@@ -1128,7 +1144,7 @@ __device__ __forceinline__ void correct_and_store(Smem& s, const Fp4Params& p,
     }
     tc_fence_before();
     __syncwarp();
-    if (lane == 0) signal_leader(smem_u32(&s.corr_done), rank, 2);
+    if (lane == 0) arrive_leader(smem_u32(&s.corr_done), rank, 2);
   }
   if (ok && !mbar_wait(smem_u32(&s.fin_full), 0, &s.abort_flag)) ok = false;
   if (!__all_sync(kFull, ok)) {
@@ -1174,7 +1190,7 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1)
     s.ctl_final = 0;
     s.ctl_last = 0;
     for (int i = 0; i < kStages; ++i) {
-      mbar_init(smem_u32(&s.full[i]), 5);  // 4 local warps + the other CTA's relay
+      mbar_init(smem_u32(&s.full[i]), 4);  // 4 local warps; and the other CTA's note
       mbar_init(smem_u32(&s.made[i]), 4);
       mbar_init(smem_u32(&s.empty[i]), 1);
     }
