@@ -95,7 +95,8 @@ enum {
  * suits; values beyond 2688 g (c_kv) and 448 g (rope) saturate.  The decode's
  * products run in f16 with fp32 sums: codes times block scales and RoPE codes
  * are exact there, queries are scaled per row by a power of two (exact down to
- * 2^-31 of the row's largest), probabilities are rounded to f16 (2^-11). */
+ * 2^-31 of the row's largest), probabilities are rounded to f16: by 2^-11 of
+ * themselves or by 2^-32 of the part's largest, whichever is more. */
 typedef enum {
   MLA_KV_BF16 = 0,
   MLA_KV_FP8_E4M3 = 1,

@@ -18,10 +18,10 @@
 //   1 thread       issues 36 MMAs of M = 64, N, K = 16 for the next page's S^T
 //                  and this page's 4 per 128 value dims of O^T (M = 128);
 //   4 or 8 warps   softmax: a thread has one token's scores of 8 to 24 rows.  The
-//                  running references only change when some score passes its
-//                  row's by 2^8: one vote per page; then the maxima cross the
-//                  lanes and warps and O^T (lane = dim) is rescaled in place.
-//                  Row sums stay per thread until the end.
+//                  running references only change when some score passes the
+//                  maximum its row's came from by 2^8: one vote per page; then
+//                  the maxima cross the lanes and warps and O^T (lane = dim) is
+//                  rescaled in place.  Row sums stay per thread until the end.
 // P (f16, row by row over the tokens) and Q (f16, mla_tc_fp4.cu's row scale)
 // are the K-major B operands in shared memory.
 //
@@ -620,7 +620,7 @@ __device__ __forceinline__ void softmax(typename Few<N>::Smem& s, const Fp4Param
       if (k % 8 == 0) asm volatile("" ::: "memory");  // no more loads ahead: registers
       y[k] = __uint_as_float(x[k]) * s.sc[n0 + k];
       if (!open && t0 + tok >= s.lim[n0 + k]) y[k] = -INFINITY;
-      over |= y[k] > s.mref[n0 + k] + kTau;
+      over |= y[k] > s.mref[n0 + k] + (kLift + kTau);
     }
     if (any_of<T>(over)) {
       // Some row's maximum rises: the page's maxima over its 64 tokens.
@@ -638,9 +638,10 @@ __device__ __forceinline__ void softmax(typename Few<N>::Smem& s, const Fp4Param
                                fmaxf(s.wred[2][dim], s.wred[3][dim]));
         const float old = s.mref[dim];
         float a = 1.f;
-        if (mt > -INFINITY && (old == -INFINITY || mt > old + kTau)) {
-          if (old > -INFINITY) a = ex2(old - mt);  // else O and l are still zero
-          s.mref[dim] = mt;
+        if (mt > -INFINITY && (old == -INFINITY || mt > old + (kLift + kTau))) {
+          const float ref = mt - kLift;
+          if (old > -INFINITY) a = ex2(old - ref);  // else O and l are still zero
+          s.mref[dim] = ref;
         }
         alpha[dim] = a;
       }
@@ -672,8 +673,8 @@ __device__ __forceinline__ void softmax(typename Few<N>::Smem& s, const Fp4Param
         }
       }
     }
-    // p = 2^(y - m_ref) (0 for a row that has seen nothing yet), f16 at
-    // [row][token] once the outputs before have read this buffer.
+    // p = 2^(y - m_ref) (0 for a row that has seen nothing yet), f16 (see kLift)
+    // at [row][token] once the outputs before have read this buffer.
     if (m >= F::kPBufs)
       ok = ok && mbar_wait_cta(smem_u32(&s.odone[pb]), (m / F::kPBufs - 1) & 1, &s.abort_flag);
     uint8_t* const dst = dst0 + pb * F::kQBox;

@@ -728,10 +728,11 @@ __device__ __forceinline__ void softmax_end(Smem& s, const Fp4Params& p, const W
 __device__ __forceinline__ float next_reference(float m_old, float mt, float& alpha) {
   alpha = 1.f;
   if (!(mt > -INFINITY)) return m_old;
-  if (m_old == -INFINITY) return mt;  // first visible token of this row: O is zero
-  if (!(mt > m_old + kTau)) return m_old;
-  alpha = ex2(m_old - mt);
-  return mt;
+  const float m_new = mt - kLift;
+  if (m_old == -INFINITY) return m_new;  // first visible token of this row: O is zero
+  if (!(mt > m_old + (kLift + kTau))) return m_old;
+  alpha = ex2(m_old - m_new);
+  return m_new;
 }
 
 // Warps 4..11 of each S-CTA: warpgroup g (warps 4-7, 8-11) takes the tiles j
@@ -817,7 +818,7 @@ __device__ __forceinline__ void softmax(Smem& s, const Fp4Params& p, const Work&
       if (q == 1 && !two) break;
       // p = 2^(x * scale - m_ref): one packed FMA per pair of columns, the
       // row sum of the unrounded p in two packed accumulators.  P is shipped
-      // as f16: at most 2^8 by the lazy rescaling, 2^-11 relative rounding.
+      // as f16 (see kLift): off by 2^-11 of itself or by 2^-25, whichever is more.
       uint32_t pk[32];
       uint64_t acc0 = f2pack(0.f, 0.f), acc1 = acc0;
 #pragma unroll

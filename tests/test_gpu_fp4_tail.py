@@ -2,9 +2,9 @@
 output consists of: one token holds the maximum and a value of zero, tens of
 thousands lie 17 to 19 nats below it and all point the same way.
 
-A probability reaches the second product as f16 at 2^6 or more of its reference's 1,
-so it is off by 2^-11 of itself or, where that is less, by half of f16's last
-step: 2^-25 / 2^6 of the row's maximum, which is a bound of 2^-31 |v| for each token.
+A probability reaches the second product as f16, the row's maximum at 2^6 or more,
+so it is off by 2^-11 of itself or, where that is more, by half of f16's last
+step: 2^-25 / 2^6 of the maximum, which is a bound of 2^-31 |v| for each token.
 """
 import numpy as np
 import pytest
@@ -65,6 +65,31 @@ def check_tail(case, O, LSE, S):
 @pytest.mark.parametrize("at", [0, 9000])
 def test_long_tail_few_rows(H, at):
     case = tail_case(1, H, 20011, at)
+    O, LSE = case.run(1)
+    assert case.status == 0
+    check_tail(case, O, LSE, 1)
+
+
+@pytest.mark.parametrize("q,H", [(1, 97), (2, 96), (5, 96)])
+@pytest.mark.parametrize("at", [0, 9000])
+@pytest.mark.parametrize("S", [1, 3])
+def test_long_tail_clusters(q, H, at, S):
+    """More than 96 rows; parts without the sink have the tail as their maximum."""
+    case = tail_case(q, H, 20011, at)
+    O, LSE = case.run(S)
+    assert case.status == 0
+    check_tail(case, O, LSE, S)
+
+
+@pytest.mark.parametrize("q,H", [(1, 16), (1, 96), (5, 96)])
+def test_rising_maxima_keep_the_tail(q, H):
+    """Sinks that rise by two nats along the context: sums and outputs are rescaled
+    again and again, by references that lie below the maxima they come from."""
+    case = tail_case(q, H, 6011, 6000)
+    rows = case.r2t_host[0, 100:6000:600]
+    case.kv_host[rows, :256] = 0
+    case.kv_host[rows, 288] = encode(44.8 * np.arange(10), E4M3)
+    case.up()
     O, LSE = case.run(1)
     assert case.status == 0
     check_tail(case, O, LSE, 1)
