@@ -5,6 +5,8 @@
 
 #include <cuda_bf16.h>
 
+#include <cfloat>
+
 #include "mla_fp4.cuh"
 #include "mla_internal.h"
 #include "ptx_sm103.cuh"
@@ -71,6 +73,15 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
+}
+
+// The factor of a row's raw scores: scale_log2 * g * row, row the power of two
+// that its queries were divided by.  Kept a normal number: 0 or an infinity would
+// make NaN of a masked column's -inf or of a score of 0, and below 2^-126 every
+// score is 0 to the last bit of its exponential anyway.
+__device__ __forceinline__ float score_factor(float scale_log2, float g, float row) {
+  const float sc = scale_log2 * row * g;
+  return sc < FLT_MIN ? FLT_MIN : sc > FLT_MAX ? FLT_MAX : sc;
 }
 
 // The kernel for requests of at most kFp4FewRows query rows (mla_fp4_few.cu).

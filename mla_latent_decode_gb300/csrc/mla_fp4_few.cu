@@ -224,7 +224,7 @@ __device__ __forceinline__ void place_query(typename Few<N>::Smem& s, const Fp4P
       lim = lim > w.L ? w.L : (lim < 0 ? 0 : lim);
     }
     s.lim[n] = (int32_t)lim;
-    s.sc[n] = p.scale_log2 * g * mine;
+    s.sc[n] = score_factor(p.scale_log2, g, mine);
     s.mref[n] = -INFINITY;
   }
   __syncwarp();

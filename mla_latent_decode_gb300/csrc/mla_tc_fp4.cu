@@ -674,8 +674,9 @@ __device__ __forceinline__ SoftmaxRow softmax_begin(Smem& s, const Fp4Params& p,
   t.qrow = (int64_t)w.b * p.q_len * p.H + rr;
   t.pool = p.g[0];
   t.ok = mbar_wait(smem_u32(&s.qbar), 0, &s.abort_flag);
-  t.sc = p.scale_log2 * t.pool *
-         place_query(s, tmem, (uint32_t)(quad * 32) << 16, (warp - 4) >> 2, t.r, t.in_range);
+  t.sc = score_factor(
+      p.scale_log2, t.pool,
+      place_query(s, tmem, (uint32_t)(quad * 32) << 16, (warp - 4) >> 2, t.r, t.in_range));
   if (warp == 4 && lane == 0) {
     mbar_arrive(smem_u32(&s.qmoved));
     arrive_leader(smem_u32(&s.qready), rank, 0);
