@@ -108,12 +108,29 @@ __device__ __forceinline__ void append_row(const AppendParams& p, int64_t r, int
     float w[2][8];
     unpack8(wp[0], w[0]);
     unpack8(wp[1], w[1]);
-    float s = 0.f;
+    float eps = p.eps;
+    const auto mean_square = [&]() -> float {
+      float s = 0.f;
 #pragma unroll
-    for (int k = 0; k < 16; ++k) s = fmaf(c[k / 8][k % 8], c[k / 8][k % 8], s);
+      for (int k = 0; k < 16; ++k) s = fmaf(c[k / 8][k % 8], c[k / 8][k % 8], s);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(kAll, s, o);
-    const float rs = 1.0f / sqrtf(s * (1.0f / MLA_NOPE_DIM) + p.eps);
+      for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(kAll, s, o);
+      return s * (1.0f / MLA_NOPE_DIM);
+    };
+    float mean = mean_square();
+    if (squares_leave_range(mean, eps)) {  // warp-uniform
+      float top = 0.f;
+#pragma unroll
+      for (int k = 0; k < 16; ++k) top = fmaxf(top, fabsf(c[k / 8][k % 8]));
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, o));
+      const float f = unit_factor(top);
+#pragma unroll
+      for (int k = 0; k < 16; ++k) c[k / 8][k % 8] *= f;
+      eps = eps * f * f;
+      mean = mean_square();
+    }
+    const float rs = 1.0f / sqrtf(mean + eps);
 #pragma unroll
     for (int k = 0; k < 16; ++k) c[k / 8][k % 8] = c[k / 8][k % 8] * rs * w[k / 8][k % 8];
   }

@@ -77,6 +77,21 @@ __device__ __forceinline__ float2 h2_to_f32(uint32_t h) {
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
+// RMS norms of rows whose squares leave fp32's range: above about 2^60 a value
+// their sum overflows, and without an eps it loses its bits below 2^-50.  Such a
+// row is divided by the power of two of its largest value (exact) and takes eps
+// by that power's square: the norm is the same.
+__device__ __forceinline__ bool squares_leave_range(float mean, float eps) {
+  return !(mean < INFINITY) || (mean < 0x1p-100f && eps == 0.f);
+}
+// 2^-e of the largest value top = m 2^e, kept a normal number; 1 for a row of
+// zeros and for one that is not finite.
+__device__ __forceinline__ float unit_factor(float top) {
+  const int e = (int)(__float_as_uint(top) >> 23);  // biased; top >= 0
+  return top > 0.f && top < INFINITY ? __uint_as_float((uint32_t)max(1, min(254 - e, 253)) << 23)
+                                     : 1.f;
+}
+
 // Quotients by one divisor b > 0: a / b from y = RN(1 / b) and one Markstein
 // correction (P. Markstein, "Computation of elementary functions on the IBM
 // RISC System/6000 processor", IBM J. Res. Dev. 34(1), 1990): three
