@@ -157,7 +157,7 @@ __device__ __forceinline__ void append_row(const AppendParams& p, int64_t r, int
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kAll, amax, o));
     const float scale = __fdiv_rn(amax, 448.0f);
-    const Divisor by(scale);
+    const Divisor by(scale, amax);
     auto code = [&](float x, float y) -> uint32_t { return e4m3_pair(by(x), by(y)); };
     uint32_t w[4];
 #pragma unroll
@@ -180,7 +180,7 @@ __device__ __forceinline__ void append_row(const AppendParams& p, int64_t r, int
   const float g = p.kv_scale[0];
   const uint32_t s8 = e4m3_pair(__fdiv_rn(amax, 6.0f * g), 0.f) & 0xFFu;
   const float step = h2_to_f32(e4m3x2_to_f16(s8)).x * g;
-  const Divisor by(step);
+  const Divisor by(step, amax);
   uint32_t w[2];
 #pragma unroll
   for (int k = 0; k < 2; ++k) {

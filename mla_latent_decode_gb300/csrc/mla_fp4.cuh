@@ -97,14 +97,18 @@ __device__ __forceinline__ float unit_factor(float top) {
 // RISC System/6000 processor", IBM J. Res. Dev. 34(1), 1990): three
 // instructions instead of a full division, off by at most one unit in the last
 // place and exact for quotients of few bits, so a code's tie stays a tie.
-// Divisors whose reciprocal leaves the normal range divide directly; b = 0
-// gives 0.
+// Divisors whose reciprocal leaves the normal range divide directly, and so do
+// those by which the largest dividend's quotient overflows (its correction would
+// be inf - inf); b = 0 gives 0.
 struct Divisor {
   float b, y;
   bool direct;
-  __device__ __forceinline__ explicit Divisor(float d)
+  __device__ __forceinline__ Divisor(float d, float largest)
       : b(d), y(0.f), direct(!(d >= 0x1p-90f && d <= 0x1p+120f)) {
-    if (!direct) y = __frcp_rn(d);
+    if (!direct) {
+      y = __frcp_rn(d);
+      direct = !(__fmul_rn(largest, y) < INFINITY);
+    }
   }
   __device__ __forceinline__ float operator()(float a) const {
     if (direct) return b == 0.f ? 0.f : __fdiv_rn(a, b);

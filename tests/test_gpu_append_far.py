@@ -54,3 +54,18 @@ def test_norm_of_one_large_value():
     got = f64(kv[:2])[:, :NOPE]
     # 2^-17 of the norm and 2^-8 of bf16; below fp32's normal range, 2^-133 (bf16's last step)
     assert np.all(np.abs(got - want) <= (2.0 ** -8 + 2.0 ** -17) * np.abs(want) + 2.0 ** -133)
+
+
+@pytest.mark.parametrize("g", [2.0 ** -60, 2.0 ** -85, 2.0 ** -120, 2.0 ** -140, 2.0 ** -149])
+def test_far_values_saturate_with_their_sign(g):
+    """Without the norm: values some 2^200 times the factor, of either sign."""
+    rows = torch.full((1, ROW), 3e38).bfloat16().cuda()
+    rows[0, 1::2] = -3e38
+    kv, _ = _pool("fp4", 64)
+    at, pos = torch.zeros(1, dtype=torch.int32, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    mla.kv_append(rows, at, pos, table(1).cuda(), kv, torch.full((1,), g, device="cuda"))
+    raw = kv[0].cpu().numpy()
+    assert np.all(raw[:256] == 0xF7)          # +6 and -6
+    assert np.all(raw[256:288] == 0x7E)       # 448
+    sign = np.where(np.arange(64) % 2, 0x80, 0)
+    assert np.all(raw[288:] == 0x7E | sign)
