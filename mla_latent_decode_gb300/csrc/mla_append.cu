@@ -178,7 +178,8 @@ __device__ __forceinline__ void append_row(const AppendParams& p, int64_t r, int
   }
   // FP4: this lane's block of 16 and its scale; the pool's factor g is fixed.
   const float g = p.kv_scale[0];
-  const uint32_t s8 = e4m3_pair(__fdiv_rn(amax, 6.0f * g), 0.f) & 0xFFu;
+  const float f = g > 0x1p+120f ? 0x1p-4f : 1.0f;  // 6 g stays in range
+  const uint32_t s8 = e4m3_pair(__fdiv_rn(amax * f, 6.0f * (g * f)), 0.f) & 0xFFu;
   const float step = h2_to_f32(e4m3x2_to_f16(s8)).x * g;
   const Divisor by(step, amax);
   uint32_t w[2];

@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import mla_latent_decode_gb300 as mla
-from latent_ref import NOPE, ROW, f64, table
+from latent_ref import E4M3, NOPE, ROW, decode4, e4m3_values, encode, f64, sure, table
 from mla_latent_decode_gb300 import build
 from test_gpu_append import _inputs, _pool
 
@@ -69,3 +69,25 @@ def test_far_values_saturate_with_their_sign(g):
     assert np.all(raw[256:288] == 0x7E)       # 448
     sign = np.where(np.arange(64) % 2, 0x80, 0)
     assert np.all(raw[288:] == 0x7E | sign)
+
+
+@pytest.mark.parametrize("g", [2.0 ** 125, 2.0 ** 126, 1.5 * 2.0 ** 127])
+def test_large_factors(g):
+    """Six times the factor is past fp32's range: blocks still get their scales."""
+    n = 6
+    rows = torch.randn((n, ROW), generator=torch.Generator().manual_seed(23)).clamp(-3, 3)
+    rows = (rows.double() * 2.0 ** 126).float().bfloat16().cuda()
+    assert rows.isfinite().all()
+    kv, _ = _pool("fp4", 64)
+    at, pos = torch.arange(n, dtype=torch.int32, device="cuda"), torch.zeros(n, dtype=torch.int32, device="cuda")
+    gd = torch.full((1,), g, device="cuda")
+    mla.kv_append(rows, at, pos, table(1).cuda(), kv, gd)
+    raw, x = kv[:n].cpu().numpy(), f64(rows)
+    quo = np.abs(x[:, :NOPE].reshape(n, 32, 16)).max(-1) / (6 * g)
+    fixed = sure(quo, E4M3, 2.0 ** -17)
+    assert fixed.mean() > 0.9 and quo.min() > 2.0 ** -6
+    assert np.array_equal(raw[:, 256:288][fixed], encode(quo, E4M3)[fixed])
+    step = np.repeat(e4m3_values(raw[:, 256:288]) * g, 16, 1)
+    got = decode4(raw, g)
+    # within half of E2M1's widest step of the block's, or the saturated last part of it
+    assert np.all(np.abs(got[:, :NOPE] - x[:, :NOPE]) <= step)
