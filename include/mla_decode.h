@@ -506,7 +506,8 @@ int mla_kv_write(const void* rows, int64_t n, const int32_t* slots,
  *          (scale j * g)) (codes 0 where that is 0), rope code = E4M3(rope /
  *          g); all to nearest even, saturated.
  *   rows         bf16, row r at rows + r * row_stride elements (>= 576, a
- *                multiple of 8), 16-B aligned; finite
+ *                multiple of 8), 16-B aligned; finite, of any magnitude (the norm
+ *                scales rows whose squares leave fp32's range by a power of two)
  *   norm_weight  bf16 [512] or NULL, 16-B aligned;  eps finite, >= 0
  *   slots        int32 [n]: a slot outside [0, num_slots) is skipped
  *                (MLA_STATUS_BAD_SLOT; its queries are still rotated)
@@ -549,6 +550,8 @@ int mla_kv_read(const void* kv_pages, mla_kv_dtype kv_dtype,
  *   448 over the row (group 0) or over each `group` values (32, 64 or 128; d a
  *   multiple of it); a group of zeros gets scale 0 and codes 0, one that holds a
  *   NaN scale NaN and codes NaN (0x7F).
+ * Rows of any magnitude: where the squares leave fp32's range (and, without an
+ * eps, below 2^-50) the row is scaled by a power of two first.
  * Values need not be finite: an infinite h makes its own y NaN and the row's
  * others 0, a NaN the whole row, as the formula has it.
  *   x, residual, residual_out, out   bf16 rows at their strides (elements);

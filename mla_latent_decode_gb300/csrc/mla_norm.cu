@@ -16,7 +16,7 @@
 // maximum) crosses the warps through shared memory once.  Few rows take a
 // thread per vector, the shortest chain; many rows of 513 to 1024 vectors four
 // vectors a thread and four blocks per SM, whose phases overlap.  Measured on a
-// GB300 at 16383 x 7168, groups of 128 (822 MB): 150 us, 5.5 TB/s, 82% of the
+// GB300 at 16383 x 7168, groups of 128 (822 MB): 153 us, 5.4 TB/s, 80% of the
 // copy rate (three blocks 173, five 172, two vectors a thread 185, one 178; a
 // resident grid that loads the next row ahead, two blocks of 125 registers,
 // 249); 80 x 7168: 3.0 us.
@@ -165,9 +165,13 @@ __device__ __forceinline__ float block_reduce(float v, float* part) {
 // to seven values and changing from row to row, as with an odd d; the vectors
 // start on the boundary before the row and the weight, which does not shift with
 // it, is read by element (6000 x 7001: 72 us, every array by element 152).
+//
+// Blocks per SM asked for: four of 256 threads for four vectors (see above), and
+// 32 registers for one vector a thread (6000 x 1536: 12.4 us, with 36 14.4).
 template <int V, int L, int T>
-__global__ void __launch_bounds__(T, T == 256 && V == 4 ? 4 : 1) mla_norm_kernel(const NormParams p) {
-  __shared__ float part[3][32];
+__global__ void __launch_bounds__(T, T == 256 && V == 4 ? 4 : V == 1 && L == kVec ? 2 : 1)
+    mla_norm_kernel(const NormParams p) {
+  __shared__ float part[4][32];
   const int64_t r = blockIdx.x;
   const int shift = L == kShift ? (int)((p.shift + r * p.x_stride) & 7) : 0;
   const auto col = [&](int k) {
@@ -192,27 +196,36 @@ __global__ void __launch_bounds__(T, T == 256 && V == 4 ? 4 : 1) mla_norm_kernel
       acc = fma2(h[k][e], h[k][e], acc);
     }
   const float inv_d = 1.0f / (float)p.d;
-  float mean = block_reduce<false>(both(acc).x + both(acc).y, part[0]) * inv_d;
-  if (!(mean < INFINITY)) {
-    // The squares' sum overflowed (or holds a NaN): sum the mean, which only
-    // overflows where the mean square itself does.
-    float ss = 0.f;
+  const float mean = block_reduce<false>(both(acc).x + both(acc).y, part[0]) * inv_d;
+  // every row element has been read: the residual may be updated in place
+  const auto store_residual = [&] {
+#pragma unroll
+    for (int k = 0; k < V; ++k)
+      if (col(k) < p.d) store8<L>(p.res_out + r * p.res_out_stride, col(k), p.d, h[k]);
+  };
+  float ms = mean + p.eps;
+  const bool far = squares_leave_range(mean, p.eps);  // the same in every thread
+  if (far) {
+    if (p.res_out) store_residual();  // h as it is; scaled from here on
+    float top = 0.f, ss = 0.f;
+#pragma unroll
+    for (int k = 0; k < V; ++k)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        top = fmaxf(top, fmaxf(fabsf(both(h[k][e]).x), fabsf(both(h[k][e]).y)));
+    const float f = unit_factor(block_reduce<true>(top, part[1]));
 #pragma unroll
     for (int k = 0; k < V; ++k)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
+        h[k][e] = mul2(h[k][e], pair(f, f));
         const float2 v = both(h[k][e]);
-        ss = fmaf(v.y, v.y * inv_d, fmaf(v.x, v.x * inv_d, ss));
+        ss = fmaf(v.y, v.y, fmaf(v.x, v.x, ss));
       }
-    mean = block_reduce<false>(ss, part[1]);
+    ms = block_reduce<false>(ss, part[2]) * inv_d + p.eps * f * f;
   }
-  // every row element has been read: the residual may be updated in place
-  if (p.res_out) {
-#pragma unroll
-    for (int k = 0; k < V; ++k)
-      if (col(k) < p.d) store8<L>(p.res_out + r * p.res_out_stride, col(k), p.d, h[k]);
-  }
-  const float rs = 1.0f / sqrtf(mean + p.eps);
+  if (p.res_out && !far) store_residual();
+  const float rs = 1.0f / sqrtf(ms);
   const uint64_t rs2 = pair(rs, rs);
   float amax[V], rowmax = 0.f;
 #pragma unroll
@@ -227,7 +240,7 @@ __global__ void __launch_bounds__(T, T == 256 && V == 4 ? 4 : 1) mla_norm_kernel
     rowmax = max_nan(rowmax, amax[k]);
   }
   if (!p.out8) return;
-  if (p.group == 0) rowmax = block_reduce<true>(rowmax, part[2]);
+  if (p.group == 0) rowmax = block_reduce<true>(rowmax, part[3]);
 #pragma unroll
   for (int k = 0; k < V; ++k) {
     if (p.group == 0) {
