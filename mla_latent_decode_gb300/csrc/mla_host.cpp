@@ -586,15 +586,17 @@ int mla_plan_sched(int B, int q_len, int H, int num_shards,
   const double split = kPlanSplitCost * rows / 1024;  // in the clusters' pages
   const int ctas = num_sms > 0 ? num_sms : decode_slots(kv_dtype, 1, 1, 0);
   if (ctas < 1) return ctas;
-  std::vector<int32_t> pages((size_t)V * 65), work((size_t)std::max<int64_t>(work_capacity, 0));
+  const int s_max = plan_s_max(false);
+  const int64_t groups = ((int64_t)q_len * H + kFp4FewRows - 1) / kFp4FewRows;
+  const int64_t most = std::min(work_capacity, (int64_t)V * s_max * groups);
+  std::vector<int32_t> pages((size_t)V * (s_max + 1)), work((size_t)std::max<int64_t>(most, 0));
   int parts = 0;
   int64_t n = 0;
   float eff = 0;
   double span_g = 0;
-  if (mla_plan_sched_ex(V, q_len, H, kFp4FewRows, seq_lens_host, ctas, plan_s_max(false),
-                        max_parts, kPlanUnitCostGroup, kPlanSplitCost / kPlanGroupPage,
-                        pages.data(), &parts, work.data(), work_capacity, &n, &eff,
-                        &span_g) != MLA_OK ||
+  if (mla_plan_sched_ex(V, q_len, H, kFp4FewRows, seq_lens_host, ctas, s_max, max_parts,
+                        kPlanUnitCostGroup, kPlanSplitCost / kPlanGroupPage, pages.data(),
+                        &parts, work.data(), most, &n, &eff, &span_g) != MLA_OK ||
       kPlanGroupPage * span_g + split * parts >= span + split * *num_parts_out)
     return MLA_OK;
   std::copy(pages.begin(), pages.begin() + (size_t)V * (parts + 1), split_pages_out);

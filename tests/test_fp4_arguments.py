@@ -186,3 +186,17 @@ def test_binding_appends_no_tokens_with_queries(lib, monkeypatch):
     rows, ids = torch.zeros((0, 576), dtype=bf), torch.zeros(0, dtype=i32)
     got = mla.kv_append(rows, ids, ids, torch.zeros((8, 64)), kv, g, q_rope=torch.zeros((5, 3, 64), dtype=bf)[:0])
     assert got.shape == (0, 3, 64) and got.dtype == bf
+
+
+@pytest.mark.parametrize("capacity", [1 << 62, (1 << 63) - 1, 1 << 40])
+def test_plan_takes_any_capacity(lib, capacity):
+    """The capacity bounds what is written; it is not a size to allocate."""
+    B, q, H = 2, 3, 128
+    bnd, work = (ctypes.c_int32 * (B * 65))(), (ctypes.c_int32 * (B * 64 * 4))()
+    S, n, eff = ctypes.c_int(), ctypes.c_int64(), ctypes.c_float()
+    lens = (ctypes.c_int32 * B)(300, 300)
+    rc = lib.mla_plan_sched(B, q, H, 1, 2, lens, 152, 8, bnd, ctypes.byref(S), work, capacity, ctypes.byref(n),
+                            ctypes.byref(eff))
+    want = mla.plan_sched(B, q, H, [300] * B, num_sms=152, kv_dtype="fp4_e2m1")
+    assert rc == 0 and S.value == want[0] and list(work[:n.value]) == list(want[2])
+    assert list(bnd[:B * (S.value + 1)]) == list(want[1].reshape(-1))
