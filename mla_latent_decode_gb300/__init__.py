@@ -462,9 +462,8 @@ def kv_write(rows, slots, kv, kv_scale=None, status=None, stream=None):
     """Store bf16 latent rows [n, 576] at `slots` of the pool `kv` (bf16, or
     uint8 E4M3 bytes with `kv_scale`); see mla_kv_write."""
     n = rows.shape[0]
-    _check(library().mla_kv_write(_ptr(rows), n, _ptr(slots), _ptr(kv),
-                                  _kv_dtype(kv), _ptr(kv_scale), kv.shape[0],
-                                  _ptr(status), _stream(stream)))
+    _launch(kv, stream, library().mla_kv_write, _ptr(rows), n, _ptr(slots), _ptr(kv),
+            _kv_dtype(kv), _ptr(kv_scale), kv.shape[0], _ptr(status))
 
 
 def _rows_arg(t: torch.Tensor, name: str, n: int, width: int, dtype=torch.bfloat16):
@@ -604,8 +603,8 @@ def absorb_q(q_nope, w_kc, out=None, status=None, stream=None):
     B, q, H, _ = q_nope.shape
     if out is None:
         out = torch.empty((B, q, H, NOPE_DIM), dtype=torch.bfloat16, device=q_nope.device)
-    _check(library().mla_absorb_q(_ptr(q_nope), _ptr(w_kc), _ptr(out), B * q, H,
-                                  _ptr(status), _stream(stream)))
+    _launch(q_nope, stream, library().mla_absorb_q, _ptr(q_nope), _ptr(w_kc), _ptr(out), B * q, H,
+            _ptr(status))
     return out
 
 
@@ -615,8 +614,8 @@ def project_out(o_latent, w_vc, out=None, status=None, stream=None):
     B, q, H, _ = o_latent.shape
     if out is None:
         out = torch.empty((B, q, H, 128), dtype=torch.bfloat16, device=o_latent.device)
-    _check(library().mla_project_out(_ptr(o_latent), _ptr(w_vc), _ptr(out), B * q,
-                                     H, _ptr(status), _stream(stream)))
+    _launch(o_latent, stream, library().mla_project_out, _ptr(o_latent), _ptr(w_vc), _ptr(out),
+            B * q, H, _ptr(status))
     return out
 
 
@@ -633,8 +632,8 @@ def lse_combine(O_part, LSE_part, out=None, lse_out=None, stream=None):
         lse_out = torch.empty(tuple(shape[lead:]), dtype=torch.float32, device=O_part.device)
     fn = (library().mla_lse_combine_bf16_parts if O_part.dtype == torch.bfloat16
           else library().mla_lse_combine)
-    _check(fn(O_part.data_ptr(), LSE_part.data_ptr(), parts, LSE_part.numel() // parts,
-              out.data_ptr(), lse_out.data_ptr(), _stream(stream)))
+    _launch(O_part, stream, fn, O_part.data_ptr(), LSE_part.data_ptr(), parts,
+            LSE_part.numel() // parts, out.data_ptr(), lse_out.data_ptr())
     return out, lse_out
 
 
@@ -642,10 +641,9 @@ def debug_gather(kv, req_to_token, seq_lens, row_offset, total_rows: int,
                  stream=None):
     """Raw-byte gather of every live token row through the TMA path."""
     out = torch.empty((max(total_rows, 1), ROW_DIM), dtype=kv.dtype, device=kv.device)
-    _check(library().mla_debug_gather(
-        _ptr(kv), _kv_dtype(kv), kv.shape[0], _ptr(req_to_token),
-        req_to_token.stride(0), _ptr(seq_lens), _ptr(row_offset),
-        req_to_token.shape[0], PAGE_SIZE, _ptr(out), _stream(stream)))
+    _launch(kv, stream, library().mla_debug_gather, _ptr(kv), _kv_dtype(kv), kv.shape[0],
+            _ptr(req_to_token), req_to_token.stride(0), _ptr(seq_lens), _ptr(row_offset),
+            req_to_token.shape[0], PAGE_SIZE, _ptr(out))
     return out[:total_rows]
 
 
