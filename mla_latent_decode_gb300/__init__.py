@@ -306,32 +306,67 @@ def check_page_table(req_to_token, seq_lens, kv_limit, q_len: int,
 
 
 # ------------------------------------------------------------------ kernels
+_BF16, _F32, _I32, _BYTES = (torch.bfloat16, torch.float32, torch.int32,
+                             (torch.uint8, torch.float8_e4m3fn))
+
+
 def _kv_dtype(kv: torch.Tensor) -> int:
-    if kv.dtype == torch.bfloat16:
+    dtype = kv.dtype
+    if dtype is _BF16:
         return KV_BF16
-    if kv.dtype in (torch.uint8, torch.float8_e4m3fn):
+    if dtype in _BYTES:
         # the two byte pools differ in their row: 576 E4M3 codes, or 352 bytes
         return KV_FP4_E2M1 if kv.shape[-1] == FP4_ROW_BYTES else KV_FP8_E4M3
     raise TypeError(f"kv dtype {kv.dtype}: expected bfloat16 or uint8 (E4M3, FP4)")
 
 
-def _check_fp4(q_nope, q_rope, kv, kv_scale, req_to_token, seq_lens) -> None:
+def _not_a_buffer(t: torch.Tensor, name: str, dtype, n: int) -> ValueError:
+    return ValueError(f"{name}: expected {n} contiguous {dtype} values, got {t.dtype} "
+                      f"{tuple(t.shape)} with strides {t.stride()}")
+
+
+def _check_buffer(t: torch.Tensor, name: str, dtype, n: int) -> None:
+    """An array that the library reads or writes by its address alone."""
+    if t.dtype is not dtype or t.numel() < n or not t.is_contiguous():
+        raise _not_a_buffer(t, name, dtype, n)
+
+
+def _check_fp4(shape, q_nope, q_rope, kv, kv_scale, req_to_token, seq_lens, kv_limit, num_shards,
+               num_splits, split_pages, work, status) -> int:
     """The layouts the FP4 decode reads (its pool and its queries are told from
-    the other formats' by shape, so a wrong one is refused here)."""
-    rows = q_nope.numel() // NOPE_DIM
-    if q_nope.dtype is not torch.bfloat16 or q_nope.shape[3] != NOPE_DIM or not q_nope.is_contiguous():
+    the other formats' by shape, so a wrong one is refused here); returns the
+    number of query rows.  shape: q_nope's.  (An attribute of a tensor costs 0.06
+    to 0.2 us, a call 0.1, and a small decode takes 9: each is read once, in place.)"""
+    B, q_len, H, width = shape
+    rows, V = B * q_len * H, B * num_shards
+    if q_nope.dtype is not _BF16 or width != NOPE_DIM or not q_nope.is_contiguous():
         raise ValueError("q_nope: expected contiguous bfloat16 [B, q_len, H, 512], got "
                          f"{q_nope.dtype} {tuple(q_nope.shape)} with strides {q_nope.stride()}")
-    if q_rope.dtype is not torch.bfloat16 or q_rope.numel() != rows * ROPE_DIM or not q_rope.is_contiguous():
+    if q_rope.dtype is not _BF16 or q_rope.numel() != rows * ROPE_DIM or not q_rope.is_contiguous():
         raise ValueError("q_rope: expected contiguous bfloat16 [B, q_len, H, 64], got "
                          f"{q_rope.dtype} {tuple(q_rope.shape)} with strides {q_rope.stride()}")
-    if not kv.is_contiguous() or kv.dim() != 2:
+    if not kv.is_contiguous() or kv.ndim != 2:
         raise ValueError(f"kv: expected a contiguous [num_slots, {FP4_ROW_BYTES}] pool")
-    if kv_scale is None or kv_scale.dtype is not torch.float32 or kv_scale.numel() < 1:
+    if kv_scale is None or kv_scale.dtype is not _F32 or kv_scale.numel() < 1:
         raise ValueError("kv_scale: expected one float32 value, the pool's factor")
-    if req_to_token.dtype is not torch.int32 or req_to_token.stride(1) != 1 or \
-            seq_lens.dtype is not torch.int32 or not seq_lens.is_contiguous():
-        raise ValueError("req_to_token, seq_lens: expected int32 with contiguous rows")
+    if req_to_token.dtype is not _I32 or req_to_token.ndim != 2 or \
+            req_to_token.stride()[1] != 1 or req_to_token.shape[0] < V:
+        raise ValueError(f"req_to_token: expected int32 [{V}, stride] with contiguous rows, got "
+                         f"{req_to_token.dtype} {tuple(req_to_token.shape)}")
+    if seq_lens.dtype is not _I32 or seq_lens.numel() < V or not seq_lens.is_contiguous():
+        raise _not_a_buffer(seq_lens, "seq_lens", _I32, V)
+    if kv_limit is not None:
+        _check_buffer(kv_limit, "kv_limit", _I32, V * q_len)
+    if split_pages is not None and (
+            split_pages.dtype is not _I32 or split_pages.numel() < V * (num_splits + 1) or
+            not split_pages.is_contiguous()):
+        raise _not_a_buffer(split_pages, "split_pages", _I32, V * (num_splits + 1))
+    # its length is checked by the library
+    if work is not None and (work.dtype is not _I32 or not work.is_contiguous()):
+        raise _not_a_buffer(work, "work", _I32, 0)
+    if status is not None:
+        _check_buffer(status, "status", _I32, 1)
+    return rows
 
 
 def decode_partial(q_nope, q_rope, kv, kv_scale, req_to_token, seq_lens,
@@ -351,24 +386,35 @@ def decode_partial(q_nope, q_rope, kv, kv_scale, req_to_token, seq_lens,
     for, LSE_part fp32 [S, shards, B, q, H]); outputs are allocated with
     torch unless given.
     """
-    B, q_len, H, _ = q_nope.shape
-    dev = q_nope.device
+    B, q_len, H, _ = shape = q_nope.shape
     kind = _kv_dtype(kv)
     if kind == KV_FP4_E2M1:
-        _check_fp4(q_nope, q_rope, kv, kv_scale, req_to_token, seq_lens)
+        parts = num_splits * num_shards * _check_fp4(
+            shape, q_nope, q_rope, kv, kv_scale, req_to_token, seq_lens, kv_limit, num_shards,
+            num_splits, split_pages, work, status)
+        if O_part is not None and (
+                O_part.dtype not in (_F32, _BF16) or O_part.numel() < parts * VALUE_DIM or
+                not O_part.is_contiguous()):
+            raise _not_a_buffer(O_part, "O_part", "float32 or bfloat16", parts * VALUE_DIM)
+        if LSE_part is not None and (
+                LSE_part.dtype is not _F32 or LSE_part.numel() < parts or
+                not LSE_part.is_contiguous()):
+            raise _not_a_buffer(LSE_part, "LSE_part", _F32, parts)
     if O_part is None:
         O_part = torch.empty((num_splits, num_shards, B, q_len, H, VALUE_DIM),
-                             dtype=part_dtype or torch.float32, device=dev)
-    bf16_parts = O_part.dtype == torch.bfloat16
+                             dtype=part_dtype or torch.float32, device=q_nope.device)
+    bf16_parts = O_part.dtype is _BF16
     if LSE_part is None:
         LSE_part = torch.empty((num_splits, num_shards, B, q_len, H),
-                               dtype=torch.float32, device=dev)
-    args = (q_nope.data_ptr(), q_rope.data_ptr(), kv.data_ptr(), _ptr(kv_scale),
+                               dtype=torch.float32, device=q_nope.device)
+    args = (q_nope.data_ptr(), q_rope.data_ptr(), kv.data_ptr(),
+            None if kv_scale is None else kv_scale.data_ptr(),
             kind, kv.shape[0], req_to_token.data_ptr(),
-            req_to_token.stride(0), seq_lens.data_ptr(), _ptr(kv_limit), B, q_len,
+            req_to_token.stride()[0], seq_lens.data_ptr(),
+            None if kv_limit is None else kv_limit.data_ptr(), B, q_len,
             H, num_shards, PAGE_SIZE, float(sm_scale), num_splits,
-            _ptr(split_pages))
-    tail = (O_part.data_ptr(), LSE_part.data_ptr(), _ptr(status))
+            None if split_pages is None else split_pages.data_ptr())
+    tail = (O_part.data_ptr(), LSE_part.data_ptr(), None if status is None else status.data_ptr())
     if simt:
         if work is not None or bf16_parts:
             raise ValueError("the CUDA-core path takes no work list and "
@@ -377,7 +423,8 @@ def decode_partial(q_nope, q_rope, kv, kv_scale, req_to_token, seq_lens,
     else:
         fn = (library().mla_decode_partial_bf16_parts if bf16_parts
               else library().mla_decode_partial)
-        _launch(q_nope, stream, fn, *args, _ptr(work), 0 if work is None else work.numel(), *tail)
+        listed = (None, 0) if work is None else (work.data_ptr(), work.numel())
+        _launch(q_nope, stream, fn, *args, *listed, *tail)
     return O_part, LSE_part
 
 
@@ -397,11 +444,20 @@ def decode_fused(q_nope, q_rope, kv, kv_scale, req_to_token, seq_lens,
 
     Returns (out bf16 [B, q, H, 512], lse fp32 [B, q, H]); workspace and
     outputs are allocated with torch unless given."""
-    B, q_len, H, _ = q_nope.shape
+    B, q_len, H, _ = shape = q_nope.shape
     dev = q_nope.device
     kind = _kv_dtype(kv)
     if kind == KV_FP4_E2M1:
-        _check_fp4(q_nope, q_rope, kv, kv_scale, req_to_token, seq_lens)
+        rows = _check_fp4(shape, q_nope, q_rope, kv, kv_scale, req_to_token, seq_lens, kv_limit,
+                          num_shards, num_splits, split_pages, work, status)
+        parts = num_splits * num_shards * rows
+        for t, name, dtype, n in ((O_part, "O_part", torch.float32, parts * VALUE_DIM),
+                                  (LSE_part, "LSE_part", torch.float32, parts),
+                                  (counters, "counters", torch.int32, B * ((q_len * H + 127) // 128)),
+                                  (out, "out", torch.bfloat16, rows * VALUE_DIM),
+                                  (lse_out, "lse_out", torch.float32, rows)):
+            if t is not None:
+                _check_buffer(t, name, dtype, n)
     if O_part is None:
         O_part = torch.empty((num_splits, num_shards, B, q_len, H, VALUE_DIM),
                              dtype=torch.float32, device=dev)
@@ -438,11 +494,16 @@ def decode_scratch(q_nope, q_rope, kv, kv_scale, req_to_token, seq_lens,
                    stream=None, split_pages=None, work=None):
     """decode_fused with its workspace in the library's static scratch; see
     mla_decode_scratch (calls that may overlap on a device race on it)."""
-    B, q_len, H, _ = q_nope.shape
+    B, q_len, H, _ = shape = q_nope.shape
     dev = q_nope.device
     kind = _kv_dtype(kv)
     if kind == KV_FP4_E2M1:
-        _check_fp4(q_nope, q_rope, kv, kv_scale, req_to_token, seq_lens)
+        rows = _check_fp4(shape, q_nope, q_rope, kv, kv_scale, req_to_token, seq_lens, kv_limit,
+                          num_shards, num_splits, split_pages, work, status)
+        if out is not None:
+            _check_buffer(out, "out", torch.bfloat16, rows * VALUE_DIM)
+        if lse_out is not None:
+            _check_buffer(lse_out, "lse_out", torch.float32, rows)
     if out is None:
         out = torch.empty((B, q_len, H, VALUE_DIM), dtype=torch.bfloat16, device=dev)
     if lse_out is None:

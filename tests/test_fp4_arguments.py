@@ -200,3 +200,65 @@ def test_plan_takes_any_capacity(lib, capacity):
     want = mla.plan_sched(B, q, H, [300] * B, num_sms=152, kv_dtype="fp4_e2m1")
     assert rc == 0 and S.value == want[0] and list(work[:n.value]) == list(want[2])
     assert list(bnd[:B * (S.value + 1)]) == list(want[1].reshape(-1))
+
+
+def _decode_args(**over):
+    bf = torch.bfloat16
+    a = dict(q_nope=torch.zeros((2, 3, 4, 512), dtype=bf), q_rope=torch.zeros((2, 3, 4, 64), dtype=bf),
+             kv=torch.zeros((64, 352), dtype=torch.uint8), kv_scale=torch.ones(4),
+             req_to_token=torch.zeros((2, 64), dtype=torch.int32), seq_lens=torch.ones(2, dtype=torch.int32),
+             kv_limit=None, num_splits=2, sm_scale=0.07)
+    a.update(over)
+    return a
+
+
+I32, F32 = torch.int32, torch.float32
+COMMON = [
+    ("seq_lens", torch.ones(1, dtype=I32)), ("req_to_token", torch.zeros((1, 64), dtype=I32)),
+    ("req_to_token", torch.zeros(128, dtype=I32)),
+    ("kv_limit", torch.ones((2, 3), dtype=torch.int64)), ("kv_limit", torch.ones((2, 2), dtype=I32)),
+    ("kv_limit", torch.ones((3, 2), dtype=I32).T),
+    ("split_pages", torch.zeros((2, 3), dtype=torch.int64)), ("split_pages", torch.zeros((2, 2), dtype=I32)),
+    ("split_pages", torch.zeros((2, 6), dtype=I32)[:, ::2]),
+    ("work", torch.zeros(4, dtype=torch.int64)), ("work", torch.zeros(8, dtype=I32)[::2]),
+    ("status", torch.zeros(1, dtype=torch.int64)), ("status", torch.zeros(0, dtype=I32))]
+N = 2 * 3 * 4
+PARTIAL = [("O_part", torch.zeros(2 * N * 512 - 1)), ("O_part", torch.zeros(2 * N * 512, dtype=torch.float16)),
+           ("O_part", torch.zeros((2 * N, 1024))[:, :512]), ("LSE_part", torch.zeros(2 * N - 1)),
+           ("LSE_part", torch.zeros(2 * N, dtype=torch.bfloat16))]
+MERGED = [("out", torch.zeros(N * 512)), ("out", torch.zeros(N * 512 - 1, dtype=torch.bfloat16)),
+          ("lse_out", torch.zeros(N, dtype=torch.float64)), ("lse_out", torch.zeros(N - 1))]
+FUSED = PARTIAL + MERGED + [("O_part", torch.zeros(2 * N * 512, dtype=torch.bfloat16)),
+                            ("counters", torch.zeros(1, dtype=I32)), ("counters", torch.zeros(2, dtype=torch.int64))]
+
+
+@pytest.mark.parametrize("call,bad", [(c, b) for c, more in (("decode_partial", PARTIAL), ("decode_fused", FUSED),
+                                                             ("decode_scratch", MERGED)) for b in COMMON + more],
+                         ids=lambda x: x if isinstance(x, str) else f"{x[0]}-{x[1].dtype}-{tuple(x[1].shape)}")
+def test_binding_refuses_fp4_decode_buffers(call, bad, monkeypatch):
+    """Whatever the kernels read or write by address is refused by name when it is
+    too small, of another type or not contiguous."""
+    launched = []
+    monkeypatch.setattr(mla, "_launch", lambda *a: launched.append(a))
+    monkeypatch.setattr(mla, "_on", lambda t: launched.append(t) or mla._HERE_ALREADY)
+    monkeypatch.setattr(mla, "_check", lambda rc: rc)
+    monkeypatch.setattr(mla, "_stream", lambda s: None)
+
+    class Library:
+        def __getattr__(self, name):
+            return lambda *a: 0
+
+    monkeypatch.setattr(mla, "library", lambda: Library())
+    good = dict(kv_limit=torch.ones((2, 3), dtype=I32), split_pages=torch.zeros((2, 3), dtype=I32),
+                work=torch.zeros(4, dtype=I32), status=torch.zeros(1, dtype=I32))
+    if call != "decode_scratch":
+        good.update(O_part=torch.zeros(2 * N * 512), LSE_part=torch.zeros(2 * N))
+    if call != "decode_partial":
+        good.update(out=torch.zeros(N * 512, dtype=torch.bfloat16), lse_out=torch.zeros(N))
+    if call == "decode_fused":
+        good.update(counters=torch.zeros(2, dtype=I32))
+    getattr(mla, call)(**_decode_args(**good))
+    assert len(launched) == 1
+    with pytest.raises(ValueError, match=bad[0]):
+        getattr(mla, call)(**_decode_args(**{**good, bad[0]: bad[1]}))
+    assert len(launched) == 1
