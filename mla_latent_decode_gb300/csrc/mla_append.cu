@@ -130,7 +130,10 @@ __device__ __forceinline__ void append_row(const AppendParams& p, int64_t r, int
       eps = eps * f * f;
       mean = mean_square();
     }
-    const float rs = 1.0f / sqrtf(mean + eps);
+    // rsqrtf (within 2 units in the last place), not 1 / sqrtf: it is also what a
+    // reference in PyTorch calls, and where a row's factor is the same bits its
+    // values near a code's border fall on the same side.
+    const float rs = rsqrtf(mean + eps);
 #pragma unroll
     for (int k = 0; k < 16; ++k) c[k / 8][k % 8] = c[k / 8][k % 8] * rs * w[k / 8][k % 8];
   }
