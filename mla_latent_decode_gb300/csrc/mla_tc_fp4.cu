@@ -42,9 +42,9 @@
 // M = 128, N = 128, K = 16 f16 MMAs at 64.1 cycles and N = 256 at 128.1, so
 // the narrower tile costs nothing and the next tile's products overlap the
 // softmax of the last.
-// Measured, with the merge: 16 requests x 5 x 96 rows x 100k tokens 1113 us, 1.50
-// PFLOP/s of useful products, 79% of the measured bf16 rate (94% of the rows are
-// real: 480 of 512); 24 ragged requests of 1k to 200k tokens 642 us, 1.34 PFLOP/s.
+// Measured, with the merge: 16 requests x 5 x 96 rows x 100k tokens 1053 us, 1.59
+// PFLOP/s of useful products, 84% of the measured bf16 rate (94% of the rows are
+// real: 480 of 512); 24 ragged requests of 1k to 200k tokens 612 us, 1.40 PFLOP/s.
 #include <cuda_bf16.h>
 
 #include <cstring>
@@ -81,7 +81,7 @@ constexpr int kPeerFlagOff = kPMsgBytes;            // rank 2: rank 1's flags
 constexpr int kPSlotStride = 17408;                 // 17 KB, 1024-aligned
 constexpr uint32_t kSCol0 = 256;                    // two S buffers of 128 columns
 constexpr int kDequantWarp0 = 12;
-constexpr uint32_t kNoteBytes = 16;
+constexpr uint32_t kNoteBytes = 4;
 constexpr uint16_t kMaskS = 0x3;     // cluster ranks of the S pair
 constexpr uint16_t kMaskO = 0xC;     // cluster ranks of the O pair
 // Register split of the S-CTAs (setmaxnreg): 512 threads launch with 128 each;
@@ -105,8 +105,8 @@ struct __align__(1024) Smem {
   uint8_t raw[kRaw][kRawBytes];             // 66 KB of pages as stored
   uint8_t qrope[kRows * 128];               // S-CTA: Q_rope rows (f16)
   uint8_t pslot[kNP][kPSlotStride];
-  uint32_t note[4];         // what a note copies, of no meaning (see relay_made)
-  float fin[kRows];
+  uint32_t note;            // pair leader: where a note lands, of no meaning (relay_made)
+  alignas(16) float fin[kRows];
   float mref[kRows];        // S-CTA: every row's running reference
   float xch[2][2][kRows];   // S-CTA: per-warpgroup row values at either end
   uint64_t raw_full[kRaw];  // a raw page landed
@@ -472,20 +472,21 @@ __device__ __forceinline__ void convert_o(Smem& s, const Fp4Params& p, const Wor
 }
 
 // The pair's odd CTA, one thread: passes "stage written" on to the leader, whose
-// MMA reads this CTA's boxes too, by a note: a bulk copy of 16 bytes into the
-// leader that completes on its full barrier.  The converters' stores are ordered
-// before the MMA by made (their release, this thread's acquire), the proxy fence,
-// the copy issued after it, the release of the copy's completion at cluster
-// scope and the leader's acquire.  A relaxed arrive would order nothing; a
-// release arrive does, but holds this thread up for its round trip: at 16 x 5 x
-// 96 x 100k tokens the kernel takes 1595 us with that, 1363 with two threads
-// taking turns at it, and 1113 with notes (1131 where the wait for made may
-// suspend the thread, 1139 where each converter warp sends its own note, 1480
-// with stages of one box; ragged 885, 771, 642, 648, 658 and 827).
+// MMA reads this CTA's boxes too, by a note: an asynchronous store of one word
+// into the leader that completes on its full barrier.  The converters' stores
+// are ordered before the MMA by made (their release, this thread's acquire), the
+// fence to the async proxy, the completion of the note, which is a release at
+// cluster scope, and the leader's acquire of it.  A relaxed arrive would order
+// nothing; a release arrive does, but holds this thread up for its round trip: at
+// 16 x 5 x 96 x 100k tokens the kernel takes 1595 us with that, 1363 with two
+// threads taking turns at it, 1113 with the note as a bulk copy (1131 where the
+// wait for made may suspend the thread, 1139 where each converter warp sends its
+// own, 1480 with stages of one box) and 1053 with the store (ragged 885, 771, 642,
+// 648, 658, 827 and 612).
 __device__ __forceinline__ void relay_made(Smem& s, const Fp4Params& p, int n, int stages,
                                            uint32_t rank, uint32_t lead) {
   const uint32_t full0 = mapa(smem_u32(&s.full[0]), lead);
-  const uint32_t note = mapa(smem_u32(s.note), lead);
+  const uint32_t note = mapa(smem_u32(&s.note), lead);
   uint32_t stage = 0, phase = 0;
   for (int i = 0; i < n; ++i) {
     const uint64_t t0 = globaltimer();
@@ -496,7 +497,7 @@ __device__ __forceinline__ void relay_made(Smem& s, const Fp4Params& p, int n, i
         return;
       }
     fence_proxy_async_smem();
-    bulk_copy_to_peer(note, smem_u32(s.note), kNoteBytes, full0 + 8u * stage);
+    st_async_u32(note, 0, full0 + 8u * stage);
     if (++stage == (uint32_t)stages) {
       stage = 0;
       phase ^= 1u;

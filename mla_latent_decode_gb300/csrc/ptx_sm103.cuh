@@ -291,6 +291,18 @@ __device__ __forceinline__ void bulk_copy_to_peer(uint32_t dst_cluster,
       : "memory");
 }
 
+// Asynchronous store of one word into a peer CTA's shared memory (cluster
+// addresses) that completes 4 bytes on the peer's barrier; the completion is a
+// release at cluster scope.
+__device__ __forceinline__ void st_async_u32(uint32_t dst_cluster, uint32_t v,
+                                             uint32_t bar_cluster) {
+  asm volatile(
+      "st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(
+          dst_cluster),
+      "r"(v), "r"(bar_cluster)
+      : "memory");
+}
+
 // Order this thread's generic-proxy shared-memory writes before later
 // async-proxy (TMA, bulk copy, tensor core) accesses.
 __device__ __forceinline__ void fence_proxy_async_smem() {

@@ -1,7 +1,7 @@
 """Order between the CTAs of the 4-bit decode's clusters, by the source: a signal on
 whose strength another CTA reads memory that threads have stored must be a release
-at cluster scope or the completion of a bulk copy.  (A missing release shows in no
-result that a run could be asked for.)
+at cluster scope or the completion of an asynchronous store or bulk copy, which is
+one.  (A missing release shows in no result that a run could be asked for.)
 """
 import os
 import re
@@ -29,8 +29,8 @@ def test_stored_operands_are_published():
     made, p, corrected = (body(code(), f) for f in ("relay_made", "relay_o", "correct_and_store"))
     for f in (made, p, corrected):
         assert ".relaxed." not in f and "signal_leader" not in f
-    # the fence to the async proxy stands between the wait and the copy that signals
-    assert made.index("mbar_test_wait") < made.index("fence_proxy_async_smem") < made.index("bulk_copy_to_peer")
+    # the fence to the async proxy stands between the wait and the store that signals
+    assert made.index("mbar_test_wait") < made.index("fence_proxy_async_smem") < made.index("st_async_u32")
     assert "mbar_arrive_cluster" in p and "arrive_leader" in corrected
 
 
