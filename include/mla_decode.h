@@ -413,7 +413,8 @@ int mla_decode_partial_bf16_parts(
  *   out        bf16 [B, q_len, H, 512] (round to nearest even), 16-B aligned
  *   lse_out    fp32 [B, q_len, H] (natural log) or NULL
  * Same errors as mla_decode_partial; MLA_ERR_INVALID_ARG if counters or out
- * is NULL.  The tensor-core kernels only (page_size 64).
+ * is NULL; MLA_ERR_UNSUPPORTED for FP4 in groups of MLA_FP4_FEW_ROWS rows with
+ * more than 65535 parts.  The tensor-core kernels only (page_size 64).
  */
 int mla_decode(const void* q_nope_absorbed, const void* q_rope,
                const void* kv_pages, const float* kv_scale,

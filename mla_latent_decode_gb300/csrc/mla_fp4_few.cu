@@ -813,17 +813,24 @@ mla_partial_fp4_few_kernel(const Fp4Params p) {
     tc_fence_after();
     if (warp == F::kMmaWarp) tmem_dealloc(tmem, F::kCols);
     if (!p.counters) return;
-    // Fused combine: the part whose arrival completes the request's count merges
-    // its rows, every part being in memory by then.
+    // Fused combine: the CTA whose arrival completes its group's count merges the
+    // group's rows, every part being in memory by then.  A request has a counter
+    // per 128 rows, so group k, which starts at row 96 k, counts at (3 k) / 4, in
+    // the high or the low half where groups 4 i and 4 i + 1 share one.
     if (threadIdx.x == 0) {
-      int* c = p.counters + w.b;
-      s.last = atom_add_acq_rel_gpu(c, 1) == p.num_splits * (p.V / p.B) * p.U - 1;
-      if (s.last) *c = 0;
+      const int k = w.r0 / kFp4FewRows, parts = p.num_splits * (p.V / p.B);
+      const bool shared = k % 4 == 1 || (k % 4 == 0 && k + 1 < p.U);
+      int* c = p.counters + (int64_t)w.b * ((R + 127) / 128) + w.r0 / 128;
+      const uint32_t one = k % 4 == 1 ? 1u << 16 : 1u;
+      const uint32_t n = (uint32_t)atom_add_acq_rel_gpu(c, (int)one) + one;
+      s.last = (!shared ? n : one == 1 ? n & 0xFFFFu : n >> 16) == (uint32_t)parts;
+      if (s.last) atomicSub(reinterpret_cast<unsigned*>(c), (uint32_t)parts * one);
     }
     __syncthreads();
     if (!s.last) return;
     __threadfence();
-    for (int r = warp; r < R; r += kThreads / 32)
+    const int r1 = min(w.r0 + kFp4FewRows, R);
+    for (int r = w.r0 + warp; r < r1; r += kThreads / 32)
       combine_row<true>(p.O_part, p.LSE_part, p.num_splits * (p.V / p.B), (int64_t)p.B * R,
                         (int64_t)w.b * R + r, p.out, p.lse_out, lane);
   };

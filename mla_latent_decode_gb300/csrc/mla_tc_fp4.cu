@@ -1397,6 +1397,10 @@ int launch_fp4(const DecodeArgs& a) {
   p.o_bf16 = a.o_bf16;
   if (few_row_groups(a)) {
     p.U = (a.q_len * a.H + kFp4FewRows - 1) / kFp4FewRows;
+    // two groups may count in the halves of one counter
+    if (a.counters && p.U > 1 && (int64_t)a.num_splits * a.num_shards > 0xFFFF)
+      return fail(MLA_ERR_UNSUPPORTED, "one launch over groups of %d rows: %lld parts above %d",
+                  kFp4FewRows, (long long)a.num_splits * a.num_shards, 0xFFFF);
     return launch_fp4_few(p, a.stream);
   }
   CUtensorMap qn_map, qr_map;

@@ -262,3 +262,11 @@ def test_binding_refuses_fp4_decode_buffers(call, bad, monkeypatch):
     with pytest.raises(ValueError, match=bad[0]):
         getattr(mla, call)(**_decode_args(**{**good, bad[0]: bad[1]}))
     assert len(launched) == 1
+
+
+def test_one_launch_over_row_groups_bounds_its_parts(lib):
+    """Two groups count in the halves of one counter."""
+    p = P
+    args = lambda S, shards, work, n: (p(16), p(16), p(16), p(16), 2, 4096, p(16), 64, p(16), None, 1, 2, 64, shards, 64,
+                                       0.07, S, None, work, n, p(16), p(16), p(16), p(16), None, None, None)
+    assert lib.mla_decode(*args(4096, 16, p(16), 2 * 4096 * 16)) == UNSUP
