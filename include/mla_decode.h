@@ -482,8 +482,8 @@ int64_t mla_scratch_bytes(int B, int q_len, int H, int num_shards,
  *   scale = fl32(max_d |x_d| / 448); code_d = E4M3(fl32(x_d / scale)), both
  *   IEEE round-to-nearest divisions, E4M3 rounded to nearest even and
  *   saturated to +-448; an all-zero row gets scale 0 and codes 0.
- * Rows must be finite.  n = 0 is a no-op.  Slots written by two rows of one
- * call get either row.
+ * Rows must be finite.  n = 0 is a no-op.  A slot written by two rows of one
+ * call may hold parts of both.
  */
 int mla_kv_write(const void* rows, int64_t n, const int32_t* slots,
                  void* kv_pages, mla_kv_dtype kv_dtype, float* kv_scale,
@@ -518,7 +518,7 @@ int mla_kv_write(const void* rows, int64_t n, const int32_t* slots,
  *   kv_scale     FP8: fp32 [num_slots], written; FP4: fp32 [1], read; BF16: NULL
  *   q, q_out     bf16 [n, H, 64] with the given strides in elements (multiples
  *                of 8), 16-B aligned; q_out may be q; H = 0: no queries
- * n = 0 is a no-op.  Slots written by two rows of one call get either row.
+ * n = 0 is a no-op.  A slot written by two rows of one call may hold parts of both.
  */
 int mla_kv_append(const void* rows, int64_t row_stride, int64_t n,
                   const void* norm_weight, float eps, const int32_t* slots,

@@ -10,7 +10,7 @@
 // work are streams bound by HBM and, at a decode step's few tokens, by the
 // launch; one launch does both, its blocks split by role.  Measured from a CUDA
 // graph on a GB300: 2.9 us for one token x 96 heads and for 80, 36.3 for 8191
-// (215 MB, 5.9 TB/s, 88% of the copy rate), 7.1 for 16383 bf16 rows (38 MB).
+// (215 MB, 5.9 TB/s, 88% of the copy rate), 7.0 for 16383 bf16 rows (38 MB).
 //
 // Row blocks: a warp per token.  Lane l holds c_kv elements 16 l .. 16 l + 15,
 // one scale block of the 4-bit format, so the block's maximum, scale and codes

@@ -30,12 +30,12 @@
 // 128 a cycle (probe: M = 64 and N = 16, 32, 64, 96: 20, 21, 28, 40 cycles, M =
 // 128: 34, 35, 41, 48).  All of it, raw pages included, is 240, 270, 370 and 430
 // KB a page for the four widths, 1870 to 3360 cycles; measured at 152 requests,
-// one per SM, 1.22, 1.27, 1.89 and 2.54 us a page (2300 to 4900 cycles) and 12 to
-// 27 us for the rest of a launch with its merge.  (A profile of N = 96: the tensor
-// cores' operand path busy 48% of the time, other shared-memory accesses 36%.)
+// one per SM, 1.23, 1.30, 1.86 and 2.61 us a page (2300 to 4900 cycles) and 10 to
+// 30 us for the rest of a launch with its merge.  (A profile of N = 96: the tensor
+// cores' operand path busy 49% of the time, other shared-memory accesses 36%.)
 // 32 ragged requests of 2k to 50k tokens x 16 heads take 86 us (165 MB, 1.9 TB/s),
-// x 32 heads 91; 48 ragged x 96 heads 182 (the clusters: 214); 152 x 96 heads x
-// 6400 tokens 286 (471).  From 97 rows on O^T and S^T need more than TMEM's 512
+// x 32 heads 92; 48 ragged x 96 heads 185 (the clusters: 214); 152 x 96 heads x
+// 6400 tokens 293 (471).  From 97 rows on O^T and S^T need more than TMEM's 512
 // columns.
 #include <atomic>
 #include <cstring>

@@ -87,11 +87,13 @@ __host__ __device__ inline void split_page_range(const int32_t* row, int S,
 int check_decode_args(const DecodeArgs& a);
 
 // Host checks of a work list against the tensor-core kernel that serves
-// a.kv_dtype (rows per unit 256 for BF16, 128 for FP8).
+// a.kv_dtype (rows per unit 256 for BF16 and FP4, 128 for FP8; FP4 also
+// kFp4FewRows).
+int check_work(const DecodeArgs& a);
+
 // Whether the one-CTA FP4 kernel serves a launch: few rows, or a work list of
 // units of kFp4FewRows rows.
 bool few_row_groups(const DecodeArgs& a);
-int check_work(const DecodeArgs& a);
 
 // Launchers (defined next to their kernels).
 int launch_simt(const DecodeArgs& a);

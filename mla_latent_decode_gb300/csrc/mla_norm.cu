@@ -14,12 +14,13 @@
 // of 32, 64 or 128 values lies in 4, 8 or 16 neighbouring lanes: its maximum
 // takes 2 to 4 shuffles.  The row's sum (and, with one scale per row, its
 // maximum) crosses the warps through shared memory once.  Few rows take a
-// thread per vector, the shortest chain; many rows of 513 to 1024 vectors four
-// vectors a thread and four blocks per SM, whose phases overlap.  Measured on a
-// GB300 at 16383 x 7168, groups of 128 (822 MB): 153 us, 5.4 TB/s, 80% of the
-// copy rate (three blocks 173, five 172, two vectors a thread 185, one 178; a
-// resident grid that loads the next row ahead, two blocks of 125 registers,
-// 249); 80 x 7168: 3.0 us.
+// thread per vector, the shortest chain; many rows of 257 to 512 vectors two a
+// thread (6000 x 3584 29.2 us, with one 30.7; 16383 x 2560 51.0 and 53.1; 6000 x
+// 4096 34.0 and 33.4), and of 513 to 1024 vectors four and four blocks per SM,
+// whose phases overlap.  Measured on a GB300 at 16383 x 7168, groups of 128 (822
+// MB): 153 us, 5.4 TB/s, 80% of the copy rate (three blocks 173, five 172, two
+// vectors a thread 185, one 178; a resident grid that loads the next row ahead,
+// two blocks of 125 registers, 249); 80 x 7168: 3.0 us.
 #include <cuda_bf16.h>
 
 #include <algorithm>
