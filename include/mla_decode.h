@@ -507,8 +507,10 @@ int mla_kv_write(const void* rows, int64_t n, const int32_t* slots,
  *          (scale j * g)) (codes 0 where that is 0), rope code = E4M3(rope /
  *          g); all to nearest even, saturated.
  *   rows         bf16, row r at rows + r * row_stride elements (>= 576, a
- *                multiple of 8), 16-B aligned; finite, of any magnitude (the norm
- *                scales rows whose squares leave fp32's range by a power of two)
+ *                multiple of 8), 16-B aligned; of any magnitude (the norm scales
+ *                rows whose squares leave fp32's range by a power of two).  A NaN
+ *                in what is to be stored stays one: in its place (BF16, FP8), as
+ *                its block's scale or RoPE code (FP4)
  *   norm_weight  bf16 [512] or NULL, 16-B aligned;  eps finite, >= 0
  *   slots        int32 [n]: a slot outside [0, num_slots) is skipped
  *                (MLA_STATUS_BAD_SLOT; its queries are still rotated)

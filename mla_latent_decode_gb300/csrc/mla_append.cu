@@ -152,11 +152,12 @@ __device__ __forceinline__ void append_row(const AppendParams& p, int64_t r, int
     }
     return;
   }
-  float amax = 0.f;
-#pragma unroll
-  for (int k = 0; k < 16; ++k) amax = fmaxf(amax, fabsf(c[k / 8][k % 8]));
   if (KIND == MLA_KV_FP8_E4M3) {
-    amax = fmaxf(amax, fmaxf(fabsf(u), fabsf(v)));
+    // A NaN stays in its code; the scale, which the decode needs finite, is that
+    // of the row's other values.
+    float amax = fmaxf(fabsf(u), fabsf(v));
+#pragma unroll
+    for (int k = 0; k < 16; ++k) amax = fmaxf(amax, fabsf(c[k / 8][k % 8]));
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kAll, amax, o));
     const float scale = __fdiv_rn(amax, 448.0f);
@@ -179,7 +180,11 @@ __device__ __forceinline__ void append_row(const AppendParams& p, int64_t r, int
     if (lane == 0) p.kv_scale[slot] = scale;
     return;
   }
-  // FP4: this lane's block of 16 and its scale; the pool's factor g is fixed.
+  // FP4: this lane's block of 16 and its scale, NaN if the block holds one (E2M1
+  // has none); the pool's factor g is fixed.
+  float amax = 0.f;
+#pragma unroll
+  for (int k = 0; k < 16; ++k) amax = max_nan(amax, fabsf(c[k / 8][k % 8]));
   const float g = p.kv_scale[0];
   const float f = g > 0x1p+120f ? 0x1p-4f : 1.0f;  // 6 g stays in range
   const uint32_t s8 = e4m3_pair(__fdiv_rn(amax * f, 6.0f * (g * f)), 0.f) & 0xFFu;

@@ -77,6 +77,14 @@ __device__ __forceinline__ float2 h2_to_f32(uint32_t h) {
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
+// The larger of two values, NaN where either is: a maximum that dropped a NaN
+// would store a broken row as zeros with scale 0.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
+
 // RMS norms of rows whose squares leave fp32's range: above about 2^60 a value
 // their sum overflows, and without an eps it loses its bits below 2^-50.  Such a
 // row is divided by the power of two of its largest value (exact) and takes eps
@@ -99,7 +107,7 @@ __device__ __forceinline__ float unit_factor(float top) {
 // place and exact for quotients of few bits, so a code's tie stays a tie.
 // Divisors whose reciprocal leaves the normal range divide directly, and so do
 // those by which the largest dividend's quotient overflows (its correction would
-// be inf - inf); b = 0 gives 0.
+// be inf - inf); b = 0 gives 0, and NaN of a NaN.
 struct Divisor {
   float b, y;
   bool direct;
@@ -111,7 +119,7 @@ struct Divisor {
     }
   }
   __device__ __forceinline__ float operator()(float a) const {
-    if (direct) return b == 0.f ? 0.f : __fdiv_rn(a, b);
+    if (direct) return b != 0.f ? __fdiv_rn(a, b) : a == a ? 0.f : a;
     const float q = __fmul_rn(a, y);
     return __fmaf_rn(__fmaf_rn(-q, b, a), y, q);
   }

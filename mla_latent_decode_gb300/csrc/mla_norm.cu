@@ -96,14 +96,6 @@ __device__ __forceinline__ uint32_t word(const uint4& u, int k) {
   return k == 0 ? u.x : k == 1 ? u.y : k == 2 ? u.z : u.w;
 }
 
-// The larger of two values, NaN where either is: a maximum that dropped a NaN
-// would store a broken row as zeros with scale 0.
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float y;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
-  return y;
-}
-
 // How a row's eight values lie: kAny element by element; kVec on whole vectors;
 // kShift on whole vectors but for the row's two ends.
 enum Lay { kAny, kVec, kShift };
