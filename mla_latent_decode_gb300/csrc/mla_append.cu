@@ -155,7 +155,7 @@ __device__ __forceinline__ void append_row(const AppendParams& p, int64_t r, int
   if (KIND == MLA_KV_FP8_E4M3) {
     // A NaN stays in its code; the scale, which the decode needs finite, is that
     // of the row's other values.
-    float amax = fmaxf(fabsf(u), fabsf(v));
+    float amax = fmaxf(fmaxf(0.f, fabsf(u)), fabsf(v));
 #pragma unroll
     for (int k = 0; k < 16; ++k) amax = fmaxf(amax, fabsf(c[k / 8][k % 8]));
 #pragma unroll
