@@ -77,9 +77,13 @@ enum {
                                   rows were read as zeros */
   MLA_STATUS_BAD_WORK = 8,     /* a work-list entry named no work unit; that
                                   cluster did nothing (see mla_plan_sched) */
-  MLA_STATUS_BAD_POSITION = 16 /* a token's position lay outside the rotation
+  MLA_STATUS_BAD_POSITION = 16, /* a token's position lay outside the rotation
                                   table (mla_kv_append); nothing of that token
                                   was written */
+  MLA_STATUS_NO_PAGES = 32,    /* mla_pages_fork needs more pages than are free */
+  MLA_STATUS_BAD_PARENT = 64,  /* mla_pages_fork: a parent is no row */
+  MLA_STATUS_BAD_SCORE = 128   /* mla_beam_select: a score or a logit that is
+                                  NaN or +inf; that beam does not go on */
 };
 
 /* Storage of a pool's rows.  MLA_KV_FP4_E2M1 (4-bit, microscaled; the library's
@@ -641,6 +645,175 @@ int mla_lse_combine(const float* O_part, const float* LSE_part, int num_parts,
 int mla_lse_combine_bf16_parts(const void* O_part, const float* LSE_part,
                                int num_parts, int64_t rows, void* out,
                                float* lse_out, mla_stream_t stream);
+
+/*
+ * Attention within packed prompts, before absorption: the prefill step's
+ * counterpart of the decode (a pair costs 128 + 64 + 128 multiply-adds here,
+ * 576 + 512 there).  N sequences lie one after another; sequence n has query rows
+ * cu_q[n] .. cu_q[n + 1] and keys cu_kv[n] .. cu_kv[n + 1], its lq queries at the
+ * end of its lk keys (lk > lq: the rest is context already in the cache).
+ * Query i of a sequence sees its first
+ *   causal:  min(lk, max(prefix[n], lk - lq + 1 + i, 0)) keys
+ *   else:    lk keys,
+ * no key of another sequence, and
+ *   s_t = sm_scale (q_nope . k_nope[t] + q_rope . k_rope[t]) over those t,
+ *   lse = ln sum_t e^s_t,   out = sum_t e^(s_t - lse) v[t].
+ * A row that sees no key, or only keys with s = -inf, has out = 0, lse = -inf.
+ * Keys and values that a row does not see do not reach it, whatever they hold;
+ * a NaN score makes its row NaN, and a value that is not finite makes the
+ * outputs of its dim NaN or infinite in the rows that see it.
+ *   q_nope   bf16 [Tq, H, 128], q_rope bf16 [Tq, H, 64], k_nope and v bf16
+ *            [Tk, H, 128], each with a token stride and a head stride
+ *            (elements, multiples of 8, head rows contiguous, 16-B aligned):
+ *            views into a projection's output serve
+ *   k_rope   bf16 [Tk, 64], one for all heads, with a token stride
+ *   cu_q, cu_kv  int32 [N + 1], non-decreasing, 0 <= . <= Tq, Tk;
+ *   prefix   int32 [N] or NULL (0): keys that every query of a sequence sees
+ *   work     int32 [num_work, 8], device: mla_plan_prefill's list; num_parts its
+ *            parts.  The plan must be made for the lengths in cu_q and cu_kv: rows
+ *            that no entry names are not written, an entry that fits no sequence
+ *            sets MLA_STATUS_BAD_WORK and does nothing, lengths that leave the
+ *            arrays set MLA_STATUS_BAD_LENGTH and their sequence is not computed.
+ *   O_part   fp32 [num_parts, H, 256, 128] (16-B aligned), LSE_part fp32
+ *            [num_parts, H, 256]: workspace, may be NULL when num_parts is 0
+ *   out      bf16 [Tq, H, 128] contiguous, 16-B aligned;  lse fp32 [Tq, H] or
+ *            NULL.  Rows past the last sequence are not written.
+ * Probabilities are rounded to bf16 (2^-8) before the product with v; sums and
+ * statistics are fp32.  H in [1, 65535], sm_scale finite and > 0.  One launch,
+ * and a second one that merges when num_parts > 0.
+ */
+int mla_prefill(const void* q_nope, int64_t qn_token_stride, int64_t qn_head_stride,
+                const void* q_rope, int64_t qr_token_stride, int64_t qr_head_stride,
+                int64_t Tq, const void* k_nope, int64_t kn_token_stride,
+                int64_t kn_head_stride, const void* k_rope, int64_t kr_token_stride,
+                const void* v, int64_t v_token_stride, int64_t v_head_stride,
+                int64_t Tk, int H, const int32_t* cu_q, const int32_t* cu_kv,
+                const int32_t* prefix, int N, int causal, float sm_scale,
+                const int32_t* work, int num_work, int num_parts, float* O_part,
+                float* LSE_part, void* out, float* lse, int* status,
+                mla_stream_t stream);
+
+/*
+ * Plan of mla_prefill on the host: the sequences' blocks of 256 query rows,
+ * longest sequences first, a sequence's heads one after another (their keys and
+ * values then stay in L2) and a head's blocks from the longest down; where
+ * there are too few blocks for the SMs, blocks are cut along the keys into
+ * parts that a second launch merges.
+ *   q_lens, kv_lens, prefix   host int32 [N] (prefix may be NULL)
+ *   num_sms     0: the current device's (148 where there is none)
+ *   work_out    host int32 [capacity, 8], entries (sequence, block, part, parts,
+ *               slot of the first part or -1, first entry of the sequence,
+ *               entries of the sequence, 0)
+ *   num_work_out, num_parts_out   host: entries and part slots
+ * An entry list longer than `capacity` is MLA_ERR_INVALID_ARG;
+ * sum_n ceil(q_lens[n] / 256) * MLA_PREFILL_MAX_PARTS always suffices.
+ */
+#define MLA_PREFILL_MAX_PARTS 32
+int mla_plan_prefill(const int32_t* q_lens, const int32_t* kv_lens,
+                     const int32_t* prefix, int N, int H, int causal, int num_sms,
+                     int32_t* work_out, int64_t capacity, int64_t* num_work_out,
+                     int* num_parts_out);
+
+/*
+ * Beam search's selection.  For every request b, over its W beams and the
+ * vocabulary,
+ *   score(w, t) = scores[b, w] + x[b, w, t] - ln sum_u exp x[b, w, u]
+ * and the k largest in order, equal ones by lowest (w, t):
+ *   out_scores fp32 [B, k], parents int32 [B, k] (the row b * W + w, as
+ *   mla_pages_fork takes it), tokens int32 [B, k].
+ * A finished beam has one continuation, end_token at the beam's own score.  A
+ * beam whose score or whose logits' sum is not finite (a NaN, an infinite
+ * logit, every logit -inf) has none; a NaN or +inf among them sets
+ * MLA_STATUS_BAD_SCORE.  Where fewer than k continuations have a score above
+ * -inf the rest of the outputs are the lowest (w, t) not among them, at -inf.
+ *   logits     bf16, fp16 or fp32 [B, W, V], rows contiguous, any strides
+ *   scores     fp32 [B, W]: the beams' summed log probabilities; -inf rules a
+ *              beam out (its logits are not read)
+ *   finished   bytes [B, W], non-zero: finished; or NULL
+ * Sums are fp32 over a thread's and a warp's logits and fp64 from there; scores
+ * are formed and compared in fp64, a beam's own tokens by their logits.
+ * W <= MLA_BEAM_MAX_W, k <= MLA_BEAM_MAX_K (else MLA_ERR_UNSUPPORTED), k <= W V.
+ */
+typedef enum { MLA_LOGIT_BF16 = 0, MLA_LOGIT_F16 = 1, MLA_LOGIT_F32 = 2 } mla_logit_dtype;
+#define MLA_BEAM_MAX_W 32
+#define MLA_BEAM_MAX_K 64
+int mla_beam_select(const void* logits, mla_logit_dtype dtype, int64_t batch_stride,
+                    int64_t beam_stride, const float* scores, const uint8_t* finished,
+                    int B, int W, int V, int end_token, int k, float* out_scores,
+                    int32_t* parents, int32_t* tokens, int* status,
+                    mla_stream_t stream);
+
+/*
+ * The page table of a step that may branch.  Row i of the new table takes the
+ * first min(keep[i], lens[parents[i]]) tokens of row parents[i] (none where
+ * parents[i] is -1) and gets room for grow[i] more:
+ *   lens_out[i] = taken + grow[i]
+ *   table_out[i, t] = the slot of token t, for every t of the row's pages
+ * so one call reorders beams, shares a prompt, drops rejected drafts, ends rows,
+ * starts new ones and makes room for a step's tokens.  Pages are shared: full
+ * ones as they are; a partly taken page stays where it is with the child that
+ * takes most of the row (the lowest of equals) if nobody else holds it, and any
+ * other child gets a new page and an entry in `copies`: run mla_kv_copy with it
+ * on every layer's pool before the step's tokens are written.
+ *   refs        int32 [num_pages]: rows that hold a page, 0 = free; page 0 (the
+ *               dummy page) is never counted nor given out
+ *   free_count  int32 [1]: the number of zeros among refs[1 ..]
+ *   table       int32 [R, stride], a page's 64 entries its slots in order (as the
+ *               decode reads it); lens int32 [R]: tokens that a row has pages for
+ *   parents, keep, grow   int32 [R] or NULL (each row goes on; all; none)
+ *   table_out   int32 [R, out_stride], not overlapping table; entries past a
+ *               row's pages are not written
+ *   copies      int32 [3, R]: source page, destination page, tokens of row i;
+ *               -1, -1, 0 where nothing is to be copied
+ * New pages are the lowest free ones, rows in order; pages that this call frees
+ * are free from the next call on.  A parent outside [-1, R) (MLA_STATUS_
+ * BAD_PARENT), a length outside its row (BAD_LENGTH), a partly taken page
+ * outside the pool (BAD_SLOT) or more new pages than free_count
+ * (NO_PAGES) leaves refs and free_count as they are, lens_out 0 and nothing to
+ * copy; table_out is then not to be used, and the old table still stands.
+ * R <= MLA_FORK_MAX_ROWS.  One launch, no workspace; results do not depend on
+ * any order of execution.  R = 0 is a no-op.
+ */
+#define MLA_FORK_MAX_ROWS 4096
+int mla_pages_fork(const int32_t* table, int64_t stride, const int32_t* lens,
+                   const int32_t* parents, const int32_t* keep, const int32_t* grow,
+                   int R, int32_t* refs, int64_t num_pages, int32_t* free_count,
+                   int32_t* table_out, int64_t out_stride, int32_t* lens_out,
+                   int32_t* copies, int* status, mla_stream_t stream);
+
+/*
+ * Compaction: the k-th highest live page of a pool moves to its k-th lowest
+ * hole, for at most max_moves pages and as long as the hole lies below; without
+ * that limit the live pages are 1 .. n afterwards.
+ *   src, dst    int32 [max_moves]: the moves' pages, -1 past *count: run
+ *               mla_kv_copy with them (and count) on every layer's pool before the
+ *               new table is used and before pages are given out again
+ *   count       int32 [1]
+ *   table_out   int32 [R, out_stride]: the live entries of `table` with the moved
+ *               pages' new numbers; may be table itself.  Every row that holds
+ *               pages has to be in the table.
+ * refs is updated (a moved page's count goes with it); free_count stays true.
+ * Two launches.  A length outside its row sets MLA_STATUS_BAD_LENGTH and that
+ * row is not renamed.
+ */
+int mla_pages_compact(const int32_t* table, int64_t stride, const int32_t* lens,
+                      int R, int32_t* refs, int64_t num_pages, int32_t* table_out,
+                      int64_t out_stride, int32_t* src, int32_t* dst, int max_moves,
+                      int32_t* count, int* status, mla_stream_t stream);
+
+/*
+ * Copy of pages within a pool of any format: the first tokens[i] rows (all 64
+ * where tokens is NULL) of page src[i] to page dst[i], i < n, or i < *count
+ * where count is given and less; with MLA_KV_FP8_E4M3 their scales too.  An entry
+ * with a negative page or src = dst does nothing; a page outside the pool sets
+ * MLA_STATUS_BAD_SLOT and does nothing.  No page may be the destination of one
+ * entry and in another one.
+ *   src, dst, tokens, count   device int32;  kv_pages 16-B aligned
+ */
+int mla_kv_copy(void* kv_pages, mla_kv_dtype kv_dtype, float* kv_scale,
+                int64_t num_slots, const int32_t* src, const int32_t* dst,
+                const int32_t* tokens, const int32_t* count, int64_t n, int* status,
+                mla_stream_t stream);
 
 /*
  * Page-table gather through the decode kernel's own TMA path (for the

@@ -30,6 +30,9 @@ PLAN_FEW_SPLITS = 160  # the default planners' largest split count for such requ
 ROWS_PER_UNIT = 256  # query rows per work unit of the BF16 tensor-core kernel
 STATUS_WAIT_TIMEOUT, STATUS_BAD_LENGTH, STATUS_BAD_SLOT, STATUS_BAD_WORK = 1, 2, 4, 8
 STATUS_BAD_POSITION = 16
+STATUS_NO_PAGES, STATUS_BAD_PARENT, STATUS_BAD_SCORE = 32, 64, 128
+BEAM_MAX_W, BEAM_MAX_K, FORK_MAX_ROWS, PREFILL_MAX_PARTS = 32, 64, 4096, 32
+_LOGITS = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 
 _lib = None
 _lock = threading.Lock()
@@ -96,6 +99,14 @@ def library() -> ctypes.CDLL:
             "mla_kv_read": (i32, [p, i32, p, i64, p, i64, p, i64, p, p]),
             "mla_add_rms_norm": (i32, [p, i64, p, i64, p, i64, p, f32, i64, i32, p, i64,
                                        p, i64, p, i64, i32, p]),
+            "mla_plan_prefill": (i32, [p, p, p, i32, i32, i32, i32, p, i64, p, p]),
+            "mla_prefill": (i32, [p, i64, i64, p, i64, i64, i64, p, i64, i64, p, i64, p, i64, i64,
+                                  i64, i32, p, p, p, i32, i32, f32, p, i32, i32, p, p, p, p, p, p]),
+            "mla_beam_select": (i32, [p, i32, i64, i64, p, p, i32, i32, i32, i32, i32, p, p, p, p,
+                                      p]),
+            "mla_pages_fork": (i32, [p, i64, p, p, p, p, i32, p, i64, p, p, i64, p, p, p, p]),
+            "mla_pages_compact": (i32, [p, i64, p, i32, p, i64, p, i64, p, p, i32, p, p, p]),
+            "mla_kv_copy": (i32, [p, i32, p, i64, p, p, p, p, i64, p, p]),
             "mla_absorb_q": (i32, [p, p, p, i32, i32, p, p]),
             "mla_project_out": (i32, [p, p, p, i32, i32, p, p]),
             "mla_lse_combine": (i32, [p, p, i32, i64, p, p, p]),
@@ -696,6 +707,217 @@ def lse_combine(O_part, LSE_part, out=None, lse_out=None, stream=None):
     _launch(O_part, stream, fn, O_part.data_ptr(), LSE_part.data_ptr(), parts,
             LSE_part.numel() // parts, out.data_ptr(), lse_out.data_ptr())
     return out, lse_out
+
+
+# ------------------------------------------------------- prompts and beams
+def plan_prefill(q_lens: Sequence[int], kv_lens: Sequence[int], H: int, prefix=None,
+                 causal: bool = True, num_sms: int = 0):
+    """Plan of `prefill` for sequences of these query and key lengths (host
+    numbers): (work np.int32 [n, 8], num_parts); see mla_plan_prefill."""
+    import numpy as np
+    lq, lk = _host_i32(q_lens), _host_i32(kv_lens)
+    pre = None if prefix is None else _host_i32(prefix)
+    if len(lk) != len(lq) or (pre is not None and len(pre) != len(lq)):
+        raise ValueError("q_lens, kv_lens and prefix differ in length")
+    cap = sum(-(-max(n, 0) // 256) for n in lq) * PREFILL_MAX_PARTS
+    out = np.empty((cap, 8), dtype=np.int32)
+    n, parts = ctypes.c_int64(), ctypes.c_int()
+    _check(library().mla_plan_prefill(lq, lk, pre, len(lq), H, 1 if causal else 0, num_sms,
+                                      out.ctypes.data, cap, ctypes.byref(n), ctypes.byref(parts)))
+    return out[:n.value].copy(), parts.value
+
+
+def _heads_arg(t: torch.Tensor, name: str, T: int, H: int, width: int):
+    """bf16 [T, H, width] with contiguous head rows: address, token and head stride."""
+    shape, stride = t.shape, t.stride()
+    if t.dtype is not _BF16 or shape != (T, H, width) or stride[2] != 1:
+        raise ValueError(f"{name}: expected bfloat16 [{T}, {H}, {width}] with contiguous head rows, "
+                         f"got {t.dtype} {tuple(shape)} with strides {stride}")
+    return t.data_ptr(), stride[0], stride[1]
+
+
+def prefill(q_nope, q_rope, k_nope, k_rope, v, cu_q, cu_kv, work, sm_scale: float, prefix=None,
+            causal: bool = True, num_parts: int = 0, O_part=None, LSE_part=None, out=None,
+            lse_out=None, status=None, stream=None):
+    """Attention within packed prompts, before absorption; see mla_prefill.
+
+    q_nope bf16 [Tq, H, 128], q_rope bf16 [Tq, H, 64], k_nope and v bf16 [Tk, H,
+    128] (any of them may be views into wider rows), k_rope bf16 [Tk, 64] for all
+    heads; cu_q, cu_kv int32 [N + 1] where the sequences start; work and num_parts
+    from plan_prefill (work as a device int32 tensor).  A sequence's queries stand
+    at the end of its keys; `prefix` int32 [N]: keys that all of them see.
+
+    Returns (out bf16 [Tq, H, 128], lse fp32 [Tq, H]); rows past the last sequence
+    are left as they were.  The workspace (O_part fp32 [num_parts, H, 256, 128],
+    LSE_part fp32 [num_parts, H, 256]) is allocated unless given."""
+    if q_nope.dim() != 3 or k_rope.dim() != 2:
+        raise ValueError(f"q_nope, k_rope: expected [Tq, H, 128] and [Tk, 64], got "
+                         f"{tuple(q_nope.shape)} and {tuple(k_rope.shape)}")
+    Tq, H, _ = q_nope.shape
+    Tk = k_rope.shape[0]
+    N = cu_q.numel() - 1
+    if N < 0:
+        raise ValueError("cu_q: expected N + 1 values")
+    if work.dtype is not _I32 or work.dim() != 2 or work.shape[1] != 8 or not work.is_contiguous():
+        raise ValueError(f"work: expected contiguous int32 [n, 8] on the device, got {work.dtype} "
+                         f"{tuple(work.shape)}")
+    qn = _heads_arg(q_nope, "q_nope", Tq, H, 128)
+    qr = _heads_arg(q_rope, "q_rope", Tq, H, ROPE_DIM)
+    kn = _heads_arg(k_nope, "k_nope", Tk, H, 128)
+    vv = _heads_arg(v, "v", Tk, H, 128)
+    kr = _rows_arg(k_rope, "k_rope", Tk, ROPE_DIM)
+    cu_args = _int32_arg(cu_q, "cu_q", N + 1), _int32_arg(cu_kv, "cu_kv", N + 1), \
+        None if prefix is None else _int32_arg(prefix, "prefix", N)
+    dev = q_nope.device
+    if out is None:
+        out = torch.empty((Tq, H, 128), dtype=_BF16, device=dev)
+    elif out.dtype is not _BF16 or out.shape != (Tq, H, 128) or not out.is_contiguous():
+        raise _not_a_buffer(out, "out", _BF16, Tq * H * 128)
+    if lse_out is None:
+        lse_out = torch.empty((Tq, H), dtype=_F32, device=dev)
+    elif lse_out.dtype is not _F32 or lse_out.shape != (Tq, H) or not lse_out.is_contiguous():
+        raise _not_a_buffer(lse_out, "lse_out", _F32, Tq * H)
+    ws = (None, None)
+    if num_parts > 0:
+        rows = num_parts * H * 256
+        if O_part is None:
+            O_part = torch.empty((num_parts, H, 256, 128), dtype=_F32, device=dev)
+        if LSE_part is None:
+            LSE_part = torch.empty((num_parts, H, 256), dtype=_F32, device=dev)
+        _check_buffer(O_part, "O_part", _F32, rows * 128)
+        _check_buffer(LSE_part, "LSE_part", _F32, rows)
+        ws = O_part.data_ptr(), LSE_part.data_ptr()
+    if status is not None:
+        _check_buffer(status, "status", _I32, 1)
+    _launch(q_nope, stream, library().mla_prefill, *qn, *qr, Tq, *kn, *kr, *vv, Tk, H, *cu_args, N,
+            1 if causal else 0, sm_scale, work.data_ptr(), work.shape[0], num_parts, *ws,
+            out.data_ptr(), lse_out.data_ptr(), _ptr(status))
+    return out, lse_out
+
+
+def beam_select(logits, scores, k: int, finished=None, end_token: int = 0, out_scores=None,
+                parents=None, tokens=None, status=None, stream=None):
+    """The k best continuations of every request over its beams and the
+    vocabulary; see mla_beam_select.
+
+    logits bf16, fp16 or fp32 [B, W, V] with contiguous rows, scores fp32 [B, W]
+    (summed log probabilities), finished bool or uint8 [B, W] or None.  Returns
+    (scores fp32 [B, k], parents int32 [B, k] as rows b * W + w, tokens int32
+    [B, k]), allocated unless given; parents go straight into pages_fork."""
+    if logits.dim() != 3 or logits.dtype not in _LOGITS or (logits.stride(2) != 1 and logits.shape[2] > 1):
+        raise ValueError(f"logits: expected bfloat16, float16 or float32 [B, W, V] with contiguous "
+                         f"rows, got {logits.dtype} {tuple(logits.shape)} with strides {logits.stride()}")
+    B, W, V = logits.shape
+    _check_buffer(scores, "scores", _F32, B * W)
+    if finished is not None and (finished.dtype not in (torch.bool, torch.uint8) or
+                                 finished.numel() != B * W or not finished.is_contiguous()):
+        raise ValueError(f"finished: expected {B * W} contiguous bool or uint8 values, got "
+                         f"{finished.dtype} {tuple(finished.shape)}")
+    dev = logits.device
+    if out_scores is None:
+        out_scores = torch.empty((B, k), dtype=_F32, device=dev)
+    if parents is None:
+        parents = torch.empty((B, k), dtype=_I32, device=dev)
+    if tokens is None:
+        tokens = torch.empty((B, k), dtype=_I32, device=dev)
+    for t, name, dtype in ((out_scores, "out_scores", _F32), (parents, "parents", _I32),
+                           (tokens, "tokens", _I32)):
+        _check_buffer(t, name, dtype, B * k)
+    if status is not None:
+        _check_buffer(status, "status", _I32, 1)
+    _launch(logits, stream, library().mla_beam_select, logits.data_ptr(), _LOGITS[logits.dtype],
+            logits.stride(0), logits.stride(1), scores.data_ptr(), _ptr(finished), B, W, V, end_token,
+            k, out_scores.data_ptr(), parents.data_ptr(), tokens.data_ptr(), _ptr(status))
+    return out_scores, parents, tokens
+
+
+def _table_arg(t: torch.Tensor, name: str, R: int):
+    """An int32 page table [R, stride] with contiguous rows: address, row stride
+    and entries a row."""
+    shape, stride = t.shape, t.stride()
+    if t.dtype is not _I32 or len(shape) != 2 or shape[0] != R or (shape[1] > 1 and stride[1] != 1) or \
+            (R > 1 and stride[0] != shape[1]):
+        raise ValueError(f"{name}: expected contiguous int32 [{R}, stride], got {t.dtype} "
+                         f"{tuple(shape)} with strides {stride}")
+    return t.data_ptr(), shape[1]
+
+
+def pages_fork(table, lens, refs, free_count, parents=None, keep=None, grow=None, table_out=None,
+               lens_out=None, copies=None, status=None, stream=None):
+    """The page table of a step that may branch: row i takes keep[i] tokens of row
+    parents[i] (-1: starts empty) and grows by grow[i]; see mla_pages_fork.
+
+    table int32 [R, stride], lens int32 [R]; refs int32 [num_pages] and free_count
+    int32 [1] are updated.  Returns (table_out int32 [R, stride], lens_out int32
+    [R], copies int32 [3, R]), allocated unless given (table_out zeroed); run
+    kv_copy(pool, copies[0], copies[1], scale, tokens=copies[2]) on every layer's
+    pool."""
+    R = table.shape[0]
+    if table_out is None:
+        table_out = torch.zeros_like(table)
+    if lens_out is None:
+        lens_out = torch.empty_like(lens)
+    if copies is None:
+        copies = torch.empty((3, R), dtype=_I32, device=table.device)
+    elif copies.dtype is not _I32 or copies.shape != (3, R) or not copies.is_contiguous():
+        raise _not_a_buffer(copies, "copies", _I32, 3 * R)
+    rows = [None if t is None else _int32_arg(t, name, R)
+            for t, name in ((parents, "parents"), (keep, "keep"), (grow, "grow"))]
+    _check_buffer(refs, "refs", _I32, 1)
+    _check_buffer(free_count, "free_count", _I32, 1)
+    if status is not None:
+        _check_buffer(status, "status", _I32, 1)
+    _launch(table, stream, library().mla_pages_fork, *_table_arg(table, "table", R),
+            _int32_arg(lens, "lens", R), *rows, R, refs.data_ptr(), refs.numel(),
+            free_count.data_ptr(), *_table_arg(table_out, "table_out", R),
+            _int32_arg(lens_out, "lens_out", R), copies.data_ptr(), _ptr(status))
+    return table_out, lens_out, copies
+
+
+def pages_compact(table, lens, refs, max_moves: Optional[int] = None, table_out=None, src=None,
+                  dst=None, count=None, status=None, stream=None):
+    """Move a pool's highest live pages into its lowest holes; see
+    mla_pages_compact.  At most max_moves pages (the length of src and dst if
+    those are given, else the pool's pages); refs is updated, table_out may be
+    table.  Returns (table_out, src int32 [max_moves], dst, count int32 [1]),
+    allocated unless given; run kv_copy(pool, src, dst, scale, count=count) on
+    every layer's pool."""
+    R = table.shape[0]
+    _check_buffer(refs, "refs", _I32, 1)
+    if max_moves is None:
+        max_moves = src.numel() if src is not None else refs.numel()
+    if table_out is None:
+        table_out = torch.zeros_like(table)
+    if src is None:
+        src = torch.empty(max_moves, dtype=_I32, device=table.device)
+    if dst is None:
+        dst = torch.empty(max_moves, dtype=_I32, device=table.device)
+    if count is None:
+        count = torch.empty(1, dtype=_I32, device=table.device)
+    _check_buffer(count, "count", _I32, 1)
+    if status is not None:
+        _check_buffer(status, "status", _I32, 1)
+    table_args = _table_arg(table, "table", R)
+    _launch(table, stream, library().mla_pages_compact, *table_args, _int32_arg(lens, "lens", R), R,
+            refs.data_ptr(), refs.numel(), *_table_arg(table_out, "table_out", R),
+            _int32_arg(src, "src", max_moves), _int32_arg(dst, "dst", max_moves), max_moves,
+            count.data_ptr(), _ptr(status))
+    return table_out, src, dst, count
+
+
+def kv_copy(kv, src, dst, kv_scale=None, tokens=None, count=None, status=None, stream=None):
+    """Copy pages src[i] to dst[i] (int32 page numbers, a negative one: nothing) of
+    a pool of any format, the first tokens[i] rows of each or all 64; only the
+    first *count entries where count (int32 [1]) is given.  See mla_kv_copy."""
+    n = src.numel()
+    kv_ptr, kind, scale_ptr, slots = _pool_args(kv, kv_scale)
+    if count is not None:
+        _check_buffer(count, "count", _I32, 1)
+    if status is not None:
+        _check_buffer(status, "status", _I32, 1)
+    _launch(kv, stream, library().mla_kv_copy, kv_ptr, kind, scale_ptr, slots,
+            _int32_arg(src, "src", n), _int32_arg(dst, "dst", n),
+            None if tokens is None else _int32_arg(tokens, "tokens", n), _ptr(count), n, _ptr(status))
 
 
 def debug_gather(kv, req_to_token, seq_lens, row_offset, total_rows: int,

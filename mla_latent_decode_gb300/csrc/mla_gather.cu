@@ -71,6 +71,26 @@ int make_tensor_map_bf16_3d(CUtensorMap* map, const void* base,
   return MLA_OK;
 }
 
+int make_tensor_map_bf16_4d(CUtensorMap* map, const void* base,
+                            const uint64_t dims[4], const uint64_t strides[3],
+                            const uint32_t box[4]) {
+  auto fn = encode_fn();
+  if (!fn) return fail(MLA_ERR_CUDA, "cuTensorMapEncodeTiled unavailable");
+  cuuint64_t d[4] = {dims[0], dims[1], dims[2], dims[3]};
+  cuuint64_t st[3] = {strides[0], strides[1], strides[2]};
+  cuuint32_t bx[4] = {box[0], box[1], box[2], box[3]};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+                  const_cast<void*>(base), d, st, bx, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS)
+    return fail(MLA_ERR_CUDA, "cuTensorMapEncodeTiled (4-D bf16) failed (%d)",
+                (int)r);
+  return MLA_OK;
+}
+
 int make_o_part_map(CUtensorMap* map, float* O_part, int64_t total_rows) {
   auto fn = encode_fn();
   if (!fn) return fail(MLA_ERR_CUDA, "cuTensorMapEncodeTiled unavailable");

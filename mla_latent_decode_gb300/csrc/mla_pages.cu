@@ -1,0 +1,671 @@
+// mla_pages.cu -- the page table of a serving step that may branch: rows taken
+// over from other rows, shared, shortened, grown, started and ended
+// (mla_pages_fork), a pool's live pages moved into its holes
+// (mla_pages_compact), and the copy of pages that both ask for (mla_kv_copy).
+//
+// A page is 64 slots; refs[page] counts the rows that hold it, 0 = free.  Page 0
+// is the pool's dummy page: never counted, never given out.  Both bookkeeping
+// kernels are one cluster of 8 CTAs: their phases are separated by cluster
+// barriers (about 1 us, against 2 us and more for a launch), counts travel
+// through distributed shared memory, and every result (which page a row gets,
+// where a page moves) is a rank in a fixed order, so it does not depend on
+// which CTA was first.
+#include <algorithm>
+
+#include "mla_internal.h"
+#include "ptx_sm103.cuh"
+
+namespace mla {
+namespace {
+
+using namespace ptx;
+
+constexpr int kPage = MLA_PAGE_SIZE;
+constexpr int kThreads = 512;
+constexpr int kWarps = kThreads / 32;
+constexpr int kCluster = 8;
+constexpr int kPerThread = 16;                      // pages a thread looks at in one round
+constexpr int kPerCta = kThreads * kPerThread;      // 8192
+constexpr int kMaxRows = MLA_FORK_MAX_ROWS;
+
+__host__ __device__ inline int64_t pages_of(int64_t tokens) { return (tokens + kPage - 1) / kPage; }
+
+// Exclusive prefix sum of one int per thread; *total receives the block's sum.
+// `scratch`: kWarps ints.
+__device__ __forceinline__ int block_scan(int v, int* scratch, int* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int s = v;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int o = __shfl_up_sync(~0u, s, d);
+    if (lane >= d) s += o;
+  }
+  __syncthreads();  // the scratch of an earlier call has been read
+  if (lane == 31) scratch[warp] = s;
+  __syncthreads();
+  int before = 0, all = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    const int x = scratch[w];
+    before += w < warp ? x : 0;
+    all += x;
+  }
+  *total = all;
+  return before + s - v;
+}
+
+// Tell every CTA of the cluster this CTA's two counts: box[2 * rank + {0, 1}].
+__device__ __forceinline__ void publish(int* box, uint32_t rank, int a, int b) {
+  if (threadIdx.x < kCluster) {
+    const uint32_t at = mapa(smem_u32(box + 2 * rank), threadIdx.x);
+    st_cluster_u32(at, (uint32_t)a);
+    st_cluster_u32(at + 4, (uint32_t)b);
+  }
+}
+
+// ---------------------------------------------------------------------- fork
+struct ForkParams {
+  const int32_t* table;
+  int64_t stride;
+  const int32_t* lens;
+  const int32_t* parents;  // NULL: row i goes on as row i
+  const int32_t* keep;     // NULL: all of the parent's tokens
+  const int32_t* grow;     // NULL: none
+  int R;
+  int32_t* refs;
+  int64_t num_pages;
+  int32_t* free_count;
+  int32_t* out;
+  int64_t out_stride;
+  int32_t* lens_out;
+  int32_t* copies;  // [3, R]: source page, destination page, tokens
+  int* status;
+  int vec;          // rows of both tables start on 16-byte boundaries
+  int chunks;       // chunks of kChunk entries a row
+  int refs_vec;     // refs starts on a 16-byte boundary
+};
+
+constexpr int kChunk = 4096;  // entries of one row that a CTA copies at a time (16 KB)
+
+// Row i of the new table: its parent (-1: none) and the tokens taken from it;
+// negative tokens: the arguments are no valid row.
+__device__ __forceinline__ int taken(const ForkParams& p, int i, int* parent) {
+  const int from = p.parents ? p.parents[i] : i;
+  *parent = from;
+  if (from < -1 || from >= p.R) return -1;
+  const int want = p.keep ? p.keep[i] : 0x7fffffff;
+  if (from < 0) return 0;
+  const int held = p.lens[from];
+  if (held < 0 || held > p.stride || want < 0) return -1;
+  return min(want, held);
+}
+
+// Entries of one page of a row: page * 64 + 0..63, cut at the row's end.
+__device__ __forceinline__ void write_page(const ForkParams& p, int row, int64_t at, int page) {
+  int32_t* dst = p.out + row * p.out_stride + at * kPage;
+  const int base = page * kPage;
+  if (p.vec && (at + 1) * kPage <= p.out_stride) {
+#pragma unroll
+    for (int j = 0; j < kPage; j += 4)
+      *reinterpret_cast<int4*>(dst + j) = make_int4(base + j, base + j + 1, base + j + 2, base + j + 3);
+  } else {
+    const int n = (int)min((int64_t)kPage, p.out_stride - at * kPage);
+    for (int j = 0; j < n; ++j) dst[j] = base + j;
+  }
+}
+
+// The full pages that a row takes over: entries copied as they are, by every
+// CTA past the first cluster.  They depend on nothing that the cluster decides.
+__device__ void copy_rows(const ForkParams& p) {
+  const int64_t tasks = (int64_t)p.R * p.chunks, step = gridDim.x - kCluster;
+  for (int64_t t = blockIdx.x - kCluster; t < tasks; t += step) {
+    const int i = (int)(t / p.chunks);
+    const int64_t e0 = (t % p.chunks) * kChunk;
+    int from;
+    const int kept = taken(p, i, &from);
+    if (kept < 0 || from < 0) continue;
+    const int64_t n = min((int64_t)kept / kPage * kPage, p.out_stride);
+    const int64_t e1 = min(e0 + kChunk, n);
+    const int32_t* src = p.table + from * p.stride;
+    int32_t* dst = p.out + i * p.out_stride;
+    if (p.vec) {
+      // n is a multiple of 4: pages, or a row's stride, which then is one
+      int4 v[kChunk / (4 * kThreads)];
+#pragma unroll
+      for (int u = 0; u < kChunk / (4 * kThreads); ++u) {
+        const int64_t e = e0 + 4 * (threadIdx.x + u * kThreads);
+        if (e < e1) v[u] = __ldg(reinterpret_cast<const int4*>(src + e));
+      }
+#pragma unroll
+      for (int u = 0; u < kChunk / (4 * kThreads); ++u) {
+        const int64_t e = e0 + 4 * (threadIdx.x + u * kThreads);
+        if (e < e1) *reinterpret_cast<int4*>(dst + e) = v[u];
+      }
+    } else {
+      for (int64_t e = e0 + threadIdx.x; e < e1; e += kThreads) dst[e] = src[e];
+    }
+  }
+}
+
+// What a child asks of its parent, for choosing the heir: most pages taken
+// first (a partly taken one counts half), then the lowest row.
+__device__ __forceinline__ unsigned long long claim(int kept, int i) {
+  return ((unsigned long long)(2u * (kept / kPage) + (kept % kPage != 0) + 1) << 32) |
+         (uint32_t)(0x7fffffff - i);
+}
+
+__global__ void __launch_bounds__(kThreads) __cluster_dims__(kCluster, 1, 1)
+    mla_pages_fork_kernel(const ForkParams p) {
+  if (blockIdx.x >= kCluster) {
+    copy_rows(p);
+    return;
+  }
+  extern __shared__ unsigned long long fork_smem[];
+  unsigned long long* best = fork_smem;                      // [R] the heir's claim
+  int* kept = reinterpret_cast<int*>(best + p.R);            // [R] tokens taken
+  int* from = kept + p.R;                                    // [R] parent
+  int* first = from + p.R;                                   // [R + 1] rank of the row's first new page
+  int* tail = first + p.R + 1;                               // [R] partly taken page; its sign: copied
+  __shared__ int scratch[kWarps], box[2][2 * kCluster], bad, freed;
+  const uint32_t rank = cluster_ctarank();
+  const int tid = threadIdx.x, R = p.R;
+  if (tid == 0) bad = freed = 0;
+  for (int i = tid; i < R; i += kThreads) best[i] = 0;
+  __syncthreads();
+
+  // Every CTA of the cluster works out the same decisions, from arguments and
+  // counts that nobody changes before the first cluster barrier.
+  for (int i = tid; i < R; i += kThreads) {
+    int parent;
+    const int k = taken(p, i, &parent);
+    const int64_t g = p.grow ? p.grow[i] : 0, held = p.lens[i];
+    if (k < 0) {
+      atomicOr(&bad, parent < -1 || parent >= R ? MLA_STATUS_BAD_PARENT : MLA_STATUS_BAD_LENGTH);
+    } else if (g < 0 || k + g > p.out_stride || held < 0 || held > p.stride) {
+      atomicOr(&bad, MLA_STATUS_BAD_LENGTH);
+    }
+    kept[i] = max(k, 0);
+    from[i] = parent;
+    if (k >= 0 && parent >= 0) atomicMax(&best[parent], claim(k, i));
+  }
+  __syncthreads();
+  if (bad == 0) {
+    for (int i = tid; i < R; i += kThreads) {
+      const int k = kept[i], parent = from[i];
+      int t = -1;
+      if (parent >= 0 && k % kPage) {
+        t = p.table[parent * p.stride + k / kPage * kPage] / kPage;
+        if (t < 1 || t >= p.num_pages) {
+          atomicOr(&bad, MLA_STATUS_BAD_SLOT);
+          t = -1;
+        } else if (best[parent] != claim(k, i) || p.refs[t] != 1) {
+          t = -1 - t;  // somebody else holds it too: copied
+        }
+      }
+      tail[i] = t;  // > 0: the row keeps it, < -1: page -1 - t is copied, -1: none
+    }
+  }
+  __syncthreads();
+  // Ranks of the new pages: rows in order, a row's pages in order.
+  int64_t total = 0;
+  if (bad == 0) {
+    int carry = 0;
+    for (int i0 = 0; i0 < R; i0 += kThreads) {
+      const int i = i0 + tid;
+      int need = 0;
+      if (i < R)
+        need = (int)(pages_of(kept[i] + (int64_t)(p.grow ? p.grow[i] : 0)) - kept[i] / kPage) -
+               (tail[i] > 0);
+      int sum;
+      const int before = block_scan(need, scratch, &sum);
+      if (i < R) first[i] = carry + before;
+      carry += sum;  // at most R * stride / 64, checked on the host
+    }
+    if (tid == 0) first[R] = carry;
+    total = carry;
+    if (tid == 0 && total > *p.free_count) bad = MLA_STATUS_NO_PAGES;
+  }
+  __syncthreads();
+  const int broken = bad;
+  // No CTA changes a count before every CTA has read those it decides on.
+  cluster_sync();
+  if (broken) {
+    if (rank == 0) {
+      for (int i = tid; i < R; i += kThreads) {
+        p.lens_out[i] = 0;
+        p.copies[i] = p.copies[R + i] = -1;
+        p.copies[2 * R + i] = 0;
+      }
+      if (tid == 0 && p.status) atomicOr(p.status, broken);
+    }
+    return;
+  }
+
+  // The lowest free pages, in rounds of 8 x 8192 counts.
+  int found = 0;
+  for (int round = 0; found < total; ++round) {
+    const int64_t p0 = ((int64_t)round * kCluster + rank) * kPerCta + tid * kPerThread;
+    if ((int64_t)round * kCluster * kPerCta >= p.num_pages) break;  // uniform in the cluster
+    uint32_t zero = 0;
+    if (p0 + kPerThread <= p.num_pages && p.refs_vec) {
+#pragma unroll
+      for (int u = 0; u < kPerThread; u += 4) {
+        const int4 v = *reinterpret_cast<const int4*>(p.refs + p0 + u);
+        zero |= (uint32_t)(v.x == 0) << u | (uint32_t)(v.y == 0) << (u + 1) |
+                (uint32_t)(v.z == 0) << (u + 2) | (uint32_t)(v.w == 0) << (u + 3);
+      }
+    } else {
+      for (int u = 0; u < kPerThread; ++u)
+        if (p0 + u < p.num_pages) zero |= (uint32_t)(p.refs[p0 + u] == 0) << u;
+    }
+    if (p0 == 0) zero &= ~1u;  // the dummy page
+    int sum;
+    int r = block_scan(__popc(zero), scratch, &sum);
+    int* b = box[round & 1];
+    publish(b, rank, sum, 0);
+    cluster_sync();
+    int all = 0;
+    for (int c = 0; c < kCluster; ++c) {
+      if (c < (int)rank) r += b[2 * c];
+      all += b[2 * c];
+    }
+    r += found;
+    found += all;
+    for (; zero && r < total; zero &= zero - 1, ++r) {
+      const int page = (int)(p0 + __ffs(zero) - 1);
+      int lo = 0, hi = R;  // the last row whose first rank is not above r
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (first[mid] <= r) lo = mid; else hi = mid;
+      }
+      const int nth = r - first[lo];
+      p.refs[page] = 1;
+      write_page(p, lo, kept[lo] / kPage + (tail[lo] > 0) + nth, page);
+      if (nth == 0 && tail[lo] < -1) p.copies[R + lo] = page;
+    }
+  }
+  // A count of free pages above what the pool has: the rows that got none are
+  // left with what their entries held.
+  if (found < total && rank == 0 && tid == 0 && p.status) atomicOr(p.status, MLA_STATUS_NO_PAGES);
+
+  // Counts.  Of a parent's pages its heir goes on holding those it takes; the
+  // rest lose the parent, and every other child adds its full pages.  A page
+  // that gains a holder has one that stays (the heir takes at least as many
+  // pages), so a count that reaches 0 is final.
+  int lost = 0;
+  const int lane = tid & 31;
+  const auto page_at = [&](int row, int64_t q) {
+    const int e = p.table[row * p.stride + q * kPage];
+    const int page = e / kPage;
+    return e >= 0 && page < p.num_pages ? page : -1;
+  };
+  bool bad_slot = false;
+  for (int i = rank * kWarps + (tid >> 5); i < R; i += kCluster * kWarps) {
+    const unsigned long long b = best[i];
+    const int heir = b ? 0x7fffffff - (int)(uint32_t)b : -1;
+    const int64_t held = pages_of(p.lens[i]);
+    for (int64_t q = (heir < 0 ? 0 : kept[heir] / kPage + (tail[heir] > 0)) + lane; q < held; q += 32) {
+      const int page = page_at(i, q);
+      bad_slot |= page < 0;
+      if (page > 0) lost += atomicSub(&p.refs[page], 1) == 1;
+    }
+    const int parent = from[i];
+    if (parent >= 0 && best[parent] != claim(kept[i], i))
+      for (int64_t q = lane; q < kept[i] / kPage; q += 32) {
+        const int page = page_at(parent, q);
+        bad_slot |= page < 0;
+        if (page > 0) atomicAdd(&p.refs[page], 1);
+      }
+    if (lane == 0) {
+      p.lens_out[i] = kept[i] + (p.grow ? p.grow[i] : 0);
+      const int t = tail[i];
+      p.copies[i] = t < -1 ? -1 - t : -1;
+      if (t >= -1) p.copies[R + i] = -1;
+      p.copies[2 * R + i] = t < -1 ? kept[i] % kPage : 0;
+      if (t > 0) write_page(p, i, kept[i] / kPage, t);
+    }
+  }
+  if (bad_slot && p.status) atomicOr(p.status, MLA_STATUS_BAD_SLOT);
+  if (lost) atomicAdd(&freed, lost);
+  __syncthreads();
+  int* b = box[0];
+  // The boxes of the last round are read before anybody writes here again.
+  cluster_sync();
+  publish(b, rank, freed, 0);
+  cluster_sync();
+  if (rank == 0 && tid == 0) {
+    int sum = 0;
+    for (int c = 0; c < kCluster; ++c) sum += b[2 * c];
+    *p.free_count += sum - (int)min((int64_t)found, total);
+  }
+}
+
+// ------------------------------------------------------------------- compact
+struct CompactParams {
+  int32_t* refs;
+  int64_t num_pages;
+  int32_t* src;
+  int32_t* dst;
+  int max_moves;
+  int32_t* count;
+};
+
+// The k-th lowest hole among pages 1 .. n and the k-th highest live page above
+// n, n the number of live pages: after all moves exactly the pages 1 .. n are
+// live.  Three passes over the counts (from L2 after the first), each CTA over
+// its own run of pages.
+__global__ void __launch_bounds__(kThreads) __cluster_dims__(kCluster, 1, 1)
+    mla_pages_compact_kernel(const CompactParams p) {
+  __shared__ int scratch[kWarps], box[2][2 * kCluster];
+  const uint32_t rank = cluster_ctarank();
+  const int tid = threadIdx.x;
+  griddep_launch_dependents();
+  const int64_t run = ((p.num_pages + kCluster - 1) / kCluster + 31) / 32 * 32;
+  const int64_t a = min(run * rank, p.num_pages), z = min(a + run, p.num_pages);
+  int live = 0;
+  for (int64_t i = a + tid; i < z; i += kThreads) live += i > 0 && p.refs[i] > 0;
+  int sum;
+  block_scan(live, scratch, &sum);
+  publish(box[0], rank, sum, 0);
+  cluster_sync();
+  int64_t n = 0;
+  for (int c = 0; c < kCluster; ++c) n += box[0][2 * c];
+  int holes = 0, high = 0;
+  for (int64_t i = a + tid; i < z; i += kThreads) {
+    const int r = p.refs[i];
+    holes += i > 0 && i <= n && r <= 0;
+    high += i > n && r > 0;
+  }
+  int my_holes, my_high;
+  block_scan(holes, scratch, &my_holes);
+  block_scan(high, scratch, &my_high);
+  publish(box[1], rank, my_holes, my_high);
+  cluster_sync();
+  int hole_at = 0, high_at = 0, all = 0;
+  for (int c = 0; c < kCluster; ++c) {
+    if (c < (int)rank) hole_at += box[1][2 * c], high_at += box[1][2 * c + 1];
+    all += box[1][2 * c + 1];
+  }
+  const int moves = min(all, p.max_moves);
+  // Runs that neither of the two lists' first `moves` entries reach are skipped.
+  for (int64_t i0 = a; i0 < z; i0 += kThreads) {
+    if (!(i0 <= n ? hole_at < moves : all - 1 - (high_at + my_high) < moves)) {
+      if (i0 + kThreads <= n || i0 > n) continue;
+    }
+    const int64_t i = i0 + tid;
+    const int r = i < z ? p.refs[i] : 0;
+    const bool is_hole = i < z && i > 0 && i <= n && r <= 0, is_high = i < z && i > n && r > 0;
+    int s0, s1;
+    const int h = hole_at + block_scan(is_hole, scratch, &s0);
+    const int g = all - 1 - (high_at + block_scan(is_high, scratch, &s1));
+    if (is_hole && h < moves) p.dst[h] = (int)i;
+    if (is_high && g < moves) p.src[g] = (int)i;
+    hole_at += s0;
+    high_at += s1;
+    my_high -= s1;
+  }
+  cluster_sync();
+  for (int k = rank * kThreads + tid; k < p.max_moves; k += kCluster * kThreads) {
+    if (k < moves) {
+      const int s = p.src[k];
+      p.refs[p.dst[k]] = p.refs[s];
+      p.refs[s] = 0;
+    } else {
+      p.src[k] = p.dst[k] = -1;
+    }
+  }
+  if (rank == 0 && tid == 0) *p.count = moves;
+}
+
+struct RenameParams {
+  const int32_t* table;
+  int64_t stride;
+  const int32_t* lens;
+  int32_t* out;
+  int64_t out_stride;
+  int R, chunks, vec;
+  const int32_t* src;
+  const int32_t* dst;
+  const int32_t* count;
+  int* status;
+};
+
+// The table's live entries with the moved pages' new numbers.  The moved pages
+// are the highest live ones, so src is sorted (descending) and an entry below
+// its last is not moved; others find their place by bisection.
+__global__ void __launch_bounds__(kThreads) mla_pages_rename_kernel(const RenameParams p) {
+  griddep_wait();
+  const int moves = *p.count;
+  const int lowest = moves ? p.src[moves - 1] : 0x7fffffff;
+  const auto renamed = [&](int e) {
+    const int page = e / kPage;
+    if (page < lowest) return e;
+    int lo = 0, hi = moves;  // the first entry not above the page
+    while (lo < hi) {
+      const int mid = (lo + hi) / 2;
+      if (p.src[mid] > page) lo = mid + 1; else hi = mid;
+    }
+    return lo < moves && p.src[lo] == page ? p.dst[lo] * kPage + e % kPage : e;
+  };
+  const bool in_place = p.table == p.out;
+  const int64_t tasks = (int64_t)p.R * p.chunks;
+  for (int64_t t = blockIdx.x; t < tasks; t += gridDim.x) {
+    const int i = (int)(t / p.chunks);
+    const int64_t e0 = (t % p.chunks) * kChunk;
+    const int64_t len = p.lens[i], room = min(p.stride, p.out_stride);
+    if (len < 0 || len > room) {
+      if (e0 == 0 && threadIdx.x == 0 && p.status) atomicOr(p.status, MLA_STATUS_BAD_LENGTH);
+      continue;
+    }
+    const int64_t e1 = min(min(e0 + kChunk, pages_of(len) * kPage), room);
+    const int32_t* src = p.table + i * p.stride;
+    int32_t* dst = p.out + i * p.out_stride;
+    if (p.vec) {
+      int4 v[kChunk / (4 * kThreads)];
+#pragma unroll
+      for (int u = 0; u < kChunk / (4 * kThreads); ++u) {
+        const int64_t e = e0 + 4 * (threadIdx.x + u * kThreads);
+        if (e < e1) v[u] = *reinterpret_cast<const int4*>(src + e);
+      }
+#pragma unroll
+      for (int u = 0; u < kChunk / (4 * kThreads); ++u) {
+        const int64_t e = e0 + 4 * (threadIdx.x + u * kThreads);
+        if (e >= e1) continue;
+        const int x = renamed(v[u].x);  // four entries of one page
+        if (in_place && x == v[u].x) continue;
+        *reinterpret_cast<int4*>(dst + e) = make_int4(x, v[u].y + (x - v[u].x), v[u].z + (x - v[u].x),
+                                                      v[u].w + (x - v[u].x));
+      }
+    } else {
+      for (int64_t e = e0 + threadIdx.x; e < e1; e += kThreads) {
+        const int x = renamed(src[e]);
+        if (!in_place || x != src[e]) dst[e] = x;
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------- copy
+constexpr int kCopyThreads = 256;
+constexpr int kCopyVecs = 4;  // 16-byte vectors in flight per thread
+constexpr int kSlice = kCopyThreads * kCopyVecs * 16;
+
+__global__ void __launch_bounds__(kCopyThreads)
+    mla_kv_copy_kernel(uint8_t* kv, float* scale, int row_bytes, int64_t num_pages,
+                       const int32_t* src, const int32_t* dst, const int32_t* tokens,
+                       const int32_t* count, int64_t n, int slices, int* status) {
+  griddep_wait();
+  if (count) n = min(n, (int64_t)max(*count, 0));
+  const int64_t tasks = n * slices;
+  for (int64_t t = blockIdx.x; t < tasks; t += gridDim.x) {
+    const int64_t i = t / slices;
+    const int s = src[i], d = dst[i];
+    if (s < 0 || d < 0 || s == d) continue;
+    if (s >= num_pages || d >= num_pages) {
+      if (threadIdx.x == 0 && status) atomicOr(status, MLA_STATUS_BAD_SLOT);
+      continue;
+    }
+    const int live = tokens ? min(max(tokens[i], 0), kPage) : kPage;
+    const int bytes = live * row_bytes, at = (int)(t % slices) * kSlice;
+    const int64_t page_bytes = (int64_t)kPage * row_bytes;
+    const uint8_t* from = kv + s * page_bytes;
+    uint8_t* to = kv + d * page_bytes;
+    uint4 v[kCopyVecs];
+#pragma unroll
+    for (int u = 0; u < kCopyVecs; ++u) {
+      const int o = at + (u * kCopyThreads + threadIdx.x) * 16;
+      if (o < bytes) v[u] = *reinterpret_cast<const uint4*>(from + o);
+    }
+#pragma unroll
+    for (int u = 0; u < kCopyVecs; ++u) {
+      const int o = at + (u * kCopyThreads + threadIdx.x) * 16;
+      if (o < bytes) *reinterpret_cast<uint4*>(to + o) = v[u];
+    }
+    if (scale && at == 0 && threadIdx.x < live)
+      scale[(int64_t)d * kPage + threadIdx.x] = scale[(int64_t)s * kPage + threadIdx.x];
+  }
+}
+
+int sm_count(int* sms) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+  return e == cudaSuccess ? MLA_OK : cuda_fail(e, "device query");
+}
+
+// A launch whose first instructions may overlap the end of the kernel before it
+// in the stream (which the kernel waits for).
+template <class... Args>
+cudaError_t launch_after(void (*kernel)(Args...), unsigned grid, unsigned threads, cudaStream_t st,
+                         Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid, 1, 1);
+  cfg.blockDim = dim3(threads, 1, 1);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+}  // namespace
+}  // namespace mla
+
+using namespace mla;
+
+extern "C" int mla_pages_fork(const int32_t* table, int64_t stride, const int32_t* lens,
+                              const int32_t* parents, const int32_t* keep, const int32_t* grow,
+                              int R, int32_t* refs, int64_t num_pages, int32_t* free_count,
+                              int32_t* table_out, int64_t out_stride, int32_t* lens_out,
+                              int32_t* copies, int* status, mla_stream_t stream) {
+  if (R < 0 || stride < 1 || out_stride < 1 || num_pages < 1)
+    return fail(MLA_ERR_INVALID_ARG, "mla_pages_fork: R %d < 0 or strides %lld, %lld or pages %lld < 1",
+                R, (long long)stride, (long long)out_stride, (long long)num_pages);
+  if (R == 0) return MLA_OK;
+  if (R > kMaxRows)
+    return fail(MLA_ERR_UNSUPPORTED, "mla_pages_fork: R %d > %d rows", R, kMaxRows);
+  if (num_pages > ((int64_t)1 << 31) / kPage || stride > 0x7fffffff || out_stride > 0x7fffffff ||
+      R * pages_of(std::max(stride, out_stride)) > 0x7fffffff)
+    return fail(MLA_ERR_INVALID_ARG, "mla_pages_fork: more than 2^31 slots or table pages");
+  if (!table || !lens || !refs || !free_count || !table_out || !lens_out || !copies)
+    return fail(MLA_ERR_INVALID_ARG, "mla_pages_fork: a required pointer is NULL");
+  if (table_out < table + (R - 1) * stride + stride && table < table_out + (R - 1) * out_stride + out_stride)
+    return fail(MLA_ERR_INVALID_ARG, "mla_pages_fork: table_out overlaps table");
+  if (lens == lens_out)
+    return fail(MLA_ERR_INVALID_ARG, "mla_pages_fork: lens_out is lens");
+  const void* all[] = {table, lens, parents, keep, grow, refs, free_count, table_out, lens_out, copies, status};
+  for (const void* q : all)
+    if (q && !aligned(q, 4)) return fail(MLA_ERR_MISALIGNED, "mla_pages_fork: arrays need 4-B alignment");
+  ForkParams p{table, stride, lens, parents, keep, grow, R, refs, num_pages, free_count,
+               table_out, out_stride, lens_out, copies, status};
+  p.vec = aligned(table, 16) && aligned(table_out, 16) && stride % 4 == 0 && out_stride % 4 == 0;
+  p.chunks = (int)((std::min(stride, out_stride) + kChunk - 1) / kChunk);
+  p.refs_vec = aligned(refs, 16);
+  int sms = 0;
+  const int rc = sm_count(&sms);
+  if (rc != MLA_OK) return rc;
+  // up to two CTAs per SM for the copies, in whole clusters
+  const int64_t tasks = (int64_t)R * p.chunks;
+  const int64_t clusters = 1 + std::min<int64_t>((tasks + kCluster - 1) / kCluster, 2 * sms / kCluster);
+  const int smem = R * 8 + (4 * R + 1) * 4;
+  static_assert(kMaxRows * 24 + 4 <= 200 * 1024, "shared memory budget");
+  cudaError_t e = cudaSuccess;
+  if (smem > 47 * 1024)
+    e = cudaFuncSetAttribute(mla_pages_fork_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             kMaxRows * 24 + 4);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(mla_pages_fork_kernel)");
+  mla_pages_fork_kernel<<<(unsigned)(clusters * kCluster), kThreads, smem, (cudaStream_t)stream>>>(p);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return cuda_fail(e, "launch mla_pages_fork_kernel");
+  return MLA_OK;
+}
+
+extern "C" int mla_pages_compact(const int32_t* table, int64_t stride, const int32_t* lens, int R,
+                                 int32_t* refs, int64_t num_pages, int32_t* table_out,
+                                 int64_t out_stride, int32_t* src, int32_t* dst, int max_moves,
+                                 int32_t* count, int* status, mla_stream_t stream) {
+  if (R < 0 || stride < 1 || out_stride < 1 || num_pages < 1 || max_moves < 0)
+    return fail(MLA_ERR_INVALID_ARG, "mla_pages_compact: R %d or max_moves %d < 0, or strides %lld, "
+                "%lld or pages %lld < 1", R, max_moves, (long long)stride, (long long)out_stride,
+                (long long)num_pages);
+  if (num_pages > ((int64_t)1 << 31) / kPage || stride > 0x7fffffff || out_stride > 0x7fffffff)
+    return fail(MLA_ERR_INVALID_ARG, "mla_pages_compact: more than 2^31 slots or table entries a row");
+  if (!refs || !count || (R > 0 && (!table || !lens || !table_out)) || (max_moves > 0 && (!src || !dst)))
+    return fail(MLA_ERR_INVALID_ARG, "mla_pages_compact: a required pointer is NULL");
+  const bool overlap = R > 0 && table_out < table + (R - 1) * stride + stride &&
+                       table < table_out + (R - 1) * out_stride + out_stride;
+  if (overlap && (table != table_out || stride != out_stride))
+    return fail(MLA_ERR_INVALID_ARG, "mla_pages_compact: table_out overlaps table without being it");
+  const void* all[] = {table, lens, refs, table_out, src, dst, count, status};
+  for (const void* q : all)
+    if (q && !aligned(q, 4)) return fail(MLA_ERR_MISALIGNED, "mla_pages_compact: arrays need 4-B alignment");
+  const cudaStream_t st = (cudaStream_t)stream;
+  const CompactParams c{refs, num_pages, src, dst, max_moves, count};
+  mla_pages_compact_kernel<<<kCluster, kThreads, 0, st>>>(c);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return cuda_fail(e, "launch mla_pages_compact_kernel");
+  if (R == 0) return MLA_OK;
+  RenameParams p{table, stride, lens, table_out, out_stride, R, 0, 0, src, dst, count, status};
+  p.vec = aligned(table, 16) && aligned(table_out, 16) && stride % 4 == 0 && out_stride % 4 == 0;
+  p.chunks = (int)((std::min(stride, out_stride) + kChunk - 1) / kChunk);
+  int sms = 0;
+  const int rc = sm_count(&sms);
+  if (rc != MLA_OK) return rc;
+  const int64_t tasks = (int64_t)R * p.chunks;
+  e = launch_after(mla_pages_rename_kernel, (unsigned)std::min<int64_t>(tasks, 4 * sms), kThreads, st, p);
+  if (e != cudaSuccess) return cuda_fail(e, "launch mla_pages_rename_kernel");
+  return MLA_OK;
+}
+
+extern "C" int mla_kv_copy(void* kv_pages, mla_kv_dtype kv_dtype, float* kv_scale, int64_t num_slots,
+                           const int32_t* src, const int32_t* dst, const int32_t* tokens,
+                           const int32_t* count, int64_t n, int* status, mla_stream_t stream) {
+  if (n < 0) return fail(MLA_ERR_INVALID_ARG, "mla_kv_copy: n = %lld < 0", (long long)n);
+  const int row_bytes = kv_dtype == MLA_KV_BF16 ? 2 * MLA_ROW_DIM
+                        : kv_dtype == MLA_KV_FP8_E4M3 ? MLA_ROW_DIM
+                        : kv_dtype == MLA_KV_FP4_E2M1 ? MLA_FP4_ROW_BYTES : 0;
+  if (!row_bytes) return fail(MLA_ERR_INVALID_ARG, "mla_kv_copy: unknown kv_dtype %d", (int)kv_dtype);
+  if (num_slots < kPage || num_slots >= (int64_t)1 << 31)
+    return fail(MLA_ERR_INVALID_ARG, "mla_kv_copy: num_slots %lld outside [%d, 2^31)",
+                (long long)num_slots, kPage);
+  if (n == 0) return MLA_OK;
+  if (!kv_pages || !src || !dst || (kv_dtype == MLA_KV_FP8_E4M3 && !kv_scale))
+    return fail(MLA_ERR_INVALID_ARG, "mla_kv_copy: a required pointer is NULL");
+  if (!aligned(kv_pages, 16)) return fail(MLA_ERR_MISALIGNED, "mla_kv_copy: the pool needs 16-B alignment");
+  const void* all[] = {kv_scale, src, dst, tokens, count, status};
+  for (const void* q : all)
+    if (q && !aligned(q, 4)) return fail(MLA_ERR_MISALIGNED, "mla_kv_copy: arrays need 4-B alignment");
+  int sms = 0;
+  const int rc = sm_count(&sms);
+  if (rc != MLA_OK) return rc;
+  const int slices = (kPage * row_bytes + kSlice - 1) / kSlice;
+  const int64_t tasks = n * slices;
+  const cudaError_t e = launch_after(
+      mla_kv_copy_kernel, (unsigned)std::min<int64_t>(tasks, 8 * sms), kCopyThreads, (cudaStream_t)stream,
+      static_cast<uint8_t*>(kv_pages), kv_dtype == MLA_KV_FP8_E4M3 ? kv_scale : (float*)nullptr, row_bytes,
+      num_slots / kPage, src, dst, tokens, count, n, slices, status);
+  if (e != cudaSuccess) return cuda_fail(e, "launch mla_kv_copy_kernel");
+  return MLA_OK;
+}

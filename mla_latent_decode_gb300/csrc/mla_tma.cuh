@@ -39,6 +39,11 @@ int make_tensor_map_bf16_3d(CUtensorMap* map, const void* base,
                             const uint64_t dims[3], const uint64_t strides[2],
                             const uint32_t box[3]);
 
+// The same in 4 dims.
+int make_tensor_map_bf16_4d(CUtensorMap* map, const void* base,
+                            const uint64_t dims[4], const uint64_t strides[3],
+                            const uint32_t box[4]);
+
 // Tensor maps of a launch's query rows, [B * q_len * H, 512] and [.., 64]
 // bf16 (as 3-D arrays with one plane), in boxes of 64 values x min(128,
 // rows) rows with the 128-byte swizzle; *box_rows receives the box height.

@@ -1,0 +1,179 @@
+"""GPU parity of the beam selection (mla_beam_select) with the float64
+definition: tokens and parents exactly, scores within the roundings.
+
+A score is c + (x - lse) in fp64, rounded to fp32 (2^-24 of itself); the lse's sum
+of exponentials is in fp32: a term's exponent is a rounded difference times a
+rounded log2(e) (2^-23 |x - max|, at most 2^-16 for the terms within 128 of the
+maximum, the others are 0), the exponential 2^-21, and the sums are up to 64 + 10
+additions deep per thread, warp and block (2^-17): 2^-15 in all, of a sum.  The order
+of two beams' tokens is the definition's where their scores differ by more than
+that, so the inputs keep them apart.
+"""
+import math
+
+import pytest
+import torch
+
+import mla_latent_decode_gb300 as mla
+from mla_latent_decode_gb300 import build
+
+pytestmark = pytest.mark.gpu
+TOL = 2.0 ** -15
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    build.build()
+    mla.library()
+
+
+def _reference(logits, scores, k, finished, end):
+    """Scores fp64, rows and tokens int64 [B, k]."""
+    B, W, V = logits.shape
+    x = logits.double().cpu()
+    c = scores.double().cpu()
+    lse = torch.logsumexp(x, -1)
+    s = c[..., None] + (x - lse[..., None])
+    whole = lse.isfinite() & c.isfinite()
+    s = torch.where(whole[..., None], s, -math.inf)
+    if finished is not None:
+        done = finished.cpu().bool()
+        s[done] = -math.inf
+        for b, w in done.nonzero().tolist():
+            if math.isfinite(float(c[b, w])):
+                s[b, w, end] = c[b, w]
+    best, at = torch.sort(s.reshape(B, -1), dim=1, descending=True, stable=True)
+    at = at[:, :k]
+    return best[:, :k], at // V + W * torch.arange(B)[:, None], at % V
+
+
+def _check(logits, scores, k, finished=None, end=0, status=0):
+    word = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got, rows, tokens = mla.beam_select(logits, scores, k, finished=finished, end_token=end, status=word)
+    want, r, t = _reference(logits, scores, k, finished, end)
+    assert int(word.item()) == status
+    got = got.cpu().double()
+    live = want > -math.inf
+    assert torch.equal(got > -math.inf, live)
+    assert bool(((got - want).abs() <= TOL + 2.0 ** -23 * want.abs())[live].all())
+    assert torch.equal(rows.cpu().long(), r)
+    assert torch.equal(tokens.cpu().long(), t)
+
+
+def _inputs(B, W, V, dtype=torch.bfloat16, seed=0):
+    g = torch.Generator().manual_seed(seed)
+    logits = (3 * torch.randn((B, W, V), generator=g)).to(dtype).cuda()
+    scores = (-5 * torch.rand((B, W), generator=g)).cuda()
+    return logits, scores
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("B,W,V,k", [
+    (1, 1, 1, 1), (1, 2, 1, 2), (2, 1, 7, 7), (1, 3, 5, 15), (3, 4, 100, 8), (2, 5, 1003, 10), (1, 4, 32000, 8),
+    (2, 3, 65537, 64), (1, 32, 2000, 64), (9, 2, 511, 1)])
+def test_matches_the_definition(B, W, V, k, dtype):
+    logits, scores = _inputs(B, W, V, dtype)
+    _check(logits, scores, k)
+
+
+@pytest.mark.parametrize("V", [131072, 262145])
+def test_large_vocabularies(V):
+    logits, scores = _inputs(2, 3, V)
+    _check(logits, scores, 6)
+
+
+def test_rows_at_odd_addresses():
+    logits, scores = _inputs(2, 3, 1200)
+    for off in (1, 3, 5):
+        _check(logits[:, :, off:off + 1001], scores, 9)
+    _check(logits[:, 1:, 7:], scores[:, 1:].contiguous(), 4)
+
+
+def test_ties_go_to_the_lowest_position():
+    logits, scores = _inputs(2, 4, 40000)
+    logits = torch.round(logits.float()).bfloat16()     # few values, many of each
+    logits[1] = logits[1, 0]                            # all beams alike
+    scores[1] = -1.0
+    _check(logits, scores, 40)
+    _check(torch.zeros_like(logits), torch.zeros_like(scores), 64)
+    logits[0, :, 20000:] = -0.0
+    logits[0, :, :20000] = 0.0
+    _check(logits, torch.zeros_like(scores), 16)
+
+
+@pytest.mark.parametrize("descending", [False, True])
+def test_sorted_vocabularies(descending):
+    """Every value above those before it, or all the best in a few threads' hands."""
+    x = torch.sort(torch.randn((2, 2, 50000), generator=torch.Generator().manual_seed(1)), dim=-1,
+                   descending=descending).values.cuda()
+    _check(x, torch.tensor([[0.0, -0.3], [-1.0, -1.1]], device="cuda"), 64)
+    x[:, :, 3000:] = -math.inf
+    _check(x, torch.tensor([[0.0, -0.3], [-1.0, -1.1]], device="cuda"), 16)
+
+
+def test_masked_vocabularies():
+    logits, scores = _inputs(3, 4, 30000, torch.float32, seed=4)
+    keep = torch.rand(logits.shape, generator=torch.Generator().manual_seed(5)).cuda() < 0.001
+    masked = logits.masked_fill(~keep, -math.inf)
+    _check(masked, scores, 16)
+    few = torch.full_like(logits, -math.inf)
+    few[0, 1, 77] = 1.0
+    few[0, 3, [5, 900]] = 2.0                       # three continuations, then the lowest positions
+    few[1, 0, 29999] = 0.0
+    _check(few, scores, 12)
+    low = torch.finfo(torch.float32).min
+    _check(logits.masked_fill(~keep, low), scores, 16)
+
+
+def test_finished_and_dead_beams():
+    logits, scores = _inputs(3, 5, 2000, seed=6)
+    done = torch.zeros((3, 5), dtype=torch.bool, device="cuda")
+    done[0, 2] = done[1, :4] = done[2] = True
+    _check(logits, scores, 10, finished=done, end=1999)
+    _check(logits, scores, 10, finished=done.to(torch.uint8), end=0)
+    scores[:, 1:] = -math.inf                       # the first step: one beam counts
+    _check(logits, scores, 10)
+    _check(logits, scores, 10, finished=done, end=3)
+    scores[:] = -math.inf
+    _check(logits, scores, 7)
+
+
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+def test_broken_beams_end(bad):
+    logits, scores = _inputs(2, 4, 3000, seed=7)
+    logits[0, 2, 2999] = bad
+    _check(logits, scores, 8, status=mla.STATUS_BAD_SCORE)
+    logits, scores = _inputs(2, 4, 3000, seed=8)
+    scores[1, 0] = bad
+    _check(logits, scores, 8, status=mla.STATUS_BAD_SCORE)
+    scores[:] = math.nan
+    _check(logits, scores, 8, status=mla.STATUS_BAD_SCORE)
+
+
+def test_far_logits():
+    logits, scores = _inputs(1, 2, 5000, torch.float32, seed=9)
+    logits[0, 0] += 3e4
+    logits[0, 1] -= 3e4
+    # lse and logit are rounded to fp32 steps of 2^-9 near 3e4: the scores follow the stored logits
+    _check(logits, scores, 8)
+    logits[0, 0, 123] = 3.3e38
+    logits[0, 1, 17] = -3.3e38
+    _check(logits, scores, 8)
+
+
+def test_captured_and_repeated():
+    logits, scores = _inputs(4, 4, 20000, seed=10)
+    want = [t.clone() for t in mla.beam_select(logits, scores, 8)]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = mla.beam_select(logits, scores, 8)
+    for _ in range(3):
+        for t in got:
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_no_requests():
+    mla.beam_select(torch.empty((0, 3, 10), device="cuda"), torch.empty((0, 3), device="cuda"), 4)
