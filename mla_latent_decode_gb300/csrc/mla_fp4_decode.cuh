@@ -176,17 +176,4 @@ __device__ __forceinline__ uint32_t finite_scales(uint32_t w) {
   return w & keep;
 }
 
-// One lane of a converged warp.  With the warp index and the TMEM base
-// shuffled from lane 0 the compiler keeps MMA descriptors in uniform
-// registers; behind a test of threadIdx they pass through vector registers, an
-// issue cost of about 45 cycles per MMA on an idle SM and more on a busy one
-// (a probe; N = 128 executes in 64).
-__device__ __forceinline__ bool elect_one() {
-  uint32_t e;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(e));
-  return e != 0;
-}
-
 }  // namespace mla

@@ -246,11 +246,17 @@ __device__ __forceinline__ void produce(uint8_t* base, Ctl& c, const PrefillPara
   }
 }
 
-__device__ __forceinline__ void issue_mmas(uint8_t* base, Ctl& c, const PrefillParams& p, const Unit& u,
+// a0, a1: key tiles of the two row tiles.
+__device__ __forceinline__ void issue_mmas(uint8_t* base, Ctl& c, const PrefillParams& p, int a0, int a1,
                                            uint32_t tmem) {
   constexpr uint32_t idesc_s = idesc_bf16_f32(kRows, kKeys, false, false);
   constexpr uint32_t idesc_o = idesc_bf16_f32(kRows, kKeys, false, true);
-  const int tiles = u.j1 - u.j0;
+  const int tiles = max(a0, a1);
+  const uint64_t q0 = sdesc_sw128(smem_u32(base), 16, 1024);
+  const uint64_t k0 = sdesc_sw128(smem_u32(base + 6 * kBox), 16, 1024);
+  // V: MN-major, the next 64 dims 8 KB (LBO) on, the next 8 tokens 1 KB (SBO) on,
+  // the next 16 tokens 2 KB; P: 16 tokens in 8 columns
+  const uint64_t v0 = sdesc_sw128(smem_u32(base + 6 * kBox), kBox / 2, 1024);
   bool ok = true;
   const auto wait = [&](uint64_t* bar, uint32_t parity) {
     ok = ok && mbar_wait_cta(smem_u32(bar), parity, &c.abort_flag);
@@ -261,7 +267,7 @@ __device__ __forceinline__ void issue_mmas(uint8_t* base, Ctl& c, const PrefillP
 #pragma unroll 1
     for (int g = 0; g < 2 && ok; ++g) {
       const uint32_t s = tmem + g * kKeys, o = tmem + (2 + g) * kKeys;
-      const int a = (g ? u.n1 : u.n0) - u.j0;  // tiles of this row tile
+      const int a = g ? a1 : a0;
       if (t > 0 && t - 1 < a) {
         if (!wait(&c.p[g], (t - 1) & 1)) break;
 #pragma unroll 1
@@ -269,9 +275,7 @@ __device__ __forceinline__ void issue_mmas(uint8_t* base, Ctl& c, const PrefillP
           const uint32_t st = (vpos + i) % kStages;
           if (!wait(&c.full[st], (vpos + i) / kStages & 1)) break;
           tc_fence_after();
-          // V: MN-major, the next 64 dims 8 KB (LBO) on, the next 8 tokens 1 KB
-          // (SBO) on, the next 16 tokens 2 KB; P: 16 tokens in 8 columns
-          const uint64_t b = sdesc_sw128(smem_u32(base + (6 + st) * kBox), kBox / 2, 1024);
+          const uint64_t b = v0 + st * (kBox >> 4);
 #pragma unroll
           for (int k = 0; k < 4; ++k)
             mma_ts(o, s + (4 * i + k) * 8, b + 128 * k, idesc_o, (t > 1 || i || k) ? 1u : 0u);
@@ -286,8 +290,7 @@ __device__ __forceinline__ void issue_mmas(uint8_t* base, Ctl& c, const PrefillP
           const uint32_t st = (kpos + i) % kStages;
           if (!wait(&c.full[st], (kpos + i) / kStages & 1)) break;
           tc_fence_after();
-          const uint64_t q = sdesc_sw128(smem_u32(base + (3 * g + i) * kBox), 16, 1024);
-          const uint64_t b = sdesc_sw128(smem_u32(base + (6 + st) * kBox), 16, 1024);
+          const uint64_t q = q0 + (3 * g + i) * (kBox >> 4), b = k0 + st * (kBox >> 4);
 #pragma unroll
           for (int k = 0; k < 4; ++k) mma_ss(s, q + 2 * k, b + 2 * k, idesc_s, (i || k) ? 1u : 0u);
         }
@@ -496,7 +499,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* base =
       reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   Ctl& c = *reinterpret_cast<Ctl*>(base + (6 + kStages) * kBox);
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int warp = __shfl_sync(~0u, (int)threadIdx.x / 32, 0), lane = threadIdx.x % 32;
   Unit u;
   if (!find_unit(p, u)) return;  // the whole CTA
   if (threadIdx.x == 0) {
@@ -525,14 +528,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = c.tmem;
+  const uint32_t tmem = __shfl_sync(~0u, c.tmem, 0);
   // Roles never rejoin below their register split: each ends with the teardown.
   if (warp >= kWarpTma) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
     if (warp == kWarpTma) {
       produce(base, c, p, u, &qn, &qr, &kn, &kr, &v, lane);
     } else if (warp == kWarpMma) {
-      if (lane == 0) issue_mmas(base, c, p, u, tmem);
+      // uniform values: see elect_one
+      const int a0 = __shfl_sync(~0u, u.n0 - u.j0, 0), a1 = __shfl_sync(~0u, u.n1 - u.j0, 0);
+      if (elect_one()) issue_mmas(base, c, p, a0, a1, tmem);
     } else {
       clean_values(base, c, p, u, warp - kWarpClean, lane);
     }
