@@ -279,6 +279,7 @@ __device__ __forceinline__ void issue_mmas(uint8_t* base, Ctl& c, const PrefillP
 #pragma unroll
           for (int k = 0; k < 4; ++k)
             mma_ts(o, s + (4 * i + k) * 8, b + 128 * k, idesc_o, (t > 1 || i || k) ? 1u : 0u);
+          if (g || t - 1 >= a1) mma_commit(smem_u32(&c.empty[st]));
         }
         if (!ok) break;
         if (t == a) mma_commit(smem_u32(&c.o[g]));
@@ -293,16 +294,12 @@ __device__ __forceinline__ void issue_mmas(uint8_t* base, Ctl& c, const PrefillP
           const uint64_t q = q0 + (3 * g + i) * (kBox >> 4), b = k0 + st * (kBox >> 4);
 #pragma unroll
           for (int k = 0; k < 4; ++k) mma_ss(s, q + 2 * k, b + 2 * k, idesc_s, (i || k) ? 1u : 0u);
+          if (g || t >= a1) mma_commit(smem_u32(&c.empty[st]));
         }
         if (!ok) break;
         mma_commit(smem_u32(&c.s[g]));
       }
     }
-    if (!ok) break;
-    if (t > 0)
-      for (int i = 0; i < 2; ++i) mma_commit(smem_u32(&c.empty[(vpos + i) % kStages]));
-    if (t < tiles)
-      for (int i = 0; i < 3; ++i) mma_commit(smem_u32(&c.empty[(kpos + i) % kStages]));
   }
   if (!ok) {
     c.abort_flag = 1;
@@ -372,7 +369,11 @@ __device__ __forceinline__ void softmax_rows(Ctl& c, const PrefillParams& p, con
   const uint64_t scale2 = f2pack(p.scale2, p.scale2);
   float ref = -INFINITY, l = 0.f;  // raw scores; sum of 2^((s - ref) scale2)
   bool ok = true;
-  const int tiles = (g ? u.n1 : u.n0) - u.j0;
+  const int tiles = (g ? u.n1 : u.n0) - u.j0, seen0 = exists ? seen - u.j0 * kKeys : 0x7fffffff;
+  // where the row's output goes: its row of out, or of the part's workspace
+  const bool whole = u.parts == 1, cleaned = u.j1 > u.clean0;
+  const int64_t row = whole ? (u.q0 + i) * p.H + u.h
+                            : ((int64_t)(u.slot + u.part) * p.H + u.h) * kBlock + g * kRows + r;
   for (int t = 0; t < tiles; ++t) {
     if (!(ok = mbar_wait_cta(smem_u32(&c.s[g]), t & 1, &c.abort_flag))) break;
     tc_fence_after();
@@ -380,7 +381,7 @@ __device__ __forceinline__ void softmax_rows(Ctl& c, const PrefillParams& p, con
 #pragma unroll
     for (int b = 0; b < 4; ++b) tmem_ld32(s_at + 32 * b, *reinterpret_cast<uint32_t(*)[32]>(&s[32 * b]));
     tmem_wait_ld();
-    const int last = seen - (u.j0 + t) * kKeys;  // columns of this tile that the row sees
+    const int last = seen0 - t * kKeys;  // columns of this tile that the row sees
     if (__any_sync(~0u, last < kKeys)) {
 #pragma unroll
       for (int e = 0; e < kKeys; ++e) s[e] = e < last ? s[e] : -INFINITY;
@@ -439,7 +440,7 @@ __device__ __forceinline__ void softmax_rows(Ctl& c, const PrefillParams& p, con
     mbar_arrive(smem_u32(&c.p[g]));
   }
   if (ok && tiles > 0) ok = mbar_wait_cta(smem_u32(&c.o[g]), 0, &c.abort_flag);
-  if (ok && u.j1 > u.clean0) ok = mbar_wait_cta(smem_u32(&c.cleaned), 0, &c.abort_flag);
+  if (ok && cleaned) ok = mbar_wait_cta(smem_u32(&c.cleaned), 0, &c.abort_flag);
   if (!ok) {
     c.abort_flag = 1;
     if (lane == 0 && p.status) atomicOr(p.status, MLA_STATUS_WAIT_TIMEOUT);
@@ -449,8 +450,6 @@ __device__ __forceinline__ void softmax_rows(Ctl& c, const PrefillParams& p, con
   const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
   const float lse = l > 0.f || l != l ? ref * p.sm_scale + logf(l) : -INFINITY;
   const bool odd = *reinterpret_cast<volatile int*>(&c.any_odd) != 0;
-  const int64_t row = (u.q0 + i) * p.H + u.h;
-  const int64_t part_row = ((int64_t)(u.slot + u.part) * p.H + u.h) * kBlock + g * kRows + r;
 #pragma unroll 1
   for (int b = 0; b < 4; ++b) {
     uint32_t o[32];
@@ -473,20 +472,20 @@ __device__ __forceinline__ void softmax_rows(Ctl& c, const PrefillParams& p, con
         if (c.odd[2][32 * b + e] < seen) f[e] -= INFINITY;
       }
     }
-    if (exists && u.parts == 1) {
+    if (exists && whole) {
       uint4* dst = reinterpret_cast<uint4*>(p.out + row * MLA_V_HEAD_DIM + 32 * b);
 #pragma unroll
       for (int e = 0; e < 4; ++e)
         dst[e] = make_uint4(pack_bf16(f[8 * e], f[8 * e + 1]), pack_bf16(f[8 * e + 2], f[8 * e + 3]),
                             pack_bf16(f[8 * e + 4], f[8 * e + 5]), pack_bf16(f[8 * e + 6], f[8 * e + 7]));
     } else if (exists) {
-      float4* dst = reinterpret_cast<float4*>(p.O_part + part_row * MLA_V_HEAD_DIM + 32 * b);
+      float4* dst = reinterpret_cast<float4*>(p.O_part + row * MLA_V_HEAD_DIM + 32 * b);
 #pragma unroll
       for (int e = 0; e < 8; ++e) dst[e] = make_float4(f[4 * e], f[4 * e + 1], f[4 * e + 2], f[4 * e + 3]);
     }
   }
   if (exists) {
-    if (u.parts > 1) p.LSE_part[part_row] = lse;
+    if (!whole) p.LSE_part[row] = lse;
     else if (p.lse) p.lse[row] = lse;
   }
 }
