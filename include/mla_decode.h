@@ -669,8 +669,8 @@ int mla_lse_combine_bf16_parts(const void* O_part, const float* LSE_part,
  *   k_rope   bf16 [Tk, 64], one for all heads, with a token stride
  *   cu_q, cu_kv  int32 [N + 1], non-decreasing, 0 <= . <= Tq, Tk;
  *   prefix   int32 [N] or NULL (0): keys that every query of a sequence sees
- *   work     int32 [num_work, 8], device: mla_plan_prefill's list; num_parts its
- *            parts.  The plan must be made for the lengths in cu_q and cu_kv: rows
+ *   work     int32 [num_work, ctas, 8], device: mla_plan_prefill's list, ctas and
+ *            num_parts as it gave them.  The plan must be made for the lengths in cu_q and cu_kv: rows
  *            that no entry names are not written, an entry that fits no sequence
  *            sets MLA_STATUS_BAD_WORK and does nothing, lengths that leave the
  *            arrays set MLA_STATUS_BAD_LENGTH and their sequence is not computed.
@@ -689,30 +689,32 @@ int mla_prefill(const void* q_nope, int64_t qn_token_stride, int64_t qn_head_str
                 const void* v, int64_t v_token_stride, int64_t v_head_stride,
                 int64_t Tk, int H, const int32_t* cu_q, const int32_t* cu_kv,
                 const int32_t* prefix, int N, int causal, float sm_scale,
-                const int32_t* work, int num_work, int num_parts, float* O_part,
+                const int32_t* work, int num_work, int ctas, int num_parts, float* O_part,
                 float* LSE_part, void* out, float* lse, int* status,
                 mla_stream_t stream);
 
 /*
- * Plan of mla_prefill on the host: the sequences' blocks of 256 query rows,
- * longest sequences first, a sequence's heads one after another (their keys and
+ * Plan of mla_prefill on the host: the sequences' blocks of 256 query rows a CTA,
+ * or of 512 rows a pair of CTAs, longest sequences first, a sequence's heads one after another (their keys and
  * values then stay in L2) and a head's blocks from the longest down; where
  * there are too few blocks for the SMs, blocks are cut along the keys into
  * parts that a second launch merges.
  *   q_lens, kv_lens, prefix   host int32 [N] (prefix may be NULL)
- *   num_sms     0: the current device's (148 where there is none)
- *   work_out    host int32 [capacity, 8], entries (sequence, block, part, parts,
- *               slot of the first part or -1, first entry of the sequence,
- *               entries of the sequence, 0)
- *   num_work_out, num_parts_out   host: entries and part slots
- * An entry list longer than `capacity` is MLA_ERR_INVALID_ARG;
- * sum_n ceil(q_lens[n] / 256) * MLA_PREFILL_MAX_PARTS always suffices.
+ *   ctas        1 or 2 CTAs a block, 0: whichever the plan's costs favour
+ *   num_sms     0: the current device's (152 where there is none)
+ *   work_out    host int32 [capacity], entries of 8 per CTA of a block (sequence,
+ *               block, part, parts, slot of the first part or -1, first entry of
+ *               the sequence, entries of the sequence, rows of a block)
+ *   num_work_out, ctas_out, num_parts_out   host: entries, CTAs of an entry's block
+ *               and workspace slots of 256 rows
+ * A list longer than `capacity` is MLA_ERR_INVALID_ARG;
+ * sum_n ceil(q_lens[n] / 256) * 16 * MLA_PREFILL_MAX_PARTS always suffices.
  */
 #define MLA_PREFILL_MAX_PARTS 32
 int mla_plan_prefill(const int32_t* q_lens, const int32_t* kv_lens,
-                     const int32_t* prefix, int N, int H, int causal, int num_sms,
-                     int32_t* work_out, int64_t capacity, int64_t* num_work_out,
-                     int* num_parts_out);
+                     const int32_t* prefix, int N, int H, int causal, int ctas,
+                     int num_sms, int32_t* work_out, int64_t capacity,
+                     int64_t* num_work_out, int* ctas_out, int* num_parts_out);
 
 /*
  * Beam search's selection.  For every request b, over its W beams and the

@@ -99,9 +99,10 @@ def library() -> ctypes.CDLL:
             "mla_kv_read": (i32, [p, i32, p, i64, p, i64, p, i64, p, p]),
             "mla_add_rms_norm": (i32, [p, i64, p, i64, p, i64, p, f32, i64, i32, p, i64,
                                        p, i64, p, i64, i32, p]),
-            "mla_plan_prefill": (i32, [p, p, p, i32, i32, i32, i32, p, i64, p, p]),
+            "mla_plan_prefill": (i32, [p, p, p, i32, i32, i32, i32, i32, p, i64, p, p, p]),
             "mla_prefill": (i32, [p, i64, i64, p, i64, i64, i64, p, i64, i64, p, i64, p, i64, i64,
-                                  i64, i32, p, p, p, i32, i32, f32, p, i32, i32, p, p, p, p, p, p]),
+                                  i64, i32, p, p, p, i32, i32, f32, p, i32, i32, i32, p, p, p, p, p,
+                                  p]),
             "mla_beam_select": (i32, [p, i32, i64, i64, p, p, i32, i32, i32, i32, i32, p, p, p, p,
                                       p]),
             "mla_pages_fork": (i32, [p, i64, p, p, p, p, i32, p, i64, p, p, i64, p, p, p, p]),
@@ -711,20 +712,24 @@ def lse_combine(O_part, LSE_part, out=None, lse_out=None, stream=None):
 
 # ------------------------------------------------------- prompts and beams
 def plan_prefill(q_lens: Sequence[int], kv_lens: Sequence[int], H: int, prefix=None,
-                 causal: bool = True, num_sms: int = 0):
+                 causal: bool = True, num_sms: int = 0, ctas: int = 0):
     """Plan of `prefill` for sequences of these query and key lengths (host
-    numbers): (work np.int32 [n, 8], num_parts); see mla_plan_prefill."""
+    numbers): (work np.int32 [n, 8], or [n, 2, 8] for blocks on pairs of CTAs,
+    num_parts).  ctas = 1 or 2 asks for one form, 0 for the faster; see
+    mla_plan_prefill."""
     import numpy as np
     lq, lk = _host_i32(q_lens), _host_i32(kv_lens)
     pre = None if prefix is None else _host_i32(prefix)
     if len(lk) != len(lq) or (pre is not None and len(pre) != len(lq)):
         raise ValueError("q_lens, kv_lens and prefix differ in length")
-    cap = sum(-(-max(n, 0) // 256) for n in lq) * PREFILL_MAX_PARTS
-    out = np.empty((cap, 8), dtype=np.int32)
-    n, parts = ctypes.c_int64(), ctypes.c_int()
-    _check(library().mla_plan_prefill(lq, lk, pre, len(lq), H, 1 if causal else 0, num_sms,
-                                      out.ctypes.data, cap, ctypes.byref(n), ctypes.byref(parts)))
-    return out[:n.value].copy(), parts.value
+    cap = sum(-(-max(n, 0) // 256) for n in lq) * 16 * PREFILL_MAX_PARTS
+    out = np.empty(cap, dtype=np.int32)
+    n, c, parts = ctypes.c_int64(), ctypes.c_int(), ctypes.c_int()
+    _check(library().mla_plan_prefill(lq, lk, pre, len(lq), H, 1 if causal else 0, ctas, num_sms,
+                                      out.ctypes.data, cap, ctypes.byref(n), ctypes.byref(c),
+                                      ctypes.byref(parts)))
+    work = out[:n.value * c.value * 8].copy()
+    return work.reshape((-1, 8) if c.value == 1 else (-1, 2, 8)), parts.value
 
 
 def _heads_arg(t: torch.Tensor, name: str, T: int, H: int, width: int):
@@ -758,9 +763,9 @@ def prefill(q_nope, q_rope, k_nope, k_rope, v, cu_q, cu_kv, work, sm_scale: floa
     N = cu_q.numel() - 1
     if N < 0:
         raise ValueError("cu_q: expected N + 1 values")
-    if work.dtype is not _I32 or work.dim() != 2 or work.shape[1] != 8 or not work.is_contiguous():
-        raise ValueError(f"work: expected contiguous int32 [n, 8] on the device, got {work.dtype} "
-                         f"{tuple(work.shape)}")
+    if work.dtype is not _I32 or tuple(work.shape[1:]) not in ((8,), (2, 8)) or not work.is_contiguous():
+        raise ValueError(f"work: expected contiguous int32 [n, 8] or [n, 2, 8] on the device, got "
+                         f"{work.dtype} {tuple(work.shape)}")
     qn = _heads_arg(q_nope, "q_nope", Tq, H, 128)
     qr = _heads_arg(q_rope, "q_rope", Tq, H, ROPE_DIM)
     kn = _heads_arg(k_nope, "k_nope", Tk, H, 128)
@@ -790,7 +795,7 @@ def prefill(q_nope, q_rope, k_nope, k_rope, v, cu_q, cu_kv, work, sm_scale: floa
     if status is not None:
         _check_buffer(status, "status", _I32, 1)
     _launch(q_nope, stream, library().mla_prefill, *qn, *qr, Tq, *kn, *kr, *vv, Tk, H, *cu_args, N,
-            1 if causal else 0, sm_scale, work.data_ptr(), work.shape[0], num_parts, *ws,
+            1 if causal else 0, sm_scale, work.data_ptr(), work.shape[0], work.dim() - 1, num_parts, *ws,
             out.data_ptr(), lse_out.data_ptr(), _ptr(status))
     return out, lse_out
 

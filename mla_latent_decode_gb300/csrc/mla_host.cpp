@@ -186,14 +186,96 @@ using namespace mla;
 
 namespace mla {
 
+// Plan of mla_prefill with blocks of 256 * ctas rows.  Costs in key tiles of a
+// CTA on its own (about 2.1 us): a tile of a pair, what a block takes besides its
+// tiles, and the merging launch with its rows.
+struct PrefillPlan {
+  int ctas = 1;
+  double end = 0;
+  std::vector<int> order;                      // sequences, longest first
+  std::vector<std::vector<int64_t>> tiles;     // key tiles of a sequence's blocks
+  int64_t limit = 1;                           // tiles of a part
+
+  int parts_of(int64_t t) const {
+    const int64_t q = (t + limit - 1) / limit;
+    return (int)std::max<int64_t>(1, std::min<int64_t>(q, MLA_PREFILL_MAX_PARTS));
+  }
+};
+
+static PrefillPlan plan_prefill_blocks(const int32_t* q_lens, const int32_t* kv_lens,
+                                       const int32_t* prefix, int N, int H, int causal,
+                                       int ctas, int num_sms) {
+  constexpr int kKeys = 128;
+  constexpr double kFixed = 2, kPairTile = 0.62, kMerge = 3, kMergeSlot = 0.002;
+  const int block = 256 * ctas;
+  PrefillPlan plan;
+  plan.ctas = ctas;
+  plan.tiles.resize(N);
+  int64_t blocks = 0, longest = 0, all = 0;
+  for (int n = 0; n < N; ++n) {
+    const int64_t lq = q_lens[n], lk = kv_lens[n], pre = prefix ? prefix[n] : 0;
+    for (int64_t r = 0; r < lq; r += block) {
+      const int64_t last = std::min(r + block, lq) - 1;
+      const int64_t sees =
+          causal ? std::min(lk, std::max({pre, lk - lq + 1 + last, (int64_t)0})) : lk;
+      plan.tiles[n].push_back((sees + kKeys - 1) / kKeys);
+      longest = std::max(longest, plan.tiles[n].back());
+      all += plan.tiles[n].back();
+    }
+    blocks += (int64_t)plan.tiles[n].size();
+  }
+  plan.order.resize(N);
+  for (int n = 0; n < N; ++n) plan.order[n] = n;
+  const auto last_of = [&](int n) { return plan.tiles[n].empty() ? -1 : plan.tiles[n].back(); };
+  std::stable_sort(plan.order.begin(), plan.order.end(),
+                   [&](int a, int b) { return last_of(a) > last_of(b); });
+  plan.limit = std::max<int64_t>(longest, 1);
+  const int slots = std::max(num_sms / ctas, 1);
+  const double tile = ctas == 1 ? 1 : kPairTile;
+  // Many blocks: they even out.
+  plan.end = ((double)all * tile + (double)blocks * kFixed) * H / slots + longest * tile / 2;
+  if (blocks == 0 || blocks * H >= 8 * (int64_t)slots) return plan;
+  // Few: a limit on a part's key tiles, the one whose list schedule in launch
+  // order ends first.
+  double best = -1;
+  int64_t best_limit = plan.limit;
+  for (int cut = 1; cut <= MLA_PREFILL_MAX_PARTS; ++cut) {
+    plan.limit = std::max<int64_t>((longest + cut - 1) / cut, 1);
+    if (cut > 1 && plan.limit < 4) break;
+    std::priority_queue<double, std::vector<double>, std::greater<double>> ends;
+    for (int i = 0; i < slots; ++i) ends.push(0);
+    double end = 0;
+    int64_t merged = 0;
+    for (int n : plan.order)
+      for (int h = 0; h < H; ++h)
+        for (auto t = plan.tiles[n].rbegin(); t != plan.tiles[n].rend(); ++t) {
+          const int parts = plan.parts_of(*t);
+          merged += parts > 1 ? parts * ctas : 0;
+          for (int s = 0; s < parts; ++s) {
+            const double at =
+                ends.top() + kFixed + tile * (double)(*t * (s + 1) / parts - *t * s / parts);
+            ends.pop();
+            ends.push(at);
+            end = std::max(end, at);
+          }
+        }
+    end += merged ? kMerge + kMergeSlot * (double)merged : 0;
+    if (best < 0 || end < best) best = end, best_limit = plan.limit;
+  }
+  plan.limit = best_limit;
+  plan.end = best;
+  return plan;
+}
+
 static int plan_prefill(const int32_t* q_lens, const int32_t* kv_lens,
-                        const int32_t* prefix, int N, int H, int causal, int num_sms,
-                        int32_t* work_out, int64_t capacity, int64_t* num_work_out,
-                        int* num_parts_out) {
-  if (N < 0 || H < 1 || num_sms < 0 || capacity < 0 || !num_work_out || !num_parts_out ||
+                        const int32_t* prefix, int N, int H, int causal, int ctas,
+                        int num_sms, int32_t* work_out, int64_t capacity,
+                        int64_t* num_work_out, int* ctas_out, int* num_parts_out) {
+  if (N < 0 || H < 1 || num_sms < 0 || ctas < 0 || ctas > 2 || capacity < 0 ||
+      !num_work_out || !ctas_out || !num_parts_out ||
       (N > 0 && (!q_lens || !kv_lens || (!work_out && capacity > 0))))
-    return fail(MLA_ERR_INVALID_ARG, "mla_plan_prefill: N=%d, num_sms=%d or capacity < 0, H=%d < 1 "
-                "or a NULL array", N, num_sms, H);
+    return fail(MLA_ERR_INVALID_ARG, "mla_plan_prefill: N=%d, num_sms=%d or capacity < 0, H=%d < 1, "
+                "ctas=%d above 2 or a NULL array", N, num_sms, H, ctas);
   for (int n = 0; n < N; ++n)
     if (q_lens[n] < 0 || kv_lens[n] < 0)
       return fail(MLA_ERR_INVALID_ARG, "mla_plan_prefill: a negative length (sequence %d)", n);
@@ -201,81 +283,37 @@ static int plan_prefill(const int32_t* q_lens, const int32_t* kv_lens,
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess ||
         cudaDeviceGetAttribute(&num_sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-      num_sms = 148;
+      num_sms = 152;
     cudaGetLastError();
   }
-  constexpr int kBlock = 256, kKeys = 128;  // rows of a CTA, tokens of a key tile
-  // Key tiles of every block, per sequence.
-  std::vector<std::vector<int64_t>> tiles(N);
-  int64_t blocks = 0, longest = 0;
-  for (int n = 0; n < N; ++n) {
-    const int64_t lq = q_lens[n], lk = kv_lens[n], pre = prefix ? prefix[n] : 0;
-    for (int64_t r = 0; r < lq; r += kBlock) {
-      const int64_t last = std::min(r + kBlock, lq) - 1;
-      const int64_t sees =
-          causal ? std::min(lk, std::max({pre, lk - lq + 1 + last, (int64_t)0})) : lk;
-      tiles[n].push_back((sees + kKeys - 1) / kKeys);
-      longest = std::max(longest, tiles[n].back());
-    }
-    blocks += (int64_t)tiles[n].size();
-  }
-  std::vector<int> order(N);
-  for (int n = 0; n < N; ++n) order[n] = n;
-  std::stable_sort(order.begin(), order.end(), [&](int a, int b) {
-    return (tiles[a].empty() ? -1 : tiles[a].back()) > (tiles[b].empty() ? -1 : tiles[b].back());
-  });
-  // Parts: a limit on a part's key tiles, the one whose list schedule in launch
-  // order ends first.  Costs in key tiles of a CTA (about 1.5 us): what a CTA
-  // takes besides its tiles, and the merging launch.
-  constexpr double kFixed = 3, kMerge = 4;
-  const auto parts_of = [&](int64_t t, int64_t limit) {
-    const int64_t q = (t + limit - 1) / limit;
-    return (int)std::max<int64_t>(1, std::min<int64_t>(q, MLA_PREFILL_MAX_PARTS));
-  };
-  int64_t best_limit = std::max<int64_t>(longest, 1);
-  if (blocks > 0 && blocks * H < 4 * (int64_t)num_sms) {
-    double best = -1;
-    for (int cut = 1; cut <= MLA_PREFILL_MAX_PARTS; ++cut) {
-      const int64_t limit = std::max<int64_t>((longest + cut - 1) / cut, 1);
-      if (cut > 1 && limit < 4) break;
-      std::priority_queue<double, std::vector<double>, std::greater<double>> ends;
-      for (int i = 0; i < num_sms; ++i) ends.push(0);
-      double end = 0;
-      bool merged = false;
-      for (int n : order)
-        for (int h = 0; h < H; ++h)
-          for (auto t = tiles[n].rbegin(); t != tiles[n].rend(); ++t) {
-            const int parts = parts_of(*t, limit);
-            merged |= parts > 1;
-            for (int s = 0; s < parts; ++s) {
-              const double at = ends.top() + kFixed + (double)(*t * (s + 1) / parts - *t * s / parts);
-              ends.pop();
-              ends.push(at);
-              end = std::max(end, at);
-            }
-          }
-      end += merged ? kMerge : 0;
-      if (best < 0 || end < best) best = end, best_limit = limit;
-    }
+  PrefillPlan plan = plan_prefill_blocks(q_lens, kv_lens, prefix, N, H, causal, ctas ? ctas : 1, num_sms);
+  if (ctas == 0) {
+    PrefillPlan pairs = plan_prefill_blocks(q_lens, kv_lens, prefix, N, H, causal, 2, num_sms);
+    if (pairs.end < plan.end) plan = std::move(pairs);
   }
   int64_t at = 0, slots = 0;
-  for (int n : order) {
+  const int width = 8 * plan.ctas;
+  for (int n : plan.order) {
     const int64_t first = at;
-    for (int b = (int)tiles[n].size() - 1; b >= 0; --b) {
-      const int parts = parts_of(tiles[n][b], best_limit);
-      if (at + parts > capacity)
-        return fail(MLA_ERR_INVALID_ARG, "mla_plan_prefill: more than %lld entries", (long long)capacity);
-      for (int s = 0; s < parts; ++s, ++at) {
-        const int32_t e[8] = {n, b, s, parts, parts > 1 ? (int32_t)slots : -1, (int32_t)first, 0, 0};
-        std::copy(e, e + 8, work_out + at * 8);
-      }
-      if (parts > 1) slots += parts;
+    for (int b = (int)plan.tiles[n].size() - 1; b >= 0; --b) {
+      const int parts = plan.parts_of(plan.tiles[n][b]);
+      if ((at + parts) * width > capacity)
+        return fail(MLA_ERR_INVALID_ARG, "mla_plan_prefill: more than %lld numbers", (long long)capacity);
+      for (int s = 0; s < parts; ++s, ++at)
+        for (int c = 0; c < plan.ctas; ++c) {
+          const int32_t e[8] = {n, b, s, parts, parts > 1 ? (int32_t)slots : -1, (int32_t)first, 0,
+                                256 * plan.ctas};
+          std::copy(e, e + 8, work_out + at * width + 8 * c);
+        }
+      if (parts > 1) slots += (int64_t)parts * plan.ctas;
     }
-    for (int64_t i = first; i < at; ++i) work_out[i * 8 + 6] = (int32_t)(at - first);
+    for (int64_t i = first; i < at; ++i)
+      for (int c = 0; c < plan.ctas; ++c) work_out[i * width + 8 * c + 6] = (int32_t)(at - first);
   }
   if (at > 0x7fffffff || slots > 0x7fffffff)
     return fail(MLA_ERR_INVALID_ARG, "mla_plan_prefill: too many blocks");
   *num_work_out = at;
+  *ctas_out = plan.ctas;
   *num_parts_out = (int)slots;
   return MLA_OK;
 }
@@ -706,12 +744,12 @@ int mla_plan_sched(int B, int q_len, int H, int num_shards,
 }
 
 int mla_plan_prefill(const int32_t* q_lens, const int32_t* kv_lens,
-                     const int32_t* prefix, int N, int H, int causal, int num_sms,
-                     int32_t* work_out, int64_t capacity, int64_t* num_work_out,
-                     int* num_parts_out) {
+                     const int32_t* prefix, int N, int H, int causal, int ctas,
+                     int num_sms, int32_t* work_out, int64_t capacity,
+                     int64_t* num_work_out, int* ctas_out, int* num_parts_out) {
   try {
-    return plan_prefill(q_lens, kv_lens, prefix, N, H, causal, num_sms, work_out, capacity,
-                        num_work_out, num_parts_out);
+    return plan_prefill(q_lens, kv_lens, prefix, N, H, causal, ctas, num_sms, work_out, capacity,
+                        num_work_out, ctas_out, num_parts_out);
   } catch (const std::exception& e) {  // out of memory
     return fail(MLA_ERR_INVALID_ARG, "mla_plan_prefill: %s", e.what());
   }

@@ -3,21 +3,35 @@
 // RoPE key for all heads, and o = softmax(s) v over the keys that a row sees,
 // which are always the first ones of its sequence.
 //
-// A CTA owns 256 query rows of one sequence and head as two tiles of 128 rows.
-// Keys come in tiles of 128 tokens: S = Q K^T is 12 tcgen05 MMAs of M = 128,
-// N = 128, K = 16 (192 dims), O += P V eight more.  TMEM holds S and O of both
-// row tiles (4 x 128 columns); P overwrites its S in bf16 and is the MMA's A
-// operand from there.  While the softmax of one row tile runs, the tensor cores
-// work for the other: PV_0(j - 1), QK_0(j), PV_1(j - 1), QK_1(j), ...  MMAs of
-// one thread execute in order, so "S_g(j) is there" also says that PV_g(j - 1)
-// is done: the softmax may rescale O in place then, and S may overwrite P.
+// Two forms of one kernel.  A work unit is a block of 256 query rows of one
+// sequence and head on one CTA (kCtas = 1), or of 512 rows on a pair of CTAs
+// whose MMAs span both SMs (cta_group::2).  Either way a CTA holds two row tiles
+// of 128 rows; keys come in tiles of 128 tokens: S = Q K^T is 12 MMAs of N = 128,
+// K = 16 (192 dims), O += P V eight more, M = 128 rows a CTA.  TMEM holds S and O
+// of both row tiles (4 x 128 columns); P overwrites its S in bf16 and is the MMA's
+// A operand from there.  While the softmax of one row tile runs, the tensor cores
+// work for the other: PV_0(t - 1), QK_0(t), PV_1(t - 1), QK_1(t), ...  MMAs of one
+// thread execute in order, so "S_g(t) is there" also says that PV_g(t - 1) is
+// done: the softmax may rescale O in place then, and S may overwrite P.
+//
+// What bounds it: on one SM the MMAs of a key tile pair take 2560 cycles and
+// their operands 256 KB of shared memory reads, which with the 80 KB that TMA
+// writes is 2690 cycles of its bandwidth and more than an SM's ring can load
+// ahead.  In the pair each SM loads and reads half of every K and V tile (40 KB,
+// and 1730 cycles of shared memory in all), which leaves the tensor cores as the
+// bound; short blocks fill only half of a pair.
 //
 //   warps 0-3, 4-7   softmax of row tile 0 and 1, one thread per row, then O / l
-//   warp 8           TMA: Q (96 KB, stays), K and V through a ring of 8 stages
-//                    of 16 KB, K in three (64 dims x 128 tokens each, the third
-//                    the RoPE key), V in two (64 tokens x 128 dims)
-//   warp 9           MMA issue (one lane)
-//   warps 10, 11     clean V: in tiles that hold tokens which some row of the CTA
+//   warp 8           TMA: Q (96 KB), K and V through a ring of 128 KB, K in three
+//                    stages (64 dims of 128 tokens each, the third the RoPE key),
+//                    V in two (64 tokens each); in a pair a CTA's stage is half as
+//                    large, its half of the tokens (K) or of the dims (V)
+//   warp 9           MMA issue (one lane; of a pair's first CTA)
+//   warp 10          the next unit: the grid has a CTA (pair) per unit, and running
+//                    ones take over those that have not started, in launch order, so
+//                    the work list is dealt out as SMs come free and a unit's loads
+//                    and first MMAs overlap the end of the one before
+//   warps 12, 13     clean V: in tiles that hold tokens which some row of the unit
 //                    does not see, values that are not finite become 0 (P is 0
 //                    there, and 0 x NaN would reach the row) and are noted per
 //                    dim; the rows that do see them get them back at the end
@@ -37,18 +51,20 @@ namespace {
 
 using namespace ptx;
 
-constexpr int kRows = 128;           // rows of a tile (MMA M)
-constexpr int kBlock = 2 * kRows;    // rows of a CTA
+constexpr int kRows = 128;           // rows of a CTA's tile (MMA M per CTA)
+constexpr int kSlot = 256;           // rows of a workspace slot
 constexpr int kKeys = 128;           // tokens of a key tile
-constexpr int kBox = 128 * 128;      // 16 KB
-constexpr int kStages = 8;
-constexpr int kThreads = 384;
-constexpr int kWarpTma = 8, kWarpMma = 9, kWarpClean = 10;
-// 384 threads launch with 168 registers (64512 in all): 256 x 216 + 128 x 72.
-constexpr int kRegsSoftmax = 216, kRegsOther = 72;
+constexpr int kBox = 128 * 128;      // 16 KB: 64 dims of 128 rows
+constexpr int kRing = 8 * kBox;
+constexpr int kRaw = 4;              // V tiles that may wait for cleaning (the ring holds parts of 3)
+constexpr int kThreads = 512;
+constexpr int kWarpTma = 8, kWarpMma = 9, kWarpNext = 10, kWarpClean = 12;
+// 512 threads launch with 128 registers (65536 in all): 256 x 200 + 256 x 56.
+constexpr int kRegsSoftmax = 200, kRegsOther = 56;
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kRise = 8.f;         // log2 of the rise that rescales O
 constexpr int kEntry = 8;            // int32 of a work entry
+constexpr int kOffsetBits = 9;       // of a note on a cleaned value: its token past the first unseen one
 
 struct PrefillParams {
   const int32_t* cu_q;
@@ -66,31 +82,45 @@ struct PrefillParams {
   int* status;
 };
 
-struct Ctl {
-  uint64_t q[2], full[kStages], empty[kStages];
-  uint64_t s[2];      // S of a row tile is in TMEM
-  uint64_t p[2];      // its P is, and S has been read
-  uint64_t o[2];      // O is complete
-  uint64_t raw[2];    // V of a tile to be cleaned has landed (tiles take turns: two may be waiting)
-  uint64_t cleaned;   // all of them are
-  uint64_t drain;
-  int odd[3][kKeys];  // per dim: the first cleaned NaN, +inf, -inf
-  uint32_t tmem;
-  int abort_flag, any_odd;
+// A work unit: `rows` rows from row0 of a sequence (first row q0, first key k0,
+// lq rows and lk keys), head h, key tiles j0 <= j < j1 of which the two row
+// tiles see those below n0 and n1.
+struct Unit {
+  int more;                 // 0: no further unit
+  int h, row0, rows, q0, k0, lq, lk, prefix;
+  int slot;                 // workspace slot of this part, -1: the whole block
+  int j0, j1, n0, n1;
+  int clean0;               // first tile whose V is cleaned
+  int unseen;               // first key that some row does not see
 };
-constexpr int kSmem = 6 * kBox + kStages * kBox + (int)sizeof(Ctl) + 1024;
+
+struct Ctl {
+  uint64_t q[2], qfree[2];       // Q of a row tile has landed; has been used up
+  uint64_t full[16], empty[16];  // ring
+  uint64_t s[2];                 // S of a row tile is in TMEM
+  uint64_t p[2];                 // its P is, and S has been read
+  uint64_t o[2];                 // O is complete
+  uint64_t raw[kRaw];            // V of a tile to be cleaned has landed (tiles take turns)
+  uint64_t cleaned;              // all of a unit's are clean
+  uint64_t done;                 // the softmax warps are through with a unit
+  uint64_t unit_full[2], unit_empty[2];
+  uint64_t answer_full, answer_free;
+  uint64_t drain;
+  alignas(16) uint32_t answer[4];
+  Unit unit[2];
+  uint32_t note;                 // where a peer's asynchronous stores go
+  // per kind (NaN, +inf, -inf) and dim: the first cleaned token, behind a tag that
+  // falls from unit to unit, so that a unit's notes replace older ones
+  uint32_t odd[3][kKeys];
+  uint32_t any_odd;              // the least tag of a unit with notes
+  uint32_t tmem;
+  int abort_flag;
+};
+constexpr int kSmem = 6 * kBox + kRing + (int)sizeof(Ctl);
 static_assert(kSmem <= 227 * 1024, "shared memory budget");
 
-// What a CTA computes.
-struct Unit {
-  int seq, h, row0, rows;   // rows: of the block that exist
-  int64_t q0, k0;           // first row and key of the sequence
-  int lq, lk, prefix;
-  int part, parts, slot;
-  int n0, n1;               // key tiles of the two row tiles: j0 <= j < n
-  int j0, j1;
-  int clean0;               // first tile whose V is cleaned
-};
+// The unit tag of notes: falls with the unit's number in this CTA.
+__device__ __forceinline__ uint32_t tag_of(uint32_t nth) { return (0x7fffffu - nth) << kOffsetBits; }
 
 // Keys that row i of a sequence sees.
 __device__ __forceinline__ int sees(const PrefillParams& p, int lq, int lk, int prefix, int i) {
@@ -98,60 +128,53 @@ __device__ __forceinline__ int sees(const PrefillParams& p, int lq, int lk, int 
   return min(lk, max(prefix, max(lk - lq + 1 + i, 0)));
 }
 
-// The CTA's unit, false if the entry or the lengths are none.
-__device__ __forceinline__ bool find_unit(const PrefillParams& p, Unit& u) {
-  const int x = blockIdx.x;
-  const int32_t* e = p.work + (int64_t)(x / p.H) * kEntry;
+// Unit x of the grid; false if its entry or lengths are none.
+template <int kCtas>
+__device__ __forceinline__ bool find_unit(const PrefillParams& p, int x, Unit& u) {
+  constexpr int kBlock = 2 * kRows * kCtas, kStride = kEntry * kCtas;
+  const int32_t* e = p.work + (int64_t)(x / p.H) * kStride;
   const int g0 = e[5], nb = e[6];
-  int bad = 0;
   if (g0 < 0 || nb < 1 || g0 > x / p.H || g0 + nb <= x / p.H || g0 + nb > p.num_work) {
-    bad = MLA_STATUS_BAD_WORK;
-  } else {
-    const int64_t local = x - (int64_t)g0 * p.H;
-    u.h = (int)(local / nb);
-    e = p.work + (g0 + local % nb) * kEntry;
-    u.seq = e[0];
-    u.part = e[2];
-    u.parts = e[3];
-    u.slot = e[4];
-    const int64_t row0 = (int64_t)e[1] * kBlock;
-    if (u.h >= p.H || u.seq < 0 || u.seq >= p.N || e[1] < 0 || u.parts < 1 ||
-        u.parts > MLA_PREFILL_MAX_PARTS || u.part < 0 || u.part >= u.parts ||
-        (u.parts > 1 && (u.slot < 0 || u.slot > p.num_parts - u.parts))) {
-      bad = MLA_STATUS_BAD_WORK;
-    } else {
-      u.q0 = p.cu_q[u.seq];
-      u.k0 = p.cu_kv[u.seq];
-      const int64_t lq = p.cu_q[u.seq + 1] - u.q0, lk = p.cu_kv[u.seq + 1] - u.k0;
-      if (u.q0 < 0 || u.k0 < 0 || lq < 0 || lk < 0 || u.q0 + lq > p.Tq || u.k0 + lk > p.Tk) {
-        bad = MLA_STATUS_BAD_LENGTH;
-      } else if (row0 >= lq) {
-        bad = MLA_STATUS_BAD_WORK;
-      } else {
-        u.lq = (int)lq;
-        u.lk = (int)lk;
-        u.row0 = (int)row0;
-        u.rows = min(kBlock, u.lq - u.row0);
-        u.prefix = p.prefix ? p.prefix[u.seq] : 0;
-        int n[2];
-#pragma unroll
-        for (int g = 0; g < 2; ++g) {
-          const int last = min(kRows * (g + 1), u.rows) - 1;
-          n[g] = last < kRows * g ? 0
-                 : (sees(p, u.lq, u.lk, u.prefix, u.row0 + last) + kKeys - 1) / kKeys;
-        }
-        const int64_t all = max(n[0], n[1]);
-        u.j0 = (int)(all * u.part / u.parts);
-        u.j1 = (int)(all * (u.part + 1) / u.parts);
-        u.n0 = min(n[0], u.j1);
-        u.n1 = min(n[1], u.j1);
-        u.clean0 = max(u.j0, sees(p, u.lq, u.lk, u.prefix, u.row0) / kKeys);
-        return true;
-      }
-    }
+    if (p.status) atomicOr(p.status, MLA_STATUS_BAD_WORK);
+    return false;
   }
-  if (threadIdx.x == 0 && p.status) atomicOr(p.status, bad);
-  return false;
+  const int64_t local = x - (int64_t)g0 * p.H;
+  u.h = (int)(local / nb);
+  e = p.work + (g0 + local % nb) * kStride;
+  const int seq = e[0], part = e[2], parts = e[3], slot = e[4];
+  const int64_t row0 = (int64_t)e[1] * kBlock;
+  if (u.h >= p.H || seq < 0 || seq >= p.N || e[1] < 0 || parts < 1 || parts > MLA_PREFILL_MAX_PARTS ||
+      part < 0 || part >= parts || e[7] != kBlock ||
+      (parts > 1 && (slot < 0 || slot > p.num_parts - parts * kCtas))) {
+    if (p.status) atomicOr(p.status, MLA_STATUS_BAD_WORK);
+    return false;
+  }
+  const int64_t q0 = p.cu_q[seq], k0 = p.cu_kv[seq];
+  const int64_t lq = p.cu_q[seq + 1] - q0, lk = p.cu_kv[seq + 1] - k0;
+  const int prefix = p.prefix ? p.prefix[seq] : 0;
+  if (q0 < 0 || k0 < 0 || lq < 0 || lk < 0 || q0 + lq > p.Tq || k0 + lk > p.Tk || row0 >= lq) {
+    const bool length = q0 < 0 || k0 < 0 || lq < 0 || lk < 0 || q0 + lq > p.Tq || k0 + lk > p.Tk;
+    if (p.status) atomicOr(p.status, length ? MLA_STATUS_BAD_LENGTH : MLA_STATUS_BAD_WORK);
+    return false;
+  }
+  u.more = 1;
+  u.row0 = (int)row0;
+  u.rows = (int)min((int64_t)kBlock, lq - row0);
+  u.q0 = (int)q0, u.k0 = (int)k0, u.lq = (int)lq, u.lk = (int)lk, u.prefix = prefix;
+  u.slot = parts > 1 ? slot + part * kCtas : -1;
+  const auto tiles = [&](int first, int end) {
+    if (u.rows <= first) return 0;
+    return (sees(p, u.lq, u.lk, prefix, u.row0 + min(u.rows, end) - 1) + kKeys - 1) / kKeys;
+  };
+  const int n0 = tiles(0, kBlock / 2), n1 = tiles(kBlock / 2, kBlock);
+  const int64_t all = max(n0, n1);
+  u.j0 = (int)(all * part / parts);
+  u.j1 = (int)(all * (part + 1) / parts);
+  u.n0 = min(n0, u.j1);
+  u.n1 = min(n1, u.j1);
+  u.unseen = sees(p, u.lq, u.lk, prefix, u.row0);
+  u.clean0 = max(u.j0, u.unseen / kKeys);
+  return true;
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -187,388 +210,606 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return *reinterpret_cast<uint32_t*>(&h);
 }
 
-// Ring positions: K(t) at 5 t .. 5 t + 2, V(t) at 5 t + 3, 5 t + 4.
-__device__ __forceinline__ void produce(uint8_t* base, Ctl& c, const PrefillParams& p, const Unit& u,
-                                        const CUtensorMap* qn, const CUtensorMap* qr,
-                                        const CUtensorMap* kn, const CUtensorMap* kr,
-                                        const CUtensorMap* v, int lane) {
-  const int tiles = u.j1 - u.j0;
-  // Q: six boxes, each from its own lane (a thread's loads go one after another)
-  const int boxes = u.rows > kRows ? 6 : 3;
-  if (lane < 2 && lane * 3 < boxes) mbar_arrive_expect_tx(smem_u32(&c.q[lane]), 3 * kBox);
-  __syncwarp();
-  if (lane < boxes) {
-    const int g = lane / 3, d = lane % 3;
-    const int row = (int)(u.q0 + u.row0 + g * kRows);
-    const uint32_t dst = smem_u32(base + lane * kBox), bar = smem_u32(&c.q[g]);
-    if (d < 2) tma_load_3d(dst, qn, bar, d * 64, u.h, row);
-    else tma_load_3d(dst, qr, bar, 0, u.h, row);
+
+// ---- the two forms' instructions
+template <int kCtas>
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  if constexpr (kCtas == 1) return mbar_wait_cta(smem_u32(bar), parity, abort);
+  else return mbar_wait(smem_u32(bar), parity, abort);
+}
+// A barrier of the pair's first CTA, which issues the MMAs.
+template <int kCtas>
+__device__ __forceinline__ uint32_t lead_bar(uint64_t* bar) {
+  if constexpr (kCtas == 1) return smem_u32(bar);
+  else return mapa(smem_u32(bar), 0);
+}
+template <int kCtas>
+__device__ __forceinline__ void expect_at_lead(uint64_t* bar, uint32_t rank, uint32_t bytes) {
+  if (kCtas == 1 || rank == 0) mbar_arrive_expect_tx(smem_u32(bar), bytes);
+  else mbar_arrive_expect_tx_cluster(lead_bar<kCtas>(bar), bytes);
+}
+template <int kCtas>
+__device__ __forceinline__ void load_3d(uint32_t dst, const CUtensorMap* m, uint32_t bar, int x, int y, int z) {
+  if constexpr (kCtas == 1) tma_load_3d(dst, m, bar, x, y, z);
+  else tma_load_3d_pair(dst, m, bar, x, y, z);
+}
+template <int kCtas>
+__device__ __forceinline__ void load_4d(uint32_t dst, const CUtensorMap* m, uint32_t bar, int x, int y, int z,
+                                        int w) {
+  if constexpr (kCtas == 1) tma_load_4d(dst, m, bar, x, y, z, w);
+  else tma_load_4d_pair(dst, m, bar, x, y, z, w);
+}
+template <int kCtas>
+__device__ __forceinline__ void mma_qk(uint32_t d, uint64_t a, uint64_t b, uint32_t acc) {
+  constexpr uint32_t idesc = idesc_bf16_f32(kRows * kCtas, kKeys, false, false);
+  if constexpr (kCtas == 1) mma_ss(d, a, b, idesc, acc);
+  else mma_ss_pair(d, a, b, idesc, acc);
+}
+template <int kCtas>
+__device__ __forceinline__ void mma_pv(uint32_t d, uint32_t a, uint64_t b, uint32_t acc) {
+  constexpr uint32_t idesc = idesc_bf16_f32(kRows * kCtas, kKeys, false, true);
+  if constexpr (kCtas == 1) mma_ts(d, a, b, idesc, acc);
+  else mma_ts_pair(d, a, b, idesc, acc);
+}
+// On the barrier of every CTA of the unit.
+template <int kCtas>
+__device__ __forceinline__ void commit(uint64_t* bar) {
+  if constexpr (kCtas == 1) mma_commit(smem_u32(bar));
+  else mma_commit_pair(smem_u32(bar), 3);
+}
+
+template <int kCtas>
+__device__ __forceinline__ void give_up(Ctl& c, const PrefillParams& p, uint32_t rank) {
+  *reinterpret_cast<volatile int*>(&c.abort_flag) = 1;
+  if constexpr (kCtas == 2) st_cluster_u32(mapa(smem_u32(&c.abort_flag), rank ^ 1), 1);
+  if (p.status) atomicOr(p.status, MLA_STATUS_WAIT_TIMEOUT);
+}
+
+// The units of a role, one after another: next() waits for one, release() hands
+// its slot back (one lane).
+template <int kCtas>
+struct Units {
+  Ctl& c;
+  uint32_t nth = 0;
+  __device__ __forceinline__ explicit Units(Ctl& ctl) : c(ctl) {}
+  __device__ __forceinline__ const Unit* next(bool& ok) {
+    ok = wait_bar<kCtas>(&c.unit_full[nth & 1], nth >> 1 & 1, &c.abort_flag);
+    const Unit* u = &c.unit[nth & 1];
+    return ok && u->more ? u : nullptr;
   }
+  __device__ __forceinline__ void release() {
+    mbar_arrive(smem_u32(&c.unit_empty[nth & 1]));
+    ++nth;
+  }
+  __device__ __forceinline__ void skip() { ++nth; }  // for the other lanes
+};
+
+// Finds the units and hands them to the CTA's roles: its own first, then those
+// it takes over, asked for one unit ahead.
+template <int kCtas>
+__device__ __forceinline__ void feed(Ctl& c, const PrefillParams& p, uint32_t rank) {
+  int x = blockIdx.x / kCtas;
+  uint32_t nth = 0, asked = 0;
   bool ok = true;
-  uint32_t pos = 0;
-  for (int t = 0; t < tiles && ok; ++t) {
-    const int tok = (int)u.k0 + (u.j0 + t) * kKeys;
-    for (int i = 0; i < 5; ++i, ++pos) {
-      const uint32_t st = pos % kStages, use = pos / kStages;
-      if (use > 0 && !mbar_wait_cta(smem_u32(&c.empty[st]), (use - 1) & 1, &c.abort_flag)) {
-        ok = false;
-        break;
-      }
-      if (lane == (int)(pos & 3)) {
-        const uint32_t dst = smem_u32(base + (6 + st) * kBox), bar = smem_u32(&c.full[st]);
-        const int nth = u.j0 + t - u.clean0;
-        if (i >= 3 && nth >= 0) {
-          // its stage is full once it is clean
-          const uint32_t raw = smem_u32(&c.raw[nth & 1]);
-          if (i == 3) mbar_arrive_expect_tx(raw, 2 * kBox);
-          tma_load_4d(dst, v, raw, 0, tok + (i - 3) * 64, 0, u.h);
-          continue;
+  while (ok) {
+    Unit u;
+    u.more = 0;
+    const bool found = x >= 0 && find_unit<kCtas>(p, x, u);
+    if (found || x < 0) {
+      const uint32_t b = nth & 1;
+      // (its slot was free before this unit was asked for)
+      c.unit[b] = u;
+      mbar_arrive(smem_u32(&c.unit_full[b]));
+      if (x < 0) return;
+      ++nth;
+      // one ahead: the unit before this one has ended
+      if (nth >= 2 && !(ok = wait_bar<kCtas>(&c.unit_empty[nth & 1], (nth >> 1) - 1 & 1, &c.abort_flag))) break;
+    }
+    mbar_arrive_expect_tx(smem_u32(&c.answer_full), 16);
+    if (rank == 0) {
+      // every CTA has armed its barrier and read the answer before
+      if (kCtas == 2 && !(ok = wait_bar<kCtas>(&c.answer_free, asked & 1, &c.abort_flag))) break;
+      try_cancel<kCtas == 2>(smem_u32(c.answer), smem_u32(&c.answer_full));
+    } else {
+      mbar_arrive_cluster(mapa(smem_u32(&c.answer_free), 0));
+    }
+    if (!(ok = wait_bar<kCtas>(&c.answer_full, asked & 1, &c.abort_flag))) break;
+    ++asked;
+    x = canceled_cta(smem_u32(c.answer));
+    // the answer has been read before the next one is written
+    fence_proxy_async_smem();
+    if (x >= 0) x /= kCtas;
+  }
+  give_up<kCtas>(c, p, rank);
+}
+
+// Ring positions of a unit's tile t: K at 5 t .. 5 t + 2, V at 5 t + 3, 5 t + 4.
+template <int kCtas>
+__device__ __forceinline__ void produce(uint8_t* base, Ctl& c, const PrefillParams& p, const CUtensorMap* qn,
+                                        const CUtensorMap* qr, const CUtensorMap* kn, const CUtensorMap* kr,
+                                        const CUtensorMap* v, uint32_t rank, int lane) {
+  constexpr int kStageBytes = kBox / kCtas, kStages = kRing / kStageBytes;
+  Units<kCtas> units(c);
+  bool ok = true;
+  uint32_t pos = 0, cleans = 0, qs[2] = {0, 0};
+  while (const Unit* up = units.next(ok)) {
+    const int h = up->h, row0 = up->row0, q0 = up->q0, k0 = up->k0, j0 = up->j0, j1 = up->j1, clean0 = up->clean0;
+    const int n[2] = {up->n0, up->n1};
+    for (int j = j0; j < j1 && ok; ++j) {
+      const int tok = k0 + j * kKeys;
+      for (int i = 0; i < 5 && ok; ++i, ++pos) {
+        if (j == j0 && i == 3) {
+          // Q after the first keys: three boxes for each row tile, one lane each
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+            if (n[g] <= j0) continue;
+            if (qs[g] > 0 && !(ok = wait_bar<kCtas>(&c.qfree[g], (qs[g] - 1) & 1, &c.abort_flag))) break;
+            ++qs[g];
+            if (lane == 0) expect_at_lead<kCtas>(&c.q[g], rank, 3 * kBox);
+            __syncwarp();
+            if (lane < 3) {
+              const int row = q0 + row0 + (g * kCtas + (int)rank) * kRows;
+              const uint32_t dst = smem_u32(base + (3 * g + lane) * kBox), bar = lead_bar<kCtas>(&c.q[g]);
+              if (lane < 2) load_3d<kCtas>(dst, qn, bar, lane * 64, h, row);
+              else load_3d<kCtas>(dst, qr, bar, 0, h, row);
+            }
+            __syncwarp();
+          }
+          if (!ok) break;
         }
-        mbar_arrive_expect_tx(bar, kBox);
-        if (i < 2) tma_load_3d(dst, kn, bar, i * 64, u.h, tok);
-        else if (i == 2) tma_load_3d(dst, kr, bar, 0, 0, tok);
-        else tma_load_4d(dst, v, bar, 0, tok + (i - 3) * 64, 0, u.h);
+        const uint32_t st = pos % kStages, use = pos / kStages;
+        if (use > 0 && !(ok = wait_bar<kCtas>(&c.empty[st], (use - 1) & 1, &c.abort_flag))) break;
+        if (lane == (int)(pos & 3)) {
+          const uint32_t dst = smem_u32(base + 6 * kBox + st * kStageBytes);
+          const int half = (int)rank * (kKeys / kCtas);  // a pair's CTA: tokens (K) from here
+          if (i >= 3 && j >= clean0) {
+            // its stage is full once it is clean
+            const uint32_t nth = cleans + (j - clean0), raw = smem_u32(&c.raw[nth % kRaw]);
+            if (i == 3) mbar_arrive_expect_tx(raw, 2 * kStageBytes);
+            tma_load_4d(dst, v, raw, 0, tok + (i - 3) * 64, (int)rank, h);
+          } else {
+            expect_at_lead<kCtas>(&c.full[st], rank, kStageBytes);
+            const uint32_t bar = lead_bar<kCtas>(&c.full[st]);
+            if (i < 2) load_3d<kCtas>(dst, kn, bar, i * 64, h, tok + half);
+            else if (i == 2) load_3d<kCtas>(dst, kr, bar, 0, 0, tok + half);
+            else load_4d<kCtas>(dst, v, bar, 0, tok + (i - 3) * 64, (int)rank, h);
+          }
+        }
+        __syncwarp();
       }
     }
+    if (!ok) break;
+    cleans += max(j1 - clean0, 0);
     __syncwarp();
+    if (lane == 0) units.release(); else units.skip();
   }
-  if (!ok && lane == 0) {
-    c.abort_flag = 1;
-    if (p.status) atomicOr(p.status, MLA_STATUS_WAIT_TIMEOUT);
-  }
-  // Every load issued has landed before the CTA may exit.
-  int never = 0;
-  for (int g = 0; g * 3 < boxes; ++g) mbar_wait_cta(smem_u32(&c.q[g]), 0, &never);
-  for (uint32_t j = pos > (uint32_t)kStages ? pos - kStages : 0; j < pos; ++j) {
-    const int nth = u.j0 + (int)(j / 5) - u.clean0;
-    if (j % 5 < 3 || nth < 0) mbar_wait_cta(smem_u32(&c.full[j % kStages]), (j / kStages) & 1, &never);
-    else mbar_wait_cta(smem_u32(&c.raw[nth & 1]), nth >> 1 & 1, &never);
+  if (!ok && lane == 0) give_up<kCtas>(c, p, rank);
+  // After an abort: every load issued has landed before the CTA may exit (without
+  // one, the MMAs have used them all).
+  if (!ok) {
+    int never = 0;
+    for (int g = 0; g < 2; ++g)
+      if (rank == 0 && qs[g] > 0) wait_bar<kCtas>(&c.q[g], (qs[g] - 1) & 1, &never);
+    for (uint32_t k = pos > (uint32_t)kStages ? pos - kStages : 0; rank == 0 && k < pos; ++k)
+      wait_bar<kCtas>(&c.full[k % kStages], (k / kStages) & 1, &never);
   }
 }
 
-// a0, a1: key tiles of the two row tiles.
-__device__ __forceinline__ void issue_mmas(uint8_t* base, Ctl& c, const PrefillParams& p, int a0, int a1,
-                                           uint32_t tmem) {
-  constexpr uint32_t idesc_s = idesc_bf16_f32(kRows, kKeys, false, false);
-  constexpr uint32_t idesc_o = idesc_bf16_f32(kRows, kKeys, false, true);
-  const int tiles = max(a0, a1);
-  const uint64_t q0 = sdesc_sw128(smem_u32(base), 16, 1024);
-  const uint64_t k0 = sdesc_sw128(smem_u32(base + 6 * kBox), 16, 1024);
+template <int kCtas>
+__device__ __forceinline__ void issue_mmas(uint8_t* base, Ctl& c, const PrefillParams& p, uint32_t tmem) {
+  constexpr int kStageBytes = kBox / kCtas, kStages = kRing / kStageBytes;
+  const uint64_t qd = sdesc_sw128(smem_u32(base), 16, 1024);
+  const uint64_t kd = sdesc_sw128(smem_u32(base + 6 * kBox), 16, 1024);
   // V: MN-major, the next 64 dims 8 KB (LBO) on, the next 8 tokens 1 KB (SBO) on,
   // the next 16 tokens 2 KB; P: 16 tokens in 8 columns
-  const uint64_t v0 = sdesc_sw128(smem_u32(base + 6 * kBox), kBox / 2, 1024);
+  const uint64_t vd = sdesc_sw128(smem_u32(base + 6 * kBox), kBox / 2, 1024);
   bool ok = true;
   const auto wait = [&](uint64_t* bar, uint32_t parity) {
-    ok = ok && mbar_wait_cta(smem_u32(bar), parity, &c.abort_flag);
+    ok = ok && wait_bar<kCtas>(bar, parity, &c.abort_flag);
     return ok;
   };
-  for (int t = 0; t <= tiles && ok; ++t) {
-    const uint32_t kpos = 5 * t, vpos = 5 * t - 2;  // vpos: V(t - 1)
+  Units<kCtas> units(c);
+  uint32_t at = 0;                              // ring position of K(t)
+  uint32_t ps0 = 0, ps1 = 0, qs0 = 0, qs1 = 0;  // tiles and units of each row tile so far
+  while (const Unit* u = units.next(ok)) {
+    const int a0 = u->n0 - u->j0, a1 = u->n1 - u->j0, tiles = u->j1 - u->j0;
+    for (int t = 0; t <= tiles && ok; ++t) {
+      const uint32_t kpos = at, vpos = kpos - 2;  // of K(t) and V(t - 1)
 #pragma unroll 1
-    for (int g = 0; g < 2 && ok; ++g) {
-      const uint32_t s = tmem + g * kKeys, o = tmem + (2 + g) * kKeys;
-      const int a = g ? a1 : a0;
-      if (t > 0 && t - 1 < a) {
-        if (!wait(&c.p[g], (t - 1) & 1)) break;
+      for (int g = 0; g < 2 && ok; ++g) {
+        const uint32_t s = tmem + g * kKeys, o = tmem + (2 + g) * kKeys;
+        const int a = g ? a1 : a0;
+        if (t > 0 && t - 1 < a) {
+          if (!wait(&c.p[g], ((g ? ps1 : ps0) + t - 1) & 1)) break;
 #pragma unroll 1
-        for (int i = 0; i < 2; ++i) {
-          const uint32_t st = (vpos + i) % kStages;
-          if (!wait(&c.full[st], (vpos + i) / kStages & 1)) break;
-          tc_fence_after();
-          const uint64_t b = v0 + st * (kBox >> 4);
+          for (int i = 0; i < 2; ++i) {
+            const uint32_t st = (vpos + i) % kStages;
+            if (!wait(&c.full[st], (vpos + i) / kStages & 1)) break;
+            tc_fence_after();
+            const uint64_t b = vd + st * (kStageBytes >> 4);
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            mma_ts(o, s + (4 * i + k) * 8, b + 128 * k, idesc_o, (t > 1 || i || k) ? 1u : 0u);
-          if (g || t - 1 >= a1) mma_commit(smem_u32(&c.empty[st]));
+            for (int k = 0; k < 4; ++k)
+              mma_pv<kCtas>(o, s + (4 * i + k) * 8, b + 128 * k, (t > 1 || i || k) ? 1u : 0u);
+            if (g || t - 1 >= a1) commit<kCtas>(&c.empty[st]);
+          }
+          if (!ok) break;
+          if (t == a) commit<kCtas>(&c.o[g]);
         }
-        if (!ok) break;
-        if (t == a) mma_commit(smem_u32(&c.o[g]));
-      }
-      if (t < a) {
-        if (t == 0 && !wait(&c.q[g], 0)) break;
+        if (t < a) {
+          if (t == 0 && !wait(&c.q[g], (g ? qs1 : qs0) & 1)) break;
 #pragma unroll 1
-        for (int i = 0; i < 3; ++i) {
-          const uint32_t st = (kpos + i) % kStages;
-          if (!wait(&c.full[st], (kpos + i) / kStages & 1)) break;
-          tc_fence_after();
-          const uint64_t q = q0 + (3 * g + i) * (kBox >> 4), b = k0 + st * (kBox >> 4);
+          for (int i = 0; i < 3; ++i) {
+            const uint32_t st = (kpos + i) % kStages;
+            if (!wait(&c.full[st], (kpos + i) / kStages & 1)) break;
+            tc_fence_after();
+            const uint64_t q = qd + (3 * g + i) * (kBox >> 4), b = kd + st * (kStageBytes >> 4);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) mma_ss(s, q + 2 * k, b + 2 * k, idesc_s, (i || k) ? 1u : 0u);
-          if (g || t >= a1) mma_commit(smem_u32(&c.empty[st]));
+            for (int k = 0; k < 4; ++k) mma_qk<kCtas>(s, q + 2 * k, b + 2 * k, (i || k) ? 1u : 0u);
+            if (g || t >= a1) commit<kCtas>(&c.empty[st]);
+          }
+          if (!ok) break;
+          commit<kCtas>(&c.s[g]);
+          if (t == a - 1) commit<kCtas>(&c.qfree[g]);
         }
-        if (!ok) break;
-        mma_commit(smem_u32(&c.s[g]));
       }
+      if (t < tiles) at += 5;
     }
+    if (!ok) break;
+    if (a0 > 0) ps0 += a0, ++qs0;
+    if (a1 > 0) ps1 += a1, ++qs1;
+    units.release();
   }
-  if (!ok) {
-    c.abort_flag = 1;
-    if (p.status) atomicOr(p.status, MLA_STATUS_WAIT_TIMEOUT);
-  }
+  if (!ok) give_up<kCtas>(c, p, 0);
   // No MMA may still run when the accumulators are freed.
   int never = 0;
-  mma_commit(smem_u32(&c.drain));
-  mbar_wait_cta(smem_u32(&c.drain), 0, &never);
+  commit<kCtas>(&c.drain);
+  wait_bar<kCtas>(&c.drain, 0, &never);
 }
 
 // Tiles from u.clean0 on hold tokens that some row does not see (its own later
 // ones, or the next sequence's).  Warp i of the two cleans stage i of a tile's V.
-__device__ __forceinline__ void clean_values(uint8_t* base, Ctl& c, const PrefillParams& p, const Unit& u,
-                                             int i, int lane) {
-  const int from = sees(p, u.lq, u.lk, u.prefix, u.row0);
-  for (int j = u.clean0; j < u.j1; ++j) {
-    const int nth = j - u.clean0;
-    if (!__all_sync(~0u, mbar_wait_cta(smem_u32(&c.raw[nth & 1]), nth >> 1 & 1, &c.abort_flag))) {
-      c.abort_flag = 1;
-      if (lane == 0 && p.status) atomicOr(p.status, MLA_STATUS_WAIT_TIMEOUT);
-      return;
-    }
-    const uint32_t st = (5 * (j - u.j0) + 3 + i) % kStages;
-    uint8_t* box = base + (6 + st) * kBox;
-    const int t0 = j * kKeys + i * 64;  // token of the stage's first row
-    // 1024 vectors: half (64 dims), row, 16-byte chunk, swizzled by the row
+template <int kCtas>
+__device__ __forceinline__ void clean_values(uint8_t* base, Ctl& c, const PrefillParams& p, uint32_t rank, int i,
+                                             int lane) {
+  constexpr int kStageBytes = kBox / kCtas, kStages = kRing / kStageBytes;
+  Units<kCtas> units(c);
+  bool ok = true;
+  uint32_t at = 0, cleans = 0;
+  while (const Unit* u = units.next(ok)) {
+    const int j0 = u->j0, j1 = u->j1, clean0 = u->clean0, unseen = u->unseen, lk = u->lk;
+    const uint32_t tag = tag_of(units.nth);
+    for (int j = clean0; j < j1; ++j) {
+      const uint32_t nth = cleans + (j - clean0);
+      if (!(ok = __all_sync(~0u, wait_bar<kCtas>(&c.raw[nth % kRaw], nth / kRaw & 1, &c.abort_flag)))) break;
+      // the notes on the unit before have been read (by both CTAs)
+      if (j == clean0 && units.nth > 0 &&
+          !(ok = __all_sync(~0u, wait_bar<kCtas>(&c.done, (units.nth - 1) & 1, &c.abort_flag))))
+        break;
+      const uint32_t st = (at + 5 * (j - j0) + 3 + i) % kStages;
+      uint8_t* box = base + 6 * kBox + st * kStageBytes;
+      const int t0 = j * kKeys + i * 64;  // token of the stage's first row
+      // 16-byte vectors: half (64 dims), row, chunk, swizzled by the row
 #pragma unroll 4
-    for (int x = lane; x < kBox / 16; x += 32) {
-      uint4* at = reinterpret_cast<uint4*>(box + x * 16);
-      const int half = x >> 9, row = (x >> 3) & 63, chunk = (x & 7) ^ (row & 7);
-      uint4 w = *at;
-      uint32_t* r = reinterpret_cast<uint32_t*>(&w);
-      uint32_t hit = 0;
+      for (int x = lane; x < kStageBytes / 16; x += 32) {
+        uint4* vec = reinterpret_cast<uint4*>(box + x * 16);
+        const int half = (int)rank + (x >> 9), row = (x >> 3) & 63, chunk = (x & 7) ^ (row & 7);
+        uint4 w = *vec;
+        uint32_t* r = reinterpret_cast<uint32_t*>(&w);
+        uint32_t hit = 0;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) hit |= (r[e] & 0x7f807f80u) + 0x00800080u;
-      if (!(hit & 0x80008000u) || t0 + row < from) continue;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const uint32_t b = r[e / 2] >> (16 * (e & 1)) & 0xffffu;
-        if ((b & 0x7f80u) != 0x7f80u) continue;
-        r[e / 2] &= e & 1 ? 0x0000ffffu : 0xffff0000u;
-        if (t0 + row < u.lk) {
-          const int kind = b & 0x7fu ? 0 : b & 0x8000u ? 2 : 1;
-          atomicMin(&c.odd[kind][half * 64 + chunk * 8 + e], t0 + row);
-          c.any_odd = 1;
+        for (int e = 0; e < 4; ++e) hit |= (r[e] & 0x7f807f80u) + 0x00800080u;
+        if (!(hit & 0x80008000u) || t0 + row < unseen) continue;
+        for (int e = 0; e < 8; ++e) {
+          const uint32_t b = r[e / 2] >> (16 * (e & 1)) & 0xffffu;
+          if ((b & 0x7f80u) != 0x7f80u) continue;
+          r[e / 2] &= e & 1 ? 0x0000ffffu : 0xffff0000u;
+          const int past = t0 + row - unseen;
+          if (t0 + row < lk && past < 1 << kOffsetBits) {  // past that no row of the unit sees it
+            uint32_t* odd = &c.odd[b & 0x7fu ? 0 : b & 0x8000u ? 2 : 1][half * 64 + chunk * 8 + e];
+            atomicMin(odd, tag | past);
+            atomicMin(&c.any_odd, tag);
+            if constexpr (kCtas == 2) {
+              red_min_cluster_u32(mapa(smem_u32(odd), rank ^ 1), tag | past);
+              red_min_cluster_u32(mapa(smem_u32(&c.any_odd), rank ^ 1), tag);
+            }
+          }
         }
+        *vec = w;
       }
-      *at = w;
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        if (rank == 0) mbar_arrive(smem_u32(&c.full[st]));
+        else mbar_arrive_cluster(lead_bar<kCtas>(&c.full[st]));
+      }
     }
-    fence_proxy_async_smem();
+    if (!ok) break;
+    at += 5 * (j1 - j0);
+    if (j1 > clean0) {
+      cleans += j1 - clean0;
+      if (lane == 0) {
+        mbar_arrive(smem_u32(&c.cleaned));
+        if constexpr (kCtas == 2) mbar_arrive_cluster(mapa(smem_u32(&c.cleaned), rank ^ 1));
+      }
+    }
     __syncwarp();
-    if (lane == 0) mbar_arrive(smem_u32(&c.full[st]));
+    if (lane == 0) units.release(); else units.skip();
   }
-  __syncwarp();
-  if (lane == 0) mbar_arrive(smem_u32(&c.cleaned));
+  if (!ok && lane == 0) give_up<kCtas>(c, p, rank);
 }
 
 // Softmax of row tile g, one thread per row, then the row's output.
-__device__ __forceinline__ void softmax_rows(Ctl& c, const PrefillParams& p, const Unit& u, uint32_t tmem,
-                                             int g, int warp, int lane) {
-  const int r = (warp & 3) * 32 + lane, i = u.row0 + g * kRows + r;
-  const bool exists = g * kRows + r < u.rows;
-  const int seen = exists ? sees(p, u.lq, u.lk, u.prefix, i) : 0x7fffffff;  // padding rows: unmasked
+template <int kCtas>
+__device__ __forceinline__ void softmax_rows(Ctl& c, const PrefillParams& p, uint32_t tmem, uint32_t rank, int g,
+                                             int warp, int lane) {
+  const int r = (warp & 3) * 32 + lane, in_block = (g * kCtas + (int)rank) * kRows + r;
   const uint32_t quad = (uint32_t)((warp & 3) * 32) << 16;
   const uint32_t s_at = tmem + quad + g * kKeys, o_at = tmem + quad + (2 + g) * kKeys;
   const uint64_t scale2 = f2pack(p.scale2, p.scale2);
-  float ref = -INFINITY, l = 0.f;  // raw scores; sum of 2^((s - ref) scale2)
+  const uint32_t lead_p = lead_bar<kCtas>(&c.p[g]), lead_note = kCtas == 1 ? 0 : mapa(smem_u32(&c.note), 0);
+  Units<kCtas> units(c);
   bool ok = true;
-  const int tiles = (g ? u.n1 : u.n0) - u.j0, seen0 = exists ? seen - u.j0 * kKeys : 0x7fffffff;
-  // where the row's output goes: its row of out, or of the part's workspace
-  const bool whole = u.parts == 1, cleaned = u.j1 > u.clean0;
-  const int64_t row = whole ? (u.q0 + i) * p.H + u.h
-                            : ((int64_t)(u.slot + u.part) * p.H + u.h) * kBlock + g * kRows + r;
-  for (int t = 0; t < tiles; ++t) {
-    if (!(ok = mbar_wait_cta(smem_u32(&c.s[g]), t & 1, &c.abort_flag))) break;
-    tc_fence_after();
-    float s[kKeys];
+  uint32_t turns = 0, outs = 0, cleans = 0;  // phases of c.s, c.o and c.cleaned
+  while (const Unit* u = units.next(ok)) {
+    const bool exists = in_block < u->rows, cleaned = u->j1 > u->clean0;
+    const int j0 = u->j0, tiles = (g ? u->n1 : u->n0) - j0;
+    // keys that the row sees, from the unit's first tile on; padding rows: all
+    const int seen = exists ? sees(p, u->lq, u->lk, u->prefix, u->row0 + in_block) - j0 * kKeys : 0x7fffffff;
+    const int unseen = u->unseen - j0 * kKeys;
+    const bool whole = u->slot < 0;
+    // where the row's output goes: its row of out, or of the part's workspace
+    const int64_t row = whole ? ((int64_t)u->q0 + u->row0 + in_block) * p.H + u->h
+                              : ((int64_t)(u->slot + in_block / kSlot) * p.H + u->h) * kSlot + in_block % kSlot;
+    float ref = -INFINITY, l = 0.f;  // raw scores; sum of 2^((s - ref) scale2)
+    for (int t = 0; t < tiles; ++t, ++turns) {
+      if (!(ok = wait_bar<kCtas>(&c.s[g], turns & 1, &c.abort_flag))) break;
+      tc_fence_after();
+      float s[kKeys];
 #pragma unroll
-    for (int b = 0; b < 4; ++b) tmem_ld32(s_at + 32 * b, *reinterpret_cast<uint32_t(*)[32]>(&s[32 * b]));
-    tmem_wait_ld();
-    const int last = seen0 - t * kKeys;  // columns of this tile that the row sees
-    if (__any_sync(~0u, last < kKeys)) {
+      for (int b = 0; b < 4; ++b) tmem_ld32(s_at + 32 * b, *reinterpret_cast<uint32_t(*)[32]>(&s[32 * b]));
+      tmem_wait_ld();
+      const int last = seen - t * kKeys;  // columns of this tile that the row sees
+      if (__any_sync(~0u, last < kKeys)) {
 #pragma unroll
-      for (int e = 0; e < kKeys; ++e) s[e] = e < last ? s[e] : -INFINITY;
-    }
-    float m4[4] = {s[0], s[1], s[2], s[3]};
-#pragma unroll
-    for (int e = 4; e < kKeys; e += 8) {
-#pragma unroll
-      for (int b = 0; b < 4; ++b)
-        m4[b] = e + 4 + b < kKeys ? max3(m4[b], s[e + b], s[e + 4 + b]) : fmaxf(m4[b], s[e + b]);
-    }
-    const float m = fmaxf(max3(m4[0], m4[1], m4[2]), m4[3]);
-    // A row's first score, or one far above the reference: a new reference.
-    const bool rise = (m - ref) * p.scale2 > kRise;  // ref = -inf: true for a finite m
-    if (__any_sync(~0u, rise)) {
-      float a = 1.f;
-      if (rise) {
-        a = ref > -INFINITY ? ex2((ref - m) * p.scale2) : 1.f;  // nothing summed so far: O is 0
-        l *= a;
-        ref = m;
+        for (int e = 0; e < kKeys; ++e) s[e] = e < last ? s[e] : -INFINITY;
       }
-      if (t > 0) {
-#pragma unroll 1
-        for (int b = 0; b < 4; ++b) {
-          uint32_t o[32];
-          tmem_ld32(o_at + 32 * b, o);
-          tmem_wait_ld();
+      float m4[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * a);
-          tmem_st32(o_at + 32 * b, o);
+      for (int e = 4; e < kKeys; e += 8) {
+#pragma unroll
+        for (int b = 0; b < 4; ++b)
+          m4[b] = e + 4 + b < kKeys ? max3(m4[b], s[e + b], s[e + 4 + b]) : fmaxf(m4[b], s[e + b]);
+      }
+      const float m = fmaxf(max3(m4[0], m4[1], m4[2]), m4[3]);
+      // A row's first score, or one far above the reference: a new reference.
+      const bool rise = (m - ref) * p.scale2 > kRise;  // ref = -inf: true for a finite m
+      if (__any_sync(~0u, rise)) {
+        float a = 1.f;
+        if (rise) {
+          a = ref > -INFINITY ? ex2((ref - m) * p.scale2) : 1.f;  // nothing summed so far: O is 0
+          l *= a;
+          ref = m;
+        }
+        if (t > 0) {
+#pragma unroll 1
+          for (int b = 0; b < 4; ++b) {
+            uint32_t o[32];
+            tmem_ld32(o_at + 32 * b, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * a);
+            tmem_st32(o_at + 32 * b, o);
+          }
         }
       }
-    }
-    const float off = ref > -INFINITY ? -ref * p.scale2 : 0.f;
-    const uint64_t off2 = f2pack(off, off);
-    uint64_t sum2[2] = {f2pack(l, 0.f), f2pack(0.f, 0.f)};
+      const float off = ref > -INFINITY ? -ref * p.scale2 : 0.f;
+      const uint64_t off2 = f2pack(off, off);
+      uint64_t sum2[2] = {f2pack(l, 0.f), f2pack(0.f, 0.f)};
 #pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      uint32_t pk[32];
+      for (int b = 0; b < 2; ++b) {
+        uint32_t pk[32];
 #pragma unroll
-      for (int e = 0; e < 32; ++e) {
-        float ya, yb;
-        f2unpack(ffma2(f2pack(s[64 * b + 2 * e], s[64 * b + 2 * e + 1]), scale2, off2), ya, yb);
-        const float pa = ex2(ya), pb = ex2(yb);
-        sum2[e & 1] = fadd2(sum2[e & 1], f2pack(pa, pb));
-        pk[e] = pack_bf16(pa, pb);
+        for (int e = 0; e < 32; ++e) {
+          float ya, yb;
+          f2unpack(ffma2(f2pack(s[64 * b + 2 * e], s[64 * b + 2 * e + 1]), scale2, off2), ya, yb);
+          const float pa = ex2(ya), pb = ex2(yb);
+          sum2[e & 1] = fadd2(sum2[e & 1], f2pack(pa, pb));
+          pk[e] = pack_bf16(pa, pb);
+        }
+        tmem_st32(s_at + 32 * b, pk);
       }
-      tmem_st32(s_at + 32 * b, pk);
+      float x, y, z, w;
+      f2unpack(sum2[0], x, y);
+      f2unpack(sum2[1], z, w);
+      l = (x + y) + (z + w);
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        // a pair's second CTA reports by an asynchronous store, whose completion on
+        // the first CTA's barrier is a release at cluster scope (a release arrive
+        // costs its round trip); the first CTA's warp 0 arms the barrier for them
+        if (kCtas == 1) mbar_arrive(lead_p);
+        else if (rank) st_async_u32(lead_note, 0, lead_p);
+        else if ((warp & 3) == 0) mbar_arrive_expect_tx(smem_u32(&c.p[g]), 16);
+        else mbar_arrive(smem_u32(&c.p[g]));
+      }
     }
-    float x, y, z, w;
-    f2unpack(sum2[0], x, y);
-    f2unpack(sum2[1], z, w);
-    l = (x + y) + (z + w);
-    tmem_wait_st();
-    tc_fence_before();
-    mbar_arrive(smem_u32(&c.p[g]));
-  }
-  if (ok && tiles > 0) ok = mbar_wait_cta(smem_u32(&c.o[g]), 0, &c.abort_flag);
-  if (ok && cleaned) ok = mbar_wait_cta(smem_u32(&c.cleaned), 0, &c.abort_flag);
-  if (!ok) {
-    c.abort_flag = 1;
-    if (lane == 0 && p.status) atomicOr(p.status, MLA_STATUS_WAIT_TIMEOUT);
-    return;
-  }
-  tc_fence_after();
-  const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
-  const float lse = l > 0.f || l != l ? ref * p.sm_scale + logf(l) : -INFINITY;
-  const bool odd = *reinterpret_cast<volatile int*>(&c.any_odd) != 0;
-#pragma unroll 1
-  for (int b = 0; b < 4; ++b) {
-    uint32_t o[32];
-    __syncwarp();
+    if (!ok) break;
     if (tiles > 0) {
-      tmem_ld32(o_at + 32 * b, o);
-      tmem_wait_ld();
-    } else {
-#pragma unroll
-      for (int e = 0; e < 32; ++e) o[e] = 0;
+      if (!(ok = wait_bar<kCtas>(&c.o[g], outs & 1, &c.abort_flag))) break;
+      ++outs;
     }
-    float f[32];
+    if (cleaned) {
+      if (!(ok = wait_bar<kCtas>(&c.cleaned, cleans & 1, &c.abort_flag))) break;
+      ++cleans;
+    }
+    tc_fence_after();
+    const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+    const float lse = l > 0.f || l != l ? ref * p.sm_scale + logf(l) : -INFINITY;
+    // notes of this unit: tokens that the row sees get their values back
+    const uint32_t tag = tag_of(units.nth), reach = tag + (uint32_t)min(max(seen - unseen, 0), 1 << kOffsetBits);
+    const bool odd = cleaned && *reinterpret_cast<volatile uint32_t*>(&c.any_odd) == tag;
+#pragma unroll 1
+    for (int b = 0; b < 4; ++b) {
+      uint32_t o[32];
+      __syncwarp();
+      if (tiles > 0) {
+        tmem_ld32(o_at + 32 * b, o);
+        tmem_wait_ld();
+      } else {
 #pragma unroll
-    for (int e = 0; e < 32; ++e) f[e] = l == 0.f ? 0.f : __uint_as_float(o[e]) * inv;
-    if (odd) {
+        for (int e = 0; e < 32; ++e) o[e] = 0;
+      }
+      float f[32];
 #pragma unroll
-      for (int e = 0; e < 32; ++e) {
-        if (c.odd[0][32 * b + e] < seen) f[e] += NAN;
-        if (c.odd[1][32 * b + e] < seen) f[e] += INFINITY;
-        if (c.odd[2][32 * b + e] < seen) f[e] -= INFINITY;
+      for (int e = 0; e < 32; ++e) f[e] = l == 0.f ? 0.f : __uint_as_float(o[e]) * inv;
+      if (odd) {
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+          if (c.odd[0][32 * b + e] < reach) f[e] += NAN;
+          if (c.odd[1][32 * b + e] < reach) f[e] += INFINITY;
+          if (c.odd[2][32 * b + e] < reach) f[e] -= INFINITY;
+        }
+      }
+      if (exists && whole) {
+        uint4* dst = reinterpret_cast<uint4*>(p.out + row * MLA_V_HEAD_DIM + 32 * b);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          dst[e] = make_uint4(pack_bf16(f[8 * e], f[8 * e + 1]), pack_bf16(f[8 * e + 2], f[8 * e + 3]),
+                              pack_bf16(f[8 * e + 4], f[8 * e + 5]), pack_bf16(f[8 * e + 6], f[8 * e + 7]));
+      } else if (exists) {
+        float4* dst = reinterpret_cast<float4*>(p.O_part + row * MLA_V_HEAD_DIM + 32 * b);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) dst[e] = make_float4(f[4 * e], f[4 * e + 1], f[4 * e + 2], f[4 * e + 3]);
       }
     }
-    if (exists && whole) {
-      uint4* dst = reinterpret_cast<uint4*>(p.out + row * MLA_V_HEAD_DIM + 32 * b);
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        dst[e] = make_uint4(pack_bf16(f[8 * e], f[8 * e + 1]), pack_bf16(f[8 * e + 2], f[8 * e + 3]),
-                            pack_bf16(f[8 * e + 4], f[8 * e + 5]), pack_bf16(f[8 * e + 6], f[8 * e + 7]));
-    } else if (exists) {
-      float4* dst = reinterpret_cast<float4*>(p.O_part + row * MLA_V_HEAD_DIM + 32 * b);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) dst[e] = make_float4(f[4 * e], f[4 * e + 1], f[4 * e + 2], f[4 * e + 3]);
+    if (exists) {
+      if (!whole) p.LSE_part[row] = lse;
+      else if (p.lse) p.lse[row] = lse;
+    }
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) {
+      mbar_arrive(smem_u32(&c.done));
+      if constexpr (kCtas == 2) mbar_arrive_cluster(mapa(smem_u32(&c.done), rank ^ 1));
+      units.release();
+    } else {
+      units.skip();
     }
   }
-  if (exists) {
-    if (!whole) p.LSE_part[row] = lse;
-    else if (p.lse) p.lse[row] = lse;
-  }
+  if (!ok && lane == 0) give_up<kCtas>(c, p, rank);
 }
 
+template <int kCtas>
 __global__ void __launch_bounds__(kThreads, 1)
     mla_prefill_kernel(const __grid_constant__ CUtensorMap qn, const __grid_constant__ CUtensorMap qr,
                        const __grid_constant__ CUtensorMap kn, const __grid_constant__ CUtensorMap kr,
                        const __grid_constant__ CUtensorMap v, const PrefillParams p) {
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* base =
-      reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  Ctl& c = *reinterpret_cast<Ctl*>(base + (6 + kStages) * kBox);
+  extern __shared__ __align__(1024) uint8_t base[];
+  Ctl& c = *reinterpret_cast<Ctl*>(base + 6 * kBox + kRing);
   const int warp = __shfl_sync(~0u, (int)threadIdx.x / 32, 0), lane = threadIdx.x % 32;
-  Unit u;
-  if (!find_unit(p, u)) return;  // the whole CTA
+  const uint32_t rank = kCtas == 1 ? 0 : __shfl_sync(~0u, cluster_ctarank(), 0);
   if (threadIdx.x == 0) {
-    c.abort_flag = c.any_odd = 0;
+    c.abort_flag = 0;
+    c.any_odd = ~0u;
     for (int g = 0; g < 2; ++g) {
-      mbar_init(smem_u32(&c.q[g]), 1);
+      mbar_init(smem_u32(&c.q[g]), kCtas);
+      mbar_init(smem_u32(&c.qfree[g]), 1);
       mbar_init(smem_u32(&c.s[g]), 1);
-      mbar_init(smem_u32(&c.p[g]), kRows);
+      mbar_init(smem_u32(&c.p[g]), 4);
       mbar_init(smem_u32(&c.o[g]), 1);
+      mbar_init(smem_u32(&c.unit_full[g]), 1);
+      mbar_init(smem_u32(&c.unit_empty[g]), 12);  // TMA, MMA, 2 cleaning, 8 softmax warps
     }
-    for (int i = 0; i < kStages; ++i) {
-      mbar_init(smem_u32(&c.full[i]), 1);
+    for (int i = 0; i < 16; ++i) {
+      mbar_init(smem_u32(&c.full[i]), kCtas);
       mbar_init(smem_u32(&c.empty[i]), 1);
     }
-    mbar_init(smem_u32(&c.raw[0]), 1);
-    mbar_init(smem_u32(&c.raw[1]), 1);
-    mbar_init(smem_u32(&c.cleaned), 2);
+    for (int i = 0; i < kRaw; ++i) mbar_init(smem_u32(&c.raw[i]), 1);
+    mbar_init(smem_u32(&c.cleaned), 2 * kCtas);
+    mbar_init(smem_u32(&c.done), 8 * kCtas);
+    mbar_init(smem_u32(&c.answer_full), 1);
+    mbar_init(smem_u32(&c.answer_free), 1);
     mbar_init(smem_u32(&c.drain), 1);
     fence_mbar_init();
+    prefetch_tmap(&qn);
+    prefetch_tmap(&qr);
+    prefetch_tmap(&kn);
+    prefetch_tmap(&kr);
+    prefetch_tmap(&v);
   }
-  for (int i = threadIdx.x; i < 3 * kKeys; i += kThreads) c.odd[i / kKeys][i % kKeys] = 0x7fffffff;
+  for (int i = threadIdx.x; i < 3 * kKeys; i += kThreads) c.odd[i / kKeys][i % kKeys] = ~0u;
   if (warp == kWarpMma) {
-    tmem_alloc(smem_u32(&c.tmem), 512);
-    tmem_relinquish();
+    if constexpr (kCtas == 1) {
+      tmem_alloc(smem_u32(&c.tmem), 512);
+      tmem_relinquish();
+    } else {
+      tmem_alloc_pair(smem_u32(&c.tmem), 512);
+      tmem_relinquish_pair();
+    }
   }
   tc_fence_before();
   __syncthreads();
+  if constexpr (kCtas == 2) cluster_sync();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(~0u, c.tmem, 0);
   // Roles never rejoin below their register split: each ends with the teardown.
+  const auto teardown = [&]() {
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if constexpr (kCtas == 2) cluster_sync();
+    tc_fence_after();
+    if (warp == kWarpMma) {
+      if constexpr (kCtas == 1) tmem_dealloc(tmem, 512);
+      else tmem_dealloc_pair(tmem, 512);
+    }
+  };
   if (warp >= kWarpTma) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
     if (warp == kWarpTma) {
-      produce(base, c, p, u, &qn, &qr, &kn, &kr, &v, lane);
+      produce<kCtas>(base, c, p, &qn, &qr, &kn, &kr, &v, rank, lane);
     } else if (warp == kWarpMma) {
-      // uniform values: see elect_one
-      const int a0 = __shfl_sync(~0u, u.n0 - u.j0, 0), a1 = __shfl_sync(~0u, u.n1 - u.j0, 0);
-      if (elect_one()) issue_mmas(base, c, p, a0, a1, tmem);
-    } else {
-      clean_values(base, c, p, u, warp - kWarpClean, lane);
+      if (rank == 0) {
+        if (elect_one()) issue_mmas<kCtas>(base, c, p, tmem);
+      } else if (lane == 0) {  // passes the units on
+        bool ok;
+        Units<kCtas> units(c);
+        while (units.next(ok)) units.release();
+        int never = 0;
+        wait_bar<kCtas>(&c.drain, 0, &never);
+      }
+    } else if (warp == kWarpNext) {
+      if (lane == 0) feed<kCtas>(c, p, rank);
+    } else if (warp == kWarpClean || warp == kWarpClean + 1) {
+      clean_values<kCtas>(base, c, p, rank, warp - kWarpClean, lane);
     }
-    __syncwarp();
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    if (warp == kWarpMma) tmem_dealloc(tmem, 512);
+    teardown();
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
-    softmax_rows(c, p, u, tmem, warp / 4, warp, lane);
-    __syncwarp();
-    tc_fence_before();
-    __syncthreads();
+    softmax_rows<kCtas>(c, p, tmem, rank, warp / 4, warp, lane);
+    teardown();
   }
 }
 
 // Merge of a block's parts, a warp per row: weights e^(LSE_s - max), parts in
 // order.  Parts without keys (LSE = -inf) weigh nothing; a NaN makes the row NaN.
+template <int kCtas>
 __global__ void __launch_bounds__(256) mla_prefill_merge_kernel(const PrefillParams p) {
-  griddep_wait();
-  const int32_t* e = p.work + (int64_t)(blockIdx.x / p.H) * kEntry;
+  constexpr int kBlock = kSlot * kCtas;
+  const int32_t* e = p.work + (int64_t)(blockIdx.x / p.H) * kEntry * kCtas;
   const int h = blockIdx.x % p.H, seq = e[0], parts = e[3], slot = e[4];
   if (e[2] != 0 || parts < 2 || parts > MLA_PREFILL_MAX_PARTS || slot < 0 ||
-      slot > p.num_parts - parts || seq < 0 || seq >= p.N || e[1] < 0)
+      slot > p.num_parts - parts * kCtas || seq < 0 || seq >= p.N || e[1] < 0 || e[7] != kBlock)
     return;  // reported by the first launch
   const int64_t q0 = p.cu_q[seq], lq = p.cu_q[seq + 1] - q0, row0 = (int64_t)e[1] * kBlock;
   const int64_t k0 = p.cu_kv[seq], lk = p.cu_kv[seq + 1] - k0;
   if (q0 < 0 || lq < 0 || q0 + lq > p.Tq || k0 < 0 || lk < 0 || k0 + lk > p.Tk) return;
   const int rows = (int)min((int64_t)kBlock, lq - row0), lane = threadIdx.x & 31;
   for (int r = threadIdx.x / 32; r < rows; r += 8) {
-    const int64_t at = ((int64_t)slot * p.H + h) * kBlock + r, step = (int64_t)p.H * kBlock;
+    const int64_t at = ((int64_t)(slot + r / kSlot) * p.H + h) * kSlot + r % kSlot;
+    const int64_t step = (int64_t)kCtas * p.H * kSlot;
     const float mine = lane < parts ? p.LSE_part[at + lane * step] : -INFINITY;
     float m = mine;
 #pragma unroll
@@ -593,14 +834,42 @@ __global__ void __launch_bounds__(256) mla_prefill_merge_kernel(const PrefillPar
   }
 }
 
-// Tensor map of [T, H, dims] bf16 in boxes of 64 dims x 128 tokens of a head.
+// Tensor map of [T, H, dims] bf16 in boxes of 64 dims x `rows` tokens of a head.
 int head_map(CUtensorMap* map, const void* base, int dims, int H, int64_t T, int64_t token_stride,
-             int64_t head_stride) {
+             int64_t head_stride, int rows) {
   const uint64_t d[3] = {(uint64_t)dims, (uint64_t)H, (uint64_t)std::max<int64_t>(T, 1)};
   const uint64_t st[2] = {(uint64_t)(H > 1 ? head_stride : dims) * 2,
                           (uint64_t)(T > 1 ? token_stride : (int64_t)H * dims) * 2};
-  const uint32_t box[3] = {64, 1, 128};
+  const uint32_t box[3] = {64, 1, (uint32_t)rows};
   return make_tensor_map_bf16_3d(map, base, d, st, box);
+}
+
+template <int kCtas>
+int launch_prefill(const CUtensorMap& qn, const CUtensorMap& qr, const CUtensorMap& kn, const CUtensorMap& kr,
+                   const CUtensorMap& v, const PrefillParams& p, cudaStream_t st) {
+  auto kernel = mla_prefill_kernel<kCtas>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(mla_prefill_kernel)");
+  const unsigned units = (unsigned)p.num_work * (unsigned)p.H;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(units * kCtas, 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.dynamicSmemBytes = kSmem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = kCtas;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = kCtas > 1 ? 1 : 0;
+  e = cudaLaunchKernelEx(&cfg, kernel, qn, qr, kn, kr, v, p);
+  if (e != cudaSuccess) return cuda_fail(e, "launch mla_prefill_kernel");
+  if (p.num_parts > 0) {
+    mla_prefill_merge_kernel<kCtas><<<units, 256, 0, st>>>(p);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return cuda_fail(e, "launch mla_prefill_merge_kernel");
+  }
+  return MLA_OK;
 }
 
 // One head's rows of `dims` values at these strides.
@@ -623,7 +892,7 @@ extern "C" int mla_prefill(const void* q_nope, int64_t qn_token_stride, int64_t 
                            const void* v, int64_t v_token_stride, int64_t v_head_stride, int64_t Tk,
                            int H, const int32_t* cu_q, const int32_t* cu_kv, const int32_t* prefix,
                            int N, int causal, float sm_scale, const int32_t* work, int num_work,
-                           int num_parts, float* O_part, float* LSE_part, void* out, float* lse,
+                           int ctas, int num_parts, float* O_part, float* LSE_part, void* out, float* lse,
                            int* status, mla_stream_t stream) {
   constexpr int kNope = MLA_QK_NOPE_DIM, kRope = MLA_ROPE_DIM, kValue = MLA_V_HEAD_DIM;
   if (Tq < 0 || Tk < 0 || N < 0 || num_work < 0 || num_parts < 0 || H < 1)
@@ -631,7 +900,9 @@ extern "C" int mla_prefill(const void* q_nope, int64_t qn_token_stride, int64_t 
                 (long long)Tq, (long long)Tk, N, num_work, num_parts, H);
   if (!(sm_scale > 0.f) || sm_scale > 1e30f)
     return fail(MLA_ERR_INVALID_ARG, "mla_prefill: sm_scale %g is not a positive number", (double)sm_scale);
-  if (Tq > 0x7fffff00 || Tk > 0x7fffff00 || H > 65535 || (int64_t)num_work * H > 0x7fffffff)
+  if (ctas != 1 && ctas != 2)
+    return fail(MLA_ERR_INVALID_ARG, "mla_prefill: ctas=%d is not 1 or 2", ctas);
+  if (Tq > 0x7fffff00 || Tk > 0x7fffff00 || H > 65535 || (int64_t)num_work * H > 1 << 30)
     return fail(MLA_ERR_INVALID_ARG, "mla_prefill: Tq=%lld, Tk=%lld, H=%d or num_work=%d too large",
                 (long long)Tq, (long long)Tk, H, num_work);
   if (num_work == 0 || N == 0 || Tq == 0) return MLA_OK;
@@ -660,32 +931,23 @@ extern "C" int mla_prefill(const void* q_nope, int64_t qn_token_stride, int64_t 
     kr_token_stride = kRope;
   }
   CUtensorMap qn, qr, kn, kr, vm;
-  int rc = head_map(&qn, q_nope, kNope, H, Tq, qn_token_stride, qn_head_stride);
-  if (rc == MLA_OK) rc = head_map(&qr, q_rope, kRope, H, Tq, qr_token_stride, qr_head_stride);
-  if (rc == MLA_OK) rc = head_map(&kn, k_nope, kNope, H, Tk, kn_token_stride, kn_head_stride);
-  if (rc == MLA_OK) rc = head_map(&kr, k_rope, kRope, 1, Tk, kr_token_stride, kRope);
+  const int keys = 128 / ctas;  // a CTA's tokens of a key tile
+  int rc = head_map(&qn, q_nope, kNope, H, Tq, qn_token_stride, qn_head_stride, 128);
+  if (rc == MLA_OK) rc = head_map(&qr, q_rope, kRope, H, Tq, qr_token_stride, qr_head_stride, 128);
+  if (rc == MLA_OK) rc = head_map(&kn, k_nope, kNope, H, Tk, kn_token_stride, kn_head_stride, keys);
+  if (rc == MLA_OK) rc = head_map(&kr, k_rope, kRope, 1, Tk, kr_token_stride, kRope, keys);
   if (rc == MLA_OK) {
-    // 64 tokens x 128 dims as two halves of 64 dims, one after the other
+    // 64 tokens x 128 dims as two halves of 64 dims, one after the other; in a pair
+    // a CTA's half
     const uint64_t d[4] = {64, (uint64_t)std::max<int64_t>(Tk, 1), 2, (uint64_t)H};
     const uint64_t st[3] = {(uint64_t)(Tk > 1 ? v_token_stride : (int64_t)H * kValue) * 2, 128,
                             (uint64_t)(H > 1 ? v_head_stride : kValue) * 2};
-    const uint32_t box[4] = {64, 64, 2, 1};
+    const uint32_t box[4] = {64, 64, (uint32_t)(2 / ctas), 1};
     rc = make_tensor_map_bf16_4d(&vm, v, d, st, box);
   }
   if (rc != MLA_OK) return rc;
-  PrefillParams p{cu_q, cu_kv, prefix, N, H, causal != 0, Tq, Tk, sm_scale, sm_scale * kLog2e, work,
-                  num_work, num_parts, O_part, LSE_part, static_cast<__nv_bfloat16*>(out), lse, status};
+  const PrefillParams p{cu_q, cu_kv, prefix, N, H, causal != 0, Tq, Tk, sm_scale, sm_scale * kLog2e, work,
+                        num_work, num_parts, O_part, LSE_part, static_cast<__nv_bfloat16*>(out), lse, status};
   const cudaStream_t st = (cudaStream_t)stream;
-  cudaError_t e = cudaFuncSetAttribute(mla_prefill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-  if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(mla_prefill_kernel)");
-  const unsigned grid = (unsigned)num_work * (unsigned)H;
-  mla_prefill_kernel<<<grid, kThreads, kSmem, st>>>(qn, qr, kn, kr, vm, p);
-  e = cudaGetLastError();
-  if (e != cudaSuccess) return cuda_fail(e, "launch mla_prefill_kernel");
-  if (num_parts > 0) {
-    mla_prefill_merge_kernel<<<grid, 256, 0, st>>>(p);
-    e = cudaGetLastError();
-    if (e != cudaSuccess) return cuda_fail(e, "launch mla_prefill_merge_kernel");
-  }
-  return MLA_OK;
+  return ctas == 1 ? launch_prefill<1>(qn, qr, kn, kr, vm, p, st) : launch_prefill<2>(qn, qr, kn, kr, vm, p, st);
 }

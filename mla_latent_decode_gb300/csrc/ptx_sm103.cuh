@@ -533,6 +533,65 @@ __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const void* tmap,
       "l"(tmap), "r"(x), "r"(y), "r"(bar_cluster)
       : "memory");
 }
+__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const void* tmap,
+                                                 uint32_t bar_cluster,
+                                                 int32_t x, int32_t y, int32_t z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global."
+      "mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(bar_cluster)
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_4d_pair(uint32_t dst, const void* tmap,
+                                                 uint32_t bar_cluster,
+                                                 int32_t x, int32_t y, int32_t z,
+                                                 int32_t w) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global."
+      "mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+      "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar_cluster)
+      : "memory");
+}
+// Minimum into a word of a CTA of the cluster.
+__device__ __forceinline__ void red_min_cluster_u32(uint32_t cluster_addr, uint32_t v) {
+  asm volatile("red.relaxed.cluster.shared::cluster.min.u32 [%0], %1;" ::"r"(cluster_addr),
+               "r"(v)
+               : "memory");
+}
+
+// Take over a cluster of this grid that has not started (a persistent CTA's next
+// work): the 16-byte answer arrives in shared memory, completing on `bar`; with
+// kAll at the same offsets in every CTA of the cluster.
+template <bool kAll>
+__device__ __forceinline__ void try_cancel(uint32_t answer, uint32_t bar) {
+  if constexpr (kAll)
+    asm volatile(
+        "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes."
+        "multicast::cluster::all.b128 [%0], [%1];" ::"r"(answer),
+        "r"(bar)
+        : "memory");
+  else
+    asm volatile(
+        "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 "
+        "[%0], [%1];" ::"r"(answer),
+        "r"(bar)
+        : "memory");
+}
+// The answer: blockIdx.x of the cluster's first CTA, or -1 when none was left.
+__device__ __forceinline__ int canceled_cta(uint32_t answer) {
+  int x;
+  asm volatile(
+      "{\n\t.reg .b128 h;\n\t.reg .pred p;\n\t"
+      "ld.shared.b128 h, [%1];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\t"
+      "mov.s32 %0, -1;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %0, h;\n\t}"
+      : "=r"(x)
+      : "r"(answer)
+      : "memory");
+  return x;
+}
+
 // 16-byte load from the shared memory of a CTA of the cluster.
 __device__ __forceinline__ uint4 ld_cluster_v4(uint32_t cluster_addr) {
   uint4 v;

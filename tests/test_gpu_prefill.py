@@ -84,9 +84,9 @@ def _reference(x, lq, lk, pre, causal, scale=SCALE):
     return tuple(torch.cat([o[i] for o in outs]) for i in range(4))
 
 
-def _run(x, lq, lk, pre, causal, scale=SCALE, plan=None, **more):
+def _run(x, lq, lk, pre, causal, scale=SCALE, plan=None, ctas=0, **more):
     H = x["q_nope"].shape[1]
-    work, parts = plan or mla.plan_prefill(lq, lk, H, prefix=pre, causal=causal)
+    work, parts = plan or mla.plan_prefill(lq, lk, H, prefix=pre, causal=causal, ctas=ctas)
     status = torch.zeros(1, dtype=torch.int32, device="cuda")
     prefix = None if pre is None else torch.tensor(pre, dtype=torch.int32, device="cuda")
     out, lse = mla.prefill(**x, cu_q=_cu(lq), cu_kv=_cu(lk), work=torch.from_numpy(work).cuda(), sm_scale=scale,
@@ -114,6 +114,7 @@ def _check(x, lq, lk, pre, causal, scale=SCALE, **more):
     return out, lse, parts
 
 
+@pytest.mark.parametrize("ctas", [1, 2])
 @pytest.mark.parametrize("lq,lk,pre,H,causal", [
     ([1], [1], None, 1, True),
     ([17], [17], None, 16, True),
@@ -127,15 +128,31 @@ def _check(x, lq, lk, pre, causal, scale=SCALE, **more):
     ([150, 70], [20, 0], [20, 5], 2, True),
     ([100, 260], [300, 129], None, 2, False),                          # in full
     ([1] * 40, list(range(1, 41)), None, 8, True),
+    ([512, 511, 1030], [512, 640, 1030], [0, 513, 700], 2, True),      # around a pair's block
 ])
-def test_matches_the_definition(lq, lk, pre, H, causal):
-    _check(_inputs(lq, lk, H), lq, lk, pre, causal)
+def test_matches_the_definition(lq, lk, pre, H, causal, ctas):
+    _check(_inputs(lq, lk, H), lq, lk, pre, causal, ctas=ctas)
 
 
+@pytest.mark.parametrize("ctas", [1, 2])
+def test_many_units_a_cta(ctas):
+    """CTAs take over units that have not started, with and without keys, cleaned values and parts."""
+    lens = [300, 1, 64, 129, 0, 513, 40, 257] * 4
+    ctx = [0, 700, 0, 128, 3, 0, 0, 1] * 4
+    pre = [0, 0, 64, 5, 0, 600, 40, 0] * 4
+    lk = [a + c for a, c in zip(lens, ctx)]
+    lk[7] = 0                                                          # rows that see nothing, between others
+    x = _inputs(lens, lk, 24, seed=2)
+    x["v"][500, 3, 7] = math.inf
+    x["v"][2000, 20, 100] = math.nan
+    _check(x, lens, lk, pre, True, ctas=ctas)
+
+
+@pytest.mark.parametrize("ctas", [1, 2])
 @pytest.mark.parametrize("lq,lk,H", [([200], [9000], 2), ([64, 300], [5000, 12000], 1), ([1], [20000], 3)])
-def test_keys_cut_into_parts(lq, lk, H):
+def test_keys_cut_into_parts(lq, lk, H, ctas):
     x = _inputs(lq, lk, H, seed=3, wide=False)
-    *_, parts = _check(x, lq, lk, None, True)
+    *_, parts = _check(x, lq, lk, None, True, ctas=ctas)
     assert parts > 1
 
 
@@ -145,13 +162,15 @@ def test_every_cut_is_the_same_sum():
     x = _inputs(lq, lk, H, seed=5)
     seen = set()
     for sms in (1, 4, 16, 64, 300):
-        plan = mla.plan_prefill(lq, lk, H, num_sms=sms)
-        _check(x, lq, lk, None, True, plan=plan)
-        seen.add(plan[1])
+        for ctas in (1, 2):
+            plan = mla.plan_prefill(lq, lk, H, num_sms=sms, ctas=ctas)
+            _check(x, lq, lk, None, True, plan=plan)
+            seen.add(plan[1])
     assert len(seen) > 1
 
 
-def test_large_scores_and_their_order():
+@pytest.mark.parametrize("ctas", [1, 2])
+def test_large_scores_and_their_order(ctas):
     """Maxima that rise through the sequence, fall, or sit on one key: the reference moves."""
     lq, lk, H = [300], [300], 3
     x = _inputs(lq, lk, H, seed=6, wide=False)
@@ -160,15 +179,16 @@ def test_large_scores_and_their_order():
     x["k_nope"][:, 1] = (x["k_nope"][:, 1].float() + ramp.flip(0)[:, None]).bfloat16()
     x["k_nope"][7, 2] = 30.0
     x["q_nope"] = x["q_nope"].abs()
-    _check(x, lq, lk, None, True)
+    _check(x, lq, lk, None, True, ctas=ctas)
 
 
+@pytest.mark.parametrize("ctas", [1, 2])
 @pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
-def test_keys_and_values_that_a_row_does_not_see(bad):
+def test_keys_and_values_that_a_row_does_not_see(bad, ctas):
     """A token's key and value reach the rows that see it and no other, whatever they hold."""
     lq, lk, pre, H = [200, 90, 40], [200, 350, 40], [0, 0, 40], 2
     x = _inputs(lq, lk, H, seed=7, spare=64, wide=False)
-    clean, _, _ = _run(x, lq, lk, pre, True)
+    clean, _, _ = _run(x, lq, lk, pre, True, ctas=ctas)
     x["v"][130, 0, 5] = bad            # sequence 0, seen from row 130 on
     x["v"][199, 1, 127] = bad          # its last token, seen by its last row
     x["v"][200 + 300, 1, 64] = bad     # sequence 1: context and drafts
@@ -176,7 +196,7 @@ def test_keys_and_values_that_a_row_does_not_see(bad):
     x["v"][sum(lk):] = math.nan        # behind the last sequence
     x["k_nope"][sum(lk):] = math.nan
     x["k_rope"][sum(lk):] = math.nan
-    out, _, _ = _check(x, lq, lk, pre, True)
+    out, _, _ = _check(x, lq, lk, pre, True, ctas=ctas)
     assert torch.equal(out[:130], clean[:130])
     assert torch.equal(out[290:330], clean[290:330])
 
@@ -204,10 +224,11 @@ def test_nothing_to_do():
     assert bool((out == 5.0).all())
 
 
-def test_bad_work_and_lengths_are_reported():
+@pytest.mark.parametrize("ctas", [1, 2])
+def test_bad_work_and_lengths_are_reported(ctas):
     lq = lk = [100, 30]
     x = _inputs(lq, lk, 2)
-    work, _ = mla.plan_prefill(lq, lk, 2)
+    work, _ = mla.plan_prefill(lq, lk, 2, ctas=ctas)
 
     def status_of(work, cu_q=_cu(lq), cu_kv=_cu(lk), num_parts=0):
         status = torch.zeros(1, dtype=torch.int32, device="cuda")
@@ -217,24 +238,25 @@ def test_bad_work_and_lengths_are_reported():
 
     assert status_of(work) == 0
     for column, value in ((0, 2), (0, -1), (1, 1), (1, -1), (2, 1), (2, -1), (3, 0), (3, 33), (5, 5), (5, -1),
-                          (6, 0), (6, 9)):
+                          (6, 0), (6, 9), (7, 128 * ctas)):
         bad = work.copy()
-        bad[0, column] = value
+        bad[0, ..., column] = value
         assert status_of(bad) == mla.STATUS_BAD_WORK, (column, value)
     bad = work.copy()
-    bad[0, 2:5] = 0, 2, 1
-    assert status_of(bad, num_parts=2) == mla.STATUS_BAD_WORK
+    bad[0, ..., 2:5] = 0, 2, 1
+    assert status_of(bad, num_parts=2 * ctas) == mla.STATUS_BAD_WORK
     assert status_of(work, cu_q=_cu([100, 31])) == mla.STATUS_BAD_LENGTH
     assert status_of(work, cu_kv=_cu([131, 0])) == mla.STATUS_BAD_LENGTH
     assert status_of(work, cu_kv=_cu([-1, 50])) == mla.STATUS_BAD_LENGTH
 
 
-def test_captured_and_on_another_stream():
+@pytest.mark.parametrize("ctas", [1, 2])
+def test_captured_and_on_another_stream(ctas):
     lq, lk, H = [300, 20], [4000, 20], 2
     x = _inputs(lq, lk, H, seed=11)
-    want, want_lse, parts = _run(x, lq, lk, None, True)
+    want, want_lse, parts = _run(x, lq, lk, None, True, ctas=ctas)
     assert parts > 1
-    work, parts = mla.plan_prefill(lq, lk, H)
+    work, parts = mla.plan_prefill(lq, lk, H, ctas=ctas)
     work, cu_q, cu_kv = torch.from_numpy(work).cuda(), _cu(lq), _cu(lk)
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
