@@ -674,9 +674,9 @@ int mla_lse_combine_bf16_parts(const void* O_part, const float* LSE_part,
  *            that no entry names are not written, an entry that fits no sequence
  *            sets MLA_STATUS_BAD_WORK and does nothing, lengths that leave the
  *            arrays set MLA_STATUS_BAD_LENGTH and their sequence is not computed.
- *   O_part   fp32 [num_parts, H, 256, 128] (16-B aligned), LSE_part fp32
+ *   O_part   fp32 [num_parts, H, 256, 128] (32-B aligned), LSE_part fp32
  *            [num_parts, H, 256]: workspace, may be NULL when num_parts is 0
- *   out      bf16 [Tq, H, 128] contiguous, 16-B aligned;  lse fp32 [Tq, H] or
+ *   out      bf16 [Tq, H, 128] contiguous, 32-B aligned;  lse fp32 [Tq, H] or
  *            NULL.  Rows past the last sequence are not written.
  * Probabilities are rounded to bf16 (2^-8) before the product with v; sums and
  * statistics are fp32.  H in [1, 65535], sm_scale finite and > 0.  One launch,

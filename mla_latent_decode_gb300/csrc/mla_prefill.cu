@@ -224,11 +224,6 @@ __device__ __forceinline__ uint32_t lead_bar(uint64_t* bar) {
   else return mapa(smem_u32(bar), 0);
 }
 template <int kCtas>
-__device__ __forceinline__ void expect_at_lead(uint64_t* bar, uint32_t rank, uint32_t bytes) {
-  if (kCtas == 1 || rank == 0) mbar_arrive_expect_tx(smem_u32(bar), bytes);
-  else mbar_arrive_expect_tx_cluster(lead_bar<kCtas>(bar), bytes);
-}
-template <int kCtas>
 __device__ __forceinline__ void load_3d(uint32_t dst, const CUtensorMap* m, uint32_t bar, int x, int y, int z) {
   if constexpr (kCtas == 1) tma_load_3d(dst, m, bar, x, y, z);
   else tma_load_3d_pair(dst, m, bar, x, y, z);
@@ -345,7 +340,8 @@ __device__ __forceinline__ void produce(uint8_t* base, Ctl& c, const PrefillPara
             if (n[g] <= j0) continue;
             if (qs[g] > 0 && !(ok = wait_bar<kCtas>(&c.qfree[g], (qs[g] - 1) & 1, &c.abort_flag))) break;
             ++qs[g];
-            if (lane == 0) expect_at_lead<kCtas>(&c.q[g], rank, 3 * kBox);
+            // (of a pair, the first CTA expects both CTAs' bytes)
+            if (lane == 0 && rank == 0) mbar_arrive_expect_tx(smem_u32(&c.q[g]), 3 * kBox * kCtas);
             __syncwarp();
             if (lane < 3) {
               const int row = q0 + row0 + (g * kCtas + (int)rank) * kRows;
@@ -368,7 +364,7 @@ __device__ __forceinline__ void produce(uint8_t* base, Ctl& c, const PrefillPara
             if (i == 3) mbar_arrive_expect_tx(raw, 2 * kStageBytes);
             tma_load_4d(dst, v, raw, 0, tok + (i - 3) * 64, (int)rank, h);
           } else {
-            expect_at_lead<kCtas>(&c.full[st], rank, kStageBytes);
+            if (rank == 0) mbar_arrive_expect_tx(smem_u32(&c.full[st]), kStageBytes * kCtas);
             const uint32_t bar = lead_bar<kCtas>(&c.full[st]);
             if (i < 2) load_3d<kCtas>(dst, kn, bar, i * 64, h, tok + half);
             else if (i == 2) load_3d<kCtas>(dst, kr, bar, 0, 0, tok + half);
@@ -519,8 +515,9 @@ __device__ __forceinline__ void clean_values(uint8_t* base, Ctl& c, const Prefil
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
-        if (rank == 0) mbar_arrive(smem_u32(&c.full[st]));
-        else mbar_arrive_cluster(lead_bar<kCtas>(&c.full[st]));
+        if (kCtas == 1) mbar_arrive(smem_u32(&c.full[st]));
+        else if (rank == 0) mbar_arrive_expect_tx(smem_u32(&c.full[st]), 4);
+        else st_async_u32(mapa(smem_u32(&c.note), 0), 0, lead_bar<kCtas>(&c.full[st]));
       }
     }
     if (!ok) break;
@@ -650,39 +647,38 @@ __device__ __forceinline__ void softmax_rows(Ctl& c, const PrefillParams& p, uin
     // notes of this unit: tokens that the row sees get their values back
     const uint32_t tag = tag_of(units.nth), reach = tag + (uint32_t)min(max(seen - unseen, 0), 1 << kOffsetBits);
     const bool odd = cleaned && *reinterpret_cast<volatile uint32_t*>(&c.any_odd) == tag;
-#pragma unroll 1
-    for (int b = 0; b < 4; ++b) {
-      uint32_t o[32];
-      __syncwarp();
-      if (tiles > 0) {
-        tmem_ld32(o_at + 32 * b, o);
-        tmem_wait_ld();
-      } else {
+    float o[kKeys];
+    if (tiles > 0) {
 #pragma unroll
-        for (int e = 0; e < 32; ++e) o[e] = 0;
+      for (int b = 0; b < 4; ++b) tmem_ld32(o_at + 32 * b, *reinterpret_cast<uint32_t(*)[32]>(&o[32 * b]));
+      tmem_wait_ld();
+    } else {
+#pragma unroll
+      for (int e = 0; e < kKeys; ++e) o[e] = 0.f;
+    }
+#pragma unroll
+    for (int e = 0; e < kKeys; ++e) o[e] = l == 0.f ? 0.f : o[e] * inv;
+    if (odd) {
+#pragma unroll
+      for (int e = 0; e < kKeys; ++e) {
+        if (c.odd[0][e] < reach) o[e] += NAN;
+        if (c.odd[1][e] < reach) o[e] += INFINITY;
+        if (c.odd[2][e] < reach) o[e] -= INFINITY;
       }
-      float f[32];
+    }
+    if (exists && whole) {
+      __nv_bfloat16* dst = p.out + row * MLA_V_HEAD_DIM;
 #pragma unroll
-      for (int e = 0; e < 32; ++e) f[e] = l == 0.f ? 0.f : __uint_as_float(o[e]) * inv;
-      if (odd) {
+      for (int e = 0; e < kKeys; e += 16) {
+        uint32_t w[8];
 #pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          if (c.odd[0][32 * b + e] < reach) f[e] += NAN;
-          if (c.odd[1][32 * b + e] < reach) f[e] += INFINITY;
-          if (c.odd[2][32 * b + e] < reach) f[e] -= INFINITY;
-        }
+        for (int x = 0; x < 8; ++x) w[x] = pack_bf16(o[e + 2 * x], o[e + 2 * x + 1]);
+        st_global_v8(dst + e, w);
       }
-      if (exists && whole) {
-        uint4* dst = reinterpret_cast<uint4*>(p.out + row * MLA_V_HEAD_DIM + 32 * b);
+    } else if (exists) {
+      float* dst = p.O_part + row * MLA_V_HEAD_DIM;
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          dst[e] = make_uint4(pack_bf16(f[8 * e], f[8 * e + 1]), pack_bf16(f[8 * e + 2], f[8 * e + 3]),
-                              pack_bf16(f[8 * e + 4], f[8 * e + 5]), pack_bf16(f[8 * e + 6], f[8 * e + 7]));
-      } else if (exists) {
-        float4* dst = reinterpret_cast<float4*>(p.O_part + row * MLA_V_HEAD_DIM + 32 * b);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) dst[e] = make_float4(f[4 * e], f[4 * e + 1], f[4 * e + 2], f[4 * e + 3]);
-      }
+      for (int e = 0; e < kKeys; e += 8) st_global_v8(dst + e, *reinterpret_cast<const uint32_t(*)[8]>(&o[e]));
     }
     if (exists) {
       if (!whole) p.LSE_part[row] = lse;
@@ -714,7 +710,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     c.abort_flag = 0;
     c.any_odd = ~0u;
     for (int g = 0; g < 2; ++g) {
-      mbar_init(smem_u32(&c.q[g]), kCtas);
+      mbar_init(smem_u32(&c.q[g]), 1);
       mbar_init(smem_u32(&c.qfree[g]), 1);
       mbar_init(smem_u32(&c.s[g]), 1);
       mbar_init(smem_u32(&c.p[g]), 4);
@@ -723,7 +719,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(&c.unit_empty[g]), 12);  // TMA, MMA, 2 cleaning, 8 softmax warps
     }
     for (int i = 0; i < 16; ++i) {
-      mbar_init(smem_u32(&c.full[i]), kCtas);
+      mbar_init(smem_u32(&c.full[i]), 1);
       mbar_init(smem_u32(&c.empty[i]), 1);
     }
     for (int i = 0; i < kRaw; ++i) mbar_init(smem_u32(&c.raw[i]), 1);
@@ -920,11 +916,11 @@ extern "C" int mla_prefill(const void* q_nope, int64_t qn_token_stride, int64_t 
       (Tk > 0 && (off_vector(k_nope, Tk, H, kn_token_stride, kn_head_stride) ||
                   off_vector(v, Tk, H, v_token_stride, v_head_stride) ||
                   off_vector(k_rope, Tk, 1, kr_token_stride, kRope))) ||
-      !aligned(out, 16) || (num_parts > 0 && (!aligned(O_part, 16) || !aligned(LSE_part, 4))) ||
+      !aligned(out, 32) || (num_parts > 0 && (!aligned(O_part, 32) || !aligned(LSE_part, 4))) ||
       !aligned(cu_q, 4) || !aligned(cu_kv, 4) || (prefix && !aligned(prefix, 4)) || !aligned(work, 4) ||
       (lse && !aligned(lse, 4)) || (status && !aligned(status, 4)))
-    return fail(MLA_ERR_MISALIGNED, "mla_prefill: queries, keys, values, out and O_part need 16-B alignment "
-                "(strides a multiple of 8 elements), the other arrays 4-B");
+    return fail(MLA_ERR_MISALIGNED, "mla_prefill: queries, keys and values need 16-B alignment (strides a "
+                "multiple of 8 elements), out and O_part 32-B, the other arrays 4-B");
   if (Tk == 0) {  // no keys: the maps are never read through
     k_nope = k_rope = v = out;
     kn_token_stride = kn_head_stride = v_token_stride = v_head_stride = kNope;
