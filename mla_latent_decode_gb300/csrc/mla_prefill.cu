@@ -27,6 +27,7 @@
 //                    V in two (64 tokens each); in a pair a CTA's stage is half as
 //                    large, its half of the tokens (K) or of the dims (V)
 //   warp 9           MMA issue (one lane; of a pair's first CTA)
+//   warp 11          TMA: Q
 //   warp 10          the next unit: the grid has a CTA (pair) per unit, and running
 //                    ones take over those that have not started, in launch order, so
 //                    the work list is dealt out as SMs come free and a unit's loads
@@ -56,15 +57,39 @@ constexpr int kSlot = 256;           // rows of a workspace slot
 constexpr int kKeys = 128;           // tokens of a key tile
 constexpr int kBox = 128 * 128;      // 16 KB: 64 dims of 128 rows
 constexpr int kRing = 8 * kBox;
+constexpr int kVBytes = 2 * kBox;    // V of a tile
 constexpr int kRaw = 4;              // V tiles that may wait for cleaning (the ring holds parts of 3)
 constexpr int kThreads = 512;
-constexpr int kWarpTma = 8, kWarpMma = 9, kWarpNext = 10, kWarpClean = 12;
+constexpr int kWarpTma = 8, kWarpMma = 9, kWarpNext = 10, kWarpQ = 11, kWarpClean = 12;
 // 512 threads launch with 128 registers (65536 in all): 256 x 200 + 256 x 56.
 constexpr int kRegsSoftmax = 200, kRegsOther = 56;
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kRise = 8.f;         // log2 of the rise that rescales O
 constexpr int kEntry = 8;            // int32 of a work entry
 constexpr int kOffsetBits = 9;       // of a note on a cleaned value: its token past the first unseen one
+
+// The ring's pieces, each with its barriers: on one CTA a box of 16 KB (64 dims of
+// K or 64 tokens of V); in a pair a CTA's half of a tile's K (24 KB) or V (16 KB).
+template <int kCtas>
+struct Ring {
+  static constexpr int kK = kCtas == 1 ? 3 : 1, kV = kCtas == 1 ? 2 : 1;  // pieces of a tile
+  static constexpr int kTile = kK + kV, kAll = kCtas == 1 ? 8 : 6;
+  static constexpr int kHalfBox = kBox / kCtas;                           // 64 dims of a CTA's tokens of K
+  static __device__ __forceinline__ uint32_t at(uint32_t piece) {
+    return kCtas == 1 ? piece * kBox : (piece >> 1) * (5 * kHalfBox) + (piece & 1) * (3 * kHalfBox);
+  }
+};
+// Where a role stands in the ring.
+template <int kCtas>
+struct Cursor {
+  uint32_t piece, phase;
+  __device__ __forceinline__ void next() {
+    if (++piece == Ring<kCtas>::kAll) piece = 0, phase ^= 1;
+  }
+  __device__ __forceinline__ void skip(int n) {
+    if ((piece += n) >= Ring<kCtas>::kAll) piece -= Ring<kCtas>::kAll, phase ^= 1;
+  }
+};
 
 struct PrefillParams {
   const int32_t* cu_q;
@@ -96,9 +121,9 @@ struct Unit {
 
 struct Ctl {
   uint64_t q[2], qfree[2];       // Q of a row tile has landed; has been used up
-  uint64_t full[16], empty[16];  // ring
+  uint64_t full[8], empty[8];    // ring
   uint64_t s[2];                 // S of a row tile is in TMEM
-  uint64_t p[2];                 // its P is, and S has been read
+  uint64_t p[2][2];              // its P of the tile's first and last 64 keys is, S has been read
   uint64_t o[2];                 // O is complete
   uint64_t raw[kRaw];            // V of a tile to be cleaned has landed (tiles take turns)
   uint64_t cleaned;              // all of a unit's are clean
@@ -138,9 +163,9 @@ __device__ __forceinline__ bool find_unit(const PrefillParams& p, int x, Unit& u
     if (p.status) atomicOr(p.status, MLA_STATUS_BAD_WORK);
     return false;
   }
-  const int64_t local = x - (int64_t)g0 * p.H;
-  u.h = (int)(local / nb);
-  e = p.work + (g0 + local % nb) * kStride;
+  const uint32_t local = (uint32_t)(x - (int64_t)g0 * p.H);  // below nb * H <= 2^30
+  u.h = (int)(local / (uint32_t)nb);
+  e = p.work + (int64_t)(g0 + (int)(local % (uint32_t)nb)) * kStride;
   const int seq = e[0], part = e[2], parts = e[3], slot = e[4];
   const int64_t row0 = (int64_t)e[1] * kBlock;
   if (u.h >= p.H || seq < 0 || seq >= p.N || e[1] < 0 || parts < 1 || parts > MLA_PREFILL_MAX_PARTS ||
@@ -167,9 +192,9 @@ __device__ __forceinline__ bool find_unit(const PrefillParams& p, int x, Unit& u
     return (sees(p, u.lq, u.lk, prefix, u.row0 + min(u.rows, end) - 1) + kKeys - 1) / kKeys;
   };
   const int n0 = tiles(0, kBlock / 2), n1 = tiles(kBlock / 2, kBlock);
-  const int64_t all = max(n0, n1);
-  u.j0 = (int)(all * part / parts);
-  u.j1 = (int)(all * (part + 1) / parts);
+  const uint32_t all = (uint32_t)max(n0, n1);  // at most 2^24, parts at most 32
+  u.j0 = (int)(all * (uint32_t)part / (uint32_t)parts);
+  u.j1 = (int)(all * (uint32_t)(part + 1) / (uint32_t)parts);
   u.n0 = min(n0, u.j1);
   u.n1 = min(n1, u.j1);
   u.unseen = sees(p, u.lq, u.lk, prefix, u.row0);
@@ -212,10 +237,29 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 
 
 // ---- the two forms' instructions
-template <int kCtas>
+// Waits are inlined (a kernel that rebalances its registers makes no calls), so
+// their code is kept short: the kernel's loops have to fit the instruction cache.
+// A CTA's own barriers are waited for at CTA scope, also where tensor memory or TMA
+// data of the pair is behind them: at cluster scope a wait takes about 170 cycles
+// more.  kWide: data that the other CTA's threads have written is behind it.
+__device__ __forceinline__ uint32_t globaltimer_lo() {
+  uint32_t t;
+  asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t));
+  return t;
+}
+template <bool kWide = false>
 __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatile int* abort) {
-  if constexpr (kCtas == 1) return mbar_wait_cta(smem_u32(bar), parity, abort);
-  else return mbar_wait(smem_u32(bar), parity, abort);
+  const uint32_t at = smem_u32(bar);
+  uint32_t t0 = 0;
+#pragma unroll 1
+  while (!(kWide ? mbar_try_wait_suspend(at, parity, kSuspendNs)
+                 : mbar_try_wait_suspend_cta(at, parity, kSuspendNs))) {
+    if (*abort) return false;
+    const uint32_t now = globaltimer_lo() | 1;
+    if (t0 == 0) t0 = now;
+    if (now - t0 > (uint32_t)kWaitNs) return false;
+  }
+  return true;
 }
 // A barrier of the pair's first CTA, which issues the MMAs.
 template <int kCtas>
@@ -246,6 +290,10 @@ __device__ __forceinline__ void mma_pv(uint32_t d, uint32_t a, uint64_t b, uint3
   if constexpr (kCtas == 1) mma_ts(d, a, b, idesc, acc);
   else mma_ts_pair(d, a, b, idesc, acc);
 }
+// A descriptor some 16-byte units on (the address field never carries out).
+__device__ __forceinline__ uint64_t plus(uint64_t desc, uint32_t n) {
+  return (desc & 0xffffffff00000000ull) | (uint32_t)((uint32_t)desc + n);
+}
 // On the barrier of every CTA of the unit.
 template <int kCtas>
 __device__ __forceinline__ void commit(uint64_t* bar) {
@@ -268,7 +316,7 @@ struct Units {
   uint32_t nth = 0;
   __device__ __forceinline__ explicit Units(Ctl& ctl) : c(ctl) {}
   __device__ __forceinline__ const Unit* next(bool& ok) {
-    ok = wait_bar<kCtas>(&c.unit_full[nth & 1], nth >> 1 & 1, &c.abort_flag);
+    ok = wait_bar(&c.unit_full[nth & 1], nth >> 1 & 1, &c.abort_flag);
     const Unit* u = &c.unit[nth & 1];
     return ok && u->more ? u : nullptr;
   }
@@ -298,17 +346,17 @@ __device__ __forceinline__ void feed(Ctl& c, const PrefillParams& p, uint32_t ra
       if (x < 0) return;
       ++nth;
       // one ahead: the unit before this one has ended
-      if (nth >= 2 && !(ok = wait_bar<kCtas>(&c.unit_empty[nth & 1], (nth >> 1) - 1 & 1, &c.abort_flag))) break;
+      if (nth >= 2 && !(ok = wait_bar(&c.unit_empty[nth & 1], (nth >> 1) - 1 & 1, &c.abort_flag))) break;
     }
     mbar_arrive_expect_tx(smem_u32(&c.answer_full), 16);
     if (rank == 0) {
       // every CTA has armed its barrier and read the answer before
-      if (kCtas == 2 && !(ok = wait_bar<kCtas>(&c.answer_free, asked & 1, &c.abort_flag))) break;
+      if (kCtas == 2 && !(ok = wait_bar<true>(&c.answer_free, asked & 1, &c.abort_flag))) break;
       try_cancel<kCtas == 2>(smem_u32(c.answer), smem_u32(&c.answer_full));
     } else {
       mbar_arrive_cluster(mapa(smem_u32(&c.answer_free), 0));
     }
-    if (!(ok = wait_bar<kCtas>(&c.answer_full, asked & 1, &c.abort_flag))) break;
+    if (!(ok = wait_bar<kCtas == 2>(&c.answer_full, asked & 1, &c.abort_flag))) break;
     ++asked;
     x = canceled_cta(smem_u32(c.answer));
     // the answer has been read before the next one is written
@@ -318,57 +366,43 @@ __device__ __forceinline__ void feed(Ctl& c, const PrefillParams& p, uint32_t ra
   give_up<kCtas>(c, p, rank);
 }
 
-// Ring positions of a unit's tile t: K at 5 t .. 5 t + 2, V at 5 t + 3, 5 t + 4.
 template <int kCtas>
-__device__ __forceinline__ void produce(uint8_t* base, Ctl& c, const PrefillParams& p, const CUtensorMap* qn,
-                                        const CUtensorMap* qr, const CUtensorMap* kn, const CUtensorMap* kr,
-                                        const CUtensorMap* v, uint32_t rank, int lane) {
-  constexpr int kStageBytes = kBox / kCtas, kStages = kRing / kStageBytes;
+__device__ __forceinline__ void produce(uint8_t* base, Ctl& c, const PrefillParams& p, const CUtensorMap* kn,
+                                        const CUtensorMap* kr, const CUtensorMap* v, uint32_t rank, int lane) {
+  using R = Ring<kCtas>;
   Units<kCtas> units(c);
   bool ok = true;
-  uint32_t pos = 0, cleans = 0, qs[2] = {0, 0};
+  uint32_t pos = 0, cleans = 0;
   while (const Unit* up = units.next(ok)) {
-    const int h = up->h, row0 = up->row0, q0 = up->q0, k0 = up->k0, j0 = up->j0, j1 = up->j1, clean0 = up->clean0;
-    const int n[2] = {up->n0, up->n1};
+    const int h = up->h, k0 = up->k0, j0 = up->j0, j1 = up->j1, clean0 = up->clean0;
+#pragma unroll 1
     for (int j = j0; j < j1 && ok; ++j) {
       const int tok = k0 + j * kKeys;
-      for (int i = 0; i < 5 && ok; ++i, ++pos) {
-        if (j == j0 && i == 3) {
-          // Q after the first keys: three boxes for each row tile, one lane each
-#pragma unroll
-          for (int g = 0; g < 2; ++g) {
-            if (n[g] <= j0) continue;
-            if (qs[g] > 0 && !(ok = wait_bar<kCtas>(&c.qfree[g], (qs[g] - 1) & 1, &c.abort_flag))) break;
-            ++qs[g];
-            // (of a pair, the first CTA expects both CTAs' bytes)
-            if (lane == 0 && rank == 0) mbar_arrive_expect_tx(smem_u32(&c.q[g]), 3 * kBox * kCtas);
-            __syncwarp();
-            if (lane < 3) {
-              const int row = q0 + row0 + (g * kCtas + (int)rank) * kRows;
-              const uint32_t dst = smem_u32(base + (3 * g + lane) * kBox), bar = lead_bar<kCtas>(&c.q[g]);
-              if (lane < 2) load_3d<kCtas>(dst, qn, bar, lane * 64, h, row);
-              else load_3d<kCtas>(dst, qr, bar, 0, h, row);
-            }
-            __syncwarp();
-          }
-          if (!ok) break;
-        }
-        const uint32_t st = pos % kStages, use = pos / kStages;
-        if (use > 0 && !(ok = wait_bar<kCtas>(&c.empty[st], (use - 1) & 1, &c.abort_flag))) break;
-        if (lane == (int)(pos & 3)) {
-          const uint32_t dst = smem_u32(base + 6 * kBox + st * kStageBytes);
-          const int half = (int)rank * (kKeys / kCtas);  // a pair's CTA: tokens (K) from here
-          if (i >= 3 && j >= clean0) {
-            // its stage is full once it is clean
-            const uint32_t nth = cleans + (j - clean0), raw = smem_u32(&c.raw[nth % kRaw]);
-            if (i == 3) mbar_arrive_expect_tx(raw, 2 * kStageBytes);
-            tma_load_4d(dst, v, raw, 0, tok + (i - 3) * 64, (int)rank, h);
+#pragma unroll 1
+      for (int i = 0; i < R::kTile && ok; ++i, ++pos) {
+        const uint32_t piece = pos % R::kAll, use = pos / R::kAll;
+        if (use > 0 && !(ok = wait_bar(&c.empty[piece], (use - 1) & 1, &c.abort_flag))) break;
+        const uint32_t dst = smem_u32(base + 6 * kBox + R::at(piece));
+        if (i < R::kK) {
+          const int first = tok + (int)rank * (kKeys / kCtas);  // a pair's CTA: its half of the tokens
+          if (lane == 0 && rank == 0) mbar_arrive_expect_tx(smem_u32(&c.full[piece]), 3 * kBox / R::kK);
+          __syncwarp();
+          const uint32_t bar = lead_bar<kCtas>(&c.full[piece]);
+          // a box a lane: 64 dims of k_nope, 64 more, k_rope
+          const int box = kCtas == 1 ? i : lane;
+          if (kCtas == 1 ? lane == 0 : lane < 3)
+            load_3d<kCtas>(dst + (kCtas == 1 ? 0 : lane * R::kHalfBox), box < 2 ? kn : kr, bar, box < 2 ? box * 64 : 0,
+                           box < 2 ? h : 0, first);
+        } else if (lane == 0) {
+          const int first = tok + (i - R::kK) * 64;             // a pair's CTA: its half of the dims
+          if (j >= clean0) {
+            // its piece is full once it is clean
+            const uint32_t raw = smem_u32(&c.raw[(cleans + (j - clean0)) % kRaw]);
+            if (i == R::kK) mbar_arrive_expect_tx(raw, kVBytes / kCtas);
+            tma_load_4d(dst, v, raw, 0, first, (int)rank, h);
           } else {
-            if (rank == 0) mbar_arrive_expect_tx(smem_u32(&c.full[st]), kStageBytes * kCtas);
-            const uint32_t bar = lead_bar<kCtas>(&c.full[st]);
-            if (i < 2) load_3d<kCtas>(dst, kn, bar, i * 64, h, tok + half);
-            else if (i == 2) load_3d<kCtas>(dst, kr, bar, 0, 0, tok + half);
-            else load_4d<kCtas>(dst, v, bar, 0, tok + (i - 3) * 64, (int)rank, h);
+            if (rank == 0) mbar_arrive_expect_tx(smem_u32(&c.full[piece]), kVBytes / R::kV);
+            load_4d<kCtas>(dst, v, lead_bar<kCtas>(&c.full[piece]), 0, first, (int)rank, h);
           }
         }
         __syncwarp();
@@ -384,124 +418,189 @@ __device__ __forceinline__ void produce(uint8_t* base, Ctl& c, const PrefillPara
   // one, the MMAs have used them all).
   if (!ok) {
     int never = 0;
-    for (int g = 0; g < 2; ++g)
-      if (rank == 0 && qs[g] > 0) wait_bar<kCtas>(&c.q[g], (qs[g] - 1) & 1, &never);
-    for (uint32_t k = pos > (uint32_t)kStages ? pos - kStages : 0; rank == 0 && k < pos; ++k)
-      wait_bar<kCtas>(&c.full[k % kStages], (k / kStages) & 1, &never);
+    for (uint32_t k = pos > (uint32_t)R::kAll ? pos - R::kAll : 0; rank == 0 && k < pos; ++k)
+      wait_bar(&c.full[k % R::kAll], (k / R::kAll) & 1, &never);
   }
 }
 
+// Q of both row tiles, as soon as the unit before has used its own up: three boxes
+// for each, one lane each.
 template <int kCtas>
-__device__ __forceinline__ void issue_mmas(uint8_t* base, Ctl& c, const PrefillParams& p, uint32_t tmem) {
-  constexpr int kStageBytes = kBox / kCtas, kStages = kRing / kStageBytes;
+__device__ __forceinline__ void load_queries(uint8_t* base, Ctl& c, const PrefillParams& p, const CUtensorMap* qn,
+                                             const CUtensorMap* qr, uint32_t rank, int lane) {
+  Units<kCtas> units(c);
+  bool ok = true;
+  uint32_t uses[2] = {0, 0};
+  while (const Unit* u = units.next(ok)) {
+    const int h = u->h, row0 = u->q0 + u->row0, j0 = u->j0;
+    const int n[2] = {u->n0, u->n1};
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+      if (n[g] <= j0) continue;
+      if (uses[g] > 0) ok = ok && wait_bar(&c.qfree[g], (uses[g] - 1) & 1, &c.abort_flag);
+      if (!ok) break;
+      ++uses[g];
+      // (of a pair, the first CTA expects both CTAs' bytes)
+      if (lane == 0 && rank == 0) mbar_arrive_expect_tx(smem_u32(&c.q[g]), 3 * kBox * kCtas);
+      __syncwarp();
+      if (lane < 3)
+        load_3d<kCtas>(smem_u32(base + (3 * g + lane) * kBox), lane < 2 ? qn : qr, lead_bar<kCtas>(&c.q[g]),
+                       lane < 2 ? lane * 64 : 0, h, row0 + (g * kCtas + (int)rank) * kRows);
+    }
+    if (!ok) break;
+    __syncwarp();
+    if (lane == 0) units.release(); else units.skip();
+  }
+  if (!ok && lane == 0) give_up<kCtas>(c, p, rank);
+  // After an abort: every load issued has landed before the CTA may exit.
+  if (!ok && rank == 0) {
+    int never = 0;
+    for (int g = 0; g < 2; ++g)
+      if (uses[g] > 0) wait_bar(&c.q[g], (uses[g] - 1) & 1, &never);
+  }
+}
+
+// The whole warp runs the loop, so that what the MMAs take stays in uniform
+// registers; one lane issues.
+template <int kCtas>
+__device__ __forceinline__ void issue_mmas(uint8_t* base, Ctl& c, const PrefillParams& p, uint32_t tmem, int lane) {
+  using R = Ring<kCtas>;
   const uint64_t qd = sdesc_sw128(smem_u32(base), 16, 1024);
   const uint64_t kd = sdesc_sw128(smem_u32(base + 6 * kBox), 16, 1024);
   // V: MN-major, the next 64 dims 8 KB (LBO) on, the next 8 tokens 1 KB (SBO) on,
   // the next 16 tokens 2 KB; P: 16 tokens in 8 columns
   const uint64_t vd = sdesc_sw128(smem_u32(base + 6 * kBox), kBox / 2, 1024);
+  const bool lead = elect_one();
   bool ok = true;
   const auto wait = [&](uint64_t* bar, uint32_t parity) {
-    ok = ok && wait_bar<kCtas>(bar, parity, &c.abort_flag);
+    ok = ok && __all_sync(~0u, wait_bar(bar, parity, &c.abort_flag));
     return ok;
   };
   Units<kCtas> units(c);
-  uint32_t at = 0;                              // ring position of K(t)
-  uint32_t ps0 = 0, ps1 = 0, qs0 = 0, qs1 = 0;  // tiles and units of each row tile so far
+  Cursor<kCtas> kc{0, 0}, vc{R::kK, 0};         // K(t) and V(t - 1)
+  uint32_t ps[2] = {0, 0}, qs[2] = {0, 0};      // tiles and units of each row tile so far
   while (const Unit* u = units.next(ok)) {
-    const int a0 = u->n0 - u->j0, a1 = u->n1 - u->j0, tiles = u->j1 - u->j0;
+    const int j0 = __shfl_sync(~0u, u->j0, 0), tiles = __shfl_sync(~0u, u->j1, 0) - j0;
+    const int a[2] = {__shfl_sync(~0u, u->n0, 0) - j0, __shfl_sync(~0u, u->n1, 0) - j0};
+    const int clean = kCtas == 1 ? 0x7fffffff : __shfl_sync(~0u, u->clean0, 0) - j0;
+#pragma unroll 1
     for (int t = 0; t <= tiles && ok; ++t) {
-      const uint32_t kpos = at, vpos = kpos - 2;  // of K(t) and V(t - 1)
-#pragma unroll 1
-      for (int g = 0; g < 2 && ok; ++g) {
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
         const uint32_t s = tmem + g * kKeys, o = tmem + (2 + g) * kKeys;
-        const int a = g ? a1 : a0;
-        if (t > 0 && t - 1 < a) {
-          if (!wait(&c.p[g], ((g ? ps1 : ps0) + t - 1) & 1)) break;
-#pragma unroll 1
-          for (int i = 0; i < 2; ++i) {
-            const uint32_t st = (vpos + i) % kStages;
-            if (!wait(&c.full[st], (vpos + i) / kStages & 1)) break;
-            tc_fence_after();
-            const uint64_t b = vd + st * (kStageBytes >> 4);
+        if (t > 0 && t - 1 < a[g]) {
+          Cursor<kCtas> at = vc;
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              mma_pv<kCtas>(o, s + (4 * i + k) * 8, b + 128 * k, (t > 1 || i || k) ? 1u : 0u);
-            if (g || t - 1 >= a1) commit<kCtas>(&c.empty[st]);
+          for (int i = 0; i < 2; ++i) {  // 64 tokens
+            if ((R::kV == 2 || i == 0) && (g == 0 || t - 1 >= a[0])) {
+              if (!wait(&c.full[at.piece], at.phase)) break;
+              // cleaned by the other CTA's threads, too
+              if (kCtas == 2 && t - 1 >= clean) fence_cluster();
+            }
+            if (!wait(&c.p[g][i], (ps[g] + t - 1) & 1)) break;
+            tc_fence_after();
+            if (lead) {
+              const uint64_t b = plus(vd, (R::at(at.piece) + (R::kV == 1 ? i * R::kHalfBox : 0)) >> 4);
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                mma_pv<kCtas>(o, s + (4 * i + k) * 8, plus(b, 128 * k), (t > 1 || i || k) ? 1u : 0u);
+              if ((R::kV == 2 || i == 1) && (g || t - 1 >= a[1])) commit<kCtas>(&c.empty[at.piece]);
+            }
+            if (R::kV == 2) at.next();
           }
           if (!ok) break;
-          if (t == a) commit<kCtas>(&c.o[g]);
+          if (lead && t == a[g]) commit<kCtas>(&c.o[g]);
         }
-        if (t < a) {
-          if (t == 0 && !wait(&c.q[g], (g ? qs1 : qs0) & 1)) break;
-#pragma unroll 1
-          for (int i = 0; i < 3; ++i) {
-            const uint32_t st = (kpos + i) % kStages;
-            if (!wait(&c.full[st], (kpos + i) / kStages & 1)) break;
-            tc_fence_after();
-            const uint64_t q = qd + (3 * g + i) * (kBox >> 4), b = kd + st * (kStageBytes >> 4);
+        if (t < a[g]) {
+          if (t == 0 && !wait(&c.q[g], qs[g] & 1)) break;
+          Cursor<kCtas> at = kc;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) mma_qk<kCtas>(s, q + 2 * k, b + 2 * k, (i || k) ? 1u : 0u);
-            if (g || t >= a1) commit<kCtas>(&c.empty[st]);
+          for (int i = 0; i < R::kK; ++i, at.next()) {
+            if ((g == 0 || t >= a[0]) && !wait(&c.full[at.piece], at.phase)) break;
+            if (lead) {
+              const uint64_t q = plus(qd, (3 * g + i) * (kBox >> 4)), b = plus(kd, R::at(at.piece) >> 4);
+#pragma unroll
+              for (int k = 0; k < 12 / R::kK; ++k)
+                mma_qk<kCtas>(s, plus(q, k / 4 * (kBox >> 4) + 2 * (k % 4)),
+                              plus(b, k / 4 * (R::kHalfBox >> 4) + 2 * (k % 4)), (i || k) ? 1u : 0u);
+              if (g || t >= a[1]) commit<kCtas>(&c.empty[at.piece]);
+            }
           }
           if (!ok) break;
-          commit<kCtas>(&c.s[g]);
-          if (t == a - 1) commit<kCtas>(&c.qfree[g]);
+          if (lead) {
+            commit<kCtas>(&c.s[g]);
+            if (t == a[g] - 1) commit<kCtas>(&c.qfree[g]);
+          }
         }
       }
-      if (t < tiles) at += 5;
+      if (t < tiles) kc.skip(R::kTile);
+      if (t > 0) vc.skip(R::kTile);
     }
     if (!ok) break;
-    if (a0 > 0) ps0 += a0, ++qs0;
-    if (a1 > 0) ps1 += a1, ++qs1;
-    units.release();
+#pragma unroll
+    for (int g = 0; g < 2; ++g)
+      if (a[g] > 0) ps[g] += a[g], ++qs[g];
+    __syncwarp();
+    if (lead) units.release(); else units.skip();
   }
-  if (!ok) give_up<kCtas>(c, p, 0);
+  if (!ok && lead) give_up<kCtas>(c, p, 0);
   // No MMA may still run when the accumulators are freed.
   int never = 0;
-  commit<kCtas>(&c.drain);
-  wait_bar<kCtas>(&c.drain, 0, &never);
+  if (lead) commit<kCtas>(&c.drain);
+  wait_bar(&c.drain, 0, &never);
 }
 
 // Tiles from u.clean0 on hold tokens that some row does not see (its own later
-// ones, or the next sequence's).  Warp i of the two cleans stage i of a tile's V.
+// ones, or the next sequence's).  A warp cleans 16 KB at a time: on one CTA warp i
+// of the two piece i of a tile's V; in a pair they take turns with the tiles.
 template <int kCtas>
 __device__ __forceinline__ void clean_values(uint8_t* base, Ctl& c, const PrefillParams& p, uint32_t rank, int i,
                                              int lane) {
-  constexpr int kStageBytes = kBox / kCtas, kStages = kRing / kStageBytes;
+  using R = Ring<kCtas>;
+  constexpr int kBatch = 8, kVecs = kBox / 16;  // 16-byte vectors: in flight per lane, of a job
   Units<kCtas> units(c);
   bool ok = true;
-  uint32_t at = 0, cleans = 0;
+  uint32_t at = 0, cleans = 0;  // pieces and cleaned tiles so far
   while (const Unit* u = units.next(ok)) {
     const int j0 = u->j0, j1 = u->j1, clean0 = u->clean0, unseen = u->unseen, lk = u->lk;
     const uint32_t tag = tag_of(units.nth);
+    bool first = true;
+#pragma unroll 1
     for (int j = clean0; j < j1; ++j) {
       const uint32_t nth = cleans + (j - clean0);
-      if (!(ok = __all_sync(~0u, wait_bar<kCtas>(&c.raw[nth % kRaw], nth / kRaw & 1, &c.abort_flag)))) break;
+      if (kCtas == 2 && (nth & 1) != (uint32_t)i) continue;
+      if (!(ok = __all_sync(~0u, wait_bar(&c.raw[nth % kRaw], nth / kRaw & 1, &c.abort_flag)))) break;
       // the notes on the unit before have been read (by both CTAs)
-      if (j == clean0 && units.nth > 0 &&
-          !(ok = __all_sync(~0u, wait_bar<kCtas>(&c.done, (units.nth - 1) & 1, &c.abort_flag))))
+      if (first && units.nth > 0 &&
+          !(ok = __all_sync(~0u, wait_bar<kCtas == 2>(&c.done, (units.nth - 1) & 1, &c.abort_flag))))
         break;
-      const uint32_t st = (at + 5 * (j - j0) + 3 + i) % kStages;
-      uint8_t* box = base + 6 * kBox + st * kStageBytes;
-      const int t0 = j * kKeys + i * 64;  // token of the stage's first row
-      // 16-byte vectors: half (64 dims), row, chunk, swizzled by the row
-#pragma unroll 4
-      for (int x = lane; x < kStageBytes / 16; x += 32) {
-        uint4* vec = reinterpret_cast<uint4*>(box + x * 16);
-        const int half = (int)rank + (x >> 9), row = (x >> 3) & 63, chunk = (x & 7) ^ (row & 7);
-        uint4 w = *vec;
-        uint32_t* r = reinterpret_cast<uint32_t*>(&w);
+      first = false;
+      const uint32_t piece = (at + R::kTile * (j - j0) + R::kK + (kCtas == 1 ? i : 0)) % R::kAll;
+      uint4* box = reinterpret_cast<uint4*>(base + 6 * kBox + R::at(piece));
+      const int t0 = j * kKeys + (kCtas == 1 ? i * 64 : 0);  // token of the first row
+#pragma unroll 1
+      for (int x0 = lane; x0 < kVecs; x0 += 32 * kBatch) {
+        uint4 w[kBatch];
         uint32_t hit = 0;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) hit |= (r[e] & 0x7f807f80u) + 0x00800080u;
-        if (!(hit & 0x80008000u) || t0 + row < unseen) continue;
-        for (int e = 0; e < 8; ++e) {
-          const uint32_t b = r[e / 2] >> (16 * (e & 1)) & 0xffffu;
-          if ((b & 0x7f80u) != 0x7f80u) continue;
-          r[e / 2] &= e & 1 ? 0x0000ffffu : 0xffff0000u;
-          const int past = t0 + row - unseen;
+        for (int b = 0; b < kBatch; ++b) w[b] = box[x0 + 32 * b];
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b)
+          hit |= ((w[b].x & 0x7f807f80u) + 0x00800080u) | ((w[b].y & 0x7f807f80u) + 0x00800080u) |
+                 ((w[b].z & 0x7f807f80u) + 0x00800080u) | ((w[b].w & 0x7f807f80u) + 0x00800080u);
+        if (!(hit & 0x80008000u)) continue;
+        // some value of these is not finite: half (64 dims), row, chunk, swizzled by the row
+#pragma unroll 1
+        for (int e = 0; e < 8 * kBatch; ++e) {
+          const int x = x0 + e / 8 * 32;
+          const int half = kCtas == 1 ? x >> 9 : (int)rank, row = (x >> 3) & (kCtas == 1 ? 63 : 127);
+          uint16_t* val = reinterpret_cast<uint16_t*>(box + x) + e % 8;
+          const uint32_t bits = *val;
+          if ((bits & 0x7f80u) != 0x7f80u || t0 + row < unseen) continue;
+          *val = 0;
+          const int past = t0 + row - unseen, dim = half * 64 + ((x & 7) ^ (row & 7)) * 8 + e % 8;
           if (t0 + row < lk && past < 1 << kOffsetBits) {  // past that no row of the unit sees it
-            uint32_t* odd = &c.odd[b & 0x7fu ? 0 : b & 0x8000u ? 2 : 1][half * 64 + chunk * 8 + e];
+            uint32_t* odd = &c.odd[bits & 0x7fu ? 0 : bits & 0x8000u ? 2 : 1][dim];
             atomicMin(odd, tag | past);
             atomicMin(&c.any_odd, tag);
             if constexpr (kCtas == 2) {
@@ -510,18 +609,17 @@ __device__ __forceinline__ void clean_values(uint8_t* base, Ctl& c, const Prefil
             }
           }
         }
-        *vec = w;
       }
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
-        if (kCtas == 1) mbar_arrive(smem_u32(&c.full[st]));
-        else if (rank == 0) mbar_arrive_expect_tx(smem_u32(&c.full[st]), 4);
-        else st_async_u32(mapa(smem_u32(&c.note), 0), 0, lead_bar<kCtas>(&c.full[st]));
+        if (kCtas == 1) mbar_arrive(smem_u32(&c.full[piece]));
+        else if (rank == 0) mbar_arrive_expect_tx(smem_u32(&c.full[piece]), 4);
+        else st_async_u32(mapa(smem_u32(&c.note), 0), 0, lead_bar<kCtas>(&c.full[piece]));
       }
     }
     if (!ok) break;
-    at += 5 * (j1 - j0);
+    at += R::kTile * (j1 - j0);
     if (j1 > clean0) {
       cleans += j1 - clean0;
       if (lane == 0) {
@@ -543,23 +641,33 @@ __device__ __forceinline__ void softmax_rows(Ctl& c, const PrefillParams& p, uin
   const uint32_t quad = (uint32_t)((warp & 3) * 32) << 16;
   const uint32_t s_at = tmem + quad + g * kKeys, o_at = tmem + quad + (2 + g) * kKeys;
   const uint64_t scale2 = f2pack(p.scale2, p.scale2);
-  const uint32_t lead_p = lead_bar<kCtas>(&c.p[g]), lead_note = kCtas == 1 ? 0 : mapa(smem_u32(&c.note), 0);
+  const uint32_t lead_p = lead_bar<kCtas>(&c.p[g][0]), lead_note = kCtas == 1 ? 0 : mapa(smem_u32(&c.note), 0);
+  // half i of a tile's P is in tensor memory
+  const auto report = [&](int i) {
+    tmem_wait_st();
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) {
+      // a pair's second CTA reports by an asynchronous store, whose completion on
+      // the first CTA's barrier is a release at cluster scope (a release arrive
+      // costs its round trip); the first CTA's warp 0 arms the barrier for them
+      if (kCtas == 1) mbar_arrive(lead_p + 8 * i);
+      else if (rank) st_async_u32(lead_note, 0, lead_p + 8 * i);
+      else if ((warp & 3) == 0) mbar_arrive_expect_tx(smem_u32(&c.p[g][i]), 16);
+      else mbar_arrive(smem_u32(&c.p[g][i]));
+    }
+  };
   Units<kCtas> units(c);
   bool ok = true;
   uint32_t turns = 0, outs = 0, cleans = 0;  // phases of c.s, c.o and c.cleaned
   while (const Unit* u = units.next(ok)) {
-    const bool exists = in_block < u->rows, cleaned = u->j1 > u->clean0;
-    const int j0 = u->j0, tiles = (g ? u->n1 : u->n0) - j0;
+    const int tiles = (g ? u->n1 : u->n0) - u->j0;
     // keys that the row sees, from the unit's first tile on; padding rows: all
-    const int seen = exists ? sees(p, u->lq, u->lk, u->prefix, u->row0 + in_block) - j0 * kKeys : 0x7fffffff;
-    const int unseen = u->unseen - j0 * kKeys;
-    const bool whole = u->slot < 0;
-    // where the row's output goes: its row of out, or of the part's workspace
-    const int64_t row = whole ? ((int64_t)u->q0 + u->row0 + in_block) * p.H + u->h
-                              : ((int64_t)(u->slot + in_block / kSlot) * p.H + u->h) * kSlot + in_block % kSlot;
+    const int seen = in_block < u->rows ? sees(p, u->lq, u->lk, u->prefix, u->row0 + in_block) - u->j0 * kKeys
+                                        : 0x7fffffff;
     float ref = -INFINITY, l = 0.f;  // raw scores; sum of 2^((s - ref) scale2)
     for (int t = 0; t < tiles; ++t, ++turns) {
-      if (!(ok = wait_bar<kCtas>(&c.s[g], turns & 1, &c.abort_flag))) break;
+      if (!(ok = wait_bar(&c.s[g], turns & 1, &c.abort_flag))) break;
       tc_fence_after();
       float s[kKeys];
 #pragma unroll
@@ -568,7 +676,12 @@ __device__ __forceinline__ void softmax_rows(Ctl& c, const PrefillParams& p, uin
       const int last = seen - t * kKeys;  // columns of this tile that the row sees
       if (__any_sync(~0u, last < kKeys)) {
 #pragma unroll
-        for (int e = 0; e < kKeys; ++e) s[e] = e < last ? s[e] : -INFINITY;
+        for (int b = 0; b < 4; ++b) {
+          const int n = last - 32 * b;
+          const uint32_t mask = n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1u;
+#pragma unroll
+          for (int e = 0; e < 32; ++e) s[32 * b + e] = mask >> e & 1 ? s[32 * b + e] : -INFINITY;
+        }
       }
       float m4[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
@@ -614,71 +727,64 @@ __device__ __forceinline__ void softmax_rows(Ctl& c, const PrefillParams& p, uin
           pk[e] = pack_bf16(pa, pb);
         }
         tmem_st32(s_at + 32 * b, pk);
+        report(b);
       }
       float x, y, z, w;
       f2unpack(sum2[0], x, y);
       f2unpack(sum2[1], z, w);
       l = (x + y) + (z + w);
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        // a pair's second CTA reports by an asynchronous store, whose completion on
-        // the first CTA's barrier is a release at cluster scope (a release arrive
-        // costs its round trip); the first CTA's warp 0 arms the barrier for them
-        if (kCtas == 1) mbar_arrive(lead_p);
-        else if (rank) st_async_u32(lead_note, 0, lead_p);
-        else if ((warp & 3) == 0) mbar_arrive_expect_tx(smem_u32(&c.p[g]), 16);
-        else mbar_arrive(smem_u32(&c.p[g]));
-      }
     }
     if (!ok) break;
     if (tiles > 0) {
-      if (!(ok = wait_bar<kCtas>(&c.o[g], outs & 1, &c.abort_flag))) break;
+      if (!(ok = wait_bar(&c.o[g], outs & 1, &c.abort_flag))) break;
       ++outs;
     }
+    const bool exists = in_block < u->rows, cleaned = u->j1 > u->clean0, whole = u->slot < 0;
     if (cleaned) {
-      if (!(ok = wait_bar<kCtas>(&c.cleaned, cleans & 1, &c.abort_flag))) break;
+      if (!(ok = wait_bar<kCtas == 2>(&c.cleaned, cleans & 1, &c.abort_flag))) break;
       ++cleans;
     }
     tc_fence_after();
     const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
     const float lse = l > 0.f || l != l ? ref * p.sm_scale + logf(l) : -INFINITY;
+    // where the row's output goes: its row of out, or of the part's workspace
+    const int64_t row = whole ? ((int64_t)u->q0 + u->row0 + in_block) * p.H + u->h
+                              : ((int64_t)(u->slot + in_block / kSlot) * p.H + u->h) * kSlot + in_block % kSlot;
+    const int unseen = u->unseen - u->j0 * kKeys;
     // notes of this unit: tokens that the row sees get their values back
     const uint32_t tag = tag_of(units.nth), reach = tag + (uint32_t)min(max(seen - unseen, 0), 1 << kOffsetBits);
     const bool odd = cleaned && *reinterpret_cast<volatile uint32_t*>(&c.any_odd) == tag;
-    float o[kKeys];
-    if (tiles > 0) {
-#pragma unroll
-      for (int b = 0; b < 4; ++b) tmem_ld32(o_at + 32 * b, *reinterpret_cast<uint32_t(*)[32]>(&o[32 * b]));
-      tmem_wait_ld();
-    } else {
-#pragma unroll
-      for (int e = 0; e < kKeys; ++e) o[e] = 0.f;
-    }
-#pragma unroll
-    for (int e = 0; e < kKeys; ++e) o[e] = l == 0.f ? 0.f : o[e] * inv;
-    if (odd) {
-#pragma unroll
-      for (int e = 0; e < kKeys; ++e) {
-        if (c.odd[0][e] < reach) o[e] += NAN;
-        if (c.odd[1][e] < reach) o[e] += INFINITY;
-        if (c.odd[2][e] < reach) o[e] -= INFINITY;
+#pragma unroll 1
+    for (int b = 0; b < kKeys; b += 32) {
+      float o[32];
+      if (tiles > 0) {
+        tmem_ld32(o_at + b, *reinterpret_cast<uint32_t(*)[32]>(&o));
+        tmem_wait_ld();
       }
-    }
-    if (exists && whole) {
-      __nv_bfloat16* dst = p.out + row * MLA_V_HEAD_DIM;
 #pragma unroll
-      for (int e = 0; e < kKeys; e += 16) {
-        uint32_t w[8];
+      for (int e = 0; e < 32; ++e) o[e] = l == 0.f ? 0.f : o[e] * inv;
+      if (odd) {
 #pragma unroll
-        for (int x = 0; x < 8; ++x) w[x] = pack_bf16(o[e + 2 * x], o[e + 2 * x + 1]);
-        st_global_v8(dst + e, w);
+        for (int e = 0; e < 32; ++e) {
+          if (c.odd[0][b + e] < reach) o[e] += NAN;
+          if (c.odd[1][b + e] < reach) o[e] += INFINITY;
+          if (c.odd[2][b + e] < reach) o[e] -= INFINITY;
+        }
       }
-    } else if (exists) {
-      float* dst = p.O_part + row * MLA_V_HEAD_DIM;
+      if (exists && whole) {
+        __nv_bfloat16* dst = p.out + row * MLA_V_HEAD_DIM + b;
 #pragma unroll
-      for (int e = 0; e < kKeys; e += 8) st_global_v8(dst + e, *reinterpret_cast<const uint32_t(*)[8]>(&o[e]));
+        for (int e = 0; e < 32; e += 16) {
+          uint32_t w[8];
+#pragma unroll
+          for (int x = 0; x < 8; ++x) w[x] = pack_bf16(o[e + 2 * x], o[e + 2 * x + 1]);
+          st_global_v8(dst + e, w);
+        }
+      } else if (exists) {
+        float* dst = p.O_part + row * MLA_V_HEAD_DIM + b;
+#pragma unroll
+        for (int e = 0; e < 32; e += 8) st_global_v8(dst + e, *reinterpret_cast<const uint32_t(*)[8]>(&o[e]));
+      }
     }
     if (exists) {
       if (!whole) p.LSE_part[row] = lse;
@@ -713,12 +819,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(&c.q[g]), 1);
       mbar_init(smem_u32(&c.qfree[g]), 1);
       mbar_init(smem_u32(&c.s[g]), 1);
-      mbar_init(smem_u32(&c.p[g]), 4);
+      for (int i = 0; i < 2; ++i) mbar_init(smem_u32(&c.p[g][i]), 4);
       mbar_init(smem_u32(&c.o[g]), 1);
       mbar_init(smem_u32(&c.unit_full[g]), 1);
-      mbar_init(smem_u32(&c.unit_empty[g]), 12);  // TMA, MMA, 2 cleaning, 8 softmax warps
+      mbar_init(smem_u32(&c.unit_empty[g]), 13);  // 2 TMA, MMA, 2 cleaning, 8 softmax warps
     }
-    for (int i = 0; i < 16; ++i) {
+    for (int i = 0; i < Ring<kCtas>::kAll; ++i) {
       mbar_init(smem_u32(&c.full[i]), 1);
       mbar_init(smem_u32(&c.empty[i]), 1);
     }
@@ -765,16 +871,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp >= kWarpTma) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
     if (warp == kWarpTma) {
-      produce<kCtas>(base, c, p, &qn, &qr, &kn, &kr, &v, rank, lane);
+      produce<kCtas>(base, c, p, &kn, &kr, &v, rank, lane);
+    } else if (warp == kWarpQ) {
+      load_queries<kCtas>(base, c, p, &qn, &qr, rank, lane);
     } else if (warp == kWarpMma) {
       if (rank == 0) {
-        if (elect_one()) issue_mmas<kCtas>(base, c, p, tmem);
+        issue_mmas<kCtas>(base, c, p, tmem, lane);
       } else if (lane == 0) {  // passes the units on
         bool ok;
         Units<kCtas> units(c);
         while (units.next(ok)) units.release();
         int never = 0;
-        wait_bar<kCtas>(&c.drain, 0, &never);
+        wait_bar(&c.drain, 0, &never);
       }
     } else if (warp == kWarpNext) {
       if (lane == 0) feed<kCtas>(c, p, rank);
@@ -934,11 +1042,11 @@ extern "C" int mla_prefill(const void* q_nope, int64_t qn_token_stride, int64_t 
   if (rc == MLA_OK) rc = head_map(&kr, k_rope, kRope, 1, Tk, kr_token_stride, kRope, keys);
   if (rc == MLA_OK) {
     // 64 tokens x 128 dims as two halves of 64 dims, one after the other; in a pair
-    // a CTA's half
+    // 128 tokens of a CTA's half
     const uint64_t d[4] = {64, (uint64_t)std::max<int64_t>(Tk, 1), 2, (uint64_t)H};
     const uint64_t st[3] = {(uint64_t)(Tk > 1 ? v_token_stride : (int64_t)H * kValue) * 2, 128,
                             (uint64_t)(H > 1 ? v_head_stride : kValue) * 2};
-    const uint32_t box[4] = {64, 64, (uint32_t)(2 / ctas), 1};
+    const uint32_t box[4] = {64, ctas == 1 ? 64u : 128u, (uint32_t)(2 / ctas), 1};
     rc = make_tensor_map_bf16_4d(&vm, v, d, st, box);
   }
   if (rc != MLA_OK) return rc;
