@@ -123,7 +123,7 @@ struct Ctl {
   uint64_t q[2], qfree[2];       // Q of a row tile has landed; has been used up
   uint64_t full[8], empty[8];    // ring
   uint64_t s[2];                 // S of a row tile is in TMEM
-  uint64_t p[2][2];              // its P of the tile's first and last 64 keys is, S has been read
+  uint64_t p[2][2];              // its P of the tile's first and last 64 keys is (one CTA: all of it, by [1]), S has been read
   uint64_t o[2];                 // O is complete
   uint64_t raw[kRaw];            // V of a tile to be cleaned has landed (tiles take turns)
   uint64_t cleaned;              // all of a unit's are clean
@@ -478,58 +478,59 @@ __device__ __forceinline__ void issue_mmas(uint8_t* base, Ctl& c, const PrefillP
   };
   Units<kCtas> units(c);
   Cursor<kCtas> kc{0, 0}, vc{R::kK, 0};         // K(t) and V(t - 1)
-  uint32_t ps[2] = {0, 0}, qs[2] = {0, 0};      // tiles and units of each row tile so far
+  uint32_t ps0 = 0, ps1 = 0, qs0 = 0, qs1 = 0;  // tiles and units of each row tile so far
   while (const Unit* u = units.next(ok)) {
     const int j0 = __shfl_sync(~0u, u->j0, 0), tiles = __shfl_sync(~0u, u->j1, 0) - j0;
-    const int a[2] = {__shfl_sync(~0u, u->n0, 0) - j0, __shfl_sync(~0u, u->n1, 0) - j0};
+    const int a0 = __shfl_sync(~0u, u->n0, 0) - j0, a1 = __shfl_sync(~0u, u->n1, 0) - j0;
     const int clean = kCtas == 1 ? 0x7fffffff : __shfl_sync(~0u, u->clean0, 0) - j0;
 #pragma unroll 1
     for (int t = 0; t <= tiles && ok; ++t) {
-#pragma unroll
+#pragma unroll 1
       for (int g = 0; g < 2; ++g) {
         const uint32_t s = tmem + g * kKeys, o = tmem + (2 + g) * kKeys;
-        if (t > 0 && t - 1 < a[g]) {
+        const int a = g ? a1 : a0;
+        if (t > 0 && t - 1 < a) {
           Cursor<kCtas> at = vc;
 #pragma unroll
           for (int i = 0; i < 2; ++i) {  // 64 tokens
-            if ((R::kV == 2 || i == 0) && (g == 0 || t - 1 >= a[0])) {
+            if ((R::kV == 2 || i == 0) && (g == 0 || t - 1 >= a0)) {
               if (!wait(&c.full[at.piece], at.phase)) break;
               // cleaned by the other CTA's threads, too
               if (kCtas == 2 && t - 1 >= clean) fence_cluster();
             }
-            if (!wait(&c.p[g][i], (ps[g] + t - 1) & 1)) break;
+            if ((kCtas == 2 || i == 0) && !wait(&c.p[g][kCtas == 1 ? 1 : i], ((g ? ps1 : ps0) + t - 1) & 1)) break;
             tc_fence_after();
             if (lead) {
               const uint64_t b = plus(vd, (R::at(at.piece) + (R::kV == 1 ? i * R::kHalfBox : 0)) >> 4);
 #pragma unroll
               for (int k = 0; k < 4; ++k)
                 mma_pv<kCtas>(o, s + (4 * i + k) * 8, plus(b, 128 * k), (t > 1 || i || k) ? 1u : 0u);
-              if ((R::kV == 2 || i == 1) && (g || t - 1 >= a[1])) commit<kCtas>(&c.empty[at.piece]);
+              if ((R::kV == 2 || i == 1) && (g || t - 1 >= a1)) commit<kCtas>(&c.empty[at.piece]);
             }
             if (R::kV == 2) at.next();
           }
           if (!ok) break;
-          if (lead && t == a[g]) commit<kCtas>(&c.o[g]);
+          if (lead && t == a) commit<kCtas>(&c.o[g]);
         }
-        if (t < a[g]) {
-          if (t == 0 && !wait(&c.q[g], qs[g] & 1)) break;
+        if (t < a) {
+          if (t == 0 && !wait(&c.q[g], (g ? qs1 : qs0) & 1)) break;
           Cursor<kCtas> at = kc;
 #pragma unroll
           for (int i = 0; i < R::kK; ++i, at.next()) {
-            if ((g == 0 || t >= a[0]) && !wait(&c.full[at.piece], at.phase)) break;
+            if ((g == 0 || t >= a0) && !wait(&c.full[at.piece], at.phase)) break;
             if (lead) {
               const uint64_t q = plus(qd, (3 * g + i) * (kBox >> 4)), b = plus(kd, R::at(at.piece) >> 4);
 #pragma unroll
               for (int k = 0; k < 12 / R::kK; ++k)
                 mma_qk<kCtas>(s, plus(q, k / 4 * (kBox >> 4) + 2 * (k % 4)),
                               plus(b, k / 4 * (R::kHalfBox >> 4) + 2 * (k % 4)), (i || k) ? 1u : 0u);
-              if (g || t >= a[1]) commit<kCtas>(&c.empty[at.piece]);
+              if (g || t >= a1) commit<kCtas>(&c.empty[at.piece]);
             }
           }
           if (!ok) break;
           if (lead) {
             commit<kCtas>(&c.s[g]);
-            if (t == a[g] - 1) commit<kCtas>(&c.qfree[g]);
+            if (t == a - 1) commit<kCtas>(&c.qfree[g]);
           }
         }
       }
@@ -537,9 +538,8 @@ __device__ __forceinline__ void issue_mmas(uint8_t* base, Ctl& c, const PrefillP
       if (t > 0) vc.skip(R::kTile);
     }
     if (!ok) break;
-#pragma unroll
-    for (int g = 0; g < 2; ++g)
-      if (a[g] > 0) ps[g] += a[g], ++qs[g];
+    if (a0 > 0) ps0 += a0, ++qs0;
+    if (a1 > 0) ps1 += a1, ++qs1;
     __syncwarp();
     if (lead) units.release(); else units.skip();
   }
@@ -727,7 +727,7 @@ __device__ __forceinline__ void softmax_rows(Ctl& c, const PrefillParams& p, uin
           pk[e] = pack_bf16(pa, pb);
         }
         tmem_st32(s_at + 32 * b, pk);
-        report(b);
+        if (kCtas == 2 || b == 1) report(b);
       }
       float x, y, z, w;
       f2unpack(sum2[0], x, y);
@@ -754,36 +754,38 @@ __device__ __forceinline__ void softmax_rows(Ctl& c, const PrefillParams& p, uin
     // notes of this unit: tokens that the row sees get their values back
     const uint32_t tag = tag_of(units.nth), reach = tag + (uint32_t)min(max(seen - unseen, 0), 1 << kOffsetBits);
     const bool odd = cleaned && *reinterpret_cast<volatile uint32_t*>(&c.any_odd) == tag;
+    __nv_bfloat16* out = p.out + row * MLA_V_HEAD_DIM;
+    float* part = p.O_part + row * MLA_V_HEAD_DIM;
 #pragma unroll 1
-    for (int b = 0; b < kKeys; b += 32) {
-      float o[32];
+    for (int b = 0; b < kKeys; b += 16) {
+      uint32_t o[16];
       if (tiles > 0) {
-        tmem_ld32(o_at + b, *reinterpret_cast<uint32_t(*)[32]>(&o));
+        tmem_ld16(o_at + b, o);
         tmem_wait_ld();
       }
 #pragma unroll
-      for (int e = 0; e < 32; ++e) o[e] = l == 0.f ? 0.f : o[e] * inv;
-      if (odd) {
-#pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          if (c.odd[0][b + e] < reach) o[e] += NAN;
-          if (c.odd[1][b + e] < reach) o[e] += INFINITY;
-          if (c.odd[2][b + e] < reach) o[e] -= INFINITY;
-        }
-      }
+      for (int e = 0; e < 16; ++e) o[e] = l == 0.f ? 0u : __float_as_uint(__uint_as_float(o[e]) * inv);
       if (exists && whole) {
-        __nv_bfloat16* dst = p.out + row * MLA_V_HEAD_DIM + b;
+        uint32_t w[8];
 #pragma unroll
-        for (int e = 0; e < 32; e += 16) {
-          uint32_t w[8];
-#pragma unroll
-          for (int x = 0; x < 8; ++x) w[x] = pack_bf16(o[e + 2 * x], o[e + 2 * x + 1]);
-          st_global_v8(dst + e, w);
-        }
+        for (int x = 0; x < 8; ++x) w[x] = pack_bf16(__uint_as_float(o[2 * x]), __uint_as_float(o[2 * x + 1]));
+        st_global_v8(out + b, w);
       } else if (exists) {
-        float* dst = p.O_part + row * MLA_V_HEAD_DIM + b;
-#pragma unroll
-        for (int e = 0; e < 32; e += 8) st_global_v8(dst + e, *reinterpret_cast<const uint32_t(*)[8]>(&o[e]));
+        st_global_v8(part + b, *reinterpret_cast<const uint32_t(*)[8]>(&o[0]));
+        st_global_v8(part + b + 8, *reinterpret_cast<const uint32_t(*)[8]>(&o[8]));
+      }
+      __syncwarp();
+    }
+    if (odd && exists) {
+#pragma unroll 1
+      for (int e = 0; e < kKeys; ++e) {
+        float add = 0.f;
+        if (c.odd[0][e] < reach) add = NAN;
+        if (c.odd[1][e] < reach) add += INFINITY;
+        if (c.odd[2][e] < reach) add -= INFINITY;
+        if (add == 0.f) continue;
+        if (whole) out[e] = __float2bfloat16(__bfloat162float(out[e]) + add);
+        else part[e] += add;
       }
     }
     if (exists) {
