@@ -694,7 +694,7 @@ int mla_prefill(const void* q_nope, int64_t qn_token_stride, int64_t qn_head_str
                 mla_stream_t stream);
 
 /*
- * Plan of mla_prefill on the host: the sequences' blocks of 256 query rows a CTA,
+ * Plan of mla_prefill on the host: the sequences' blocks of 128 query rows a CTA,
  * or of 512 rows a pair of CTAs, longest sequences first, a sequence's heads one after another (their keys and
  * values then stay in L2) and a head's blocks from the longest down; where
  * there are too few blocks for the SMs, blocks are cut along the keys into
@@ -703,8 +703,8 @@ int mla_prefill(const void* q_nope, int64_t qn_token_stride, int64_t qn_head_str
  *   ctas        1 or 2 CTAs a block, 0: whichever the plan's costs favour
  *   num_sms     0: the current device's (152 where there is none)
  *   work_out    host int32 [capacity], entries of 8 per CTA of a block (sequence,
- *               block, part, parts, slot of the first part or -1, first entry of
- *               the sequence, entries of the sequence, rows of a block)
+ *               block, part, parts, slot of 128 rows of the first part or -1, first
+ *               entry of the sequence, entries of the sequence, rows of a block)
  *   num_work_out, ctas_out, num_parts_out   host: entries, CTAs of an entry's block
  *               and workspace slots of 256 rows
  * A list longer than `capacity` is MLA_ERR_INVALID_ARG;

@@ -186,9 +186,10 @@ using namespace mla;
 
 namespace mla {
 
-// Plan of mla_prefill with blocks of 256 * ctas rows.  Costs in key tiles of a
-// CTA on its own (about 2.1 us): a tile of a pair, what a block takes besides its
-// tiles, and the merging launch with its rows.
+// Plan of mla_prefill with blocks of 128 rows (one CTA, two of them an SM) or 512
+// (a pair of CTAs).  Costs in key tiles of a single CTA with another beside it
+// (about 1.6 us): a tile of a pair, what a block takes besides its tiles, and the
+// merging launch with its rows.
 struct PrefillPlan {
   int ctas = 1;
   double end = 0;
@@ -206,8 +207,8 @@ static PrefillPlan plan_prefill_blocks(const int32_t* q_lens, const int32_t* kv_
                                        const int32_t* prefix, int N, int H, int causal,
                                        int ctas, int num_sms) {
   constexpr int kKeys = 128;
-  constexpr double kFixed = 2, kPairTile = 0.62, kMerge = 3, kMergeSlot = 0.002;
-  const int block = 256 * ctas;
+  constexpr double kFixed = 2, kPairFixed = 4, kPairTile = 0.95, kMerge = 3, kMergeSlot = 0.001;
+  const int block = ctas == 1 ? 128 : 512, slots_of = block / 128;
   PrefillPlan plan;
   plan.ctas = ctas;
   plan.tiles.resize(N);
@@ -230,10 +231,10 @@ static PrefillPlan plan_prefill_blocks(const int32_t* q_lens, const int32_t* kv_
   std::stable_sort(plan.order.begin(), plan.order.end(),
                    [&](int a, int b) { return last_of(a) > last_of(b); });
   plan.limit = std::max<int64_t>(longest, 1);
-  const int slots = std::max(num_sms / ctas, 1);
-  const double tile = ctas == 1 ? 1 : kPairTile;
+  const int slots = ctas == 1 ? 2 * std::max(num_sms, 1) : std::max(num_sms / 2, 1);
+  const double tile = ctas == 1 ? 1 : kPairTile, fixed = ctas == 1 ? kFixed : kPairFixed;
   // Many blocks: they even out.
-  plan.end = ((double)all * tile + (double)blocks * kFixed) * H / slots + longest * tile / 2;
+  plan.end = ((double)all * tile + (double)blocks * fixed) * H / slots + longest * tile / 2;
   if (blocks == 0 || blocks * H >= 8 * (int64_t)slots) return plan;
   // Few: a limit on a part's key tiles, the one whose list schedule in launch
   // order ends first.
@@ -250,10 +251,10 @@ static PrefillPlan plan_prefill_blocks(const int32_t* q_lens, const int32_t* kv_
       for (int h = 0; h < H; ++h)
         for (auto t = plan.tiles[n].rbegin(); t != plan.tiles[n].rend(); ++t) {
           const int parts = plan.parts_of(*t);
-          merged += parts > 1 ? parts * ctas : 0;
+          merged += parts > 1 ? parts * slots_of : 0;
           for (int s = 0; s < parts; ++s) {
             const double at =
-                ends.top() + kFixed + tile * (double)(*t * (s + 1) / parts - *t * s / parts);
+                ends.top() + fixed + tile * (double)(*t * (s + 1) / parts - *t * s / parts);
             ends.pop();
             ends.push(at);
             end = std::max(end, at);
@@ -292,7 +293,7 @@ static int plan_prefill(const int32_t* q_lens, const int32_t* kv_lens,
     if (pairs.end < plan.end) plan = std::move(pairs);
   }
   int64_t at = 0, slots = 0;
-  const int width = 8 * plan.ctas;
+  const int width = 8 * plan.ctas, rows = plan.ctas == 1 ? 128 : 512;
   for (int n : plan.order) {
     const int64_t first = at;
     for (int b = (int)plan.tiles[n].size() - 1; b >= 0; --b) {
@@ -302,10 +303,10 @@ static int plan_prefill(const int32_t* q_lens, const int32_t* kv_lens,
       for (int s = 0; s < parts; ++s, ++at)
         for (int c = 0; c < plan.ctas; ++c) {
           const int32_t e[8] = {n, b, s, parts, parts > 1 ? (int32_t)slots : -1, (int32_t)first, 0,
-                                256 * plan.ctas};
+                                rows};
           std::copy(e, e + 8, work_out + at * width + 8 * c);
         }
-      if (parts > 1) slots += (int64_t)parts * plan.ctas;
+      if (parts > 1) slots += (int64_t)parts * (rows / 128);
     }
     for (int64_t i = first; i < at; ++i)
       for (int c = 0; c < plan.ctas; ++c) work_out[i * width + 8 * c + 6] = (int32_t)(at - first);
@@ -314,7 +315,7 @@ static int plan_prefill(const int32_t* q_lens, const int32_t* kv_lens,
     return fail(MLA_ERR_INVALID_ARG, "mla_plan_prefill: too many blocks");
   *num_work_out = at;
   *ctas_out = plan.ctas;
-  *num_parts_out = (int)slots;
+  *num_parts_out = (int)((slots + 1) / 2);
   return MLA_OK;
 }
 

@@ -53,28 +53,35 @@ namespace {
 using namespace ptx;
 
 constexpr int kRows = 128;           // rows of a CTA's tile (MMA M per CTA)
-constexpr int kSlot = 256;           // rows of a workspace slot
+constexpr int kSlot = 128;           // rows of a workspace slot, two to a part of the caller's
 constexpr int kKeys = 128;           // tokens of a key tile
 constexpr int kBox = 128 * 128;      // 16 KB: 64 dims of 128 rows
-constexpr int kRing = 8 * kBox;
 constexpr int kVBytes = 2 * kBox;    // V of a tile
 constexpr int kRaw = 4;              // V tiles that may wait for cleaning (the ring holds parts of 3)
-constexpr int kThreads = 512;
-constexpr int kWarpTma = 8, kWarpMma = 9, kWarpNext = 10, kWarpQ = 11, kWarpClean = 12;
-// 512 threads launch with 128 registers (65536 in all): 256 x 200 + 256 x 56.
+// The softmax warps take 200 registers a thread, the others 56: as many threads of
+// each kind, 128 on average, as the kernels launch with.
 constexpr int kRegsSoftmax = 200, kRegsOther = 56;
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kRise = 8.f;         // log2 of the rise that rescales O
 constexpr int kEntry = 8;            // int32 of a work entry
-constexpr int kOffsetBits = 9;       // of a note on a cleaned value: its token past the first unseen one
 
-// The ring's pieces, each with its barriers: on one CTA a box of 16 KB (64 dims of
-// K or 64 tokens of V); in a pair a CTA's half of a tile's K (24 KB) or V (16 KB).
+// A form of the kernel: kCtas CTAs a unit, each with kTiles row tiles.  The ring's
+// pieces, each with its barriers: on one CTA a box of 16 KB (64 dims of K or 64
+// tokens of V); in a pair a CTA's half of a tile's K (24 KB) or V (16 KB).
 template <int kCtas>
-struct Ring {
+struct Form {
+  static constexpr int kTiles = kCtas;
+  static constexpr int kBlock = kTiles * kRows * kCtas;                   // rows of a unit
+  static constexpr int kSoftmax = 4 * kTiles;                             // warps; the others after them
+  static constexpr int kTma = kSoftmax, kMma = kTma + 1, kNext = kTma + 2, kClean = kTma + (kCtas == 1 ? 3 : 4);
+  [[maybe_unused]] static constexpr int kQ = kTma + 3;                    // (one CTA: Q from warp kTma)
+  static constexpr int kCleaners = kCtas;
+  static constexpr int kThreads = 2 * 32 * kSoftmax;
   static constexpr int kK = kCtas == 1 ? 3 : 1, kV = kCtas == 1 ? 2 : 1;  // pieces of a tile
-  static constexpr int kTile = kK + kV, kAll = kCtas == 1 ? 8 : 6;
+  static constexpr int kTile = kK + kV, kAll = kCtas == 1 ? 4 : 6;
   static constexpr int kHalfBox = kBox / kCtas;                           // 64 dims of a CTA's tokens of K
+  static constexpr int kQBytes = 3 * kTiles * kBox, kRing = kCtas == 1 ? 4 * kBox : 15 * kHalfBox;
+  static constexpr uint32_t kColumns = 256 * kTiles;                      // tensor memory: S, then O of the row tiles
   static __device__ __forceinline__ uint32_t at(uint32_t piece) {
     return kCtas == 1 ? piece * kBox : (piece >> 1) * (5 * kHalfBox) + (piece & 1) * (3 * kHalfBox);
   }
@@ -84,10 +91,13 @@ template <int kCtas>
 struct Cursor {
   uint32_t piece, phase;
   __device__ __forceinline__ void next() {
-    if (++piece == Ring<kCtas>::kAll) piece = 0, phase ^= 1;
+    if (++piece == Form<kCtas>::kAll) piece = 0, phase ^= 1;
   }
-  __device__ __forceinline__ void skip(int n) {
-    if ((piece += n) >= Ring<kCtas>::kAll) piece -= Ring<kCtas>::kAll, phase ^= 1;
+  __device__ __forceinline__ void next_tile() {
+    piece += Form<kCtas>::kTile;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      if (piece >= Form<kCtas>::kAll) piece -= Form<kCtas>::kAll, phase ^= 1;
   }
 };
 
@@ -119,33 +129,77 @@ struct Unit {
   int unseen;               // first key that some row does not see
 };
 
+// Notes on cleaned values: per kind (NaN, +inf, -inf) and dim the first such token,
+// counted from the unit's first unseen one (below the unit's rows).  Kept apart
+// from those of earlier units: in a pair by a tag that falls from unit to unit, so
+// that one minimum replaces older notes; on one CTA, which has less shared memory,
+// all of a dim's in one word under a tag that comes again after 127 units, the
+// notes being wiped in between.
+template <int kCtas>
+struct Notes;
+template <>
+struct Notes<2> {
+  static constexpr int kPastBits = 9;
+  uint32_t first[3][kKeys];
+  static __device__ __forceinline__ uint32_t tag(uint32_t nth) { return (0x7fffffu - nth) << kPastBits; }
+  __device__ __forceinline__ void clear(int dim) { first[0][dim] = first[1][dim] = first[2][dim] = ~0u; }
+  __device__ __forceinline__ void add(uint32_t nth, int kind, int dim, uint32_t past, uint32_t rank) {
+    atomicMin(&first[kind][dim], tag(nth) | past);
+    red_min_cluster_u32(mapa(smem_u32(&first[kind][dim]), rank ^ 1), tag(nth) | past);
+  }
+  __device__ __forceinline__ bool below(uint32_t nth, int kind, int dim, uint32_t reach) const {
+    return first[kind][dim] < tag(nth) + reach;
+  }
+};
+template <>
+struct Notes<1> {
+  uint32_t word[kKeys];
+  static constexpr uint32_t kWipe = 127;
+  static __device__ __forceinline__ uint32_t tag(uint32_t nth) { return (nth % kWipe + 1) << 24; }
+  __device__ __forceinline__ void clear(int dim) { word[dim] = 0; }
+  __device__ __forceinline__ void add(uint32_t nth, int kind, int dim, uint32_t past, uint32_t) {
+    uint32_t old = word[dim];
+    for (;;) {
+      const uint32_t mine = old >> 24 == tag(nth) >> 24 ? old : tag(nth) | 0xffffffu;
+      const uint32_t least = min(mine >> (8 * kind) & 0xffu, past);
+      const uint32_t next = (mine & ~(0xffu << (8 * kind))) | least << (8 * kind);
+      const uint32_t seen = atomicCAS(&word[dim], old, next);
+      if (seen == old) return;
+      old = seen;
+    }
+  }
+  __device__ __forceinline__ bool below(uint32_t nth, int kind, int dim, uint32_t reach) const {
+    return word[dim] >> 24 == tag(nth) >> 24 && (word[dim] >> (8 * kind) & 0xffu) < reach;
+  }
+};
+
+template <int kCtas>
 struct Ctl {
-  uint64_t q[2], qfree[2];       // Q of a row tile has landed; has been used up
-  uint64_t full[8], empty[8];    // ring
-  uint64_t s[2];                 // S of a row tile is in TMEM
-  uint64_t p[2][2];              // its P of the tile's first and last 64 keys is (one CTA: all of it, by [1]), S has been read
-  uint64_t o[2];                 // O is complete
-  uint64_t raw[kRaw];            // V of a tile to be cleaned has landed (tiles take turns)
-  uint64_t cleaned;              // all of a unit's are clean
-  uint64_t done;                 // the softmax warps are through with a unit
+  static constexpr int kTiles = Form<kCtas>::kTiles, kAll = Form<kCtas>::kAll;
+  uint64_t q[kTiles], qfree[kTiles];  // Q of a row tile has landed; has been used up
+  uint64_t full[kAll], empty[kAll];   // ring
+  uint64_t s[kTiles];                 // S of a row tile is in TMEM
+  uint64_t p[kTiles][2];              // its P of the tile's first and last 64 keys is, S has been read
+                                      // (on one CTA all of it, by [1])
+  uint64_t o[kTiles];                 // O is complete
+  uint64_t raw[kRaw];                 // V of a tile to be cleaned has landed (tiles take turns)
+  uint64_t cleaned;                   // all of a unit's are clean
+  uint64_t done;                      // the softmax warps are through with a unit
   uint64_t unit_full[2], unit_empty[2];
   uint64_t answer_full, answer_free;
   uint64_t drain;
   alignas(16) uint32_t answer[4];
   Unit unit[2];
-  uint32_t note;                 // where a peer's asynchronous stores go
-  // per kind (NaN, +inf, -inf) and dim: the first cleaned token, behind a tag that
-  // falls from unit to unit, so that a unit's notes replace older ones
-  uint32_t odd[3][kKeys];
-  uint32_t any_odd;              // the least tag of a unit with notes
+  uint32_t note;                      // where a peer's asynchronous stores go
   uint32_t tmem;
   int abort_flag;
+  uint32_t any_odd;                   // the last unit with notes, counted from 1
+  Notes<kCtas> notes;
 };
-constexpr int kSmem = 6 * kBox + kRing + (int)sizeof(Ctl);
-static_assert(kSmem <= 227 * 1024, "shared memory budget");
-
-// The unit tag of notes: falls with the unit's number in this CTA.
-__device__ __forceinline__ uint32_t tag_of(uint32_t nth) { return (0x7fffffu - nth) << kOffsetBits; }
+template <int kCtas>
+constexpr int kSmem = Form<kCtas>::kQBytes + Form<kCtas>::kRing + (int)sizeof(Ctl<kCtas>);
+static_assert(kSmem<1> <= 113 * 1024, "shared memory of two CTAs an SM");
+static_assert(kSmem<2> <= 227 * 1024, "shared memory budget");
 
 // Keys that row i of a sequence sees.
 __device__ __forceinline__ int sees(const PrefillParams& p, int lq, int lk, int prefix, int i) {
@@ -156,7 +210,7 @@ __device__ __forceinline__ int sees(const PrefillParams& p, int lq, int lk, int 
 // Unit x of the grid; false if its entry or lengths are none.
 template <int kCtas>
 __device__ __forceinline__ bool find_unit(const PrefillParams& p, int x, Unit& u) {
-  constexpr int kBlock = 2 * kRows * kCtas, kStride = kEntry * kCtas;
+  constexpr int kBlock = Form<kCtas>::kBlock, kStride = kEntry * kCtas;
   const int32_t* e = p.work + (int64_t)(x / p.H) * kStride;
   const int g0 = e[5], nb = e[6];
   if (g0 < 0 || nb < 1 || g0 > x / p.H || g0 + nb <= x / p.H || g0 + nb > p.num_work) {
@@ -170,7 +224,7 @@ __device__ __forceinline__ bool find_unit(const PrefillParams& p, int x, Unit& u
   const int64_t row0 = (int64_t)e[1] * kBlock;
   if (u.h >= p.H || seq < 0 || seq >= p.N || e[1] < 0 || parts < 1 || parts > MLA_PREFILL_MAX_PARTS ||
       part < 0 || part >= parts || e[7] != kBlock ||
-      (parts > 1 && (slot < 0 || slot > p.num_parts - parts * kCtas))) {
+      (parts > 1 && (slot < 0 || slot > 2 * (int64_t)p.num_parts - parts * (kBlock / kSlot)))) {
     if (p.status) atomicOr(p.status, MLA_STATUS_BAD_WORK);
     return false;
   }
@@ -186,12 +240,13 @@ __device__ __forceinline__ bool find_unit(const PrefillParams& p, int x, Unit& u
   u.row0 = (int)row0;
   u.rows = (int)min((int64_t)kBlock, lq - row0);
   u.q0 = (int)q0, u.k0 = (int)k0, u.lq = (int)lq, u.lk = (int)lk, u.prefix = prefix;
-  u.slot = parts > 1 ? slot + part * kCtas : -1;
+  u.slot = parts > 1 ? slot + part * (kBlock / kSlot) : -1;
   const auto tiles = [&](int first, int end) {
     if (u.rows <= first) return 0;
     return (sees(p, u.lq, u.lk, prefix, u.row0 + min(u.rows, end) - 1) + kKeys - 1) / kKeys;
   };
-  const int n0 = tiles(0, kBlock / 2), n1 = tiles(kBlock / 2, kBlock);
+  constexpr int kTileRows = kBlock / Form<kCtas>::kTiles;
+  const int n0 = tiles(0, kTileRows), n1 = Form<kCtas>::kTiles == 1 ? n0 : tiles(kTileRows, kBlock);
   const uint32_t all = (uint32_t)max(n0, n1);  // at most 2^24, parts at most 32
   u.j0 = (int)(all * (uint32_t)part / (uint32_t)parts);
   u.j1 = (int)(all * (uint32_t)(part + 1) / (uint32_t)parts);
@@ -302,7 +357,7 @@ __device__ __forceinline__ void commit(uint64_t* bar) {
 }
 
 template <int kCtas>
-__device__ __forceinline__ void give_up(Ctl& c, const PrefillParams& p, uint32_t rank) {
+__device__ __forceinline__ void give_up(Ctl<kCtas>& c, const PrefillParams& p, uint32_t rank) {
   *reinterpret_cast<volatile int*>(&c.abort_flag) = 1;
   if constexpr (kCtas == 2) st_cluster_u32(mapa(smem_u32(&c.abort_flag), rank ^ 1), 1);
   if (p.status) atomicOr(p.status, MLA_STATUS_WAIT_TIMEOUT);
@@ -312,9 +367,9 @@ __device__ __forceinline__ void give_up(Ctl& c, const PrefillParams& p, uint32_t
 // its slot back (one lane).
 template <int kCtas>
 struct Units {
-  Ctl& c;
+  Ctl<kCtas>& c;
   uint32_t nth = 0;
-  __device__ __forceinline__ explicit Units(Ctl& ctl) : c(ctl) {}
+  __device__ __forceinline__ explicit Units(Ctl<kCtas>& ctl) : c(ctl) {}
   __device__ __forceinline__ const Unit* next(bool& ok) {
     ok = wait_bar(&c.unit_full[nth & 1], nth >> 1 & 1, &c.abort_flag);
     const Unit* u = &c.unit[nth & 1];
@@ -330,7 +385,7 @@ struct Units {
 // Finds the units and hands them to the CTA's roles: its own first, then those
 // it takes over, asked for one unit ahead.
 template <int kCtas>
-__device__ __forceinline__ void feed(Ctl& c, const PrefillParams& p, uint32_t rank) {
+__device__ __forceinline__ void feed(Ctl<kCtas>& c, const PrefillParams& p, uint32_t rank) {
   int x = blockIdx.x / kCtas;
   uint32_t nth = 0, asked = 0;
   bool ok = true;
@@ -366,42 +421,62 @@ __device__ __forceinline__ void feed(Ctl& c, const PrefillParams& p, uint32_t ra
   give_up<kCtas>(c, p, rank);
 }
 
+// Q of a row tile: three boxes, one lane each (of a pair, the first CTA expects
+// both CTAs' bytes).
 template <int kCtas>
-__device__ __forceinline__ void produce(uint8_t* base, Ctl& c, const PrefillParams& p, const CUtensorMap* kn,
-                                        const CUtensorMap* kr, const CUtensorMap* v, uint32_t rank, int lane) {
-  using R = Ring<kCtas>;
+__device__ __forceinline__ bool load_q(uint8_t* base, Ctl<kCtas>& c, const CUtensorMap* qn, const CUtensorMap* qr,
+                                       uint32_t rank, int lane, int g, uint32_t use, int h, int row) {
+  if (use > 0 && !wait_bar(&c.qfree[g], (use - 1) & 1, &c.abort_flag)) return false;
+  if (lane == 0 && rank == 0) mbar_arrive_expect_tx(smem_u32(&c.q[g]), 3 * kBox * kCtas);
+  __syncwarp();
+  if (lane < 3)
+    load_3d<kCtas>(smem_u32(base + (3 * g + lane) * kBox), lane < 2 ? qn : qr, lead_bar<kCtas>(&c.q[g]),
+                   lane < 2 ? lane * 64 : 0, h, row + (g * kCtas + (int)rank) * kRows);
+  __syncwarp();
+  return true;
+}
+
+template <int kCtas>
+__device__ __forceinline__ void produce(uint8_t* base, Ctl<kCtas>& c, const PrefillParams& p, const CUtensorMap* qn,
+                                        const CUtensorMap* qr, const CUtensorMap* kn, const CUtensorMap* kr,
+                                        const CUtensorMap* v, uint32_t rank, int lane) {
+  using F = Form<kCtas>;
   Units<kCtas> units(c);
   bool ok = true;
-  uint32_t pos = 0, cleans = 0;
+  uint32_t pos = 0, cleans = 0, uses = 0;
   while (const Unit* up = units.next(ok)) {
     const int h = up->h, k0 = up->k0, j0 = up->j0, j1 = up->j1, clean0 = up->clean0;
+    const int row = up->q0 + up->row0;
 #pragma unroll 1
     for (int j = j0; j < j1 && ok; ++j) {
       const int tok = k0 + j * kKeys;
 #pragma unroll 1
-      for (int i = 0; i < R::kTile && ok; ++i, ++pos) {
-        const uint32_t piece = pos % R::kAll, use = pos / R::kAll;
+      for (int i = 0; i < F::kTile && ok; ++i, ++pos) {
+        // Q after the first keys
+        if (kCtas == 1 && j == j0 && i == F::kK && !(ok = load_q<kCtas>(base, c, qn, qr, rank, lane, 0, uses++, h, row)))
+          break;
+        const uint32_t piece = pos % F::kAll, use = pos / F::kAll;
         if (use > 0 && !(ok = wait_bar(&c.empty[piece], (use - 1) & 1, &c.abort_flag))) break;
-        const uint32_t dst = smem_u32(base + 6 * kBox + R::at(piece));
-        if (i < R::kK) {
+        const uint32_t dst = smem_u32(base + F::kQBytes + F::at(piece));
+        if (i < F::kK) {
           const int first = tok + (int)rank * (kKeys / kCtas);  // a pair's CTA: its half of the tokens
-          if (lane == 0 && rank == 0) mbar_arrive_expect_tx(smem_u32(&c.full[piece]), 3 * kBox / R::kK);
+          if (lane == 0 && rank == 0) mbar_arrive_expect_tx(smem_u32(&c.full[piece]), 3 * kBox / F::kK);
           __syncwarp();
           const uint32_t bar = lead_bar<kCtas>(&c.full[piece]);
           // a box a lane: 64 dims of k_nope, 64 more, k_rope
           const int box = kCtas == 1 ? i : lane;
           if (kCtas == 1 ? lane == 0 : lane < 3)
-            load_3d<kCtas>(dst + (kCtas == 1 ? 0 : lane * R::kHalfBox), box < 2 ? kn : kr, bar, box < 2 ? box * 64 : 0,
+            load_3d<kCtas>(dst + (kCtas == 1 ? 0 : lane * F::kHalfBox), box < 2 ? kn : kr, bar, box < 2 ? box * 64 : 0,
                            box < 2 ? h : 0, first);
         } else if (lane == 0) {
-          const int first = tok + (i - R::kK) * 64;             // a pair's CTA: its half of the dims
+          const int first = tok + (i - F::kK) * 64;             // a pair's CTA: its half of the dims
           if (j >= clean0) {
             // its piece is full once it is clean
             const uint32_t raw = smem_u32(&c.raw[(cleans + (j - clean0)) % kRaw]);
-            if (i == R::kK) mbar_arrive_expect_tx(raw, kVBytes / kCtas);
+            if (i == F::kK) mbar_arrive_expect_tx(raw, kVBytes / kCtas);
             tma_load_4d(dst, v, raw, 0, first, (int)rank, h);
           } else {
-            if (rank == 0) mbar_arrive_expect_tx(smem_u32(&c.full[piece]), kVBytes / R::kV);
+            if (rank == 0) mbar_arrive_expect_tx(smem_u32(&c.full[piece]), kVBytes / F::kV);
             load_4d<kCtas>(dst, v, lead_bar<kCtas>(&c.full[piece]), 0, first, (int)rank, h);
           }
         }
@@ -418,40 +493,29 @@ __device__ __forceinline__ void produce(uint8_t* base, Ctl& c, const PrefillPara
   // one, the MMAs have used them all).
   if (!ok) {
     int never = 0;
-    for (uint32_t k = pos > (uint32_t)R::kAll ? pos - R::kAll : 0; rank == 0 && k < pos; ++k)
-      wait_bar(&c.full[k % R::kAll], (k / R::kAll) & 1, &never);
+    if (kCtas == 1 && uses > 0) wait_bar(&c.q[0], (uses - 1) & 1, &never);
+    for (uint32_t k = pos > (uint32_t)F::kAll ? pos - F::kAll : 0; rank == 0 && k < pos; ++k)
+      wait_bar(&c.full[k % F::kAll], (k / F::kAll) & 1, &never);
   }
 }
 
-// Q of both row tiles, as soon as the unit before has used its own up: three boxes
-// for each, one lane each.
-template <int kCtas>
-__device__ __forceinline__ void load_queries(uint8_t* base, Ctl& c, const PrefillParams& p, const CUtensorMap* qn,
+// A pair's Q has a warp of its own: it waits for the unit before to have used its
+// up, which keys and values need not.
+__device__ __forceinline__ void load_queries(uint8_t* base, Ctl<2>& c, const PrefillParams& p, const CUtensorMap* qn,
                                              const CUtensorMap* qr, uint32_t rank, int lane) {
-  Units<kCtas> units(c);
+  Units<2> units(c);
   bool ok = true;
   uint32_t uses[2] = {0, 0};
   while (const Unit* u = units.next(ok)) {
-    const int h = u->h, row0 = u->q0 + u->row0, j0 = u->j0;
+    const int h = u->h, row = u->q0 + u->row0, j0 = u->j0;
     const int n[2] = {u->n0, u->n1};
 #pragma unroll
-    for (int g = 0; g < 2; ++g) {
-      if (n[g] <= j0) continue;
-      if (uses[g] > 0) ok = ok && wait_bar(&c.qfree[g], (uses[g] - 1) & 1, &c.abort_flag);
-      if (!ok) break;
-      ++uses[g];
-      // (of a pair, the first CTA expects both CTAs' bytes)
-      if (lane == 0 && rank == 0) mbar_arrive_expect_tx(smem_u32(&c.q[g]), 3 * kBox * kCtas);
-      __syncwarp();
-      if (lane < 3)
-        load_3d<kCtas>(smem_u32(base + (3 * g + lane) * kBox), lane < 2 ? qn : qr, lead_bar<kCtas>(&c.q[g]),
-                       lane < 2 ? lane * 64 : 0, h, row0 + (g * kCtas + (int)rank) * kRows);
-    }
+    for (int g = 0; g < 2; ++g)
+      if (n[g] > j0) ok = ok && load_q<2>(base, c, qn, qr, rank, lane, g, uses[g]++, h, row);
     if (!ok) break;
-    __syncwarp();
     if (lane == 0) units.release(); else units.skip();
   }
-  if (!ok && lane == 0) give_up<kCtas>(c, p, rank);
+  if (!ok && lane == 0) give_up<2>(c, p, rank);
   // After an abort: every load issued has landed before the CTA may exit.
   if (!ok && rank == 0) {
     int never = 0;
@@ -463,13 +527,13 @@ __device__ __forceinline__ void load_queries(uint8_t* base, Ctl& c, const Prefil
 // The whole warp runs the loop, so that what the MMAs take stays in uniform
 // registers; one lane issues.
 template <int kCtas>
-__device__ __forceinline__ void issue_mmas(uint8_t* base, Ctl& c, const PrefillParams& p, uint32_t tmem, int lane) {
-  using R = Ring<kCtas>;
+__device__ __forceinline__ void issue_mmas(uint8_t* base, Ctl<kCtas>& c, const PrefillParams& p, uint32_t tmem, int lane) {
+  using F = Form<kCtas>;
   const uint64_t qd = sdesc_sw128(smem_u32(base), 16, 1024);
-  const uint64_t kd = sdesc_sw128(smem_u32(base + 6 * kBox), 16, 1024);
+  const uint64_t kd = sdesc_sw128(smem_u32(base + F::kQBytes), 16, 1024);
   // V: MN-major, the next 64 dims 8 KB (LBO) on, the next 8 tokens 1 KB (SBO) on,
   // the next 16 tokens 2 KB; P: 16 tokens in 8 columns
-  const uint64_t vd = sdesc_sw128(smem_u32(base + 6 * kBox), kBox / 2, 1024);
+  const uint64_t vd = sdesc_sw128(smem_u32(base + F::kQBytes), kBox / 2, 1024);
   const bool lead = elect_one();
   bool ok = true;
   const auto wait = [&](uint64_t* bar, uint32_t parity) {
@@ -477,7 +541,7 @@ __device__ __forceinline__ void issue_mmas(uint8_t* base, Ctl& c, const PrefillP
     return ok;
   };
   Units<kCtas> units(c);
-  Cursor<kCtas> kc{0, 0}, vc{R::kK, 0};         // K(t) and V(t - 1)
+  Cursor<kCtas> kc{0, 0}, vc{F::kK, 0};         // K(t) and V(t - 1)
   uint32_t ps0 = 0, ps1 = 0, qs0 = 0, qs1 = 0;  // tiles and units of each row tile so far
   while (const Unit* u = units.next(ok)) {
     const int j0 = __shfl_sync(~0u, u->j0, 0), tiles = __shfl_sync(~0u, u->j1, 0) - j0;
@@ -486,14 +550,14 @@ __device__ __forceinline__ void issue_mmas(uint8_t* base, Ctl& c, const PrefillP
 #pragma unroll 1
     for (int t = 0; t <= tiles && ok; ++t) {
 #pragma unroll 1
-      for (int g = 0; g < 2; ++g) {
-        const uint32_t s = tmem + g * kKeys, o = tmem + (2 + g) * kKeys;
+      for (int g = 0; g < F::kTiles; ++g) {
+        const uint32_t s = tmem + g * kKeys, o = tmem + (F::kTiles + g) * kKeys;
         const int a = g ? a1 : a0;
         if (t > 0 && t - 1 < a) {
           Cursor<kCtas> at = vc;
 #pragma unroll
           for (int i = 0; i < 2; ++i) {  // 64 tokens
-            if ((R::kV == 2 || i == 0) && (g == 0 || t - 1 >= a0)) {
+            if ((F::kV == 2 || i == 0) && (g == 0 || t - 1 >= a0)) {
               if (!wait(&c.full[at.piece], at.phase)) break;
               // cleaned by the other CTA's threads, too
               if (kCtas == 2 && t - 1 >= clean) fence_cluster();
@@ -501,13 +565,13 @@ __device__ __forceinline__ void issue_mmas(uint8_t* base, Ctl& c, const PrefillP
             if ((kCtas == 2 || i == 0) && !wait(&c.p[g][kCtas == 1 ? 1 : i], ((g ? ps1 : ps0) + t - 1) & 1)) break;
             tc_fence_after();
             if (lead) {
-              const uint64_t b = plus(vd, (R::at(at.piece) + (R::kV == 1 ? i * R::kHalfBox : 0)) >> 4);
+              const uint64_t b = plus(vd, (F::at(at.piece) + (F::kV == 1 ? i * F::kHalfBox : 0)) >> 4);
 #pragma unroll
               for (int k = 0; k < 4; ++k)
                 mma_pv<kCtas>(o, s + (4 * i + k) * 8, plus(b, 128 * k), (t > 1 || i || k) ? 1u : 0u);
-              if ((R::kV == 2 || i == 1) && (g || t - 1 >= a1)) commit<kCtas>(&c.empty[at.piece]);
+              if ((F::kV == 2 || i == 1) && (g + 1 == F::kTiles || t - 1 >= a1)) commit<kCtas>(&c.empty[at.piece]);
             }
-            if (R::kV == 2) at.next();
+            if (F::kV == 2) at.next();
           }
           if (!ok) break;
           if (lead && t == a) commit<kCtas>(&c.o[g]);
@@ -516,15 +580,15 @@ __device__ __forceinline__ void issue_mmas(uint8_t* base, Ctl& c, const PrefillP
           if (t == 0 && !wait(&c.q[g], (g ? qs1 : qs0) & 1)) break;
           Cursor<kCtas> at = kc;
 #pragma unroll
-          for (int i = 0; i < R::kK; ++i, at.next()) {
+          for (int i = 0; i < F::kK; ++i, at.next()) {
             if ((g == 0 || t >= a0) && !wait(&c.full[at.piece], at.phase)) break;
             if (lead) {
-              const uint64_t q = plus(qd, (3 * g + i) * (kBox >> 4)), b = plus(kd, R::at(at.piece) >> 4);
+              const uint64_t q = plus(qd, (3 * g + i) * (kBox >> 4)), b = plus(kd, F::at(at.piece) >> 4);
 #pragma unroll
-              for (int k = 0; k < 12 / R::kK; ++k)
+              for (int k = 0; k < 12 / F::kK; ++k)
                 mma_qk<kCtas>(s, plus(q, k / 4 * (kBox >> 4) + 2 * (k % 4)),
-                              plus(b, k / 4 * (R::kHalfBox >> 4) + 2 * (k % 4)), (i || k) ? 1u : 0u);
-              if (g || t >= a1) commit<kCtas>(&c.empty[at.piece]);
+                              plus(b, k / 4 * (F::kHalfBox >> 4) + 2 * (k % 4)), (i || k) ? 1u : 0u);
+              if (g + 1 == F::kTiles || t >= a1) commit<kCtas>(&c.empty[at.piece]);
             }
           }
           if (!ok) break;
@@ -534,12 +598,12 @@ __device__ __forceinline__ void issue_mmas(uint8_t* base, Ctl& c, const PrefillP
           }
         }
       }
-      if (t < tiles) kc.skip(R::kTile);
-      if (t > 0) vc.skip(R::kTile);
+      if (t < tiles) kc.next_tile();
+      if (t > 0) vc.next_tile();
     }
     if (!ok) break;
     if (a0 > 0) ps0 += a0, ++qs0;
-    if (a1 > 0) ps1 += a1, ++qs1;
+    if (F::kTiles == 2 && a1 > 0) ps1 += a1, ++qs1;
     __syncwarp();
     if (lead) units.release(); else units.skip();
   }
@@ -551,33 +615,38 @@ __device__ __forceinline__ void issue_mmas(uint8_t* base, Ctl& c, const PrefillP
 }
 
 // Tiles from u.clean0 on hold tokens that some row does not see (its own later
-// ones, or the next sequence's).  A warp cleans 16 KB at a time: on one CTA warp i
-// of the two piece i of a tile's V; in a pair they take turns with the tiles.
+// ones, or the next sequence's).  A warp cleans 16 KB at a time: on one CTA a
+// tile's pieces one after the other; a pair's two warps take turns with the tiles.
 template <int kCtas>
-__device__ __forceinline__ void clean_values(uint8_t* base, Ctl& c, const PrefillParams& p, uint32_t rank, int i,
+__device__ __forceinline__ void clean_values(uint8_t* base, Ctl<kCtas>& c, const PrefillParams& p, uint32_t rank, int i,
                                              int lane) {
-  using R = Ring<kCtas>;
+  using F = Form<kCtas>;
   constexpr int kBatch = 8, kVecs = kBox / 16;  // 16-byte vectors: in flight per lane, of a job
   Units<kCtas> units(c);
   bool ok = true;
   uint32_t at = 0, cleans = 0;  // pieces and cleaned tiles so far
   while (const Unit* u = units.next(ok)) {
     const int j0 = u->j0, j1 = u->j1, clean0 = u->clean0, unseen = u->unseen, lk = u->lk;
-    const uint32_t tag = tag_of(units.nth);
     bool first = true;
+    if (kCtas == 1 && units.nth % Notes<1>::kWipe == 0 && units.nth > 0) {
+      if (!(ok = __all_sync(~0u, wait_bar(&c.done, (units.nth - 1) & 1, &c.abort_flag)))) break;
+      for (int d = lane; d < kKeys; d += 32) c.notes.clear(d);
+      __syncwarp();
+    }
 #pragma unroll 1
-    for (int j = clean0; j < j1; ++j) {
+    for (int x = kCtas == 1 ? 2 * clean0 : clean0; x < (kCtas == 1 ? 2 * j1 : j1); ++x) {
+      const int j = kCtas == 1 ? x >> 1 : x, half = kCtas == 1 ? x & 1 : 0;
       const uint32_t nth = cleans + (j - clean0);
       if (kCtas == 2 && (nth & 1) != (uint32_t)i) continue;
-      if (!(ok = __all_sync(~0u, wait_bar(&c.raw[nth % kRaw], nth / kRaw & 1, &c.abort_flag)))) break;
+      if (half == 0 && !(ok = __all_sync(~0u, wait_bar(&c.raw[nth % kRaw], nth / kRaw & 1, &c.abort_flag)))) break;
       // the notes on the unit before have been read (by both CTAs)
       if (first && units.nth > 0 &&
           !(ok = __all_sync(~0u, wait_bar<kCtas == 2>(&c.done, (units.nth - 1) & 1, &c.abort_flag))))
         break;
       first = false;
-      const uint32_t piece = (at + R::kTile * (j - j0) + R::kK + (kCtas == 1 ? i : 0)) % R::kAll;
-      uint4* box = reinterpret_cast<uint4*>(base + 6 * kBox + R::at(piece));
-      const int t0 = j * kKeys + (kCtas == 1 ? i * 64 : 0);  // token of the first row
+      const uint32_t piece = (at + F::kTile * (j - j0) + F::kK + half) % F::kAll;
+      uint4* box = reinterpret_cast<uint4*>(base + F::kQBytes + F::at(piece));
+      const int t0 = j * kKeys + half * 64;  // token of the first row
 #pragma unroll 1
       for (int x0 = lane; x0 < kVecs; x0 += 32 * kBatch) {
         uint4 w[kBatch];
@@ -592,21 +661,17 @@ __device__ __forceinline__ void clean_values(uint8_t* base, Ctl& c, const Prefil
         // some value of these is not finite: half (64 dims), row, chunk, swizzled by the row
 #pragma unroll 1
         for (int e = 0; e < 8 * kBatch; ++e) {
-          const int x = x0 + e / 8 * 32;
-          const int half = kCtas == 1 ? x >> 9 : (int)rank, row = (x >> 3) & (kCtas == 1 ? 63 : 127);
-          uint16_t* val = reinterpret_cast<uint16_t*>(box + x) + e % 8;
+          const int v = x0 + e / 8 * 32;
+          const int dims = kCtas == 1 ? v >> 9 : (int)rank, row = (v >> 3) & (kCtas == 1 ? 63 : 127);
+          uint16_t* val = reinterpret_cast<uint16_t*>(box + v) + e % 8;
           const uint32_t bits = *val;
           if ((bits & 0x7f80u) != 0x7f80u || t0 + row < unseen) continue;
           *val = 0;
-          const int past = t0 + row - unseen, dim = half * 64 + ((x & 7) ^ (row & 7)) * 8 + e % 8;
-          if (t0 + row < lk && past < 1 << kOffsetBits) {  // past that no row of the unit sees it
-            uint32_t* odd = &c.odd[bits & 0x7fu ? 0 : bits & 0x8000u ? 2 : 1][dim];
-            atomicMin(odd, tag | past);
-            atomicMin(&c.any_odd, tag);
-            if constexpr (kCtas == 2) {
-              red_min_cluster_u32(mapa(smem_u32(odd), rank ^ 1), tag | past);
-              red_min_cluster_u32(mapa(smem_u32(&c.any_odd), rank ^ 1), tag);
-            }
+          const int past = t0 + row - unseen, dim = dims * 64 + ((v & 7) ^ (row & 7)) * 8 + e % 8;
+          if (t0 + row < lk && past < F::kBlock) {  // past that no row of the unit sees it
+            c.notes.add(units.nth, bits & 0x7fu ? 0 : bits & 0x8000u ? 2 : 1, dim, past, rank);
+            c.any_odd = units.nth + 1;
+            if constexpr (kCtas == 2) st_cluster_u32(mapa(smem_u32(&c.any_odd), rank ^ 1), units.nth + 1);
           }
         }
       }
@@ -619,7 +684,7 @@ __device__ __forceinline__ void clean_values(uint8_t* base, Ctl& c, const Prefil
       }
     }
     if (!ok) break;
-    at += R::kTile * (j1 - j0);
+    at += F::kTile * (j1 - j0);
     if (j1 > clean0) {
       cleans += j1 - clean0;
       if (lane == 0) {
@@ -635,11 +700,11 @@ __device__ __forceinline__ void clean_values(uint8_t* base, Ctl& c, const Prefil
 
 // Softmax of row tile g, one thread per row, then the row's output.
 template <int kCtas>
-__device__ __forceinline__ void softmax_rows(Ctl& c, const PrefillParams& p, uint32_t tmem, uint32_t rank, int g,
+__device__ __forceinline__ void softmax_rows(Ctl<kCtas>& c, const PrefillParams& p, uint32_t tmem, uint32_t rank, int g,
                                              int warp, int lane) {
   const int r = (warp & 3) * 32 + lane, in_block = (g * kCtas + (int)rank) * kRows + r;
   const uint32_t quad = (uint32_t)((warp & 3) * 32) << 16;
-  const uint32_t s_at = tmem + quad + g * kKeys, o_at = tmem + quad + (2 + g) * kKeys;
+  const uint32_t s_at = tmem + quad + g * kKeys, o_at = tmem + quad + (Form<kCtas>::kTiles + g) * kKeys;
   const uint64_t scale2 = f2pack(p.scale2, p.scale2);
   const uint32_t lead_p = lead_bar<kCtas>(&c.p[g][0]), lead_note = kCtas == 1 ? 0 : mapa(smem_u32(&c.note), 0);
   // half i of a tile's P is in tensor memory
@@ -752,8 +817,8 @@ __device__ __forceinline__ void softmax_rows(Ctl& c, const PrefillParams& p, uin
                               : ((int64_t)(u->slot + in_block / kSlot) * p.H + u->h) * kSlot + in_block % kSlot;
     const int unseen = u->unseen - u->j0 * kKeys;
     // notes of this unit: tokens that the row sees get their values back
-    const uint32_t tag = tag_of(units.nth), reach = tag + (uint32_t)min(max(seen - unseen, 0), 1 << kOffsetBits);
-    const bool odd = cleaned && *reinterpret_cast<volatile uint32_t*>(&c.any_odd) == tag;
+    const uint32_t reach = (uint32_t)min(max(seen - unseen, 0), Form<kCtas>::kBlock);
+    const bool odd = cleaned && *reinterpret_cast<volatile uint32_t*>(&c.any_odd) == units.nth + 1;
     __nv_bfloat16* out = p.out + row * MLA_V_HEAD_DIM;
     float* part = p.O_part + row * MLA_V_HEAD_DIM;
 #pragma unroll 1
@@ -780,9 +845,9 @@ __device__ __forceinline__ void softmax_rows(Ctl& c, const PrefillParams& p, uin
 #pragma unroll 1
       for (int e = 0; e < kKeys; ++e) {
         float add = 0.f;
-        if (c.odd[0][e] < reach) add = NAN;
-        if (c.odd[1][e] < reach) add += INFINITY;
-        if (c.odd[2][e] < reach) add -= INFINITY;
+        if (c.notes.below(units.nth, 0, e, reach)) add = NAN;
+        if (c.notes.below(units.nth, 1, e, reach)) add += INFINITY;
+        if (c.notes.below(units.nth, 2, e, reach)) add -= INFINITY;
         if (add == 0.f) continue;
         if (whole) out[e] = __float2bfloat16(__bfloat162float(out[e]) + add);
         else part[e] += add;
@@ -806,33 +871,37 @@ __device__ __forceinline__ void softmax_rows(Ctl& c, const PrefillParams& p, uin
 }
 
 template <int kCtas>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Form<kCtas>::kThreads, kCtas == 1 ? 2 : 1)
     mla_prefill_kernel(const __grid_constant__ CUtensorMap qn, const __grid_constant__ CUtensorMap qr,
                        const __grid_constant__ CUtensorMap kn, const __grid_constant__ CUtensorMap kr,
                        const __grid_constant__ CUtensorMap v, const PrefillParams p) {
   extern __shared__ __align__(1024) uint8_t base[];
-  Ctl& c = *reinterpret_cast<Ctl*>(base + 6 * kBox + kRing);
+  using F = Form<kCtas>;
+  Ctl<kCtas>& c = *reinterpret_cast<Ctl<kCtas>*>(base + F::kQBytes + F::kRing);
   const int warp = __shfl_sync(~0u, (int)threadIdx.x / 32, 0), lane = threadIdx.x % 32;
   const uint32_t rank = kCtas == 1 ? 0 : __shfl_sync(~0u, cluster_ctarank(), 0);
   if (threadIdx.x == 0) {
     c.abort_flag = 0;
-    c.any_odd = ~0u;
-    for (int g = 0; g < 2; ++g) {
+    c.any_odd = 0;
+    for (int g = 0; g < F::kTiles; ++g) {
       mbar_init(smem_u32(&c.q[g]), 1);
       mbar_init(smem_u32(&c.qfree[g]), 1);
       mbar_init(smem_u32(&c.s[g]), 1);
       for (int i = 0; i < 2; ++i) mbar_init(smem_u32(&c.p[g][i]), 4);
       mbar_init(smem_u32(&c.o[g]), 1);
-      mbar_init(smem_u32(&c.unit_full[g]), 1);
-      mbar_init(smem_u32(&c.unit_empty[g]), 13);  // 2 TMA, MMA, 2 cleaning, 8 softmax warps
     }
-    for (int i = 0; i < Ring<kCtas>::kAll; ++i) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&c.unit_full[i]), 1);
+      // TMA (a pair: two warps), MMA, cleaning, softmax
+      mbar_init(smem_u32(&c.unit_empty[i]), kCtas + 1 + F::kCleaners + F::kSoftmax);
+    }
+    for (int i = 0; i < Form<kCtas>::kAll; ++i) {
       mbar_init(smem_u32(&c.full[i]), 1);
       mbar_init(smem_u32(&c.empty[i]), 1);
     }
     for (int i = 0; i < kRaw; ++i) mbar_init(smem_u32(&c.raw[i]), 1);
-    mbar_init(smem_u32(&c.cleaned), 2 * kCtas);
-    mbar_init(smem_u32(&c.done), 8 * kCtas);
+    mbar_init(smem_u32(&c.cleaned), F::kCleaners * kCtas);
+    mbar_init(smem_u32(&c.done), F::kSoftmax * kCtas);
     mbar_init(smem_u32(&c.answer_full), 1);
     mbar_init(smem_u32(&c.answer_free), 1);
     mbar_init(smem_u32(&c.drain), 1);
@@ -843,13 +912,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     prefetch_tmap(&kr);
     prefetch_tmap(&v);
   }
-  for (int i = threadIdx.x; i < 3 * kKeys; i += kThreads) c.odd[i / kKeys][i % kKeys] = ~0u;
-  if (warp == kWarpMma) {
+  if (threadIdx.x < kKeys) c.notes.clear(threadIdx.x);
+  if (warp == F::kMma) {
     if constexpr (kCtas == 1) {
-      tmem_alloc(smem_u32(&c.tmem), 512);
+      tmem_alloc(smem_u32(&c.tmem), F::kColumns);
       tmem_relinquish();
     } else {
-      tmem_alloc_pair(smem_u32(&c.tmem), 512);
+      tmem_alloc_pair(smem_u32(&c.tmem), F::kColumns);
       tmem_relinquish_pair();
     }
   }
@@ -865,18 +934,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     if constexpr (kCtas == 2) cluster_sync();
     tc_fence_after();
-    if (warp == kWarpMma) {
-      if constexpr (kCtas == 1) tmem_dealloc(tmem, 512);
-      else tmem_dealloc_pair(tmem, 512);
+    if (warp == F::kMma) {
+      if constexpr (kCtas == 1) tmem_dealloc(tmem, F::kColumns);
+      else tmem_dealloc_pair(tmem, F::kColumns);
     }
   };
-  if (warp >= kWarpTma) {
+  if (warp >= F::kSoftmax) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
-    if (warp == kWarpTma) {
-      produce<kCtas>(base, c, p, &kn, &kr, &v, rank, lane);
-    } else if (warp == kWarpQ) {
-      load_queries<kCtas>(base, c, p, &qn, &qr, rank, lane);
-    } else if (warp == kWarpMma) {
+    if (warp == F::kTma) {
+      produce<kCtas>(base, c, p, &qn, &qr, &kn, &kr, &v, rank, lane);
+    } else if (warp == F::kMma) {
       if (rank == 0) {
         issue_mmas<kCtas>(base, c, p, tmem, lane);
       } else if (lane == 0) {  // passes the units on
@@ -886,10 +953,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         int never = 0;
         wait_bar(&c.drain, 0, &never);
       }
-    } else if (warp == kWarpNext) {
+    } else if (warp == F::kNext) {
       if (lane == 0) feed<kCtas>(c, p, rank);
-    } else if (warp == kWarpClean || warp == kWarpClean + 1) {
-      clean_values<kCtas>(base, c, p, rank, warp - kWarpClean, lane);
+    } else if (warp >= F::kClean && warp < F::kClean + F::kCleaners) {
+      clean_values<kCtas>(base, c, p, rank, warp - F::kClean, lane);
+    } else if constexpr (kCtas == 2) {
+      if (warp == F::kQ) load_queries(base, c, p, &qn, &qr, rank, lane);
     }
     teardown();
   } else {
@@ -903,11 +972,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 // order.  Parts without keys (LSE = -inf) weigh nothing; a NaN makes the row NaN.
 template <int kCtas>
 __global__ void __launch_bounds__(256) mla_prefill_merge_kernel(const PrefillParams p) {
-  constexpr int kBlock = kSlot * kCtas;
+  constexpr int kBlock = Form<kCtas>::kBlock, kSlots = kBlock / kSlot;
   const int32_t* e = p.work + (int64_t)(blockIdx.x / p.H) * kEntry * kCtas;
   const int h = blockIdx.x % p.H, seq = e[0], parts = e[3], slot = e[4];
   if (e[2] != 0 || parts < 2 || parts > MLA_PREFILL_MAX_PARTS || slot < 0 ||
-      slot > p.num_parts - parts * kCtas || seq < 0 || seq >= p.N || e[1] < 0 || e[7] != kBlock)
+      slot > 2 * (int64_t)p.num_parts - parts * kSlots || seq < 0 || seq >= p.N || e[1] < 0 || e[7] != kBlock)
     return;  // reported by the first launch
   const int64_t q0 = p.cu_q[seq], lq = p.cu_q[seq + 1] - q0, row0 = (int64_t)e[1] * kBlock;
   const int64_t k0 = p.cu_kv[seq], lk = p.cu_kv[seq + 1] - k0;
@@ -915,7 +984,7 @@ __global__ void __launch_bounds__(256) mla_prefill_merge_kernel(const PrefillPar
   const int rows = (int)min((int64_t)kBlock, lq - row0), lane = threadIdx.x & 31;
   for (int r = threadIdx.x / 32; r < rows; r += 8) {
     const int64_t at = ((int64_t)(slot + r / kSlot) * p.H + h) * kSlot + r % kSlot;
-    const int64_t step = (int64_t)kCtas * p.H * kSlot;
+    const int64_t step = (int64_t)kSlots * p.H * kSlot;
     const float mine = lane < parts ? p.LSE_part[at + lane * step] : -INFINITY;
     float m = mine;
 #pragma unroll
@@ -954,13 +1023,13 @@ template <int kCtas>
 int launch_prefill(const CUtensorMap& qn, const CUtensorMap& qr, const CUtensorMap& kn, const CUtensorMap& kr,
                    const CUtensorMap& v, const PrefillParams& p, cudaStream_t st) {
   auto kernel = mla_prefill_kernel<kCtas>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem<kCtas>);
   if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(mla_prefill_kernel)");
   const unsigned units = (unsigned)p.num_work * (unsigned)p.H;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(units * kCtas, 1, 1);
-  cfg.blockDim = dim3(kThreads, 1, 1);
-  cfg.dynamicSmemBytes = kSmem;
+  cfg.blockDim = dim3(Form<kCtas>::kThreads, 1, 1);
+  cfg.dynamicSmemBytes = kSmem<kCtas>;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;

@@ -238,12 +238,12 @@ def test_bad_work_and_lengths_are_reported(ctas):
 
     assert status_of(work) == 0
     for column, value in ((0, 2), (0, -1), (1, 1), (1, -1), (2, 1), (2, -1), (3, 0), (3, 33), (5, 5), (5, -1),
-                          (6, 0), (6, 9), (7, 128 * ctas)):
+                          (6, 0), (6, 9), (7, 256)):
         bad = work.copy()
         bad[0, ..., column] = value
         assert status_of(bad) == mla.STATUS_BAD_WORK, (column, value)
     bad = work.copy()
-    bad[0, ..., 2:5] = 0, 2, 1
+    bad[0, ..., 2:5] = 0, 2, 3
     assert status_of(bad, num_parts=2 * ctas) == mla.STATUS_BAD_WORK
     assert status_of(work, cu_q=_cu([100, 31])) == mla.STATUS_BAD_LENGTH
     assert status_of(work, cu_kv=_cu([131, 0])) == mla.STATUS_BAD_LENGTH
