@@ -101,6 +101,12 @@ struct Cursor {
   }
 };
 
+// Tensor maps; [1]: boxes of 32 rows, for the ends of sequences (one CTA).
+struct PrefillMaps {
+  CUtensorMap qn[2], qr[2], kn[2], kr[2], v[2];
+};
+constexpr int kFew = 32, kFewBytes = kFew * 128;
+
 struct PrefillParams {
   const int32_t* cu_q;
   const int32_t* cu_kv;
@@ -127,6 +133,7 @@ struct Unit {
   int j0, j1, n0, n1;
   int clean0;               // first tile whose V is cleaned
   int unseen;               // first key that some row does not see
+  int end;                  // keys that some row sees
 };
 
 // Notes on cleaned values: per kind (NaN, +inf, -inf) and dim the first such token,
@@ -253,6 +260,7 @@ __device__ __forceinline__ bool find_unit(const PrefillParams& p, int x, Unit& u
   u.n0 = min(n0, u.j1);
   u.n1 = min(n1, u.j1);
   u.unseen = sees(p, u.lq, u.lk, prefix, u.row0);
+  u.end = sees(p, u.lq, u.lk, prefix, u.row0 + u.rows - 1);
   u.clean0 = max(u.j0, u.unseen / kKeys);
   return true;
 }
@@ -321,17 +329,6 @@ template <int kCtas>
 __device__ __forceinline__ uint32_t lead_bar(uint64_t* bar) {
   if constexpr (kCtas == 1) return smem_u32(bar);
   else return mapa(smem_u32(bar), 0);
-}
-template <int kCtas>
-__device__ __forceinline__ void load_3d(uint32_t dst, const CUtensorMap* m, uint32_t bar, int x, int y, int z) {
-  if constexpr (kCtas == 1) tma_load_3d(dst, m, bar, x, y, z);
-  else tma_load_3d_pair(dst, m, bar, x, y, z);
-}
-template <int kCtas>
-__device__ __forceinline__ void load_4d(uint32_t dst, const CUtensorMap* m, uint32_t bar, int x, int y, int z,
-                                        int w) {
-  if constexpr (kCtas == 1) tma_load_4d(dst, m, bar, x, y, z, w);
-  else tma_load_4d_pair(dst, m, bar, x, y, z, w);
 }
 template <int kCtas>
 __device__ __forceinline__ void mma_qk(uint32_t d, uint64_t a, uint64_t b, uint32_t acc) {
@@ -421,63 +418,117 @@ __device__ __forceinline__ void feed(Ctl<kCtas>& c, const PrefillParams& p, uint
   give_up<kCtas>(c, p, rank);
 }
 
-// Q of a row tile: three boxes, one lane each (of a pair, the first CTA expects
-// both CTAs' bytes).
-template <int kCtas>
-__device__ __forceinline__ bool load_q(uint8_t* base, Ctl<kCtas>& c, const CUtensorMap* qn, const CUtensorMap* qr,
-                                       uint32_t rank, int lane, int g, uint32_t use, int h, int row) {
-  if (use > 0 && !wait_bar(&c.qfree[g], (use - 1) & 1, &c.abort_flag)) return false;
-  if (lane == 0 && rank == 0) mbar_arrive_expect_tx(smem_u32(&c.q[g]), 3 * kBox * kCtas);
-  __syncwarp();
-  if (lane < 3)
-    load_3d<kCtas>(smem_u32(base + (3 * g + lane) * kBox), lane < 2 ? qn : qr, lead_bar<kCtas>(&c.q[g]),
-                   lane < 2 ? lane * 64 : 0, h, row + (g * kCtas + (int)rank) * kRows);
-  __syncwarp();
-  return true;
-}
-
-template <int kCtas>
-__device__ __forceinline__ void produce(uint8_t* base, Ctl<kCtas>& c, const PrefillParams& p, const CUtensorMap* qn,
-                                        const CUtensorMap* qr, const CUtensorMap* kn, const CUtensorMap* kr,
-                                        const CUtensorMap* v, uint32_t rank, int lane) {
-  using F = Form<kCtas>;
-  Units<kCtas> units(c);
+// Where a unit's keys and values go through the ring: on one CTA, box by box.  Q
+// comes after the first keys.  At the ends of sequences only what some row needs is
+// loaded, in 32 rows: with sequences of a few hundred tokens the rest of a tile,
+// the next sequence's, would be a third more traffic (64 documents: 1.49 GB of reads
+// for 1.15).  What stays in shared memory there is masked, or cleaned.
+__device__ __forceinline__ void produce_one(uint8_t* base, Ctl<1>& c, const PrefillParams& p, const PrefillMaps& m,
+                                            int lane) {
+  using F = Form<1>;
+  const auto v_boxes = [](int left) { return left > kFew ? 1 : left > 0 ? 2 : 0; };
+  const auto v_bytes = [](int left) { return left > kFew ? kBox : left > 0 ? 2 * kFewBytes : 0; };
+  Units<1> units(c);
   bool ok = true;
   uint32_t pos = 0, cleans = 0, uses = 0;
-  while (const Unit* up = units.next(ok)) {
-    const int h = up->h, k0 = up->k0, j0 = up->j0, j1 = up->j1, clean0 = up->clean0;
-    const int row = up->q0 + up->row0;
+  while (const Unit* u = units.next(ok)) {
+    const int h = u->h, k0 = u->k0, j0 = u->j0, j1 = u->j1, clean0 = u->clean0, end = u->end;
+    const int row = u->q0 + u->row0, rows = u->rows;
+#pragma unroll 1
+    for (int j = j0; j < j1 && ok; ++j) {
+      const int left = end - j * kKeys;
+#pragma unroll 1
+      for (int i = 0; i < F::kTile; ++i, ++pos) {
+        if (j == j0 && i == F::kK) {
+          if (uses > 0 && !(ok = wait_bar(&c.qfree[0], (uses - 1) & 1, &c.abort_flag))) break;
+          ++uses;
+          const int few = rows > kRows - kFew ? 0 : 1, n = few ? (rows + kFew - 1) / kFew : 1;
+          if (lane == 0) mbar_arrive_expect_tx(smem_u32(&c.q[0]), 3 * (few ? n * kFewBytes : kBox));
+          __syncwarp();
+          if (lane < 3 * n) {
+            const int box = lane % 3, part = lane / 3;
+            tma_load_3d(smem_u32(base + box * kBox + part * kFewBytes), box < 2 ? &m.qn[few] : &m.qr[few],
+                        smem_u32(&c.q[0]), box < 2 ? box * 64 : 0, h, row + part * kFew);
+          }
+          __syncwarp();
+        }
+        const uint32_t piece = pos % F::kAll, use = pos / F::kAll;
+        if (use > 0 && !(ok = wait_bar(&c.empty[piece], (use - 1) & 1, &c.abort_flag))) break;
+        const uint32_t dst = smem_u32(base + F::kQBytes + F::at(piece));
+        uint32_t bar = smem_u32(&c.full[piece]);
+        if (i < F::kK) {
+          const int few = left > kKeys - kFew ? 0 : 1, n = few ? (left + kFew - 1) / kFew : 1;
+          if (lane == 0) mbar_arrive_expect_tx(bar, few ? n * kFewBytes : kBox);
+          __syncwarp();
+          if (lane < n)
+            tma_load_3d(dst + lane * kFewBytes, i < 2 ? &m.kn[few] : &m.kr[few], bar, i < 2 ? i * 64 : 0,
+                        i < 2 ? h : 0, k0 + j * kKeys + lane * kFew);
+        } else {
+          const int first = (i - F::kK) * 64, n = v_boxes(left - first);
+          if (j >= clean0) {
+            // its piece is full once it is clean; also one that gets nothing has to be
+            // free before it is cleaned
+            bar = smem_u32(&c.raw[(cleans + (j - clean0)) % kRaw]);
+            if (lane == 0 && n > 0) mbar_arrive_expect_tx(bar, v_bytes(left - first));
+            if (lane == 0 && n == 0) mbar_arrive(bar);
+          } else if (lane == 0) {
+            mbar_arrive_expect_tx(bar, kBox);  // (every row sees all of the tile)
+          }
+          __syncwarp();
+          if (lane < n)
+            tma_load_4d(dst + lane * (kBox / 2), &m.v[n == 1 ? 0 : 1], bar, 0, k0 + j * kKeys + first, lane, h);
+        }
+        __syncwarp();
+      }
+    }
+    if (!ok) break;
+    cleans += max(j1 - clean0, 0);
+    if (lane == 0) units.release(); else units.skip();
+  }
+  if (!ok && lane == 0) give_up<1>(c, p, 0);
+  // After an abort: every load issued has landed before the CTA may exit (without
+  // one, the MMAs have used them all).
+  if (!ok) {
+    int never = 0;
+    if (uses > 0) wait_bar(&c.q[0], (uses - 1) & 1, &never);
+    for (uint32_t k = pos > (uint32_t)F::kAll ? pos - F::kAll : 0; k < pos; ++k)
+      wait_bar(&c.full[k % F::kAll], (k / F::kAll) & 1, &never);
+  }
+}
+
+// The same for a pair: a CTA loads its half of a tile's tokens (K) or dims (V); the
+// first CTA expects both CTAs' bytes.
+__device__ __forceinline__ void produce_pair(uint8_t* base, Ctl<2>& c, const PrefillParams& p, const PrefillMaps& m,
+                                             uint32_t rank, int lane) {
+  using F = Form<2>;
+  Units<2> units(c);
+  bool ok = true;
+  uint32_t pos = 0, cleans = 0;
+  while (const Unit* u = units.next(ok)) {
+    const int h = u->h, k0 = u->k0, j0 = u->j0, j1 = u->j1, clean0 = u->clean0;
 #pragma unroll 1
     for (int j = j0; j < j1 && ok; ++j) {
       const int tok = k0 + j * kKeys;
 #pragma unroll 1
-      for (int i = 0; i < F::kTile && ok; ++i, ++pos) {
-        // Q after the first keys
-        if (kCtas == 1 && j == j0 && i == F::kK && !(ok = load_q<kCtas>(base, c, qn, qr, rank, lane, 0, uses++, h, row)))
-          break;
+      for (int i = 0; i < F::kTile; ++i, ++pos) {
         const uint32_t piece = pos % F::kAll, use = pos / F::kAll;
         if (use > 0 && !(ok = wait_bar(&c.empty[piece], (use - 1) & 1, &c.abort_flag))) break;
-        const uint32_t dst = smem_u32(base + F::kQBytes + F::at(piece));
-        if (i < F::kK) {
-          const int first = tok + (int)rank * (kKeys / kCtas);  // a pair's CTA: its half of the tokens
-          if (lane == 0 && rank == 0) mbar_arrive_expect_tx(smem_u32(&c.full[piece]), 3 * kBox / F::kK);
+        const uint32_t dst = smem_u32(base + F::kQBytes + F::at(piece)), bar = lead_bar<2>(&c.full[piece]);
+        if (i == 0) {
+          if (lane == 0 && rank == 0) mbar_arrive_expect_tx(smem_u32(&c.full[piece]), 3 * kBox);
           __syncwarp();
-          const uint32_t bar = lead_bar<kCtas>(&c.full[piece]);
-          // a box a lane: 64 dims of k_nope, 64 more, k_rope
-          const int box = kCtas == 1 ? i : lane;
-          if (kCtas == 1 ? lane == 0 : lane < 3)
-            load_3d<kCtas>(dst + (kCtas == 1 ? 0 : lane * F::kHalfBox), box < 2 ? kn : kr, bar, box < 2 ? box * 64 : 0,
-                           box < 2 ? h : 0, first);
+          if (lane < 3)  // a box a lane
+            tma_load_3d_pair(dst + lane * F::kHalfBox, lane < 2 ? &m.kn[0] : &m.kr[0], bar, lane < 2 ? lane * 64 : 0,
+                             lane < 2 ? h : 0, tok + (int)rank * (kKeys / 2));
         } else if (lane == 0) {
-          const int first = tok + (i - F::kK) * 64;             // a pair's CTA: its half of the dims
           if (j >= clean0) {
             // its piece is full once it is clean
             const uint32_t raw = smem_u32(&c.raw[(cleans + (j - clean0)) % kRaw]);
-            if (i == F::kK) mbar_arrive_expect_tx(raw, kVBytes / kCtas);
-            tma_load_4d(dst, v, raw, 0, first, (int)rank, h);
+            mbar_arrive_expect_tx(raw, kVBytes / 2);
+            tma_load_4d(dst, &m.v[0], raw, 0, tok, (int)rank, h);
           } else {
-            if (rank == 0) mbar_arrive_expect_tx(smem_u32(&c.full[piece]), kVBytes / F::kV);
-            load_4d<kCtas>(dst, v, lead_bar<kCtas>(&c.full[piece]), 0, first, (int)rank, h);
+            if (rank == 0) mbar_arrive_expect_tx(smem_u32(&c.full[piece]), kVBytes);
+            tma_load_4d_pair(dst, &m.v[0], bar, 0, tok, (int)rank, h);
           }
         }
         __syncwarp();
@@ -485,24 +536,20 @@ __device__ __forceinline__ void produce(uint8_t* base, Ctl<kCtas>& c, const Pref
     }
     if (!ok) break;
     cleans += max(j1 - clean0, 0);
-    __syncwarp();
     if (lane == 0) units.release(); else units.skip();
   }
-  if (!ok && lane == 0) give_up<kCtas>(c, p, rank);
-  // After an abort: every load issued has landed before the CTA may exit (without
-  // one, the MMAs have used them all).
+  if (!ok && lane == 0) give_up<2>(c, p, rank);
   if (!ok) {
     int never = 0;
-    if (kCtas == 1 && uses > 0) wait_bar(&c.q[0], (uses - 1) & 1, &never);
     for (uint32_t k = pos > (uint32_t)F::kAll ? pos - F::kAll : 0; rank == 0 && k < pos; ++k)
       wait_bar(&c.full[k % F::kAll], (k / F::kAll) & 1, &never);
   }
 }
 
 // A pair's Q has a warp of its own: it waits for the unit before to have used its
-// up, which keys and values need not.
-__device__ __forceinline__ void load_queries(uint8_t* base, Ctl<2>& c, const PrefillParams& p, const CUtensorMap* qn,
-                                             const CUtensorMap* qr, uint32_t rank, int lane) {
+// up, which keys and values need not.  Three boxes for each row tile.
+__device__ __forceinline__ void load_queries(uint8_t* base, Ctl<2>& c, const PrefillParams& p, const PrefillMaps& m,
+                                             uint32_t rank, int lane) {
   Units<2> units(c);
   bool ok = true;
   uint32_t uses[2] = {0, 0};
@@ -510,8 +557,18 @@ __device__ __forceinline__ void load_queries(uint8_t* base, Ctl<2>& c, const Pre
     const int h = u->h, row = u->q0 + u->row0, j0 = u->j0;
     const int n[2] = {u->n0, u->n1};
 #pragma unroll
-    for (int g = 0; g < 2; ++g)
-      if (n[g] > j0) ok = ok && load_q<2>(base, c, qn, qr, rank, lane, g, uses[g]++, h, row);
+    for (int g = 0; g < 2; ++g) {
+      if (n[g] <= j0) continue;
+      if (uses[g] > 0) ok = ok && wait_bar(&c.qfree[g], (uses[g] - 1) & 1, &c.abort_flag);
+      if (!ok) break;
+      ++uses[g];
+      if (lane == 0 && rank == 0) mbar_arrive_expect_tx(smem_u32(&c.q[g]), 3 * kBox * 2);
+      __syncwarp();
+      if (lane < 3)
+        tma_load_3d_pair(smem_u32(base + (3 * g + lane) * kBox), lane < 2 ? &m.qn[0] : &m.qr[0], lead_bar<2>(&c.q[g]),
+                         lane < 2 ? lane * 64 : 0, h, row + (g * 2 + (int)rank) * kRows);
+      __syncwarp();
+    }
     if (!ok) break;
     if (lane == 0) units.release(); else units.skip();
   }
@@ -872,9 +929,7 @@ __device__ __forceinline__ void softmax_rows(Ctl<kCtas>& c, const PrefillParams&
 
 template <int kCtas>
 __global__ void __launch_bounds__(Form<kCtas>::kThreads, kCtas == 1 ? 2 : 1)
-    mla_prefill_kernel(const __grid_constant__ CUtensorMap qn, const __grid_constant__ CUtensorMap qr,
-                       const __grid_constant__ CUtensorMap kn, const __grid_constant__ CUtensorMap kr,
-                       const __grid_constant__ CUtensorMap v, const PrefillParams p) {
+    mla_prefill_kernel(const __grid_constant__ PrefillMaps m, const PrefillParams p) {
   extern __shared__ __align__(1024) uint8_t base[];
   using F = Form<kCtas>;
   Ctl<kCtas>& c = *reinterpret_cast<Ctl<kCtas>*>(base + F::kQBytes + F::kRing);
@@ -899,18 +954,18 @@ __global__ void __launch_bounds__(Form<kCtas>::kThreads, kCtas == 1 ? 2 : 1)
       mbar_init(smem_u32(&c.full[i]), 1);
       mbar_init(smem_u32(&c.empty[i]), 1);
     }
-    for (int i = 0; i < kRaw; ++i) mbar_init(smem_u32(&c.raw[i]), 1);
+    for (int i = 0; i < kRaw; ++i) mbar_init(smem_u32(&c.raw[i]), F::kV);
     mbar_init(smem_u32(&c.cleaned), F::kCleaners * kCtas);
     mbar_init(smem_u32(&c.done), F::kSoftmax * kCtas);
     mbar_init(smem_u32(&c.answer_full), 1);
     mbar_init(smem_u32(&c.answer_free), 1);
     mbar_init(smem_u32(&c.drain), 1);
     fence_mbar_init();
-    prefetch_tmap(&qn);
-    prefetch_tmap(&qr);
-    prefetch_tmap(&kn);
-    prefetch_tmap(&kr);
-    prefetch_tmap(&v);
+    prefetch_tmap(&m.qn[0]);
+    prefetch_tmap(&m.qr[0]);
+    prefetch_tmap(&m.kn[0]);
+    prefetch_tmap(&m.kr[0]);
+    prefetch_tmap(&m.v[0]);
   }
   if (threadIdx.x < kKeys) c.notes.clear(threadIdx.x);
   if (warp == F::kMma) {
@@ -942,7 +997,8 @@ __global__ void __launch_bounds__(Form<kCtas>::kThreads, kCtas == 1 ? 2 : 1)
   if (warp >= F::kSoftmax) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
     if (warp == F::kTma) {
-      produce<kCtas>(base, c, p, &qn, &qr, &kn, &kr, &v, rank, lane);
+      if constexpr (kCtas == 1) produce_one(base, c, p, m, lane);
+      else produce_pair(base, c, p, m, rank, lane);
     } else if (warp == F::kMma) {
       if (rank == 0) {
         issue_mmas<kCtas>(base, c, p, tmem, lane);
@@ -958,7 +1014,7 @@ __global__ void __launch_bounds__(Form<kCtas>::kThreads, kCtas == 1 ? 2 : 1)
     } else if (warp >= F::kClean && warp < F::kClean + F::kCleaners) {
       clean_values<kCtas>(base, c, p, rank, warp - F::kClean, lane);
     } else if constexpr (kCtas == 2) {
-      if (warp == F::kQ) load_queries(base, c, p, &qn, &qr, rank, lane);
+      if (warp == F::kQ) load_queries(base, c, p, m, rank, lane);
     }
     teardown();
   } else {
@@ -1020,8 +1076,7 @@ int head_map(CUtensorMap* map, const void* base, int dims, int H, int64_t T, int
 }
 
 template <int kCtas>
-int launch_prefill(const CUtensorMap& qn, const CUtensorMap& qr, const CUtensorMap& kn, const CUtensorMap& kr,
-                   const CUtensorMap& v, const PrefillParams& p, cudaStream_t st) {
+int launch_prefill(const PrefillMaps& m, const PrefillParams& p, cudaStream_t st) {
   auto kernel = mla_prefill_kernel<kCtas>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem<kCtas>);
   if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(mla_prefill_kernel)");
@@ -1037,7 +1092,7 @@ int launch_prefill(const CUtensorMap& qn, const CUtensorMap& qr, const CUtensorM
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = kCtas > 1 ? 1 : 0;
-  e = cudaLaunchKernelEx(&cfg, kernel, qn, qr, kn, kr, v, p);
+  e = cudaLaunchKernelEx(&cfg, kernel, m, p);
   if (e != cudaSuccess) return cuda_fail(e, "launch mla_prefill_kernel");
   if (p.num_parts > 0) {
     mla_prefill_merge_kernel<kCtas><<<units, 256, 0, st>>>(p);
@@ -1105,24 +1160,27 @@ extern "C" int mla_prefill(const void* q_nope, int64_t qn_token_stride, int64_t 
     kn_token_stride = kn_head_stride = v_token_stride = v_head_stride = kNope;
     kr_token_stride = kRope;
   }
-  CUtensorMap qn, qr, kn, kr, vm;
-  const int keys = 128 / ctas;  // a CTA's tokens of a key tile
-  int rc = head_map(&qn, q_nope, kNope, H, Tq, qn_token_stride, qn_head_stride, 128);
-  if (rc == MLA_OK) rc = head_map(&qr, q_rope, kRope, H, Tq, qr_token_stride, qr_head_stride, 128);
-  if (rc == MLA_OK) rc = head_map(&kn, k_nope, kNope, H, Tk, kn_token_stride, kn_head_stride, keys);
-  if (rc == MLA_OK) rc = head_map(&kr, k_rope, kRope, 1, Tk, kr_token_stride, kRope, keys);
-  if (rc == MLA_OK) {
-    // 64 tokens x 128 dims as two halves of 64 dims, one after the other; in a pair
-    // 128 tokens of a CTA's half
-    const uint64_t d[4] = {64, (uint64_t)std::max<int64_t>(Tk, 1), 2, (uint64_t)H};
-    const uint64_t st[3] = {(uint64_t)(Tk > 1 ? v_token_stride : (int64_t)H * kValue) * 2, 128,
-                            (uint64_t)(H > 1 ? v_head_stride : kValue) * 2};
-    const uint32_t box[4] = {64, ctas == 1 ? 64u : 128u, (uint32_t)(2 / ctas), 1};
-    rc = make_tensor_map_bf16_4d(&vm, v, d, st, box);
+  PrefillMaps m = {};
+  int rc = MLA_OK;
+  for (int few = 0; few < (ctas == 1 ? 2 : 1) && rc == MLA_OK; ++few) {
+    const int rows = few ? kFew : kRows, keys = few ? kFew : kKeys / ctas;  // a CTA's tokens of a key tile
+    rc = head_map(&m.qn[few], q_nope, kNope, H, Tq, qn_token_stride, qn_head_stride, rows);
+    if (rc == MLA_OK) rc = head_map(&m.qr[few], q_rope, kRope, H, Tq, qr_token_stride, qr_head_stride, rows);
+    if (rc == MLA_OK) rc = head_map(&m.kn[few], k_nope, kNope, H, Tk, kn_token_stride, kn_head_stride, keys);
+    if (rc == MLA_OK) rc = head_map(&m.kr[few], k_rope, kRope, 1, Tk, kr_token_stride, kRope, keys);
+    if (rc == MLA_OK) {
+      // 64 tokens x 128 dims as two halves of 64 dims, one after the other; in a pair
+      // 128 tokens of a CTA's half; few: 32 tokens of a half
+      const uint64_t d[4] = {64, (uint64_t)std::max<int64_t>(Tk, 1), 2, (uint64_t)H};
+      const uint64_t st[3] = {(uint64_t)(Tk > 1 ? v_token_stride : (int64_t)H * kValue) * 2, 128,
+                              (uint64_t)(H > 1 ? v_head_stride : kValue) * 2};
+      const uint32_t box[4] = {64, few ? (uint32_t)kFew : 64u * ctas, few || ctas == 2 ? 1u : 2u, 1};
+      rc = make_tensor_map_bf16_4d(&m.v[few], v, d, st, box);
+    }
   }
   if (rc != MLA_OK) return rc;
   const PrefillParams p{cu_q, cu_kv, prefix, N, H, causal != 0, Tq, Tk, sm_scale, sm_scale * kLog2e, work,
                         num_work, num_parts, O_part, LSE_part, static_cast<__nv_bfloat16*>(out), lse, status};
   const cudaStream_t st = (cudaStream_t)stream;
-  return ctas == 1 ? launch_prefill<1>(qn, qr, kn, kr, vm, p, st) : launch_prefill<2>(qn, qr, kn, kr, vm, p, st);
+  return ctas == 1 ? launch_prefill<1>(m, p, st) : launch_prefill<2>(m, p, st);
 }
