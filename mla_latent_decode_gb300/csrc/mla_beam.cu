@@ -3,23 +3,26 @@
 //
 //   score(w, t) = c[w] + x[w, t] - ln sum_u exp x[w, u]
 //
-// and the k largest over (w, t), equal ones by lowest (w, t).  Each logit is
-// read once: a thread keeps its 64 bytes of a row in registers, takes their
-// maximum and sum of exponentials, and hands on the few that may be among the
-// row's k best.  One cluster of 8 CTAs serves a request, each CTA an eighth of
-// the vocabulary of all beams; the rows' statistics and the CTAs' k best meet
-// through distributed shared memory, so there is one launch, no workspace, and
-// no result that depends on an order of arrival.
+// and the k largest over (w, t), equal ones by lowest (w, t).  Bound by the logits'
+// bytes: each is read once, 64 bytes a lane and tile, the next tile's loads under
+// way.  A warp has a part of a row to itself and meets no barrier before its end: it
+// keeps the part's maximum and sum of exponentials and its k best, the CTAs of a
+// cluster (one request) exchange the rows' statistics and their k best through
+// distributed shared memory.  One launch, no workspace, and no result that depends on
+// an order of arrival.
 //
-// Which logits of a tile may count: the k-th largest of the warps' largest
-// thread maxima is a bound that at least k of the tile's values reach, and few
-// more do (about k ln k for values in random order).  Where too many do (masked
-// vocabularies, sorted ones) the bound is taken again from all 512 threads'
-// maxima with their positions, which no more than k threads' values can reach.
-// Exponents are fp32 differences to the thread's own maximum; sums are fp32 per
-// thread, warp and CTA (8192 terms deep at 131072 logits, 2^-24 each) and meet
-// in fp64, where the scores are formed and compared: two beams' tokens often
-// differ by less than fp32 shows of their sums.
+// Which logits of a tile may count: the k-th largest of the 64 largest values that a
+// warp's lanes have met in their even and odd vectors (cut to 16 bits, so found in 16
+// votes) is a bound that at least k values of the part reach, and few more do (about
+// k ln k for values in random order).  A tile without a value above the bound, which
+// most are, costs its maximum and its sum only.  Where too many reach it (ties, a
+// vocabulary that is mostly masked) the best k so far are selected exactly, and
+// later values have to exceed the last of them.
+//
+// Exponents are fp32 differences to the lane's own maximum; sums are fp32 over a
+// tile (64 terms), compensated over tiles, and meet in fp64, where the scores are
+// formed: two beams' tokens often differ by less than fp32 shows of their sums.
+// Scores are compared as ordered integers (fp64 compares run at 2 a cycle and SM).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -31,14 +34,16 @@ namespace {
 
 using namespace ptx;
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kCluster = 8;
-constexpr int kVecs = 4;                    // 16-byte vectors of a row per thread and tile
+constexpr int kMaxCluster = 16;
+constexpr int kVecs = 8;                    // 16-byte vectors of a row per lane and tile
 constexpr int kMaxK = MLA_BEAM_MAX_K, kMaxW = MLA_BEAM_MAX_W;
-constexpr int kMaxBound = 5;                // thread maxima per warp in the bound: k / 16 + 1
-constexpr int kCap = kMaxK * 32 + kMaxK;    // a tile's values behind the exact bound, and the row's so far
+constexpr int kMaxLists = 32;               // parts of rows in a CTA
+constexpr int kCap = kMaxK + 8 * 32 + 64;   // candidates of a warp: its best so far, a vector's, room
 constexpr float kLog2e = 1.44269504088896340736f;
+constexpr uint32_t kLeast = 0x00800000u;    // the least finite value's place in the order
+typedef unsigned long long u64;
 
 struct BeamParams {
   const void* logits;
@@ -50,23 +55,23 @@ struct BeamParams {
   int32_t* parents;
   int32_t* tokens;
   int* status;
+  int cluster, parts;
 };
 
 struct Smem {
-  unsigned long long buf[kCap];             // candidates of the row at hand; later: positions
-  unsigned long long list[kMaxW * kMaxK];   // each row's best in order; later: their scores
-  unsigned long long top[kThreads];         // threads' best (exact bound)
-  uint32_t bound[kWarps * kMaxBound];
-  float2 warp_stat[kWarps];
-  float2 stat[kCluster][kMaxW];             // (max, sum) of every CTA's part of a row
+  union {
+    u64 buf[kWarps][kCap];                  // candidates of the warps' parts at hand
+    long long pos[kMaxLists * kMaxK];       // later: w * V + t of the lists' entries
+  };
+  u64 list[kMaxLists * kMaxK];              // the parts' best in order; later: their scores
+  float2 stat[kMaxCluster][kMaxLists];      // (max, sum) of every CTA's parts
   double lse[kMaxW];
-  int num[kMaxW];                           // candidates in a row's list
-  double got_score[kCluster * kMaxK];       // in CTA 0: every CTA's best
-  long long got_pos[kCluster * kMaxK];
-  int got_num[kCluster];
+  int num[kMaxLists];                       // entries of a list
+  int ends[kMaxW];                          // a finished beam's end counts
+  u64 got_score[kMaxCluster * kMaxK];       // in CTA 0: every CTA's best
+  long long got_pos[kMaxCluster * kMaxK];
+  int got_num[kMaxCluster];
   long long member[kMaxK];
-  unsigned long long exact;
-  int count[2];
 };
 
 __device__ __forceinline__ uint32_t ordered(float x) {
@@ -82,6 +87,56 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+__device__ __forceinline__ u64 ordered(double x) {
+  const u64 u = (u64)__double_as_longlong(x + 0.0);
+  return u >> 63 ? ~u : u | 1ull << 63;
+}
+__device__ __forceinline__ double unordered(u64 u) {
+  return __longlong_as_double((long long)(u >> 63 ? u & ~(1ull << 63) : ~u));
+}
+__device__ __forceinline__ u64 f2(float a, float b) {
+  u64 x;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(a), "f"(b));
+  return x;
+}
+__device__ __forceinline__ void f2(u64 x, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x));
+}
+__device__ __forceinline__ u64 add2(u64 a, u64 b) {
+  u64 d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ u64 mul2(u64 a, u64 b) {
+  u64 d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+// e^x for x <= 0 in fp64: 2^n times the Taylor series of e^r, |r| <= ln 2 / 2
+// (0.35^11 / 11! is 2^-42).
+__device__ __forceinline__ double exp64(double x) {
+  if (!(x > -700.0)) return x == x ? 0.0 : x;
+  const double n = rint(x * 1.4426950408889634);
+  const double r = fma(n, -0.6931471805599453, x);
+  double p = 1.0 / 3628800;
+  p = fma(p, r, 1.0 / 362880);
+  p = fma(p, r, 1.0 / 40320);
+  p = fma(p, r, 1.0 / 5040);
+  p = fma(p, r, 1.0 / 720);
+  p = fma(p, r, 1.0 / 120);
+  p = fma(p, r, 1.0 / 24);
+  p = fma(p, r, 1.0 / 6);
+  p = fma(p, r, 0.5);
+  p = fma(p, r, 1.0);
+  p = fma(p, r, 1.0);
+  return p * __longlong_as_double((long long)(1023 + (int)n) << 52);
+}
+// ln x for finite x >= 1 (a sum with its largest term 1): fp32's, and a Newton step.
+__device__ __forceinline__ double log64(double x) {
+  const double l = (double)logf((float)x);
+  return l + (x * exp64(-l) - 1.0);
+}
+
 template <typename T>
 struct Type;
 template <>
@@ -91,6 +146,10 @@ struct Type<float> {
     return __uint_as_float(j == 0 ? v.x : j == 1 ? v.y : j == 2 ? v.z : v.w);
   }
   static constexpr uint32_t kNone = 0xff800000u;  // -inf
+  static __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+    return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
+  }
+  static __device__ __forceinline__ float top(uint32_t a) { return __uint_as_float(a); }
 };
 template <>
 struct Type<__nv_bfloat16> {
@@ -100,6 +159,13 @@ struct Type<__nv_bfloat16> {
     return __uint_as_float(j & 1 ? w & 0xffff0000u : w << 16);
   }
   static constexpr uint32_t kNone = 0xff80ff80u;
+  static __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+    const __nv_bfloat162 m = __hmax2(*reinterpret_cast<__nv_bfloat162*>(&a), *reinterpret_cast<__nv_bfloat162*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&m);
+  }
+  static __device__ __forceinline__ float top(uint32_t a) {
+    return fmaxf(__uint_as_float(a << 16), __uint_as_float(a & 0xffff0000u));
+  }
 };
 template <>
 struct Type<__half> {
@@ -110,6 +176,14 @@ struct Type<__half> {
     return j & 1 ? __high2float(h) : __low2float(h);
   }
   static constexpr uint32_t kNone = 0xfc00fc00u;
+  static __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+    const __half2 m = __hmax2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&m);
+  }
+  static __device__ __forceinline__ float top(uint32_t a) {
+    const __half2 h = *reinterpret_cast<const __half2*>(&a);
+    return fmaxf(__low2float(h), __high2float(h));
+  }
 };
 
 // Positions [e, e + kPer) of a row, those outside [lo, hi) as -inf.
@@ -137,15 +211,155 @@ __device__ __forceinline__ uint4 load(const T* row, int64_t e, int64_t lo, int64
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// The k best of n keys, in order, to `out`: each key's rank is the number of
-// greater ones (keys differ).  All threads; no barrier inside.
-__device__ __forceinline__ void best_keys(const unsigned long long* keys, int n, int k,
-                                          unsigned long long* out) {
-  for (int i = threadIdx.x; i < n; i += kThreads) {
-    const unsigned long long mine = keys[i];
+// The k best of a warp's n keys, in order, to `out`: a key's rank is the number of
+// greater ones (keys differ).
+__device__ __noinline__ void best_keys(const u64* keys, int n, int k, u64* out) {
+  const int lane = threadIdx.x & 31;
+  __syncwarp();
+  for (int i = lane; i < n; i += 32) {
+    const u64 mine = keys[i];
     int rank = 0;
+#pragma unroll 4
     for (int j = 0; j < n; ++j) rank += keys[j] > mine;
     if (rank < k) out[rank] = mine;
+  }
+  __syncwarp();
+}
+
+// The k-th largest of the warp's 64 values, its place in the order cut to 16 bits.
+__device__ __forceinline__ uint32_t kth_of(float a, float b, int k) {
+  const uint32_t ka = ordered(a) >> 16, kb = ordered(b) >> 16;
+  uint32_t x = 0;
+#pragma unroll
+  for (int bit = 15; bit >= 0; --bit) {
+    const uint32_t y = x | 1u << bit;
+    if (__popc(__ballot_sync(~0u, ka >= y)) + __popc(__ballot_sync(~0u, kb >= y)) >= k) x = y;
+  }
+  return x << 16;
+}
+
+template <typename T>
+__device__ __forceinline__ void load_tile(uint4 (&v)[kVecs], const T* row, int64_t t0, int64_t lo, int64_t hi, int lane) {
+  constexpr int kPer = Type<T>::kPer;
+#pragma unroll
+  for (int u = 0; u < kVecs; ++u) v[u] = load<T>(row, t0 + (u * 32 + lane) * kPer, lo, hi);
+}
+
+// One warp over positions [lo, hi) of a row: the k best to `list` (their number to
+// *num), maximum and sum of exponentials to *stat.
+template <typename T>
+__device__ __forceinline__ void scan_part(const T* row, int64_t lo, int64_t hi, int k, u64* buf, u64* list, int* num,
+                                          float2* stat) {
+  constexpr int kPer = Type<T>::kPer, kTile = 32 * kVecs * kPer;
+  const int lane = threadIdx.x & 31;
+  const auto key = [](float x, int64_t at) { return (u64)ordered(x) << 32 | (uint32_t)~(uint32_t)at; };
+  float m = -INFINITY, s = 0.f, s_low = 0.f;   // the lane's maximum and sum
+  float a = -INFINITY, b = -INFINITY;          // its largest in even and odd vectors
+  uint32_t limit = kLeast;                     // values from here on may count
+  int n = 0;
+  int64_t t0 = lo - (int64_t)(reinterpret_cast<uintptr_t>(row + lo) / sizeof(T) % kPer);
+  uint4 v[kVecs], next[kVecs];
+  if (t0 < hi) load_tile<T>(v, row, t0, lo, hi, lane);
+#pragma unroll 1
+  for (; t0 < hi; t0 += kTile) {
+    if (t0 + kTile < hi) load_tile<T>(next, row, t0 + kTile, lo, hi, lane);
+    uint32_t most[2] = {Type<T>::kNone, Type<T>::kNone};
+#pragma unroll
+    for (int u = 0; u < kVecs; ++u)
+      most[u & 1] = Type<T>::max2(most[u & 1], Type<T>::max2(Type<T>::max2(v[u].x, v[u].y), Type<T>::max2(v[u].z, v[u].w)));
+    const float even = Type<T>::top(most[0]), odd = Type<T>::top(most[1]), top = fmaxf(even, odd);
+    a = fmaxf(a, even);
+    b = fmaxf(b, odd);
+    // the sum, over differences to the lane's maximum
+    if (top > m) {
+      const float f = ex2((m - top) * kLog2e);
+      s *= f;
+      s_low *= f;
+      m = top;
+    }
+    const float ref = m > -INFINITY ? m : 0.f;
+    const u64 minus = f2(-ref, -ref), scale = f2(kLog2e, kLog2e);
+    u64 sum[2] = {0, 0};
+#pragma unroll
+    for (int u = 0; u < kVecs; ++u)
+#pragma unroll
+      for (int j = 0; j < kPer; j += 2) {
+        float p, q;
+        f2(mul2(add2(f2(Type<T>::at(v[u], j), Type<T>::at(v[u], j + 1)), minus), scale), p, q);
+        sum[j / 2 & 1] = add2(sum[j / 2 & 1], f2(ex2(p), ex2(q)));
+      }
+    float p0, p1, p2, p3;
+    f2(sum[0], p0, p1);
+    f2(sum[1], p2, p3);
+    const float x = (p0 + p1) + (p2 + p3), t = s + x, back = t - s;
+    s_low += (s - (t - back)) + (x - back);
+    s = t;
+    if (__any_sync(~0u, top >= unordered(limit))) {
+      limit = max(limit, kth_of(a, b, k));
+      const float least = unordered(limit);
+      int mine = 0;
+      if (top >= least) {
+#pragma unroll
+        for (int u = 0; u < kVecs; ++u)
+#pragma unroll
+          for (int j = 0; j < kPer; ++j) mine += Type<T>::at(v[u], j) >= least;
+      }
+      const int total = __reduce_add_sync(~0u, mine);
+      if (n + total <= kCap) {
+        int at = mine;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+          const int o = __shfl_up_sync(~0u, at, d);
+          if (lane >= d) at += o;
+        }
+        at += n - mine;
+        if (mine) {
+#pragma unroll
+          for (int u = 0; u < kVecs; ++u)
+#pragma unroll
+            for (int j = 0; j < kPer; ++j) {
+              const float y = Type<T>::at(v[u], j);
+              if (y >= least) buf[at++] = key(y, t0 + (u * 32 + lane) * kPer + j);
+            }
+        }
+        n += total;
+      } else {
+        // Too many: vector by vector, read again, with the best so far selected
+        // whenever the buffer has no room for one more.
+#pragma unroll 1
+        for (int u = 0; u < kVecs; ++u) {
+          if (n + 32 * kPer > kCap) {
+            best_keys(buf, n, k, list);
+            n = min(n, k);
+            for (int i = lane; i < n; i += 32) buf[i] = list[i];
+            if (n == k) limit = max(limit, (uint32_t)(list[k - 1] >> 32) + 1);  // later ones have to be greater
+            __syncwarp();
+          }
+          const int64_t e = t0 + (u * 32 + lane) * kPer;
+          const uint4 w = load<T>(row, e, lo, hi);
+#pragma unroll
+          for (int j = 0; j < kPer; ++j) {
+            const float y = Type<T>::at(w, j);
+            const bool in = y >= unordered(limit);
+            const uint32_t all = __ballot_sync(~0u, in);
+            if (in) buf[n + __popc(all & ((1u << lane) - 1))] = key(y, e + j);
+            n += __popc(all);
+          }
+        }
+      }
+      __syncwarp();
+    }
+#pragma unroll
+    for (int u = 0; u < kVecs; ++u) v[u] = next[u];
+  }
+  best_keys(buf, n, k, list);
+  const float wm = unordered(__reduce_max_sync(~0u, ordered(m)));
+  s = (s + s_low) * ex2((wm > -INFINITY ? m - wm : 0.f) * kLog2e);
+#pragma unroll
+  for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(~0u, s, d);
+  if (lane == 0) {
+    *num = min(n, k);
+    *stat = make_float2(wm, s);
   }
 }
 
@@ -153,12 +367,12 @@ __device__ __forceinline__ void best_keys(const unsigned long long* keys, int n,
 // score, equal ones by position; entry e goes to put(rank, e).  Its rank is its
 // place in its own list and, by bisection, in every other.
 template <typename Put>
-__device__ __forceinline__ void merge_lists(const double* score, const long long* pos, const int* num,
+__device__ __forceinline__ void merge_lists(const u64* score, const long long* pos, const int* num,
                                             int lists, int pitch, int k, Put put) {
   for (int e = threadIdx.x; e < lists * pitch; e += kThreads) {
     const int l = e / pitch, j = e % pitch;
     if (j >= num[l]) continue;
-    const double s = score[e];
+    const u64 s = score[e];
     const long long at = pos[e];
     int rank = j;
     for (int m = 0; m < lists && rank < k; ++m) {
@@ -175,212 +389,93 @@ __device__ __forceinline__ void merge_lists(const double* score, const long long
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 2) __cluster_dims__(kCluster, 1, 1)
-    mla_beam_select_kernel(const BeamParams p) {
-  constexpr int kPer = Type<T>::kPer, kElems = kVecs * kPer, kTile = kThreads * kElems;
+__global__ void __launch_bounds__(kThreads, 2) mla_beam_select_kernel(const BeamParams p) {
   extern __shared__ __align__(16) uint8_t beam_smem[];
   Smem& sm = *reinterpret_cast<Smem*>(beam_smem);
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, warp = tid >> 5;
   const uint32_t rank = cluster_ctarank();
-  const int64_t b = blockIdx.x / kCluster;
-  const int W = p.W, V = p.V, k = p.k, r = k / 16 + 1;
-  const int seg = ((V + kCluster - 1) / kCluster + 63) / 64 * 64;
-  const int64_t lo = min((int64_t)V, (int64_t)seg * rank), hi = min((int64_t)V, lo + seg);
-  if (tid < 2) sm.count[tid] = 0;
-  __syncthreads();
-
-  int turn = 0;  // rows read so far
-  for (int w = 0; w < W; ++w) {
+  const int cluster = p.cluster, parts = p.parts;  // parts of a row in a CTA
+  const int64_t b = blockIdx.x / cluster;
+  const int W = p.W, V = p.V, k = p.k, lists = W * parts;
+  cluster_arrive();  // the CTAs have started when they write to each other
+  const int64_t seg = ((int64_t)(V + cluster - 1) / cluster + 63) / 64 * 64;
+  const int64_t lo = min((int64_t)V, seg * rank), hi = min((int64_t)V, lo + seg);
+  const int64_t len = ((hi - lo + parts - 1) / parts + 63) / 64 * 64;
+  for (int l = warp; l < lists; l += kWarps) {
+    const int w = l / parts;
     const float c = p.scores[b * W + w];
     const bool done = p.finished && p.finished[b * W + w];
-    if (done || !(fabsf(c) < INFINITY)) {  // the same in every thread: nothing of the row counts
-      if (tid == 0) {
-        sm.num[w] = 0;
-        sm.stat[rank][w] = make_float2(-INFINITY, 0.f);
-      }
+    if (done || !(fabsf(c) < INFINITY)) {  // nothing of the row counts
+      sm.num[l] = 0;
+      sm.stat[rank][l] = make_float2(-INFINITY, 0.f);
       continue;
     }
+    const int64_t from = min(hi, lo + len * (l % parts));
     const T* row = static_cast<const T*>(p.logits) + b * p.batch_stride + w * p.beam_stride;
-    const int shift = (int)(reinterpret_cast<uintptr_t>(row + lo) / sizeof(T) % kPer);
-    int* count = &sm.count[turn & 1];
-    int* next_count = &sm.count[++turn & 1];
-    float m = -INFINITY, s = 0.f;  // the thread's maximum and sum
-    uint32_t bound = 1;            // k values of the row reach it (1: no bound yet)
-    int n = 0;
-    for (int64_t t0 = lo - shift; t0 < hi; t0 += kTile) {
-      uint4 v[kVecs];
-#pragma unroll
-      for (int u = 0; u < kVecs; ++u) v[u] = load<T>(row, t0 + (int64_t)(u * kThreads + tid) * kPer, lo, hi);
-      float mx = -INFINITY;
-#pragma unroll
-      for (int u = 0; u < kVecs; ++u)
-#pragma unroll
-        for (int j = 0; j < kPer; ++j) mx = fmaxf(mx, Type<T>::at(v[u], j));
-      // the bound's thread maxima: r per warp, in order
-      const uint32_t mine = mx > -INFINITY ? ordered(mx) : 0;
-      uint32_t left = mine;
-      for (int j = 0; j < r; ++j) {
-        const uint32_t best = __reduce_max_sync(~0u, left);
-        const uint32_t who = __ballot_sync(~0u, left == best);
-        if (lane == __ffs(who) - 1) left = 0;
-        if (lane == 0) sm.bound[warp * r + j] = best;
-      }
-      if (tid == 0) *next_count = 0;
-      // the sum, over differences to the thread's maximum
-      if (mx > m) {
-        s *= ex2((m - mx) * kLog2e);
-        m = mx;
-      }
-      const float ref = m > -INFINITY ? m : 0.f;
-#pragma unroll
-      for (int u = 0; u < kVecs; ++u)
-#pragma unroll
-        for (int j = 0; j < kPer; ++j) s += ex2((Type<T>::at(v[u], j) - ref) * kLog2e);
-      __syncthreads();
-      {
-        uint32_t kth = 0;
-        for (int i = lane; i < kWarps * r; i += 32) {
-          const uint32_t x = sm.bound[i];
-          int above = 0;
-          for (int j = 0; j < kWarps * r; ++j) above += sm.bound[j] > x || (sm.bound[j] == x && j < i);
-          if (above == k - 1) kth = x;
-        }
-        bound = max(bound, __reduce_max_sync(~0u, kth));
-      }
-      const auto key = [&](int u, int j, float x) {
-        const int64_t at = t0 + (int64_t)(u * kThreads + tid) * kPer + j;
-        return (unsigned long long)ordered(x) << 32 | (uint32_t)~(uint32_t)at;
-      };
-      if (mine >= bound) {
-        const float limit = unordered(bound);
-#pragma unroll
-        for (int u = 0; u < kVecs; ++u)
-#pragma unroll
-          for (int j = 0; j < kPer; ++j) {
-            const float x = Type<T>::at(v[u], j);
-            if (bound > 1 ? x >= limit : x > -INFINITY) {
-              const int at = atomicAdd(count, 1);
-              if (at < kCap) sm.buf[at] = key(u, j, x);
-            }
-          }
-      }
-      __syncthreads();
-      const int before = n;
-      n = *count;
-      if (n > kCap) {
-        // Too many: the row's best so far stay, the tile's values come again
-        // behind the exact bound, at most k threads' values.
-        const int stay = min(before, k);
-        __syncthreads();
-        unsigned long long* mine_row = sm.list + w * k;
-        best_keys(sm.buf, before, k, mine_row);
-        unsigned long long top = 0;
-#pragma unroll
-        for (int u = 0; u < kVecs; ++u)
-#pragma unroll
-          for (int j = 0; j < kPer; ++j) {
-            const float x = Type<T>::at(v[u], j);
-            if (x > -INFINITY) top = max(top, key(u, j, x));
-          }
-        sm.top[tid] = top;
-        if (tid == 0) sm.exact = 1;
-        __syncthreads();
-        if (tid < stay) sm.buf[tid] = mine_row[tid];
-        if (top) {
-          int above = 0;
-          for (int j = 0; j < kThreads; ++j) above += sm.top[j] > top;
-          if (above == k - 1) sm.exact = top;
-        }
-        if (tid == 0) *count = stay;
-        __syncthreads();
-        const unsigned long long exact = sm.exact;
-        if (top >= exact) {
-#pragma unroll
-          for (int u = 0; u < kVecs; ++u)
-#pragma unroll
-            for (int j = 0; j < kPer; ++j) {
-              const float x = Type<T>::at(v[u], j);
-              if (x > -INFINITY && key(u, j, x) >= exact) sm.buf[atomicAdd(count, 1)] = key(u, j, x);
-            }
-        }
-        __syncthreads();
-        n = *count;
-      }
-    }
-    best_keys(sm.buf, n, k, sm.list + w * k);
-    // the row's maximum and sum in this CTA
-    const float wm = unordered(__reduce_max_sync(~0u, ordered(m)));
-    s *= ex2((wm > -INFINITY ? m - wm : 0.f) * kLog2e);
-#pragma unroll
-    for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(~0u, s, d);
-    if (lane == 0) sm.warp_stat[warp] = make_float2(wm, s);
-    __syncthreads();
-    if (warp == 0) {
-      const float2 x = lane < kWarps ? sm.warp_stat[lane] : make_float2(-INFINITY, 0.f);
-      const float cm = unordered(__reduce_max_sync(~0u, ordered(x.x)));
-      float sum = x.y * ex2((cm > -INFINITY ? x.x - cm : 0.f) * kLog2e);
-#pragma unroll
-      for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(~0u, sum, d);
-      if (lane == 0) {
-        sm.stat[rank][w] = make_float2(cm, sum);
-        sm.num[w] = min(n, k);
-      }
-    }
+    scan_part<T>(row, from, min(hi, from + len), k, sm.buf[warp], sm.list + l * k, &sm.num[l], &sm.stat[rank][l]);
   }
   __syncthreads();
+  cluster_wait();
   // Every CTA gets every CTA's part of the rows' statistics.
-  for (int i = tid; i < kCluster * W; i += kThreads) {
-    const int to = i / W, w = i % W;
+  for (int i = tid; i < cluster * lists; i += kThreads) {
+    const int to = i / lists, l = i % lists;
     if (to == (int)rank) continue;
-    const float2 x = sm.stat[rank][w];
-    const uint32_t at = mapa(smem_u32(&sm.stat[rank][w]), to);
+    const float2 x = sm.stat[rank][l];
+    const uint32_t at = mapa(smem_u32(&sm.stat[rank][l]), to);
     st_cluster_u32(at, __float_as_uint(x.x));
     st_cluster_u32(at + 4, __float_as_uint(x.y));
   }
   cluster_sync();
-  if (tid < W) {
+  // A row's sum: a quarter warp a row.
+  for (int w0 = 0; w0 < W; w0 += kThreads / 8) {
+    const int w = w0 + tid / 8, of = cluster * parts;
     float m = -INFINITY;
-    for (int c = 0; c < kCluster; ++c) m = fmaxf(m, sm.stat[c][tid].x);
     double sum = 0;
-    for (int c = 0; c < kCluster; ++c) {
-      const float2 x = sm.stat[c][tid];
-      sum += m > -INFINITY ? (double)x.y * exp((double)x.x - (double)m) : (double)x.y;
+    if (w < W) {
+      for (int i = tid % 8; i < of; i += 8) m = fmaxf(m, sm.stat[i / parts][w * parts + i % parts].x);
     }
-    // an infinite or undefined logit: no continuation of this beam counts
-    const double lse = (double)m + log(sum);
-    const bool whole = sum > 0 && fabs(lse) < INFINITY;
-    sm.lse[tid] = lse;
-    if (!whole) sm.num[tid] = 0;
-    if (rank == 0) {
-      const float c = p.scores[b * W + tid];
-      const bool done = p.finished && p.finished[b * W + tid];
-      const bool odd = !(c < INFINITY) || (!done && (sum != sum || m == INFINITY));
-      if (odd && p.status) atomicOr(p.status, MLA_STATUS_BAD_SCORE);
-      if (done && fabsf(c) < INFINITY) sm.num[tid] = -1;  // its end, at its score
+#pragma unroll
+    for (int d = 4; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, d));
+    if (w < W) {
+      for (int i = tid % 8; i < of; i += 8) {
+        const float2 x = sm.stat[i / parts][w * parts + i % parts];
+        sum += m > -INFINITY ? (double)x.y * exp64((double)x.x - (double)m) : (double)x.y;
+      }
+    }
+#pragma unroll
+    for (int d = 4; d; d >>= 1) sum += __shfl_xor_sync(~0u, sum, d);
+    if (w < W && tid % 8 == 0) {
+      const float c = p.scores[b * W + w];
+      const bool done = p.finished && p.finished[b * W + w];
+      // an infinite or undefined logit: no continuation of this beam counts
+      const bool whole = sum > 0 && sum < INFINITY && fabsf(m) < INFINITY;
+      sm.lse[w] = whole ? (double)m + log64(sum) : INFINITY;
+      sm.ends[w] = done && fabsf(c) < INFINITY && rank == 0;  // its end, at its score
+      if (rank == 0 && p.status && (!(c < INFINITY) || (!done && (sum != sum || m == INFINITY))))
+        atomicOr(p.status, MLA_STATUS_BAD_SCORE);
     }
   }
   __syncthreads();
-  double* score = reinterpret_cast<double*>(sm.list);
-  long long* pos = reinterpret_cast<long long*>(sm.buf);
-  for (int e = tid; e < W * k; e += kThreads) {
-    const int w = e / k, j = e % k;
+  if (tid < lists) {
+    const int w = tid / parts;
+    if (sm.ends[w]) sm.num[tid] = tid % parts == 0;
+    else if (!(sm.lse[w] < INFINITY)) sm.num[tid] = 0;
+  }
+  __syncthreads();
+  for (int e = tid; e < lists * k; e += kThreads) {
+    const int l = e / k, w = l / parts;
+    if (e % k >= sm.num[l]) continue;
     const double c = p.scores[b * W + w];
-    if (j < sm.num[w]) {
-      const unsigned long long key = sm.list[e];
-      pos[e] = (long long)w * V + (uint32_t)~(uint32_t)key;
-      score[e] = c + ((double)unordered((uint32_t)(key >> 32)) - sm.lse[w]);
-    } else if (j == 0 && sm.num[w] < 0) {
-      pos[e] = (long long)w * V + p.end_token;
-      score[e] = c;
-    }
+    const u64 key = sm.list[e];
+    const bool end = sm.ends[w];
+    sm.pos[e] = (long long)w * V + (end ? (uint32_t)p.end_token : (uint32_t)~(uint32_t)key);
+    sm.list[e] = ordered(end ? c : c + ((double)unordered((uint32_t)(key >> 32)) - sm.lse[w]));
   }
-  __syncthreads();
-  if (tid < W) sm.num[tid] = abs(sm.num[tid]);
   __syncthreads();
   const uint32_t to_score = mapa(smem_u32(sm.got_score + rank * k), 0);
   const uint32_t to_pos = mapa(smem_u32(sm.got_pos + rank * k), 0);
-  merge_lists(score, pos, sm.num, W, k, k, [&](int at, int e) {
-    const unsigned long long a = __double_as_longlong(score[e]), q = (unsigned long long)pos[e];
+  merge_lists(sm.list, sm.pos, sm.num, lists, k, k, [&](int at, int e) {
+    const u64 a = sm.list[e], q = (u64)sm.pos[e];
     st_cluster_u32(to_score + 8 * at, (uint32_t)a);
     st_cluster_u32(to_score + 8 * at + 4, (uint32_t)(a >> 32));
     st_cluster_u32(to_pos + 8 * at, (uint32_t)q);
@@ -388,7 +483,7 @@ __global__ void __launch_bounds__(kThreads, 2) __cluster_dims__(kCluster, 1, 1)
   });
   if (tid == 0) {
     int sum = 0;
-    for (int w = 0; w < W; ++w) sum += sm.num[w];
+    for (int l = 0; l < lists; ++l) sum += sm.num[l];
     st_cluster_u32(mapa(smem_u32(sm.got_num + rank), 0), (uint32_t)min(sum, k));
   }
   cluster_sync();
@@ -399,10 +494,10 @@ __global__ void __launch_bounds__(kThreads, 2) __cluster_dims__(kCluster, 1, 1)
     p.tokens[b * k + at] = (int)(q % V);
   };
   int have = 0;
-  for (int c = 0; c < kCluster; ++c) have += sm.got_num[c];
+  for (int c = 0; c < cluster; ++c) have += sm.got_num[c];
   have = min(have, k);
-  merge_lists(sm.got_score, sm.got_pos, sm.got_num, kCluster, k, k, [&](int at, int e) {
-    put(at, (float)sm.got_score[e], sm.got_pos[e]);
+  merge_lists(sm.got_score, sm.got_pos, sm.got_num, cluster, k, k, [&](int at, int e) {
+    put(at, (float)unordered(sm.got_score[e]), sm.got_pos[e]);
     sm.member[at] = sm.got_pos[e];
   });
   // Fewer than k continuations: the lowest positions that are none, at -inf.
@@ -419,13 +514,39 @@ __global__ void __launch_bounds__(kThreads, 2) __cluster_dims__(kCluster, 1, 1)
   }
 }
 
+// CTAs of a request: as many as find room at once (two an SM), while a warp has
+// about a tile's worth of logits; parts of a row in a CTA: what evens out the warps.
 template <typename T>
-int launch_beam(const BeamParams& p, int B, cudaStream_t st) {
-  const cudaError_t a = cudaFuncSetAttribute(mla_beam_select_kernel<T>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem));
-  if (a != cudaSuccess) return cuda_fail(a, "cudaFuncSetAttribute(mla_beam_select_kernel)");
-  mla_beam_select_kernel<T><<<(unsigned)(B * kCluster), kThreads, sizeof(Smem), st>>>(p);
-  const cudaError_t e = cudaGetLastError();
+int launch_beam(BeamParams p, int B, cudaStream_t st) {
+  auto kernel = mla_beam_select_kernel<T>;
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem));
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(mla_beam_select_kernel)");
+  constexpr int kTile = 32 * kVecs * Type<T>::kPer;
+  p.cluster = 1;
+  while (p.cluster < kMaxCluster && (int64_t)B * p.cluster * 2 <= 2 * sms &&
+         (int64_t)p.W * p.V > (int64_t)p.cluster * kWarps * kTile / 2)
+    p.cluster *= 2;
+  p.parts = 1;
+  const auto rounds = [&](int parts) { return (double)((p.W * parts + kWarps - 1) / kWarps) / parts; };
+  for (int parts = 2; parts <= kWarps && p.W * parts <= kMaxLists; parts *= 2)
+    if (rounds(parts) < rounds(p.parts)) p.parts = parts;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(B * p.cluster), 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.dynamicSmemBytes = sizeof(Smem);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)p.cluster;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, kernel, p);
   if (e != cudaSuccess) return cuda_fail(e, "launch mla_beam_select_kernel");
   return MLA_OK;
 }
@@ -446,7 +567,7 @@ extern "C" int mla_beam_select(const void* logits, mla_logit_dtype dtype, int64_
                 "[1, W * V]", B, W, V, k);
   if (W > kMaxW || k > kMaxK)
     return fail(MLA_ERR_UNSUPPORTED, "mla_beam_select: W=%d > %d beams or k=%d > %d", W, kMaxW, k, kMaxK);
-  if ((int64_t)B * W > 0x7fffffff || B > 0x7fffffff / kCluster)
+  if ((int64_t)B * W > 0x7fffffff || B > 0x7fffffff / kMaxCluster)
     return fail(MLA_ERR_INVALID_ARG, "mla_beam_select: B=%d W=%d: too many rows", B, W);
   if (end_token < 0 || end_token >= V)
     return fail(MLA_ERR_INVALID_ARG, "mla_beam_select: end_token %d outside [0, %d)", end_token, V);
@@ -462,7 +583,7 @@ extern "C" int mla_beam_select(const void* logits, mla_logit_dtype dtype, int64_
   if (!aligned(logits, dtype == MLA_LOGIT_F32 ? 4 : 2))
     return fail(MLA_ERR_MISALIGNED, "mla_beam_select: logits off their type's alignment");
   const BeamParams p{logits, batch_stride, beam_stride, scores, finished, W, V, k, end_token,
-                     out_scores, parents, tokens, status};
+                     out_scores, parents, tokens, status, 1, 1};
   const cudaStream_t st = (cudaStream_t)stream;
   if (dtype == MLA_LOGIT_BF16) return launch_beam<__nv_bfloat16>(p, B, st);
   if (dtype == MLA_LOGIT_F16) return launch_beam<__half>(p, B, st);

@@ -188,7 +188,7 @@ namespace mla {
 
 // Plan of mla_prefill with blocks of 128 rows (one CTA, two of them an SM) or 512
 // (a pair of CTAs).  Costs in key tiles of a single CTA with another beside it
-// (about 1.6 us): a tile of a pair, what a block takes besides its tiles, and the
+// (about 2.05 us): a tile of a pair, what a block takes besides its tiles, and the
 // merging launch with its rows.
 struct PrefillPlan {
   int ctas = 1;
@@ -207,7 +207,7 @@ static PrefillPlan plan_prefill_blocks(const int32_t* q_lens, const int32_t* kv_
                                        const int32_t* prefix, int N, int H, int causal,
                                        int ctas, int num_sms) {
   constexpr int kKeys = 128;
-  constexpr double kFixed = 2, kPairFixed = 4, kPairTile = 0.95, kMerge = 3, kMergeSlot = 0.001;
+  constexpr double kFixed = 1.7, kPairFixed = 1.4, kPairTile = 0.82, kMerge = 3, kMergeSlot = 0.001;
   const int block = ctas == 1 ? 128 : 512, slots_of = block / 128;
   PrefillPlan plan;
   plan.ctas = ctas;
