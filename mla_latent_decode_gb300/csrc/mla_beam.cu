@@ -38,8 +38,10 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 16;
 constexpr int kVecs = 8;                    // 16-byte vectors of a row per lane and tile
+constexpr int kStages = 2;                  // tiles of a warp in shared memory
 constexpr int kMaxK = MLA_BEAM_MAX_K, kMaxW = MLA_BEAM_MAX_W;
 constexpr int kMaxLists = 32;               // parts of rows in a CTA
+constexpr int kCount = 512;
 constexpr int kCap = kMaxK + 8 * 32 + 64;   // candidates of a warp: its best so far, a vector's, room
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr uint32_t kLeast = 0x00800000u;    // the least finite value's place in the order
@@ -58,21 +60,27 @@ struct BeamParams {
   int cluster, parts;
 };
 
+// Two CTAs an SM.
 struct Smem {
   union {
-    u64 buf[kWarps][kCap];                  // candidates of the warps' parts at hand
-    long long pos[kMaxLists * kMaxK];       // later: w * V + t of the lists' entries
+    uint4 tile[kWarps][kStages][kVecs][32];
+    struct {                                // once every CTA has read its logits
+      long long pos[kMaxLists * kMaxK];     // w * 2^32 + t of the lists' entries
+      u64 got_score[kMaxCluster * kMaxK];   // in CTA 0: every CTA's best
+      long long got_pos[kMaxCluster * kMaxK];
+    };
   };
+  u64 buf[kWarps][kCap];                    // candidates of the warps' parts at hand
   u64 list[kMaxLists * kMaxK];              // the parts' best in order; later: their scores
   float2 stat[kMaxCluster][kMaxLists];      // (max, sum) of every CTA's parts
   double lse[kMaxW];
   int num[kMaxLists];                       // entries of a list
   int ends[kMaxW];                          // a finished beam's end counts
-  u64 got_score[kMaxCluster * kMaxK];       // in CTA 0: every CTA's best
-  long long got_pos[kMaxCluster * kMaxK];
   int got_num[kMaxCluster];
+  int count[kWarps];
   long long member[kMaxK];
 };
+static_assert(sizeof(Smem) <= 113 * 1024, "shared memory of two CTAs an SM");
 
 __device__ __forceinline__ uint32_t ordered(float x) {
   const uint32_t u = __float_as_uint(x + 0.f);  // -0 as 0
@@ -188,15 +196,8 @@ struct Type<__half> {
 
 // Positions [e, e + kPer) of a row, those outside [lo, hi) as -inf.
 template <typename T>
-__device__ __forceinline__ uint4 load(const T* row, int64_t e, int64_t lo, int64_t hi) {
+__device__ __noinline__ uint4 load_edge(const T* row, int64_t e, int64_t lo, int64_t hi) {
   constexpr int kPer = Type<T>::kPer;
-  if (e >= lo && e + kPer <= hi) {
-    uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(row + e));
-    return v;
-  }
   uint32_t w[4] = {Type<T>::kNone, Type<T>::kNone, Type<T>::kNone, Type<T>::kNone};
 #pragma unroll
   for (int j = 0; j < kPer; ++j) {
@@ -230,154 +231,84 @@ __device__ __noinline__ void best_keys(const u64* keys, int n, int k, u64* out) 
 __device__ __forceinline__ uint32_t kth_of(float a, float b, int k) {
   const uint32_t ka = ordered(a) >> 16, kb = ordered(b) >> 16;
   uint32_t x = 0;
-#pragma unroll
-  for (int bit = 15; bit >= 0; --bit) {
-    const uint32_t y = x | 1u << bit;
+#pragma unroll 2
+  for (uint32_t bit = 1u << 15; bit; bit >>= 1) {
+    const uint32_t y = x | bit;
     if (__popc(__ballot_sync(~0u, ka >= y)) + __popc(__ballot_sync(~0u, kb >= y)) >= k) x = y;
   }
   return x << 16;
 }
 
+// A warp's way through its parts of rows, tile by tile; parts of which nothing
+// counts (finished or dead beams) are left out.
 template <typename T>
-__device__ __forceinline__ void load_tile(uint4 (&v)[kVecs], const T* row, int64_t t0, int64_t lo, int64_t hi, int lane) {
-  constexpr int kPer = Type<T>::kPer;
-#pragma unroll
-  for (int u = 0; u < kVecs; ++u) v[u] = load<T>(row, t0 + (u * 32 + lane) * kPer, lo, hi);
-}
+struct Walk {
+  const T* row;
+  int64_t t0, lo, hi;  // the tile's first position, the part
+  int l;               // list of the part; none left: p.W * p.parts
+  static constexpr int kTile = 32 * kVecs * Type<T>::kPer;
+  __device__ __forceinline__ void enter(const BeamParams& p, int64_t b, int64_t seg_lo, int64_t seg_hi, int64_t len, int at) {
+    const int lists = p.W * p.parts;
+#pragma unroll 1
+    for (l = at; l < lists; l += kWarps) {
+      const int w = l / p.parts;
+      const bool done = p.finished && p.finished[b * p.W + w];
+      lo = min(seg_hi, seg_lo + len * (l % p.parts));
+      hi = min(seg_hi, lo + len);
+      if (done || !(fabsf(p.scores[b * p.W + w]) < INFINITY) || lo == hi) continue;
+      row = static_cast<const T*>(p.logits) + b * p.batch_stride + w * p.beam_stride;
+      t0 = lo - (int64_t)(reinterpret_cast<uintptr_t>(row + lo) / sizeof(T) % Type<T>::kPer);
+      return;
+    }
+    l = lists;
+  }
+  __device__ __forceinline__ bool last() const { return t0 + kTile >= hi; }
+};
 
-// One warp over positions [lo, hi) of a row: the k best to `list` (their number to
-// *num), maximum and sum of exponentials to *stat.
-template <typename T>
-__device__ __forceinline__ void scan_part(const T* row, int64_t lo, int64_t hi, int k, u64* buf, u64* list, int* num,
-                                          float2* stat) {
-  constexpr int kPer = Type<T>::kPer, kTile = 32 * kVecs * kPer;
-  const int lane = threadIdx.x & 31;
-  const auto key = [](float x, int64_t at) { return (u64)ordered(x) << 32 | (uint32_t)~(uint32_t)at; };
-  float m = -INFINITY, s = 0.f, s_low = 0.f;   // the lane's maximum and sum
-  float a = -INFINITY, b = -INFINITY;          // its largest in even and odd vectors
-  uint32_t limit = kLeast;                     // values from here on may count
-  int n = 0;
-  int64_t t0 = lo - (int64_t)(reinterpret_cast<uintptr_t>(row + lo) / sizeof(T) % kPer);
-  uint4 v[kVecs], next[kVecs];
-  if (t0 < hi) load_tile<T>(v, row, t0, lo, hi, lane);
-#pragma unroll 1
-  for (; t0 < hi; t0 += kTile) {
-    if (t0 + kTile < hi) load_tile<T>(next, row, t0 + kTile, lo, hi, lane);
-    uint32_t most[2] = {Type<T>::kNone, Type<T>::kNone};
-#pragma unroll
-    for (int u = 0; u < kVecs; ++u)
-      most[u & 1] = Type<T>::max2(most[u & 1], Type<T>::max2(Type<T>::max2(v[u].x, v[u].y), Type<T>::max2(v[u].z, v[u].w)));
-    const float even = Type<T>::top(most[0]), odd = Type<T>::top(most[1]), top = fmaxf(even, odd);
-    a = fmaxf(a, even);
-    b = fmaxf(b, odd);
-    // the sum, over differences to the lane's maximum
-    if (top > m) {
-      const float f = ex2((m - top) * kLog2e);
-      s *= f;
-      s_low *= f;
-      m = top;
-    }
-    const float ref = m > -INFINITY ? m : 0.f;
-    const u64 minus = f2(-ref, -ref), scale = f2(kLog2e, kLog2e);
-    u64 sum[2] = {0, 0};
-#pragma unroll
-    for (int u = 0; u < kVecs; ++u)
-#pragma unroll
-      for (int j = 0; j < kPer; j += 2) {
-        float p, q;
-        f2(mul2(add2(f2(Type<T>::at(v[u], j), Type<T>::at(v[u], j + 1)), minus), scale), p, q);
-        sum[j / 2 & 1] = add2(sum[j / 2 & 1], f2(ex2(p), ex2(q)));
-      }
-    float p0, p1, p2, p3;
-    f2(sum[0], p0, p1);
-    f2(sum[1], p2, p3);
-    const float x = (p0 + p1) + (p2 + p3), t = s + x, back = t - s;
-    s_low += (s - (t - back)) + (x - back);
-    s = t;
-    if (__any_sync(~0u, top >= unordered(limit))) {
-      limit = max(limit, kth_of(a, b, k));
-      const float least = unordered(limit);
-      int mine = 0;
-      if (top >= least) {
-#pragma unroll
-        for (int u = 0; u < kVecs; ++u)
-#pragma unroll
-          for (int j = 0; j < kPer; ++j) mine += Type<T>::at(v[u], j) >= least;
-      }
-      const int total = __reduce_add_sync(~0u, mine);
-      if (n + total <= kCap) {
-        int at = mine;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-          const int o = __shfl_up_sync(~0u, at, d);
-          if (lane >= d) at += o;
-        }
-        at += n - mine;
-        if (mine) {
-#pragma unroll
-          for (int u = 0; u < kVecs; ++u)
-#pragma unroll
-            for (int j = 0; j < kPer; ++j) {
-              const float y = Type<T>::at(v[u], j);
-              if (y >= least) buf[at++] = key(y, t0 + (u * 32 + lane) * kPer + j);
-            }
-        }
-        n += total;
-      } else {
-        // Too many: vector by vector, read again, with the best so far selected
-        // whenever the buffer has no room for one more.
-#pragma unroll 1
-        for (int u = 0; u < kVecs; ++u) {
-          if (n + 32 * kPer > kCap) {
-            best_keys(buf, n, k, list);
-            n = min(n, k);
-            for (int i = lane; i < n; i += 32) buf[i] = list[i];
-            if (n == k) limit = max(limit, (uint32_t)(list[k - 1] >> 32) + 1);  // later ones have to be greater
-            __syncwarp();
-          }
-          const int64_t e = t0 + (u * 32 + lane) * kPer;
-          const uint4 w = load<T>(row, e, lo, hi);
-#pragma unroll
-          for (int j = 0; j < kPer; ++j) {
-            const float y = Type<T>::at(w, j);
-            const bool in = y >= unordered(limit);
-            const uint32_t all = __ballot_sync(~0u, in);
-            if (in) buf[n + __popc(all & ((1u << lane) - 1))] = key(y, e + j);
-            n += __popc(all);
-          }
-        }
-      }
-      __syncwarp();
-    }
-#pragma unroll
-    for (int u = 0; u < kVecs; ++u) v[u] = next[u];
-  }
-  best_keys(buf, n, k, list);
-  const float wm = unordered(__reduce_max_sync(~0u, ordered(m)));
-  s = (s + s_low) * ex2((wm > -INFINITY ? m - wm : 0.f) * kLog2e);
-#pragma unroll
-  for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(~0u, s, d);
-  if (lane == 0) {
-    *num = min(n, k);
-    *stat = make_float2(wm, s);
-  }
+__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
 }
 
 // The k best of `lists` sorted lists (list l: num[l] entries at l * pitch) by
 // score, equal ones by position; entry e goes to put(rank, e).  Its rank is its
 // place in its own list and, by bisection, in every other.
 template <typename Put>
-__device__ __forceinline__ void merge_lists(const u64* score, const long long* pos, const int* num,
-                                            int lists, int pitch, int k, Put put) {
+__device__ __forceinline__ void merge_lists(u64* score, const long long* pos, const int* num, int lists, int pitch, int k,
+                                            Put put) {
+  const int all = lists * pitch;
+  if (all <= kCount) {  // (above about 500 entries bisection is faster than counting)
+#pragma unroll 1
+    for (int e = threadIdx.x; e < all + (all & 1); e += kThreads)
+      if (e == all || e % pitch >= num[e / pitch]) score[e] = 0;  // below every score
+    __syncthreads();
+#pragma unroll 1
+    for (int e = threadIdx.x; e < all; e += kThreads) {
+      const u64 s = score[e];
+      if (s == 0) continue;
+      int rank = 0;
+#pragma unroll 4
+      for (int j = 0; j < all; j += 2) {
+        const ulonglong2 x = *reinterpret_cast<const ulonglong2*>(score + j);
+        rank += (x.x > s) + (x.y > s);
+        if (x.x == s && j != e) rank += pos[j] < pos[e];
+        if (x.y == s && j + 1 != e) rank += pos[j + 1] < pos[e];
+      }
+      if (rank < k) put(rank, e);
+    }
+    return;
+  }
+#pragma unroll 1
   for (int e = threadIdx.x; e < lists * pitch; e += kThreads) {
     const int l = e / pitch, j = e % pitch;
     if (j >= num[l]) continue;
     const u64 s = score[e];
     const long long at = pos[e];
     int rank = j;
+#pragma unroll 1
     for (int m = 0; m < lists && rank < k; ++m) {
       if (m == l) continue;
       int lo = 0, hi = num[m];
+#pragma unroll 1
       while (lo < hi) {
         const int mid = (lo + hi) / 2, f = m * pitch + mid;
         if (score[f] > s || (score[f] == s && pos[f] < at)) lo = mid + 1; else hi = mid;
@@ -398,25 +329,164 @@ __global__ void __launch_bounds__(kThreads, 2) mla_beam_select_kernel(const Beam
   const int64_t b = blockIdx.x / cluster;
   const int W = p.W, V = p.V, k = p.k, lists = W * parts;
   cluster_arrive();  // the CTAs have started when they write to each other
-  const int64_t seg = ((int64_t)(V + cluster - 1) / cluster + 63) / 64 * 64;
+  const int64_t seg = ((uint32_t)(V + cluster - 1) / (uint32_t)cluster + 63) / 64 * 64;
   const int64_t lo = min((int64_t)V, seg * rank), hi = min((int64_t)V, lo + seg);
-  const int64_t len = ((hi - lo + parts - 1) / parts + 63) / 64 * 64;
+  const int64_t len = ((uint32_t)(hi - lo + parts - 1) / (uint32_t)parts + 63) / 64 * 64;
+  const int lane = tid & 31;
+#pragma unroll 1
   for (int l = warp; l < lists; l += kWarps) {
-    const int w = l / parts;
-    const float c = p.scores[b * W + w];
-    const bool done = p.finished && p.finished[b * W + w];
-    if (done || !(fabsf(c) < INFINITY)) {  // nothing of the row counts
+    if (lane == 0) {
       sm.num[l] = 0;
       sm.stat[rank][l] = make_float2(-INFINITY, 0.f);
+    }
+  }
+  constexpr int kPer = Type<T>::kPer;
+  Walk<T> at = {}, to = {};  // the tile at hand, the tile to load
+  const auto fetch = [&](int stage) {
+    if (to.l < lists) {
+      uint4* dst = &sm.tile[warp][stage][0][lane];
+      const int64_t e0 = to.t0 + lane * kPer;
+#pragma unroll 2
+      for (int u = 0; u < kVecs; ++u) {
+        const int64_t e = e0 + u * 32 * kPer;
+        if (e >= to.lo && e + kPer <= to.hi) cp_async16(dst + u * 32, to.row + e);
+        else dst[u * 32] = load_edge<T>(to.row, e, to.lo, to.hi);
+      }
+      if (to.last()) to.enter(p, b, lo, hi, len, to.l + kWarps);
+      else to.t0 += Walk<T>::kTile;
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  to.enter(p, b, lo, hi, len, warp);
+  at = to;
+#pragma unroll 1
+  for (int i = 0; i < kStages - 1; ++i) fetch(i);
+  u64* buf = sm.buf[warp];
+  float m = -INFINITY, s = 0.f, s_low = 0.f;   // the lane's maximum and sum
+  float a = -INFINITY, c = -INFINITY;          // its largest in even and odd vectors
+  uint32_t limit = kLeast;                     // values from here on may count
+  int n = 0, known = 0;                        // candidates, those when the limit was found
+#pragma unroll 1
+  for (int stage = 0; at.l < lists; stage = stage + 1 < kStages ? stage + 1 : 0) {
+    fetch(stage == 0 ? kStages - 1 : stage - 1);
+    asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+    const uint4* tile = &sm.tile[warp][stage][0][lane];
+    const auto key = [&](float x, int u, int j) {
+      const uint32_t pos = (uint32_t)(at.t0 + (u * 32 + lane) * kPer + j);
+      return (u64)ordered(x) << 32 | ~pos;
+    };
+    const auto select = [&](uint32_t& limit) {
+      u64* list = sm.list + at.l * k;
+      best_keys(buf, n, k, list);
+      n = known = min(n, k);
+      for (int i = lane; i < n; i += 32) buf[i] = list[i];
+      if (n == k) limit = max(limit, (uint32_t)(list[k - 1] >> 32));
+      __syncwarp();
+    };
+    uint32_t most[2] = {Type<T>::kNone, Type<T>::kNone};
+#pragma unroll
+    for (int u = 0; u < kVecs; ++u) {
+      const uint4 v = tile[u * 32];
+      most[u & 1] = Type<T>::max2(most[u & 1], Type<T>::max2(Type<T>::max2(v.x, v.y), Type<T>::max2(v.z, v.w)));
+    }
+    const float even = Type<T>::top(most[0]), odd = Type<T>::top(most[1]), top = fmaxf(even, odd);
+    a = fmaxf(a, even);
+    c = fmaxf(c, odd);
+    // the sum, over differences to the lane's maximum
+    if (top > m) {
+      const float f = ex2((m - top) * kLog2e);
+      s *= f;
+      s_low *= f;
+      m = top;
+    }
+    const float ref = m > -INFINITY ? m : 0.f;
+    const u64 minus = f2(-ref, -ref), scale = f2(kLog2e, kLog2e);
+    u64 sum[2] = {0, 0};
+#pragma unroll 2
+    for (int u = 0; u < kVecs; ++u) {
+      const uint4 v = tile[u * 32];
+#pragma unroll
+      for (int j = 0; j < kPer; j += 2) {
+        float x, y;
+        f2(mul2(add2(f2(Type<T>::at(v, j), Type<T>::at(v, j + 1)), minus), scale), x, y);
+        sum[j / 2 & 1] = add2(sum[j / 2 & 1], f2(ex2(x), ex2(y)));
+      }
+    }
+    float p0, p1, p2, p3;
+    f2(sum[0], p0, p1);
+    f2(sum[1], p2, p3);
+    const float x = (p0 + p1) + (p2 + p3), t = s + x, back = t - s;
+    s_low += (s - (t - back)) + (x - back);
+    s = t;
+    if (__any_sync(~0u, top >= unordered(limit))) {
+      // a new limit for the first tile, then whenever it has let k more through
+      if (n - known >= k || n == 0) {
+        limit = max(limit, kth_of(a, c, k));
+        known = n;
+      }
+      // the lane's vectors that reach it, one after the other
+      uint32_t hits = 0;
+      if (top >= unordered(limit)) {
+#pragma unroll
+        for (int u = 0; u < kVecs; ++u) {
+          const uint4 v = tile[u * 32];
+          const uint32_t best = Type<T>::max2(Type<T>::max2(v.x, v.y), Type<T>::max2(v.z, v.w));
+          hits |= (uint32_t)(Type<T>::top(best) >= unordered(limit)) << u;
+        }
+      }
+      bool selected = false;
+#pragma unroll 1
+      while (__any_sync(~0u, hits != 0)) {
+        if (n + 32 * kPer > kCap) {
+          // No room for whatever comes: the best so far are selected exactly.
+          select(limit);
+          selected = true;
+        }
+        const float least = unordered(limit);
+        if (lane == 0) sm.count[warp] = n;
+        __syncwarp();
+        if (hits) {
+          const int u = __ffs(hits) - 1;
+          hits &= hits - 1;
+          const uint4 v = tile[u * 32];
+#pragma unroll
+          for (int j = 0; j < kPer; ++j) {
+            const float y = Type<T>::at(v, j);
+            if (y >= least) buf[atomicAdd(&sm.count[warp], 1)] = key(y, u, j);
+          }
+        }
+        __syncwarp();
+        n = sm.count[warp];
+      }
+      if (selected) {  // later tiles' values have to be greater than the last of the best
+        select(limit);
+        if (n == k) ++limit;
+      }
+    }
+    if (!at.last()) {
+      at.t0 += Walk<T>::kTile;
       continue;
     }
-    const int64_t from = min(hi, lo + len * (l % parts));
-    const T* row = static_cast<const T*>(p.logits) + b * p.batch_stride + w * p.beam_stride;
-    scan_part<T>(row, from, min(hi, from + len), k, sm.buf[warp], sm.list + l * k, &sm.num[l], &sm.stat[rank][l]);
+    // the part's end
+    best_keys(buf, n, k, sm.list + at.l * k);
+    const float wm = unordered(__reduce_max_sync(~0u, ordered(m)));
+    s = (s + s_low) * ex2((wm > -INFINITY ? m - wm : 0.f) * kLog2e);
+#pragma unroll
+    for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(~0u, s, d);
+    if (lane == 0) {
+      sm.num[at.l] = min(n, k);
+      sm.stat[rank][at.l] = make_float2(wm, s);
+    }
+    at.enter(p, b, lo, hi, len, at.l + kWarps);
+    m = a = c = -INFINITY;
+    s = s_low = 0.f;
+    limit = kLeast;
+    n = known = 0;
   }
   __syncthreads();
   cluster_wait();
   // Every CTA gets every CTA's part of the rows' statistics.
+#pragma unroll 1
   for (int i = tid; i < cluster * lists; i += kThreads) {
     const int to = i / lists, l = i % lists;
     if (to == (int)rank) continue;
@@ -427,16 +497,19 @@ __global__ void __launch_bounds__(kThreads, 2) mla_beam_select_kernel(const Beam
   }
   cluster_sync();
   // A row's sum: a quarter warp a row.
+#pragma unroll 1
   for (int w0 = 0; w0 < W; w0 += kThreads / 8) {
     const int w = w0 + tid / 8, of = cluster * parts;
     float m = -INFINITY;
     double sum = 0;
     if (w < W) {
+#pragma unroll 1
       for (int i = tid % 8; i < of; i += 8) m = fmaxf(m, sm.stat[i / parts][w * parts + i % parts].x);
     }
 #pragma unroll
     for (int d = 4; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, d));
     if (w < W) {
+#pragma unroll 1
       for (int i = tid % 8; i < of; i += 8) {
         const float2 x = sm.stat[i / parts][w * parts + i % parts];
         sum += m > -INFINITY ? (double)x.y * exp64((double)x.x - (double)m) : (double)x.y;
@@ -462,13 +535,14 @@ __global__ void __launch_bounds__(kThreads, 2) mla_beam_select_kernel(const Beam
     else if (!(sm.lse[w] < INFINITY)) sm.num[tid] = 0;
   }
   __syncthreads();
+#pragma unroll 1
   for (int e = tid; e < lists * k; e += kThreads) {
     const int l = e / k, w = l / parts;
     if (e % k >= sm.num[l]) continue;
     const double c = p.scores[b * W + w];
     const u64 key = sm.list[e];
     const bool end = sm.ends[w];
-    sm.pos[e] = (long long)w * V + (end ? (uint32_t)p.end_token : (uint32_t)~(uint32_t)key);
+    sm.pos[e] = (long long)w << 32 | (end ? (uint32_t)p.end_token : (uint32_t)~(uint32_t)key);
     sm.list[e] = ordered(end ? c : c + ((double)unordered((uint32_t)(key >> 32)) - sm.lse[w]));
   }
   __syncthreads();
@@ -483,34 +557,40 @@ __global__ void __launch_bounds__(kThreads, 2) mla_beam_select_kernel(const Beam
   });
   if (tid == 0) {
     int sum = 0;
+#pragma unroll 1
     for (int l = 0; l < lists; ++l) sum += sm.num[l];
     st_cluster_u32(mapa(smem_u32(sm.got_num + rank), 0), (uint32_t)min(sum, k));
   }
   cluster_sync();
   if (rank != 0) return;
-  const auto put = [&](int at, float s, long long q) {
+  const auto put = [&](int at, float s, int w, int t) {
     p.out_scores[b * k + at] = s;
-    p.parents[b * k + at] = (int)(b * W + q / V);
-    p.tokens[b * k + at] = (int)(q % V);
+    p.parents[b * k + at] = (int)(b * W + w);
+    p.tokens[b * k + at] = t;
   };
   int have = 0;
+#pragma unroll 1
   for (int c = 0; c < cluster; ++c) have += sm.got_num[c];
   have = min(have, k);
   merge_lists(sm.got_score, sm.got_pos, sm.got_num, cluster, k, k, [&](int at, int e) {
-    put(at, (float)unordered(sm.got_score[e]), sm.got_pos[e]);
-    sm.member[at] = sm.got_pos[e];
+    const long long q = sm.got_pos[e];
+    put(at, (float)unordered(sm.got_score[e]), (int)(q >> 32), (int)(uint32_t)q);
+    sm.member[at] = (q >> 32) * V + (uint32_t)q;
   });
   // Fewer than k continuations: the lowest positions that are none, at -inf.
   __syncthreads();
   if (tid < k - have) {
     long long q = tid;
+#pragma unroll 1
     for (bool moved = true; moved;) {
       int below = 0;
+#pragma unroll 1
       for (int j = 0; j < have; ++j) below += sm.member[j] <= q;
       moved = tid + below != q;
       q = tid + below;
     }
-    put(have + tid, -INFINITY, q);
+    // (q < W + k: at most one of either is above V)
+    put(have + tid, -INFINITY, (int)(q / V), (int)(q % V));
   }
 }
 
