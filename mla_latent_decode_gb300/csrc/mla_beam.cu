@@ -12,19 +12,20 @@
 // an order of arrival.
 //
 // Which logits of a tile may count: the k-th largest of the 64 largest values that a
-// warp's lanes have met in their even and odd vectors (cut to 16 bits, so found in 16
-// votes) is a bound that at least k values of the part reach, and few more do (about
-// k ln k for values in random order).  A tile without a value above the bound, which
-// most are, costs its maximum and its sum only.  Where too many reach it (ties, a
+// warp's lanes have met in their even and odd vectors is a bound that at least k
+// values of the part reach, and few more do (about k ln k for values in random
+// order).  A tile without a value above the bound costs its maximum and its sum only.  Where too many reach it (ties, a
 // vocabulary that is mostly masked) the best k so far are selected exactly, and
 // later values have to exceed the last of them.
 //
 // Exponents are fp32 differences to the lane's own maximum; sums are fp32 over a
 // tile (64 terms), compensated over tiles, and meet in fp64, where the scores are
 // formed: two beams' tokens often differ by less than fp32 shows of their sums.
-// Scores are compared as ordered integers (fp64 compares run at 2 a cycle and SM).
+// Scores are compared as ordered integers (fp64 runs at 2 a cycle and SM).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+
+#include <algorithm>
 
 #include "mla_internal.h"
 #include "ptx_sm103.cuh"
@@ -41,8 +42,9 @@ constexpr int kVecs = 8;                    // 16-byte vectors of a row per lane
 constexpr int kStages = 2;                  // tiles of a warp in shared memory
 constexpr int kMaxK = MLA_BEAM_MAX_K, kMaxW = MLA_BEAM_MAX_W;
 constexpr int kMaxLists = 32;               // parts of rows in a CTA
+constexpr int kMaxParts = 512;              // in a cluster
 constexpr int kCount = 512;
-constexpr int kCap = kMaxK + 8 * 32 + 64;   // candidates of a warp: its best so far, a vector's, room
+constexpr int kCap = kMaxK + 8 * 32 + 62;   // candidates of a warp: its best so far, a vector's, room
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr uint32_t kLeast = 0x00800000u;    // the least finite value's place in the order
 typedef unsigned long long u64;
@@ -57,7 +59,7 @@ struct BeamParams {
   int32_t* parents;
   int32_t* tokens;
   int* status;
-  int cluster, parts;
+  int cluster, parts;  // CTAs of a request, parts of a row
 };
 
 // Two CTAs an SM.
@@ -70,14 +72,15 @@ struct Smem {
       long long got_pos[kMaxCluster * kMaxK];
     };
   };
-  u64 buf[kWarps][kCap];                    // candidates of the warps' parts at hand
+  u64 buf[kWarps][kCap + 2];                // candidates of the warps' parts at hand
+  uint32_t words[kWarps][64];
   u64 list[kMaxLists * kMaxK];              // the parts' best in order; later: their scores
-  float2 stat[kMaxCluster][kMaxLists];      // (max, sum) of every CTA's parts
+  float2 stat[kMaxParts];                   // (max, sum) of the cluster's parts
   double lse[kMaxW];
   int num[kMaxLists];                       // entries of a list
   int ends[kMaxW];                          // a finished beam's end counts
   int got_num[kMaxCluster];
-  int count[kWarps];
+  float score[kMaxW], live[kMaxW];          // the beams'; with finished ones at -inf
   long long member[kMaxK];
 };
 static_assert(sizeof(Smem) <= 113 * 1024, "shared memory of two CTAs an SM");
@@ -120,29 +123,45 @@ __device__ __forceinline__ u64 mul2(u64 a, u64 b) {
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
 }
-// e^x for x <= 0 in fp64: 2^n times the Taylor series of e^r, |r| <= ln 2 / 2
-// (0.35^11 / 11! is 2^-42).
-__device__ __forceinline__ double exp64(double x) {
-  if (!(x > -700.0)) return x == x ? 0.0 : x;
-  const double n = rint(x * 1.4426950408889634);
-  const double r = fma(n, -0.6931471805599453, x);
-  double p = 1.0 / 3628800;
-  p = fma(p, r, 1.0 / 362880);
-  p = fma(p, r, 1.0 / 40320);
-  p = fma(p, r, 1.0 / 5040);
-  p = fma(p, r, 1.0 / 720);
-  p = fma(p, r, 1.0 / 120);
-  p = fma(p, r, 1.0 / 24);
-  p = fma(p, r, 1.0 / 6);
-  p = fma(p, r, 0.5);
-  p = fma(p, r, 1.0);
-  p = fma(p, r, 1.0);
-  return p * __longlong_as_double((long long)(1023 + (int)n) << 52);
+// Pairs (hi, lo) of fp32, hi + lo exact to about 2^-45 of it: fp64 arithmetic runs at
+// 2 a cycle and SM, and these few sums would take longer than the logits.
+struct Two {
+  float hi, lo;
+};
+__device__ __forceinline__ Two plus(Two a, Two b) {
+  const float s = a.hi + b.hi, t = s - a.hi, e = (a.hi - (s - t)) + (b.hi - t) + a.lo + b.lo;
+  const float hi = s + e;
+  return {hi, s < INFINITY ? e - (hi - s) : 0.f};
 }
-// ln x for finite x >= 1 (a sum with its largest term 1): fp32's, and a Newton step.
-__device__ __forceinline__ double log64(double x) {
-  const double l = (double)logf((float)x);
-  return l + (x * exp64(-l) - 1.0);
+// e^x for x <= 0 within about 2^-26: 2^n (1 + r + r^2 (1/2 + r/6 + ...)), |r| <= ln 2 / 2.
+__device__ __forceinline__ Two exp2f(float x) {
+  if (!(x > -80.f)) return {x == x ? 0.f : x, 0.f};  // (2^-115 of a sum's largest term)
+  const float n = rintf(x * kLog2e);
+  float r = fmaf(n, -0.693145752f, x);  // ln 2 in two parts, the first of 15 bits
+  r = fmaf(n, -1.42860677e-6f, r);
+  float q = 1.f / 40320;
+  q = fmaf(q, r, 1.f / 5040);
+  q = fmaf(q, r, 1.f / 720);
+  q = fmaf(q, r, 1.f / 120);
+  q = fmaf(q, r, 1.f / 24);
+  q = fmaf(q, r, 1.f / 6);
+  q = fmaf(q, r, 0.5f);
+  q = q * r * r;
+  const float a = 1.f + r, low = (r - (a - 1.f)) + q, scale = __int_as_float((127 + (int)n) << 23);
+  const float hi = a + low;
+  return {hi * scale, (low - (hi - a)) * scale};
+}
+// y e^x
+__device__ __forceinline__ Two times_exp(float y, float x) {
+  const Two e = exp2f(x);
+  const float hi = y * e.hi;
+  return {hi, fmaf(y, e.hi, -hi) + y * e.lo};
+}
+// ln of a finite x >= 1 (a sum with its largest term 1): fp32's, and a Newton step.
+__device__ __forceinline__ double log_of(Two x) {
+  const float l = logf(x.hi);
+  const Two e = exp2f(-l);
+  return (double)l + (double)(fmaf(x.hi, e.hi, -1.f) + (x.hi * e.lo + x.lo * e.hi));
 }
 
 template <typename T>
@@ -150,6 +169,7 @@ struct Type;
 template <>
 struct Type<float> {
   static constexpr int kPer = 4;
+  static __device__ __forceinline__ float one(float x) { return x; }
   static __device__ __forceinline__ float at(const uint4& v, int j) {
     return __uint_as_float(j == 0 ? v.x : j == 1 ? v.y : j == 2 ? v.z : v.w);
   }
@@ -162,6 +182,7 @@ struct Type<float> {
 template <>
 struct Type<__nv_bfloat16> {
   static constexpr int kPer = 8;
+  static __device__ __forceinline__ float one(__nv_bfloat16 x) { return __bfloat162float(x); }
   static __device__ __forceinline__ float at(const uint4& v, int j) {
     const uint32_t w = j < 2 ? v.x : j < 4 ? v.y : j < 6 ? v.z : v.w;
     return __uint_as_float(j & 1 ? w & 0xffff0000u : w << 16);
@@ -178,6 +199,7 @@ struct Type<__nv_bfloat16> {
 template <>
 struct Type<__half> {
   static constexpr int kPer = 8;
+  static __device__ __forceinline__ float one(__half x) { return __half2float(x); }
   static __device__ __forceinline__ float at(const uint4& v, int j) {
     const uint32_t w = j < 2 ? v.x : j < 4 ? v.y : j < 6 ? v.z : v.w;
     const __half2 h = *reinterpret_cast<const __half2*>(&w);
@@ -212,55 +234,84 @@ __device__ __noinline__ uint4 load_edge(const T* row, int64_t e, int64_t lo, int
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// The k best of a warp's n keys, in order, to `out`: a key's rank is the number of
-// greater ones (keys differ).
-__device__ __noinline__ void best_keys(const u64* keys, int n, int k, u64* out) {
+// The k best of a warp's n keys, in order, to `out`, of those with values from
+// `limit` on (at least k, or all): they are moved to the front first, then a key's
+// rank is the number of greater ones (keys differ).  Returns their number, k at most.
+__device__ __noinline__ int best_keys(u64* keys, int n, int k, uint32_t limit, u64* out) {
   const int lane = threadIdx.x & 31;
   __syncwarp();
-  for (int i = lane; i < n; i += 32) {
+  int m = 0;
+#pragma unroll 1
+  for (int i0 = 0; i0 < n; i0 += 32) {
+    const u64 mine = i0 + lane < n ? keys[i0 + lane] : 0;
+    const bool stays = (uint32_t)(mine >> 32) >= limit;
+    const uint32_t all = __ballot_sync(~0u, stays);
+    if (stays) keys[m + __popc(all & ((1u << lane) - 1))] = mine;
+    m += __popc(all);
+  }
+  if (lane == 0) keys[m] = 0;  // (the buffer has room)
+  __syncwarp();
+#pragma unroll 1
+  for (int i = lane; i < m; i += 32) {
     const u64 mine = keys[i];
     int rank = 0;
 #pragma unroll 4
-    for (int j = 0; j < n; ++j) rank += keys[j] > mine;
+    for (int j = 0; j < m; j += 2) {
+      const ulonglong2 x = *reinterpret_cast<const ulonglong2*>(keys + j);
+      rank += (x.x > mine) + (x.y > mine);
+    }
     if (rank < k) out[rank] = mine;
   }
   __syncwarp();
+  return min(m, k);
 }
 
-// The k-th largest of the warp's 64 values, its place in the order cut to 16 bits.
-__device__ __forceinline__ uint32_t kth_of(float a, float b, int k) {
-  const uint32_t ka = ordered(a) >> 16, kb = ordered(b) >> 16;
-  uint32_t x = 0;
-#pragma unroll 2
-  for (uint32_t bit = 1u << 15; bit; bit >>= 1) {
-    const uint32_t y = x | bit;
-    if (__popc(__ballot_sync(~0u, ka >= y)) + __popc(__ballot_sync(~0u, kb >= y)) >= k) x = y;
+// The place in the order of the k-th largest of the warp's 64 values: each is
+// compared with all of them, through 64 words of shared memory.
+__device__ __forceinline__ uint32_t kth_of(float a, float b, int k, uint32_t* words) {
+  const int lane = threadIdx.x & 31;
+  const uint32_t ka = ordered(a), kb = ordered(b);
+  __syncwarp();
+  words[lane] = ka;
+  words[32 + lane] = kb;
+  __syncwarp();
+  int above_a = 0, above_b = 0;
+#pragma unroll 4
+  for (int j = 0; j < 16; ++j) {
+    const uint4 x = *reinterpret_cast<const uint4*>(words + 4 * j);
+    above_a += (x.x > ka) + (x.y > ka) + (x.z > ka) + (x.w > ka);
+    above_b += (x.x > kb) + (x.y > kb) + (x.z > kb) + (x.w > kb);
   }
-  return x << 16;
+  // the least value that fewer than k exceed
+  return __reduce_min_sync(~0u, min(above_a < k ? ka : ~0u, above_b < k ? kb : ~0u));
 }
 
 // A warp's way through its parts of rows, tile by tile; parts of which nothing
-// counts (finished or dead beams) are left out.
+// counts (finished or dead beams) are left out.  Part g is row g / p.parts's; the
+// cluster's warps take turns with them.
 template <typename T>
 struct Walk {
   const T* row;
   int64_t t0, lo, hi;  // the tile's first position, the part
-  int l;               // list of the part; none left: p.W * p.parts
+  int g;               // the part; none left: p.W * p.parts
   static constexpr int kTile = 32 * kVecs * Type<T>::kPer;
-  __device__ __forceinline__ void enter(const BeamParams& p, int64_t b, int64_t seg_lo, int64_t seg_hi, int64_t len, int at) {
-    const int lists = p.W * p.parts;
+  __device__ __forceinline__ void enter(const BeamParams& p, const float* score, int64_t b, int len, int from) {
+    const int all = p.W * p.parts, step = p.cluster * kWarps;
 #pragma unroll 1
-    for (l = at; l < lists; l += kWarps) {
-      const int w = l / p.parts;
-      const bool done = p.finished && p.finished[b * p.W + w];
-      lo = min(seg_hi, seg_lo + len * (l % p.parts));
-      hi = min(seg_hi, lo + len);
-      if (done || !(fabsf(p.scores[b * p.W + w]) < INFINITY) || lo == hi) continue;
+    for (g = from; g < all; g += step) {
+      const int w = (uint32_t)g / (uint32_t)p.parts;
       row = static_cast<const T*>(p.logits) + b * p.batch_stride + w * p.beam_stride;
-      t0 = lo - (int64_t)(reinterpret_cast<uintptr_t>(row + lo) / sizeof(T) % Type<T>::kPer);
+      // cut where 16-byte vectors start: only a row's ends have partial ones
+      const int shift = (int)(reinterpret_cast<uintptr_t>(row) / sizeof(T) % Type<T>::kPer);
+      lo = min((int64_t)p.V, (int64_t)len * (g - w * p.parts));
+      hi = min((int64_t)p.V, lo + len);
+      if (lo > 0 && lo < p.V) lo -= shift;
+      if (hi < p.V) hi -= shift;
+      if (!(fabsf(score[w]) < INFINITY) || lo >= hi) continue;
+      t0 = lo > 0 ? lo : -shift;
       return;
     }
-    l = lists;
+    g = all;
   }
   __device__ __forceinline__ bool last() const { return t0 + kTile >= hi; }
 };
@@ -281,19 +332,28 @@ __device__ __forceinline__ void merge_lists(u64* score, const long long* pos, co
     for (int e = threadIdx.x; e < all + (all & 1); e += kThreads)
       if (e == all || e % pitch >= num[e / pitch]) score[e] = 0;  // below every score
     __syncthreads();
+    // as many threads an entry as there are (a power of two, within a warp)
+    int group = 1;
 #pragma unroll 1
-    for (int e = threadIdx.x; e < all; e += kThreads) {
-      const u64 s = score[e];
-      if (s == 0) continue;
+    while (group < 32 && 2 * group * all <= kThreads) group *= 2;
+    const int sub = threadIdx.x % group;
+#pragma unroll 1
+    for (int e0 = 0; e0 < all; e0 += kThreads / group) {
+      const int e = e0 + threadIdx.x / group;
+      const u64 s = e < all ? score[e] : 0;
       int rank = 0;
+      if (s) {
+        const long long at = pos[e];
 #pragma unroll 4
-      for (int j = 0; j < all; j += 2) {
-        const ulonglong2 x = *reinterpret_cast<const ulonglong2*>(score + j);
-        rank += (x.x > s) + (x.y > s);
-        if (x.x == s && j != e) rank += pos[j] < pos[e];
-        if (x.y == s && j + 1 != e) rank += pos[j + 1] < pos[e];
+        for (int j = 2 * sub; j < all; j += 2 * group) {
+          const ulonglong2 x = *reinterpret_cast<const ulonglong2*>(score + j);
+          const longlong2 q = *reinterpret_cast<const longlong2*>(pos + j);
+          rank += (x.x > s || (x.x == s && q.x < at)) + (x.y > s || (x.y == s && q.y < at));
+        }
       }
-      if (rank < k) put(rank, e);
+#pragma unroll 1
+      for (int d = group / 2; d; d >>= 1) rank += __shfl_xor_sync(~0u, rank, d);
+      if (s && sub == 0 && rank < k) put(rank, e);
     }
     return;
   }
@@ -327,47 +387,56 @@ __global__ void __launch_bounds__(kThreads, 2) mla_beam_select_kernel(const Beam
   const uint32_t rank = cluster_ctarank();
   const int cluster = p.cluster, parts = p.parts;  // parts of a row in a CTA
   const int64_t b = blockIdx.x / cluster;
-  const int W = p.W, V = p.V, k = p.k, lists = W * parts;
-  cluster_arrive();  // the CTAs have started when they write to each other
-  const int64_t seg = ((uint32_t)(V + cluster - 1) / (uint32_t)cluster + 63) / 64 * 64;
-  const int64_t lo = min((int64_t)V, seg * rank), hi = min((int64_t)V, lo + seg);
-  const int64_t len = ((uint32_t)(hi - lo + parts - 1) / (uint32_t)parts + 63) / 64 * 64;
-  const int lane = tid & 31;
-#pragma unroll 1
-  for (int l = warp; l < lists; l += kWarps) {
-    if (lane == 0) {
-      sm.num[l] = 0;
-      sm.stat[rank][l] = make_float2(-INFINITY, 0.f);
-    }
+  const int W = p.W, V = p.V, k = p.k, all = W * parts, step = cluster * kWarps;
+  const int lists = kWarps * ((all + step - 1) / step);  // of this CTA: list l is part own(l)
+  const auto own = [&](int l) { return l / kWarps * step + (int)rank * kWarps + l % kWarps; };
+  if (tid < W) {
+    const float c = p.scores[b * W + tid];
+    sm.score[tid] = c;
+    sm.live[tid] = p.finished && p.finished[b * W + tid] ? -INFINITY : c;
   }
+  cluster_arrive();  // the CTAs have started when they write to each other
+  const int len = (int)((((uint32_t)V + parts - 1) / (uint32_t)parts + 63) / 64 * 64);
+  const int lane = tid & 31;
+  for (int l = tid; l < lists; l += kThreads) {
+    sm.num[l] = 0;
+    if (own(l) < all) sm.stat[own(l)] = make_float2(-INFINITY, 0.f);
+  }
+  __syncthreads();
   constexpr int kPer = Type<T>::kPer;
   Walk<T> at = {}, to = {};  // the tile at hand, the tile to load
   const auto fetch = [&](int stage) {
-    if (to.l < lists) {
+    if (to.g < all) {
       uint4* dst = &sm.tile[warp][stage][0][lane];
       const int64_t e0 = to.t0 + lane * kPer;
-#pragma unroll 2
-      for (int u = 0; u < kVecs; ++u) {
-        const int64_t e = e0 + u * 32 * kPer;
-        if (e >= to.lo && e + kPer <= to.hi) cp_async16(dst + u * 32, to.row + e);
-        else dst[u * 32] = load_edge<T>(to.row, e, to.lo, to.hi);
+      if (to.t0 >= to.lo && to.t0 + Walk<T>::kTile <= to.hi) {
+        const T* src = to.row + e0;
+#pragma unroll
+        for (int u = 0; u < kVecs; ++u) cp_async16(dst + u * 32, src + u * 32 * kPer);
+      } else {
+#pragma unroll 1
+        for (int u = 0; u < kVecs; ++u) {
+          const int64_t e = e0 + u * 32 * kPer;
+          if (e >= to.lo && e + kPer <= to.hi) cp_async16(dst + u * 32, to.row + e);
+          else dst[u * 32] = load_edge<T>(to.row, e, to.lo, to.hi);
+        }
       }
-      if (to.last()) to.enter(p, b, lo, hi, len, to.l + kWarps);
+      if (to.last()) to.enter(p, sm.live, b, len, to.g + step);
       else to.t0 += Walk<T>::kTile;
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  to.enter(p, b, lo, hi, len, warp);
+  to.enter(p, sm.live, b, len, (int)rank * kWarps + warp);
   at = to;
 #pragma unroll 1
   for (int i = 0; i < kStages - 1; ++i) fetch(i);
   u64* buf = sm.buf[warp];
   float m = -INFINITY, s = 0.f, s_low = 0.f;   // the lane's maximum and sum
   float a = -INFINITY, c = -INFINITY;          // its largest in even and odd vectors
-  uint32_t limit = kLeast;                     // values from here on may count
+  uint32_t floor = kLeast, limit = kLeast;     // k values reach the one; from the other on values count
   int n = 0, known = 0;                        // candidates, those when the limit was found
 #pragma unroll 1
-  for (int stage = 0; at.l < lists; stage = stage + 1 < kStages ? stage + 1 : 0) {
+  for (int stage = 0; at.g < all; stage = stage + 1 < kStages ? stage + 1 : 0) {
     fetch(stage == 0 ? kStages - 1 : stage - 1);
     asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
     const uint4* tile = &sm.tile[warp][stage][0][lane];
@@ -375,19 +444,20 @@ __global__ void __launch_bounds__(kThreads, 2) mla_beam_select_kernel(const Beam
       const uint32_t pos = (uint32_t)(at.t0 + (u * 32 + lane) * kPer + j);
       return (u64)ordered(x) << 32 | ~pos;
     };
-    const auto select = [&](uint32_t& limit) {
-      u64* list = sm.list + at.l * k;
-      best_keys(buf, n, k, list);
-      n = known = min(n, k);
+    const auto select = [&]() {
+      u64* list = sm.list + (at.g / step * kWarps + warp) * k;
+      n = known = best_keys(buf, n, k, floor, list);
       for (int i = lane; i < n; i += 32) buf[i] = list[i];
-      if (n == k) limit = max(limit, (uint32_t)(list[k - 1] >> 32));
+      if (n == k) floor = max(floor, (uint32_t)(list[k - 1] >> 32));
+      limit = max(limit, floor);
       __syncwarp();
     };
-    uint32_t most[2] = {Type<T>::kNone, Type<T>::kNone};
+    uint32_t best[kVecs], most[2];
 #pragma unroll
     for (int u = 0; u < kVecs; ++u) {
       const uint4 v = tile[u * 32];
-      most[u & 1] = Type<T>::max2(most[u & 1], Type<T>::max2(Type<T>::max2(v.x, v.y), Type<T>::max2(v.z, v.w)));
+      best[u] = Type<T>::max2(Type<T>::max2(v.x, v.y), Type<T>::max2(v.z, v.w));
+      most[u & 1] = u < 2 ? best[u] : Type<T>::max2(most[u & 1], best[u]);
     }
     const float even = Type<T>::top(most[0]), odd = Type<T>::top(most[1]), top = fmaxf(even, odd);
     a = fmaxf(a, even);
@@ -402,7 +472,7 @@ __global__ void __launch_bounds__(kThreads, 2) mla_beam_select_kernel(const Beam
     const float ref = m > -INFINITY ? m : 0.f;
     const u64 minus = f2(-ref, -ref), scale = f2(kLog2e, kLog2e);
     u64 sum[2] = {0, 0};
-#pragma unroll 2
+#pragma unroll 4
     for (int u = 0; u < kVecs; ++u) {
       const uint4 v = tile[u * 32];
 #pragma unroll
@@ -421,46 +491,47 @@ __global__ void __launch_bounds__(kThreads, 2) mla_beam_select_kernel(const Beam
     if (__any_sync(~0u, top >= unordered(limit))) {
       // a new limit for the first tile, then whenever it has let k more through
       if (n - known >= k || n == 0) {
-        limit = max(limit, kth_of(a, c, k));
+        floor = max(floor, kth_of(a, c, k, sm.words[warp]));
+        limit = max(limit, floor);
         known = n;
       }
       // the lane's vectors that reach it, one after the other
       uint32_t hits = 0;
       if (top >= unordered(limit)) {
 #pragma unroll
-        for (int u = 0; u < kVecs; ++u) {
-          const uint4 v = tile[u * 32];
-          const uint32_t best = Type<T>::max2(Type<T>::max2(v.x, v.y), Type<T>::max2(v.z, v.w));
-          hits |= (uint32_t)(Type<T>::top(best) >= unordered(limit)) << u;
-        }
+        for (int u = 0; u < kVecs; ++u) hits |= (uint32_t)(Type<T>::top(best[u]) >= unordered(limit)) << u;
       }
       bool selected = false;
 #pragma unroll 1
       while (__any_sync(~0u, hits != 0)) {
         if (n + 32 * kPer > kCap) {
           // No room for whatever comes: the best so far are selected exactly.
-          select(limit);
+          select();
           selected = true;
         }
         const float least = unordered(limit);
-        if (lane == 0) sm.count[warp] = n;
-        __syncwarp();
+        const int u = __ffs(hits) - 1;
+        uint32_t which = 0;  // of the vector's values
         if (hits) {
-          const int u = __ffs(hits) - 1;
           hits &= hits - 1;
           const uint4 v = tile[u * 32];
 #pragma unroll
-          for (int j = 0; j < kPer; ++j) {
-            const float y = Type<T>::at(v, j);
-            if (y >= least) buf[atomicAdd(&sm.count[warp], 1)] = key(y, u, j);
+          for (int j = 0; j < kPer; ++j) which |= (uint32_t)(Type<T>::at(v, j) >= least) << j;
+        }
+        // one a lane at a time: hardly any lane has more
+#pragma unroll 1
+        for (uint32_t all; (all = __ballot_sync(~0u, which != 0)) != 0; n += __popc(all)) {
+          if (which) {
+            const int j = __ffs(which) - 1;
+            which &= which - 1;
+            const float y = Type<T>::one(reinterpret_cast<const T*>(&tile[u * 32])[j]);
+            buf[n + __popc(all & ((1u << lane) - 1))] = key(y, u, j);
           }
         }
-        __syncwarp();
-        n = sm.count[warp];
       }
       if (selected) {  // later tiles' values have to be greater than the last of the best
-        select(limit);
-        if (n == k) ++limit;
+        select();
+        if (n == k) limit = max(limit, floor + 1);
       }
     }
     if (!at.last()) {
@@ -468,19 +539,21 @@ __global__ void __launch_bounds__(kThreads, 2) mla_beam_select_kernel(const Beam
       continue;
     }
     // the part's end
-    best_keys(buf, n, k, sm.list + at.l * k);
+    if (n > k) floor = max(floor, kth_of(a, c, k, sm.words[warp]));
+    const int l = at.g / step * kWarps + warp;
+    n = best_keys(buf, n, k, floor, sm.list + l * k);
     const float wm = unordered(__reduce_max_sync(~0u, ordered(m)));
     s = (s + s_low) * ex2((wm > -INFINITY ? m - wm : 0.f) * kLog2e);
 #pragma unroll
     for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(~0u, s, d);
     if (lane == 0) {
-      sm.num[at.l] = min(n, k);
-      sm.stat[rank][at.l] = make_float2(wm, s);
+      sm.num[l] = n;
+      sm.stat[at.g] = make_float2(wm, s);
     }
-    at.enter(p, b, lo, hi, len, at.l + kWarps);
+    at.enter(p, sm.live, b, len, at.g + step);
     m = a = c = -INFINITY;
     s = s_low = 0.f;
-    limit = kLeast;
+    floor = limit = kLeast;
     n = known = 0;
   }
   __syncthreads();
@@ -488,10 +561,10 @@ __global__ void __launch_bounds__(kThreads, 2) mla_beam_select_kernel(const Beam
   // Every CTA gets every CTA's part of the rows' statistics.
 #pragma unroll 1
   for (int i = tid; i < cluster * lists; i += kThreads) {
-    const int to = i / lists, l = i % lists;
-    if (to == (int)rank) continue;
-    const float2 x = sm.stat[rank][l];
-    const uint32_t at = mapa(smem_u32(&sm.stat[rank][l]), to);
+    const int to = i / lists, g = own(i % lists);
+    if (to == (int)rank || g >= all) continue;
+    const float2 x = sm.stat[g];
+    const uint32_t at = mapa(smem_u32(&sm.stat[g]), to);
     st_cluster_u32(at, __float_as_uint(x.x));
     st_cluster_u32(at + 4, __float_as_uint(x.y));
   }
@@ -499,47 +572,47 @@ __global__ void __launch_bounds__(kThreads, 2) mla_beam_select_kernel(const Beam
   // A row's sum: a quarter warp a row.
 #pragma unroll 1
   for (int w0 = 0; w0 < W; w0 += kThreads / 8) {
-    const int w = w0 + tid / 8, of = cluster * parts;
+    const int w = w0 + tid / 8;
     float m = -INFINITY;
-    double sum = 0;
+    Two sum = {0.f, 0.f};
     if (w < W) {
 #pragma unroll 1
-      for (int i = tid % 8; i < of; i += 8) m = fmaxf(m, sm.stat[i / parts][w * parts + i % parts].x);
+      for (int i = tid % 8; i < parts; i += 8) m = fmaxf(m, sm.stat[w * parts + i].x);
     }
 #pragma unroll
     for (int d = 4; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, d));
     if (w < W) {
 #pragma unroll 1
-      for (int i = tid % 8; i < of; i += 8) {
-        const float2 x = sm.stat[i / parts][w * parts + i % parts];
-        sum += m > -INFINITY ? (double)x.y * exp64((double)x.x - (double)m) : (double)x.y;
+      for (int i = tid % 8; i < parts; i += 8) {
+        const float2 x = sm.stat[w * parts + i];
+        sum = plus(sum, times_exp(x.y, m > -INFINITY ? x.x - m : 0.f));
       }
     }
 #pragma unroll
-    for (int d = 4; d; d >>= 1) sum += __shfl_xor_sync(~0u, sum, d);
+    for (int d = 4; d; d >>= 1) sum = plus(sum, {__shfl_xor_sync(~0u, sum.hi, d), __shfl_xor_sync(~0u, sum.lo, d)});
     if (w < W && tid % 8 == 0) {
-      const float c = p.scores[b * W + w];
+      const float c = sm.score[w];
       const bool done = p.finished && p.finished[b * W + w];
       // an infinite or undefined logit: no continuation of this beam counts
-      const bool whole = sum > 0 && sum < INFINITY && fabsf(m) < INFINITY;
-      sm.lse[w] = whole ? (double)m + log64(sum) : INFINITY;
-      sm.ends[w] = done && fabsf(c) < INFINITY && rank == 0;  // its end, at its score
-      if (rank == 0 && p.status && (!(c < INFINITY) || (!done && (sum != sum || m == INFINITY))))
+      const bool whole = sum.hi > 0 && sum.hi < INFINITY && fabsf(m) < INFINITY;
+      sm.lse[w] = whole ? (double)m + log_of(sum) : INFINITY;
+      sm.ends[w] = done && fabsf(c) < INFINITY;  // its end, at its score
+      if (rank == 0 && p.status && (!(c < INFINITY) || (!done && (sum.hi != sum.hi || m == INFINITY))))
         atomicOr(p.status, MLA_STATUS_BAD_SCORE);
     }
   }
   __syncthreads();
-  if (tid < lists) {
-    const int w = tid / parts;
-    if (sm.ends[w]) sm.num[tid] = tid % parts == 0;
+  if (tid < lists && own(tid) < all) {
+    const int w = own(tid) / parts;
+    if (sm.ends[w]) sm.num[tid] = own(tid) % parts == 0;
     else if (!(sm.lse[w] < INFINITY)) sm.num[tid] = 0;
   }
   __syncthreads();
 #pragma unroll 1
   for (int e = tid; e < lists * k; e += kThreads) {
-    const int l = e / k, w = l / parts;
+    const int l = e / k, w = own(l) / parts;
     if (e % k >= sm.num[l]) continue;
-    const double c = p.scores[b * W + w];
+    const double c = sm.score[w];
     const u64 key = sm.list[e];
     const bool end = sm.ends[w];
     sm.pos[e] = (long long)w << 32 | (end ? (uint32_t)p.end_token : (uint32_t)~(uint32_t)key);
@@ -595,7 +668,8 @@ __global__ void __launch_bounds__(kThreads, 2) mla_beam_select_kernel(const Beam
 }
 
 // CTAs of a request: as many as find room at once (two an SM), while a warp has
-// about a tile's worth of logits; parts of a row in a CTA: what evens out the warps.
+// about a tile of logits.  Parts of a row: the number whose rounds over the cluster's
+// warps cost least, a part its tiles and about three more.
 template <typename T>
 int launch_beam(BeamParams p, int B, cudaStream_t st) {
   auto kernel = mla_beam_select_kernel<T>;
@@ -611,10 +685,12 @@ int launch_beam(BeamParams p, int B, cudaStream_t st) {
   while (p.cluster < kMaxCluster && (int64_t)B * p.cluster * 2 <= 2 * sms &&
          (int64_t)p.W * p.V > (int64_t)p.cluster * kWarps * kTile / 2)
     p.cluster *= 2;
-  p.parts = 1;
-  const auto rounds = [&](int parts) { return (double)((p.W * parts + kWarps - 1) / kWarps) / parts; };
-  for (int parts = 2; parts <= kWarps && p.W * parts <= kMaxLists; parts *= 2)
-    if (rounds(parts) < rounds(p.parts)) p.parts = parts;
+  double least = 0;
+  for (int parts = 1; p.W * parts <= std::max(2 * p.cluster * kWarps, p.W) && p.W * parts <= kMaxParts; ++parts) {
+    const int rounds = (p.W * parts + p.cluster * kWarps - 1) / (p.cluster * kWarps);
+    const double cost = rounds * ((double)((p.V / parts + kTile) / kTile) + 3);
+    if (parts == 1 || cost < least) least = cost, p.parts = parts;
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(B * p.cluster), 1, 1);
   cfg.blockDim = dim3(kThreads, 1, 1);
