@@ -14,7 +14,9 @@
 // Which logits of a tile may count: the k-th largest of the 64 largest values that a
 // warp's lanes have met in their even and odd vectors is a bound that at least k
 // values of the part reach, and few more do (about k ln k for values in random
-// order).  A tile without a value above the bound costs its maximum and its sum only.  Where too many reach it (ties, a
+// order).  While tiles pass only each lane's largest value of each is kept; after 16 of
+// them, or at the part's end, the bound is found and the few lanes' tiles that reach
+// it are read again (about 20 times 128 bytes of 64 KB).  Where too many reach it (ties, a
 // vocabulary that is mostly masked) the best k so far are selected exactly, and
 // later values have to exceed the last of them.
 //
@@ -35,16 +37,17 @@ namespace {
 
 using namespace ptx;
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
-constexpr int kMaxCluster = 16;
+constexpr int kWarps = 8;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kMaxCluster = 8;               // (16 of them start later: 16 x 5 x 100003 took 33 us, not 22)
 constexpr int kVecs = 8;                    // 16-byte vectors of a row per lane and tile
 constexpr int kStages = 2;                  // tiles of a warp in shared memory
 constexpr int kMaxK = MLA_BEAM_MAX_K, kMaxW = MLA_BEAM_MAX_W;
 constexpr int kMaxLists = 32;               // parts of rows in a CTA
 constexpr int kMaxParts = 512;              // in a cluster
 constexpr int kCount = 512;
-constexpr int kCap = kMaxK + 8 * 32 + 62;   // candidates of a warp: its best so far, a vector's, room
+constexpr int kEpoch = 16;                  // tiles whose values are looked for at once
+constexpr int kCap = kMaxK + 126;           // candidates of a warp: its best so far, room for a lane's tile
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr uint32_t kLeast = 0x00800000u;    // the least finite value's place in the order
 typedef unsigned long long u64;
@@ -74,6 +77,7 @@ struct Smem {
   };
   u64 buf[kWarps][kCap + 2];                // candidates of the warps' parts at hand
   uint32_t words[kWarps][64];
+  uint16_t tops[kWarps][kEpoch * 32];       // lanes' largest values of the tiles, cut to 16 bits; later: pairs
   u64 list[kMaxLists * kMaxK];              // the parts' best in order; later: their scores
   float2 stat[kMaxParts];                   // (max, sum) of the cluster's parts
   double lse[kMaxW];
@@ -169,7 +173,7 @@ struct Type;
 template <>
 struct Type<float> {
   static constexpr int kPer = 4;
-  static __device__ __forceinline__ float one(float x) { return x; }
+  static __device__ __forceinline__ uint32_t second(float x) { return __float_as_uint(x); }
   static __device__ __forceinline__ float at(const uint4& v, int j) {
     return __uint_as_float(j == 0 ? v.x : j == 1 ? v.y : j == 2 ? v.z : v.w);
   }
@@ -182,7 +186,7 @@ struct Type<float> {
 template <>
 struct Type<__nv_bfloat16> {
   static constexpr int kPer = 8;
-  static __device__ __forceinline__ float one(__nv_bfloat16 x) { return __bfloat162float(x); }
+  static __device__ __forceinline__ uint32_t second(__nv_bfloat16 x) { return (uint32_t)__bfloat16_as_ushort(x) << 16 | (kNone & 0xffffu); }
   static __device__ __forceinline__ float at(const uint4& v, int j) {
     const uint32_t w = j < 2 ? v.x : j < 4 ? v.y : j < 6 ? v.z : v.w;
     return __uint_as_float(j & 1 ? w & 0xffff0000u : w << 16);
@@ -199,7 +203,7 @@ struct Type<__nv_bfloat16> {
 template <>
 struct Type<__half> {
   static constexpr int kPer = 8;
-  static __device__ __forceinline__ float one(__half x) { return __half2float(x); }
+  static __device__ __forceinline__ uint32_t second(__half x) { return (uint32_t)__half_as_ushort(x) << 16 | (kNone & 0xffffu); }
   static __device__ __forceinline__ float at(const uint4& v, int j) {
     const uint32_t w = j < 2 ? v.x : j < 4 ? v.y : j < 6 ? v.z : v.w;
     const __half2 h = *reinterpret_cast<const __half2*>(&w);
@@ -264,6 +268,16 @@ __device__ __noinline__ int best_keys(u64* keys, int n, int k, uint32_t limit, u
   }
   __syncwarp();
   return min(m, k);
+}
+
+// Keeps the k best of a warp's n candidates; all later ones have to reach the last
+// of them.  Returns their number.
+__device__ __noinline__ int select(u64* keys, int n, int k, u64* out, uint32_t* floor) {
+  n = best_keys(keys, n, k, *floor, out);
+  for (int i = threadIdx.x & 31; i < n; i += 32) keys[i] = out[i];
+  if (n == k) *floor = max(*floor, (uint32_t)(out[k - 1] >> 32));
+  __syncwarp();
+  return n;
 }
 
 // The place in the order of the k-th largest of the warp's 64 values: each is
@@ -434,30 +448,18 @@ __global__ void __launch_bounds__(kThreads, 2) mla_beam_select_kernel(const Beam
   float m = -INFINITY, s = 0.f, s_low = 0.f;   // the lane's maximum and sum
   float a = -INFINITY, c = -INFINITY;          // its largest in even and odd vectors
   uint32_t floor = kLeast, limit = kLeast;     // k values reach the one; from the other on values count
-  int n = 0, known = 0;                        // candidates, those when the limit was found
+  int n = 0, tiles = 0;                        // candidates, tiles of the epoch
 #pragma unroll 1
   for (int stage = 0; at.g < all; stage = stage + 1 < kStages ? stage + 1 : 0) {
     fetch(stage == 0 ? kStages - 1 : stage - 1);
     asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
     const uint4* tile = &sm.tile[warp][stage][0][lane];
-    const auto key = [&](float x, int u, int j) {
-      const uint32_t pos = (uint32_t)(at.t0 + (u * 32 + lane) * kPer + j);
-      return (u64)ordered(x) << 32 | ~pos;
-    };
-    const auto select = [&]() {
-      u64* list = sm.list + (at.g / step * kWarps + warp) * k;
-      n = known = best_keys(buf, n, k, floor, list);
-      for (int i = lane; i < n; i += 32) buf[i] = list[i];
-      if (n == k) floor = max(floor, (uint32_t)(list[k - 1] >> 32));
-      limit = max(limit, floor);
-      __syncwarp();
-    };
-    uint32_t best[kVecs], most[2];
+    uint32_t most[2];
 #pragma unroll
     for (int u = 0; u < kVecs; ++u) {
       const uint4 v = tile[u * 32];
-      best[u] = Type<T>::max2(Type<T>::max2(v.x, v.y), Type<T>::max2(v.z, v.w));
-      most[u & 1] = u < 2 ? best[u] : Type<T>::max2(most[u & 1], best[u]);
+      const uint32_t best = Type<T>::max2(Type<T>::max2(v.x, v.y), Type<T>::max2(v.z, v.w));
+      most[u & 1] = u < 2 ? best : Type<T>::max2(most[u & 1], best);
     }
     const float even = Type<T>::top(most[0]), odd = Type<T>::top(most[1]), top = fmaxf(even, odd);
     a = fmaxf(a, even);
@@ -488,73 +490,88 @@ __global__ void __launch_bounds__(kThreads, 2) mla_beam_select_kernel(const Beam
     const float x = (p0 + p1) + (p2 + p3), t = s + x, back = t - s;
     s_low += (s - (t - back)) + (x - back);
     s = t;
-    if (__any_sync(~0u, top >= unordered(limit))) {
-      // a new limit for the first tile, then whenever it has let k more through
-      if (n - known >= k || n == 0) {
-        floor = max(floor, kth_of(a, c, k, sm.words[warp]));
-        limit = max(limit, floor);
-        known = n;
+    uint16_t* tops = sm.tops[warp];
+    u64* list = sm.list + (at.g / step * kWarps + warp) * k;
+    tops[tiles++ * 32 + lane] = (uint16_t)(ordered(top) >> 16);
+    if (tiles == kEpoch || at.last()) {
+      floor = max(floor, kth_of(a, c, k, sm.words[warp]));
+      limit = max(limit, floor);
+      // lanes and tiles with a value that reaches it, in place
+      int pairs = 0;
+#pragma unroll 2
+      for (int i = 0; i < tiles; ++i) {
+        const bool hit = tops[i * 32 + lane] >= limit >> 16;
+        const uint32_t all = __ballot_sync(~0u, hit);
+        if (hit) tops[pairs + __popc(all & ((1u << lane) - 1))] = (uint16_t)(i * 32 + lane);
+        pairs += __popc(all);
+        __syncwarp();
       }
-      // the lane's vectors that reach it, one after the other
-      uint32_t hits = 0;
-      if (top >= unordered(limit)) {
-#pragma unroll
-        for (int u = 0; u < kVecs; ++u) hits |= (uint32_t)(Type<T>::top(best[u]) >= unordered(limit)) << u;
-      }
+      // their values: the last tile's are at hand, others are read again
+      constexpr int kAtOnce = 8, kMine = kPer / 4;  // a lane's values (4 bytes) of a pair's tile
       bool selected = false;
 #pragma unroll 1
-      while (__any_sync(~0u, hits != 0)) {
-        if (n + 32 * kPer > kCap) {
-          // No room for whatever comes: the best so far are selected exactly.
-          select();
-          selected = true;
-        }
-        const float least = unordered(limit);
-        const int u = __ffs(hits) - 1;
-        uint32_t which = 0;  // of the vector's values
-        if (hits) {
-          hits &= hits - 1;
-          const uint4 v = tile[u * 32];
+      for (int i0 = 0; i0 < pairs; i0 += kAtOnce) {
+        uint32_t y[kAtOnce];
+        const auto place = [&](int i) {  // of the first value, from the last tile's first
+          const int pair = tops[min(i0 + i, pairs - 1)];
+          return ((pair >> 5) + 1 - tiles) * Walk<T>::kTile + ((lane >> 2) * 32 + (pair & 31)) * kPer + (lane & 3) * kMine;
+        };
 #pragma unroll
-          for (int j = 0; j < kPer; ++j) which |= (uint32_t)(Type<T>::at(v, j) >= least) << j;
+        for (int i = 0; i < kAtOnce; ++i) {
+          const int in = place(i);
+          const int64_t e = at.t0 + in;
+          y[i] = Type<T>::kNone;
+          if (i0 + i >= pairs || lane >= 4 * kVecs) continue;
+          if (in >= 0) y[i] = *reinterpret_cast<const uint32_t*>(reinterpret_cast<const T*>(&sm.tile[warp][stage][0][0]) + in);
+          else if (e >= at.lo) y[i] = *reinterpret_cast<const uint32_t*>(at.row + e);
+          else if (e + kMine > at.lo) y[i] = Type<T>::second(at.row[e + kMine - 1]);  // a row that starts inside the word
         }
-        // one a lane at a time: hardly any lane has more
-#pragma unroll 1
-        for (uint32_t all; (all = __ballot_sync(~0u, which != 0)) != 0; n += __popc(all)) {
-          if (which) {
-            const int j = __ffs(which) - 1;
-            which &= which - 1;
-            const float y = Type<T>::one(reinterpret_cast<const T*>(&tile[u * 32])[j]);
-            buf[n + __popc(all & ((1u << lane) - 1))] = key(y, u, j);
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) {
+          if (i0 + i >= pairs) break;
+          if (n + 32 * kMine > kCap) {
+            // No room for whatever comes: the best so far are selected exactly.
+            n = select(buf, n, k, list, &floor);
+            limit = max(limit, floor);
+            selected = true;
+          }
+#pragma unroll
+          for (int j = 0; j < kMine; ++j) {
+            const float x = Type<T>::at(make_uint4(y[i], 0, 0, 0), j);
+            const bool in = x >= unordered(limit);
+            const uint32_t all = __ballot_sync(~0u, in);
+            if (in)
+              buf[n + __popc(all & ((1u << lane) - 1))] = (u64)ordered(x) << 32 | ~(uint32_t)(at.t0 + place(i) + j);
+            n += __popc(all);
           }
         }
       }
+      __syncwarp();
       if (selected) {  // later tiles' values have to be greater than the last of the best
-        select();
+        n = select(buf, n, k, list, &floor);
         if (n == k) limit = max(limit, floor + 1);
       }
+      tiles = 0;
     }
     if (!at.last()) {
       at.t0 += Walk<T>::kTile;
       continue;
     }
     // the part's end
-    if (n > k) floor = max(floor, kth_of(a, c, k, sm.words[warp]));
-    const int l = at.g / step * kWarps + warp;
-    n = best_keys(buf, n, k, floor, sm.list + l * k);
+    n = best_keys(buf, n, k, floor, list);
     const float wm = unordered(__reduce_max_sync(~0u, ordered(m)));
     s = (s + s_low) * ex2((wm > -INFINITY ? m - wm : 0.f) * kLog2e);
 #pragma unroll
     for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(~0u, s, d);
     if (lane == 0) {
-      sm.num[l] = n;
+      sm.num[at.g / step * kWarps + warp] = n;
       sm.stat[at.g] = make_float2(wm, s);
     }
     at.enter(p, sm.live, b, len, at.g + step);
     m = a = c = -INFINITY;
     s = s_low = 0.f;
     floor = limit = kLeast;
-    n = known = 0;
+    n = 0;
   }
   __syncthreads();
   cluster_wait();
@@ -678,7 +695,6 @@ int launch_beam(BeamParams p, int B, cudaStream_t st) {
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e == cudaSuccess)
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem));
-  if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(mla_beam_select_kernel)");
   constexpr int kTile = 32 * kVecs * Type<T>::kPer;
   p.cluster = 1;
