@@ -839,12 +839,10 @@ def beam_select(logits, scores, k: int, finished=None, end_token: int = 0, out_s
 def _table_arg(t: torch.Tensor, name: str, R: int):
     """An int32 page table [R, stride] with contiguous rows: address, row stride
     and entries a row."""
-    shape, stride = t.shape, t.stride()
-    if t.dtype is not _I32 or len(shape) != 2 or shape[0] != R or (shape[1] > 1 and stride[1] != 1) or \
-            (R > 1 and stride[0] != shape[1]):
+    if t.dtype is not _I32 or t.dim() != 2 or t.size(0) != R or not t.is_contiguous():
         raise ValueError(f"{name}: expected contiguous int32 [{R}, stride], got {t.dtype} "
-                         f"{tuple(shape)} with strides {stride}")
-    return t.data_ptr(), shape[1]
+                         f"{tuple(t.shape)} with strides {t.stride()}")
+    return t.data_ptr(), t.size(1)
 
 
 def pages_fork(table, lens, refs, free_count, parents=None, keep=None, grow=None, table_out=None,

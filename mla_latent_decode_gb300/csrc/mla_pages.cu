@@ -100,17 +100,15 @@ __device__ __forceinline__ int taken(const ForkParams& p, int i, int* parent) {
   return min(want, held);
 }
 
-// Entries of one page of a row: page * 64 + 0..63, cut at the row's end.
-__device__ __forceinline__ void write_page(const ForkParams& p, int row, int64_t at, int page) {
-  int32_t* dst = p.out + row * p.out_stride + at * kPage;
-  const int base = page * kPage;
-  if (p.vec && (at + 1) * kPage <= p.out_stride) {
-#pragma unroll
-    for (int j = 0; j < kPage; j += 4)
-      *reinterpret_cast<int4*>(dst + j) = make_int4(base + j, base + j + 1, base + j + 2, base + j + 3);
+// Entries 4 q .. 4 q + 3 of a row's page `at`, cut at the row's end.
+__device__ __forceinline__ void write_quad(const ForkParams& p, int row, int64_t at, int page, int q) {
+  const int64_t e = at * kPage + 4 * q;
+  int32_t* dst = p.out + row * p.out_stride + e;
+  const int base = page * kPage + 4 * q;
+  if (p.vec && e + 4 <= p.out_stride) {
+    *reinterpret_cast<int4*>(dst) = make_int4(base, base + 1, base + 2, base + 3);
   } else {
-    const int n = (int)min((int64_t)kPage, p.out_stride - at * kPage);
-    for (int j = 0; j < n; ++j) dst[j] = base + j;
+    for (int j = 0; j < 4 && e + j < p.out_stride; ++j) dst[j] = base + j;
   }
 }
 
@@ -166,6 +164,8 @@ __global__ void __launch_bounds__(kThreads) __cluster_dims__(kCluster, 1, 1)
   int* from = kept + p.R;                                    // [R] parent
   int* first = from + p.R;                                   // [R + 1] rank of the row's first new page
   int* tail = first + p.R + 1;                               // [R] partly taken page; its sign: copied
+  int* held = tail + p.R;                                    // [R] pages of the old row
+  uint32_t* ops = reinterpret_cast<uint32_t*>(held + p.R);   // [R + 1] counts to change before the row's
   __shared__ int scratch[kWarps], box[2][2 * kCluster], bad, freed;
   const uint32_t rank = cluster_ctarank();
   const int tid = threadIdx.x, R = p.R;
@@ -178,13 +178,14 @@ __global__ void __launch_bounds__(kThreads) __cluster_dims__(kCluster, 1, 1)
   for (int i = tid; i < R; i += kThreads) {
     int parent;
     const int k = taken(p, i, &parent);
-    const int64_t g = p.grow ? p.grow[i] : 0, held = p.lens[i];
+    const int64_t g = p.grow ? p.grow[i] : 0, old = p.lens[i];
     if (k < 0) {
       atomicOr(&bad, parent < -1 || parent >= R ? MLA_STATUS_BAD_PARENT : MLA_STATUS_BAD_LENGTH);
-    } else if (g < 0 || k + g > p.out_stride || held < 0 || held > p.stride) {
+    } else if (g < 0 || k + g > p.out_stride || old < 0 || old > p.stride) {
       atomicOr(&bad, MLA_STATUS_BAD_LENGTH);
     }
     kept[i] = max(k, 0);
+    held[i] = (int)pages_of(max(old, (int64_t)0));
     from[i] = parent;
     if (k >= 0 && parent >= 0) atomicMax(&best[parent], claim(k, i));
   }
@@ -241,6 +242,14 @@ __global__ void __launch_bounds__(kThreads) __cluster_dims__(kCluster, 1, 1)
     return;
   }
 
+  const auto row_of = [&](int r) {  // the last row whose first rank is not above r
+    int lo = 0, hi = R;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) / 2;
+      if (first[mid] <= r) lo = mid; else hi = mid;
+    }
+    return lo;
+  };
   // The lowest free pages, in rounds of 8 x 8192 counts.
   int found = 0;
   for (int round = 0; found < total; ++round) {
@@ -271,19 +280,16 @@ __global__ void __launch_bounds__(kThreads) __cluster_dims__(kCluster, 1, 1)
     }
     r += found;
     found += all;
+    // Of a new page only the first entry is written here: the lowest pages are mostly
+    // one CTA's, and all of them write the rest.
     for (; zero && r < total; zero &= zero - 1, ++r) {
-      const int page = (int)(p0 + __ffs(zero) - 1);
-      int lo = 0, hi = R;  // the last row whose first rank is not above r
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) / 2;
-        if (first[mid] <= r) lo = mid; else hi = mid;
-      }
-      const int nth = r - first[lo];
+      const int page = (int)(p0 + __ffs(zero) - 1), row = row_of(r), nth = r - first[row];
       p.refs[page] = 1;
-      write_page(p, lo, kept[lo] / kPage + (tail[lo] > 0) + nth, page);
-      if (nth == 0 && tail[lo] < -1) p.copies[R + lo] = page;
+      p.out[row * p.out_stride + (kept[row] / kPage + (tail[row] > 0) + (int64_t)nth) * kPage] = page * kPage;
+      if (nth == 0 && tail[row] < -1) p.copies[R + row] = page;
     }
   }
+  cluster_arrive();
   // A count of free pages above what the pool has: the rows that got none are
   // left with what their entries held.
   if (found < total && rank == 0 && tid == 0 && p.status) atomicOr(p.status, MLA_STATUS_NO_PAGES);
@@ -291,46 +297,83 @@ __global__ void __launch_bounds__(kThreads) __cluster_dims__(kCluster, 1, 1)
   // Counts.  Of a parent's pages its heir goes on holding those it takes; the
   // rest lose the parent, and every other child adds its full pages.  A page
   // that gains a holder has one that stays (the heir takes at least as many
-  // pages), so a count that reaches 0 is final.
-  int lost = 0;
-  const int lane = tid & 31;
-  const auto page_at = [&](int row, int64_t q) {
-    const int e = p.table[row * p.stride + q * kPage];
-    const int page = e / kPage;
-    return e >= 0 && page < p.num_pages ? page : -1;
-  };
-  bool bad_slot = false;
-  for (int i = rank * kWarps + (tid >> 5); i < R; i += kCluster * kWarps) {
+  // pages), so a count that reaches 0 is final.  The changes of all rows are dealt
+  // out evenly, kOps of a thread under way at once: rows differ in length, and a
+  // change takes two trips to L2 (a warp a row took longest with one long row).
+  const auto stays = [&](int i) {  // pages of row i that its heir goes on holding
     const unsigned long long b = best[i];
     const int heir = b ? 0x7fffffff - (int)(uint32_t)b : -1;
-    const int64_t held = pages_of(p.lens[i]);
-    for (int64_t q = (heir < 0 ? 0 : kept[heir] / kPage + (tail[heir] > 0)) + lane; q < held; q += 32) {
-      const int page = page_at(i, q);
-      bad_slot |= page < 0;
-      if (page > 0) lost += atomicSub(&p.refs[page], 1) == 1;
+    return heir < 0 ? 0 : min(held[i], kept[heir] / kPage + (tail[heir] > 0));
+  };
+  uint32_t changes = 0;
+  for (int i0 = 0; i0 < R; i0 += kThreads) {
+    const int i = i0 + tid;
+    uint32_t mine = 0;
+    if (i < R) {
+      const int parent = from[i];
+      mine = (uint32_t)(held[i] - stays(i));
+      if (parent >= 0 && best[parent] != claim(kept[i], i)) mine += (uint32_t)(kept[i] / kPage);
     }
-    const int parent = from[i];
-    if (parent >= 0 && best[parent] != claim(kept[i], i))
-      for (int64_t q = lane; q < kept[i] / kPage; q += 32) {
-        const int page = page_at(parent, q);
-        bad_slot |= page < 0;
-        if (page > 0) atomicAdd(&p.refs[page], 1);
+    int sum;
+    const int before = block_scan((int)mine, scratch, &sum);
+    if (i < R) ops[i] = changes + (uint32_t)before;
+    changes += (uint32_t)sum;
+  }
+  if (tid == 0) ops[R] = changes;
+  __syncthreads();
+  constexpr int kOps = 8;
+  int lost = 0;
+  bool bad_slot = false;
+  for (int64_t t0 = rank * kThreads + tid; t0 < changes; t0 += (int64_t)kOps * kCluster * kThreads) {
+    int page[kOps];
+    bool less[kOps];
+#pragma unroll
+    for (int u = 0; u < kOps; ++u) {
+      const int64_t t = t0 + (int64_t)u * kCluster * kThreads;
+      page[u] = 0;
+      if (t >= changes) continue;
+      int lo = 0, hi = R;  // the last row whose changes start at t or before
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (ops[mid] <= (uint32_t)t) lo = mid; else hi = mid;
       }
-    if (lane == 0) {
-      p.lens_out[i] = kept[i] + (p.grow ? p.grow[i] : 0);
-      const int t = tail[i];
-      p.copies[i] = t < -1 ? -1 - t : -1;
-      if (t >= -1) p.copies[R + i] = -1;
-      p.copies[2 * R + i] = t < -1 ? kept[i] % kPage : 0;
-      if (t > 0) write_page(p, i, kept[i] / kPage, t);
+      const int skip = stays(lo), nth = (int)((uint32_t)t - ops[lo]);
+      less[u] = nth < held[lo] - skip;
+      const int e = less[u] ? p.table[lo * p.stride + (int64_t)(skip + nth) * kPage]
+                            : p.table[from[lo] * p.stride + (int64_t)(nth - (held[lo] - skip)) * kPage];
+      page[u] = e / kPage;
+      if (e < 0 || page[u] >= p.num_pages) bad_slot = true, page[u] = 0;
     }
+#pragma unroll
+    for (int u = 0; u < kOps; ++u) {
+      if (page[u] <= 0) continue;
+      if (less[u]) lost += atomicSub(&p.refs[page[u]], 1) == 1;
+      else atomicAdd(&p.refs[page[u]], 1);
+    }
+  }
+  for (int i = rank * kThreads + tid; i < R; i += kCluster * kThreads) {
+    p.lens_out[i] = kept[i] + (p.grow ? p.grow[i] : 0);
+    const int t = tail[i];
+    p.copies[i] = t < -1 ? -1 - t : -1;
+    if (t >= -1) p.copies[R + i] = -1;
+    p.copies[2 * R + i] = t < -1 ? kept[i] % kPage : 0;
+  }
+  // Entries: kept partly taken pages, then the new ones', 16 threads a page.
+  for (int64_t t = rank * kThreads + tid; t < (int64_t)R * 16; t += kCluster * kThreads) {
+    const int i = (int)(t / 16);
+    if (tail[i] > 0) write_quad(p, i, kept[i] / kPage, tail[i], (int)(t % 16));
+  }
+  cluster_wait();  // the new pages' first entries; the boxes have been read, too
+  for (int64_t t = rank * kThreads + tid; t < min((int64_t)found, total) * 16; t += kCluster * kThreads) {
+    const int r = (int)(t / 16), row = row_of(r);
+    const int64_t at = kept[row] / kPage + (tail[row] > 0) + r - first[row];
+    const int page = p.out[row * p.out_stride + at * kPage] / kPage;
+    write_quad(p, row, at, page, (int)(t % 16));
   }
   if (bad_slot && p.status) atomicOr(p.status, MLA_STATUS_BAD_SLOT);
   if (lost) atomicAdd(&freed, lost);
   __syncthreads();
   int* b = box[0];
-  // The boxes of the last round are read before anybody writes here again.
-  cluster_sync();
   publish(b, rank, freed, 0);
   cluster_sync();
   if (rank == 0 && tid == 0) {
@@ -348,62 +391,71 @@ struct CompactParams {
   int32_t* dst;
   int max_moves;
   int32_t* count;
+  int refs_vec;  // refs starts on a 16-byte boundary
 };
 
 // The k-th lowest hole among pages 1 .. n and the k-th highest live page above
 // n, n the number of live pages: after all moves exactly the pages 1 .. n are
-// live.  Three passes over the counts (from L2 after the first), each CTA over
-// its own run of pages.
+// live.  Every thread has a run of pages of its own and looks at it three times
+// (from L2 after the first); between them two sums over the block and the cluster.
 __global__ void __launch_bounds__(kThreads) __cluster_dims__(kCluster, 1, 1)
     mla_pages_compact_kernel(const CompactParams p) {
   __shared__ int scratch[kWarps], box[2][2 * kCluster];
   const uint32_t rank = cluster_ctarank();
   const int tid = threadIdx.x;
   griddep_launch_dependents();
-  const int64_t run = ((p.num_pages + kCluster - 1) / kCluster + 31) / 32 * 32;
-  const int64_t a = min(run * rank, p.num_pages), z = min(a + run, p.num_pages);
+  cluster_arrive();  // the CTAs have started when they write to each other
+  const int64_t run = ((p.num_pages + kCluster * kThreads - 1) / (kCluster * kThreads) + 3) / 4 * 4;
+  const int64_t a = min(run * (rank * kThreads + tid), p.num_pages), z = min(a + run, p.num_pages);
+  // f(page, live) for the thread's pages but the dummy one
+  const auto walk = [&](auto f) {
+    for (int64_t i = a; i < z; i += 4) {
+      int r[4];
+      if (p.refs_vec && i + 4 <= z) {
+        *reinterpret_cast<int4*>(r) = *reinterpret_cast<const int4*>(p.refs + i);
+      } else {
+        for (int u = 0; u < 4; ++u) r[u] = i + u < z ? p.refs[i + u] : 0;
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (i + u > 0 && i + u < z) f(i + u, r[u] > 0);
+    }
+  };
   int live = 0;
-  for (int64_t i = a + tid; i < z; i += kThreads) live += i > 0 && p.refs[i] > 0;
+  walk([&](int64_t, bool is) { live += is; });
   int sum;
   block_scan(live, scratch, &sum);
+  cluster_wait();
   publish(box[0], rank, sum, 0);
   cluster_sync();
   int64_t n = 0;
   for (int c = 0; c < kCluster; ++c) n += box[0][2 * c];
   int holes = 0, high = 0;
-  for (int64_t i = a + tid; i < z; i += kThreads) {
-    const int r = p.refs[i];
-    holes += i > 0 && i <= n && r <= 0;
-    high += i > n && r > 0;
-  }
+  walk([&](int64_t i, bool is) {
+    holes += i <= n && !is;
+    high += i > n && is;
+  });
   int my_holes, my_high;
-  block_scan(holes, scratch, &my_holes);
-  block_scan(high, scratch, &my_high);
+  int hole_at = block_scan(holes, scratch, &my_holes), high_at = block_scan(high, scratch, &my_high);
   publish(box[1], rank, my_holes, my_high);
   cluster_sync();
-  int hole_at = 0, high_at = 0, all = 0;
+  int all = 0;
   for (int c = 0; c < kCluster; ++c) {
     if (c < (int)rank) hole_at += box[1][2 * c], high_at += box[1][2 * c + 1];
     all += box[1][2 * c + 1];
   }
   const int moves = min(all, p.max_moves);
-  // Runs that neither of the two lists' first `moves` entries reach are skipped.
-  for (int64_t i0 = a; i0 < z; i0 += kThreads) {
-    if (!(i0 <= n ? hole_at < moves : all - 1 - (high_at + my_high) < moves)) {
-      if (i0 + kThreads <= n || i0 > n) continue;
-    }
-    const int64_t i = i0 + tid;
-    const int r = i < z ? p.refs[i] : 0;
-    const bool is_hole = i < z && i > 0 && i <= n && r <= 0, is_high = i < z && i > n && r > 0;
-    int s0, s1;
-    const int h = hole_at + block_scan(is_hole, scratch, &s0);
-    const int g = all - 1 - (high_at + block_scan(is_high, scratch, &s1));
-    if (is_hole && h < moves) p.dst[h] = (int)i;
-    if (is_high && g < moves) p.src[g] = (int)i;
-    hole_at += s0;
-    high_at += s1;
-    my_high -= s1;
-  }
+  if ((holes && hole_at < moves) || (high && all - high_at - high < moves))
+    walk([&](int64_t i, bool is) {
+      if (i <= n && !is) {
+        if (hole_at < moves) p.dst[hole_at] = (int)i;
+        ++hole_at;
+      }
+      if (i > n && is) {
+        const int g = all - 1 - high_at++;
+        if (g < moves) p.src[g] = (int)i;
+      }
+    });
   cluster_sync();
   for (int k = rank * kThreads + tid; k < p.max_moves; k += kCluster * kThreads) {
     if (k < moves) {
@@ -567,8 +619,8 @@ extern "C" int mla_pages_fork(const int32_t* table, int64_t stride, const int32_
   if (R > kMaxRows)
     return fail(MLA_ERR_UNSUPPORTED, "mla_pages_fork: R %d > %d rows", R, kMaxRows);
   if (num_pages > ((int64_t)1 << 31) / kPage || stride > 0x7fffffff || out_stride > 0x7fffffff ||
-      R * pages_of(std::max(stride, out_stride)) > 0x7fffffff)
-    return fail(MLA_ERR_INVALID_ARG, "mla_pages_fork: more than 2^31 slots or table pages");
+      R * pages_of(std::max(stride, out_stride)) > 0x3fffffff)
+    return fail(MLA_ERR_INVALID_ARG, "mla_pages_fork: more than 2^31 slots or 2^30 table pages");
   if (!table || !lens || !refs || !free_count || !table_out || !lens_out || !copies)
     return fail(MLA_ERR_INVALID_ARG, "mla_pages_fork: a required pointer is NULL");
   if (table_out < table + (R - 1) * stride + stride && table < table_out + (R - 1) * out_stride + out_stride)
@@ -589,12 +641,12 @@ extern "C" int mla_pages_fork(const int32_t* table, int64_t stride, const int32_
   // up to two CTAs per SM for the copies, in whole clusters
   const int64_t tasks = (int64_t)R * p.chunks;
   const int64_t clusters = 1 + std::min<int64_t>((tasks + kCluster - 1) / kCluster, 2 * sms / kCluster);
-  const int smem = R * 8 + (4 * R + 1) * 4;
-  static_assert(kMaxRows * 24 + 4 <= 200 * 1024, "shared memory budget");
+  const int smem = R * 8 + (6 * R + 2) * 4;
+  static_assert(kMaxRows * 32 + 8 <= 200 * 1024, "shared memory budget");
   cudaError_t e = cudaSuccess;
   if (smem > 47 * 1024)
     e = cudaFuncSetAttribute(mla_pages_fork_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             kMaxRows * 24 + 4);
+                             kMaxRows * 32 + 8);
   if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(mla_pages_fork_kernel)");
   mla_pages_fork_kernel<<<(unsigned)(clusters * kCluster), kThreads, smem, (cudaStream_t)stream>>>(p);
   e = cudaGetLastError();
@@ -622,7 +674,7 @@ extern "C" int mla_pages_compact(const int32_t* table, int64_t stride, const int
   for (const void* q : all)
     if (q && !aligned(q, 4)) return fail(MLA_ERR_MISALIGNED, "mla_pages_compact: arrays need 4-B alignment");
   const cudaStream_t st = (cudaStream_t)stream;
-  const CompactParams c{refs, num_pages, src, dst, max_moves, count};
+  const CompactParams c{refs, num_pages, src, dst, max_moves, count, aligned(refs, 16)};
   mla_pages_compact_kernel<<<kCluster, kThreads, 0, st>>>(c);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_fail(e, "launch mla_pages_compact_kernel");
