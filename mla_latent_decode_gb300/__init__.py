@@ -763,9 +763,10 @@ def prefill(q_nope, q_rope, k_nope, k_rope, v, cu_q, cu_kv, work, sm_scale: floa
     N = cu_q.numel() - 1
     if N < 0:
         raise ValueError("cu_q: expected N + 1 values")
-    if work.dtype is not _I32 or tuple(work.shape[1:]) not in ((8,), (2, 8)) or not work.is_contiguous():
-        raise ValueError(f"work: expected contiguous int32 [n, 8] or [n, 2, 8] on the device, got "
-                         f"{work.dtype} {tuple(work.shape)}")
+    if work.dtype is not _I32 or tuple(work.shape[1:]) not in ((8,), (2, 8)) or not work.is_contiguous() \
+            or work.device != q_nope.device:
+        raise ValueError(f"work: expected contiguous int32 [n, 8] or [n, 2, 8] on {q_nope.device}, got "
+                         f"{work.dtype} {tuple(work.shape)} on {work.device}")
     qn = _heads_arg(q_nope, "q_nope", Tq, H, 128)
     qr = _heads_arg(q_rope, "q_rope", Tq, H, ROPE_DIM)
     kn = _heads_arg(k_nope, "k_nope", Tk, H, 128)
