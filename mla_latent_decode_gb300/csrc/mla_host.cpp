@@ -187,9 +187,11 @@ using namespace mla;
 namespace mla {
 
 // Plan of mla_prefill with blocks of 128 rows (one CTA, two of them an SM) or 512
-// (a pair of CTAs).  Costs in key tiles of a single CTA with another beside it
-// (about 2.05 us): a tile of a pair, what a block takes besides its tiles, and the
-// merging launch with its rows.
+// (a pair of CTAs).  Costs in key tiles of a single CTA with another beside it (about
+// 2 us), from times of both forms: 8191 tokens x 96 heads 1428 us on single CTAs and
+// 1215 on pairs, 24 prompts of 100 to 6000 tokens x 16 heads 508 and 480, 64 documents
+// of 33 to 700 tokens x 96 heads 349 and 580.  A tile of a pair, what a block takes
+// besides its tiles, and the merging launch with its rows.
 struct PrefillPlan {
   int ctas = 1;
   double end = 0;
@@ -207,7 +209,7 @@ static PrefillPlan plan_prefill_blocks(const int32_t* q_lens, const int32_t* kv_
                                        const int32_t* prefix, int N, int H, int causal,
                                        int ctas, int num_sms) {
   constexpr int kKeys = 128;
-  constexpr double kFixed = 1.7, kPairFixed = 1.4, kPairTile = 0.82, kMerge = 3, kMergeSlot = 0.001;
+  constexpr double kFixed = 1.7, kPairFixed = 2.2, kPairTile = 0.78, kMerge = 3, kMergeSlot = 0.008;
   const int block = ctas == 1 ? 128 : 512, slots_of = block / 128;
   PrefillPlan plan;
   plan.ctas = ctas;
@@ -236,16 +238,17 @@ static PrefillPlan plan_prefill_blocks(const int32_t* q_lens, const int32_t* kv_
   // Many blocks: they even out.
   plan.end = ((double)all * tile + (double)blocks * fixed) * H / slots + longest * tile / 2;
   if (blocks == 0 || blocks * H >= 8 * (int64_t)slots) return plan;
-  // Few: a limit on a part's key tiles, the one whose list schedule in launch
-  // order ends first.
+  // Few: a limit on a part's key tiles, the one that ends first: halfway between
+  // the list schedule in launch order and full use of all slots, as blocks run faster
+  // while others' slots are idle.
   double best = -1;
   int64_t best_limit = plan.limit;
-  for (int cut = 1; cut <= MLA_PREFILL_MAX_PARTS; ++cut) {
+  for (int cut : {1, 2, 3, 4, 5, 6, 8, 10, 12, 16, 20, 24, 28, 32}) {
     plan.limit = std::max<int64_t>((longest + cut - 1) / cut, 1);
     if (cut > 1 && plan.limit < 4) break;
     std::priority_queue<double, std::vector<double>, std::greater<double>> ends;
     for (int i = 0; i < slots; ++i) ends.push(0);
-    double end = 0;
+    double end = 0, sum = 0;
     int64_t merged = 0;
     for (int n : plan.order)
       for (int h = 0; h < H; ++h)
@@ -253,14 +256,15 @@ static PrefillPlan plan_prefill_blocks(const int32_t* q_lens, const int32_t* kv_
           const int parts = plan.parts_of(*t);
           merged += parts > 1 ? parts * slots_of : 0;
           for (int s = 0; s < parts; ++s) {
-            const double at =
-                ends.top() + fixed + tile * (double)(*t * (s + 1) / parts - *t * s / parts);
+            const double cost = fixed + tile * (double)(*t * (s + 1) / parts - *t * s / parts);
+            const double at = ends.top() + cost;
             ends.pop();
             ends.push(at);
             end = std::max(end, at);
+            sum += cost;
           }
         }
-    end += merged ? kMerge + kMergeSlot * (double)merged : 0;
+    end = (end + sum / slots) / 2 + (merged ? kMerge + kMergeSlot * (double)merged : 0);
     if (best < 0 || end < best) best = end, best_limit = plan.limit;
   }
   plan.limit = best_limit;

@@ -1024,8 +1024,10 @@ __global__ void __launch_bounds__(Form<kCtas>::kThreads, kCtas == 1 ? 2 : 1)
   }
 }
 
-// Merge of a block's parts, a warp per row: weights e^(LSE_s - max), parts in
+// Merge of a block's parts, a warp per row and 16 rows a CTA (a row takes two trips to
+// L2 or DRAM, so a warp has few of them): weights e^(LSE_s - max), parts in
 // order.  Parts without keys (LSE = -inf) weigh nothing; a NaN makes the row NaN.
+constexpr int kMergeRows = 16;
 template <int kCtas>
 __global__ void __launch_bounds__(256) mla_prefill_merge_kernel(const PrefillParams p) {
   constexpr int kBlock = Form<kCtas>::kBlock, kSlots = kBlock / kSlot;
@@ -1038,7 +1040,8 @@ __global__ void __launch_bounds__(256) mla_prefill_merge_kernel(const PrefillPar
   const int64_t k0 = p.cu_kv[seq], lk = p.cu_kv[seq + 1] - k0;
   if (q0 < 0 || lq < 0 || q0 + lq > p.Tq || k0 < 0 || lk < 0 || k0 + lk > p.Tk) return;
   const int rows = (int)min((int64_t)kBlock, lq - row0), lane = threadIdx.x & 31;
-  for (int r = threadIdx.x / 32; r < rows; r += 8) {
+  const int r0 = blockIdx.y * kMergeRows;
+  for (int r = r0 + threadIdx.x / 32; r < min(rows, r0 + kMergeRows); r += 8) {
     const int64_t at = ((int64_t)(slot + r / kSlot) * p.H + h) * kSlot + r % kSlot;
     const int64_t step = (int64_t)kSlots * p.H * kSlot;
     const float mine = lane < parts ? p.LSE_part[at + lane * step] : -INFINITY;
@@ -1095,7 +1098,7 @@ int launch_prefill(const PrefillMaps& m, const PrefillParams& p, cudaStream_t st
   e = cudaLaunchKernelEx(&cfg, kernel, m, p);
   if (e != cudaSuccess) return cuda_fail(e, "launch mla_prefill_kernel");
   if (p.num_parts > 0) {
-    mla_prefill_merge_kernel<kCtas><<<units, 256, 0, st>>>(p);
+    mla_prefill_merge_kernel<kCtas><<<dim3(units, Form<kCtas>::kBlock / kMergeRows), 256, 0, st>>>(p);
     e = cudaGetLastError();
     if (e != cudaSuccess) return cuda_fail(e, "launch mla_prefill_merge_kernel");
   }
