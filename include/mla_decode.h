@@ -728,7 +728,8 @@ int mla_plan_prefill(const int32_t* q_lens, const int32_t* kv_lens,
  * logit, every logit -inf) has none; a NaN or +inf among them sets
  * MLA_STATUS_BAD_SCORE.  Where fewer than k continuations have a score above
  * -inf the rest of the outputs are the lowest (w, t) not among them, at -inf.
- *   logits     bf16, fp16 or fp32 [B, W, V], rows contiguous, any strides
+ *   logits     bf16, fp16 or fp32 [B, W, V], rows contiguous, strides of V or more
+ *              values (rows may start anywhere)
  *   scores     fp32 [B, W]: the beams' summed log probabilities; -inf rules a
  *              beam out (its logits are not read)
  *   finished   bytes [B, W], non-zero: finished; or NULL

@@ -309,7 +309,7 @@ struct Walk {
   int64_t t0, lo, hi;  // the tile's first position, the part
   int g;               // the part; none left: p.W * p.parts
   static constexpr int kTile = 32 * kVecs * Type<T>::kPer;
-  __device__ __forceinline__ void enter(const BeamParams& p, const float* score, int64_t b, int len, int from) {
+  __device__ __forceinline__ void enter(const BeamParams& p, const float* score, int64_t b, int64_t len, int from) {
     const int all = p.W * p.parts, step = p.cluster * kWarps;
 #pragma unroll 1
     for (g = from; g < all; g += step) {
@@ -317,7 +317,7 @@ struct Walk {
       row = static_cast<const T*>(p.logits) + b * p.batch_stride + w * p.beam_stride;
       // cut where 16-byte vectors start: only a row's ends have partial ones
       const int shift = (int)(reinterpret_cast<uintptr_t>(row) / sizeof(T) % Type<T>::kPer);
-      lo = min((int64_t)p.V, (int64_t)len * (g - w * p.parts));
+      lo = min((int64_t)p.V, len * (g - w * p.parts));
       hi = min((int64_t)p.V, lo + len);
       if (lo > 0 && lo < p.V) lo -= shift;
       if (hi < p.V) hi -= shift;
@@ -410,7 +410,7 @@ __global__ void __launch_bounds__(kThreads, 2) mla_beam_select_kernel(const Beam
     sm.live[tid] = p.finished && p.finished[b * W + tid] ? -INFINITY : c;
   }
   cluster_arrive();  // the CTAs have started when they write to each other
-  const int len = (int)((((uint32_t)V + parts - 1) / (uint32_t)parts + 63) / 64 * 64);
+  const int64_t len = ((int64_t)(((uint32_t)V + parts - 1) / (uint32_t)parts) + 63) / 64 * 64;
   const int lane = tid & 31;
   for (int l = tid; l < lists; l += kThreads) {
     sm.num[l] = 0;
@@ -679,7 +679,6 @@ __global__ void __launch_bounds__(kThreads, 2) mla_beam_select_kernel(const Beam
       moved = tid + below != q;
       q = tid + below;
     }
-    // (q < W + k: at most one of either is above V)
     put(have + tid, -INFINITY, (int)(q / V), (int)(q % V));
   }
 }
@@ -691,11 +690,10 @@ template <typename T>
 int launch_beam(BeamParams p, int B, cudaStream_t st) {
   auto kernel = mla_beam_select_kernel<T>;
   int dev = 0, sms = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem));
-  if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(mla_beam_select_kernel)");
+  int rc = device_sms(&dev, &sms);
+  static std::atomic<uint64_t> set_on{0};
+  if (rc == MLA_OK) rc = allow_shared(kernel, (int)sizeof(Smem), dev, set_on, "cudaFuncSetAttribute(mla_beam_select_kernel)");
+  if (rc != MLA_OK) return rc;
   constexpr int kTile = 32 * kVecs * Type<T>::kPer;
   p.cluster = 1;
   while (p.cluster < kMaxCluster && (int64_t)B * p.cluster * 2 <= 2 * sms &&
@@ -704,7 +702,7 @@ int launch_beam(BeamParams p, int B, cudaStream_t st) {
   double least = 0;
   for (int parts = 1; p.W * parts <= std::max(2 * p.cluster * kWarps, p.W) && p.W * parts <= kMaxParts; ++parts) {
     const int rounds = (p.W * parts + p.cluster * kWarps - 1) / (p.cluster * kWarps);
-    const double cost = rounds * ((double)((p.V / parts + kTile) / kTile) + 3);
+    const double cost = rounds * (double)(p.V / parts / kTile + 4);
     if (parts == 1 || cost < least) least = cost, p.parts = parts;
   }
   cudaLaunchConfig_t cfg = {};
@@ -718,7 +716,7 @@ int launch_beam(BeamParams p, int B, cudaStream_t st) {
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, kernel, p);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, p);
   if (e != cudaSuccess) return cuda_fail(e, "launch mla_beam_select_kernel");
   return MLA_OK;
 }

@@ -2,6 +2,7 @@
 // (error reporting and argument checks used by every entry point).
 #pragma once
 
+#include <atomic>
 #include <cstdarg>
 #include <cstdint>
 #include <cstdio>
@@ -25,6 +26,30 @@ inline bool aligned(const void* p, uintptr_t a) {
 
 inline int cuda_fail(cudaError_t e, const char* what) {
   return fail(MLA_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
+}
+
+// The current device and its SMs, asked of each device once.
+inline int device_sms(int* dev, int* sms) {
+  static std::atomic<int> sms_of[64];
+  cudaError_t e = cudaGetDevice(dev);
+  *sms = e == cudaSuccess && *dev < 64 ? sms_of[*dev].load() : 0;
+  if (e == cudaSuccess && *sms == 0) {
+    e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, *dev);
+    if (e == cudaSuccess && *dev < 64) sms_of[*dev].store(*sms);
+  }
+  return e == cudaSuccess ? MLA_OK : cuda_fail(e, "device query");
+}
+
+// Allow a kernel its dynamic shared memory on a device; the attribute lasts as
+// long as the device's context, so it is set once (set_on: devices where it is).
+template <class Kernel>
+int allow_shared(Kernel kernel, int bytes, int dev, std::atomic<uint64_t>& set_on, const char* name) {
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (set_on.load() & bit) return MLA_OK;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e != cudaSuccess) return cuda_fail(e, name);
+  set_on.fetch_or(bit);
+  return MLA_OK;
 }
 
 // Arguments shared by the two partial-decode entry points.

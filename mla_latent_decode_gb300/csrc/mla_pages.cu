@@ -11,6 +11,7 @@
 // where a page moves) is a rank in a fixed order, so it does not depend on
 // which CTA was first.
 #include <algorithm>
+#include <atomic>
 
 #include "mla_internal.h"
 #include "ptx_sm103.cuh"
@@ -394,12 +395,80 @@ struct CompactParams {
   int refs_vec;  // refs starts on a 16-byte boundary
 };
 
+struct RenameParams {
+  const int32_t* table;
+  int64_t stride;
+  const int32_t* lens;
+  int32_t* out;
+  int64_t out_stride;
+  int R, chunks, vec;
+  const int32_t* src;
+  const int32_t* dst;
+  const int32_t* count;
+  int* status;
+};
+
+// The table's live entries with the moved pages' new numbers, a chunk of a row
+// at a time.  The moved pages are the highest live ones, so src is sorted
+// (descending) and an entry below its last is not moved; others find their place
+// by bisection.
+__device__ void rename_rows(const RenameParams& p, int moves, int64_t first, int64_t step) {
+  const int lowest = moves ? p.src[moves - 1] : 0x7fffffff;
+  const auto renamed = [&](int e) {
+    const int page = e / kPage;
+    if (page < lowest) return e;
+    int lo = 0, hi = moves;  // the first entry not above the page
+    while (lo < hi) {
+      const int mid = (lo + hi) / 2;
+      if (p.src[mid] > page) lo = mid + 1; else hi = mid;
+    }
+    return lo < moves && p.src[lo] == page ? p.dst[lo] * kPage + e % kPage : e;
+  };
+  const bool in_place = p.table == p.out;
+  const int64_t tasks = (int64_t)p.R * p.chunks;
+  for (int64_t t = first; t < tasks; t += step) {
+    const int i = (int)(t / p.chunks);
+    const int64_t e0 = (t % p.chunks) * kChunk;
+    const int64_t len = p.lens[i], room = min(p.stride, p.out_stride);
+    if (len < 0 || len > room) {
+      if (e0 == 0 && threadIdx.x == 0 && p.status) atomicOr(p.status, MLA_STATUS_BAD_LENGTH);
+      continue;
+    }
+    const int64_t e1 = min(min(e0 + kChunk, pages_of(len) * kPage), room);
+    const int32_t* src = p.table + i * p.stride;
+    int32_t* dst = p.out + i * p.out_stride;
+    if (p.vec) {
+      int4 v[kChunk / (4 * kThreads)];
+#pragma unroll
+      for (int u = 0; u < kChunk / (4 * kThreads); ++u) {
+        const int64_t e = e0 + 4 * (threadIdx.x + u * kThreads);
+        if (e < e1) v[u] = *reinterpret_cast<const int4*>(src + e);
+      }
+#pragma unroll
+      for (int u = 0; u < kChunk / (4 * kThreads); ++u) {
+        const int64_t e = e0 + 4 * (threadIdx.x + u * kThreads);
+        if (e >= e1) continue;
+        const int x = renamed(v[u].x);  // four entries of one page
+        if (in_place && x == v[u].x) continue;
+        *reinterpret_cast<int4*>(dst + e) = make_int4(x, v[u].y + (x - v[u].x), v[u].z + (x - v[u].x),
+                                                      v[u].w + (x - v[u].x));
+      }
+    } else {
+      for (int64_t e = e0 + threadIdx.x; e < e1; e += kThreads) {
+        const int x = renamed(src[e]);
+        if (!in_place || x != src[e]) dst[e] = x;
+      }
+    }
+  }
+}
+
 // The k-th lowest hole among pages 1 .. n and the k-th highest live page above
 // n, n the number of live pages: after all moves exactly the pages 1 .. n are
 // live.  Every thread has a run of pages of its own and looks at it three times
 // (from L2 after the first); between them two sums over the block and the cluster.
+template <bool kRename>
 __global__ void __launch_bounds__(kThreads) __cluster_dims__(kCluster, 1, 1)
-    mla_pages_compact_kernel(const CompactParams p) {
+    mla_pages_compact_kernel(const CompactParams p, const RenameParams r) {
   __shared__ int scratch[kWarps], box[2][2 * kCluster];
   const uint32_t rank = cluster_ctarank();
   const int tid = threadIdx.x;
@@ -467,74 +536,12 @@ __global__ void __launch_bounds__(kThreads) __cluster_dims__(kCluster, 1, 1)
     }
   }
   if (rank == 0 && tid == 0) *p.count = moves;
+  if constexpr (kRename) rename_rows(r, moves, rank, kCluster);
 }
 
-struct RenameParams {
-  const int32_t* table;
-  int64_t stride;
-  const int32_t* lens;
-  int32_t* out;
-  int64_t out_stride;
-  int R, chunks, vec;
-  const int32_t* src;
-  const int32_t* dst;
-  const int32_t* count;
-  int* status;
-};
-
-// The table's live entries with the moved pages' new numbers.  The moved pages
-// are the highest live ones, so src is sorted (descending) and an entry below
-// its last is not moved; others find their place by bisection.
 __global__ void __launch_bounds__(kThreads) mla_pages_rename_kernel(const RenameParams p) {
   griddep_wait();
-  const int moves = *p.count;
-  const int lowest = moves ? p.src[moves - 1] : 0x7fffffff;
-  const auto renamed = [&](int e) {
-    const int page = e / kPage;
-    if (page < lowest) return e;
-    int lo = 0, hi = moves;  // the first entry not above the page
-    while (lo < hi) {
-      const int mid = (lo + hi) / 2;
-      if (p.src[mid] > page) lo = mid + 1; else hi = mid;
-    }
-    return lo < moves && p.src[lo] == page ? p.dst[lo] * kPage + e % kPage : e;
-  };
-  const bool in_place = p.table == p.out;
-  const int64_t tasks = (int64_t)p.R * p.chunks;
-  for (int64_t t = blockIdx.x; t < tasks; t += gridDim.x) {
-    const int i = (int)(t / p.chunks);
-    const int64_t e0 = (t % p.chunks) * kChunk;
-    const int64_t len = p.lens[i], room = min(p.stride, p.out_stride);
-    if (len < 0 || len > room) {
-      if (e0 == 0 && threadIdx.x == 0 && p.status) atomicOr(p.status, MLA_STATUS_BAD_LENGTH);
-      continue;
-    }
-    const int64_t e1 = min(min(e0 + kChunk, pages_of(len) * kPage), room);
-    const int32_t* src = p.table + i * p.stride;
-    int32_t* dst = p.out + i * p.out_stride;
-    if (p.vec) {
-      int4 v[kChunk / (4 * kThreads)];
-#pragma unroll
-      for (int u = 0; u < kChunk / (4 * kThreads); ++u) {
-        const int64_t e = e0 + 4 * (threadIdx.x + u * kThreads);
-        if (e < e1) v[u] = *reinterpret_cast<const int4*>(src + e);
-      }
-#pragma unroll
-      for (int u = 0; u < kChunk / (4 * kThreads); ++u) {
-        const int64_t e = e0 + 4 * (threadIdx.x + u * kThreads);
-        if (e >= e1) continue;
-        const int x = renamed(v[u].x);  // four entries of one page
-        if (in_place && x == v[u].x) continue;
-        *reinterpret_cast<int4*>(dst + e) = make_int4(x, v[u].y + (x - v[u].x), v[u].z + (x - v[u].x),
-                                                      v[u].w + (x - v[u].x));
-      }
-    } else {
-      for (int64_t e = e0 + threadIdx.x; e < e1; e += kThreads) {
-        const int x = renamed(src[e]);
-        if (!in_place || x != src[e]) dst[e] = x;
-      }
-    }
-  }
+  rename_rows(p, *p.count, blockIdx.x, gridDim.x);
 }
 
 // ---------------------------------------------------------------------- copy
@@ -576,13 +583,6 @@ __global__ void __launch_bounds__(kCopyThreads)
     if (scale && at == 0 && threadIdx.x < live)
       scale[(int64_t)d * kPage + threadIdx.x] = scale[(int64_t)s * kPage + threadIdx.x];
   }
-}
-
-int sm_count(int* sms) {
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
-  return e == cudaSuccess ? MLA_OK : cuda_fail(e, "device query");
 }
 
 // A launch whose first instructions may overlap the end of the kernel before it
@@ -635,21 +635,21 @@ extern "C" int mla_pages_fork(const int32_t* table, int64_t stride, const int32_
   p.vec = aligned(table, 16) && aligned(table_out, 16) && stride % 4 == 0 && out_stride % 4 == 0;
   p.chunks = (int)((std::min(stride, out_stride) + kChunk - 1) / kChunk);
   p.refs_vec = aligned(refs, 16);
-  int sms = 0;
-  const int rc = sm_count(&sms);
+  int dev = 0, sms = 0;
+  const int rc = device_sms(&dev, &sms);
   if (rc != MLA_OK) return rc;
   // up to two CTAs per SM for the copies, in whole clusters
   const int64_t tasks = (int64_t)R * p.chunks;
   const int64_t clusters = 1 + std::min<int64_t>((tasks + kCluster - 1) / kCluster, 2 * sms / kCluster);
   const int smem = R * 8 + (6 * R + 2) * 4;
   static_assert(kMaxRows * 32 + 8 <= 200 * 1024, "shared memory budget");
-  cudaError_t e = cudaSuccess;
-  if (smem > 47 * 1024)
-    e = cudaFuncSetAttribute(mla_pages_fork_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             kMaxRows * 32 + 8);
-  if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(mla_pages_fork_kernel)");
+  static std::atomic<uint64_t> set_on{0};
+  if (smem > 47 * 1024) {
+    const int set = allow_shared(mla_pages_fork_kernel, kMaxRows * 32 + 8, dev, set_on, "cudaFuncSetAttribute(mla_pages_fork_kernel)");
+    if (set != MLA_OK) return set;
+  }
   mla_pages_fork_kernel<<<(unsigned)(clusters * kCluster), kThreads, smem, (cudaStream_t)stream>>>(p);
-  e = cudaGetLastError();
+  const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_fail(e, "launch mla_pages_fork_kernel");
   return MLA_OK;
 }
@@ -675,17 +675,19 @@ extern "C" int mla_pages_compact(const int32_t* table, int64_t stride, const int
     if (q && !aligned(q, 4)) return fail(MLA_ERR_MISALIGNED, "mla_pages_compact: arrays need 4-B alignment");
   const cudaStream_t st = (cudaStream_t)stream;
   const CompactParams c{refs, num_pages, src, dst, max_moves, count, aligned(refs, 16)};
-  mla_pages_compact_kernel<<<kCluster, kThreads, 0, st>>>(c);
+  RenameParams p{table, stride, lens, table_out, out_stride, R, 0, 0, src, dst, count, status};
+  p.vec = R > 0 && aligned(table, 16) && aligned(table_out, 16) && stride % 4 == 0 && out_stride % 4 == 0;
+  p.chunks = (int)((std::min(stride, out_stride) + kChunk - 1) / kChunk);
+  const int64_t tasks = (int64_t)R * p.chunks;
+  // a small table is renamed by the same cluster: a launch less
+  if (tasks <= 2 * kCluster) mla_pages_compact_kernel<true><<<kCluster, kThreads, 0, st>>>(c, p);
+  else mla_pages_compact_kernel<false><<<kCluster, kThreads, 0, st>>>(c, p);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_fail(e, "launch mla_pages_compact_kernel");
-  if (R == 0) return MLA_OK;
-  RenameParams p{table, stride, lens, table_out, out_stride, R, 0, 0, src, dst, count, status};
-  p.vec = aligned(table, 16) && aligned(table_out, 16) && stride % 4 == 0 && out_stride % 4 == 0;
-  p.chunks = (int)((std::min(stride, out_stride) + kChunk - 1) / kChunk);
-  int sms = 0;
-  const int rc = sm_count(&sms);
+  if (tasks <= 2 * kCluster) return MLA_OK;
+  int dev = 0, sms = 0;
+  const int rc = device_sms(&dev, &sms);
   if (rc != MLA_OK) return rc;
-  const int64_t tasks = (int64_t)R * p.chunks;
   e = launch_after(mla_pages_rename_kernel, (unsigned)std::min<int64_t>(tasks, 4 * sms), kThreads, st, p);
   if (e != cudaSuccess) return cuda_fail(e, "launch mla_pages_rename_kernel");
   return MLA_OK;
@@ -709,8 +711,8 @@ extern "C" int mla_kv_copy(void* kv_pages, mla_kv_dtype kv_dtype, float* kv_scal
   const void* all[] = {kv_scale, src, dst, tokens, count, status};
   for (const void* q : all)
     if (q && !aligned(q, 4)) return fail(MLA_ERR_MISALIGNED, "mla_kv_copy: arrays need 4-B alignment");
-  int sms = 0;
-  const int rc = sm_count(&sms);
+  int dev = 0, sms = 0;
+  const int rc = device_sms(&dev, &sms);
   if (rc != MLA_OK) return rc;
   const int slices = (kPage * row_bytes + kSlice - 1) / kSlice;
   const int64_t tasks = n * slices;

@@ -43,6 +43,7 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "mla_tma.cuh"
 #include "ptx_sm103.cuh"
@@ -74,7 +75,6 @@ struct Form {
   static constexpr int kBlock = kTiles * kRows * kCtas;                   // rows of a unit
   static constexpr int kSoftmax = 4 * kTiles;                             // warps; the others after them
   static constexpr int kTma = kSoftmax, kMma = kTma + 1, kNext = kTma + 2, kClean = kTma + (kCtas == 1 ? 3 : 4);
-  [[maybe_unused]] static constexpr int kQ = kTma + 3;                    // (one CTA: Q from warp kTma)
   static constexpr int kCleaners = kCtas;
   static constexpr int kThreads = 2 * 32 * kSoftmax;
   static constexpr int kK = kCtas == 1 ? 3 : 1, kV = kCtas == 1 ? 2 : 1;  // pieces of a tile
@@ -121,6 +121,7 @@ struct PrefillParams {
   __nv_bfloat16* out;
   float* lse;
   int* status;
+  int ends;                // maps of 32 rows are there
 };
 
 // A work unit: `rows` rows from row0 of a sequence (first row q0, first key k0,
@@ -426,8 +427,8 @@ __device__ __forceinline__ void feed(Ctl<kCtas>& c, const PrefillParams& p, uint
 __device__ __forceinline__ void produce_one(uint8_t* base, Ctl<1>& c, const PrefillParams& p, const PrefillMaps& m,
                                             int lane) {
   using F = Form<1>;
-  const auto v_boxes = [](int left) { return left > kFew ? 1 : left > 0 ? 2 : 0; };
-  const auto v_bytes = [](int left) { return left > kFew ? kBox : left > 0 ? 2 * kFewBytes : 0; };
+  const auto v_boxes = [&](int left) { return left > kFew || !p.ends ? 1 : left > 0 ? 2 : 0; };
+  const auto v_bytes = [&](int left) { return left > kFew || !p.ends ? kBox : left > 0 ? 2 * kFewBytes : 0; };
   Units<1> units(c);
   bool ok = true;
   uint32_t pos = 0, cleans = 0, uses = 0;
@@ -442,7 +443,7 @@ __device__ __forceinline__ void produce_one(uint8_t* base, Ctl<1>& c, const Pref
         if (j == j0 && i == F::kK) {
           if (uses > 0 && !(ok = wait_bar(&c.qfree[0], (uses - 1) & 1, &c.abort_flag))) break;
           ++uses;
-          const int few = rows > kRows - kFew ? 0 : 1, n = few ? (rows + kFew - 1) / kFew : 1;
+          const int few = p.ends && rows <= kRows - kFew, n = few ? (rows + kFew - 1) / kFew : 1;
           if (lane == 0) mbar_arrive_expect_tx(smem_u32(&c.q[0]), 3 * (few ? n * kFewBytes : kBox));
           __syncwarp();
           if (lane < 3 * n) {
@@ -457,7 +458,7 @@ __device__ __forceinline__ void produce_one(uint8_t* base, Ctl<1>& c, const Pref
         const uint32_t dst = smem_u32(base + F::kQBytes + F::at(piece));
         uint32_t bar = smem_u32(&c.full[piece]);
         if (i < F::kK) {
-          const int few = left > kKeys - kFew ? 0 : 1, n = few ? (left + kFew - 1) / kFew : 1;
+          const int few = p.ends && left <= kKeys - kFew, n = few ? (left + kFew - 1) / kFew : 1;
           if (lane == 0) mbar_arrive_expect_tx(bar, few ? n * kFewBytes : kBox);
           __syncwarp();
           if (lane < n)
@@ -1014,7 +1015,7 @@ __global__ void __launch_bounds__(Form<kCtas>::kThreads, kCtas == 1 ? 2 : 1)
     } else if (warp >= F::kClean && warp < F::kClean + F::kCleaners) {
       clean_values<kCtas>(base, c, p, rank, warp - F::kClean, lane);
     } else if constexpr (kCtas == 2) {
-      if (warp == F::kQ) load_queries(base, c, p, m, rank, lane);
+      if (warp == F::kNext + 1) load_queries(base, c, p, m, rank, lane);
     }
     teardown();
   } else {
@@ -1079,10 +1080,11 @@ int head_map(CUtensorMap* map, const void* base, int dims, int H, int64_t T, int
 }
 
 template <int kCtas>
-int launch_prefill(const PrefillMaps& m, const PrefillParams& p, cudaStream_t st) {
+int launch_prefill(const PrefillMaps& m, const PrefillParams& p, int dev, cudaStream_t st) {
   auto kernel = mla_prefill_kernel<kCtas>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem<kCtas>);
-  if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(mla_prefill_kernel)");
+  static std::atomic<uint64_t> set_on{0};
+  const int rc = allow_shared(kernel, kSmem<kCtas>, dev, set_on, "cudaFuncSetAttribute(mla_prefill_kernel)");
+  if (rc != MLA_OK) return rc;
   const unsigned units = (unsigned)p.num_work * (unsigned)p.H;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(units * kCtas, 1, 1);
@@ -1095,7 +1097,7 @@ int launch_prefill(const PrefillMaps& m, const PrefillParams& p, cudaStream_t st
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = kCtas > 1 ? 1 : 0;
-  e = cudaLaunchKernelEx(&cfg, kernel, m, p);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, m, p);
   if (e != cudaSuccess) return cuda_fail(e, "launch mla_prefill_kernel");
   if (p.num_parts > 0) {
     mla_prefill_merge_kernel<kCtas><<<dim3(units, Form<kCtas>::kBlock / kMergeRows), 256, 0, st>>>(p);
@@ -1163,9 +1165,13 @@ extern "C" int mla_prefill(const void* q_nope, int64_t qn_token_stride, int64_t 
     kn_token_stride = kn_head_stride = v_token_stride = v_head_stride = kNope;
     kr_token_stride = kRope;
   }
-  PrefillMaps m = {};
-  int rc = MLA_OK;
-  for (int few = 0; few < (ctas == 1 ? 2 : 1) && rc == MLA_OK; ++few) {
+  PrefillMaps m;
+  int dev = 0, sms = 0;
+  int rc = device_sms(&dev, &sms);
+  // boxes of 32 rows pay where there is traffic to save: a few units wait for
+  // nothing else, and five more maps take the host 2 us
+  const int ends = ctas == 1 && (int64_t)num_work * H >= 2 * sms;
+  for (int few = 0; few <= ends && rc == MLA_OK; ++few) {
     const int rows = few ? kFew : kRows, keys = few ? kFew : kKeys / ctas;  // a CTA's tokens of a key tile
     rc = head_map(&m.qn[few], q_nope, kNope, H, Tq, qn_token_stride, qn_head_stride, rows);
     if (rc == MLA_OK) rc = head_map(&m.qr[few], q_rope, kRope, H, Tq, qr_token_stride, qr_head_stride, rows);
@@ -1183,7 +1189,7 @@ extern "C" int mla_prefill(const void* q_nope, int64_t qn_token_stride, int64_t 
   }
   if (rc != MLA_OK) return rc;
   const PrefillParams p{cu_q, cu_kv, prefix, N, H, causal != 0, Tq, Tk, sm_scale, sm_scale * kLog2e, work,
-                        num_work, num_parts, O_part, LSE_part, static_cast<__nv_bfloat16*>(out), lse, status};
+                        num_work, num_parts, O_part, LSE_part, static_cast<__nv_bfloat16*>(out), lse, status, ends};
   const cudaStream_t st = (cudaStream_t)stream;
-  return ctas == 1 ? launch_prefill<1>(m, p, st) : launch_prefill<2>(m, p, st);
+  return ctas == 1 ? launch_prefill<1>(m, p, dev, st) : launch_prefill<2>(m, p, dev, st);
 }
