@@ -14,7 +14,7 @@
 // Which logits of a tile may count: the k-th largest of the 64 largest values that a
 // warp's lanes have met in their even and odd vectors is a bound that at least k
 // values of the part reach, and few more do (about k ln k for values in random
-// order).  While tiles pass only each lane's largest value of each is kept; after 16 of
+// order).  While tiles pass only each lane's largest value of each is kept; after 32 of
 // them, or at the part's end, the bound is found and the few lanes' tiles that reach
 // it are read again (about 20 times 128 bytes of 64 KB).  Where too many reach it (ties, a
 // vocabulary that is mostly masked) the best k so far are selected exactly, and
@@ -43,10 +43,10 @@ constexpr int kMaxCluster = 8;               // (16 of them start later: 16 x 5 
 constexpr int kVecs = 8;                    // 16-byte vectors of a row per lane and tile
 constexpr int kStages = 2;                  // tiles of a warp in shared memory
 constexpr int kMaxK = MLA_BEAM_MAX_K, kMaxW = MLA_BEAM_MAX_W;
-constexpr int kMaxLists = 32;               // parts of rows in a CTA
+constexpr int kMaxLists = 16;               // parts of rows in a CTA: two for a warp
 constexpr int kMaxParts = 512;              // in a cluster
 constexpr int kCount = 512;
-constexpr int kEpoch = 16;                  // tiles whose values are looked for at once
+constexpr int kEpoch = 32;                  // tiles whose values are looked for at once
 constexpr int kCap = kMaxK + 126;           // candidates of a warp: its best so far, room for a lane's tile
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr uint32_t kLeast = 0x00800000u;    // the least finite value's place in the order
@@ -695,7 +695,7 @@ int launch_beam(BeamParams p, int B, cudaStream_t st) {
   if (rc == MLA_OK) rc = allow_shared(kernel, (int)sizeof(Smem), dev, set_on, "cudaFuncSetAttribute(mla_beam_select_kernel)");
   if (rc != MLA_OK) return rc;
   constexpr int kTile = 32 * kVecs * Type<T>::kPer;
-  p.cluster = 1;
+  p.cluster = p.W > kMaxLists ? 2 : 1;
   while (p.cluster < kMaxCluster && (int64_t)B * p.cluster * 2 <= 2 * sms &&
          (int64_t)p.W * p.V > (int64_t)p.cluster * kWarps * kTile / 2)
     p.cluster *= 2;
