@@ -547,41 +547,44 @@ __global__ void __launch_bounds__(kThreads) mla_pages_rename_kernel(const Rename
 // ---------------------------------------------------------------------- copy
 constexpr int kCopyThreads = 256;
 constexpr int kCopyVecs = 4;  // 16-byte vectors in flight per thread
-constexpr int kSlice = kCopyThreads * kCopyVecs * 16;
+constexpr int kSlice = kCopyThreads * kCopyVecs;  // vectors of a block's turn: less than a page's
 
+// All entries' pages as one sequence of 16-byte vectors, so that every turn is
+// full whatever a page takes (slices of a page: 326 MB in 4-bit pages took 60 us).
 __global__ void __launch_bounds__(kCopyThreads)
-    mla_kv_copy_kernel(uint8_t* kv, float* scale, int row_bytes, int64_t num_pages,
+    mla_kv_copy_kernel(uint8_t* kv, float* scale, int row_vecs, int64_t num_pages,
                        const int32_t* src, const int32_t* dst, const int32_t* tokens,
-                       const int32_t* count, int64_t n, int slices, int* status) {
+                       const int32_t* count, int64_t n, int* status) {
   griddep_wait();
   if (count) n = min(n, (int64_t)max(*count, 0));
-  const int64_t tasks = n * slices;
-  for (int64_t t = blockIdx.x; t < tasks; t += gridDim.x) {
-    const int64_t i = t / slices;
-    const int s = src[i], d = dst[i];
-    if (s < 0 || d < 0 || s == d) continue;
-    if (s >= num_pages || d >= num_pages) {
-      if (threadIdx.x == 0 && status) atomicOr(status, MLA_STATUS_BAD_SLOT);
-      continue;
-    }
-    const int live = tokens ? min(max(tokens[i], 0), kPage) : kPage;
-    const int bytes = live * row_bytes, at = (int)(t % slices) * kSlice;
-    const int64_t page_bytes = (int64_t)kPage * row_bytes;
-    const uint8_t* from = kv + s * page_bytes;
-    uint8_t* to = kv + d * page_bytes;
+  const int vecs = kPage * row_vecs;  // of a page
+  uint4* pool = reinterpret_cast<uint4*>(kv);
+  for (int64_t t = (int64_t)blockIdx.x * kSlice; t < n * vecs; t += (int64_t)gridDim.x * kSlice) {
+    const int64_t entry = t / vecs;
+    const int at = (int)(t - entry * vecs) + threadIdx.x;
     uint4 v[kCopyVecs];
+    int64_t to[kCopyVecs];
 #pragma unroll
     for (int u = 0; u < kCopyVecs; ++u) {
-      const int o = at + (u * kCopyThreads + threadIdx.x) * 16;
-      if (o < bytes) v[u] = *reinterpret_cast<const uint4*>(from + o);
+      const int past = at + u * kCopyThreads >= vecs, o = at + u * kCopyThreads - past * vecs;
+      const int64_t i = entry + past;
+      to[u] = -1;
+      if (i >= n) continue;
+      const int s = src[i], d = dst[i];
+      if (s < 0 || d < 0 || s == d) continue;
+      if (s >= num_pages || d >= num_pages) {
+        if (o == 0 && status) atomicOr(status, MLA_STATUS_BAD_SLOT);
+        continue;
+      }
+      const int live = tokens ? min(max(tokens[i], 0), kPage) : kPage;
+      if (o >= live * row_vecs) continue;
+      v[u] = pool[(int64_t)s * vecs + o];
+      to[u] = (int64_t)d * vecs + o;
+      if (scale && o < live) scale[(int64_t)d * kPage + o] = scale[(int64_t)s * kPage + o];
     }
 #pragma unroll
-    for (int u = 0; u < kCopyVecs; ++u) {
-      const int o = at + (u * kCopyThreads + threadIdx.x) * 16;
-      if (o < bytes) *reinterpret_cast<uint4*>(to + o) = v[u];
-    }
-    if (scale && at == 0 && threadIdx.x < live)
-      scale[(int64_t)d * kPage + threadIdx.x] = scale[(int64_t)s * kPage + threadIdx.x];
+    for (int u = 0; u < kCopyVecs; ++u)
+      if (to[u] >= 0) pool[to[u]] = v[u];
   }
 }
 
@@ -714,12 +717,14 @@ extern "C" int mla_kv_copy(void* kv_pages, mla_kv_dtype kv_dtype, float* kv_scal
   int dev = 0, sms = 0;
   const int rc = device_sms(&dev, &sms);
   if (rc != MLA_OK) return rc;
-  const int slices = (kPage * row_bytes + kSlice - 1) / kSlice;
-  const int64_t tasks = n * slices;
+  static_assert(kSlice <= kPage * MLA_FP4_ROW_BYTES / 16, "a turn touches two pages at most");
+  const int row_vecs = row_bytes / 16;
+  // a turn's blocks as many as n entries take, up to eight per SM
+  const int64_t turns = n > (int64_t)1 << 24 ? (int64_t)1 << 24 : (n * kPage * row_vecs + kSlice - 1) / kSlice;
   const cudaError_t e = launch_after(
-      mla_kv_copy_kernel, (unsigned)std::min<int64_t>(tasks, 8 * sms), kCopyThreads, (cudaStream_t)stream,
-      static_cast<uint8_t*>(kv_pages), kv_dtype == MLA_KV_FP8_E4M3 ? kv_scale : (float*)nullptr, row_bytes,
-      num_slots / kPage, src, dst, tokens, count, n, slices, status);
+      mla_kv_copy_kernel, (unsigned)std::min<int64_t>(turns, 8 * sms), kCopyThreads, (cudaStream_t)stream,
+      static_cast<uint8_t*>(kv_pages), kv_dtype == MLA_KV_FP8_E4M3 ? kv_scale : (float*)nullptr, row_vecs,
+      num_slots / kPage, src, dst, tokens, count, n, status);
   if (e != cudaSuccess) return cuda_fail(e, "launch mla_kv_copy_kernel");
   return MLA_OK;
 }
