@@ -11,9 +11,9 @@
 // distributed shared memory.  One launch, no workspace, and no result that depends on
 // an order of arrival.
 //
-// Which logits of a tile may count: the k-th largest of the 64 largest values that a
-// warp's lanes have met in their even and odd vectors is a bound that at least k
-// values of the part reach, and few more do (about k ln k for values in random
+// Which logits of a tile may count: the k-th largest of the 64 or 128 values that a
+// warp's lanes have met as the largest of every second or fourth vector is a bound
+// that at least k values of the part reach, and few more do (about k ln k for values in random
 // order).  While tiles pass only each lane's largest value of each is kept; after 32 of
 // them, or at the part's end, the bound is found and the few lanes' tiles that reach
 // it are read again (about 20 times 128 bytes of 64 KB).  Where too many reach it (ties, a
@@ -41,6 +41,7 @@ constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kMaxCluster = 8;               // (16 of them start later: 16 x 5 x 100003 took 33 us, not 22)
 constexpr int kVecs = 8;                    // 16-byte vectors of a row per lane and tile
+constexpr int kTops = 4;                    // values a lane gives to the bound: its largest of every fourth vector
 constexpr int kStages = 2;                  // tiles of a warp in shared memory
 constexpr int kMaxK = MLA_BEAM_MAX_K, kMaxW = MLA_BEAM_MAX_W;
 constexpr int kMaxLists = 16;               // parts of rows in a CTA: two for a warp
@@ -76,7 +77,7 @@ struct Smem {
     };
   };
   u64 buf[kWarps][kCap + 2];                // candidates of the warps' parts at hand
-  uint32_t words[kWarps][64];
+  uint32_t words[kWarps][32 * kTops];
   uint16_t tops[kWarps][kEpoch * 32];       // lanes' largest values of the tiles, cut to 16 bits; later: pairs
   u64 list[kMaxLists * kMaxK];              // the parts' best in order; later: their scores
   float2 stat[kMaxParts];                   // (max, sum) of the cluster's parts
@@ -280,24 +281,32 @@ __device__ __noinline__ int select(u64* keys, int n, int k, u64* out, uint32_t* 
   return n;
 }
 
-// The place in the order of the k-th largest of the warp's 64 values: each is
-// compared with all of them, through 64 words of shared memory.
-__device__ __forceinline__ uint32_t kth_of(float a, float b, int k, uint32_t* words) {
+// The place in the order of the k-th largest of the lanes' kTops values: each is
+// compared with all of them, through shared memory.
+template <int kTops>
+__device__ __forceinline__ uint32_t kth_of(const float (&x)[kTops], int k, uint32_t* words) {
   const int lane = threadIdx.x & 31;
-  const uint32_t ka = ordered(a), kb = ordered(b);
+  uint32_t mine[kTops];
+  int above[kTops];
   __syncwarp();
-  words[lane] = ka;
-  words[32 + lane] = kb;
+#pragma unroll
+  for (int i = 0; i < kTops; ++i) {
+    mine[i] = ordered(x[i]);
+    above[i] = 0;
+    words[32 * i + lane] = mine[i];
+  }
   __syncwarp();
-  int above_a = 0, above_b = 0;
 #pragma unroll 4
-  for (int j = 0; j < 16; ++j) {
-    const uint4 x = *reinterpret_cast<const uint4*>(words + 4 * j);
-    above_a += (x.x > ka) + (x.y > ka) + (x.z > ka) + (x.w > ka);
-    above_b += (x.x > kb) + (x.y > kb) + (x.z > kb) + (x.w > kb);
+  for (int j = 0; j < 8 * kTops; ++j) {
+    const uint4 y = *reinterpret_cast<const uint4*>(words + 4 * j);
+#pragma unroll
+    for (int i = 0; i < kTops; ++i) above[i] += (y.x > mine[i]) + (y.y > mine[i]) + (y.z > mine[i]) + (y.w > mine[i]);
   }
   // the least value that fewer than k exceed
-  return __reduce_min_sync(~0u, min(above_a < k ? ka : ~0u, above_b < k ? kb : ~0u));
+  uint32_t least = ~0u;
+#pragma unroll
+  for (int i = 0; i < kTops; ++i) least = min(least, above[i] < k ? mine[i] : ~0u);
+  return __reduce_min_sync(~0u, least);
 }
 
 // A warp's way through its parts of rows, tile by tile; parts of which nothing
@@ -371,23 +380,28 @@ __device__ __forceinline__ void merge_lists(u64* score, const long long* pos, co
     }
     return;
   }
+  int top = 1;  // the highest power of two up to pitch
+  while (2 * top <= pitch) top *= 2;
 #pragma unroll 1
-  for (int e = threadIdx.x; e < lists * pitch; e += kThreads) {
+  for (int e = threadIdx.x; e < all; e += kThreads) {
     const int l = e / pitch, j = e % pitch;
     if (j >= num[l]) continue;
     const u64 s = score[e];
     const long long at = pos[e];
     int rank = j;
 #pragma unroll 1
-    for (int m = 0; m < lists && rank < k; ++m) {
-      if (m == l) continue;
-      int lo = 0, hi = num[m];
+    for (int m0 = 0; m0 < lists && rank < k; m0 += 4) {
+      int below[4] = {0, 0, 0, 0};  // entries of four lists that come before
 #pragma unroll 1
-      while (lo < hi) {
-        const int mid = (lo + hi) / 2, f = m * pitch + mid;
-        if (score[f] > s || (score[f] == s && pos[f] < at)) lo = mid + 1; else hi = mid;
+      for (int step = top; step; step >>= 1) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int m = min(m0 + u, lists - 1), f = m * pitch + below[u] + step - 1;
+          if (below[u] + step <= num[m] && (score[f] > s || (score[f] == s && pos[f] < at))) below[u] += step;
+        }
       }
-      rank += lo;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) rank += m0 + u < lists && m0 + u != l ? below[u] : 0;
     }
     if (rank < k) put(rank, e);
   }
@@ -432,6 +446,7 @@ __global__ void __launch_bounds__(kThreads, 2) mla_beam_select_kernel(const Beam
         for (int u = 0; u < kVecs; ++u) {
           const int64_t e = e0 + u * 32 * kPer;
           if (e >= to.lo && e + kPer <= to.hi) cp_async16(dst + u * 32, to.row + e);
+          else if (e + kPer <= to.lo || e >= to.hi) dst[u * 32] = make_uint4(Type<T>::kNone, Type<T>::kNone, Type<T>::kNone, Type<T>::kNone);
           else dst[u * 32] = load_edge<T>(to.row, e, to.lo, to.hi);
         }
       }
@@ -446,7 +461,9 @@ __global__ void __launch_bounds__(kThreads, 2) mla_beam_select_kernel(const Beam
   for (int i = 0; i < kStages - 1; ++i) fetch(i);
   u64* buf = sm.buf[warp];
   float m = -INFINITY, s = 0.f, s_low = 0.f;   // the lane's maximum and sum
-  float a = -INFINITY, c = -INFINITY;          // its largest in even and odd vectors
+  float a[kTops];                              // its largest of every fourth vector
+#pragma unroll
+  for (int i = 0; i < kTops; ++i) a[i] = -INFINITY;
   uint32_t floor = kLeast, limit = kLeast;     // k values reach the one; from the other on values count
   int n = 0, tiles = 0;                        // candidates, tiles of the epoch
 #pragma unroll 1
@@ -454,16 +471,20 @@ __global__ void __launch_bounds__(kThreads, 2) mla_beam_select_kernel(const Beam
     fetch(stage == 0 ? kStages - 1 : stage - 1);
     asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
     const uint4* tile = &sm.tile[warp][stage][0][lane];
-    uint32_t most[2];
+    uint32_t most[kTops];
 #pragma unroll
     for (int u = 0; u < kVecs; ++u) {
       const uint4 v = tile[u * 32];
       const uint32_t best = Type<T>::max2(Type<T>::max2(v.x, v.y), Type<T>::max2(v.z, v.w));
-      most[u & 1] = u < 2 ? best : Type<T>::max2(most[u & 1], best);
+      most[u % kTops] = u < kTops ? best : Type<T>::max2(most[u % kTops], best);
     }
-    const float even = Type<T>::top(most[0]), odd = Type<T>::top(most[1]), top = fmaxf(even, odd);
-    a = fmaxf(a, even);
-    c = fmaxf(c, odd);
+    float top = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < kTops; ++i) {
+      const float x = Type<T>::top(most[i]);
+      a[i] = fmaxf(a[i], x);
+      top = fmaxf(top, x);
+    }
     // the sum, over differences to the lane's maximum
     if (top > m) {
       const float f = ex2((m - top) * kLog2e);
@@ -494,7 +515,14 @@ __global__ void __launch_bounds__(kThreads, 2) mla_beam_select_kernel(const Beam
     u64* list = sm.list + (at.g / step * kWarps + warp) * k;
     tops[tiles++ * 32 + lane] = (uint16_t)(ordered(top) >> 16);
     if (tiles == kEpoch || at.last()) {
-      floor = max(floor, kth_of(a, c, k, sm.words[warp]));
+      // the largest of every second vector do for few (10.6 us of one request's
+      // beams against 12.5), for k near 64 hardly anything would lie below them
+      if (k <= 24) {
+        const float two[2] = {fmaxf(a[0], a[2]), fmaxf(a[1], a[3])};
+        floor = max(floor, kth_of(two, k, sm.words[warp]));
+      } else {
+        floor = max(floor, kth_of(a, k, sm.words[warp]));
+      }
       limit = max(limit, floor);
       // lanes and tiles with a value that reaches it, in place
       int pairs = 0;
@@ -568,7 +596,9 @@ __global__ void __launch_bounds__(kThreads, 2) mla_beam_select_kernel(const Beam
       sm.stat[at.g] = make_float2(wm, s);
     }
     at.enter(p, sm.live, b, len, at.g + step);
-    m = a = c = -INFINITY;
+    m = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < kTops; ++i) a[i] = -INFINITY;
     s = s_low = 0.f;
     floor = limit = kLeast;
     n = 0;
