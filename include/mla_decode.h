@@ -733,8 +733,8 @@ int mla_plan_prefill(const int32_t* q_lens, const int32_t* kv_lens,
  *   scores     fp32 [B, W]: the beams' summed log probabilities; -inf rules a
  *              beam out (its logits are not read)
  *   finished   bytes [B, W], non-zero: finished; or NULL
- * Sums are fp32 over a thread's and a warp's logits and fp64 from there; scores
- * are formed and compared in fp64, a beam's own tokens by their logits.
+ * Sums are fp32 over a lane's tiles (compensated) and a warp, and pairs of fp32 from
+ * there; scores are formed and compared in fp64, a beam's own tokens by their logits.
  * W <= MLA_BEAM_MAX_W, k <= MLA_BEAM_MAX_K (else MLA_ERR_UNSUPPORTED), k <= W V.
  */
 typedef enum { MLA_LOGIT_BF16 = 0, MLA_LOGIT_F16 = 1, MLA_LOGIT_F32 = 2 } mla_logit_dtype;

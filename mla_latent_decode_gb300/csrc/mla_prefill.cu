@@ -3,43 +3,50 @@
 // RoPE key for all heads, and o = softmax(s) v over the keys that a row sees,
 // which are always the first ones of its sequence.
 //
-// Two forms of one kernel.  A work unit is a block of 256 query rows of one
-// sequence and head on one CTA (kCtas = 1), or of 512 rows on a pair of CTAs
-// whose MMAs span both SMs (cta_group::2).  Either way a CTA holds two row tiles
-// of 128 rows; keys come in tiles of 128 tokens: S = Q K^T is 12 MMAs of N = 128,
-// K = 16 (192 dims), O += P V eight more, M = 128 rows a CTA.  TMEM holds S and O
-// of both row tiles (4 x 128 columns); P overwrites its S in bf16 and is the MMA's
-// A operand from there.  While the softmax of one row tile runs, the tensor cores
-// work for the other: PV_0(t - 1), QK_0(t), PV_1(t - 1), QK_1(t), ...  MMAs of one
-// thread execute in order, so "S_g(t) is there" also says that PV_g(t - 1) is
-// done: the softmax may rescale O in place then, and S may overwrite P.
+// Two forms of one kernel.  A work unit is a block of rows of one sequence and head:
+// 128 rows on one CTA with one row tile (kCtas = 1; two CTAs share an SM, so that one's
+// loads and softmax overlap the other's MMAs), or 512 rows on a pair of CTAs with two
+// row tiles each, whose MMAs span both SMs (cta_group::2).  A row tile has 128 rows of
+// a CTA; keys come in tiles of 128 tokens: S = Q K^T is 12 MMAs of N = 128, K = 16 (192
+// dims), O += P V eight more.  TMEM holds S and O of a row tile (128 columns each); P
+// overwrites its S in bf16 and is the MMA's A operand from there.  In a pair, while the
+// softmax of one row tile runs, the tensor cores work for the other: PV_0(t - 1),
+// QK_0(t), PV_1(t - 1), QK_1(t), ...  MMAs of one thread execute in order, so "S_g(t)
+// is there" also says that PV_g(t - 1) is done: the softmax may rescale O in place
+// then, and S may overwrite P.
 //
-// What bounds it: on one SM the MMAs of a key tile pair take 2560 cycles and
-// their operands 256 KB of shared memory reads, which with the 80 KB that TMA
-// writes is 2690 cycles of its bandwidth and more than an SM's ring can load
-// ahead.  In the pair each SM loads and reads half of every K and V tile (40 KB,
-// and 1730 cycles of shared memory in all), which leaves the tensor cores as the
-// bound; short blocks fill only half of a pair.
+// What bounds it (GB300).  Pairs: the tensor cores under the power cap, one prompt of
+// 8191 tokens x 96 heads (2.06 PFLOP) in 1192 us, 1.73 PFLOP/s, 91% of the measured burst
+// and all of the measured sustained rate, tensor pipe active 78% of the cycles; each SM
+// loads and reads half of every K and V tile (40 KB).  On single CTAs a row tile's 80 KB
+// of keys and values a tile come in through a ring of 64 KB, so a tile waits for loads
+// that are issued as the one before is used up: 64 documents of 33 to 700 tokens x 96
+// heads 344 us, 1.62 GB moved, 70% of the copy rate.  A block of 512 rows of a short
+// sequence would mostly be padding (580 us).
 //
-//   warps 0-3, 4-7   softmax of row tile 0 and 1, one thread per row, then O / l
-//   warp 8           TMA: Q (96 KB), K and V through a ring of 128 KB, K in three
-//                    stages (64 dims of 128 tokens each, the third the RoPE key),
-//                    V in two (64 tokens each); in a pair a CTA's stage is half as
-//                    large, its half of the tokens (K) or of the dims (V)
-//   warp 9           MMA issue (one lane; of a pair's first CTA)
-//   warp 11          TMA: Q
-//   warp 10          the next unit: the grid has a CTA (pair) per unit, and running
-//                    ones take over those that have not started, in launch order, so
-//                    the work list is dealt out as SMs come free and a unit's loads
-//                    and first MMAs overlap the end of the one before
-//   warps 12, 13     clean V: in tiles that hold tokens which some row of the unit
+//   softmax warps    4 a row tile, one thread per row, then O / l
+//   TMA warp         K and V through the ring; on one CTA Q (48 KB) too
+//   Q warp           a pair's Q (96 KB a CTA)
+//   MMA warp         of a pair's first CTA; runs converged, one lane issues
+//   next unit's warp the grid has a CTA (pair) per unit, and running ones take over
+//                    those that have not started, in launch order, so the work list is
+//                    dealt out as SMs come free and a unit's loads and first MMAs
+//                    overlap the end of the one before
+//   cleaning warps   clean V: in tiles that hold tokens which some row of the unit
 //                    does not see, values that are not finite become 0 (P is 0
 //                    there, and 0 x NaN would reach the row) and are noted per
 //                    dim; the rows that do see them get them back at the end
 //
 // Softmax in base 2 with fp32 statistics; O is rescaled only when a row's
 // maximum has risen by more than 2^8, so P stays below 2^8 and its rounding to
-// bf16 is 2^-8 of each probability either way.
+// bf16 is 2^-8 of each probability either way.  A pair's softmax hands P over in two
+// halves, so that PV starts on the first (1414 -> 1298 us); on one CTA, where the
+// other CTA fills the gap, the second handshake costs more than it gives (350, 360).
+//
+// Code size matters as much as any of this: the warps' loops are long and different,
+// and at 118 KB of code everything ran at half its speed for want of instructions
+// (1414 us and 434 with 66 KB, 1215 and 347 with 55): waits are a few instructions
+// each, rare paths loop instead of being unrolled.
 #include <cuda_bf16.h>
 
 #include <algorithm>
