@@ -82,6 +82,38 @@ def test_large_vocabularies(V):
     _check(logits, scores, 6)
 
 
+@pytest.mark.parametrize("k", [1, 24, 25, 64])
+def test_parts_of_many_tiles(k):
+    """So many requests that a warp has more tiles of a row than are looked at together."""
+    V = 1200001
+    g = torch.Generator().manual_seed(k)
+    rows = torch.empty((4, 1, V))
+    rows[0, 0] = 3 * torch.randn(V, generator=g)
+    rows[1, 0] = torch.round(2 * torch.randn(V, generator=g))         # ties in every tile
+    rows[2, 0] = torch.sort(torch.randn(V, generator=g)).values       # the best at the end
+    rows[3, 0] = -math.inf
+    rows[3, 0, torch.randint(V, (40,), generator=g)] = 1.5
+    rows = rows.bfloat16()
+    scores = -torch.rand((4, 1), generator=g)
+    want, r, t = _reference(rows.cuda(), scores.cuda(), k, None, 0)
+    word = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got, parents, tokens = mla.beam_select(rows.cuda().repeat(40, 1, 1), scores.cuda().repeat(40, 1), k, status=word)
+    assert int(word.item()) == 0
+    live = want > -math.inf
+    for b in range(160):
+        assert torch.equal(tokens[b].cpu().long(), t[b % 4])
+        assert bool((parents[b] == b).all())
+        assert bool(((got[b].cpu().double() - want[b % 4]).abs() <= TOL + 2.0 ** -23 * want[b % 4].abs())[live[b % 4]].all())
+        assert torch.equal(got[b].cpu() > -math.inf, live[b % 4])
+
+
+@pytest.mark.parametrize("B,W", [(1, 32), (100, 17), (160, 32), (170, 8)])
+def test_many_rows_a_warp(B, W):
+    """Clusters with fewer warps than rows."""
+    logits, scores = _inputs(B, W, 300, torch.float16, seed=B)
+    _check(logits, scores, 40)
+
+
 def test_rows_at_odd_addresses():
     logits, scores = _inputs(2, 3, 1200)
     for off in (1, 3, 5):

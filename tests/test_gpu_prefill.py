@@ -201,6 +201,36 @@ def test_keys_and_values_that_a_row_does_not_see(bad, ctas):
     assert torch.equal(out[290:330], clean[290:330])
 
 
+@pytest.mark.parametrize("ctas", [1, 2])
+def test_ends_of_many_sequences(ctas):
+    """Launches of many units load sequences' ends in boxes of 32 rows; what is left of other
+    tiles in shared memory, NaN among it, reaches no row."""
+    lens = [1, 31, 32, 33, 63, 64, 65, 95, 96, 97, 127, 128, 129, 160, 200, 255, 257]
+    lk = [n + c for n, c in zip(lens, [0, 7, 64, 0, 31, 1, 95, 33, 0, 128, 2, 96, 0, 40, 8, 0, 63])]
+    x = _inputs(lens, lk, 40, seed=4, spare=32)
+    g = torch.Generator().manual_seed(5)
+    for name in ("k_nope", "v"):
+        for _ in range(12):
+            t, h = int(torch.randint(sum(lk), (1,), generator=g)), int(torch.randint(40, (1,), generator=g))
+            x[name][t, h, int(torch.randint(128, (1,), generator=g))] = math.nan
+    for name in ("k_nope", "v", "k_rope"):
+        x[name][sum(lk):] = math.nan
+    for name in ("q_nope", "q_rope"):
+        x[name][sum(lens):] = math.nan
+    _check(x, lens, lk, None, True, ctas=ctas)
+    _check(x, lens, lk, [0, 9] * 8 + [3], True, ctas=ctas)
+
+
+def test_broken_values_in_hundreds_of_units_a_cta():
+    """Notes on cleaned values are told apart over more units than their tags have numbers."""
+    lens, H = [5] * 60, 1200
+    x = _inputs(lens, lens, H, seed=8, wide=False)
+    for n in range(60):
+        for i, bad in enumerate((math.nan, math.inf, -math.inf)):
+            x["v"][5 * n + 1 + i, (37 * n + 400 * i) % H, (n + i) % 128] = bad
+    _check(x, lens, lens, None, True, ctas=1)
+
+
 def test_rows_behind_the_last_sequence_stay():
     lq, lk, H = [100], [100], 2
     x = _inputs(lq, lk, H, spare=50)

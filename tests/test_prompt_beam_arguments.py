@@ -2,6 +2,7 @@
 launch (no GPU needed), and the prompts' planner against its contract: every block
 of every sequence in exactly one set of parts.
 """
+import contextlib
 import ctypes
 import random
 
@@ -144,6 +145,41 @@ def test_binding_refuses():
                  dict(tokens=z(1, dtype=i32)), dict(count=z(1)), dict(src=z(2))):
         with pytest.raises(ValueError):
             mla.kv_copy(**{**k, **over})
+
+
+def _z(*shape, dtype=bf):
+    return torch.zeros(shape, dtype=dtype)
+
+
+CALLS = {
+    "prefill": lambda: mla.prefill(_z(5, 2, 128), _z(5, 2, 64), _z(7, 2, 128), _z(7, 64), _z(7, 2, 128), _z(2, dtype=i32),
+                                   _z(2, dtype=i32), _z(1, 8, dtype=i32), 0.07),
+    "beam_select": lambda: mla.beam_select(_z(2, 3, 50), _z(2, 3, dtype=f32), 4),
+    "pages_fork": lambda: mla.pages_fork(_z(2, 128, dtype=i32), _z(2, dtype=i32), _z(9, dtype=i32), _z(1, dtype=i32)),
+    "pages_compact": lambda: mla.pages_compact(_z(2, 128, dtype=i32), _z(2, dtype=i32), _z(9, dtype=i32)),
+    "kv_copy": lambda: mla.kv_copy(_z(128, 576), _z(2, dtype=i32), _z(2, dtype=i32)),
+}
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_launches_on_the_tensors_device(name, monkeypatch):
+    inside, seen = [], []
+
+    @contextlib.contextmanager
+    def on(t):
+        inside.append(t.device)
+        yield
+        inside.pop()
+
+    class Library:
+        def __getattr__(self, fn):
+            return lambda *args: seen.append(list(inside)) or 0
+
+    monkeypatch.setattr(mla, "_on", on)
+    monkeypatch.setattr(mla, "_stream", lambda stream: 0)
+    monkeypatch.setattr(mla, "library", lambda: Library())
+    CALLS[name]()
+    assert seen == [[torch.device("cpu")]]
 
 
 def test_plan_covers_every_block_once():
