@@ -65,7 +65,7 @@ constexpr int kSlot = 128;           // rows of a workspace slot, two to a part 
 constexpr int kKeys = 128;           // tokens of a key tile
 constexpr int kBox = 128 * 128;      // 16 KB: 64 dims of 128 rows
 constexpr int kVBytes = 2 * kBox;    // V of a tile
-constexpr int kRaw = 4;              // V tiles that may wait for cleaning (the ring holds parts of 3)
+constexpr int kRaw = 4;              // pieces of V that may wait for cleaning
 // The softmax warps take 200 registers a thread, the others 56: as many threads of
 // each kind, 128 on average, as the kernels launch with.
 constexpr int kRegsSoftmax = 200, kRegsOther = 56;
@@ -692,7 +692,7 @@ __device__ __forceinline__ void clean_values(uint8_t* base, Ctl<kCtas>& c, const
   uint32_t at = 0, cleans = 0;  // pieces and cleaned tiles so far
   while (const Unit* u = units.next(ok)) {
     const int j0 = u->j0, j1 = u->j1, clean0 = u->clean0, unseen = u->unseen, lk = u->lk;
-    bool first = true;
+    bool read = units.nth == 0;  // the notes on the unit before have been (by both CTAs)
     if (kCtas == 1 && units.nth % Notes<1>::kWipe == 0 && units.nth > 0) {
       if (!(ok = __all_sync(~0u, wait_bar(&c.done, (units.nth - 1) & 1, &c.abort_flag)))) break;
       for (int d = lane; d < kKeys; d += 32) c.notes.clear(d);
@@ -704,20 +704,15 @@ __device__ __forceinline__ void clean_values(uint8_t* base, Ctl<kCtas>& c, const
       const uint32_t nth = cleans + (j - clean0);
       if (kCtas == 2 && (nth & 1) != (uint32_t)i) continue;
       if (half == 0 && !(ok = __all_sync(~0u, wait_bar(&c.raw[nth % kRaw], nth / kRaw & 1, &c.abort_flag)))) break;
-      // the notes on the unit before have been read (by both CTAs)
-      if (first && units.nth > 0 &&
-          !(ok = __all_sync(~0u, wait_bar<kCtas == 2>(&c.done, (units.nth - 1) & 1, &c.abort_flag))))
-        break;
-      first = false;
       const uint32_t piece = (at + F::kTile * (j - j0) + F::kK + half) % F::kAll;
       uint4* box = reinterpret_cast<uint4*>(base + F::kQBytes + F::at(piece));
       const int t0 = j * kKeys + half * 64;  // token of the first row
 #pragma unroll 1
       for (int x0 = lane; x0 < kVecs; x0 += 32 * kBatch) {
         uint4 w[kBatch];
-        uint32_t hit = 0;
 #pragma unroll
         for (int b = 0; b < kBatch; ++b) w[b] = box[x0 + 32 * b];
+        uint32_t hit = 0;
 #pragma unroll
         for (int b = 0; b < kBatch; ++b)
           hit |= ((w[b].x & 0x7f807f80u) + 0x00800080u) | ((w[b].y & 0x7f807f80u) + 0x00800080u) |
@@ -734,6 +729,7 @@ __device__ __forceinline__ void clean_values(uint8_t* base, Ctl<kCtas>& c, const
           *val = 0;
           const int past = t0 + row - unseen, dim = dims * 64 + ((v & 7) ^ (row & 7)) * 8 + e % 8;
           if (t0 + row < lk && past < F::kBlock) {  // past that no row of the unit sees it
+            read = read || wait_bar<kCtas == 2>(&c.done, (units.nth - 1) & 1, &c.abort_flag);
             c.notes.add(units.nth, bits & 0x7fu ? 0 : bits & 0x8000u ? 2 : 1, dim, past, rank);
             c.any_odd = units.nth + 1;
             if constexpr (kCtas == 2) st_cluster_u32(mapa(smem_u32(&c.any_odd), rank ^ 1), units.nth + 1);
@@ -751,6 +747,11 @@ __device__ __forceinline__ void clean_values(uint8_t* base, Ctl<kCtas>& c, const
     if (!ok) break;
     at += F::kTile * (j1 - j0);
     if (j1 > clean0) {
+      // not before the softmax warps are through with the unit before, whose phase of
+      // `cleaned` they may still have to see
+      if (units.nth > 0 &&
+          !(ok = __all_sync(~0u, read || wait_bar<kCtas == 2>(&c.done, (units.nth - 1) & 1, &c.abort_flag))))
+        break;
       cleans += j1 - clean0;
       if (lane == 0) {
         mbar_arrive(smem_u32(&c.cleaned));
