@@ -51,7 +51,6 @@ constexpr int kStages = 2;                  // tiles of a warp in shared memory
 constexpr int kMaxK = MLA_BEAM_MAX_K, kMaxW = MLA_BEAM_MAX_W;
 constexpr int kMaxLists = 16;               // parts of rows in a CTA: two for a warp
 constexpr int kMaxParts = 512;              // in a cluster
-constexpr int kCount = 512;
 constexpr int kEpoch = 32;                  // tiles whose values are looked for at once
 constexpr int kCap = kMaxK + 126;           // candidates of a warp: its best so far, room for a lane's tile
 constexpr float kLog2e = 1.44269504088896340736f;
@@ -92,8 +91,12 @@ struct Smem {
   int got_num[kMaxCluster];
   float score[kMaxW], live[kMaxW];          // the beams'; with finished ones at -inf
   long long member[kMaxK];
+  uint16_t order[kMaxK];
 };
 static_assert(sizeof(Smem) <= 113 * 1024, "shared memory of two CTAs an SM");
+
+extern __shared__ __align__(16) uint8_t beam_smem[];
+__device__ __forceinline__ Smem& shared() { return *reinterpret_cast<Smem*>(beam_smem); }
 
 __device__ __forceinline__ uint32_t ordered(float x) {
   const uint32_t u = __float_as_uint(x + 0.f);  // -0 as 0
@@ -244,11 +247,14 @@ __device__ __noinline__ uint4 load_edge(const T* row, int64_t e, int64_t lo, int
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// The k best of a warp's n keys, in order, to `out`, of those with values from
-// `limit` on (at least k, or all): they are moved to the front first, then a key's
-// rank is the number of greater ones (keys differ).  Returns their number, k at most.
-__device__ __noinline__ int best_keys(u64* keys, int n, int k, uint32_t limit, u64* out) {
+// The k best of a warp's n candidates, in order, to list l, of those with values
+// from `limit` on (at least k, or all): they are moved to the front first, then a
+// key's rank is the number of greater ones (keys differ).  Returns their number, k at
+// most.
+__device__ __noinline__ int best_keys(int l, int n, int k, uint32_t limit) {
+  Smem& sm = shared();
   const int lane = threadIdx.x & 31;
+  u64 *keys = sm.buf[threadIdx.x >> 5], *out = sm.list + l * k;
   __syncwarp();
   int m = 0;
 #pragma unroll 1
@@ -278,10 +284,11 @@ __device__ __noinline__ int best_keys(u64* keys, int n, int k, uint32_t limit, u
 
 // Keeps the k best of a warp's n candidates; all later ones have to reach the last
 // of them.  Returns their number.
-__device__ __noinline__ int select(u64* keys, int n, int k, u64* out, uint32_t* floor) {
-  n = best_keys(keys, n, k, *floor, out);
-  for (int i = threadIdx.x & 31; i < n; i += 32) keys[i] = out[i];
-  if (n == k) *floor = max(*floor, (uint32_t)(out[k - 1] >> 32));
+__device__ __noinline__ int select(int l, int n, int k, uint32_t* floor) {
+  Smem& sm = shared();
+  n = best_keys(l, n, k, *floor);
+  for (int i = threadIdx.x & 31; i < n; i += 32) sm.buf[threadIdx.x >> 5][i] = sm.list[l * k + i];
+  if (n == k) *floor = max(*floor, (uint32_t)(sm.list[l * k + k - 1] >> 32));
   __syncwarp();
   return n;
 }
@@ -348,74 +355,48 @@ __device__ __forceinline__ void cp_async16(void* dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
 }
 
-// The k best of `lists` sorted lists (list l: num[l] entries at l * pitch) by
-// score, equal ones by position; entry e goes to put(rank, e).  Its rank is its
-// place in its own list and, by bisection, in every other.
-template <typename Put>
-__device__ __forceinline__ void merge_lists(u64* score, const long long* pos, const int* num, int lists, int pitch, int k,
-                                            Put put) {
-  const int all = lists * pitch;
-  if (all <= kCount) {  // (above about 500 entries bisection is faster than counting)
+// The k best of up to 32 sorted lists (list l: num[l] entries at l * pitch) by
+// score, equal ones by position, one after the other by a warp whose lanes hold the
+// lists' heads and the entries behind them: about 100 cycles each, whatever the lists
+// hold.  (Every entry's rank by comparing it with all others: as fast up to 64
+// entries, 40 thousand cycles for 500; 23 x 7 x 52472 fp32 logits, k = 62, took 99 us
+// with it, 50 so.)  The rank-th best is entry order[rank].  A list's own order is that
+// of its row's logits, which stands where two scores agree in fp64.
+__device__ __forceinline__ void merge_lists(const u64* score, const long long* pos, const int* num, int lists, int pitch,
+                                            int k, uint16_t* order) {
+  const int lane = threadIdx.x & 31, end = lane < lists ? lane * pitch + num[lane] : 0;
+  int e = lane < lists ? lane * pitch : 0;
+  u64 head = e < end ? score[e] : 0, next = e + 1 < end ? score[e + 1] : 0;  // 0: below every score
 #pragma unroll 1
-    for (int e = threadIdx.x; e < all + (all & 1); e += kThreads)
-      if (e == all || e % pitch >= num[e / pitch]) score[e] = 0;  // below every score
-    __syncthreads();
-    // as many threads an entry as there are (a power of two, within a warp)
-    int group = 1;
-#pragma unroll 1
-    while (group < 32 && 2 * group * all <= kThreads) group *= 2;
-    const int sub = threadIdx.x % group;
-#pragma unroll 1
-    for (int e0 = 0; e0 < all; e0 += kThreads / group) {
-      const int e = e0 + threadIdx.x / group;
-      const u64 s = e < all ? score[e] : 0;
-      int rank = 0;
-      if (s) {
-        const long long at = pos[e];
-#pragma unroll 4
-        for (int j = 2 * sub; j < all; j += 2 * group) {
-          const ulonglong2 x = *reinterpret_cast<const ulonglong2*>(score + j);
-          const longlong2 q = *reinterpret_cast<const longlong2*>(pos + j);
-          rank += (x.x > s || (x.x == s && q.x < at)) + (x.y > s || (x.y == s && q.y < at));
-        }
+  for (int rank = 0; rank < k; ++rank) {
+    const uint32_t high = __reduce_max_sync(~0u, (uint32_t)(head >> 32));
+    if (high == 0) break;  // no entry is left
+    bool best = (uint32_t)(head >> 32) == high;
+    uint32_t all = __ballot_sync(~0u, best);
+    if (all & (all - 1)) {
+      const uint32_t low = __reduce_max_sync(~0u, best ? (uint32_t)head : 0);
+      best = best && (uint32_t)head == low;
+      all = __ballot_sync(~0u, best);
+      if (all & (all - 1)) {
+        const u64 at = best ? (u64)pos[e] : ~0ull;
+        const uint32_t w = __reduce_min_sync(~0u, (uint32_t)(at >> 32));
+        best = best && (uint32_t)(at >> 32) == w;
+        const uint32_t t = __reduce_min_sync(~0u, best ? (uint32_t)at : ~0u);
+        best = best && (uint32_t)at == t;
       }
-#pragma unroll 1
-      for (int d = group / 2; d; d >>= 1) rank += __shfl_xor_sync(~0u, rank, d);
-      if (s && sub == 0 && rank < k) put(rank, e);
     }
-    return;
-  }
-  int top = 1;  // the highest power of two up to pitch
-  while (2 * top <= pitch) top *= 2;
-#pragma unroll 1
-  for (int e = threadIdx.x; e < all; e += kThreads) {
-    const int l = e / pitch, j = e % pitch;
-    if (j >= num[l]) continue;
-    const u64 s = score[e];
-    const long long at = pos[e];
-    int rank = j;
-#pragma unroll 1
-    for (int m0 = 0; m0 < lists && rank < k; m0 += 4) {
-      int below[4] = {0, 0, 0, 0};  // entries of four lists that come before
-#pragma unroll 1
-      for (int step = top; step; step >>= 1) {
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const int m = min(m0 + u, lists - 1), f = m * pitch + below[u] + step - 1;
-          if (below[u] + step <= num[m] && (score[f] > s || (score[f] == s && pos[f] < at))) below[u] += step;
-        }
-      }
-#pragma unroll
-      for (int u = 0; u < 4; ++u) rank += m0 + u < lists && m0 + u != l ? below[u] : 0;
+    if (best) {
+      order[rank] = (uint16_t)e;
+      ++e;
+      head = next;
+      next = e + 1 < end ? score[e + 1] : 0;
     }
-    if (rank < k) put(rank, e);
   }
 }
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 2) mla_beam_select_kernel(const BeamParams p) {
-  extern __shared__ __align__(16) uint8_t beam_smem[];
-  Smem& sm = *reinterpret_cast<Smem*>(beam_smem);
+  Smem& sm = shared();
   const int tid = threadIdx.x, warp = tid >> 5;
   const uint32_t rank = cluster_ctarank();
   const int cluster = p.cluster, parts = p.parts;  // parts of a row in a CTA
@@ -517,7 +498,7 @@ __global__ void __launch_bounds__(kThreads, 2) mla_beam_select_kernel(const Beam
     s_low += (s - (t - back)) + (x - back);
     s = t;
     uint16_t* tops = sm.tops[warp];
-    u64* list = sm.list + (at.g / step * kWarps + warp) * k;
+    const int l = (uint32_t)at.g / (uint32_t)step * kWarps + warp;  // the part's list
     tops[tiles++ * 32 + lane] = (uint16_t)(ordered(top) >> 16);
     if (tiles == kEpoch || at.last()) {
       // the largest of every second vector do for few (10.6 us of one request's
@@ -564,7 +545,7 @@ __global__ void __launch_bounds__(kThreads, 2) mla_beam_select_kernel(const Beam
           if (i0 + i >= pairs) break;
           if (n + 32 * kMine > kCap) {
             // No room for whatever comes: the best so far are selected exactly.
-            n = select(buf, n, k, list, &floor);
+            n = select(l, n, k, &floor);
             limit = max(limit, floor);
             selected = true;
           }
@@ -581,7 +562,7 @@ __global__ void __launch_bounds__(kThreads, 2) mla_beam_select_kernel(const Beam
       }
       __syncwarp();
       if (selected) {  // later tiles' values have to be greater than the last of the best
-        n = select(buf, n, k, list, &floor);
+        n = select(l, n, k, &floor);
         if (n == k) limit = max(limit, floor + 1);
       }
       tiles = 0;
@@ -591,13 +572,13 @@ __global__ void __launch_bounds__(kThreads, 2) mla_beam_select_kernel(const Beam
       continue;
     }
     // the part's end
-    n = best_keys(buf, n, k, floor, list);
+    n = best_keys(l, n, k, floor);
     const float wm = unordered(__reduce_max_sync(~0u, ordered(m)));
     s = (s + s_low) * ex2((wm > -INFINITY ? m - wm : 0.f) * kLog2e);
 #pragma unroll
     for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(~0u, s, d);
     if (lane == 0) {
-      sm.num[at.g / step * kWarps + warp] = n;
+      sm.num[l] = n;
       sm.stat[at.g] = make_float2(wm, s);
     }
     at.enter(p, sm.live, b, len, at.g + step);
@@ -673,19 +654,18 @@ __global__ void __launch_bounds__(kThreads, 2) mla_beam_select_kernel(const Beam
   __syncthreads();
   const uint32_t to_score = mapa(smem_u32(sm.got_score + rank * k), 0);
   const uint32_t to_pos = mapa(smem_u32(sm.got_pos + rank * k), 0);
-  merge_lists(sm.list, sm.pos, sm.num, lists, k, k, [&](int at, int e) {
+  const int sum = min(__reduce_add_sync(~0u, lane < lists ? sm.num[lane] : 0), k);
+  if (warp == 0) merge_lists(sm.list, sm.pos, sm.num, lists, k, k, sm.order);
+  __syncthreads();
+  if (tid < sum) {
+    const int e = sm.order[tid];
     const u64 a = sm.list[e], q = (u64)sm.pos[e];
-    st_cluster_u32(to_score + 8 * at, (uint32_t)a);
-    st_cluster_u32(to_score + 8 * at + 4, (uint32_t)(a >> 32));
-    st_cluster_u32(to_pos + 8 * at, (uint32_t)q);
-    st_cluster_u32(to_pos + 8 * at + 4, (uint32_t)(q >> 32));
-  });
-  if (tid == 0) {
-    int sum = 0;
-#pragma unroll 1
-    for (int l = 0; l < lists; ++l) sum += sm.num[l];
-    st_cluster_u32(mapa(smem_u32(sm.got_num + rank), 0), (uint32_t)min(sum, k));
+    st_cluster_u32(to_score + 8 * tid, (uint32_t)a);
+    st_cluster_u32(to_score + 8 * tid + 4, (uint32_t)(a >> 32));
+    st_cluster_u32(to_pos + 8 * tid, (uint32_t)q);
+    st_cluster_u32(to_pos + 8 * tid + 4, (uint32_t)(q >> 32));
   }
+  if (tid == 0) st_cluster_u32(mapa(smem_u32(sm.got_num + rank), 0), (uint32_t)sum);
   cluster_sync();
   if (rank != 0) return;
   const auto put = [&](int at, float s, int w, int t) {
@@ -693,15 +673,16 @@ __global__ void __launch_bounds__(kThreads, 2) mla_beam_select_kernel(const Beam
     p.parents[b * k + at] = (int)(b * W + w);
     p.tokens[b * k + at] = t;
   };
-  int have = 0;
-#pragma unroll 1
-  for (int c = 0; c < cluster; ++c) have += sm.got_num[c];
+  int have = __reduce_add_sync(~0u, lane < cluster ? sm.got_num[lane] : 0);
   have = min(have, k);
-  merge_lists(sm.got_score, sm.got_pos, sm.got_num, cluster, k, k, [&](int at, int e) {
+  if (warp == 0) merge_lists(sm.got_score, sm.got_pos, sm.got_num, cluster, k, k, sm.order);
+  __syncthreads();
+  if (tid < have) {
+    const int e = sm.order[tid];
     const long long q = sm.got_pos[e];
-    put(at, (float)unordered(sm.got_score[e]), (int)(q >> 32), (int)(uint32_t)q);
-    sm.member[at] = (q >> 32) * V + (uint32_t)q;
-  });
+    put(tid, (float)unordered(sm.got_score[e]), (int)(q >> 32), (int)(uint32_t)q);
+    sm.member[tid] = (q >> 32) * V + (uint32_t)q;
+  }
   // Fewer than k continuations: the lowest positions that are none, at -inf.
   __syncthreads();
   if (tid < k - have) {
