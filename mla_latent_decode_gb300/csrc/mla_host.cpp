@@ -189,8 +189,8 @@ namespace mla {
 // Plan of mla_prefill with blocks of 128 rows (one CTA, two of them an SM) or 512
 // (a pair of CTAs).  Costs in key tiles of a single CTA with another beside it (about
 // 2 us), from times of both forms: 8191 tokens x 96 heads 1428 us on single CTAs and
-// 1215 on pairs, 24 prompts of 100 to 6000 tokens x 16 heads 508 and 480, 64 documents
-// of 33 to 700 tokens x 96 heads 349 and 580.  A tile of a pair, what a block takes
+// 1215 on pairs, 24 prompts of 100 to 6000 tokens x 16 heads 508 and 462, 64 documents
+// of 33 to 700 tokens x 96 heads 349 and 558.  A tile of a pair, what a block takes
 // besides its tiles, and the merging launch with its rows.
 struct PrefillPlan {
   int ctas = 1;

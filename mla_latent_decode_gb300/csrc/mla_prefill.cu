@@ -22,7 +22,7 @@
 // of keys and values a tile come in through a ring of 64 KB, so a tile waits for loads
 // that are issued as the one before is used up: 64 documents of 33 to 700 tokens x 96
 // heads 344 us, 1.62 GB moved, 70% of the copy rate.  A block of 512 rows of a short
-// sequence would mostly be padding (580 us).
+// sequence would mostly be padding (558 us).
 //
 //   softmax warps    4 a row tile, one thread per row, then O / l
 //   TMA warp         K and V through the ring; on one CTA Q (48 KB) too
