@@ -86,6 +86,8 @@ struct Smem {
   u64 list[kMaxLists * kMaxK];              // the parts' best in order; later: their scores
   float2 stat[kMaxParts];                   // (max, sum) of the cluster's parts
   double lse[kMaxW];
+  float2 row[kMaxW];                        // (max, sum) of the beams' rows
+  int like[kMaxW];                          // the first row with the same sum
   int num[kMaxLists];                       // entries of a list
   int ends[kMaxW];                          // a finished beam's end counts
   int got_num[kMaxCluster];
@@ -628,6 +630,7 @@ __global__ void __launch_bounds__(kThreads, 2) mla_beam_select_kernel(const Beam
       const bool done = p.finished && p.finished[b * W + w];
       // an infinite or undefined logit: no continuation of this beam counts
       const bool whole = sum.hi > 0 && sum.hi < INFINITY && fabsf(m) < INFINITY;
+      sm.row[w] = make_float2(m, sum.hi);
       sm.lse[w] = whole ? (double)m + log_of(sum) : INFINITY;
       sm.ends[w] = done && fabsf(c) < INFINITY;  // its end, at its score
       if (rank == 0 && p.status && (!(c < INFINITY) || (!done && (sum.hi != sum.hi || m == INFINITY))))
@@ -635,6 +638,19 @@ __global__ void __launch_bounds__(kThreads, 2) mla_beam_select_kernel(const Beam
     }
   }
   __syncthreads();
+  // Rows of equal values have equal scores, and the lowest row's go first; but where
+  // they start at other places modulo 16 bytes their values meet in another order.  A
+  // term errs by 2^-22, by as much for each of the few times that its lane's maximum
+  // rises, and by its exponent's error, of which up to about 24 halvings matter and
+  // 2^-24 of them at the subtraction and at the multiplication: sums of rows with the
+  // same maximum that differ by less than 2 (2^-22 + 2 x 24 x 2^-24 ln 2), doubled for
+  // the rises, are taken as one: 2^-17 (a score is off by that at most).
+#pragma unroll 1
+  for (int w = warp; w < W; w += kWarps) {
+    const float2 x = sm.row[w], y = sm.row[min(lane, w)];
+    const uint32_t like = __ballot_sync(~0u, lane == w || (lane < w && y.x == x.x && fabsf(y.y - x.y) <= x.y * 0x1p-17f));
+    if (lane == 0) sm.like[w] = __ffs(like) - 1;
+  }
   if (tid < lists && own(tid) < all) {
     const int w = own(tid) / parts;
     if (sm.ends[w]) sm.num[tid] = own(tid) % parts == 0;
@@ -649,7 +665,7 @@ __global__ void __launch_bounds__(kThreads, 2) mla_beam_select_kernel(const Beam
     const u64 key = sm.list[e];
     const bool end = sm.ends[w];
     sm.pos[e] = (long long)w << 32 | (end ? (uint32_t)p.end_token : (uint32_t)~(uint32_t)key);
-    sm.list[e] = ordered(end ? c : c + ((double)unordered((uint32_t)(key >> 32)) - sm.lse[w]));
+    sm.list[e] = ordered(end ? c : c + ((double)unordered((uint32_t)(key >> 32)) - sm.lse[sm.like[w]]));
   }
   __syncthreads();
   const uint32_t to_score = mapa(smem_u32(sm.got_score + rank * k), 0);
@@ -699,8 +715,24 @@ __global__ void __launch_bounds__(kThreads, 2) mla_beam_select_kernel(const Beam
   }
 }
 
-// CTAs of a request: as many as find room at once (two an SM), while a warp has
-// about a tile of logits.  Parts of a row: the number whose rounds over the cluster's
+// Clusters of a size that the device holds at once, asked of each device once (fewer
+// than its places for CTAs divide into: a GPC's SMs leave a rest).
+template <typename T>
+int clusters_at_once(cudaLaunchConfig_t cfg, int dev, int* n) {
+  static std::atomic<int> known[64][kMaxCluster + 1];
+  const int size = (int)cfg.attrs->val.clusterDim.x;
+  *n = dev < 64 ? known[dev][size].load() : 0;
+  if (*n) return MLA_OK;
+  const cudaError_t e = cudaOccupancyMaxActiveClusters(n, mla_beam_select_kernel<T>, &cfg);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaOccupancyMaxActiveClusters");
+  if (dev < 64) known[dev][size].store(*n);
+  return MLA_OK;
+}
+
+// CTAs of a request: as many as all find room at once (two an SM; a second round of
+// clusters costs more than it brings: 60 x 8 x 131072 bf16 took 53 us with clusters of
+// 5, 37 with 4; 76 requests 60 with 4, 45 with 3), while a warp has about a tile of
+// logits.  Parts of a row: the number whose rounds over the cluster's
 // warps cost least, a part its tiles and about three more.
 template <typename T>
 int launch_beam(BeamParams p, int B, cudaStream_t st) {
@@ -711,27 +743,32 @@ int launch_beam(BeamParams p, int B, cudaStream_t st) {
   if (rc == MLA_OK) rc = allow_shared(kernel, (int)sizeof(Smem), dev, set_on, "cudaFuncSetAttribute(mla_beam_select_kernel)");
   if (rc != MLA_OK) return rc;
   constexpr int kTile = 32 * kVecs * Type<T>::kPer;
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.dynamicSmemBytes = sizeof(Smem);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
   p.cluster = p.W > kMaxLists ? 2 : 1;
-  while (p.cluster < kMaxCluster && (int64_t)B * p.cluster * 2 <= 2 * sms &&
-         (int64_t)p.W * p.V > (int64_t)p.cluster * kWarps * kTile / 2)
-    p.cluster *= 2;
+  for (int c = p.cluster + 1; c <= kMaxCluster && (int64_t)B * c <= 2 * sms &&
+                              (int64_t)p.W * p.V > (int64_t)(c - 1) * kWarps * kTile / 2; ++c) {
+    int at_once = 0;
+    cfg.gridDim = dim3((unsigned)c, 1, 1);
+    attr[0].val.clusterDim.x = (unsigned)c;
+    if ((rc = clusters_at_once<T>(cfg, dev, &at_once)) != MLA_OK) return rc;
+    if (B <= at_once) p.cluster = c;
+  }
   double least = 0;
   for (int parts = 1; p.W * parts <= std::max(2 * p.cluster * kWarps, p.W) && p.W * parts <= kMaxParts; ++parts) {
     const int rounds = (p.W * parts + p.cluster * kWarps - 1) / (p.cluster * kWarps);
     const double cost = rounds * (double)(p.V / parts / kTile + 4);
     if (parts == 1 || cost < least) least = cost, p.parts = parts;
   }
-  cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(B * p.cluster), 1, 1);
-  cfg.blockDim = dim3(kThreads, 1, 1);
-  cfg.dynamicSmemBytes = sizeof(Smem);
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = (unsigned)p.cluster;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, p);
   if (e != cudaSuccess) return cuda_fail(e, "launch mla_beam_select_kernel");
   return MLA_OK;

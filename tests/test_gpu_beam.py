@@ -114,6 +114,16 @@ def test_many_rows_a_warp(B, W):
     _check(logits, scores, 40)
 
 
+@pytest.mark.parametrize("B", [37, 45, 57, 79, 120])
+def test_clusters_of_every_size(B):
+    # eight CTAs a request down to two, by how many requests there are
+    logits, scores = _inputs(B, 3, 24001, torch.float16, seed=B)
+    logits[B // 2] = logits[B // 2].round()  # ties across the CTAs' parts
+    logits[B // 3] = logits[B // 3, :1]
+    scores[B // 3] = 0
+    _check(logits, scores, 33)
+
+
 def test_rows_at_odd_addresses():
     logits, scores = _inputs(2, 3, 1200)
     for off in (1, 3, 5):
