@@ -184,7 +184,6 @@ struct Type;
 template <>
 struct Type<float> {
   static constexpr int kPer = 4;
-  static __device__ __forceinline__ uint32_t second(float x) { return __float_as_uint(x); }
   static __device__ __forceinline__ float at(const uint4& v, int j) {
     return __uint_as_float(j == 0 ? v.x : j == 1 ? v.y : j == 2 ? v.z : v.w);
   }
@@ -197,7 +196,6 @@ struct Type<float> {
 template <>
 struct Type<__nv_bfloat16> {
   static constexpr int kPer = 8;
-  static __device__ __forceinline__ uint32_t second(__nv_bfloat16 x) { return (uint32_t)__bfloat16_as_ushort(x) << 16 | (kNone & 0xffffu); }
   static __device__ __forceinline__ float at(const uint4& v, int j) {
     const uint32_t w = j < 2 ? v.x : j < 4 ? v.y : j < 6 ? v.z : v.w;
     return __uint_as_float(j & 1 ? w & 0xffff0000u : w << 16);
@@ -214,7 +212,6 @@ struct Type<__nv_bfloat16> {
 template <>
 struct Type<__half> {
   static constexpr int kPer = 8;
-  static __device__ __forceinline__ uint32_t second(__half x) { return (uint32_t)__half_as_ushort(x) << 16 | (kNone & 0xffffu); }
   static __device__ __forceinline__ float at(const uint4& v, int j) {
     const uint32_t w = j < 2 ? v.x : j < 4 ? v.y : j < 6 ? v.z : v.w;
     const __half2 h = *reinterpret_cast<const __half2*>(&w);
@@ -523,43 +520,44 @@ __global__ void __launch_bounds__(kThreads, 2) mla_beam_select_kernel(const Beam
         __syncwarp();
       }
       // their values: the last tile's are at hand, others are read again
-      constexpr int kAtOnce = 8, kMine = kPer / 4;  // a lane's values (4 bytes) of a pair's tile
+      constexpr int kAtOnce = 32 / kVecs, kAhead = 1;  // pairs a step (a vector a lane), steps read ahead
       bool selected = false;
+      const auto place = [&](int i) {  // of the lane's vector, from the last tile's first value
+        const int pair = tops[min(i + lane / kVecs, pairs - 1)];
+        return ((pair >> 5) + 1 - tiles) * Walk<T>::kTile + (lane % kVecs * 32 + (pair & 31)) * kPer;
+      };
+      const uint4 none = make_uint4(Type<T>::kNone, Type<T>::kNone, Type<T>::kNone, Type<T>::kNone);
+      uint4 y[kAhead + 1];
 #pragma unroll 1
-      for (int i0 = 0; i0 < pairs; i0 += kAtOnce) {
-        uint32_t y[kAtOnce];
-        const auto place = [&](int i) {  // of the first value, from the last tile's first
-          const int pair = tops[min(i0 + i, pairs - 1)];
-          return ((pair >> 5) + 1 - tiles) * Walk<T>::kTile + ((lane >> 2) * 32 + (pair & 31)) * kPer + (lane & 3) * kMine;
-        };
+      for (int i = -kAhead * kAtOnce; i < pairs; i += kAtOnce) {
 #pragma unroll
-        for (int i = 0; i < kAtOnce; ++i) {
-          const int in = place(i);
+        for (int j = 0; j < kAhead; ++j) y[j] = y[j + 1];
+        y[kAhead] = none;
+        const int ahead = i + kAhead * kAtOnce;
+        if (ahead + lane / kVecs < pairs) {
+          const int in = place(ahead);
           const int64_t e = at.t0 + in;
-          y[i] = Type<T>::kNone;
-          if (i0 + i >= pairs || lane >= 4 * kVecs) continue;
-          if (in >= 0) y[i] = *reinterpret_cast<const uint32_t*>(reinterpret_cast<const T*>(&sm.tile[warp][stage][0][0]) + in);
-          else if (e >= at.lo) y[i] = *reinterpret_cast<const uint32_t*>(at.row + e);
-          else if (e + kMine > at.lo) y[i] = Type<T>::second(at.row[e + kMine - 1]);  // a row that starts inside the word
+          if (in >= 0) y[kAhead] = *reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(&sm.tile[warp][stage][0][0]) + in);
+          else if (e >= at.lo) y[kAhead] = *reinterpret_cast<const uint4*>(at.row + e);
+          else if (e + kPer > at.lo) y[kAhead] = load_edge<T>(at.row, e, at.lo, at.hi);
         }
+        if (i < 0) continue;
+        const float least = unordered(limit);
+        const uint32_t where = ~(uint32_t)(at.t0 + place(i));
+        uint32_t hits[kPer];
 #pragma unroll
-        for (int i = 0; i < kAtOnce; ++i) {
-          if (i0 + i >= pairs) break;
-          if (n + 32 * kMine > kCap) {
+        for (int j = 0; j < kPer; ++j) hits[j] = __ballot_sync(~0u, Type<T>::at(y[0], j) >= least);
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) {
+          if (n + 32 > kCap) {
             // No room for whatever comes: the best so far are selected exactly.
             n = select(l, n, k, &floor);
             limit = max(limit, floor);
             selected = true;
           }
-#pragma unroll
-          for (int j = 0; j < kMine; ++j) {
-            const float x = Type<T>::at(make_uint4(y[i], 0, 0, 0), j);
-            const bool in = x >= unordered(limit);
-            const uint32_t all = __ballot_sync(~0u, in);
-            if (in)
-              buf[n + __popc(all & ((1u << lane) - 1))] = (u64)ordered(x) << 32 | ~(uint32_t)(at.t0 + place(i) + j);
-            n += __popc(all);
-          }
+          if (hits[j] >> lane & 1)
+            buf[n + __popc(hits[j] & ((1u << lane) - 1))] = (u64)ordered(Type<T>::at(y[0], j)) << 32 | (where - j);
+          n += __popc(hits[j]);
         }
       }
       __syncwarp();
