@@ -354,43 +354,109 @@ __device__ __forceinline__ void cp_async16(void* dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
 }
 
-// The k best of up to 32 sorted lists (list l: num[l] entries at l * pitch) by
-// score, equal ones by position, one after the other by a warp whose lanes hold the
-// lists' heads and the entries behind them: about 100 cycles each, whatever the lists
-// hold.  (Every entry's rank by comparing it with all others: as fast up to 64
-// entries, 40 thousand cycles for 500; 23 x 7 x 52472 fp32 logits, k = 62, took 99 us
-// with it, 50 so.)  The rank-th best is entry order[rank].  A list's own order is that
-// of its row's logits, which stands where two scores agree in fp64.
-__device__ __forceinline__ void merge_lists(const u64* score, const long long* pos, const int* num, int lists, int pitch,
-                                            int k, uint16_t* order) {
-  const int lane = threadIdx.x & 31, end = lane < lists ? lane * pitch + num[lane] : 0;
-  int e = lane < lists ? lane * pitch : 0;
-  u64 head = e < end ? score[e] : 0, next = e + 1 < end ? score[e + 1] : 0;  // 0: below every score
+struct Entry {
+  u64 score, pos;
+  __device__ __forceinline__ bool before(const Entry& o) const {
+    return score > o.score || (score == o.score && pos < o.pos);
+  }
+};
+
+// The k best of sorted lists (list l: num[l] entries at l * k) by score, equal ones by
+// position: the i-th of them is entry order[i].  Returns their number.
+//
+// Few: one after the other by a warp whose lanes hold the lists' heads and the entries
+// behind them, about 200 cycles each.  From kTree on: two lists' into the first of
+// them, until all are in list 0; k (a power of two from it on) by the greater of one
+// list's entries and the other's from its end, which rise and fall, and a warp sorts
+// them by halves.  1 x 4 x 32000, k = 8: 11.0 us by heads, 11.5 by pairs; 16 x 5 x
+// 100003, k = 10: 20.9 and 21.8; 2 x 7 x 2208, k = 14: 13.8 and 12.9; 23 x 7 x 52472,
+// k = 62: 43 and 36 (and 92 with every entry compared with all others).
+// A list's own order is that of its row's logits, which stands where two scores agree
+// in fp64.
+constexpr int kTree = 12;
+__device__ __noinline__ int merge_lists(u64* score, long long* pos, int* num, int lists, int k, uint16_t* order) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (k < kTree) {
+    static_assert(kMaxLists <= 32 && kMaxCluster <= 32, "a list a lane");
+    const int sum = min(__reduce_add_sync(~0u, lane < lists ? num[lane] : 0), k);
+    if (warp == 0) {
+      int e = lane < lists ? lane * k : 0;
+      const int end = lane < lists ? e + num[lane] : 0;
+      u64 head = e < end ? score[e] : 0, next = e + 1 < end ? score[e + 1] : 0;  // 0: below every score
 #pragma unroll 1
-  for (int rank = 0; rank < k; ++rank) {
-    const uint32_t high = __reduce_max_sync(~0u, (uint32_t)(head >> 32));
-    if (high == 0) break;  // no entry is left
-    bool best = (uint32_t)(head >> 32) == high;
-    uint32_t all = __ballot_sync(~0u, best);
-    if (all & (all - 1)) {
-      const uint32_t low = __reduce_max_sync(~0u, best ? (uint32_t)head : 0);
-      best = best && (uint32_t)head == low;
-      all = __ballot_sync(~0u, best);
-      if (all & (all - 1)) {
-        const u64 at = best ? (u64)pos[e] : ~0ull;
-        const uint32_t w = __reduce_min_sync(~0u, (uint32_t)(at >> 32));
-        best = best && (uint32_t)(at >> 32) == w;
-        const uint32_t t = __reduce_min_sync(~0u, best ? (uint32_t)at : ~0u);
-        best = best && (uint32_t)at == t;
+      for (int i = 0; i < sum; ++i) {
+        const uint32_t high = __reduce_max_sync(~0u, (uint32_t)(head >> 32));
+        bool best = (uint32_t)(head >> 32) == high;
+        uint32_t all = __ballot_sync(~0u, best);
+        if (all & (all - 1)) {
+          const uint32_t low = __reduce_max_sync(~0u, best ? (uint32_t)head : 0);
+          best = best && (uint32_t)head == low;
+          all = __ballot_sync(~0u, best);
+          if (all & (all - 1)) {
+            const u64 at = best ? (u64)pos[e] : ~0ull;
+            const uint32_t w = __reduce_min_sync(~0u, (uint32_t)(at >> 32));
+            best = best && (uint32_t)(at >> 32) == w;
+            const uint32_t t = __reduce_min_sync(~0u, best ? (uint32_t)at : ~0u);
+            best = best && (uint32_t)at == t;
+          }
+        }
+        if (best) {
+          order[i] = (uint16_t)e;
+          ++e;
+          head = next;
+          next = e + 1 < end ? score[e + 1] : 0;
+        }
       }
     }
-    if (best) {
-      order[rank] = (uint16_t)e;
-      ++e;
-      head = next;
-      next = e + 1 < end ? score[e + 1] : 0;
-    }
+    __syncthreads();
+    return sum;
   }
+  static_assert(kMaxK <= 64 && kMaxLists <= 2 * kWarps && kMaxCluster <= 2 * kWarps, "two entries a lane, two lists a warp");
+  if (threadIdx.x < k) order[threadIdx.x] = (uint16_t)threadIdx.x;
+  const int all = 1 << (32 - __clz(k - 1));
+#pragma unroll 1
+  for (int n = lists; n > 1; n = (n + 1) / 2) {
+    const int half = (n + 1) / 2;
+    if (warp + half < n && num[warp + half] > 0) {
+      const int a = warp, b = warp + half, na = num[a], nb = num[b], sum = min(na + nb, k);
+      Entry x[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int i = lane + 32 * h, j = all - 1 - i;
+        x[h] = {0, ~0ull};  // behind every entry
+        if (i < na) x[h] = {score[a * k + i], (u64)pos[a * k + i]};
+        if (j >= 0 && j < nb) {
+          const Entry y = {score[b * k + j], (u64)pos[b * k + j]};
+          if (y.before(x[h])) x[h] = y;
+        }
+      }
+      if (all == 64 && x[1].before(x[0])) {
+        const Entry y = x[0];
+        x[0] = x[1];
+        x[1] = y;
+      }
+#pragma unroll 1
+      for (int d = min(all, 32) / 2; d; d /= 2) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (h == 1 && all < 64) break;
+          const Entry y = {__shfl_xor_sync(~0u, x[h].score, d), __shfl_xor_sync(~0u, x[h].pos, d)};
+          if (((lane & d) == 0) != x[h].before(y)) x[h] = y;
+        }
+      }
+      __syncwarp();
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int i = lane + 32 * h;
+        if (i >= sum) break;
+        score[a * k + i] = x[h].score;
+        pos[a * k + i] = (long long)x[h].pos;
+      }
+      if (lane == 0) num[a] = sum;
+    }
+    __syncthreads();
+  }
+  return num[0];
 }
 
 template <typename T>
@@ -668,9 +734,7 @@ __global__ void __launch_bounds__(kThreads, 2) mla_beam_select_kernel(const Beam
   __syncthreads();
   const uint32_t to_score = mapa(smem_u32(sm.got_score + rank * k), 0);
   const uint32_t to_pos = mapa(smem_u32(sm.got_pos + rank * k), 0);
-  const int sum = min(__reduce_add_sync(~0u, lane < lists ? sm.num[lane] : 0), k);
-  if (warp == 0) merge_lists(sm.list, sm.pos, sm.num, lists, k, k, sm.order);
-  __syncthreads();
+  const int sum = merge_lists(sm.list, sm.pos, sm.num, lists, k, sm.order);
   if (tid < sum) {
     const int e = sm.order[tid];
     const u64 a = sm.list[e], q = (u64)sm.pos[e];
@@ -687,10 +751,7 @@ __global__ void __launch_bounds__(kThreads, 2) mla_beam_select_kernel(const Beam
     p.parents[b * k + at] = (int)(b * W + w);
     p.tokens[b * k + at] = t;
   };
-  int have = __reduce_add_sync(~0u, lane < cluster ? sm.got_num[lane] : 0);
-  have = min(have, k);
-  if (warp == 0) merge_lists(sm.got_score, sm.got_pos, sm.got_num, cluster, k, k, sm.order);
-  __syncthreads();
+  const int have = merge_lists(sm.got_score, sm.got_pos, sm.got_num, cluster, k, sm.order);
   if (tid < have) {
     const int e = sm.order[tid];
     const long long q = sm.got_pos[e];
