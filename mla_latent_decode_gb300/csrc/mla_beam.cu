@@ -81,7 +81,7 @@ struct Smem {
     };
   };
   u64 buf[kWarps][kCap + 2];                // candidates of the warps' parts at hand
-  uint32_t words[kWarps][32 * kTops];
+  uint32_t words[kWarps][64];
   uint16_t tops[kWarps][kEpoch * 32];       // lanes' largest values of the tiles, cut to 16 bits; later: pairs
   u64 list[kMaxLists * kMaxK];              // the parts' best in order; later: their scores
   float2 stat[kMaxParts];                   // (max, sum) of the cluster's parts
@@ -267,15 +267,17 @@ __device__ __noinline__ int best_keys(int l, int n, int k, uint32_t limit) {
   if (lane == 0) keys[m] = 0;  // (the buffer has room)
   __syncwarp();
 #pragma unroll 1
-  for (int i = lane; i < m; i += 32) {
-    const u64 mine = keys[i];
-    int rank = 0;
+  for (int i = lane; i < m; i += 64) {  // two a lane at once
+    const u64 one = keys[i], two = i + 32 < m ? keys[i + 32] : 0;
+    int above = 0, over = 0;
 #pragma unroll 4
     for (int j = 0; j < m; j += 2) {
       const ulonglong2 x = *reinterpret_cast<const ulonglong2*>(keys + j);
-      rank += (x.x > mine) + (x.y > mine);
+      above += (x.x > one) + (x.y > one);
+      over += (x.x > two) + (x.y > two);
     }
-    if (rank < k) out[rank] = mine;
+    if (above < k) out[above] = one;
+    if (i + 32 < m && over < k) out[over] = two;
   }
   __syncwarp();
   return min(m, k);
@@ -295,7 +297,7 @@ __device__ __noinline__ int select(int l, int n, int k, uint32_t* floor) {
 // The place in the order of the k-th largest of the lanes' kTops values: each is
 // compared with all of them, through shared memory.
 template <int kTops>
-__device__ __forceinline__ uint32_t kth_of(const float (&x)[kTops], int k, uint32_t* words) {
+__device__ __forceinline__ uint32_t kth_by_all(const float (&x)[kTops], int k, uint32_t* words) {
   const int lane = threadIdx.x & 31;
   uint32_t mine[kTops];
   int above[kTops];
@@ -318,6 +320,35 @@ __device__ __forceinline__ uint32_t kth_of(const float (&x)[kTops], int k, uint3
 #pragma unroll
   for (int i = 0; i < kTops; ++i) least = min(least, above[i] < k ? mine[i] : ~0u);
   return __reduce_min_sync(~0u, least);
+}
+
+// A place in the order that at least k of the lanes' kTops values reach, and no more
+// where that many can be told apart (kLeast if fewer are finite): by bisection, ten
+// steps of 60 cycles and more (32 where values tie; comparing all 128 takes 4000, all
+// 64 1100).
+template <int kTops>
+__device__ __forceinline__ uint32_t kth_of(const float (&x)[kTops], int k) {
+  uint32_t mine[kTops], least = ~0u, most = 0;
+  int n = 0;
+#pragma unroll
+  for (int i = 0; i < kTops; ++i) {
+    mine[i] = ordered(x[i]);
+    if (mine[i] >= kLeast) least = min(least, mine[i]);
+    most = max(most, mine[i]);
+    n += __popc(__ballot_sync(~0u, mine[i] >= kLeast));
+  }
+  if (n < k) return kLeast;
+  uint32_t lo = __reduce_min_sync(~0u, least), hi = __reduce_max_sync(~0u, most) + 1;  // hi: none reaches it
+#pragma unroll 1
+  while (hi - lo > 1 && n != k) {
+    const uint32_t mid = lo + (hi - lo) / 2;
+    n = 0;
+#pragma unroll
+    for (int i = 0; i < kTops; ++i) n += __popc(__ballot_sync(~0u, mine[i] >= mid));
+    if (n >= k) lo = mid;
+    else hi = mid;
+  }
+  return lo;
 }
 
 // A warp's way through its parts of rows, tile by tile; parts of which nothing
@@ -570,9 +601,9 @@ __global__ void __launch_bounds__(kThreads, 2) mla_beam_select_kernel(const Beam
       // beams against 12.5), for k near 64 hardly anything would lie below them
       if (k <= 24) {
         const float two[2] = {fmaxf(a[0], a[2]), fmaxf(a[1], a[3])};
-        floor = max(floor, kth_of(two, k, sm.words[warp]));
+        floor = max(floor, kth_by_all(two, k, sm.words[warp]));
       } else {
-        floor = max(floor, kth_of(a, k, sm.words[warp]));
+        floor = max(floor, kth_of(a, k));
       }
       limit = max(limit, floor);
       // lanes and tiles with a value that reaches it, in place
