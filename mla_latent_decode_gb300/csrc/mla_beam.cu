@@ -16,12 +16,13 @@
 // that at least k values of the part reach, and few more do (about k ln k for values
 // in random order).  While tiles pass only each lane's largest value of each is kept;
 // after 32 of them, or at the part's end, the bound is found and the few lanes' tiles
-// that reach it are read again (for k = 16 about 20 times 128 bytes of 128 KB).  Where
+// that reach it are read again (for k = 16 about 20 times 128 bytes of 128 KB), four
+// of them at a time, a vector a lane.  Where
 // too many reach it (ties) the best k so far are selected exactly, and later values
 // have to exceed the last of them.
 //
-// Measured: 64 requests x 16 beams x 131072 bf16 logits, a tenth finished (241 MB) 57 us,
-// 62% of the copy rate: the 256 CTAs are two on 104 SMs and one on 48, and a tile's
+// Measured: 64 requests x 16 beams x 131072 bf16 logits, a tenth finished (241 MB) 55 us,
+// 65% of the copy rate: the 256 CTAs are two on 104 SMs and one on 48, and a tile's
 // arithmetic (3.6 instructions a logit) takes as long as its bytes.  Candidates looked
 // for tile by tile took 65 us, tiles in registers 165, a CTA a row with its barriers 215.
 //

@@ -16,12 +16,12 @@
 // then, and S may overwrite P.
 //
 // What bounds it (GB300).  Pairs: the tensor cores under the power cap, one prompt of
-// 8191 tokens x 96 heads (2.06 PFLOP) in 1192 us, 1.73 PFLOP/s, 91% of the measured burst
+// 8191 tokens x 96 heads (2.06 PFLOP) in 1174 us, 1.75 PFLOP/s, 92% of the measured burst
 // and all of the measured sustained rate, tensor pipe active 78% of the cycles; each SM
 // loads and reads half of every K and V tile (40 KB).  On single CTAs a row tile's 80 KB
 // of keys and values a tile come in through a ring of 64 KB, so a tile waits for loads
 // that are issued as the one before is used up: 64 documents of 33 to 700 tokens x 96
-// heads 344 us, 1.62 GB moved, 70% of the copy rate.  A block of 512 rows of a short
+// heads 343 us, 1.62 GB moved, 70% of the copy rate.  A block of 512 rows of a short
 // sequence would mostly be padding (558 us).
 //
 //   softmax warps    4 a row tile, one thread per row, then O / l
