@@ -143,6 +143,15 @@ def test_ties_go_to_the_lowest_position():
     _check(logits, torch.zeros_like(scores), 16)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("W,V,scale", [(32, 1003, 0.1), (7, 24001, 1.0), (3, 131071, 3.0), (9, 333, 30.0)])
+def test_equal_rows_that_start_anywhere(W, V, scale, dtype):
+    row = (scale * torch.randn(V, generator=torch.Generator().manual_seed(V))).to(dtype)
+    row[V // 2] = row.max()                             # equal values within a row, too
+    logits = row.expand(2, W, V).contiguous().cuda()
+    _check(logits, torch.full((2, W), -2.0, device="cuda"), 50)
+
+
 @pytest.mark.parametrize("descending", [False, True])
 def test_sorted_vocabularies(descending):
     """Every value above those before it, or all the best in a few threads' hands."""
