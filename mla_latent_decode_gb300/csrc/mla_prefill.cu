@@ -146,10 +146,11 @@ struct Unit {
 
 // Notes on cleaned values: per kind (NaN, +inf, -inf) and dim the first such token,
 // counted from the unit's first unseen one (below the unit's rows).  Kept apart
-// from those of earlier units: in a pair by a tag that falls from unit to unit, so
-// that one minimum replaces older notes; on one CTA, which has less shared memory,
-// all of a dim's in one word under a tag that comes again after 127 units, the
-// notes being wiped in between.
+// from those of earlier units by a tag of the unit's number among the CTA's cleaned
+// ones (`nth`, counted alike by the warps that clean and those that read): in a pair
+// one that falls, so that one minimum replaces older notes; on one CTA, which has less
+// shared memory, all of a dim's in one word under a tag that comes again after 127
+// cleaned units, the notes being wiped in between.
 template <int kCtas>
 struct Notes;
 template <>
@@ -208,7 +209,7 @@ struct Ctl {
   uint32_t note;                      // where a peer's asynchronous stores go
   uint32_t tmem;
   int abort_flag;
-  uint32_t any_odd;                   // the last unit with notes, counted from 1
+  uint32_t any_odd;                   // the last cleaned unit with notes, counted from 1
   Notes<kCtas> notes;
 };
 template <int kCtas>
@@ -689,12 +690,17 @@ __device__ __forceinline__ void clean_values(uint8_t* base, Ctl<kCtas>& c, const
   constexpr int kBatch = 8, kVecs = kBox / 16;  // 16-byte vectors: in flight per lane, of a job
   Units<kCtas> units(c);
   bool ok = true;
-  uint32_t at = 0, cleans = 0;  // pieces and cleaned tiles so far
+  uint32_t at = 0, cleans = 0, turn = 0;  // pieces, cleaned tiles and cleaned units so far
   while (const Unit* u = units.next(ok)) {
     const int j0 = u->j0, j1 = u->j1, clean0 = u->clean0, unseen = u->unseen, lk = u->lk;
     bool read = units.nth == 0;  // the notes on the unit before have been (by both CTAs)
-    if (kCtas == 1 && units.nth % Notes<1>::kWipe == 0 && units.nth > 0) {
-      if (!(ok = __all_sync(~0u, wait_bar(&c.done, (units.nth - 1) & 1, &c.abort_flag)))) break;
+    // `done` is waited for only at a unit that is cleaned: the softmax warps cannot be
+    // through with that one, so the phase of the unit before is the last or the present
+    // one, and no warp has arrived twice in it.  (They run through units that are not
+    // cleaned without these warps; through those without keys not even together.)
+    if (kCtas == 1 && j1 > clean0 && turn > 0 && turn % Notes<1>::kWipe == 0) {
+      if (!(ok = __all_sync(~0u, read || wait_bar(&c.done, (units.nth - 1) & 1, &c.abort_flag)))) break;
+      read = true;
       for (int d = lane; d < kKeys; d += 32) c.notes.clear(d);
       __syncwarp();
     }
@@ -730,9 +736,9 @@ __device__ __forceinline__ void clean_values(uint8_t* base, Ctl<kCtas>& c, const
           const int past = t0 + row - unseen, dim = dims * 64 + ((v & 7) ^ (row & 7)) * 8 + e % 8;
           if (t0 + row < lk && past < F::kBlock) {  // past that no row of the unit sees it
             read = read || wait_bar<kCtas == 2>(&c.done, (units.nth - 1) & 1, &c.abort_flag);
-            c.notes.add(units.nth, bits & 0x7fu ? 0 : bits & 0x8000u ? 2 : 1, dim, past, rank);
-            c.any_odd = units.nth + 1;
-            if constexpr (kCtas == 2) st_cluster_u32(mapa(smem_u32(&c.any_odd), rank ^ 1), units.nth + 1);
+            c.notes.add(turn, bits & 0x7fu ? 0 : bits & 0x8000u ? 2 : 1, dim, past, rank);
+            c.any_odd = turn + 1;
+            if constexpr (kCtas == 2) st_cluster_u32(mapa(smem_u32(&c.any_odd), rank ^ 1), turn + 1);
           }
         }
       }
@@ -753,6 +759,7 @@ __device__ __forceinline__ void clean_values(uint8_t* base, Ctl<kCtas>& c, const
           !(ok = __all_sync(~0u, read || wait_bar<kCtas == 2>(&c.done, (units.nth - 1) & 1, &c.abort_flag))))
         break;
       cleans += j1 - clean0;
+      ++turn;
       if (lane == 0) {
         mbar_arrive(smem_u32(&c.cleaned));
         if constexpr (kCtas == 2) mbar_arrive_cluster(mapa(smem_u32(&c.cleaned), rank ^ 1));
@@ -790,7 +797,7 @@ __device__ __forceinline__ void softmax_rows(Ctl<kCtas>& c, const PrefillParams&
   };
   Units<kCtas> units(c);
   bool ok = true;
-  uint32_t turns = 0, outs = 0, cleans = 0;  // phases of c.s, c.o and c.cleaned
+  uint32_t turns = 0, outs = 0, cleans = 0;  // phases of c.s, c.o and c.cleaned (units cleaned so far)
   while (const Unit* u = units.next(ok)) {
     const int tiles = (g ? u->n1 : u->n0) - u->j0;
     // keys that the row sees, from the unit's first tile on; padding rows: all
@@ -884,7 +891,8 @@ __device__ __forceinline__ void softmax_rows(Ctl<kCtas>& c, const PrefillParams&
     const int unseen = u->unseen - u->j0 * kKeys;
     // notes of this unit: tokens that the row sees get their values back
     const uint32_t reach = (uint32_t)min(max(seen - unseen, 0), Form<kCtas>::kBlock);
-    const bool odd = cleaned && *reinterpret_cast<volatile uint32_t*>(&c.any_odd) == units.nth + 1;
+    const uint32_t turn = cleans - 1;
+    const bool odd = cleaned && *reinterpret_cast<volatile uint32_t*>(&c.any_odd) == turn + 1;
     __nv_bfloat16* out = p.out + row * MLA_V_HEAD_DIM;
     float* part = p.O_part + row * MLA_V_HEAD_DIM;
 #pragma unroll 1
@@ -911,9 +919,9 @@ __device__ __forceinline__ void softmax_rows(Ctl<kCtas>& c, const PrefillParams&
 #pragma unroll 1
       for (int e = 0; e < kKeys; ++e) {
         float add = 0.f;
-        if (c.notes.below(units.nth, 0, e, reach)) add = NAN;
-        if (c.notes.below(units.nth, 1, e, reach)) add += INFINITY;
-        if (c.notes.below(units.nth, 2, e, reach)) add -= INFINITY;
+        if (c.notes.below(turn, 0, e, reach)) add = NAN;
+        if (c.notes.below(turn, 1, e, reach)) add += INFINITY;
+        if (c.notes.below(turn, 2, e, reach)) add -= INFINITY;
         if (add == 0.f) continue;
         if (whole) out[e] = __float2bfloat16(__bfloat162float(out[e]) + add);
         else part[e] += add;
