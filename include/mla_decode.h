@@ -735,8 +735,9 @@ int mla_plan_prefill(const int32_t* q_lens, const int32_t* kv_lens,
  *   finished   bytes [B, W], non-zero: finished; or NULL
  * Sums are fp32 over a lane's tiles (compensated) and a warp, and pairs of fp32 from
  * there; scores are formed and compared in fp64, a beam's own tokens by their logits.
- * Sums of rows with the same largest logit that agree to 2^-17 count as the same, so
- * that rows of equal logits tie wherever they start.
+ * A row's sum is its own, within (10 + tiles) 2^-21 of itself at worst (tiles of a part
+ * of a row: 1024 fp32 or 2048 16-bit logits each); rows of equal logits have equal scores,
+ * wherever they start.
  * W <= MLA_BEAM_MAX_W, k <= MLA_BEAM_MAX_K (else MLA_ERR_UNSUPPORTED), k <= W V.
  */
 typedef enum { MLA_LOGIT_BF16 = 0, MLA_LOGIT_F16 = 1, MLA_LOGIT_F32 = 2 } mla_logit_dtype;

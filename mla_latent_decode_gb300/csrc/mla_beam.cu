@@ -88,7 +88,8 @@ struct Smem {
   float2 stat[kMaxParts];                   // (max, sum) of the cluster's parts
   double lse[kMaxW];
   float2 row[kMaxW];                        // (max, sum) of the beams' rows
-  int like[kMaxW];                          // the first row with the same sum
+  int like[kMaxW];                          // the first row with the same values
+  int differ[kMaxW];                        // the last round in which a row differed from the one it was compared with
   int num[kMaxLists];                       // entries of a list
   int ends[kMaxW];                          // a finished beam's end counts
   int got_num[kMaxCluster];
@@ -491,8 +492,130 @@ __device__ __noinline__ int merge_lists(u64* score, long long* pos, int* num, in
   return num[0];
 }
 
+__device__ __forceinline__ float value(float x) { return x; }
+__device__ __forceinline__ float value(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ float value(__half x) { return __half2float(x); }
+
+// Part `part` of `parts` of a comparison of two rows, their first elements `from` and
+// `at` (not the same) places behind a 16-byte boundary, by a warp: false if it, or
+// (*differ >= round) another warp, found a difference.  A vector of x against the two of
+// y that hold the same elements, shifted into place; the ends one by one.
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 2) mla_beam_select_kernel(const BeamParams p) {
+__device__ __forceinline__ bool same_values(const T* x, const T* y, int from, int at, int V, int part, int parts,
+                                            volatile int* differ, int round) {
+  constexpr int kPer = Type<T>::kPer, kAtOnce = 4;
+  const int lane = threadIdx.x & 31;
+  const int d = (at - from + kPer) % kPer, bits = d * (int)sizeof(T) % 4 * 8;
+  const int64_t begin = (kPer - from) % kPer, head = begin < d ? begin + kPer : begin;  // y's vectors from head - d on
+  const int64_t n = max(((int64_t)V - kPer - head + d) / kPer, (int64_t)0);             // vectors whose y lie in the row
+  bool equal = true;
+  if (part == 0) {
+    const int64_t ends = n ? head : V, rest = V - n * kPer;
+    for (int64_t i = lane; i < rest; i += 32) {
+      const int64_t e = i < ends ? i : i + n * kPer;
+      equal = equal && value(x[e]) == value(y[e]);
+    }
+  }
+  bool same = __all_sync(~0u, equal);
+#pragma unroll 1
+  for (int64_t i0 = (int64_t)part * 32 * kAtOnce; i0 < n && same; i0 += (int64_t)parts * 32 * kAtOnce) {
+    uint4 u[kAtOnce], v[kAtOnce][2];
+#pragma unroll
+    for (int j = 0; j < kAtOnce; ++j) {
+      const int64_t i = min(i0 + j * 32 + lane, n - 1);
+      u[j] = *reinterpret_cast<const uint4*>(x + head + i * kPer);
+      v[j][0] = *reinterpret_cast<const uint4*>(y + head - d + i * kPer);
+      v[j][1] = *reinterpret_cast<const uint4*>(y + head - d + i * kPer + kPer);
+    }
+#pragma unroll
+    for (int j = 0; j < kAtOnce; ++j) {
+      uint32_t w[8] = {v[j][0].x, v[j][0].y, v[j][0].z, v[j][0].w, v[j][1].x, v[j][1].y, v[j][1].z, v[j][1].w};
+      const int words = d * (int)sizeof(T) / 4;
+#pragma unroll
+      for (int k = 0; k < 6; ++k) w[k] = words & 2 ? w[k + 2] : w[k];
+#pragma unroll
+      for (int k = 0; k < 5; ++k) w[k] = words & 1 ? w[k + 1] : w[k];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) w[k] = __funnelshift_r(w[k], w[k + 1], bits);
+      if (u[j].x != w[0] || u[j].y != w[1] || u[j].z != w[2] || u[j].w != w[3]) {
+        const uint4 z = make_uint4(w[0], w[1], w[2], w[3]);  // 0 and -0 are equal
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) equal = equal && Type<T>::at(u[j], k) == Type<T>::at(z, k);
+      }
+    }
+    same = __all_sync(~0u, equal && *differ < round);
+  }
+  return same;
+}
+
+// Rows of equal values have equal scores, and the lowest row's tokens go first; but
+// where they start at other places modulo 16 bytes their values meet in another order,
+// and their sums differ in the last bits.  So rows that start at other places are
+// compared, value by value, if their maxima agree and their sums as far as those of
+// equal rows do; rows that start at the same place have the same sum if they are equal.
+// How far that is, of a sum: a term's exponent is a difference and a product, 2^-24
+// of itself each, in hops (to its lane's maximum, to the later ones, to the warp's)
+// whose lengths add up to log2 of how often the term goes into the largest one; the
+// mean of that over the terms is log2 V, at most 31: 31 x 2^-23 ln 2, or 5.4 x 2^-21.  Every
+// hop's exponential errs by 2^-22 and its product by 2^-24, the hops two and one for
+// each tile: 0.63 x 2^-21 each; 25 additions of a tile, a part and the lanes by 2^-24: 3.2
+// x 2^-21.  That is below (10 + tiles) x 2^-21 for one of the two sums.
+//
+// All warps of the cluster call it and find the same.  Rounds: every row left is
+// compared with the first row it may equal, its values dealt out over all warps,
+// which tell each other of a difference.  Measured: 0.3 to 0.6 us where rows start at
+// other places and none may be equal (64 x 16 x 32001 bf16 28.0 -> 28.6, 16 x 5 x 100003
+// fp32 20.4 -> 20.8), a second reading where all are (64 x 16 x 131071 69 -> 145).
+template <typename T>
+__device__ __noinline__ int first_equal(const BeamParams& p, int64_t b, uint32_t rank, int tiles) {
+  Smem& sm = shared();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, W = p.W, all = p.cluster * kWarps;
+  const T* first = static_cast<const T*>(p.logits) + b * p.batch_stride;
+  const int start = (int)(reinterpret_cast<uintptr_t>(first + min(lane, W - 1) * p.beam_stride) / sizeof(T) % Type<T>::kPer);
+  const float2 mine = sm.row[min(lane, W - 1)];
+  const float near = (float)(2 * (10 + tiles)) * 0x1p-21f * mine.y;
+  uint32_t open = 0;  // rows before the lane's that it may equal
+#pragma unroll 4
+  for (int w = 0; w < W - 1; ++w) {
+    const float2 x = sm.row[w];
+    open |= (uint32_t)(x.x == mine.x && fabsf(x.y - mine.y) <= near) << w;
+  }
+  const uint32_t together = __match_any_sync(~0u, start);
+  open = lane < W ? open & ~together & ((1u << lane) - 1) : 0;
+  int like = lane;
+  if (!__any_sync(~0u, open)) return like;
+#pragma unroll 1
+  for (int round = 1; __any_sync(~0u, open); ++round) {
+    const uint32_t rows = __ballot_sync(~0u, open);
+    const int pairs = __popc(rows), turns = max(all / pairs, 1);  // warps of a pair
+#pragma unroll 1
+    for (int t = (int)rank * kWarps + warp; t < pairs * turns; t += all) {
+      uint32_t left = rows;
+#pragma unroll 1
+      for (int i = t % pairs; i; --i) left &= left - 1;
+      const int w = __ffs(left) - 1, with = __ffs(__shfl_sync(~0u, open, w)) - 1;
+      const bool same = same_values<T>(first + w * p.beam_stride, first + with * p.beam_stride,
+                                       __shfl_sync(~0u, start, w), __shfl_sync(~0u, start, with), p.V, t / pairs, turns,
+                                       &sm.differ[w], round);
+      if (!same && lane < p.cluster) st_cluster_u32(mapa(smem_u32(&sm.differ[w]), lane), (uint32_t)round);
+    }
+    cluster_sync();
+    if (open) {
+      // (a row that differed may be told so again by a CTA in the next round)
+      if (*reinterpret_cast<volatile int*>(&sm.differ[lane]) >= round) open &= open - 1;
+      else like = __ffs(open) - 1, open = 0;
+    }
+  }
+#pragma unroll 1
+  for (int w = 1; w < W; ++w) {  // the first of all rows that equal each other
+    const int root = __shfl_sync(~0u, like, __shfl_sync(~0u, like, w));
+    if (lane == w) like = root;
+  }
+  return like;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads, 2) mla_beam_select_kernel(const __grid_constant__ BeamParams p) {
   Smem& sm = shared();
   const int tid = threadIdx.x, warp = tid >> 5;
   const uint32_t rank = cluster_ctarank();
@@ -509,6 +632,7 @@ __global__ void __launch_bounds__(kThreads, 2) mla_beam_select_kernel(const Beam
   cluster_arrive();  // the CTAs have started when they write to each other
   const int64_t len = ((int64_t)(((uint32_t)V + parts - 1) / (uint32_t)parts) + 63) / 64 * 64;
   const int lane = tid & 31;
+  if (tid < kMaxW) sm.differ[tid] = 0;
   for (int l = tid; l < lists; l += kThreads) {
     sm.num[l] = 0;
     if (own(l) < all) sm.stat[own(l)] = make_float2(-INFINITY, 0.f);
@@ -733,7 +857,7 @@ __global__ void __launch_bounds__(kThreads, 2) mla_beam_select_kernel(const Beam
       const bool done = p.finished && p.finished[b * W + w];
       // an infinite or undefined logit: no continuation of this beam counts
       const bool whole = sum.hi > 0 && sum.hi < INFINITY && fabsf(m) < INFINITY;
-      sm.row[w] = make_float2(m, sum.hi);
+      sm.row[w] = make_float2(whole ? m : NAN, sum.hi);
       sm.lse[w] = whole ? (double)m + log_of(sum) : INFINITY;
       sm.ends[w] = done && fabsf(c) < INFINITY;  // its end, at its score
       if (rank == 0 && p.status && (!(c < INFINITY) || (!done && (sum.hi != sum.hi || m == INFINITY))))
@@ -741,19 +865,9 @@ __global__ void __launch_bounds__(kThreads, 2) mla_beam_select_kernel(const Beam
     }
   }
   __syncthreads();
-  // Rows of equal values have equal scores, and the lowest row's go first; but where
-  // they start at other places modulo 16 bytes their values meet in another order.  A
-  // term errs by 2^-22, by as much for each of the few times that its lane's maximum
-  // rises, and by its exponent's error, of which up to about 24 halvings matter and
-  // 2^-24 of them at the subtraction and at the multiplication: sums of rows with the
-  // same maximum that differ by less than 2 (2^-22 + 2 x 24 x 2^-24 ln 2), doubled for
-  // the rises, are taken as one: 2^-17 (a score is off by that at most).
-#pragma unroll 1
-  for (int w = warp; w < W; w += kWarps) {
-    const float2 x = sm.row[w], y = sm.row[min(lane, w)];
-    const uint32_t like = __ballot_sync(~0u, lane == w || (lane < w && y.x == x.x && fabsf(y.y - x.y) <= x.y * 0x1p-17f));
-    if (lane == 0) sm.like[w] = __ffs(like) - 1;
-  }
+  // rows that start at the same place modulo 16 bytes need no comparison
+  const int like = p.beam_stride % kPer ? first_equal<T>(p, b, rank, (int)(len / Walk<T>::kTile) + 2) : lane;
+  if (warp == 0) sm.like[lane] = like;
   if (tid < lists && own(tid) < all) {
     const int w = own(tid) / parts;
     if (sm.ends[w]) sm.num[tid] = own(tid) % parts == 0;
