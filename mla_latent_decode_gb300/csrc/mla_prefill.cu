@@ -895,6 +895,9 @@ __device__ __forceinline__ void softmax_rows(Ctl<kCtas>& c, const PrefillParams&
     const bool odd = cleaned && *reinterpret_cast<volatile uint32_t*>(&c.any_odd) == turn + 1;
     __nv_bfloat16* out = p.out + row * MLA_V_HEAD_DIM;
     float* part = p.O_part + row * MLA_V_HEAD_DIM;
+    // without a key, or with impossible ones only, 0; in a part these may have left a NaN
+    // (0 x inf), which the row's other parts' keys make count
+    if (!whole && tiles > 0) l = 1.f;
 #pragma unroll 1
     for (int b = 0; b < kKeys; b += 16) {
       uint32_t o[16];
@@ -1043,7 +1046,8 @@ __global__ void __launch_bounds__(Form<kCtas>::kThreads, kCtas == 1 ? 2 : 1)
 
 // Merge of a block's parts, a warp per row and 16 rows a CTA (a row takes two trips to
 // L2 or DRAM, so a warp has few of them): weights e^(LSE_s - max), parts in
-// order.  Parts without keys (LSE = -inf) weigh nothing; a NaN makes the row NaN.
+// order.  A part that weighs nothing is added all the same, as 0 x inf is NaN where the
+// keys are not cut; a NaN makes the row NaN, and a row without a possible key is 0.
 constexpr int kMergeRows = 16;
 template <int kCtas>
 __global__ void __launch_bounds__(256) mla_prefill_merge_kernel(const PrefillParams p) {
@@ -1073,10 +1077,10 @@ __global__ void __launch_bounds__(256) mla_prefill_merge_kernel(const PrefillPar
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int s = 0; s < parts; ++s) {
       const float ws = __shfl_sync(~0u, w, s);
-      if (ws == 0.f) continue;
       const float4 x = reinterpret_cast<const float4*>(p.O_part + (at + s * step) * MLA_V_HEAD_DIM)[lane];
       o.x += ws * x.x, o.y += ws * x.y, o.z += ws * x.z, o.w += ws * x.w;
     }
+    if (sum == 0.f) o = make_float4(0.f, 0.f, 0.f, 0.f);
     const float inv = nan ? NAN : sum > 0.f ? 1.f / sum : 0.f;
     const int64_t row = (q0 + row0 + r) * p.H + h;
     reinterpret_cast<uint2*>(p.out + row * MLA_V_HEAD_DIM)[lane] =
