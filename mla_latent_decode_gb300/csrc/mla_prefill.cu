@@ -918,7 +918,7 @@ __device__ __forceinline__ void softmax_rows(Ctl<kCtas>& c, const PrefillParams&
       }
       __syncwarp();
     }
-    if (odd && exists) {
+    if (odd && exists && l != 0.f) {  // (a row of impossible keys is 0 whatever their values are)
 #pragma unroll 1
       for (int e = 0; e < kKeys; ++e) {
         float add = 0.f;

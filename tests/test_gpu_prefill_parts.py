@@ -89,3 +89,24 @@ def test_values_of_probability_zero(ctas):
     # below 6; sums of up to 6000 / 4 terms in a row
     assert bool(((whole.float() - cut.float()).abs()[want] <= 4 * 2.0 ** -8 * 6).all())
     assert bool(((whole_lse - cut_lse).abs() <= 2.0 ** -12).all())
+
+
+@pytest.mark.parametrize("ctas", [1, 2])
+@pytest.mark.parametrize("lk,sms", [(200, 1), (6000, 1), (6000, 300)])
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+def test_rows_that_see_only_impossible_keys(bad, lk, sms, ctas):
+    """out = 0 and lse = -inf, whatever the values hold and wherever they stand."""
+    lq, H = 100, 16
+    x = _inputs(lq, lk, H, 3)
+    x["q_nope"][:] = x["q_nope"].abs() + 0.125
+    x["k_nope"][:, 2, 0] = -math.inf
+    x["k_nope"][:, 5, 0] = -math.inf
+    for t in (3, lk - lq + 10, lk - 1):
+        x["v"][t, 2] = bad
+        x["v"][t, 4, 9] = bad                                # a head with ordinary keys
+    out, lse, _ = _run(x, lq, lk, H, sms, ctas)
+    for h in (2, 5):
+        assert bool((out[:, h] == 0).all()) and bool((lse[:, h] == -math.inf).all())
+    other = out[:, 4]
+    assert not bool(other[:, 9].isfinite().any())
+    assert bool(other[:, :9].isfinite().all() and other[:, 10:].isfinite().all())
