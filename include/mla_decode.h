@@ -776,7 +776,9 @@ int mla_beam_select(const void* logits, mla_logit_dtype dtype, int64_t batch_str
  * BAD_PARENT), a length outside its row (BAD_LENGTH), a partly taken page
  * outside the pool (BAD_SLOT) or more new pages than free_count
  * (NO_PAGES) leaves refs and free_count as they are, lens_out 0 and nothing to
- * copy; table_out is then not to be used, and the old table still stands.
+ * copy; table_out is then not to be used, and the old table still stands.  (Where
+ * free_count says more than the pool has, NO_PAGES too, but the last rows end with the
+ * pages that were left, lens_out says where, and nothing is copied for a row without.)
  * R <= MLA_FORK_MAX_ROWS.  One launch, no workspace; results do not depend on
  * any order of execution.  R = 0 is a no-op.
  */

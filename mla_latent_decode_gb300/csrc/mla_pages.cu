@@ -297,9 +297,10 @@ __global__ void __launch_bounds__(kThreads) __cluster_dims__(kCluster, 1, 1)
     }
   }
   cluster_arrive();
-  // A count of free pages above what the pool has: the rows that got none are
-  // left with what their entries held.
-  if (found < total && rank == 0 && tid == 0 && p.status) atomicOr(p.status, MLA_STATUS_NO_PAGES);
+  // A count of free pages above what the pool has: the last rows end with the pages
+  // that they hold.
+  const int given = (int)min((int64_t)found, total);
+  if (given < total && rank == 0 && tid == 0 && p.status) atomicOr(p.status, MLA_STATUS_NO_PAGES);
 
   // Counts.  Of a parent's pages its heir goes on holding those it takes; the
   // rest lose the parent, and every other child adds its full pages.  A page
@@ -359,11 +360,14 @@ __global__ void __launch_bounds__(kThreads) __cluster_dims__(kCluster, 1, 1)
     }
   }
   for (int i = rank * kThreads + tid; i < R; i += kCluster * kThreads) {
-    p.lens_out[i] = kept[i] + (p.grow ? p.grow[i] : 0);
+    int64_t len = kept[i] + (int64_t)(p.grow ? p.grow[i] : 0);
     const int t = tail[i];
-    p.copies[i] = t < -1 ? -1 - t : -1;
-    if (t >= -1) p.copies[R + i] = -1;
-    p.copies[2 * R + i] = t < -1 ? kept[i] % kPage : 0;
+    if (first[i + 1] > given) len = min(len, ((int64_t)(kept[i] / kPage) + (t > 0) + max(given - first[i], 0)) * kPage);
+    p.lens_out[i] = (int)len;
+    const bool copied = t < -1 && first[i] < given;
+    p.copies[i] = copied ? -1 - t : -1;
+    if (!copied) p.copies[R + i] = -1;
+    p.copies[2 * R + i] = copied ? kept[i] % kPage : 0;
   }
   // Entries: kept partly taken pages, then the new ones', 16 threads a page.
   for (int64_t t = rank * kThreads + tid; t < (int64_t)R * 16; t += kCluster * kThreads) {
@@ -371,7 +375,7 @@ __global__ void __launch_bounds__(kThreads) __cluster_dims__(kCluster, 1, 1)
     if (tail[i] > 0) write_quad(p, i, kept[i] / kPage, tail[i], (int)(t % 16));
   }
   cluster_wait();  // the new pages' first entries; the boxes have been read, too
-  for (int64_t t = rank * kThreads + tid; t < min((int64_t)found, total) * 16; t += kCluster * kThreads) {
+  for (int64_t t = rank * kThreads + tid; t < (int64_t)given * 16; t += kCluster * kThreads) {
     const int r = (int)(t / 16), row = row_of(r);
     const int64_t at = kept[row] / kPage + (tail[row] > 0) + r - first[row];
     const int page = p.out[row * p.out_stride + at * kPage] / kPage;
@@ -386,7 +390,7 @@ __global__ void __launch_bounds__(kThreads) __cluster_dims__(kCluster, 1, 1)
   if (rank == 0 && tid == 0) {
     int sum = 0;
     for (int c = 0; c < kCluster; ++c) sum += b[2 * c];
-    *p.free_count += sum - (int)min((int64_t)found, total);
+    *p.free_count += sum - given;
   }
 }
 
