@@ -190,8 +190,65 @@ namespace mla {
 // (a pair of CTAs).  Costs in key tiles of a single CTA with another beside it (about
 // 2 us), from times of both forms: 8191 tokens x 96 heads 1428 us on single CTAs and
 // 1215 on pairs, 24 prompts of 100 to 6000 tokens x 16 heads 508 and 462, 64 documents
-// of 33 to 700 tokens x 96 heads 349 and 558.  A tile of a pair, what a block takes
-// besides its tiles, and the merging launch with its rows.
+// of 33 to 700 tokens x 96 heads 349 and 558.  What a block takes besides its tiles, a
+// tile of either form, and the merging launch with its rows, in fiftieths of that tile.
+constexpr int64_t kSingleFixed = 85, kSingleTile = 50, kPairFixed = 110, kPairTile = 39;
+constexpr double kMerge = 150, kMergeSlot = 0.4;
+
+// List schedule on equal slots: every job goes to the slot that is free first.  The
+// times at which slots are free lie within one job's cost of each other, so they are
+// kept as counts in a ring of times, found by a bitmap: a few ns a job, where a heap of
+// 304 slots takes 50.  Costs above 2^16 are rounded to a multiple of a power of two.
+// Plans of 0.05 to 0.35 ms (8191 tokens x 16 heads, 8 x 2000 against 200000 x 8), where the
+// heap and every cut took 4 and 13, and 28 for 8 x 2000 against 30000 x 16 (0.06).
+class ListSchedule {
+ public:
+  ListSchedule(int slots, int64_t largest) {
+    while (((largest + 1) >> shift_) >= 1 << 16) ++shift_;
+    size_t times = 64;
+    while ((int64_t)times <= (largest >> shift_) + 1) times *= 2;
+    mask_ = times - 1;
+    free_.assign(times, 0);
+    some_.assign(times / 64, 0);
+    put(0, slots);
+  }
+  // One after another, `n` jobs of a cost; false once the schedule ends after `limit`.
+  bool deal(int64_t cost, int64_t n, double limit) {
+    cost = std::max<int64_t>(cost >> shift_, 1);
+    while (n > 0) {
+      advance();
+      int& here = free_[now_ & mask_];
+      const int m = (int)std::min<int64_t>(n, here);
+      here -= m;
+      if (here == 0) some_[(now_ & mask_) / 64] &= ~(1ull << (now_ & 63));
+      put(now_ + cost, m);
+      end_ = std::max(end_, now_ + cost);
+      n -= m;
+    }
+    return (double)end() <= limit;
+  }
+  int64_t end() const { return end_ << shift_; }
+
+ private:
+  void put(int64_t at, int n) {
+    free_[at & mask_] += n;
+    some_[(at & mask_) / 64] |= 1ull << (at & 63);
+  }
+  void advance() {  // to the first time at which a slot is free
+    uint64_t word = some_[(now_ & mask_) / 64] >> (now_ & 63);
+    if (!word) {
+      now_ = (now_ | 63) + 1;
+      while (!(word = some_[(now_ & mask_) / 64])) now_ += 64;
+    }
+    now_ += __builtin_ctzll(word);
+  }
+  int shift_ = 0;
+  size_t mask_ = 0;
+  int64_t now_ = 0, end_ = 0;
+  std::vector<int> free_;
+  std::vector<uint64_t> some_;
+};
+
 struct PrefillPlan {
   int ctas = 1;
   double end = 0;
@@ -209,7 +266,6 @@ static PrefillPlan plan_prefill_blocks(const int32_t* q_lens, const int32_t* kv_
                                        const int32_t* prefix, int N, int H, int causal,
                                        int ctas, int num_sms) {
   constexpr int kKeys = 128;
-  constexpr double kFixed = 1.7, kPairFixed = 2.2, kPairTile = 0.78, kMerge = 3, kMergeSlot = 0.008;
   const int block = ctas == 1 ? 128 : 512, slots_of = block / 128;
   PrefillPlan plan;
   plan.ctas = ctas;
@@ -233,39 +289,70 @@ static PrefillPlan plan_prefill_blocks(const int32_t* q_lens, const int32_t* kv_
   std::stable_sort(plan.order.begin(), plan.order.end(),
                    [&](int a, int b) { return last_of(a) > last_of(b); });
   plan.limit = std::max<int64_t>(longest, 1);
-  const int slots = ctas == 1 ? 2 * std::max(num_sms, 1) : std::max(num_sms / 2, 1);
-  const double tile = ctas == 1 ? 1 : kPairTile, fixed = ctas == 1 ? kFixed : kPairFixed;
+  num_sms = std::min(std::max(num_sms, 1), 1 << 20);
+  const int slots = ctas == 1 ? 2 * num_sms : std::max(num_sms / 2, 1);
+  const int64_t tile = ctas == 1 ? kSingleTile : kPairTile, fixed = ctas == 1 ? kSingleFixed : kPairFixed;
   // Many blocks: they even out.
-  plan.end = ((double)all * tile + (double)blocks * fixed) * H / slots + longest * tile / 2;
+  plan.end = (double)(all * tile + blocks * fixed) * H / slots + (double)(longest * tile) / 2;
   if (blocks == 0 || blocks * H >= 8 * (int64_t)slots) return plan;
   // Few: a limit on a part's key tiles, the one that ends first: halfway between
   // the list schedule in launch order and full use of all slots, as blocks run faster
   // while others' slots are idle.
-  double best = -1;
-  int64_t best_limit = plan.limit;
+  // A cut's schedule ends no earlier than its longest part does, nor than all slots'
+  // shares: cuts are tried in the order of that bound, and those whose bound is above
+  // the best so far are not, nor are schedules followed that end too late.
+  struct Cut {
+    int64_t limit, longest;     // of a part: key tiles, cost
+    double share, merge, bound;
+    int nth;
+  };
+  std::vector<Cut> cuts;
   for (int cut : {1, 2, 3, 4, 5, 6, 8, 10, 12, 16, 20, 24, 28, 32}) {
     plan.limit = std::max<int64_t>((longest + cut - 1) / cut, 1);
     if (cut > 1 && plan.limit < 4) break;
-    std::priority_queue<double, std::vector<double>, std::greater<double>> ends;
-    for (int i = 0; i < slots; ++i) ends.push(0);
-    double end = 0, sum = 0;
-    int64_t merged = 0;
-    for (int n : plan.order)
-      for (int h = 0; h < H; ++h)
-        for (auto t = plan.tiles[n].rbegin(); t != plan.tiles[n].rend(); ++t) {
-          const int parts = plan.parts_of(*t);
-          merged += parts > 1 ? parts * slots_of : 0;
-          for (int s = 0; s < parts; ++s) {
-            const double cost = fixed + tile * (double)(*t * (s + 1) / parts - *t * s / parts);
-            const double at = ends.top() + cost;
-            ends.pop();
-            ends.push(at);
-            end = std::max(end, at);
-            sum += cost;
+    Cut c{plan.limit, 0, 0, 0, 0, (int)cuts.size()};
+    int64_t sum = 0, merged = 0;
+    for (int n = 0; n < N; ++n)
+      for (int64_t t : plan.tiles[n]) {
+        const int parts = plan.parts_of(t);
+        merged += parts > 1 ? (int64_t)parts * slots_of * H : 0;
+        sum += (parts * fixed + t * tile) * H;
+        c.longest = std::max(c.longest, fixed + tile * ((t + parts - 1) / parts));
+      }
+    c.share = (double)sum / slots;
+    c.merge = merged ? kMerge + kMergeSlot * (double)merged : 0;
+    c.bound = (std::max((double)c.longest, c.share) + c.share) / 2 + c.merge;
+    cuts.push_back(c);
+  }
+  std::sort(cuts.begin(), cuts.end(),
+            [](const Cut& a, const Cut& b) { return a.bound != b.bound ? a.bound < b.bound : a.nth < b.nth; });
+  double best = -1;
+  int best_nth = 0;
+  int64_t best_limit = plan.limit;
+  for (const Cut& c : cuts) {
+    if (best >= 0 && c.bound > best) break;
+    plan.limit = c.limit;
+    const double latest = best < 0 ? HUGE_VAL : 2 * (best - c.merge) - c.share;
+    ListSchedule schedule(slots, c.longest);
+    bool in_time = true;
+    for (int n : plan.order) {
+      const auto& tiles = plan.tiles[n];
+      const bool one = tiles.size() == 1 && tiles[0] % plan.parts_of(tiles[0]) == 0;  // all heads' parts alike
+      for (int h = 0; h < (one ? 1 : H) && in_time; ++h)
+        for (auto t = tiles.rbegin(); t != tiles.rend() && in_time; ++t) {
+          const int64_t parts = plan.parts_of(*t);
+          if (*t % parts == 0) {
+            in_time = schedule.deal(fixed + tile * (*t / parts), parts * (one ? H : 1), latest);
+          } else {
+            for (int64_t s = 0; s < parts && in_time; ++s)
+              in_time = schedule.deal(fixed + tile * (*t * (s + 1) / parts - *t * s / parts), 1, latest);
           }
         }
-    end = (end + sum / slots) / 2 + (merged ? kMerge + kMergeSlot * (double)merged : 0);
-    if (best < 0 || end < best) best = end, best_limit = plan.limit;
+      if (!in_time) break;
+    }
+    if (!in_time) continue;
+    const double end = ((double)schedule.end() + c.share) / 2 + c.merge;
+    if (best < 0 || end < best || (end == best && c.nth < best_nth)) best = end, best_nth = c.nth, best_limit = c.limit;
   }
   plan.limit = best_limit;
   plan.end = best;
