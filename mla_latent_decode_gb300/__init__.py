@@ -711,6 +711,15 @@ def lse_combine(O_part, LSE_part, out=None, lse_out=None, stream=None):
 
 
 # ------------------------------------------------------- prompts and beams
+def _check_device(first: torch.Tensor, names: str, *tensors) -> None:
+    """All arrays (None: not given) are where the first one is: the kernels read them
+    by address.  (A call of get_device takes 0.05 us, of device with a comparison 0.15.)"""
+    at = first.get_device()
+    for i, t in enumerate(tensors):
+        if t is not None and t.get_device() != at:
+            raise ValueError(f"{names.split()[i]}: expected on {first.device}, got {t.device}")
+
+
 def plan_prefill(q_lens: Sequence[int], kv_lens: Sequence[int], H: int, prefix=None,
                  causal: bool = True, num_sms: int = 0, ctas: int = 0):
     """Plan of `prefill` for sequences of these query and key lengths (host
@@ -763,10 +772,9 @@ def prefill(q_nope, q_rope, k_nope, k_rope, v, cu_q, cu_kv, work, sm_scale: floa
     N = cu_q.numel() - 1
     if N < 0:
         raise ValueError("cu_q: expected N + 1 values")
-    if work.dtype is not _I32 or tuple(work.shape[1:]) not in ((8,), (2, 8)) or not work.is_contiguous() \
-            or work.device != q_nope.device:
-        raise ValueError(f"work: expected contiguous int32 [n, 8] or [n, 2, 8] on {q_nope.device}, got "
-                         f"{work.dtype} {tuple(work.shape)} on {work.device}")
+    if work.dtype is not _I32 or work.shape[1:] not in ((8,), (2, 8)) or not work.is_contiguous():
+        raise ValueError(f"work: expected contiguous int32 [n, 8] or [n, 2, 8], got {work.dtype} "
+                         f"{tuple(work.shape)}")
     qn = _heads_arg(q_nope, "q_nope", Tq, H, 128)
     qr = _heads_arg(q_rope, "q_rope", Tq, H, ROPE_DIM)
     kn = _heads_arg(k_nope, "k_nope", Tk, H, 128)
@@ -774,6 +782,8 @@ def prefill(q_nope, q_rope, k_nope, k_rope, v, cu_q, cu_kv, work, sm_scale: floa
     kr = _rows_arg(k_rope, "k_rope", Tk, ROPE_DIM)
     cu_args = _int32_arg(cu_q, "cu_q", N + 1), _int32_arg(cu_kv, "cu_kv", N + 1), \
         None if prefix is None else _int32_arg(prefix, "prefix", N)
+    _check_device(q_nope, "q_rope k_nope k_rope v cu_q cu_kv work prefix O_part LSE_part out lse_out status",
+                  q_rope, k_nope, k_rope, v, cu_q, cu_kv, work, prefix, O_part, LSE_part, out, lse_out, status)
     dev = q_nope.device
     if out is None:
         out = torch.empty((Tq, H, 128), dtype=_BF16, device=dev)
@@ -819,6 +829,8 @@ def beam_select(logits, scores, k: int, finished=None, end_token: int = 0, out_s
                                  finished.numel() != B * W or not finished.is_contiguous()):
         raise ValueError(f"finished: expected {B * W} contiguous bool or uint8 values, got "
                          f"{finished.dtype} {tuple(finished.shape)}")
+    _check_device(logits, "scores finished out_scores parents tokens status", scores, finished, out_scores, parents,
+                  tokens, status)
     dev = logits.device
     if out_scores is None:
         out_scores = torch.empty((B, k), dtype=_F32, device=dev)
@@ -857,6 +869,8 @@ def pages_fork(table, lens, refs, free_count, parents=None, keep=None, grow=None
     kv_copy(pool, copies[0], copies[1], scale, tokens=copies[2]) on every layer's
     pool."""
     R = table.shape[0]
+    _check_device(table, "lens refs free_count parents keep grow table_out lens_out copies status", lens, refs,
+                  free_count, parents, keep, grow, table_out, lens_out, copies, status)
     if table_out is None:
         table_out = torch.zeros_like(table)
     if lens_out is None:
@@ -887,6 +901,7 @@ def pages_compact(table, lens, refs, max_moves: Optional[int] = None, table_out=
     allocated unless given; run kv_copy(pool, src, dst, scale, count=count) on
     every layer's pool."""
     R = table.shape[0]
+    _check_device(table, "lens refs table_out src dst count status", lens, refs, table_out, src, dst, count, status)
     _check_buffer(refs, "refs", _I32, 1)
     if max_moves is None:
         max_moves = src.numel() if src is not None else refs.numel()
@@ -915,6 +930,7 @@ def kv_copy(kv, src, dst, kv_scale=None, tokens=None, count=None, status=None, s
     first *count entries where count (int32 [1]) is given.  See mla_kv_copy."""
     n = src.numel()
     kv_ptr, kind, scale_ptr, slots = _pool_args(kv, kv_scale)
+    _check_device(kv, "src dst kv_scale tokens count status", src, dst, kv_scale, tokens, count, status)
     if count is not None:
         _check_buffer(count, "count", _I32, 1)
     if status is not None:
