@@ -876,6 +876,16 @@ int mla_debug_wait(int mode, int delay_us, int* status, uint64_t* elapsed_ns,
 int mla_debug_quotients(uint64_t* bit_mismatches, uint64_t* code_mismatches,
                         mla_stream_t stream);
 
+/*
+ * Test hook for mla_beam_select's exponential and logarithm: exp_x[i] = e^x[i]
+ * (x <= 0; 0 from -80 down) and log_y[i] = ln y[i] (1 <= y <= e^79), as the selection
+ * forms them.  All arrays [n], on the device.
+ * Errors: n < 0 or a NULL array -> MLA_ERR_INVALID_ARG; misaligned ->
+ * MLA_ERR_MISALIGNED.
+ */
+int mla_debug_beam_math(const float* x, const float* y, int64_t n, double* exp_x,
+                        double* log_y, mla_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -115,6 +115,7 @@ def library() -> ctypes.CDLL:
             "mla_debug_gather": (i32, [p, i32, i64, p, i64, p, p, i32, i32, p, p]),
             "mla_debug_wait": (i32, [i32, i32, p, p, p]),
             "mla_debug_quotients": (i32, [p, p, p]),
+            "mla_debug_beam_math": (i32, [p, p, i64, p, p, p]),
         }
         for name, (res, args) in sig.items():
             fn = getattr(lib, name)
@@ -1015,3 +1016,15 @@ def decode(batch, num_splits: Optional[int] = None, simt: bool = False,
 def batch_lengths(batch):
     """Host list of the (virtual) request lengths of a batch."""
     return [int(x) for x in batch.seq_lens.tolist()]
+
+
+def debug_beam_math(x, y, stream=None):
+    """beam_select's e^x (x <= 0) and ln y (y >= 1) of float32 arrays, as float64;
+    see mla_debug_beam_math."""
+    n = x.numel()
+    _check_device(x, "y", y)
+    _check_buffer(x, "x", _F32, n)
+    _check_buffer(y, "y", _F32, n)
+    exp_x, log_y = (torch.empty(n, dtype=torch.float64, device=x.device) for _ in range(2))
+    _launch(x, stream, library().mla_debug_beam_math, x.data_ptr(), y.data_ptr(), n, exp_x.data_ptr(), log_y.data_ptr())
+    return exp_x, log_y

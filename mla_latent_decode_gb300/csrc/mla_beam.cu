@@ -150,12 +150,17 @@ __device__ __forceinline__ Two plus(Two a, Two b) {
   const float hi = s + e;
   return {hi, s < INFINITY ? e - (hi - s) : 0.f};
 }
-// e^x for x <= 0 within about 2^-26: 2^n (1 + r + r^2 (1/2 + r/6 + ...)), |r| <= ln 2 / 2.
-__device__ __forceinline__ Two exp2f(float x) {
+// e^x for x <= 0 within 2^-24.8 of it (0 from -80 down): 2^n (1 + r + r^2 (1/2 + r/6 + ...)),
+// r = x - n ln 2, |r| <= ln 2 / 2, with ln 2 as 355/512 - 2.12194440e-4 (W. J. Cody and W.
+// Waite, Software Manual for the Elementary Functions, 1980): n has 7 bits and 355 nine, so
+// the first difference is exact.  r is off by 1.07 x 2^-26 (its rounding, and n times that of
+// the second part), r^2 (...) by its terms' roundings, 0.8 x 2^-26, the rest of the series
+// 2^-32, all of e^r >= 0.707.
+__device__ __forceinline__ Two exp_two(float x) {
   if (!(x > -80.f)) return {x == x ? 0.f : x, 0.f};  // (2^-115 of a sum's largest term)
   const float n = rintf(x * kLog2e);
-  float r = fmaf(n, -0.693145752f, x);  // ln 2 in two parts, the first of 15 bits
-  r = fmaf(n, -1.42860677e-6f, r);
+  float r = fmaf(n, -355.f / 512, x);
+  r = fmaf(n, 2.12194440e-4f, r);
   float q = 1.f / 40320;
   q = fmaf(q, r, 1.f / 5040);
   q = fmaf(q, r, 1.f / 720);
@@ -170,14 +175,16 @@ __device__ __forceinline__ Two exp2f(float x) {
 }
 // y e^x
 __device__ __forceinline__ Two times_exp(float y, float x) {
-  const Two e = exp2f(x);
+  const Two e = exp_two(x);
   const float hi = y * e.hi;
   return {hi, fmaf(y, e.hi, -hi) + y * e.lo};
 }
-// ln of a finite x >= 1 (a sum with its largest term 1): fp32's, and a Newton step.
+// ln of x, 1 <= x <= e^79 (a sum of 2^31 terms at most, the largest 1), within 2^-24.7:
+// fp32's l, and a Newton step, l + (x e^-l - 1), which errs as e^-l does.  Both are checked
+// against float64 by mla_debug_beam_math (over 2^24 values 1.53 x 2^-26 at most).
 __device__ __forceinline__ double log_of(Two x) {
   const float l = logf(x.hi);
-  const Two e = exp2f(-l);
+  const Two e = exp_two(-l);
   return (double)l + (double)(fmaf(x.hi, e.hi, -1.f) + (x.hi * e.lo + x.lo * e.hi));
 }
 
@@ -927,6 +934,14 @@ __global__ void __launch_bounds__(kThreads, 2) mla_beam_select_kernel(const __gr
   }
 }
 
+__global__ void mla_beam_math_kernel(const float* x, const float* y, int64_t n, double* exp_x, double* log_y) {
+  for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < n; i += (int64_t)gridDim.x * blockDim.x) {
+    const Two e = exp_two(x[i]);
+    exp_x[i] = (double)e.hi + (double)e.lo;
+    log_y[i] = log_of({y[i], 0.f});
+  }
+}
+
 // Clusters of a size that the device holds at once, asked of each device once (fewer
 // than its places for CTAs divide into: a GPC's SMs leave a rest).
 template <typename T>
@@ -1023,4 +1038,17 @@ extern "C" int mla_beam_select(const void* logits, mla_logit_dtype dtype, int64_
   if (dtype == MLA_LOGIT_BF16) return launch_beam<__nv_bfloat16>(p, B, st);
   if (dtype == MLA_LOGIT_F16) return launch_beam<__half>(p, B, st);
   return launch_beam<float>(p, B, st);
+}
+
+extern "C" int mla_debug_beam_math(const float* x, const float* y, int64_t n, double* exp_x, double* log_y,
+                                   mla_stream_t stream) {
+  if (n < 0) return fail(MLA_ERR_INVALID_ARG, "mla_debug_beam_math: n = %lld < 0", (long long)n);
+  if (n == 0) return MLA_OK;
+  if (!x || !y || !exp_x || !log_y) return fail(MLA_ERR_INVALID_ARG, "mla_debug_beam_math: a required pointer is NULL");
+  if (!aligned(x, 4) || !aligned(y, 4) || !aligned(exp_x, 8) || !aligned(log_y, 8))
+    return fail(MLA_ERR_MISALIGNED, "mla_debug_beam_math: inputs need 4-B alignment, outputs 8-B");
+  mla_beam_math_kernel<<<(unsigned)std::min<int64_t>((n + 255) / 256, 1024), 256, 0, (cudaStream_t)stream>>>(x, y, n, exp_x, log_y);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return cuda_fail(e, "launch mla_beam_math_kernel");
+  return MLA_OK;
 }
