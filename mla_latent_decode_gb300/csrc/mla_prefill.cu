@@ -1157,7 +1157,8 @@ extern "C" int mla_prefill(const void* q_nope, int64_t qn_token_stride, int64_t 
     return fail(MLA_ERR_INVALID_ARG, "mla_prefill: sm_scale %g is not a positive number", (double)sm_scale);
   if (ctas != 1 && ctas != 2)
     return fail(MLA_ERR_INVALID_ARG, "mla_prefill: ctas=%d is not 1 or 2", ctas);
-  if (Tq > 0x7fffff00 || Tk > 0x7fffff00 || H > 65535 || (int64_t)num_work * H > 1 << 30)
+  if (Tq > 0x7fffff00 || Tk > 0x7fffff00 || H > 65535 || (int64_t)num_work * H > 1 << 30 ||
+      (int64_t)num_work * H * ctas > 0x7fffffff)
     return fail(MLA_ERR_INVALID_ARG, "mla_prefill: Tq=%lld, Tk=%lld, H=%d or num_work=%d too large",
                 (long long)Tq, (long long)Tk, H, num_work);
   if (num_work == 0 || N == 0 || Tq == 0) return MLA_OK;
