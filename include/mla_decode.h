@@ -758,7 +758,7 @@ int mla_beam_select(const void* logits, mla_logit_dtype dtype, int64_t batch_str
  * so one call reorders beams, shares a prompt, drops rejected drafts, ends rows,
  * starts new ones and makes room for a step's tokens.  Pages are shared: full
  * ones as they are; a partly taken page stays where it is with the child that
- * takes most of the row (the lowest of equals) if nobody else holds it, and any
+ * takes most pages of the row (the lowest of equals) if nobody else holds it, and any
  * other child gets a new page and an entry in `copies`: run mla_kv_copy with it
  * on every layer's pool before the step's tokens are written.
  *   refs        int32 [num_pages]: rows that hold a page, 0 = free; page 0 (the
@@ -801,8 +801,8 @@ int mla_pages_fork(const int32_t* table, int64_t stride, const int32_t* lens,
  *               pages' new numbers; may be table itself.  Every row that holds
  *               pages has to be in the table.
  * refs is updated (a moved page's count goes with it); free_count stays true.
- * Two launches.  A length outside its row sets MLA_STATUS_BAD_LENGTH and that
- * row is not renamed.
+ * Two launches, one where the table is small.  A length outside its row sets
+ * MLA_STATUS_BAD_LENGTH and that row is not renamed.
  */
 int mla_pages_compact(const int32_t* table, int64_t stride, const int32_t* lens,
                       int R, int32_t* refs, int64_t num_pages, int32_t* table_out,

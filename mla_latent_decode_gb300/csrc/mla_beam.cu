@@ -21,8 +21,8 @@
 // too many reach it (ties) the best k so far are selected exactly, and later values
 // have to exceed the last of them.
 //
-// Measured: 64 requests x 16 beams x 131072 bf16 logits, a tenth finished (241 MB) 55 us,
-// 65% of the copy rate: the 256 CTAs are two on 104 SMs and one on 48, and a tile's
+// Measured: 64 requests x 16 beams x 131072 bf16 logits, a tenth finished (241 MB) 56 us,
+// 64% of the copy rate: the 256 CTAs are two on 104 SMs and one on 48, and a tile's
 // arithmetic (3.6 instructions a logit) takes as long as its bytes.  Candidates looked
 // for tile by tile took 65 us, tiles in registers 165, a CTA a row with its barriers 215.
 //

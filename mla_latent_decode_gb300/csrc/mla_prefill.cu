@@ -16,13 +16,13 @@
 // then, and S may overwrite P.
 //
 // What bounds it (GB300).  Pairs: the tensor cores under the power cap, one prompt of
-// 8191 tokens x 96 heads (2.06 PFLOP) in 1174 us, 1.75 PFLOP/s, 92% of the measured burst
-// and all of the measured sustained rate, tensor pipe active 78% of the cycles; each SM
-// loads and reads half of every K and V tile (40 KB).  On single CTAs a row tile's 80 KB
-// of keys and values a tile come in through a ring of 64 KB, so a tile waits for loads
-// that are issued as the one before is used up: 64 documents of 33 to 700 tokens x 96
-// heads 343 us, 1.62 GB moved, 70% of the copy rate.  A block of 512 rows of a short
-// sequence would mostly be padding (558 us).
+// 8191 tokens x 96 heads (2.06 TFLOP) in 1172 to 1251 us, 1.65 to 1.75 PFLOP/s, 86 to 92% of
+// the measured burst and 96 to 102% of the measured sustained rate, tensor pipe active 78%
+// of the cycles; each SM loads and reads half of every K and V tile (40 KB).  On single
+// CTAs a row tile's 80 KB of keys and values a tile come in through a ring of 64 KB, so a
+// tile waits for loads that are issued as the one before is used up: 64 documents of 33
+// to 700 tokens x 96 heads 348 us, 1.62 GB moved, 69% of the copy rate.  A block of 512
+// rows of a short sequence would mostly be padding (558 us).
 //
 //   softmax warps    4 a row tile, one thread per row, then O / l
 //   TMA warp         K and V through the ring; on one CTA Q (48 KB) too
